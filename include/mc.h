@@ -222,6 +222,95 @@ int mc_decode_step(const void *q, const void *k, const void *v, const void *u,
                    void *y, int is_bf16, mc_stream_t stream);
 
 /*
+ * mc_forward_delta -- the forward over a gated delta memory.  Inside a segment, from an
+ * empty memory at its first token,
+ *     e_t = v_t - a_t M_{t-1} k_t        (what the decayed memory gets wrong at k_t)
+ *     M_t = a_t M_{t-1} + beta_t e_t k_t^T,   a_t = exp(log_alpha_t),
+ * and everything else -- the cached states, the gates, the aggregations -- as mc_forward.
+ * One segment (seg_len >= L) is the plain gated delta rule, whatever the aggregation; then
+ * u is not read.
+ *   log_alpha, beta : [B][H][L], of q's element type.  log_alpha <= 0 (values below -60, and
+ *                     -inf, count as -60: a decay by one part in 1e26); a segment's first one
+ *                     meets an empty memory.  beta is any number; with unit keys the memory
+ *                     stays bounded for beta in [0, 2].
+ *   states          : as mc_forward (fp32 whatever the element type); may be NULL.
+ *   is_bf16         : q, k, v, u, log_alpha, beta and y are bf16 if non-zero, fp32 otherwise.
+ *   Every d of mc_forward and any seg_len; errors as mc_forward.
+ */
+int mc_forward_delta(const void *q, const void *k, const void *v, const void *u,
+                     const void *log_alpha, const void *beta, int B, int H, int L, int d,
+                     int seg_len, int agg_mode, int topk, void *y, float *states, int is_bf16,
+                     mc_stream_t stream);
+
+/*
+ * mc_backward_delta -- gradients of <y, dy> for mc_forward_delta: dq, dk, dv, du as
+ * mc_backward, and dlog_alpha, dbeta [B][H][L] (written, of the element type; dlog_alpha is
+ * zero at a segment's first token).  The states have no gradient of their own (a loss reads
+ * them through y).  du may be NULL for MC_RESIDUAL and MC_MEAN; if given it is zeroed.  No
+ * input may share memory with an output.  The call recomputes the forward in scratch (for
+ * fp32 inputs two d x d fp32 states per 64 tokens and head, about 4 L d more floats).
+ */
+int mc_backward_delta(const void *q, const void *k, const void *v, const void *u,
+                      const void *log_alpha, const void *beta, const void *dy, int B, int H, int L,
+                      int d, int seg_len, int agg_mode, int topk, void *dq, void *dk, void *dv,
+                      void *du, void *dlog_alpha, void *dbeta, int is_bf16, mc_stream_t stream);
+
+/*
+ * mc_decode_step_delta -- mc_decode_step over the gated delta memory: log_alpha and beta are
+ * the token's, [B][H], of q's element type; caches, rules and errors as mc_decode_step.  Run
+ * from t = 0 it reproduces mc_forward_delta token by token.
+ */
+int mc_decode_step_delta(const void *q, const void *k, const void *v, const void *u,
+                         const void *log_alpha, const void *beta, int B, int H, int d, int seg_len,
+                         int agg_mode, int topk, int t, float *states, float *kbar, float *online,
+                         float *ksum, int n_max, void *y, int is_bf16, mc_stream_t stream);
+
+/*
+ * mc_decode_step_evict -- a decoding step that never runs out of cache.  The n_max slots of
+ * every head hold the segments that slot_seg names, in any order, and each gathers the gate
+ * weight of the tokens that read it:
+ *   mass     : fp32 [B][H][n_max] (in/out), mass_i += g_{t,i}.
+ *   slot_seg : int32 [B][H][n_max] (in/out), the segment a slot holds, -1 if it is empty.
+ * At a segment's last token its memory and mean key go to the first empty slot or, if there is
+ * none, replace the segment with the least mass (this token's weight included; equal mass: the
+ * oldest) among those that are not the `protect` newest completed ones; its own mass starts at
+ * 0.  Heads choose independently.  The token still reads the segment that it drives out.
+ *   t        : the token's position, any number >= 0.  Start from empty slots (slot_seg = -1,
+ *              mass = 0) at t = 0, or from mc_cache_compact's cache at t = L.
+ *   log_alpha, beta : the token's, for the gated delta memory; both NULL for the linear one.
+ *   agg_mode : MC_GRM, MC_SOUP or MC_SSC (equal scores: the older segment first); the
+ *              aggregations with constant gates return MC_ERR_MODE.
+ *   protect  : 0 .. n_max - 1; n_max: 1 .. 64.
+ *   Other arguments and errors as mc_decode_step.
+ */
+int mc_decode_step_evict(const void *q, const void *k, const void *v, const void *u,
+                         const void *log_alpha, const void *beta, int B, int H, int d, int seg_len,
+                         int agg_mode, int topk, int t, int protect, float *states, float *kbar,
+                         float *mass, int32_t *slot_seg, float *online, float *ksum, int n_max,
+                         void *y, int is_bf16, mc_stream_t stream);
+
+/*
+ * mc_cache_compact -- from a prefill of any number of segments to a decoding cache of n_max
+ * slots.  Every complete segment's mass is the gate weight that the prefill's later tokens gave
+ * it (fp32, summed in a fixed order).  The min(protect, complete) newest complete segments stay;
+ * of the others those with the most mass (equal mass: the newer) fill the rest of the n_max
+ * slots.  Slots come in order of time, empty ones (fewer complete segments than slots) last:
+ * zeros, with slot_seg -1.  A last, incomplete segment becomes the online memory (zeros if
+ * there is none); decoding goes on at t = L.
+ *   k, u           : the prefill's, [B][H][L][d], bf16 if is_bf16 != 0 else fp32.
+ *   prefill_states : the prefill's states, fp32 [B][H][N][d][d], N = ceil(L / seg_len) <= 16384.
+ *   states, kbar, mass, slot_seg, online, ksum : the cache, as mc_decode_step_evict; written.
+ *   prefill_mass   : fp32 [B][H][N], every segment's mass (0 for the last one); may be NULL.
+ *   agg_mode, topk : the prefill's; MC_GRM, MC_SOUP or MC_SSC, else MC_ERR_MODE.
+ *   protect        : 0 .. n_max; n_max: 1 .. 64.
+ *   The cache shares no memory with the prefill's states.  Errors as mc_forward.
+ */
+int mc_cache_compact(const void *k, const void *u, const float *prefill_states, int B, int H, int L,
+                     int d, int seg_len, int agg_mode, int topk, int protect, float *states,
+                     float *kbar, float *mass, int32_t *slot_seg, float *online, float *ksum,
+                     int n_max, float *prefill_mass, int is_bf16, mc_stream_t stream);
+
+/*
  * mc_ssc_select -- the SSC router alone ([MC-sum §3.4]), for inspection and tests.
  *   k, u     : [B][H][L][d], bf16 if is_bf16 != 0 else fp32, device.
  *   idx      : int32 [B][H][L][topk], written: for token t of segment s, the

@@ -24,7 +24,8 @@ MC_ERR_NULL, MC_ERR_SHAPE, MC_ERR_MODE, MC_ERR_TOPK = -1, -2, -3, -4
 MC_ERR_ALLOC, MC_ERR_CUDA, MC_ERR_DEVICE_TIMEOUT, MC_ERR_ALIGN, MC_ERR_DEVICE = -5, -6, -7, -8, -9
 MC_ERR_SCRATCH = -10
 
-EXPORTED = ("mc_forward", "mc_forward_f32", "mc_forward_swla", "mc_forward_segments", "mc_log_segments", "mc_backward", "mc_backward_f32", "mc_decode_step", "mc_ssc_select", "mc_forward_host", "mc_forward_noalloc",
+EXPORTED = ("mc_forward", "mc_forward_f32", "mc_forward_swla", "mc_forward_segments", "mc_log_segments", "mc_backward", "mc_backward_f32", "mc_decode_step", "mc_forward_delta", "mc_backward_delta",
+            "mc_decode_step_delta", "mc_decode_step_evict", "mc_cache_compact", "mc_ssc_select", "mc_forward_host", "mc_forward_noalloc",
             "mc_check_device", "mc_trim_scratch", "mc_set_readout_form", "mc_profile_begin", "mc_profile_end",
             "mc_profile_stage", "mc_status_string")
 MC_READOUT_AUTO, MC_READOUT_FACTORISED = 0, 1
@@ -65,6 +66,16 @@ def load_library():
     lib.mc_backward_f32.restype = i
     lib.mc_decode_step.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, i, vp, vp, vp, vp, i, vp, i, vp]
     lib.mc_decode_step.restype = i
+    lib.mc_forward_delta.argtypes = [vp] * 6 + [i] * 7 + [vp, vp, i, vp]
+    lib.mc_forward_delta.restype = i
+    lib.mc_backward_delta.argtypes = [vp] * 7 + [i] * 7 + [vp] * 6 + [i, vp]
+    lib.mc_backward_delta.restype = i
+    lib.mc_decode_step_delta.argtypes = [vp] * 6 + [i] * 7 + [vp] * 4 + [i, vp, i, vp]
+    lib.mc_decode_step_delta.restype = i
+    lib.mc_decode_step_evict.argtypes = [vp] * 6 + [i] * 8 + [vp] * 6 + [i, vp, i, vp]
+    lib.mc_decode_step_evict.restype = i
+    lib.mc_cache_compact.argtypes = [vp] * 3 + [i] * 8 + [vp] * 6 + [i, vp, i, vp]
+    lib.mc_cache_compact.restype = i
     lib.mc_ssc_select.argtypes = [vp, vp, i, i, i, i, i, i, vp, i, vp]
     lib.mc_ssc_select.restype = i
     lib.mc_forward_host.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, i, vp, vp, i, vp]
@@ -305,6 +316,210 @@ def mc_backward(q, k, v, u, dy, seg_len: int, agg_mode: int, topk: int = 0, *, d
     if st != MC_OK:
         raise MCError(st, "mc_backward")
     return (*out, du)
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _sequence_args(q, named, dims):
+    """Check that q has ``dims`` dimensions and a supported dtype and that the ``named`` tensors
+    (name, tensor, shape or None for q's) match it; returns (shape, device, dtype)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != dims:
+        raise ValueError("q must be [B, H, L, d]" if dims == 4 else "q must be [B, H, d]")
+    if q.device.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    if q.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("inputs must be bf16 or fp32")
+    for name, t, shape in named:
+        _check(t, name, q.dtype, q.shape if shape is None else shape, q.device)
+    return q.shape, q.device, q.dtype
+
+
+def _new(t, name, dtype, shape, dev):
+    t = torch.empty(shape, dtype=dtype, device=dev) if t is None else t
+    _check(t, name, dtype, shape, dev)
+    return t
+
+
+def _on(device):
+    """The library works on the current device: make it the tensors'."""
+    return torch.cuda.device(device)
+
+
+def mc_forward_delta(q, k, v, u, log_alpha, beta, seg_len: int, agg_mode: int, topk: int = 0, *, y=None, states=None,
+                     want_states: bool = True, stream=None):
+    """Forward over the gated delta memory (``mc_forward_delta`` in mc.h); bf16 or fp32 inputs, log_alpha
+    and beta [B, H, L] of the same dtype.  u may be None for Residual and Mean, and when one segment
+    covers the sequence with one of these.  Returns (y, states); states is None when ``want_states`` is
+    False and none was given."""
+    (B, H, L, d), dev, dtype = _sequence_args(q, [("q", q, None), ("k", k, None), ("v", v, None)], 4)
+    if u is not None:
+        _check(u, "u", dtype, q.shape, dev)
+    _check(log_alpha, "log_alpha", dtype, (B, H, L), dev)
+    _check(beta, "beta", dtype, (B, H, L), dev)
+    y = _new(y, "y", dtype, q.shape, dev)
+    if states is not None or want_states:
+        N = num_segments(L, seg_len) if seg_len >= 1 else 1
+        states = _new(states, "states", torch.float32, (B, H, N, d, d), dev)
+    with _on(dev):
+        st = load_library().mc_forward_delta(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(u), log_alpha.data_ptr(), beta.data_ptr(), B, H, L, d,
+            int(seg_len), int(agg_mode), int(topk), y.data_ptr(), _ptr(states), int(dtype == torch.bfloat16),
+            _stream_handle(stream, dev))
+    if st != MC_OK:
+        raise MCError(st, "mc_forward_delta")
+    return y, states
+
+
+def mc_backward_delta(q, k, v, u, log_alpha, beta, dy, seg_len: int, agg_mode: int, topk: int = 0, *, dq=None, dk=None,
+                      dv=None, du=None, dlog_alpha=None, dbeta=None, stream=None):
+    """Gradients (dq, dk, dv, du, dlog_alpha, dbeta) of <y, dy> for :func:`mc_forward_delta`
+    (``mc_backward_delta`` in mc.h).  du is None for Residual and Mean unless a buffer is given (then it
+    is zeroed)."""
+    (B, H, L, d), dev, dtype = _sequence_args(
+        q, [("q", q, None), ("k", k, None), ("v", v, None), ("dy", dy, None)], 4)
+    if u is not None:
+        _check(u, "u", dtype, q.shape, dev)
+    _check(log_alpha, "log_alpha", dtype, (B, H, L), dev)
+    _check(beta, "beta", dtype, (B, H, L), dev)
+    dq, dk, dv = (_new(t, n, dtype, q.shape, dev) for t, n in ((dq, "dq"), (dk, "dk"), (dv, "dv")))
+    if du is not None or agg_mode in (MC_GRM, MC_SOUP, MC_SSC):
+        du = _new(du, "du", dtype, q.shape, dev)
+    dlog_alpha = _new(dlog_alpha, "dlog_alpha", dtype, (B, H, L), dev)
+    dbeta = _new(dbeta, "dbeta", dtype, (B, H, L), dev)
+    with _on(dev):
+        st = load_library().mc_backward_delta(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(u), log_alpha.data_ptr(), beta.data_ptr(), dy.data_ptr(),
+            B, H, L, d, int(seg_len), int(agg_mode), int(topk), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(du),
+            dlog_alpha.data_ptr(), dbeta.data_ptr(), int(dtype == torch.bfloat16), _stream_handle(stream, dev))
+    if st != MC_OK:
+        raise MCError(st, "mc_backward_delta")
+    return dq, dk, dv, du, dlog_alpha, dbeta
+
+
+class DeltaMemoryCaching(torch.autograd.Function):
+    """Autograd wrapper of the gated delta memory: y = DeltaMemoryCaching.apply(q, k, v, u, log_alpha,
+    beta, seg_len, agg_mode, topk) runs ``mc_forward_delta`` and, on backward, ``mc_backward_delta``
+    (u may be None for Residual and Mean)."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, u, log_alpha, beta, seg_len: int, agg_mode: int, topk: int = 0):
+        y, _ = mc_forward_delta(q, k, v, u, log_alpha, beta, seg_len, agg_mode, topk, want_states=False)
+        ctx.save_for_backward(q, k, v, u, log_alpha, beta)
+        ctx.cfg = (seg_len, agg_mode, topk)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        q, k, v, u, log_alpha, beta = ctx.saved_tensors
+        dq, dk, dv, du, dla, dbe = mc_backward_delta(q, k, v, u, log_alpha, beta, dy.contiguous(), *ctx.cfg)
+        if u is None:
+            du = None
+        elif du is None:
+            du = torch.zeros_like(u)
+        return dq, dk, dv, du, dla, dbe, None, None, None
+
+
+class EvictingCache(DecodeCache):
+    """A :class:`DecodeCache` of ``n_max`` slots that never fills up: each slot also has the gate weight
+    that its segment gathered (``mass`` [B, H, n_max], fp32) and the segment it holds (``slot_seg``,
+    int32, -1 empty).  The ``protect`` newest completed segments are never evicted."""
+
+    def __init__(self, B: int, H: int, d: int, seg_len: int, n_max: int, protect: int = 1, device="cuda"):
+        super().__init__(B, H, d, seg_len, n_max, device)
+        self.protect = int(protect)
+        self.mass = torch.zeros((B, H, n_max), dtype=torch.float32, device=device)
+        self.slot_seg = torch.full((B, H, n_max), -1, dtype=torch.int32, device=device)
+
+    def copy_(self, other: "EvictingCache") -> "EvictingCache":
+        """Take over another cache's contents and position (to go on from one prompt several times)."""
+        if (other.seg_len, other.n_max, other.protect) != (self.seg_len, self.n_max, self.protect):
+            raise ValueError("the caches differ in seg_len, n_max or protect")
+        for name in ("states", "kbar", "online", "ksum", "mass", "slot_seg"):
+            getattr(self, name).copy_(getattr(other, name))
+        self.t = other.t
+        return self
+
+
+def _cache_args(cache, B, H, d, dev):
+    n = cache.n_max
+    f32 = [("states", (B, H, n, d, d)), ("kbar", (B, H, n, d)), ("online", (B, H, d, d)), ("ksum", (B, H, d))]
+    if isinstance(cache, EvictingCache):
+        f32.append(("mass", (B, H, n)))
+        _check(cache.slot_seg, "slot_seg", torch.int32, (B, H, n), dev)
+    for name, shape in f32:
+        _check(getattr(cache, name), name, torch.float32, shape, dev)
+
+
+def _token_args(cache, q, k, v, u, log_alpha, beta, y):
+    (B, H, d), dev, dtype = _sequence_args(q, [("q", q, None), ("k", k, None), ("v", v, None)], 3)
+    if u is not None:
+        _check(u, "u", dtype, (B, H, d), dev)
+    for t, n in ((log_alpha, "log_alpha"), (beta, "beta")):
+        if t is not None:
+            _check(t, n, dtype, (B, H), dev)
+    _cache_args(cache, B, H, d, dev)
+    return B, H, d, dev, _new(y, "y", dtype, (B, H, d), dev)
+
+
+def mc_decode_step_delta(cache: DecodeCache, q, k, v, u, log_alpha, beta, agg_mode: int, topk: int = 0, *, y=None,
+                         stream=None):
+    """One decoding step over the gated delta memory (``mc_decode_step_delta`` in mc.h): q, k, v, u
+    [B, H, d], log_alpha and beta [B, H]; advances ``cache.t`` and returns y [B, H, d]."""
+    B, H, d, dev, y = _token_args(cache, q, k, v, u, log_alpha, beta, y)
+    with _on(dev):
+        st = load_library().mc_decode_step_delta(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(u), _ptr(log_alpha), _ptr(beta), B, H, d, cache.seg_len,
+            int(agg_mode), int(topk), cache.t, cache.states.data_ptr(), cache.kbar.data_ptr(), cache.online.data_ptr(),
+            cache.ksum.data_ptr(), cache.n_max, y.data_ptr(), int(q.dtype == torch.bfloat16), _stream_handle(stream, dev))
+    if st != MC_OK:
+        raise MCError(st, "mc_decode_step_delta")
+    cache.t += 1
+    return y
+
+
+def mc_decode_step_evict(cache: EvictingCache, q, k, v, u, agg_mode: int, topk: int = 0, *, log_alpha=None, beta=None,
+                         y=None, stream=None):
+    """One decoding step over an :class:`EvictingCache` (``mc_decode_step_evict`` in mc.h), of the linear
+    memory or, with log_alpha and beta [B, H], of the gated delta memory; advances ``cache.t`` and returns
+    y [B, H, d]."""
+    if not isinstance(cache, EvictingCache):
+        raise TypeError("cache must be an EvictingCache")
+    B, H, d, dev, y = _token_args(cache, q, k, v, u, log_alpha, beta, y)
+    with _on(dev):
+        st = load_library().mc_decode_step_evict(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(u), _ptr(log_alpha), _ptr(beta), B, H, d, cache.seg_len,
+            int(agg_mode), int(topk), cache.t, cache.protect, cache.states.data_ptr(), cache.kbar.data_ptr(),
+            cache.mass.data_ptr(), cache.slot_seg.data_ptr(), cache.online.data_ptr(), cache.ksum.data_ptr(),
+            cache.n_max, y.data_ptr(), int(q.dtype == torch.bfloat16), _stream_handle(stream, dev))
+    if st != MC_OK:
+        raise MCError(st, "mc_decode_step_evict")
+    cache.t += 1
+    return y
+
+
+def mc_cache_compact(cache: EvictingCache, k, u, states, agg_mode: int, topk: int = 0, *, mass=None, stream=None):
+    """Fill an :class:`EvictingCache` from a prefill of [B, H, L, d] keys and router inputs and its states
+    [B, H, N, d, d] (``mc_cache_compact`` in mc.h); sets ``cache.t`` to L.  Returns the mass of every
+    segment of the prefill, [B, H, N]."""
+    if not isinstance(cache, EvictingCache):
+        raise TypeError("cache must be an EvictingCache")
+    (B, H, L, d), dev, dtype = _sequence_args(k, [("k", k, None), ("u", u, None)], 4)
+    N = num_segments(L, cache.seg_len)
+    _check(states, "states", torch.float32, (B, H, N, d, d), dev)
+    _cache_args(cache, B, H, d, dev)
+    mass = _new(mass, "mass", torch.float32, (B, H, N), dev)
+    with _on(dev):
+        st = load_library().mc_cache_compact(
+            k.data_ptr(), u.data_ptr(), states.data_ptr(), B, H, L, d, cache.seg_len, int(agg_mode), int(topk),
+            cache.protect, cache.states.data_ptr(), cache.kbar.data_ptr(), cache.mass.data_ptr(),
+            cache.slot_seg.data_ptr(), cache.online.data_ptr(), cache.ksum.data_ptr(), cache.n_max, mass.data_ptr(),
+            int(dtype == torch.bfloat16), _stream_handle(stream, dev))
+    if st != MC_OK:
+        raise MCError(st, "mc_cache_compact")
+    cache.t = L
+    return mass
 
 
 class MemoryCaching(torch.autograd.Function):

@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kThreads) bwd_gates_simt(BwdArgs a)
     }
 
     // the online memory: dg_on = dy_t . O_on[t], dq += g_on M_t^T dy_t
-    const float *Oon = a.O_on + base, *Xon = a.X_on + base;
+    const float *Oon = a.O_on + base, *Xon = a.X_on ? a.X_on + base : nullptr;
     float dgon[TPT];
 #pragma unroll
     for (int p = 0; p < TPT; ++p) {
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kThreads) bwd_gates_simt(BwdArgs a)
             for (int r = 0; r < RB; ++r) {
                 const size_t gi = (size_t)(tb + t) * D + tx + 16 * r;
                 part = fmaf(Ys[t * P + tx + 16 * r], Oon[gi], part);
-                dq[p][r] = fmaf(g, Xon[gi], dq[p][r]);
+                if (Xon) dq[p][r] = fmaf(g, Xon[gi], dq[p][r]);
             }
         }
 #pragma unroll
@@ -374,7 +374,8 @@ __global__ void __launch_bounds__(kThreads) bwd_gates_simt(BwdArgs a)
         for (int r = 0; r < RB; ++r) {
             const int c = tx + 16 * r;
             const size_t gi = (size_t)(tb + t) * D + c;
-            dqo[gi] = from_f<T>(dq[p][r]);
+            if (a.dq_f32) a.dq_f32[base + gi] = dq[p][r];
+            else dqo[gi] = from_f<T>(dq[p][r]);
             if (gated) {
                 float ps = kpre[c];  // pooled keys of the segment up to t
                 for (int j = 0; j <= t; ++j) ps += Ks[j * P + c];
@@ -1027,8 +1028,9 @@ cudaError_t gates_impl(const Problem &p, const BwdArgs &a, cudaStream_t s)
     return cudaSuccess;
 }
 
+// The gate work and the cached states' gradients G.
 template <typename T, int D>
-cudaError_t backward_impl(const Problem &p, const BwdArgs &a, cudaStream_t s)
+cudaError_t router_impl(const Problem &p, const BwdArgs &a, cudaStream_t s)
 {
     constexpr int P = D + 1;
     cudaError_t e = gates_impl<T, D>(p, a, s);
@@ -1041,6 +1043,15 @@ cudaError_t backward_impl(const Problem &p, const BwdArgs &a, cudaStream_t s)
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         profile_after_kernel(s, "bwd_G_simt");
     }
+    return cudaSuccess;
+}
+
+template <typename T, int D>
+cudaError_t backward_impl(const Problem &p, const BwdArgs &a, cudaStream_t s)
+{
+    constexpr int P = D + 1;
+    cudaError_t e = router_impl<T, D>(p, a, s);
+    if (e != cudaSuccess) return e;
     {
         constexpr int TC = D >= 128 ? 32 : 64;
         constexpr int TP = TC + 1;
@@ -1132,6 +1143,8 @@ size_t backward_scratch_bytes(const Problem &p)
     const size_t sel = p.mode == MC_SSC ? (size_t)p.topk : 0;
     return common + pad256(4 * BH * L) + 2 * pad256(4 * BH * L * d) + 2 * pad256(4 * BH * L * sel);
 }
+
+cudaError_t launch_bwd_router_simt(const Problem &p, const BwdArgs &a, cudaStream_t s) { MC_BWD_DISPATCH(router_impl, p, a, s); }
 
 cudaError_t launch_backward_simt(const Problem &p, const void *q, const void *k, const void *v, const void *u,
                                  const void *dy, void *dq, void *dk, void *dv, void *du, void *scratch,

@@ -1,0 +1,581 @@
+// k_delta_simt.cu -- CUDA-core (FFMA) kernels of the gated delta memory: its forward scan, its
+// reverse scan and the gradients, for fp32 inputs and for d in {16, 32} (fp32 arithmetic end to
+// end), and the pooled-key sums that every delta path needs.
+//
+// Per (b,h) and segment, from an empty memory, with a_t = exp(log_alpha_t):
+//   e_t = v_t - a_t M_{t-1} k_t            the error of the decayed memory at the new key
+//   M_t = a_t M_{t-1} + beta_t e_t k_t^T   the write,   o_t = M_t q_t   the read
+// Value row r of M depends on row r of v alone, so the rows are independent walkers.
+//
+// Adjoint, with N_t the gradient of M_t through o_t and every later step, p_t = g_t dy_t:
+//   N_t += p_t q_t^T,  z_t = N_t k_t,  w_t = beta_t z_t,  N_{t-1} = a_t (N_t - w_t k_t^T)
+//   dv_t = w_t,  dbeta_t = z_t . e_t,  dq_t = M_t^T p_t,  dk_t = beta_t N_t^T e_t - a_t M_{t-1}^T w_t
+//   dlog_alpha_t = <N_{t-1}, M_{t-1}> = h_t,  and since o_t and e_t are linear in M,
+//   h_t = h_{t+1} + p_t . o_t - w_t . v_t  (p_t . o_t = dq_t . q_t), restarted from
+//   <N, M> at every 64-token chunk's end so that no rounding runs along a whole segment.
+// The rows of N are independent walkers too.  What sums over rows (dq, dk, dbeta, dlog_alpha) is
+// formed per 64-token chunk from the states at the chunk's two ends: with S the memory before the
+// chunk, R the adjoint after it, c_i the running sum of log_alpha in the chunk, D_ij = exp(c_i - c_j),
+//   B1_ij = D_ij p_i.e_j (i >= j),  B2_ij = D_ij w_i.e_j (i > j)
+//   Y_j   = sum_i B1_ij q_i + D_Cj R^T e_j - sum_i B2_ij k_i          (= N_j^T e_j)
+//   dk_j  = beta_j Y_j - exp(c_j) S^T w_j - sum_i B2_ji beta_i k_i,   dbeta_j = Y_j . k_j
+//   dq_i  = exp(c_i) S^T p_i + sum_j B1_ij beta_j k_j
+#include <cstdint>
+
+#include "mc_internal.cuh"
+
+namespace mc {
+namespace {
+
+constexpr int kCH = kDeltaChunk;  // 64 tokens
+
+template <typename F>
+cudaError_t set_smem(F *kern, size_t bytes)
+{
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+// A row of M lies on G neighbouring lanes, KPL keys each: lane g holds the 16-byte pieces
+// g, g + G, ... of the row, so that the lanes of a row read one run of shared memory.
+template <int D>
+struct RowSplit {
+    static constexpr int KPL = D >= 64 ? 16 : 8;
+    static constexpr int G = D / KPL;
+    static constexpr int RW = 32 / G;                          // rows per warp
+    static constexpr int W = D / RW < 4 ? D / RW : 4;          // warps per CTA
+    static constexpr int RC = RW * W;                          // rows per CTA
+    static constexpr int TT = 16;                              // tokens staged at once
+};
+
+template <int D>
+__device__ __forceinline__ void load_keys(float (&x)[RowSplit<D>::KPL], const float *row, int g)
+{
+    constexpr int G = RowSplit<D>::G;
+#pragma unroll
+    for (int m = 0; m < RowSplit<D>::KPL / 4; ++m) {
+        const float4 f = reinterpret_cast<const float4 *>(row)[g + G * m];
+        x[4 * m] = f.x; x[4 * m + 1] = f.y; x[4 * m + 2] = f.z; x[4 * m + 3] = f.w;
+    }
+}
+
+template <int D>
+__device__ __forceinline__ void store_keys(float *row, const float (&x)[RowSplit<D>::KPL], int g)
+{
+    constexpr int G = RowSplit<D>::G;
+#pragma unroll
+    for (int m = 0; m < RowSplit<D>::KPL / 4; ++m)
+        reinterpret_cast<float4 *>(row)[g + G * m] = make_float4(x[4 * m], x[4 * m + 1], x[4 * m + 2], x[4 * m + 3]);
+}
+
+template <int D>
+__device__ __forceinline__ float dot_keys(const float (&x)[RowSplit<D>::KPL], const float (&y)[RowSplit<D>::KPL])
+{
+    float p[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < RowSplit<D>::KPL; ++i) p[i & 3] = fmaf(x[i], y[i], p[i & 3]);
+    float s = (p[0] + p[1]) + (p[2] + p[3]);
+#pragma unroll
+    for (int o = RowSplit<D>::G / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+
+// ---------------------------------------------------------------------------
+// delta_scan_simt: one CTA per (bh, segment, RC value rows).  Bound by the chain of one token
+// to the next (two dot products of a row, about 0.1 us a token); it keeps the row in registers
+// and the rows, heads and segments run side by side.
+// ---------------------------------------------------------------------------
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * RowSplit<D>::W) delta_scan_simt(DeltaArgs a)
+{
+    using R = RowSplit<D>;
+    constexpr int NT = 32 * R::W;
+    __shared__ __align__(16) float Ks[R::TT * D], Qs[R::TT * D], Vs[R::TT * R::RC];
+    __shared__ float As[R::TT], Bs[R::TT];
+    constexpr int splits = D / R::RC;
+    const int rs = blockIdx.x % splits;
+    const int seg = (int)(blockIdx.x / splits) % a.N, bh = (int)(blockIdx.x / splits) / a.N;
+    const int t0 = seg * a.C, t1 = min(t0 + a.C, a.L);
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane % R::G;
+    const int rl = warp * R::RW + lane / R::G, row = rs * R::RC + rl;
+    const size_t base = (size_t)bh * a.L * D, sbase = (size_t)bh * a.L;
+    const T *q = static_cast<const T *>(a.q) + base, *k = static_cast<const T *>(a.k) + base;
+    const T *v = static_cast<const T *>(a.v) + base;
+    const T *la = static_cast<const T *>(a.la) + sbase, *be = static_cast<const T *>(a.be) + sbase;
+    float M[R::KPL], x[R::KPL];
+#pragma unroll
+    for (int i = 0; i < R::KPL; ++i) M[i] = 0.f;
+    for (int c0 = t0; c0 < t1; c0 += R::TT) {
+        const int cnt = min(R::TT, t1 - c0);
+        if (a.S_c && (c0 - t0) % kCH == 0)
+            store_keys<D>(a.S_c + (((size_t)bh * a.N + seg) * a.NCH + (c0 - t0) / kCH) * D * D + (size_t)row * D, M, g);
+        __syncthreads();
+        for (int e = tid; e < cnt * D; e += NT) {
+            Ks[e] = to_f(k[(size_t)c0 * D + e]);
+            Qs[e] = to_f(q[(size_t)c0 * D + e]);
+        }
+        for (int e = tid; e < cnt * R::RC; e += NT)
+            Vs[e] = to_f(v[(size_t)(c0 + e / R::RC) * D + rs * R::RC + e % R::RC]);
+        if (tid < cnt) {
+            As[tid] = delta_decay(to_f(la[c0 + tid]));
+            Bs[tid] = to_f(be[c0 + tid]);
+        }
+        __syncthreads();
+        for (int t = 0; t < cnt; ++t) {
+            const float at = As[t];
+            load_keys<D>(x, Ks + t * D, g);
+            const float e = Vs[t * R::RC + rl] - at * dot_keys<D>(M, x);
+            const float ue = Bs[t] * e;
+#pragma unroll
+            for (int i = 0; i < R::KPL; ++i) M[i] = fmaf(ue, x[i], at * M[i]);
+            load_keys<D>(x, Qs + t * D, g);
+            const float o = dot_keys<D>(M, x);
+            if (g == 0) {
+                const size_t at_ = base + (size_t)(c0 + t) * D + row;
+                if (a.y) static_cast<T *>(a.y)[at_] = from_f<T>(o);
+                if (a.O_on) a.O_on[at_] = o;
+                if (a.E) a.E[at_] = e;
+            }
+        }
+    }
+    if (a.states) store_keys<D>(a.states + ((size_t)bh * a.N + seg) * D * D + (size_t)row * D, M, g);
+}
+
+// The same walk backwards over the adjoint N: dv_t = w_t (and fp32 w for the chunks), R at every chunk's end.
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * RowSplit<D>::W) delta_rscan_simt(DeltaArgs a)
+{
+    using R = RowSplit<D>;
+    constexpr int NT = 32 * R::W;
+    __shared__ __align__(16) float Ks[R::TT * D], Qs[R::TT * D], Ps[R::TT * R::RC];
+    __shared__ float As[R::TT], Bs[R::TT], Gs[R::TT];
+    constexpr int splits = D / R::RC;
+    const int rs = blockIdx.x % splits;
+    const int seg = (int)(blockIdx.x / splits) % a.N, bh = (int)(blockIdx.x / splits) / a.N;
+    const int t0 = seg * a.C, t1 = min(t0 + a.C, a.L);
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane % R::G;
+    const int rl = warp * R::RW + lane / R::G, row = rs * R::RC + rl;
+    const size_t base = (size_t)bh * a.L * D, sbase = (size_t)bh * a.L;
+    const T *q = static_cast<const T *>(a.q) + base, *k = static_cast<const T *>(a.k) + base;
+    const T *dy = static_cast<const T *>(a.dy) + base;
+    const T *la = static_cast<const T *>(a.la) + sbase, *be = static_cast<const T *>(a.be) + sbase;
+    T *dv = static_cast<T *>(a.dv) + base;
+    float N[R::KPL], kx[R::KPL], qx[R::KPL];
+    if (a.G && seg < a.N - 1)
+        load_keys<D>(N, a.G + ((size_t)bh * a.N + seg) * D * D + (size_t)row * D, g);
+    else {
+#pragma unroll
+        for (int i = 0; i < R::KPL; ++i) N[i] = 0.f;
+    }
+    const int nt = (t1 - t0 + R::TT - 1) / R::TT;
+    for (int ti = nt - 1; ti >= 0; --ti) {
+        const int c0 = t0 + ti * R::TT, cnt = min(R::TT, t1 - c0);
+        if (c0 + cnt == t1 || (c0 + cnt - t0) % kCH == 0)
+            store_keys<D>(a.R_c + (((size_t)bh * a.N + seg) * a.NCH + (c0 - t0) / kCH) * D * D + (size_t)row * D, N, g);
+        __syncthreads();
+        for (int e = tid; e < cnt * D; e += NT) {
+            Ks[e] = to_f(k[(size_t)c0 * D + e]);
+            Qs[e] = to_f(q[(size_t)c0 * D + e]);
+        }
+        for (int e = tid; e < cnt * R::RC; e += NT)
+            Ps[e] = to_f(dy[(size_t)(c0 + e / R::RC) * D + rs * R::RC + e % R::RC]);
+        if (tid < cnt) {
+            As[tid] = delta_decay(to_f(la[c0 + tid]));
+            Bs[tid] = to_f(be[c0 + tid]);
+            Gs[tid] = a.tok ? a.tok[(sbase + c0 + tid) * kBwdTokWords + 2] : 1.f;
+        }
+        __syncthreads();
+        for (int t = cnt - 1; t >= 0; --t) {
+            load_keys<D>(qx, Qs + t * D, g);
+            load_keys<D>(kx, Ks + t * D, g);
+            const float p = Gs[t] * Ps[t * R::RC + rl];
+#pragma unroll
+            for (int i = 0; i < R::KPL; ++i) N[i] = fmaf(p, qx[i], N[i]);
+            const float w = Bs[t] * dot_keys<D>(N, kx);
+            const float at = As[t];
+#pragma unroll
+            for (int i = 0; i < R::KPL; ++i) N[i] = at * fmaf(-w, kx[i], N[i]);
+            if (g == 0) {
+                const size_t at_ = (size_t)(c0 + t) * D + row;
+                dv[at_] = from_f<T>(w);
+                a.W[base + at_] = w;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// delta_grads_simt: one CTA per (bh, segment, 64-token chunk): everything that sums over value
+// rows, as in the header.  Tiles of q, k, p, e, w in shared memory (fp32, rows padded by one word);
+// S and R come through in blocks of 32 rows.  tx = tid % 16, ty = tid / 16: a thread owns tokens
+// ty + 16 p and dimensions tx + 16 r.
+// ---------------------------------------------------------------------------
+constexpr int kGT = 256;
+constexpr int kGB = 32;  // rows of S and R at once (16 for d = 16)
+
+template <int D>
+constexpr size_t grads_smem()
+{
+    return sizeof(float) * (5 * kCH * (D + 1) + 2 * kCH * (kCH + 1) + (D < kGB ? D : kGB) * (D + 1) + 6 * kCH + 32);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kGT) delta_grads_simt(DeltaArgs a)
+{
+    constexpr int P = D + 1, BP = kCH + 1, RB = D / 16, TP = kCH / 16, GB = D < kGB ? D : kGB;
+    extern __shared__ float sm[];
+    float *Qs = sm, *Ks = Qs + kCH * P, *Ps = Ks + kCH * P, *Es = Ps + kCH * P, *Ws = Es + kCH * P;
+    float *B1 = Ws + kCH * P, *B2 = B1 + kCH * BP, *Ms = B2 + kCH * BP;
+    float *cum = Ms + GB * P, *bet = cum + kCH, *hd = bet + kCH, *hb = hd + kCH, *dbe = hb + kCH, *red = dbe + kCH;
+
+    const int ch = (int)blockIdx.x % a.NCH;
+    const int seg = (int)(blockIdx.x / a.NCH) % a.N, bh = (int)(blockIdx.x / a.NCH) / a.N;
+    const int t0 = seg * a.C, tb = t0 + ch * kCH, te = min(min(tb + kCH, t0 + a.C), a.L);
+    if (tb >= te) return;
+    const int cnt = te - tb, last = cnt - 1;
+    const size_t base = (size_t)bh * a.L * D, sbase = (size_t)bh * a.L;
+    const T *q = static_cast<const T *>(a.q) + base, *k = static_cast<const T *>(a.k) + base;
+    const T *v = static_cast<const T *>(a.v) + base, *dy = static_cast<const T *>(a.dy) + base;
+    const T *u = a.rho ? static_cast<const T *>(a.u) + base : nullptr;
+    const T *la = static_cast<const T *>(a.la) + sbase, *be = static_cast<const T *>(a.be) + sbase;
+    const size_t cidx = ((size_t)bh * a.N + seg) * a.NCH + ch;
+    const float *S = a.S_c + cidx * D * D, *Rc = a.R_c + cidx * D * D;
+    const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
+
+    for (int e = tid; e < kCH * D; e += kGT) {
+        const int r = e / D, c = e % D;
+        const bool ok = r < cnt;
+        const size_t gi = (size_t)(tb + r) * D + c;
+        const float gon = ok && a.tok ? a.tok[(sbase + tb + r) * kBwdTokWords + 2] : 1.f;
+        Qs[r * P + c] = ok ? to_f(q[gi]) : 0.f;
+        Ks[r * P + c] = ok ? to_f(k[gi]) : 0.f;
+        Ps[r * P + c] = ok ? gon * to_f(dy[gi]) : 0.f;
+        Es[r * P + c] = ok ? a.E[base + gi] : 0.f;
+        Ws[r * P + c] = ok ? a.W[base + gi] : 0.f;
+    }
+    if (tid < kCH) {
+        cum[tid] = tid < cnt ? delta_log(to_f(la[tb + tid])) : 0.f;
+        bet[tid] = tid < cnt ? to_f(be[tb + tid]) : 0.f;
+        hd[tid] = hb[tid] = dbe[tid] = 0.f;
+    }
+    __syncthreads();
+    if (tid == 0)
+        for (int i = 1; i < kCH; ++i) cum[i] += cum[i - 1];
+    __syncthreads();
+    const float cend = cum[last];
+    for (int e = tid; e < kCH * kCH; e += kGT) {
+        const int i = e / kCH, j = e % kCH;
+        float b1 = 0.f, b2 = 0.f;
+        if (j <= i && i < cnt) {
+            for (int c = 0; c < D; ++c) {
+                b1 = fmaf(Ps[i * P + c], Es[j * P + c], b1);
+                b2 = fmaf(Ws[i * P + c], Es[j * P + c], b2);
+            }
+            const float dec = expf(cum[i] - cum[j]);
+            b1 *= dec;
+            b2 = j < i ? b2 * dec : 0.f;
+        }
+        B1[i * BP + j] = b1;
+        B2[i * BP + j] = b2;
+    }
+    // P S, W S, E R (rows of S and R by blocks)
+    float xs[TP][RB], ws[TP][RB], er[TP][RB];
+#pragma unroll
+    for (int p = 0; p < TP; ++p)
+#pragma unroll
+        for (int r = 0; r < RB; ++r) xs[p][r] = ws[p][r] = er[p][r] = 0.f;
+    float inner = 0.f;  // <R, S>, by element
+    for (int b = 0; b < D; b += GB) {
+        __syncthreads();
+        for (int e = tid; e < GB * D; e += kGT) {
+            const float s = S[(size_t)b * D + e];
+            inner = fmaf(s, Rc[(size_t)b * D + e], inner);
+            Ms[(e / D) * P + e % D] = s;
+        }
+        __syncthreads();
+        for (int c = 0; c < GB; ++c) {
+            float m[RB];
+#pragma unroll
+            for (int r = 0; r < RB; ++r) m[r] = Ms[c * P + tx + 16 * r];
+#pragma unroll
+            for (int p = 0; p < TP; ++p) {
+                const float pv = Ps[(ty + 16 * p) * P + b + c], wv = Ws[(ty + 16 * p) * P + b + c];
+#pragma unroll
+                for (int r = 0; r < RB; ++r) {
+                    xs[p][r] = fmaf(pv, m[r], xs[p][r]);
+                    ws[p][r] = fmaf(wv, m[r], ws[p][r]);
+                }
+            }
+        }
+        __syncthreads();
+        for (int e = tid; e < GB * D; e += kGT) Ms[(e / D) * P + e % D] = Rc[(size_t)b * D + e];
+        __syncthreads();
+        for (int c = 0; c < GB; ++c) {
+            float m[RB];
+#pragma unroll
+            for (int r = 0; r < RB; ++r) m[r] = Ms[c * P + tx + 16 * r];
+#pragma unroll
+            for (int p = 0; p < TP; ++p) {
+                const float ev = Es[(ty + 16 * p) * P + b + c];
+#pragma unroll
+                for (int r = 0; r < RB; ++r) er[p][r] = fmaf(ev, m[r], er[p][r]);
+            }
+        }
+    }
+    // <R, S> of the chunk over the CTA, in a fixed order
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) inner += __shfl_xor_sync(0xffffffffu, inner, o);
+    if (tid % 32 == 0) red[tid / 32] = inner;
+    T *dqo = static_cast<T *>(a.dq) + base, *dko = static_cast<T *>(a.dk) + base;
+    float dk[TP][RB];
+#pragma unroll
+    for (int p = 0; p < TP; ++p) {
+        const int t = ty + 16 * p;
+        const float ge = expf(cum[t]), gr = expf(cend - cum[t]);
+        float dq[RB], y[RB], kk[RB];
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+            dq[r] = ge * xs[p][r];
+            y[r] = gr * er[p][r];
+            kk[r] = -ge * ws[p][r];
+        }
+        float hpart = 0.f;  // beta_t D_Ct (R^T e_t) . k_t, the chunk's own share of <R, M at its end>
+#pragma unroll
+        for (int r = 0; r < RB; ++r) hpart = fmaf(y[r], Ks[t * P + tx + 16 * r], hpart);
+        for (int j = 0; j <= t; ++j) {
+            const float b1 = B1[t * BP + j] * bet[j], b2 = B2[t * BP + j] * bet[j];
+#pragma unroll
+            for (int r = 0; r < RB; ++r) {
+                const float kj = Ks[j * P + tx + 16 * r];
+                dq[r] = fmaf(b1, kj, dq[r]);
+                kk[r] = fmaf(-b2, kj, kk[r]);
+            }
+        }
+        for (int i = t; i < cnt; ++i) {
+            const float b1 = B1[i * BP + t], b2 = B2[i * BP + t];
+#pragma unroll
+            for (int r = 0; r < RB; ++r)
+                y[r] = fmaf(b1, Qs[i * P + tx + 16 * r], fmaf(-b2, Ks[i * P + tx + 16 * r], y[r]));
+        }
+        float dbp = 0.f, hq = 0.f, hv = 0.f;
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+            const int c = tx + 16 * r;
+            dk[p][r] = fmaf(bet[t], y[r], kk[r]);
+            dbp = fmaf(y[r], Ks[t * P + c], dbp);
+            hq = fmaf(dq[r], Qs[t * P + c], hq);
+            if (t < cnt) {
+                const size_t gi = (size_t)(tb + t) * D + c;
+                hv = fmaf(Ws[t * P + c], to_f(v[gi]), hv);
+                dqo[gi] = from_f<T>(dq[r] + (a.dq_add ? a.dq_add[base + gi] : 0.f));
+            }
+        }
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) {
+            dbp += __shfl_xor_sync(0xffffffffu, dbp, o);
+            hq += __shfl_xor_sync(0xffffffffu, hq, o);
+            hv += __shfl_xor_sync(0xffffffffu, hv, o);
+            hpart += __shfl_xor_sync(0xffffffffu, hpart, o);
+        }
+        if (tx == 0) {
+            dbe[t] = dbp;
+            hd[t] = hq - hv;
+            hb[t] = bet[t] * hpart;
+        }
+    }
+    __syncthreads();
+    if (tid == 0) {  // h backwards over the chunk
+        float in = 0.f;
+        for (int w = 0; w < kGT / 32; ++w) in += red[w];
+        float h = expf(cend) * in;
+        for (int t = 0; t < cnt; ++t) h += hb[t];
+        for (int t = last; t >= 0; --t) {
+            h += hd[t];
+            hd[t] = h;
+        }
+    }
+    // the pooled keys' share of dk: sum over the segment's tokens from t on of w_t' u_t' (word 4 of tok)
+    if (a.rho) {
+        __syncthreads();
+        if (tid < D) {
+            float acc = a.rho[cidx * D + tid];
+            for (int t = last; t >= 0; --t) {
+                acc = fmaf(a.tok[(sbase + tb + t) * kBwdTokWords + 4], to_f(u[(size_t)(tb + t) * D + tid]), acc);
+                Ps[t * P + tid] = acc;
+            }
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < TP; ++p) {
+        const int t = ty + 16 * p;
+        if (t >= cnt) continue;
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+            const int c = tx + 16 * r;
+            dko[(size_t)(tb + t) * D + c] = from_f<T>(dk[p][r] + (a.rho ? Ps[t * P + c] : 0.f));
+        }
+    }
+    if (tid < cnt) {
+        static_cast<T *>(a.dbe)[sbase + tb + tid] = from_f<T>(dbe[tid]);
+        // a segment's first decay meets an empty memory
+        static_cast<T *>(a.dla)[sbase + tb + tid] = from_f<T>(tb + tid == t0 ? 0.f : hd[tid]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Pooled sums over the 64-token chunks of every segment: x_t, or s_t x_t.
+//   pool_sums : per chunk, the sum over its tokens                       -> out [BH][N][NCH][d]
+//   pool_scan : per segment, exclusive prefix (keys; and the key mean) or exclusive suffix
+//               plus dkbar / segment length (the gradient), in place
+//   pool_score: r_on[t] = <u_t, keys of the segment up to t> / their number
+// ---------------------------------------------------------------------------
+template <typename T, int D>
+__global__ void __launch_bounds__(256) pool_sums(DeltaArgs a, const T *x, const float *tok, float *out)
+{
+    __shared__ float part[256];
+    const int ch = (int)blockIdx.x % a.NCH;
+    const int seg = (int)(blockIdx.x / a.NCH) % a.N, bh = (int)(blockIdx.x / a.NCH) / a.N;
+    const int t0 = seg * a.C, tb = t0 + ch * kCH, te = min(min(tb + kCH, t0 + a.C), a.L);
+    constexpr int ways = 256 / D;
+    const int c = threadIdx.x % D, w = threadIdx.x / D;
+    float s = 0.f;
+    for (int t = tb + w; t < te; t += ways) {
+        const size_t tt = (size_t)bh * a.L + t;
+        s = fmaf(tok ? tok[tt * kBwdTokWords + 4] : 1.f, to_f(x[tt * D + c]), s);
+    }
+    part[threadIdx.x] = s;
+    __syncthreads();
+    if (w == 0) {
+#pragma unroll
+        for (int i = 1; i < ways; ++i) s += part[i * D + c];
+        out[(size_t)blockIdx.x * D + c] = s;
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(D) pool_scan(DeltaArgs a, float *sums, float *kbar, const float *dkbar)
+{
+    const int seg = (int)blockIdx.x % a.N, bh = (int)blockIdx.x / a.N, c = threadIdx.x;
+    const int len = min((seg + 1) * a.C, a.L) - seg * a.C, n = (len + kCH - 1) / kCH;
+    float *s = sums + (size_t)blockIdx.x * a.NCH * D + c;
+    if (!dkbar) {
+        float acc = 0.f;
+        for (int i = 0; i < n; ++i) {
+            const float x = s[(size_t)i * D];
+            s[(size_t)i * D] = acc;
+            acc += x;
+        }
+        if (kbar) kbar[((size_t)bh * a.N + seg) * D + c] = acc / (float)len;
+        return;
+    }
+    float acc = dkbar[((size_t)bh * a.N + seg) * D + c] / (float)len;
+    for (int i = n - 1; i >= 0; --i) {
+        const float x = s[(size_t)i * D];
+        s[(size_t)i * D] = acc;
+        acc += x;
+    }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(256) pool_score(DeltaArgs a, const float *kpre, float *r_on)
+{
+    constexpr int P = D + 1;
+    extern __shared__ float sm[];  // kCH x P running key sums
+    const int ch = (int)blockIdx.x % a.NCH;
+    const int seg = (int)(blockIdx.x / a.NCH) % a.N, bh = (int)(blockIdx.x / a.NCH) / a.N;
+    const int t0 = seg * a.C, tb = t0 + ch * kCH, te = min(min(tb + kCH, t0 + a.C), a.L);
+    if (tb >= te) return;
+    const int cnt = te - tb, tid = threadIdx.x;
+    const size_t base = (size_t)bh * a.L * D;
+    const T *k = static_cast<const T *>(a.k) + base, *u = static_cast<const T *>(a.u) + base;
+    for (int e = tid; e < cnt * D; e += 256) sm[(e / D) * P + e % D] = to_f(k[(size_t)tb * D + e]);
+    __syncthreads();
+    if (tid < D) {
+        float acc = kpre[(size_t)blockIdx.x * D + tid];
+        for (int t = 0; t < cnt; ++t) {
+            acc += sm[t * P + tid];
+            sm[t * P + tid] = acc;
+        }
+    }
+    __syncthreads();
+    const int lane = tid % 32;
+    for (int t = tid / 32; t < cnt; t += 8) {
+        float s = 0.f;
+        for (int c = lane; c < D; c += 32) s = fmaf(to_f(u[(size_t)(tb + t) * D + c]), sm[t * P + c], s);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) r_on[(size_t)bh * a.L + tb + t] = s / (float)(tb + t - t0 + 1);
+    }
+}
+
+template <typename T, int D>
+cudaError_t scan_impl(const Problem &p, const DeltaArgs &a, cudaStream_t s)
+{
+    constexpr int splits = D / RowSplit<D>::RC;
+    delta_scan_simt<T, D><<<(unsigned)((long long)p.BH * p.N * splits), 32 * RowSplit<D>::W, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t rscan_impl(const Problem &p, const DeltaArgs &a, cudaStream_t s)
+{
+    constexpr int splits = D / RowSplit<D>::RC;
+    delta_rscan_simt<T, D><<<(unsigned)((long long)p.BH * p.N * splits), 32 * RowSplit<D>::W, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t grads_impl(const Problem &p, const DeltaArgs &a, cudaStream_t s)
+{
+    const size_t smem = grads_smem<D>();
+    auto kern = delta_grads_simt<T, D>;
+    cudaError_t e = set_smem(kern, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)((long long)p.BH * p.N * a.NCH), kGT, smem, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t pool_impl(const Problem &p, const DeltaArgs &a, float *sums, float *kbar, float *r_on, cudaStream_t s)
+{
+    const unsigned chunks = (unsigned)((long long)p.BH * p.N * a.NCH);
+    pool_sums<T, D><<<chunks, 256, 0, s>>>(a, static_cast<const T *>(a.k), nullptr, sums);
+    pool_scan<D><<<(unsigned)((long long)p.BH * p.N), D, 0, s>>>(a, sums, kbar, nullptr);
+    if (r_on) pool_score<T, D><<<chunks, 256, sizeof(float) * kCH * (D + 1), s>>>(a, sums, r_on);
+    return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t pool_grad_impl(const Problem &p, const DeltaArgs &a, float *rho, const float *dkbar, cudaStream_t s)
+{
+    pool_sums<T, D><<<(unsigned)((long long)p.BH * p.N * a.NCH), 256, 0, s>>>(a, static_cast<const T *>(a.u), a.tok, rho);
+    pool_scan<D><<<(unsigned)((long long)p.BH * p.N), D, 0, s>>>(a, rho, nullptr, dkbar);
+    return cudaGetLastError();
+}
+
+#define MC_DELTA_DISPATCH(FN, p, ...)                                                               \
+    do {                                                                                            \
+        switch ((p).d) {                                                                            \
+        case 16: return (p).bf16 ? FN<__nv_bfloat16, 16>(p, __VA_ARGS__) : FN<float, 16>(p, __VA_ARGS__);    \
+        case 32: return (p).bf16 ? FN<__nv_bfloat16, 32>(p, __VA_ARGS__) : FN<float, 32>(p, __VA_ARGS__);    \
+        case 64: return (p).bf16 ? FN<__nv_bfloat16, 64>(p, __VA_ARGS__) : FN<float, 64>(p, __VA_ARGS__);    \
+        case 128: return (p).bf16 ? FN<__nv_bfloat16, 128>(p, __VA_ARGS__) : FN<float, 128>(p, __VA_ARGS__); \
+        default: return cudaErrorInvalidValue;                                                      \
+        }                                                                                           \
+    } while (0)
+
+}  // namespace
+
+cudaError_t launch_delta_scan_simt(const Problem &p, const DeltaArgs &a, cudaStream_t s) { MC_DELTA_DISPATCH(scan_impl, p, a, s); }
+cudaError_t launch_delta_rscan_simt(const Problem &p, const DeltaArgs &a, cudaStream_t s) { MC_DELTA_DISPATCH(rscan_impl, p, a, s); }
+cudaError_t launch_delta_grads_simt(const Problem &p, const DeltaArgs &a, cudaStream_t s) { MC_DELTA_DISPATCH(grads_impl, p, a, s); }
+cudaError_t launch_pool_simt(const Problem &p, const DeltaArgs &a, float *sums, float *kbar, float *r_on, cudaStream_t s)
+{
+    MC_DELTA_DISPATCH(pool_impl, p, a, sums, kbar, r_on, s);
+}
+cudaError_t launch_pool_grad_simt(const Problem &p, const DeltaArgs &a, float *rho, const float *dkbar, cudaStream_t s)
+{
+    MC_DELTA_DISPATCH(pool_grad_impl, p, a, rho, dkbar, s);
+}
+
+}  // namespace mc

@@ -83,6 +83,8 @@ namespace {
 
 std::atomic<int> g_readout_form{MC_READOUT_AUTO};
 
+}  // namespace
+
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int check_device()
@@ -115,6 +117,8 @@ int check_shape(int B, int H, int L, int d, int seg_len)
 }
 
 size_t round_up(size_t x) { return (x + 255) & ~(size_t)255; }
+
+namespace {
 
 struct ScratchPlan {
     size_t off_states, off_O, off_r, off_kbar, total;

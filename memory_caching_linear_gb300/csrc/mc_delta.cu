@@ -1,0 +1,360 @@
+// mc_delta.cu -- the entry points of the gated delta memory and of the evicting decode cache
+// (include/mc.h): argument checks, scratch, and the choice of kernels.
+#include <cstdint>
+
+#include "mc_internal.cuh"
+
+namespace mc {
+namespace {
+
+// A block of stream-ordered scratch handed out in 256-byte aligned pieces: a first walk with a null
+// base adds the sizes up, a second one hands out the pointers.
+struct Carver {
+    char *base;
+    size_t used;
+    template <typename T>
+    T *take(size_t count, bool want = true)
+    {
+        if (!want) return nullptr;
+        char *p = base ? base + used : nullptr;
+        used += round_up(sizeof(T) * count);
+        return reinterpret_cast<T *>(p);
+    }
+};
+
+int fail(cudaError_t e)
+{
+    cudaGetLastError();
+    return e == cudaErrorMemoryAllocation ? MC_ERR_ALLOC : MC_ERR_CUDA;
+}
+
+struct Call {
+    Problem p;
+    int NCH;
+    bool uses_u;
+};
+
+int check_call(Call &c, int B, int H, int L, int d, int seg_len, int agg_mode, int topk, bool bf16)
+{
+    int st = check_shape(B, H, L, d, seg_len);
+    if (st != MC_OK) return st;
+    if (seg_len > L) seg_len = L;
+    Problem &p = c.p;
+    p = Problem{};
+    p.B = B; p.H = H; p.L = L; p.d = d; p.C = seg_len;
+    p.N = (L + seg_len - 1) / seg_len;
+    p.BH = B * H;
+    p.bf16 = bf16;
+    c.NCH = (seg_len + kDeltaChunk - 1) / kDeltaChunk;
+    // one CTA per 64-token chunk, up to eight per segment
+    if ((long long)p.BH * p.N * (c.NCH > 8 ? c.NCH : 8) >= (1ll << 31)) return MC_ERR_SHAPE;
+    if (agg_mode < MC_RESIDUAL || agg_mode > MC_MEAN) return MC_ERR_MODE;
+    c.uses_u = mode_uses_u(agg_mode);
+    p.mode = agg_mode == MC_SOUP ? MC_GRM : agg_mode;  // the same function for a matrix memory
+    if (agg_mode == MC_SSC) {
+        if (topk < 0) return MC_ERR_TOPK;
+        if (topk >= p.N - 1) p.mode = MC_GRM;
+        else if (topk > kMaxTopk) return MC_ERR_TOPK;
+    }
+    p.topk = p.mode == MC_SSC ? topk : 0;
+    return MC_OK;
+}
+
+bool any_null(std::initializer_list<const void *> ptrs)
+{
+    for (const void *x : ptrs)
+        if (!x) return true;
+    return false;
+}
+
+// NULL pointers are left to any_null.
+bool any_misaligned(std::initializer_list<const void *> ptrs)
+{
+    for (const void *x : ptrs)
+        if (!aligned16(x)) return true;
+    return false;
+}
+
+DeltaArgs delta_args(const Call &c)
+{
+    DeltaArgs a{};
+    a.BH = c.p.BH; a.L = c.p.L; a.C = c.p.C; a.N = c.p.N; a.NCH = c.NCH;
+    return a;
+}
+
+int forward_delta(const void *q, const void *k, const void *v, const void *u, const void *la, const void *be, int B,
+                  int H, int L, int d, int seg_len, int agg_mode, int topk, void *y, float *states, bool bf16,
+                  cudaStream_t s)
+{
+    Call c;
+    int st = check_call(c, B, H, L, d, seg_len, agg_mode, topk, bf16);
+    if (st != MC_OK) return st;
+    if (any_null({q, k, v, la, be, y}) || (c.uses_u && !u)) return MC_ERR_NULL;
+    if (any_misaligned({q, k, v, u, la, be, y, states})) return MC_ERR_ALIGN;
+    if ((st = check_device()) != MC_OK) return st;
+    const Problem &p = c.p;
+    const size_t BH = p.BH, N = p.N;
+    const bool routed = mode_uses_u(p.mode);
+    DeltaArgs a = delta_args(c);
+    a.q = q; a.k = k; a.v = v; a.la = la; a.be = be;
+    a.u = routed ? u : nullptr;
+    a.states = states;
+    if (N == 1) {  // one memory, every gate is 1: the scan writes y
+        a.y = y;
+        profile_call_start(s);
+        cudaError_t e = launch_delta_scan_simt(p, a, s);
+        profile_after_kernel(s, "delta_scan_simt");
+        return e == cudaSuccess ? MC_OK : fail(e);
+    }
+    float *sums = nullptr, *kbar = nullptr, *r_on = nullptr;
+    void *scratch = nullptr;
+    for (int pass = 0; pass < 2; ++pass) {
+        Carver cv{static_cast<char *>(scratch), 0};
+        float *own_states = cv.take<float>(BH * N * d * d, !states);
+        a.states = states ? states : own_states;
+        a.O_on = cv.take<float>(BH * L * d);
+        kbar = cv.take<float>(BH * N * d, routed);
+        r_on = cv.take<float>(BH * L, routed);
+        sums = cv.take<float>(BH * N * c.NCH * d, routed);
+        if (pass == 0 && scratch_alloc(&scratch, cv.used, s) != cudaSuccess) {
+            cudaGetLastError();
+            return MC_ERR_ALLOC;
+        }
+    }
+    profile_call_start(s);
+    cudaError_t e = launch_delta_scan_simt(p, a, s);
+    profile_after_kernel(s, "delta_scan_simt");
+    if (e == cudaSuccess && routed) {
+        e = launch_pool_simt(p, a, sums, kbar, r_on, s);
+        profile_after_kernel(s, "pool_simt");
+    }
+    if (e == cudaSuccess) {
+        FwdArgs f{};
+        f.q = q; f.u = a.u; f.y = y;
+        f.states = a.states; f.O_on = a.O_on; f.r_on = r_on; f.kbar = kbar;
+        f.BH = p.BH; f.L = L; f.C = p.C; f.N = p.N; f.mode = p.mode; f.topk = p.topk;
+        e = launch_readout_simt(p, f, s);
+        profile_after_kernel(s, "readout_simt");
+    }
+    cudaError_t ef = cudaFreeAsync(scratch, s);
+    return e == cudaSuccess && ef == cudaSuccess ? MC_OK : fail(e != cudaSuccess ? e : ef);
+}
+
+int backward_delta(const void *q, const void *k, const void *v, const void *u, const void *la, const void *be,
+                   const void *dy, int B, int H, int L, int d, int seg_len, int agg_mode, int topk, void *dq, void *dk,
+                   void *dv, void *du, void *dla, void *dbe, bool bf16, cudaStream_t s)
+{
+    Call c;
+    int st = check_call(c, B, H, L, d, seg_len, agg_mode, topk, bf16);
+    if (st != MC_OK) return st;
+    if (any_null({q, k, v, la, be, dy, dq, dk, dv, dla, dbe}) || (c.uses_u && (!u || !du))) return MC_ERR_NULL;
+    if (any_misaligned({q, k, v, u, la, be, dy, dq, dk, dv, du, dla, dbe})) return MC_ERR_ALIGN;
+    if ((st = check_device()) != MC_OK) return st;
+    const Problem &p = c.p;
+    const size_t BH = p.BH, N = p.N, NCH = c.NCH;
+    const bool many = N > 1, routed = many && mode_uses_u(p.mode);
+    DeltaArgs a = delta_args(c);
+    a.q = q; a.k = k; a.v = v; a.la = la; a.be = be; a.dy = dy;
+    a.u = routed ? u : nullptr;
+    a.dq = dq; a.dk = dk; a.dv = dv; a.dla = dla; a.dbe = dbe;
+    BwdArgs b{};
+    float *sums = nullptr, *kbar = nullptr, *r_on = nullptr, *G = nullptr, *dkbar = nullptr, *tok = nullptr,
+          *dq_add = nullptr;
+    void *scratch = nullptr;
+    for (int pass = 0; pass < 2; ++pass) {
+        Carver cv{static_cast<char *>(scratch), 0};
+        a.E = cv.take<float>(BH * L * d);
+        a.W = cv.take<float>(BH * L * d);
+        a.S_c = cv.take<float>(BH * N * NCH * d * d);
+        a.R_c = cv.take<float>(BH * N * NCH * d * d);
+        a.states = cv.take<float>(BH * N * d * d, many);
+        a.O_on = cv.take<float>(BH * L * d, many);
+        G = cv.take<float>(BH * N * d * d, many);
+        tok = cv.take<float>(BH * L * kBwdTokWords, many);
+        dq_add = cv.take<float>(BH * L * d, many);
+        kbar = cv.take<float>(BH * N * d, many);
+        dkbar = cv.take<float>(BH * N * d, many);
+        r_on = cv.take<float>(BH * L, routed);
+        sums = cv.take<float>(BH * N * NCH * d, routed);
+        b.sel_idx = cv.take<int32_t>(BH * L * p.topk, routed && p.mode == MC_SSC);
+        b.sel_g = cv.take<float>(BH * L * p.topk, routed && p.mode == MC_SSC);
+        if (pass == 0 && scratch_alloc(&scratch, cv.used, s) != cudaSuccess) {
+            cudaGetLastError();
+            return MC_ERR_ALLOC;
+        }
+    }
+    cudaError_t e = cudaSuccess;
+    if (du && !routed) e = cudaMemsetAsync(du, 0, BH * L * d * (bf16 ? 2 : 4), s);  // no score has a weight to move
+    profile_call_start(s);
+    if (e == cudaSuccess) e = launch_delta_scan_simt(p, a, s);
+    profile_after_kernel(s, "delta_scan_simt");
+    if (e == cudaSuccess && many) {
+        if (routed) {
+            e = launch_pool_simt(p, a, sums, kbar, r_on, s);
+            profile_after_kernel(s, "pool_simt");
+            if (e == cudaSuccess) e = cudaMemsetAsync(dkbar, 0, sizeof(float) * BH * N * d, s);
+        }
+        b.q = q; b.k = k; b.v = v; b.u = a.u; b.dy = dy;
+        b.dq_f32 = dq_add; b.du = routed ? du : nullptr;
+        b.states = a.states; b.kbar = kbar; b.r_on = r_on; b.O_on = a.O_on;
+        b.G = G; b.dkbar = dkbar; b.tok = tok;
+        b.BH = p.BH; b.L = L; b.C = p.C; b.N = p.N; b.mode = p.mode; b.topk = p.topk;
+        if (e == cudaSuccess) e = launch_bwd_router_simt(p, b, s);
+        if (e == cudaSuccess && routed) {
+            a.tok = tok;
+            e = launch_pool_grad_simt(p, a, sums, dkbar, s);
+            profile_after_kernel(s, "pool_grad_simt");
+            a.rho = sums;
+        }
+        a.tok = tok;
+        a.G = G;
+        a.dq_add = dq_add;
+    }
+    if (e == cudaSuccess) e = launch_delta_rscan_simt(p, a, s);
+    profile_after_kernel(s, "delta_rscan_simt");
+    if (e == cudaSuccess) e = launch_delta_grads_simt(p, a, s);
+    profile_after_kernel(s, "delta_grads_simt");
+    cudaError_t ef = cudaFreeAsync(scratch, s);
+    return e == cudaSuccess && ef == cudaSuccess ? MC_OK : fail(e != cudaSuccess ? e : ef);
+}
+
+int decode_slots(SlotArgs a, int B, int H, int seg_len, int agg_mode, int topk, bool evict, cudaStream_t s)
+{
+    int st = check_shape(B, H, 1, a.d, seg_len);
+    if (st != MC_OK) return st;
+    if (a.t < 0 || a.nmax < 1 || a.nmax > kDecMaxN - 1) return MC_ERR_SHAPE;
+    if (evict ? a.protect < 0 || a.protect >= a.nmax : a.t / seg_len >= a.nmax) return MC_ERR_SHAPE;
+    if (agg_mode < MC_RESIDUAL || agg_mode > MC_MEAN) return MC_ERR_MODE;
+    const bool routed = mode_uses_u(agg_mode);
+    if (evict && !routed) return MC_ERR_MODE;  // constant gates tell no segment from another
+    if (agg_mode == MC_SSC && topk < 0) return MC_ERR_TOPK;
+    if (any_null({a.q, a.k, a.v, a.y, a.states, a.kbar, a.online, a.ksum}) || (routed && !a.u)) return MC_ERR_NULL;
+    if (evict && any_null({a.mass, a.slot_seg})) return MC_ERR_NULL;
+    if (evict ? !a.la != !a.be : !a.la || !a.be) return MC_ERR_NULL;
+    if (any_misaligned({a.q, a.k, a.v, a.u, a.la, a.be, a.y, a.states, a.kbar, a.online, a.ksum, a.mass, a.slot_seg}))
+        return MC_ERR_ALIGN;
+    if ((st = check_device()) != MC_OK) return st;
+    a.BH = B * H;
+    a.C = seg_len;
+    a.mode = agg_mode == MC_SOUP ? MC_GRM : agg_mode;
+    a.topk = agg_mode == MC_SSC ? topk : 0;
+    if (!routed) a.u = nullptr;
+    profile_call_start(s);
+    cudaError_t e = launch_decode_slots(a, s);
+    profile_after_kernel(s, "decode_slots");
+    return e == cudaSuccess ? MC_OK : fail(e);
+}
+
+int cache_compact(const void *k, const void *u, const float *states_all, int B, int H, int L, int d, int seg_len,
+                  int agg_mode, int topk, int protect, float *states, float *kbar, float *mass, int32_t *slot_seg,
+                  float *online, float *ksum, int n_max, float *mass_all, bool bf16, cudaStream_t s)
+{
+    Call c;
+    int st = check_shape(B, H, L, d, seg_len);
+    if (st != MC_OK) return st;
+    if (n_max < 1 || n_max > kDecMaxN - 1 || protect < 0 || protect > n_max) return MC_ERR_SHAPE;
+    if ((st = check_call(c, B, H, L, d, seg_len, agg_mode, topk, bf16)) != MC_OK) return st;
+    if (!c.uses_u) return MC_ERR_MODE;  // constant gates tell no segment from another
+    Problem &p = c.p;
+    const long long tiles = ((long long)L + 63) / 64;
+    if (p.N > 16384 || (long long)p.BH * tiles >= (1ll << 31) || (long long)p.BH * (n_max + 1) >= (1ll << 31))
+        return MC_ERR_SHAPE;
+    if (any_null({k, u, states_all, states, kbar, mass, slot_seg, online, ksum})) return MC_ERR_NULL;
+    if (any_misaligned({k, u, states_all, states, kbar, mass, slot_seg, online, ksum, mass_all})) return MC_ERR_ALIGN;
+    if ((st = check_device()) != MC_OK) return st;
+    const size_t BH = p.BH, N = p.N;
+    DeltaArgs a = delta_args(c);
+    a.k = k; a.u = u;
+    CompactArgs m{};
+    m.u = u; m.states_all = states_all; m.mass_all = mass_all;
+    m.states = states; m.kbar = kbar; m.mass = mass; m.online = online; m.ksum = ksum; m.slot_seg = slot_seg;
+    m.BH = p.BH; m.L = L; m.C = p.C; m.N = p.N; m.d = d; m.mode = p.mode; m.topk = p.topk; m.tiles = (int)tiles;
+    m.done = L / seg_len; m.nmax = n_max;
+    m.protect = protect < m.done ? protect : m.done;
+    float *sums = nullptr, *kbar_all = nullptr, *r_on = nullptr;
+    void *scratch = nullptr;
+    for (int pass = 0; pass < 2; ++pass) {
+        Carver cv{static_cast<char *>(scratch), 0};
+        kbar_all = cv.take<float>(BH * N * d);
+        r_on = cv.take<float>(BH * L);
+        sums = cv.take<float>(BH * N * c.NCH * d);
+        m.part = cv.take<float>(BH * m.tiles * N);
+        m.order = cv.take<int32_t>(BH * n_max);
+        if (pass == 0 && scratch_alloc(&scratch, cv.used, s) != cudaSuccess) {
+            cudaGetLastError();
+            return MC_ERR_ALLOC;
+        }
+    }
+    m.kbar_all = kbar_all;
+    m.r_on = r_on;
+    profile_call_start(s);
+    cudaError_t e = launch_pool_simt(p, a, sums, kbar_all, r_on, s);
+    profile_after_kernel(s, "pool_simt");
+    if (e == cudaSuccess) {
+        e = launch_gate_mass(p, m, s);
+        profile_after_kernel(s, "gate_mass");
+    }
+    if (e == cudaSuccess) {
+        e = launch_compact(p, m, s);
+        profile_after_kernel(s, "compact");
+    }
+    cudaError_t ef = cudaFreeAsync(scratch, s);
+    return e == cudaSuccess && ef == cudaSuccess ? MC_OK : fail(e != cudaSuccess ? e : ef);
+}
+
+}  // namespace
+}  // namespace mc
+
+extern "C" {
+
+int mc_forward_delta(const void *q, const void *k, const void *v, const void *u, const void *log_alpha,
+                     const void *beta, int B, int H, int L, int d, int seg_len, int agg_mode, int topk, void *y,
+                     float *states, int is_bf16, mc_stream_t stream)
+{
+    return mc::forward_delta(q, k, v, u, log_alpha, beta, B, H, L, d, seg_len, agg_mode, topk, y, states, is_bf16 != 0,
+                             reinterpret_cast<cudaStream_t>(stream));
+}
+
+int mc_backward_delta(const void *q, const void *k, const void *v, const void *u, const void *log_alpha,
+                      const void *beta, const void *dy, int B, int H, int L, int d, int seg_len, int agg_mode, int topk,
+                      void *dq, void *dk, void *dv, void *du, void *dlog_alpha, void *dbeta, int is_bf16,
+                      mc_stream_t stream)
+{
+    return mc::backward_delta(q, k, v, u, log_alpha, beta, dy, B, H, L, d, seg_len, agg_mode, topk, dq, dk, dv, du,
+                              dlog_alpha, dbeta, is_bf16 != 0, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int mc_decode_step_delta(const void *q, const void *k, const void *v, const void *u, const void *log_alpha,
+                         const void *beta, int B, int H, int d, int seg_len, int agg_mode, int topk, int t,
+                         float *states, float *kbar, float *online, float *ksum, int n_max, void *y, int is_bf16,
+                         mc_stream_t stream)
+{
+    mc::SlotArgs a{};
+    a.q = q; a.k = k; a.v = v; a.u = u; a.la = log_alpha; a.be = beta; a.y = y;
+    a.states = states; a.kbar = kbar; a.online = online; a.ksum = ksum;
+    a.d = d; a.t = t; a.nmax = n_max; a.bf16 = is_bf16 != 0;
+    return mc::decode_slots(a, B, H, seg_len, agg_mode, topk, false, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int mc_decode_step_evict(const void *q, const void *k, const void *v, const void *u, const void *log_alpha,
+                         const void *beta, int B, int H, int d, int seg_len, int agg_mode, int topk, int t, int protect,
+                         float *states, float *kbar, float *mass, int32_t *slot_seg, float *online, float *ksum,
+                         int n_max, void *y, int is_bf16, mc_stream_t stream)
+{
+    mc::SlotArgs a{};
+    a.q = q; a.k = k; a.v = v; a.u = u; a.la = log_alpha; a.be = beta; a.y = y;
+    a.states = states; a.kbar = kbar; a.online = online; a.ksum = ksum; a.mass = mass; a.slot_seg = slot_seg;
+    a.d = d; a.t = t; a.nmax = n_max; a.protect = protect; a.bf16 = is_bf16 != 0;
+    return mc::decode_slots(a, B, H, seg_len, agg_mode, topk, true, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int mc_cache_compact(const void *k, const void *u, const float *prefill_states, int B, int H, int L, int d, int seg_len,
+                     int agg_mode, int topk, int protect, float *states, float *kbar, float *mass, int32_t *slot_seg,
+                     float *online, float *ksum, int n_max, float *prefill_mass, int is_bf16, mc_stream_t stream)
+{
+    return mc::cache_compact(k, u, prefill_states, B, H, L, d, seg_len, agg_mode, topk, protect, states, kbar, mass,
+                             slot_seg, online, ksum, n_max, prefill_mass, is_bf16 != 0,
+                             reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -221,6 +221,7 @@ struct BwdArgs {
     float *sel_g;         // SSC: [BH][L][topk] their gates
     float *gam;           // [BH][N][L] gates of the cached segments, for the tensor-core G (routed modes), or null
     const float *dg_in;   // [BH][N][L] dy_t . M^(i) q_t from the tensor cores, or null (computed here)
+    float *dq_f32;        // [BH][L][d] the cached memories' dq instead of dq, without the online one (X_on null), or null
     const float *dq_in;   // [BH][L][d] dq from the tensor cores (all of it when X_on is null), or null (written already)
     const float *dgon_in; // [BH][L] dy_t . M_t q_t from the tensor cores, or null (from O_on)
     const float *dg_in2, *dgon_in2;  // second partial sums of dg_in and dgon_in (added to them), or null
@@ -254,5 +255,69 @@ cudaError_t launch_bwd_dkbar_tc(const Problem &p, const void *u, const __nv_bflo
 cudaError_t launch_backward_simt(const Problem &p, const void *q, const void *k, const void *v, const void *u,
                                  const void *dy, void *dq, void *dk, void *dv, void *du, void *scratch,
                                  cudaStream_t s);
+
+// The gated delta memory (k_delta_simt.cu, k_delta_tc.cu): M_t = a_t M_{t-1} + beta_t e_t k_t^T with
+// e_t = v_t - a_t M_{t-1} k_t and a_t = exp(log_alpha_t), per (b,h) and segment.
+constexpr int kDeltaChunk = 64;  // tokens of a chunk
+// Decays below exp(-60) (one part in 1e26) count as that: differences of their running sums stay finite.
+__device__ __forceinline__ float delta_log(float x) { return x < -60.f ? -60.f : x; }
+__device__ __forceinline__ float delta_decay(float x) { return expf(delta_log(x)); }
+struct DeltaArgs {
+    const void *q, *k, *v, *u, *dy;  // [BH][L][d], element type per Problem::bf16
+    const void *la, *be;             // log_alpha, beta [BH][L], the same type
+    void *y;                         // online reads in the element type (one segment), or null
+    float *O_on;                     // online reads in fp32, or null
+    float *states;                   // [BH][N][d][d], or null
+    void *dq, *dk, *dv, *dla, *dbe;  // gradients
+    float *E, *W;                    // [BH][L][d] e_t, w_t (fp32 scratch; E null: not kept)
+    float *S_c, *R_c;                // [BH][N][NCH][d][d] memory before / adjoint after every chunk (S_c null: not kept)
+    const float *G;                  // [BH][N][d][d] adjoint of the cached states, or null
+    const float *tok;                // [BH][L][kBwdTokWords] online gate (word 2), pooled-key weight (4), or null (1, 0)
+    const float *dq_add;             // [BH][L][d] added to dq, or null
+    const float *rho;                // [BH][N][NCH][d] later tokens' pooled-key gradient after every chunk, or null
+    int BH, L, C, N, NCH;            // NCH = ceil(C / 64)
+};
+cudaError_t launch_delta_scan_simt(const Problem &p, const DeltaArgs &a, cudaStream_t s);
+cudaError_t launch_delta_rscan_simt(const Problem &p, const DeltaArgs &a, cudaStream_t s);
+cudaError_t launch_delta_grads_simt(const Problem &p, const DeltaArgs &a, cudaStream_t s);
+// Key sums before every 64-token chunk (sums [BH][N][NCH][d]), key means, online scores (r_on null: not formed).
+cudaError_t launch_pool_simt(const Problem &p, const DeltaArgs &a, float *sums, float *kbar, float *r_on, cudaStream_t s);
+// rho from tok's pooled-key weights, u and the key means' gradient.
+cudaError_t launch_pool_grad_simt(const Problem &p, const DeltaArgs &a, float *rho, const float *dkbar, cudaStream_t s);
+// The gates, the cached reads' gradients and G of the FFMA backward alone (k_bwd_simt.cu): tok, dq_f32, du, dkbar, G.
+cudaError_t launch_bwd_router_simt(const Problem &p, const BwdArgs &a, cudaStream_t s);
+
+// One decoding step over a cache of slots (k_decode_slots.cu): the delta memory where la is not
+// null, eviction by accumulated gate weight where mass is not null (then slot_seg names the slots).
+struct SlotArgs {
+    const void *q, *k, *v, *u, *la, *be;  // [BH][d]; la, be [BH]
+    void *y;
+    float *states, *kbar, *online, *ksum, *mass;
+    int32_t *slot_seg;
+    int BH, d, C, mode, topk, t, nmax, protect;
+    bool bf16;
+};
+cudaError_t launch_decode_slots(const SlotArgs &a, cudaStream_t s);
+
+// Compaction of a prefill into a cache of slots (k_compact.cu).
+struct CompactArgs {
+    const void *u;                     // [BH][L][d]
+    const float *kbar_all, *r_on;      // [BH][N][d], [BH][L]
+    const float *states_all;           // [BH][N][d][d]
+    float *part;                       // [BH][tiles][N] scratch
+    float *mass_all;                   // [BH][N], or null
+    int32_t *order;                    // [BH][nmax] scratch
+    float *states, *kbar, *mass, *online, *ksum;
+    int32_t *slot_seg;
+    int BH, L, C, N, d, mode, topk, tiles, done, nmax, protect;
+};
+cudaError_t launch_gate_mass(const Problem &p, const CompactArgs &a, cudaStream_t s);
+cudaError_t launch_compact(const Problem &p, const CompactArgs &a, cudaStream_t s);
+
+// Checks shared by the entry points (mc_api.cu).
+bool aligned16(const void *p);
+int check_device();
+int check_shape(int B, int H, int L, int d, int seg_len);
+size_t round_up(size_t x);
 
 }  // namespace mc
