@@ -82,6 +82,84 @@ DeltaArgs delta_args(const Call &c)
     return a;
 }
 
+DeltaTcArgs delta_tc_args(const Call &c, const void *q, const void *k, const void *v, const void *la, const void *be)
+{
+    DeltaTcArgs t{};
+    t.q = static_cast<const __nv_bfloat16 *>(q);
+    t.k = static_cast<const __nv_bfloat16 *>(k);
+    t.v = static_cast<const __nv_bfloat16 *>(v);
+    t.la = static_cast<const __nv_bfloat16 *>(la);
+    t.be = static_cast<const __nv_bfloat16 *>(be);
+    t.BH = c.p.BH; t.L = c.p.L; t.C = c.p.C; t.N = c.p.N; t.NCH = c.NCH;
+    return t;
+}
+
+// bf16, d = 64 or 128.  One memory: the walk writes y.  Several, where the readout's tensor-core kernels take
+// the shape: the walk writes the states and the written values beta_t e_t, and the readout runs over these
+// with the decay.  Otherwise the walk writes the online reads for the CUDA-core readout.
+int forward_delta_tc(const Call &c, const void *q, const void *k, const void *v, const void *u, const void *la,
+                     const void *be, void *y, float *states, cudaStream_t s)
+{
+    const Problem &p = c.p;
+    const size_t BH = p.BH, N = p.N, L = p.L, d = p.d;
+    const bool one = N == 1, routed = mode_uses_u(p.mode), tc = !one && tc_fused_gates(p);
+    DeltaTcArgs t = delta_tc_args(c, q, k, v, la, be);
+    t.states = states;
+    FwdArgs f{};
+    float *kbar = nullptr, *r_on = nullptr, *sums = nullptr, *alpha = nullptr, *zero = nullptr, *ones = nullptr;
+    char *tc_scratch = nullptr;
+    void *scratch = nullptr;
+    for (int pass = 0; pass < 2; ++pass) {
+        Carver cv{static_cast<char *>(scratch), 0};
+        t.rec = cv.take<uint8_t>(BH * N * c.NCH * kDeltaRecBytes);
+        if (!one) {
+            float *own_states = cv.take<float>(BH * N * d * d, !states);
+            t.states = states ? states : own_states;
+        }
+        if (tc) {
+            t.U = cv.take<__nv_bfloat16>(BH * L * d);
+            alpha = cv.take<float>(BH * L);
+            zero = cv.take<float>(BH * L);
+            ones = cv.take<float>(BH * L);
+            f.states = cv.take<float>(BH * N * d * d);
+            tc_scratch = cv.take<char>(tc_scratch_bytes(p));
+        } else if (!one) {
+            t.O_on = cv.take<float>(BH * L * d);
+            kbar = cv.take<float>(BH * N * d, routed);
+            r_on = cv.take<float>(BH * L, routed);
+            sums = cv.take<float>(BH * N * c.NCH * d, routed);
+        }
+        if (pass == 0 && scratch_alloc(&scratch, cv.used, s) != cudaSuccess) {
+            cudaGetLastError();
+            return MC_ERR_ALLOC;
+        }
+    }
+    if (one) t.y = static_cast<__nv_bfloat16 *>(y);
+    f.q = q; f.k = k; f.u = routed ? u : nullptr; f.y = y;
+    f.BH = p.BH; f.L = p.L; f.C = p.C; f.N = p.N; f.mode = p.mode; f.topk = p.topk;
+    profile_call_start(s);
+    cudaError_t e = launch_delta_walk_tc(p, t, !tc, s);
+    if (e == cudaSuccess && tc) {
+        f.v = t.U;
+        f.alpha = alpha; f.beta = zero; f.lam = ones;
+        e = launch_delta_scalars(p, la, alpha, zero, ones, s);
+        profile_after_kernel(s, "delta_scalars");
+        if (e == cudaSuccess) e = launch_forward_tc(p, f, tc_scratch, s);
+    } else if (e == cudaSuccess && !one) {
+        DeltaArgs a = delta_args(c);
+        a.k = k; a.u = f.u;
+        if (routed) {
+            e = launch_pool_simt(p, a, sums, kbar, r_on, s);
+            profile_after_kernel(s, "pool_simt");
+        }
+        f.states = t.states; f.O_on = t.O_on; f.r_on = r_on; f.kbar = kbar;
+        if (e == cudaSuccess) e = launch_readout_simt(p, f, s);
+        profile_after_kernel(s, "readout_simt");
+    }
+    cudaError_t ef = cudaFreeAsync(scratch, s);
+    return e == cudaSuccess && ef == cudaSuccess ? MC_OK : fail(e != cudaSuccess ? e : ef);
+}
+
 int forward_delta(const void *q, const void *k, const void *v, const void *u, const void *la, const void *be, int B,
                   int H, int L, int d, int seg_len, int agg_mode, int topk, void *y, float *states, bool bf16,
                   cudaStream_t s)
@@ -95,6 +173,7 @@ int forward_delta(const void *q, const void *k, const void *v, const void *u, co
     const Problem &p = c.p;
     const size_t BH = p.BH, N = p.N;
     const bool routed = mode_uses_u(p.mode);
+    if (delta_tc_supported(p)) return forward_delta_tc(c, q, k, v, u, la, be, y, states, s);
     DeltaArgs a = delta_args(c);
     a.q = q; a.k = k; a.v = v; a.la = la; a.be = be;
     a.u = routed ? u : nullptr;

@@ -284,6 +284,24 @@ cudaError_t launch_delta_grads_simt(const Problem &p, const DeltaArgs &a, cudaSt
 cudaError_t launch_pool_simt(const Problem &p, const DeltaArgs &a, float *sums, float *kbar, float *r_on, cudaStream_t s);
 // rho from tok's pooled-key weights, u and the key means' gradient.
 cudaError_t launch_pool_grad_simt(const Problem &p, const DeltaArgs &a, float *rho, const float *dkbar, cudaStream_t s);
+// The same on the tensor cores (k_delta_tc.cu): bf16, d = 64 or 128, any segment length.
+constexpr int kDeltaRecBytes = 16384;  // a chunk's record between its two kernels
+struct DeltaTcArgs {
+    const __nv_bfloat16 *q, *k, *v, *la, *be;
+    uint8_t *rec;          // [BH][N][NCH] x kDeltaRecBytes scratch
+    __nv_bfloat16 *y;      // online reads in bf16 (one segment), or null
+    float *O_on;           // online reads in fp32, or null
+    float *states;         // [BH][N][d][d], or null
+    __nv_bfloat16 *U;      // [BH][L][d] beta_t e_t, or null
+    __nv_bfloat16 *E;      // [BH][L][d] e_t, or null
+    __nv_bfloat16 *S_c;    // [BH][N][NCH][d][d] memory before every chunk, or null
+    int BH, L, C, N, NCH;
+};
+bool delta_tc_supported(const Problem &p);
+// read: q is read and y or O_on written.
+cudaError_t launch_delta_scalars(const Problem &p, const void *la, float *alpha, float *zero, float *one, cudaStream_t s);
+cudaError_t launch_delta_walk_tc(const Problem &p, const DeltaTcArgs &a, bool read, cudaStream_t s);
+
 // The gates, the cached reads' gradients and G of the FFMA backward alone (k_bwd_simt.cu): tok, dq_f32, du, dkbar, G.
 cudaError_t launch_bwd_router_simt(const Problem &p, const BwdArgs &a, cudaStream_t s);
 
