@@ -43,6 +43,18 @@ constexpr int kRecT = kTiles * 32 * 16, kRecP = kTiles * 32 * 8, kRecV = 1024;
 constexpr int kRec = kDeltaRecBytes;
 static_assert(kRecT + kRecP + kRecV == kRec, "record");
 
+// The other way round, rows m >= columns i: column tile nt needs row tiles kt = nt / 2 .. 3.
+__host__ __device__ constexpr int rev_base(int nt) { return 8 * (nt / 2) - nt / 2 * (nt / 2 - 1) + (nt & 1) * (4 - nt / 2); }
+static_assert(rev_base(7) + 1 == kTiles, "tiles of an upper triangle");
+__device__ __forceinline__ void rev_tile(int t, int &nt, int &kt)
+{
+    nt = 0;
+    while (nt < 7 && rev_base(nt + 1) <= t) ++nt;
+    kt = nt / 2 + t - rev_base(nt);
+}
+// The reverse walk's record: T - 1 (one term), P, and exp(c_i), exp(c_end - c_i), beta_i, [192] exp(c_end).
+static_assert(2 * kRecP + kRecV == kDeltaRRecBytes, "record");
+
 struct Where {
     int bh, seg, ch, tb, cnt;
 };
@@ -63,13 +75,14 @@ __device__ __forceinline__ Where chunk_at(const DeltaTcArgs &a, long long id)
 // warp; (1 + A)^-1 in fp32 by 16 x 16 blocks: each warp inverts a diagonal block by substitution (a lane
 // per column), then X_ij = -X_ii sum_k A_ik X_kj, one block diagonal after the other.
 // ---------------------------------------------------------------------------
-template <int D, bool READ>
+template <int D, bool READ, bool REV>
 __global__ void __launch_bounds__(kPrepThreads) delta_prep_tc(DeltaTcArgs a)
 {
     constexpr int ROW = D * 2, PIECES = D / 8;
+    constexpr bool QK = READ || REV;
     extern __shared__ __align__(16) uint8_t sm[];
     uint8_t *Kt = sm, *Qt = Kt + kCH * ROW;
-    float *A = reinterpret_cast<float *>(Qt + (READ ? kCH * ROW : 0)), *X = A + kCH * kAP, *Y = X + kCH * kAP;
+    float *A = reinterpret_cast<float *>(Qt + (QK ? kCH * ROW : 0)), *X = A + kCH * kAP, *Y = X + kCH * kAP;
     __shared__ float cum[kCH], bet[kCH];
     const Where w = chunk_at(a, blockIdx.x);
     if (w.cnt <= 0) return;
@@ -79,7 +92,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_tc(DeltaTcArgs a)
         const int r = e / PIECES, pc = e % PIECES;
         const size_t off = (row0 + (r < w.cnt ? r : 0)) * D + pc * 8;
         cp16(smem_addr(Kt) + tile_off<ROW>(r, pc), a.k + off, r < w.cnt);
-        if (READ) cp16(smem_addr(Qt) + tile_off<ROW>(r, pc), a.q + off, r < w.cnt);
+        if (QK) cp16(smem_addr(Qt) + tile_off<ROW>(r, pc), a.q + off, r < w.cnt);
     }
     cp_commit();
     if (warp == 0) {  // running sums of the chunk's decays, two tokens per lane
@@ -113,7 +126,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_tc(DeltaTcArgs a)
         for (int ks = 0; ks < D / 16; ++ks) {
             uint32_t ak[4], aq[4];
             ldsm4(ak, smem_addr(Kt) + tile_off<ROW>(ar, 2 * ks + ac));
-            if (READ) ldsm4(aq, smem_addr(Qt) + tile_off<ROW>(ar, 2 * ks + ac));
+            if (QK) ldsm4(aq, smem_addr(Qt) + tile_off<ROW>(ar, 2 * ks + ac));
 #pragma unroll
             for (int n2 = 0; n2 < 4; ++n2) {
                 if (n2 > warp) break;
@@ -121,7 +134,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_tc(DeltaTcArgs a)
                 ldsm4(b, smem_addr(Kt) + tile_off<ROW>(16 * n2 + br, 2 * ks + bc));
                 mma16816(kk[2 * n2], ak, b[0], b[1]);
                 mma16816(kk[2 * n2 + 1], ak, b[2], b[3]);
-                if (READ) {
+                if (QK) {
                     mma16816(qk[2 * n2], aq, b[0], b[1]);
                     mma16816(qk[2 * n2 + 1], aq, b[2], b[3]);
                 }
@@ -134,7 +147,7 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_tc(DeltaTcArgs a)
                 const int i = 16 * warp + g + 8 * (e >> 1), j = 8 * n + 2 * c + (e & 1);
                 const float dec = j <= i ? expf(cum[i] - cum[j]) : 0.f;
                 A[i * kAP + j] = j < i ? kk[n][e] * dec * bet[j] : 0.f;
-                if (READ) Y[i * kAP + j] = qk[n][e] * dec;
+                if (QK) Y[i * kAP + j] = qk[n][e] * dec;
                 X[i * kAP + j] = 0.f;
             }
     }
@@ -158,7 +171,18 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_tc(DeltaTcArgs a)
         }
     }
     __syncthreads();
-    if (READ) {  // P tiles while the blocks settle (nothing below touches Y until the next barrier)
+    if (REV) {  // the same P as an operand of rows i, columns j
+        uint2 *pt = reinterpret_cast<uint2 *>(a.rrec + (size_t)blockIdx.x * kDeltaRRecBytes + kRecP);
+        for (int e = tid; e < kTiles * 32; e += kPrepThreads) {
+            int nt, kt;
+            rev_tile(e / 32, nt, kt);
+            const int l = e % 32;
+            const float *y = Y + (16 * kt + 2 * (l % 4)) * kAP + 8 * nt + l / 4;
+            pt[e] = make_uint2(pack2(y[0], y[kAP]), pack2(y[8 * kAP], y[9 * kAP]));
+        }
+        if (!READ) __syncthreads();
+    }
+    if (READ) {  // P tiles (nothing below touches Y until the next barrier)
         uint2 *pt = reinterpret_cast<uint2 *>(rec + kRecT);
         for (int e = tid; e < kTiles * 32; e += kPrepThreads) {
             const int t = e / 32, l = e % 32;
@@ -209,6 +233,26 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_tc(DeltaTcArgs a)
         split2(j < i ? x[0] : 0.f, j + 1 < i ? x[1] : 0.f, o.x, o.z);
         split2(j + 8 < i ? x[8] : 0.f, j + 9 < i ? x[9] : 0.f, o.y, o.w);
         tt[e] = o;
+    }
+    if (REV) {
+        uint8_t *rrec = a.rrec + (size_t)blockIdx.x * kDeltaRRecBytes;
+        uint2 *lt = reinterpret_cast<uint2 *>(rrec);
+        for (int e = tid; e < kTiles * 32; e += kPrepThreads) {
+            int nt, kt;
+            rev_tile(e / 32, nt, kt);
+            const int l = e % 32, i = 8 * nt + l / 4, m = 16 * kt + 2 * (l % 4);  // T_mi, m > i
+            const float *x = X + m * kAP + i;
+            lt[e] = make_uint2(pack2(m > i ? x[0] : 0.f, m + 1 > i ? x[kAP] : 0.f),
+                               pack2(m + 8 > i ? x[8 * kAP] : 0.f, m + 9 > i ? x[9 * kAP] : 0.f));
+        }
+        if (tid < kCH) {
+            float *vec = reinterpret_cast<float *>(rrec + 2 * kRecP);
+            const float ce = cum[kCH - 1];
+            vec[tid] = expf(cum[tid]);
+            vec[64 + tid] = expf(ce - cum[tid]);
+            vec[128 + tid] = bet[tid];
+            if (tid == 0) vec[192] = expf(ce);
+        }
     }
     if (tid < kCH) {
         float *vec = reinterpret_cast<float *>(rec + kRecT + kRecP);
@@ -478,6 +522,689 @@ __global__ void __launch_bounds__(32 * NW) delta_walk_tc(DeltaTcArgs a)
     }
 }
 
+// ---------------------------------------------------------------------------
+// delta_rwalk_tc: the walk backwards over the adjoint, with the layout of delta_walk_tc.  Per chunk,
+// with p_i = g_i dy_i and R the adjoint after the chunk:
+//   X   = diag(exp(c_end - c)) K R^T + P^T p,   W = T^T diag(beta) X            (dv = W)
+//   R' = exp(c_end) R + sum_i exp(c_i) (p_i q_i^T - w_i k_i^T)
+// R itself enters the products in two bf16 terms, the rest in one: the results are bf16 gradients.
+// ---------------------------------------------------------------------------
+template <int D, int NW>
+struct RWalkSmem {
+    static constexpr int kK = kCH * D * 2, kV = kCH * NW * 32;
+    static constexpr int kStage = 2 * kK + kV + kDeltaRRecBytes + 256;  // K, Q, dy columns, record, gates
+    static constexpr int kTotal = 2 * kStage + NW * 2048;
+};
+
+template <int D, int NW>
+__global__ void __launch_bounds__(32 * NW) delta_rwalk_tc(DeltaTcArgs a)
+{
+    using W = RWalkSmem<D, NW>;
+    constexpr int ROW = D * 2, PIECES = D / 8, NT = 32 * NW, KS = D / 16, VROW = NW * 32, VP = NW * 2;
+    extern __shared__ __align__(16) uint8_t sm[];
+    constexpr int splits = D / (16 * NW);
+    const int rs = (int)blockIdx.x % splits;
+    const long long sid = blockIdx.x / splits;
+    const int seg = (int)(sid % a.N), bh = (int)(sid / a.N);
+    const int t0 = seg * a.C, len = min((seg + 1) * a.C, a.L) - t0, nch = (len + kCH - 1) / kCH;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, c = lane % 4;
+    const int vbase = rs * 16 * NW;
+
+    auto load = [&](int ch) {
+        uint8_t *st = sm + (ch & 1) * W::kStage;
+        const int cnt = min(kCH, len - ch * kCH);
+        const size_t row0 = (size_t)bh * a.L + t0 + ch * kCH;
+        for (int e = tid; e < kCH * PIECES; e += NT) {
+            const int r = e / PIECES, pc = e % PIECES;
+            const size_t off = (row0 + (r < cnt ? r : 0)) * D + pc * 8;
+            cp16(smem_addr(st) + tile_off<ROW>(r, pc), a.k + off, r < cnt);
+            cp16(smem_addr(st) + W::kK + tile_off<ROW>(r, pc), a.q + off, r < cnt);
+        }
+        for (int e = tid; e < kCH * VP; e += NT) {
+            const int r = e / VP, pc = e % VP;
+            cp16(smem_addr(st) + 2 * W::kK + r * VROW + ((pc ^ (r & (VP < 8 ? VP - 1 : 7))) << 4),
+                 a.dy + (row0 + (r < cnt ? r : 0)) * D + vbase + pc * 8, r < cnt);
+        }
+        const uint8_t *rec = a.rrec + ((size_t)sid * a.NCH + ch) * kDeltaRRecBytes;
+        const uint32_t dst = smem_addr(st) + 2 * W::kK + W::kV;
+        for (int e = tid; e < kDeltaRRecBytes / 16; e += NT) cp16(dst + e * 16, rec + e * 16, true);
+        float *gs = reinterpret_cast<float *>(st + 2 * W::kK + W::kV + kDeltaRRecBytes);
+        for (int e = tid; e < kCH; e += NT) gs[e] = a.gon && e < cnt ? a.gon[(row0 + e) * a.gw_stride] : 1.f;
+        cp_commit();
+    };
+
+    float R[2 * KS][4];
+    if (a.G && seg < a.N - 1) {
+        const float *src = a.G + ((size_t)sid * D + vbase + 16 * warp) * D;
+#pragma unroll
+        for (int n = 0; n < 2 * KS; ++n) {
+            const float2 x = *reinterpret_cast<const float2 *>(src + (size_t)g * D + 8 * n + 2 * c);
+            const float2 y = *reinterpret_cast<const float2 *>(src + (size_t)(g + 8) * D + 8 * n + 2 * c);
+            R[n][0] = x.x; R[n][1] = x.y; R[n][2] = y.x; R[n][3] = y.y;
+        }
+    } else {
+#pragma unroll
+        for (int n = 0; n < 2 * KS; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) R[n][e] = 0.f;
+    }
+
+    uint8_t *outb = sm + 2 * W::kStage + warp * 2048;
+    load(nch - 1);
+    for (int ch = nch - 1; ch >= 0; --ch) {
+        cp_wait<0>();
+        __syncthreads();
+        if (ch > 0) load(ch - 1);
+        const uint8_t *st = sm + (ch & 1) * W::kStage;
+        const uint32_t kt = smem_addr(st), qt = kt + W::kK, vt = qt + W::kK;
+        const uint8_t *rec = st + 2 * W::kK + W::kV;
+        const float *vec = reinterpret_cast<const float *>(rec + 2 * kRecP);
+        const float *gs = reinterpret_cast<const float *>(rec + kDeltaRRecBytes);
+        const size_t row0 = (size_t)bh * a.L + t0 + ch * kCH;
+        const int cnt = min(kCH, len - ch * kCH);
+        {
+            __nv_bfloat16 *dst = a.R_c + (((size_t)sid * a.NCH + ch) * D + vbase + 16 * warp) * D;
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) {
+#pragma unroll
+                for (int n = 0; n < 8; n += 2)
+                    stsm4(smem_addr(outb) + tile_off<128>(lane & 15, n + (lane >> 4)), pack2(R[8 * h + n][0], R[8 * h + n][1]),
+                          pack2(R[8 * h + n][2], R[8 * h + n][3]), pack2(R[8 * h + n + 1][0], R[8 * h + n + 1][1]),
+                          pack2(R[8 * h + n + 1][2], R[8 * h + n + 1][3]));
+                __syncwarp();
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int r = x * 4 + lane / 8, pc = lane % 8;
+                    *reinterpret_cast<uint4 *>(dst + (size_t)r * D + 64 * h + pc * 8) =
+                        *reinterpret_cast<const uint4 *>(outb + tile_off<128>(r, pc));
+                }
+                __syncwarp();
+            }
+        }
+        float X[8][4];
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) X[n][e] = 0.f;
+        const int br = (lane >> 4) * 8 + (lane & 7), bc = (lane >> 3) & 1;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            uint32_t hi[4], lo[4];
+            split2(R[2 * ks][0], R[2 * ks][1], hi[0], lo[0]);
+            split2(R[2 * ks][2], R[2 * ks][3], hi[1], lo[1]);
+            split2(R[2 * ks + 1][0], R[2 * ks + 1][1], hi[2], lo[2]);
+            split2(R[2 * ks + 1][2], R[2 * ks + 1][3], hi[3], lo[3]);
+#pragma unroll
+            for (int n2 = 0; n2 < 4; ++n2) {
+                uint32_t b[4];
+                ldsm4(b, kt + tile_off<ROW>(16 * n2 + br, 2 * ks + bc));
+                mma16816(X[2 * n2], hi, b[0], b[1]);
+                mma16816(X[2 * n2 + 1], hi, b[2], b[3]);
+                mma16816(X[2 * n2], lo, b[0], b[1]);
+                mma16816(X[2 * n2 + 1], lo, b[2], b[3]);
+            }
+        }
+        uint32_t pf[4][4], pg[4][4];  // p, and exp(c) p
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4) {
+            uint32_t v4[4];
+            const int r = 16 * k4 + (lane >> 4) * 8 + (lane & 7), pc = 2 * warp + ((lane >> 3) & 1);
+            ldsm4t(v4, vt + r * VROW + ((pc ^ (r & (VP < 8 ? VP - 1 : 7))) << 4));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int n = 2 * k4 + h;
+                const float2 re = *reinterpret_cast<const float2 *>(vec + 64 + 8 * n + 2 * c);
+                const float2 ga = *reinterpret_cast<const float2 *>(vec + 8 * n + 2 * c);
+                const float2 go = *reinterpret_cast<const float2 *>(gs + 8 * n + 2 * c);
+                X[n][0] *= re.x;
+                X[n][1] *= re.y;
+                X[n][2] *= re.x;
+                X[n][3] *= re.y;
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    const float p0 = go.x * low_f(v4[2 * h + z]), p1 = go.y * high_f(v4[2 * h + z]);
+                    pf[k4][2 * h + z] = pack2(p0, p1);
+                    pg[k4][2 * h + z] = pack2(ga.x * p0, ga.y * p1);
+                }
+            }
+        }
+        const uint2 *lt = reinterpret_cast<const uint2 *>(rec) + lane;
+        const uint2 *pt = reinterpret_cast<const uint2 *>(rec + kRecP) + lane;
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4)
+#pragma unroll
+            for (int n = 0; n < 2 * k4 + 2; ++n) {
+                const uint2 b = pt[(rev_base(n) + k4 - n / 2) * 32];
+                mma16816(X[n], pf[k4], b.x, b.y);
+            }
+        {
+            uint32_t yh[4][4];
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                const float2 be = *reinterpret_cast<const float2 *>(vec + 128 + 8 * n + 2 * c);
+                X[n][0] *= be.x;
+                X[n][1] *= be.y;
+                X[n][2] *= be.x;
+                X[n][3] *= be.y;
+                yh[n / 2][2 * (n & 1)] = pack2(X[n][0], X[n][1]);
+                yh[n / 2][2 * (n & 1) + 1] = pack2(X[n][2], X[n][3]);
+            }
+#pragma unroll
+            for (int k4 = 0; k4 < 4; ++k4)
+#pragma unroll
+                for (int n = 0; n < 2 * k4 + 2; ++n) {
+                    const uint2 b = lt[(rev_base(n) + k4 - n / 2) * 32];
+                    mma16816(X[n], yh[k4], b.x, b.y);
+                }
+        }
+        uint32_t wf[4][4], wl[4][4];
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            split2(X[n][0], X[n][1], wf[n / 2][2 * (n & 1)], wl[n / 2][2 * (n & 1)]);
+            split2(X[n][2], X[n][3], wf[n / 2][2 * (n & 1) + 1], wl[n / 2][2 * (n & 1) + 1]);
+        }
+        auto put = [&](__nv_bfloat16 *dst, const uint32_t (&f)[4][4]) {
+#pragma unroll
+            for (int k4 = 0; k4 < 4; ++k4) {
+                const int r = 16 * k4 + (lane >> 4) * 8 + (lane & 7), pc = (lane >> 3) & 1;
+                stsm4t(smem_addr(outb) + r * 32 + ((pc ^ ((r >> 2) & 1)) << 4), f[k4][0], f[k4][1], f[k4][2], f[k4][3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int r = 16 * x + lane / 2, pc = lane % 2;
+                if (r < cnt)
+                    *reinterpret_cast<uint4 *>(dst + (row0 + r) * D + vbase + 16 * warp + 8 * pc) =
+                        *reinterpret_cast<const uint4 *>(outb + r * 32 + ((pc ^ ((r >> 2) & 1)) << 4));
+            }
+            __syncwarp();
+        };
+        put(a.dv, wf);
+        put(a.W_lo, wl);
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {  // -exp(c) w
+            const float2 ga = *reinterpret_cast<const float2 *>(vec + 8 * n + 2 * c);
+            wf[n / 2][2 * (n & 1)] = pack2(-ga.x * X[n][0], -ga.y * X[n][1]);
+            wf[n / 2][2 * (n & 1) + 1] = pack2(-ga.x * X[n][2], -ga.y * X[n][3]);
+        }
+        const float dec = vec[192];
+#pragma unroll
+        for (int n = 0; n < 2 * KS; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) R[n][e] *= dec;
+        const int tr = ((lane >> 3) & 1) * 8 + (lane & 7), tc = lane >> 4;
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4)
+#pragma unroll
+            for (int n2 = 0; n2 < KS; ++n2) {
+                uint32_t b[4];
+                ldsm4t(b, kt + tile_off<ROW>(16 * k4 + tr, 2 * n2 + tc));
+                mma16816(R[2 * n2], wf[k4], b[0], b[1]);
+                mma16816(R[2 * n2 + 1], wf[k4], b[2], b[3]);
+                ldsm4t(b, qt + tile_off<ROW>(16 * k4 + tr, 2 * n2 + tc));
+                mma16816(R[2 * n2], pg[k4], b[0], b[1]);
+                mma16816(R[2 * n2 + 1], pg[k4], b[2], b[3]);
+            }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// delta_grads_tc: one CTA per chunk, everything that sums over value rows (k_delta_simt.cu's header).
+// Eight warps: warp % 4 takes 16 tokens, warp / 4 half of the dimensions.  B1, B2 and their transposes
+// are formed by each warp for its own tokens straight into operand registers.  S and R share a buffer,
+// so that two CTAs fit on an SM (d = 128) and one's loads run under the other's products.
+// ---------------------------------------------------------------------------
+constexpr int kGradThreads = 256;
+
+template <int D>
+struct GradSmem {
+    static constexpr int kT = kCH * D * 2;         // a 64-token tile
+    static constexpr int kM = D * D * 2;           // S, then R
+    static constexpr int kVec = 4 * (8 * kCH + 2 * kCH * 4 + 32);
+    static constexpr int kTotal = 5 * kT + kM + kVec;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kGradThreads, D == 128 ? 1 : 2) delta_grads_tc(DeltaTcArgs a)
+{
+    using G = GradSmem<D>;
+    constexpr int ROW = D * 2, PIECES = D / 8, KS = D / 16, HD = D / 2, HN = HD / 8;  // HN column tiles per warp
+    extern __shared__ __align__(16) uint8_t sm[];
+    uint8_t *Qt = sm, *Kt = Qt + G::kT, *Pt = Kt + G::kT, *Et = Pt + G::kT, *Wt = Et + G::kT, *Mt = Wt + G::kT;
+    float *cum = reinterpret_cast<float *>(Mt + G::kM), *bet = cum + kCH, *gs = bet + kCH, *pw = gs + kCH;
+    float *hv = pw + kCH, *rowsum = hv + kCH;  // rowsum[3][2][64]: dbeta, dq.q, boundary, by half
+    float *red = rowsum + 6 * kCH;
+    const Where w = chunk_at(a, blockIdx.x);
+    if (w.cnt <= 0) return;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, c = lane % 4;
+    const int m0 = 16 * (warp & 3), half = warp >> 2, d0 = half * HD;
+    const size_t row0 = (size_t)w.bh * a.L + w.tb;
+    const __nv_bfloat16 *S = a.S_c + (size_t)blockIdx.x * D * D, *R = a.R_c + (size_t)blockIdx.x * D * D;
+
+    for (int e = tid; e < kCH * PIECES; e += kGradThreads) {
+        const int r = e / PIECES, pc = e % PIECES;
+        const bool ok = r < w.cnt;
+        const size_t off = (row0 + (ok ? r : 0)) * D + pc * 8;
+        const uint32_t o = tile_off<ROW>(r, pc);
+        cp16(smem_addr(Qt) + o, a.q + off, ok);
+        cp16(smem_addr(Kt) + o, a.k + off, ok);
+        cp16(smem_addr(Pt) + o, a.dy + off, ok);
+        cp16(smem_addr(Et) + o, a.E + off, ok);
+        cp16(smem_addr(Wt) + o, a.dv + off, ok);
+    }
+    for (int e = tid; e < D * PIECES; e += kGradThreads)
+        cp16(smem_addr(Mt) + tile_off<ROW>(e / PIECES, e % PIECES), S + (size_t)e * 8, true);
+    cp_commit();
+    if (warp == 0) {
+        const int i = 2 * lane;
+        const float x0 = i < w.cnt ? delta_log(__bfloat162float(a.la[row0 + i])) : 0.f;
+        const float x1 = i + 1 < w.cnt ? delta_log(__bfloat162float(a.la[row0 + i + 1])) : 0.f;
+        float s = x0 + x1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float n = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += n;
+        }
+        cum[i] = s - x1;
+        cum[i + 1] = s;
+    }
+    if (tid < kCH) {
+        const bool ok = tid < w.cnt;
+        bet[tid] = ok ? __bfloat162float(a.be[row0 + tid]) : 0.f;
+        gs[tid] = ok && a.gon ? a.gon[(row0 + tid) * a.gw_stride] : 1.f;
+        pw[tid] = ok && a.pw ? a.pw[(row0 + tid) * a.gw_stride] : 0.f;
+    }
+    cp_wait<0>();
+    __syncthreads();
+    if (a.gon) {  // p = g dy, in place
+        for (int e = tid; e < kCH * PIECES; e += kGradThreads) {
+            const int r = e / PIECES;
+            uint4 *x = reinterpret_cast<uint4 *>(Pt + tile_off<ROW>(r, e % PIECES));
+            uint4 y = *x;
+            uint32_t *yw = reinterpret_cast<uint32_t *>(&y);
+#pragma unroll
+            for (int z = 0; z < 4; ++z) yw[z] = pack2(gs[r] * low_f(yw[z]), gs[r] * high_f(yw[z]));
+            *x = y;
+        }
+    }
+    // w . v, D / 8 lanes per token
+    for (int r = tid / PIECES; r < kCH; r += kGradThreads / PIECES) {
+        const int pc = tid % PIECES;
+        float s = 0.f;
+        if (r < w.cnt) {
+            const uint4 vv = *reinterpret_cast<const uint4 *>(a.v + (row0 + r) * D + pc * 8);
+            const uint4 ww = *reinterpret_cast<const uint4 *>(Wt + tile_off<ROW>(r, pc));
+            const uint4 wl = *reinterpret_cast<const uint4 *>(a.W_lo + (row0 + r) * D + pc * 8);
+            const uint32_t *v4 = reinterpret_cast<const uint32_t *>(&vv), *w4 = reinterpret_cast<const uint32_t *>(&ww);
+            const uint32_t *l4 = reinterpret_cast<const uint32_t *>(&wl);
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+                s = fmaf(low_f(v4[z]), low_f(w4[z]) + low_f(l4[z]), fmaf(high_f(v4[z]), high_f(w4[z]) + high_f(l4[z]), s));
+        }
+#pragma unroll
+        for (int o = PIECES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (pc == 0) hv[r] = s;
+    }
+    auto inner = [](const uint4 &x, const uint4 &y, float s) {
+        const uint32_t *xw = reinterpret_cast<const uint32_t *>(&x), *yw = reinterpret_cast<const uint32_t *>(&y);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) s = fmaf(low_f(xw[q]), low_f(yw[q]), fmaf(high_f(xw[q]), high_f(yw[q]), s));
+        return s;
+    };
+    uint4 sk[D * PIECES / kGradThreads];  // this thread's pieces of S, for <R, S>
+    float start = 0.f;                    // <adjoint before the chunk, S>
+#pragma unroll
+    for (int x = 0; x < D * PIECES / kGradThreads; ++x) {
+        const int e = tid + x * kGradThreads;
+        sk[x] = *reinterpret_cast<const uint4 *>(Mt + tile_off<ROW>(e / PIECES, e % PIECES));
+        if (w.ch > 0) start = inner(sk[x], *(reinterpret_cast<const uint4 *>(R - (size_t)D * D) + e), start);
+    }
+    __syncthreads();
+
+    const int ar = m0 + (lane & 15), ac = lane >> 4;                       // A operand of a token tile
+    const int br = (lane >> 4) * 8 + (lane & 7), bc = (lane >> 3) & 1;     // B, columns = rows of the tile
+    const int tr = ((lane >> 3) & 1) * 8 + (lane & 7), tc = lane >> 4;     // B, rows = rows of the tile
+    float dq[HN][4], y[HN][4], z[HN][4];
+#pragma unroll
+    for (int n = 0; n < HN; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dq[n][e] = y[n][e] = z[n][e] = 0.f;
+    // p S and w S
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+        uint32_t ap[4], aw[4];
+        ldsm4(ap, smem_addr(Pt) + tile_off<ROW>(ar, 2 * ks + ac));
+        ldsm4(aw, smem_addr(Wt) + tile_off<ROW>(ar, 2 * ks + ac));
+#pragma unroll
+        for (int n2 = 0; n2 < HN / 2; ++n2) {
+            uint32_t b[4];
+            ldsm4t(b, smem_addr(Mt) + tile_off<ROW>(16 * ks + tr, d0 / 8 + 2 * n2 + tc));
+            mma16816(dq[2 * n2], ap, b[0], b[1]);
+            mma16816(dq[2 * n2 + 1], ap, b[2], b[3]);
+            mma16816(z[2 * n2], aw, b[0], b[1]);
+            mma16816(z[2 * n2 + 1], aw, b[2], b[3]);
+        }
+    }
+    __syncthreads();  // S has been read
+    for (int e = tid; e < D * PIECES; e += kGradThreads)
+        cp16(smem_addr(Mt) + tile_off<ROW>(e / PIECES, e % PIECES), R + (size_t)e * 8, true);
+    cp_commit();
+    const float c_lo = cum[m0 + g], c_hi = cum[m0 + g + 8], ce = cum[kCH - 1];
+    {
+        const float e0 = expf(c_lo), e1 = expf(c_hi);
+#pragma unroll
+        for (int n = 0; n < HN; ++n) {
+            dq[n][0] *= e0; dq[n][1] *= e0; dq[n][2] *= e1; dq[n][3] *= e1;
+            z[n][0] *= e0; z[n][1] *= e0; z[n][2] *= e1; z[n][3] *= e1;
+        }
+    }
+    // rows i of B1 beta and B2 beta (columns j <= i): dq += B1 K, z += B2 K
+    {
+        float b1[8][4], b2[8][4];
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) b1[n][e] = b2[n][e] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            uint32_t ap[4], aw[4];
+            ldsm4(ap, smem_addr(Pt) + tile_off<ROW>(ar, 2 * ks + ac));
+            ldsm4(aw, smem_addr(Wt) + tile_off<ROW>(ar, 2 * ks + ac));
+#pragma unroll
+            for (int n2 = 0; n2 < 4; ++n2) {
+                if (n2 > (warp & 3)) break;
+                uint32_t b[4];
+                ldsm4(b, smem_addr(Et) + tile_off<ROW>(16 * n2 + br, 2 * ks + bc));
+                mma16816(b1[2 * n2], ap, b[0], b[1]);
+                mma16816(b1[2 * n2 + 1], ap, b[2], b[3]);
+                mma16816(b2[2 * n2], aw, b[0], b[1]);
+                mma16816(b2[2 * n2 + 1], aw, b[2], b[3]);
+            }
+        }
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4) {
+            if (k4 > (warp & 3)) break;
+            uint32_t f1[4], f2[4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int n = 2 * k4 + h;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = m0 + g + 8 * (e >> 1), j = 8 * n + 2 * c + (e & 1);
+                    const float f = j <= i ? expf((e >> 1 ? c_hi : c_lo) - cum[j]) * bet[j] : 0.f;
+                    b1[n][e] *= f;
+                    b2[n][e] *= j < i ? f : 0.f;
+                }
+                f1[2 * h] = pack2(b1[n][0], b1[n][1]);
+                f1[2 * h + 1] = pack2(b1[n][2], b1[n][3]);
+                f2[2 * h] = pack2(b2[n][0], b2[n][1]);
+                f2[2 * h + 1] = pack2(b2[n][2], b2[n][3]);
+            }
+#pragma unroll
+            for (int n2 = 0; n2 < HN / 2; ++n2) {
+                uint32_t b[4];
+                ldsm4t(b, smem_addr(Kt) + tile_off<ROW>(16 * k4 + tr, d0 / 8 + 2 * n2 + tc));
+                mma16816(dq[2 * n2], f1, b[0], b[1]);
+                mma16816(dq[2 * n2 + 1], f1, b[2], b[3]);
+                mma16816(z[2 * n2], f2, b[0], b[1]);
+                mma16816(z[2 * n2 + 1], f2, b[2], b[3]);
+            }
+        }
+    }
+    cp_wait<0>();
+    __syncthreads();  // R has come
+    {
+        float in = 0.f;
+#pragma unroll
+        for (int x = 0; x < D * PIECES / kGradThreads; ++x) {
+            const int e = tid + x * kGradThreads;
+            in = inner(sk[x], *reinterpret_cast<const uint4 *>(Mt + tile_off<ROW>(e / PIECES, e % PIECES)), in);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            in += __shfl_xor_sync(0xffffffffu, in, o);
+            start += __shfl_xor_sync(0xffffffffu, start, o);
+        }
+        if (lane == 0) {
+            red[warp] = in;
+            red[8 + warp] = start;
+        }
+    }
+    // E R
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+        uint32_t ae[4];
+        ldsm4(ae, smem_addr(Et) + tile_off<ROW>(ar, 2 * ks + ac));
+#pragma unroll
+        for (int n2 = 0; n2 < HN / 2; ++n2) {
+            uint32_t b[4];
+            ldsm4t(b, smem_addr(Mt) + tile_off<ROW>(16 * ks + tr, d0 / 8 + 2 * n2 + tc));
+            mma16816(y[2 * n2], ae, b[0], b[1]);
+            mma16816(y[2 * n2 + 1], ae, b[2], b[3]);
+        }
+    }
+    auto row_dot = [&](const float (&x)[HN][4], const uint8_t *tile, int what) {  // per token, over this half
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int n = 0; n < HN; ++n) {
+            const uint32_t a0 = *reinterpret_cast<const uint32_t *>(tile + tile_off<ROW>(m0 + g, d0 / 8 + n) + 4 * c);
+            const uint32_t a1 = *reinterpret_cast<const uint32_t *>(tile + tile_off<ROW>(m0 + g + 8, d0 / 8 + n) + 4 * c);
+            s0 = fmaf(x[n][0], low_f(a0), fmaf(x[n][1], high_f(a0), s0));
+            s1 = fmaf(x[n][2], low_f(a1), fmaf(x[n][3], high_f(a1), s1));
+        }
+        s0 += __shfl_xor_sync(0xffffffffu, s0, 1);
+        s0 += __shfl_xor_sync(0xffffffffu, s0, 2);
+        s1 += __shfl_xor_sync(0xffffffffu, s1, 1);
+        s1 += __shfl_xor_sync(0xffffffffu, s1, 2);
+        if (c == 0) {
+            rowsum[(2 * what + half) * kCH + m0 + g] = s0;
+            rowsum[(2 * what + half) * kCH + m0 + g + 8] = s1;
+        }
+    };
+    {
+        const float e0 = expf(ce - c_lo), e1 = expf(ce - c_hi);
+#pragma unroll
+        for (int n = 0; n < HN; ++n) {
+            y[n][0] *= e0; y[n][1] *= e0; y[n][2] *= e1; y[n][3] *= e1;
+        }
+    }
+    row_dot(y, Kt, 2);
+    // rows j of B1^T and B2^T (columns i >= j): y += B1^T Q - B2^T K
+    {
+        float b1[8][4], b2[8][4];
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) b1[n][e] = b2[n][e] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            uint32_t ae[4];
+            ldsm4(ae, smem_addr(Et) + tile_off<ROW>(ar, 2 * ks + ac));
+#pragma unroll
+            for (int n2 = 0; n2 < 4; ++n2) {
+                if (n2 < (warp & 3)) continue;
+                uint32_t b[4];
+                ldsm4(b, smem_addr(Pt) + tile_off<ROW>(16 * n2 + br, 2 * ks + bc));
+                mma16816(b1[2 * n2], ae, b[0], b[1]);
+                mma16816(b1[2 * n2 + 1], ae, b[2], b[3]);
+                ldsm4(b, smem_addr(Wt) + tile_off<ROW>(16 * n2 + br, 2 * ks + bc));
+                mma16816(b2[2 * n2], ae, b[0], b[1]);
+                mma16816(b2[2 * n2 + 1], ae, b[2], b[3]);
+            }
+        }
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4) {
+            if (k4 < (warp & 3)) continue;
+            uint32_t f1[4], f2[4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int n = 2 * k4 + h;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = m0 + g + 8 * (e >> 1), i = 8 * n + 2 * c + (e & 1);
+                    const float f = i >= j ? expf(cum[i] - (e >> 1 ? c_hi : c_lo)) : 0.f;
+                    b1[n][e] *= f;
+                    b2[n][e] *= i > j ? -f : 0.f;
+                }
+                f1[2 * h] = pack2(b1[n][0], b1[n][1]);
+                f1[2 * h + 1] = pack2(b1[n][2], b1[n][3]);
+                f2[2 * h] = pack2(b2[n][0], b2[n][1]);
+                f2[2 * h + 1] = pack2(b2[n][2], b2[n][3]);
+            }
+#pragma unroll
+            for (int n2 = 0; n2 < HN / 2; ++n2) {
+                uint32_t b[4];
+                ldsm4t(b, smem_addr(Qt) + tile_off<ROW>(16 * k4 + tr, d0 / 8 + 2 * n2 + tc));
+                mma16816(y[2 * n2], f1, b[0], b[1]);
+                mma16816(y[2 * n2 + 1], f1, b[2], b[3]);
+                ldsm4t(b, smem_addr(Kt) + tile_off<ROW>(16 * k4 + tr, d0 / 8 + 2 * n2 + tc));
+                mma16816(y[2 * n2], f2, b[0], b[1]);
+                mma16816(y[2 * n2 + 1], f2, b[2], b[3]);
+            }
+        }
+    }
+    row_dot(y, Kt, 0);
+    row_dot(dq, Qt, 1);
+    {
+        const float be0 = bet[m0 + g], be1 = bet[m0 + g + 8];
+#pragma unroll
+        for (int n = 0; n < HN; ++n) {  // dk
+            y[n][0] = fmaf(be0, y[n][0], -z[n][0]);
+            y[n][1] = fmaf(be0, y[n][1], -z[n][1]);
+            y[n][2] = fmaf(be1, y[n][2], -z[n][2]);
+            y[n][3] = fmaf(be1, y[n][3], -z[n][3]);
+        }
+    }
+    __syncthreads();  // the tiles have been read
+    if (a.pw) {  // the pooled keys' share: rho after the chunk + sum over the chunk's tokens t >= j of pw_t u_t
+        for (int e = tid; e < kCH * PIECES; e += kGradThreads) {
+            const int r = e / PIECES, pc = e % PIECES;
+            cp16(smem_addr(Et) + tile_off<ROW>(r, pc), a.u + (row0 + (r < w.cnt ? r : 0)) * D + pc * 8, r < w.cnt);
+        }
+        cp_commit();
+        cp_wait<0>();
+        __syncthreads();
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4) {
+            if (k4 < (warp & 3)) continue;
+            uint32_t fh[4], fl[4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int j = m0 + g + 8 * x, t = 8 * (2 * k4 + h) + 2 * c;
+                    split2(t >= j ? pw[t] : 0.f, t + 1 >= j ? pw[t + 1] : 0.f, fh[2 * h + x], fl[2 * h + x]);
+                }
+#pragma unroll
+            for (int n2 = 0; n2 < HN / 2; ++n2) {
+                uint32_t b[4];
+                ldsm4t(b, smem_addr(Et) + tile_off<ROW>(16 * k4 + tr, d0 / 8 + 2 * n2 + tc));
+                mma16816(y[2 * n2], fh, b[0], b[1]);
+                mma16816(y[2 * n2 + 1], fh, b[2], b[3]);
+                mma16816(y[2 * n2], fl, b[0], b[1]);
+                mma16816(y[2 * n2 + 1], fl, b[2], b[3]);
+            }
+        }
+        const float *rho = a.rho + (size_t)blockIdx.x * D + d0 + 2 * c;
+#pragma unroll
+        for (int n = 0; n < HN; ++n) {
+            const float2 x = *reinterpret_cast<const float2 *>(rho + 8 * n);
+            y[n][0] += x.x; y[n][1] += x.y; y[n][2] += x.x; y[n][3] += x.y;
+        }
+    }
+    if (a.dq_add) {
+#pragma unroll
+        for (int n = 0; n < HN; ++n)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int t = m0 + g + 8 * x;
+                if (t >= w.cnt) continue;
+                const float2 f = *reinterpret_cast<const float2 *>(a.dq_add + (row0 + t) * D + d0 + 8 * n + 2 * c);
+                dq[n][2 * x] += f.x;
+                dq[n][2 * x + 1] += f.y;
+            }
+    }
+    // out through this warp's own part of two tiles
+#pragma unroll
+    for (int n = 0; n < HN; n += 2) {
+        const uint32_t o = tile_off<ROW>(m0 + (lane & 15), d0 / 8 + n + (lane >> 4));
+        stsm4(smem_addr(Qt) + o, pack2(dq[n][0], dq[n][1]), pack2(dq[n][2], dq[n][3]), pack2(dq[n + 1][0], dq[n + 1][1]),
+              pack2(dq[n + 1][2], dq[n + 1][3]));
+        stsm4(smem_addr(Kt) + o, pack2(y[n][0], y[n][1]), pack2(y[n][2], y[n][3]), pack2(y[n + 1][0], y[n + 1][1]),
+              pack2(y[n + 1][2], y[n + 1][3]));
+    }
+    __syncwarp();
+#pragma unroll
+    for (int x = 0; x < 16 * (HD / 8) / 32; ++x) {
+        const int e = x * 32 + lane, r = m0 + e / (HD / 8), pc = d0 / 8 + e % (HD / 8);
+        if (r < w.cnt) {
+            *reinterpret_cast<uint4 *>(a.dq + (row0 + r) * D + pc * 8) = *reinterpret_cast<const uint4 *>(Qt + tile_off<ROW>(r, pc));
+            *reinterpret_cast<uint4 *>(a.dk + (row0 + r) * D + pc * 8) = *reinterpret_cast<const uint4 *>(Kt + tile_off<ROW>(r, pc));
+        }
+    }
+    if (warp == 0) {  // dbeta, and h backwards over the chunk: two tokens per lane
+        const int i = 2 * lane;
+        float in = 0.f, hb = 0.f, first = 0.f;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            in += red[x];
+            first += red[8 + x];
+        }
+        float h0 = 0.f, h1 = 0.f;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const float r = rowsum[2 * kCH + i + x] + rowsum[3 * kCH + i + x] - hv[i + x];
+            (x ? h1 : h0) = r;
+            hb += bet[i + x] * (rowsum[4 * kCH + i + x] + rowsum[5 * kCH + i + x]);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) hb += __shfl_xor_sync(0xffffffffu, hb, o);
+        float s = h0 + h1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float n = __shfl_down_sync(0xffffffffu, s, o);
+            if (lane + o < 32) s += n;
+        }
+        // h is known at both ends of the chunk; the running sum between them gathers the roundings of its
+        // terms, and the gap at the first token is taken out along the way
+        const float end = expf(ce) * in + hb;
+        const float gap = (first - (end + __shfl_sync(0xffffffffu, s, 0))) / (float)w.cnt;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            if (i + x >= w.cnt) continue;
+            const float h = end + s - (x ? h0 : 0.f) + gap * (float)(w.cnt - i - x);
+            a.dla[row0 + i + x] = __float2bfloat16_rn(w.ch == 0 && i + x == 0 ? 0.f : h);  // the first decay meets an empty memory
+            a.dbe[row0 + i + x] = __float2bfloat16_rn(rowsum[i + x] + rowsum[kCH + i + x]);
+        }
+    }
+}
+
+template <int D, int NW>
+cudaError_t rwalk_launch(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
+{
+    constexpr int smem = RWalkSmem<D, NW>::kTotal;
+    auto kern = delta_rwalk_tc<D, NW>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)((long long)p.BH * p.N * (D / (16 * NW))), 32 * NW, smem, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t grads_tc_impl(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
+{
+    cudaError_t e = rwalk_launch<D, 4>(p, a, s);
+    if (e != cudaSuccess) return e;
+    profile_after_kernel(s, "delta_rwalk_tc");
+    constexpr int smem = GradSmem<D>::kTotal;
+    auto kern = delta_grads_tc<D>;
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+    kern<<<(unsigned)((long long)p.BH * p.N * a.NCH), kGradThreads, smem, s>>>(a);
+    e = cudaGetLastError();
+    profile_after_kernel(s, "delta_grads_tc");
+    return e;
+}
+
 // The scalars of the window update that the readout's kernels take (mc_forward_swla's alpha, beta, lambda):
 // over the written values beta_t e_t the delta memory is the one with alpha = exp(log_alpha), beta = 0, lambda = 1.
 __global__ void __launch_bounds__(256) delta_scalars(const __nv_bfloat16 *la, float *alpha, float *zero, float *one, long long n)
@@ -489,11 +1216,11 @@ __global__ void __launch_bounds__(256) delta_scalars(const __nv_bfloat16 *la, fl
     one[i] = 1.f;
 }
 
-template <int D, bool READ>
+template <int D, bool READ, bool REV>
 cudaError_t prep_impl(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
 {
-    const size_t smem = (READ ? 2 : 1) * kCH * D * 2 + 3 * sizeof(float) * kCH * kAP;
-    auto kern = delta_prep_tc<D, READ>;
+    const size_t smem = (READ || REV ? 2 : 1) * kCH * D * 2 + 3 * sizeof(float) * kCH * kAP;
+    auto kern = delta_prep_tc<D, READ, REV>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)((long long)p.BH * p.N * a.NCH), kPrepThreads, smem, s>>>(a);
@@ -514,7 +1241,7 @@ cudaError_t walk_launch(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
 template <int D, bool READ>
 cudaError_t walk_impl(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
 {
-    cudaError_t e = prep_impl<D, READ>(p, a, s);
+    cudaError_t e = a.rrec ? prep_impl<D, READ, true>(p, a, s) : prep_impl<D, READ, false>(p, a, s);
     if (e != cudaSuccess) return e;
     profile_after_kernel(s, "delta_prep_tc");
     e = walk_launch<D, 4, READ>(p, a, s);
@@ -523,6 +1250,11 @@ cudaError_t walk_impl(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
 }
 
 }  // namespace
+
+cudaError_t launch_delta_grads_tc(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
+{
+    return p.d == 64 ? grads_tc_impl<64>(p, a, s) : grads_tc_impl<128>(p, a, s);
+}
 
 bool delta_tc_supported(const Problem &p) { return p.bf16 && (p.d == 64 || p.d == 128); }
 

@@ -236,16 +236,31 @@ int backward_delta(const void *q, const void *k, const void *v, const void *u, c
     a.q = q; a.k = k; a.v = v; a.la = la; a.be = be; a.dy = dy;
     a.u = routed ? u : nullptr;
     a.dq = dq; a.dk = dk; a.dv = dv; a.dla = dla; a.dbe = dbe;
+    const bool tc = delta_tc_supported(p);
+    DeltaTcArgs t = delta_tc_args(c, q, k, v, la, be);
+    t.dy = static_cast<const __nv_bfloat16 *>(dy);
+    t.u = static_cast<const __nv_bfloat16 *>(a.u);
+    t.dq = static_cast<__nv_bfloat16 *>(dq);
+    t.dk = static_cast<__nv_bfloat16 *>(dk);
+    t.dv = static_cast<__nv_bfloat16 *>(dv);
+    t.dla = static_cast<__nv_bfloat16 *>(dla);
+    t.dbe = static_cast<__nv_bfloat16 *>(dbe);
     BwdArgs b{};
     float *sums = nullptr, *kbar = nullptr, *r_on = nullptr, *G = nullptr, *dkbar = nullptr, *tok = nullptr,
           *dq_add = nullptr;
     void *scratch = nullptr;
     for (int pass = 0; pass < 2; ++pass) {
         Carver cv{static_cast<char *>(scratch), 0};
-        a.E = cv.take<float>(BH * L * d);
-        a.W = cv.take<float>(BH * L * d);
-        a.S_c = cv.take<float>(BH * N * NCH * d * d);
-        a.R_c = cv.take<float>(BH * N * NCH * d * d);
+        a.E = cv.take<float>(BH * L * d, !tc);
+        a.W = cv.take<float>(BH * L * d, !tc);
+        a.S_c = cv.take<float>(BH * N * NCH * d * d, !tc);
+        a.R_c = cv.take<float>(BH * N * NCH * d * d, !tc);
+        t.rec = cv.take<uint8_t>(BH * N * NCH * kDeltaRecBytes, tc);
+        t.rrec = cv.take<uint8_t>(BH * N * NCH * kDeltaRRecBytes, tc);
+        t.E = cv.take<__nv_bfloat16>(BH * L * d, tc);
+        t.W_lo = cv.take<__nv_bfloat16>(BH * L * d, tc);
+        t.S_c = cv.take<__nv_bfloat16>(BH * N * NCH * d * d, tc);
+        t.R_c = cv.take<__nv_bfloat16>(BH * N * NCH * d * d, tc);
         a.states = cv.take<float>(BH * N * d * d, many);
         a.O_on = cv.take<float>(BH * L * d, many);
         G = cv.take<float>(BH * N * d * d, many);
@@ -265,8 +280,14 @@ int backward_delta(const void *q, const void *k, const void *v, const void *u, c
     cudaError_t e = cudaSuccess;
     if (du && !routed) e = cudaMemsetAsync(du, 0, BH * L * d * (bf16 ? 2 : 4), s);  // no score has a weight to move
     profile_call_start(s);
-    if (e == cudaSuccess) e = launch_delta_scan_simt(p, a, s);
-    profile_after_kernel(s, "delta_scan_simt");
+    if (tc) {
+        t.states = a.states;
+        t.O_on = a.O_on;
+        if (e == cudaSuccess) e = launch_delta_walk_tc(p, t, many, s);
+    } else {
+        if (e == cudaSuccess) e = launch_delta_scan_simt(p, a, s);
+        profile_after_kernel(s, "delta_scan_simt");
+    }
     if (e == cudaSuccess && many) {
         if (routed) {
             e = launch_pool_simt(p, a, sums, kbar, r_on, s);
@@ -288,11 +309,21 @@ int backward_delta(const void *q, const void *k, const void *v, const void *u, c
         a.tok = tok;
         a.G = G;
         a.dq_add = dq_add;
+        t.gon = tok + 2;
+        t.gw_stride = kBwdTokWords;
+        t.G = G;
+        t.dq_add = dq_add;
+        t.rho = a.rho;
+        t.pw = routed ? tok + 4 : nullptr;
     }
-    if (e == cudaSuccess) e = launch_delta_rscan_simt(p, a, s);
-    profile_after_kernel(s, "delta_rscan_simt");
-    if (e == cudaSuccess) e = launch_delta_grads_simt(p, a, s);
-    profile_after_kernel(s, "delta_grads_simt");
+    if (tc) {
+        if (e == cudaSuccess) e = launch_delta_grads_tc(p, t, s);
+    } else {
+        if (e == cudaSuccess) e = launch_delta_rscan_simt(p, a, s);
+        profile_after_kernel(s, "delta_rscan_simt");
+        if (e == cudaSuccess) e = launch_delta_grads_simt(p, a, s);
+        profile_after_kernel(s, "delta_grads_simt");
+    }
     cudaError_t ef = cudaFreeAsync(scratch, s);
     return e == cudaSuccess && ef == cudaSuccess ? MC_OK : fail(e != cudaSuccess ? e : ef);
 }

@@ -295,8 +295,22 @@ struct DeltaTcArgs {
     __nv_bfloat16 *U;      // [BH][L][d] beta_t e_t, or null
     __nv_bfloat16 *E;      // [BH][L][d] e_t, or null
     __nv_bfloat16 *S_c;    // [BH][N][NCH][d][d] memory before every chunk, or null
+    // gradients
+    const __nv_bfloat16 *dy, *u;
+    uint8_t *rrec;         // [BH][N][NCH] x kDeltaRRecBytes scratch: the reverse walk's record, or null
+    const float *gon, *pw; // online gate and pooled-key weight of token t at [t * gw_stride], or null (1; no pooled keys)
+    int gw_stride;
+    const float *G;        // [BH][N][d][d] adjoint of the cached states, or null
+    const float *dq_add;   // [BH][L][d] added to dq, or null
+    const float *rho;      // [BH][N][NCH][d], with pw
+    __nv_bfloat16 *R_c;    // [BH][N][NCH][d][d] adjoint after every chunk
+    __nv_bfloat16 *W_lo;   // [BH][L][d] what the rounding of w_t to dv_t left
+    __nv_bfloat16 *dq, *dk, *dv, *dla, *dbe;
     int BH, L, C, N, NCH;
 };
+constexpr int kDeltaRRecBytes = 11264;
+// After the walk with rrec, E and S_c: dv and R_c, then the other gradients.
+cudaError_t launch_delta_grads_tc(const Problem &p, const DeltaTcArgs &a, cudaStream_t s);
 bool delta_tc_supported(const Problem &p);
 // read: q is read and y or O_on written.
 cudaError_t launch_delta_scalars(const Problem &p, const void *la, float *alpha, float *zero, float *one, cudaStream_t s);
