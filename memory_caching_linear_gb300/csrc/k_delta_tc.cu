@@ -697,30 +697,26 @@ __global__ void __launch_bounds__(32 * NW) delta_rwalk_tc(DeltaTcArgs a)
                     mma16816(X[n], yh[k4], b.x, b.y);
                 }
         }
-        uint32_t wf[4][4], wl[4][4];
+        uint32_t wf[4][4];
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
-            split2(X[n][0], X[n][1], wf[n / 2][2 * (n & 1)], wl[n / 2][2 * (n & 1)]);
-            split2(X[n][2], X[n][3], wf[n / 2][2 * (n & 1) + 1], wl[n / 2][2 * (n & 1) + 1]);
+            wf[n / 2][2 * (n & 1)] = pack2(X[n][0], X[n][1]);
+            wf[n / 2][2 * (n & 1) + 1] = pack2(X[n][2], X[n][3]);
         }
-        auto put = [&](__nv_bfloat16 *dst, const uint32_t (&f)[4][4]) {
 #pragma unroll
-            for (int k4 = 0; k4 < 4; ++k4) {
-                const int r = 16 * k4 + (lane >> 4) * 8 + (lane & 7), pc = (lane >> 3) & 1;
-                stsm4t(smem_addr(outb) + r * 32 + ((pc ^ ((r >> 2) & 1)) << 4), f[k4][0], f[k4][1], f[k4][2], f[k4][3]);
-            }
-            __syncwarp();
+        for (int k4 = 0; k4 < 4; ++k4) {
+            const int r = 16 * k4 + (lane >> 4) * 8 + (lane & 7), pc = (lane >> 3) & 1;
+            stsm4t(smem_addr(outb) + r * 32 + ((pc ^ ((r >> 2) & 1)) << 4), wf[k4][0], wf[k4][1], wf[k4][2], wf[k4][3]);
+        }
+        __syncwarp();
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int r = 16 * x + lane / 2, pc = lane % 2;
-                if (r < cnt)
-                    *reinterpret_cast<uint4 *>(dst + (row0 + r) * D + vbase + 16 * warp + 8 * pc) =
-                        *reinterpret_cast<const uint4 *>(outb + r * 32 + ((pc ^ ((r >> 2) & 1)) << 4));
-            }
-            __syncwarp();
-        };
-        put(a.dv, wf);
-        put(a.W_lo, wl);
+        for (int x = 0; x < 4; ++x) {
+            const int r = 16 * x + lane / 2, pc = lane % 2;
+            if (r < cnt)
+                *reinterpret_cast<uint4 *>(a.dv + (row0 + r) * D + vbase + 16 * warp + 8 * pc) =
+                    *reinterpret_cast<const uint4 *>(outb + r * 32 + ((pc ^ ((r >> 2) & 1)) << 4));
+        }
+        __syncwarp();
 #pragma unroll
         for (int n = 0; n < 8; ++n) {  // -exp(c) w
             const float2 ga = *reinterpret_cast<const float2 *>(vec + 8 * n + 2 * c);
@@ -760,7 +756,7 @@ template <int D>
 struct GradSmem {
     static constexpr int kT = kCH * D * 2;         // a 64-token tile
     static constexpr int kM = D * D * 2;           // S, then R
-    static constexpr int kVec = 4 * (8 * kCH + 2 * kCH * 4 + 32);
+    static constexpr int kVec = 4 * (22 * kCH + 16);
     static constexpr int kTotal = 5 * kT + kM + kVec;
 };
 
@@ -772,8 +768,9 @@ __global__ void __launch_bounds__(kGradThreads, D == 128 ? 1 : 2) delta_grads_tc
     extern __shared__ __align__(16) uint8_t sm[];
     uint8_t *Qt = sm, *Kt = Qt + G::kT, *Pt = Kt + G::kT, *Et = Pt + G::kT, *Wt = Et + G::kT, *Mt = Wt + G::kT;
     float *cum = reinterpret_cast<float *>(Mt + G::kM), *bet = cum + kCH, *gs = bet + kCH, *pw = gs + kCH;
-    float *hv = pw + kCH, *rowsum = hv + kCH;  // rowsum[3][2][64]: dbeta, dq.q, boundary, by half
-    float *red = rowsum + 6 * kCH;
+    float *rowsum = pw + kCH;                      // [4][2][64] by half: Y.k, exp(c) p S q, D R e k, exp(c) w S k
+    float *rowf = rowsum + 8 * kCH, *colf = rowf + 2 * kCH;  // [2][64], [2][4][64]: sums of F over its rows, columns
+    float *red = colf + 8 * kCH;
     const Where w = chunk_at(a, blockIdx.x);
     if (w.cnt <= 0) return;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, c = lane % 4;
@@ -827,24 +824,6 @@ __global__ void __launch_bounds__(kGradThreads, D == 128 ? 1 : 2) delta_grads_tc
             *x = y;
         }
     }
-    // w . v, D / 8 lanes per token
-    for (int r = tid / PIECES; r < kCH; r += kGradThreads / PIECES) {
-        const int pc = tid % PIECES;
-        float s = 0.f;
-        if (r < w.cnt) {
-            const uint4 vv = *reinterpret_cast<const uint4 *>(a.v + (row0 + r) * D + pc * 8);
-            const uint4 ww = *reinterpret_cast<const uint4 *>(Wt + tile_off<ROW>(r, pc));
-            const uint4 wl = *reinterpret_cast<const uint4 *>(a.W_lo + (row0 + r) * D + pc * 8);
-            const uint32_t *v4 = reinterpret_cast<const uint32_t *>(&vv), *w4 = reinterpret_cast<const uint32_t *>(&ww);
-            const uint32_t *l4 = reinterpret_cast<const uint32_t *>(&wl);
-#pragma unroll
-            for (int z = 0; z < 4; ++z)
-                s = fmaf(low_f(v4[z]), low_f(w4[z]) + low_f(l4[z]), fmaf(high_f(v4[z]), high_f(w4[z]) + high_f(l4[z]), s));
-        }
-#pragma unroll
-        for (int o = PIECES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (pc == 0) hv[r] = s;
-    }
     auto inner = [](const uint4 &x, const uint4 &y, float s) {
         const uint32_t *xw = reinterpret_cast<const uint32_t *>(&x), *yw = reinterpret_cast<const uint32_t *>(&y);
 #pragma unroll
@@ -852,12 +831,10 @@ __global__ void __launch_bounds__(kGradThreads, D == 128 ? 1 : 2) delta_grads_tc
         return s;
     };
     uint4 sk[D * PIECES / kGradThreads];  // this thread's pieces of S, for <R, S>
-    float start = 0.f;                    // <adjoint before the chunk, S>
 #pragma unroll
     for (int x = 0; x < D * PIECES / kGradThreads; ++x) {
         const int e = tid + x * kGradThreads;
         sk[x] = *reinterpret_cast<const uint4 *>(Mt + tile_off<ROW>(e / PIECES, e % PIECES));
-        if (w.ch > 0) start = inner(sk[x], *(reinterpret_cast<const uint4 *>(R - (size_t)D * D) + e), start);
     }
     __syncthreads();
 
@@ -898,7 +875,28 @@ __global__ void __launch_bounds__(kGradThreads, D == 128 ? 1 : 2) delta_grads_tc
             z[n][0] *= e0; z[n][1] *= e0; z[n][2] *= e1; z[n][3] *= e1;
         }
     }
-    // rows i of B1 beta and B2 beta (columns j <= i): dq += B1 K, z += B2 K
+    auto row_dot = [&](const float (&x)[HN][4], const uint8_t *tile, int what) {  // per token, over this half
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int n = 0; n < HN; ++n) {
+            const uint32_t a0 = *reinterpret_cast<const uint32_t *>(tile + tile_off<ROW>(m0 + g, d0 / 8 + n) + 4 * c);
+            const uint32_t a1 = *reinterpret_cast<const uint32_t *>(tile + tile_off<ROW>(m0 + g + 8, d0 / 8 + n) + 4 * c);
+            s0 = fmaf(x[n][0], low_f(a0), fmaf(x[n][1], high_f(a0), s0));
+            s1 = fmaf(x[n][2], low_f(a1), fmaf(x[n][3], high_f(a1), s1));
+        }
+        s0 += __shfl_xor_sync(0xffffffffu, s0, 1);
+        s0 += __shfl_xor_sync(0xffffffffu, s0, 2);
+        s1 += __shfl_xor_sync(0xffffffffu, s1, 1);
+        s1 += __shfl_xor_sync(0xffffffffu, s1, 2);
+        if (c == 0) {
+            rowsum[(2 * what + half) * kCH + m0 + g] = s0;
+            rowsum[(2 * what + half) * kCH + m0 + g + 8] = s1;
+        }
+    };
+    row_dot(dq, Qt, 1);
+    row_dot(z, Kt, 3);
+    // rows i of B1 beta and B2 beta (columns j <= i): dq += B1 K, z += B2 K.  F_ij = beta_j (B1_ij q_i.k_j - B2_ij k_i.k_j)
+    // for j < i, the first term on the warps of half 0, the second on those of half 1
     {
         float b1[8][4], b2[8][4];
 #pragma unroll
@@ -920,6 +918,59 @@ __global__ void __launch_bounds__(kGradThreads, D == 128 ? 1 : 2) delta_grads_tc
                 mma16816(b2[2 * n2], aw, b[0], b[1]);
                 mma16816(b2[2 * n2 + 1], aw, b[2], b[3]);
             }
+        }
+        float f0 = 0.f, f1s = 0.f;  // row sums of F
+#pragma unroll
+        for (int n2 = 0; n2 < 4; ++n2) {
+            float *cf = colf + (4 * half + (warp & 3)) * kCH + 16 * n2;
+            if (n2 > (warp & 3)) {
+                if (lane < 16) cf[lane] = 0.f;
+                continue;
+            }
+            float kk[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) kk[h][e] = 0.f;
+            const uint32_t at = smem_addr(half ? Kt : Qt);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                uint32_t aq[4], b[4];
+                ldsm4(aq, at + tile_off<ROW>(ar, 2 * ks + ac));
+                ldsm4(b, smem_addr(Kt) + tile_off<ROW>(16 * n2 + br, 2 * ks + bc));
+                mma16816(kk[0], aq, b[0], b[1]);
+                mma16816(kk[1], aq, b[2], b[3]);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int n = 2 * n2 + h, j = 8 * n + 2 * c;
+                float col[2] = {0.f, 0.f};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = m0 + g + 8 * (e >> 1), jj = j + (e & 1);
+                    const float f = jj < i ? expf((e >> 1 ? c_hi : c_lo) - cum[jj]) * bet[jj] * kk[h][e] * (half ? -b2[n][e] : b1[n][e]) : 0.f;
+                    col[e & 1] += f;
+                    if (e >> 1) f1s += f;
+                    else f0 += f;
+                }
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) {
+                    col[0] += __shfl_xor_sync(0xffffffffu, col[0], o);
+                    col[1] += __shfl_xor_sync(0xffffffffu, col[1], o);
+                }
+                if (g == 0) {
+                    cf[8 * h + 2 * c] = col[0];
+                    cf[8 * h + 2 * c + 1] = col[1];
+                }
+            }
+        }
+        f0 += __shfl_xor_sync(0xffffffffu, f0, 1);
+        f0 += __shfl_xor_sync(0xffffffffu, f0, 2);
+        f1s += __shfl_xor_sync(0xffffffffu, f1s, 1);
+        f1s += __shfl_xor_sync(0xffffffffu, f1s, 2);
+        if (c == 0) {
+            rowf[half * kCH + m0 + g] = f0;
+            rowf[half * kCH + m0 + g + 8] = f1s;
         }
 #pragma unroll
         for (int k4 = 0; k4 < 4; ++k4) {
@@ -961,14 +1012,8 @@ __global__ void __launch_bounds__(kGradThreads, D == 128 ? 1 : 2) delta_grads_tc
             in = inner(sk[x], *reinterpret_cast<const uint4 *>(Mt + tile_off<ROW>(e / PIECES, e % PIECES)), in);
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            in += __shfl_xor_sync(0xffffffffu, in, o);
-            start += __shfl_xor_sync(0xffffffffu, start, o);
-        }
-        if (lane == 0) {
-            red[warp] = in;
-            red[8 + warp] = start;
-        }
+        for (int o = 16; o > 0; o >>= 1) in += __shfl_xor_sync(0xffffffffu, in, o);
+        if (lane == 0) red[warp] = in;
     }
     // E R
 #pragma unroll
@@ -983,24 +1028,6 @@ __global__ void __launch_bounds__(kGradThreads, D == 128 ? 1 : 2) delta_grads_tc
             mma16816(y[2 * n2 + 1], ae, b[2], b[3]);
         }
     }
-    auto row_dot = [&](const float (&x)[HN][4], const uint8_t *tile, int what) {  // per token, over this half
-        float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-        for (int n = 0; n < HN; ++n) {
-            const uint32_t a0 = *reinterpret_cast<const uint32_t *>(tile + tile_off<ROW>(m0 + g, d0 / 8 + n) + 4 * c);
-            const uint32_t a1 = *reinterpret_cast<const uint32_t *>(tile + tile_off<ROW>(m0 + g + 8, d0 / 8 + n) + 4 * c);
-            s0 = fmaf(x[n][0], low_f(a0), fmaf(x[n][1], high_f(a0), s0));
-            s1 = fmaf(x[n][2], low_f(a1), fmaf(x[n][3], high_f(a1), s1));
-        }
-        s0 += __shfl_xor_sync(0xffffffffu, s0, 1);
-        s0 += __shfl_xor_sync(0xffffffffu, s0, 2);
-        s1 += __shfl_xor_sync(0xffffffffu, s1, 1);
-        s1 += __shfl_xor_sync(0xffffffffu, s1, 2);
-        if (c == 0) {
-            rowsum[(2 * what + half) * kCH + m0 + g] = s0;
-            rowsum[(2 * what + half) * kCH + m0 + g + 8] = s1;
-        }
-    };
     {
         const float e0 = expf(ce - c_lo), e1 = expf(ce - c_hi);
 #pragma unroll
@@ -1064,7 +1091,6 @@ __global__ void __launch_bounds__(kGradThreads, D == 128 ? 1 : 2) delta_grads_tc
         }
     }
     row_dot(y, Kt, 0);
-    row_dot(dq, Qt, 1);
     {
         const float be0 = bet[m0 + g], be1 = bet[m0 + g + 8];
 #pragma unroll
@@ -1142,37 +1168,39 @@ __global__ void __launch_bounds__(kGradThreads, D == 128 ? 1 : 2) delta_grads_tc
             *reinterpret_cast<uint4 *>(a.dk + (row0 + r) * D + pc * 8) = *reinterpret_cast<const uint4 *>(Kt + tile_off<ROW>(r, pc));
         }
     }
-    if (warp == 0) {  // dbeta, and h backwards over the chunk: two tokens per lane
+    if (warp == 0) {
+        // dbeta, and h_t = <adjoint, memory> before token t: exp(c_end) <R, S>, the reads of S by tokens i >= t, the
+        // writes of tokens j < t into R, and the pairs F_ij on either side of t.  As a running sum from the end every
+        // pair enters with one value and leaves with the same, so nothing of the pairs on one side stays behind.
         const int i = 2 * lane;
-        float in = 0.f, hb = 0.f, first = 0.f;
+        float in = 0.f, fr = 0.f;
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            in += red[x];
-            first += red[8 + x];
-        }
+        for (int x = 0; x < 8; ++x) in += red[x];
         float h0 = 0.f, h1 = 0.f;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const float r = rowsum[2 * kCH + i + x] + rowsum[3 * kCH + i + x] - hv[i + x];
+            const int t = i + x;
+            const float f = bet[t] * (rowsum[4 * kCH + t] + rowsum[5 * kCH + t]);
+            float r = (rowsum[2 * kCH + t] + rowsum[3 * kCH + t]) - (rowsum[6 * kCH + t] + rowsum[7 * kCH + t]) - f;
+            r += rowf[t] + rowf[kCH + t];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) r -= colf[q * kCH + t];
             (x ? h1 : h0) = r;
-            hb += bet[i + x] * (rowsum[4 * kCH + i + x] + rowsum[5 * kCH + i + x]);
+            fr += f;
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) hb += __shfl_xor_sync(0xffffffffu, hb, o);
+        for (int o = 16; o > 0; o >>= 1) fr += __shfl_xor_sync(0xffffffffu, fr, o);
         float s = h0 + h1;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const float n = __shfl_down_sync(0xffffffffu, s, o);
             if (lane + o < 32) s += n;
         }
-        // h is known at both ends of the chunk; the running sum between them gathers the roundings of its
-        // terms, and the gap at the first token is taken out along the way
-        const float end = expf(ce) * in + hb;
-        const float gap = (first - (end + __shfl_sync(0xffffffffu, s, 0))) / (float)w.cnt;
+        const float end = expf(ce) * in + fr;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             if (i + x >= w.cnt) continue;
-            const float h = end + s - (x ? h0 : 0.f) + gap * (float)(w.cnt - i - x);
+            const float h = end + s - (x ? h0 : 0.f);
             a.dla[row0 + i + x] = __float2bfloat16_rn(w.ch == 0 && i + x == 0 ? 0.f : h);  // the first decay meets an empty memory
             a.dbe[row0 + i + x] = __float2bfloat16_rn(rowsum[i + x] + rowsum[kCH + i + x]);
         }

@@ -304,7 +304,6 @@ struct DeltaTcArgs {
     const float *dq_add;   // [BH][L][d] added to dq, or null
     const float *rho;      // [BH][N][NCH][d], with pw
     __nv_bfloat16 *R_c;    // [BH][N][NCH][d][d] adjoint after every chunk
-    __nv_bfloat16 *W_lo;   // [BH][L][d] what the rounding of w_t to dv_t left
     __nv_bfloat16 *dq, *dk, *dv, *dla, *dbe;
     int BH, L, C, N, NCH;
 };
