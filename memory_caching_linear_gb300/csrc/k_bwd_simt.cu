@@ -1144,6 +1144,8 @@ size_t backward_scratch_bytes(const Problem &p)
     return common + pad256(4 * BH * L) + 2 * pad256(4 * BH * L * d) + 2 * pad256(4 * BH * L * sel);
 }
 
+cudaError_t launch_bwd_route(const Problem &p, const BwdArgs &a, cudaStream_t s) { MC_BWD_DISPATCH(route_impl, p, a, s); }
+
 cudaError_t launch_bwd_router_simt(const Problem &p, const BwdArgs &a, cudaStream_t s) { MC_BWD_DISPATCH(router_impl, p, a, s); }
 
 cudaError_t launch_backward_simt(const Problem &p, const void *q, const void *k, const void *v, const void *u,

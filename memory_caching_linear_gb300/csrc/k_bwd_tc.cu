@@ -255,9 +255,13 @@ struct CArgs {
     float *dg;              // 2 x [BH][N][L] out: dy_t . M^(i) q_t, summed over each column half
     float *dgon;            // 2 x [BH][L] out: dy_t . M_t q_t, the same
     __nv_bfloat16 *dq;      // [BH][L][d] out: dq
+    float *dqf;             // !ONLINE: [BH][L][d] out: the cached memories' dq
     int BH, L, C, N, CPS, d, mode, num_tiles;
 };
 
+// ONLINE false: the cached memories' part alone (for a memory whose online reads have their own kernels):
+// no prefix state, K or V, dg_on is not written and dq goes out in fp32.
+template <bool ONLINE>
 __global__ void __launch_bounds__(kCThreads, 1)
     bwd_cached_tc(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                   const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mY, CArgs a)
@@ -329,8 +333,8 @@ __global__ void __launch_bounds__(kCThreads, 1)
                 tma_load_2d(sY, &mY, 0, row, &tile_full);
                 tma_load_2d(sY + 16384, &mY, 64, row, &tile_full);
                 // ring items: K, V, then the prefix state (chunk c > 0) and the cached states
-                const int nimg = (c > 0 ? 1 : 0) + n;
-                for (int m = -2; m < nimg && ok; ++m, ++gr) {
+                const int npre = ONLINE && c > 0 ? 1 : 0, nimg = npre + n;
+                for (int m = ONLINE ? -2 : 0; m < nimg && ok; ++m, ++gr) {
                     const int s = gr % kCRing;
                     if (!(ok = mbar_wait(&ring_empty[s], ((gr / kCRing) & 1) ^ 1, &abort_flag))) break;
                     mbar_arrive_expect_tx(&ring_full[s], kGTile);
@@ -341,9 +345,8 @@ __global__ void __launch_bounds__(kCThreads, 1)
                         tma_load_2d(dst + 16384, map, 64, row, &ring_full[s]);
                         continue;
                     }
-                    const uint8_t *src = (c > 0 && m == 0)
-                                             ? a.spre + (((size_t)bh * a.N + n) * a.CPS + c) * kGTile
-                                             : a.images + ((size_t)bh * a.N + (m - (c > 0 ? 1 : 0))) * kGTile;
+                    const uint8_t *src = m < npre ? a.spre + (((size_t)bh * a.N + n) * a.CPS + c) * kGTile
+                                                  : a.images + ((size_t)bh * a.N + (m - npre)) * kGTile;
                     bulk_load(dst, src, kGTile, &ring_full[s]);
                 }
             }
@@ -367,7 +370,10 @@ __global__ void __launch_bounds__(kCThreads, 1)
             for (int j = 0; j < my_tiles && ok; ++j) {
                 int bh, n, c;
                 tile(j, bh, n, c);
-                const int nimg = (c > 0 ? 1 : 0) + n;
+                const int nimg = (ONLINE && c > 0 ? 1 : 0) + n;
+                if (!ONLINE) {
+                    if (!(ok = mbar_wait(&tile_full, j & 1, &abort_flag))) break;
+                } else {
                 // K and V: the tile's first two ring items
                 const uint32_t sk = gr % kCRing, sv = (gr + 1) % kCRing;
                 const uint32_t k0 = r0 + sk * kGTile, v0 = r0 + sv * kGTile;
@@ -409,6 +415,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
                 mma_commit(&ring_empty[sk]);  // K is spent
                 ++gw;
                 ++ga;
+                }
                 if (nimg == 0) mma_commit(&tile_empty);
                 for (int m = 0; m < nimg && ok; ++m, ++gw, ++gr) {
                     const uint32_t s = gr % kCRing, w = gw % kCW;
@@ -444,14 +451,14 @@ __global__ void __launch_bounds__(kCThreads, 1)
         for (int j = 0; j < my_tiles && ok; ++j) {
             int bh, n, c;
             tile(j, bh, n, c);
-            const int nimg = (c > 0 ? 1 : 0) + n;
+            const int npre = ONLINE && c > 0 ? 1 : 0, nimg = npre + n;
             const int t = n * a.C + c * kGT + row;  // token within the head
             if (!(ok = mbar_wait(&tile_full, j & 1, &abort_flag))) break;
-            const float gon = routed ? __ldg(a.tok + ((size_t)bh * a.L + t) * kBwdTokWords + 2)
+            const float gon = !ONLINE ? 0.f : routed ? __ldg(a.tok + ((size_t)bh * a.L + t) * kBwdTokWords + 2)
                                      : (a.mode == MC_MEAN ? 1.f / (float)(n + 1) : 1.f);
             // in-chunk online part over the half's key columns: dg_on += sum_{j<=t} G1 G2, P2 = g_on mask(G2)
             float dgon = 0.f;
-            {
+            if (ONLINE) {
                 const uint32_t w1 = gw % kCW, w2 = (gw + 1) % kCW;
                 if (!(ok = mbar_wait(&w_full[w1], (gw / kCW) & 1, &abort_flag) &&
                            mbar_wait(&w_full[w2], ((gw + 1) / kCW) & 1, &abort_flag) &&
@@ -494,7 +501,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
             const float *grow = routed ? a.gam + (size_t)bh * a.N * a.L + t : nullptr;
             float *dgrow = a.dg + hoff * a.N + (size_t)bh * a.N * a.L + t;
             const float gconst = a.mode == MC_MEAN ? 1.f / (float)(n + 1) : 1.f;
-            const int i0 = c > 0 ? -1 : 0;  // state index of item m is i0 + m (-1: the prefix state)
+            const int i0 = -npre;  // state index of item m is i0 + m (-1: the prefix state)
             auto gate = [&](int m) {
                 const int i = i0 + m;
                 return i < 0 ? gon : (routed ? __ldg(grow + (size_t)i * a.L) : gconst);
@@ -502,7 +509,10 @@ __global__ void __launch_bounds__(kCThreads, 1)
             float g_cur = nimg > 0 ? gate(0) : 0.f, g_nxt = nimg > 1 ? gate(1) : 0.f;
             // dq starts from the in-chunk product P2 K (the half's 64 columns)
             float dqa[64];
-            {
+            if (!ONLINE) {
+#pragma unroll
+                for (int k = 0; k < 64; ++k) dqa[k] = 0.f;
+            } else {
                 const uint32_t w = gw % kCW;
                 if (!(ok = mbar_wait(&w_full[w], (gw / kCW) & 1, &abort_flag))) break;
                 tc_fence_after();
@@ -554,6 +564,15 @@ __global__ void __launch_bounds__(kCThreads, 1)
                 else dgrow[(size_t)(i0 + m) * a.L] = d0 + d1;
             }
             if (!ok) break;
+            if (!ONLINE) {
+                float *dst = a.dqf + ((size_t)bh * a.L + t) * a.d + 64 * half;
+                if (64 * half < a.d) {
+#pragma unroll
+                    for (int k = 0; k < 64; k += 4)
+                        *reinterpret_cast<float4 *>(dst + k) = make_float4(dqa[k], dqa[k + 1], dqa[k + 2], dqa[k + 3]);
+                }
+                continue;
+            }
             a.dgon[hoff + (size_t)bh * a.L + t] = dgon;
             // the half's 64 columns of dq
             __nv_bfloat16 *dqrow = a.dq + ((size_t)bh * a.L + t) * a.d;
@@ -1227,14 +1246,39 @@ cudaError_t launch_bwd_cached_tc(const Problem &p, const void *q, const void *k,
     a.dq = static_cast<__nv_bfloat16 *>(dq);
     a.BH = p.BH; a.L = p.L; a.C = p.C; a.N = p.N; a.CPS = p.C / kGT; a.d = p.d; a.mode = p.mode;
     a.num_tiles = p.BH * p.N * a.CPS;
-    cudaError_t e = cudaFuncSetAttribute(bwd_cached_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kCSmem);
+    cudaError_t e = cudaFuncSetAttribute(bwd_cached_tc<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kCSmem);
     if (e != cudaSuccess) return e;
     int dev = 0, sms = 0;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (sms <= 0) sms = 148;
     const int grid = a.num_tiles < sms ? a.num_tiles : sms;
-    bwd_cached_tc<<<grid, kCThreads, kCSmem, s>>>(mQ, mK, mV, mY, a);
+    bwd_cached_tc<true><<<grid, kCThreads, kCSmem, s>>>(mQ, mK, mV, mY, a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_bwd_cached_only_tc(const Problem &p, const void *q, const void *dy, const uint8_t *states_img,
+                                      const float *gam, float *dq, float *dg, cudaStream_t s)
+{
+    CUtensorMap mQ, mY;
+    const unsigned long long rows = (unsigned long long)p.BH * p.L;
+    if (!make_tmap_bf16_sw128(&mQ, q, rows, p.d, kGT) || !make_tmap_bf16_sw128(&mY, dy, rows, p.d, kGT))
+        return cudaErrorInvalidValue;
+    CArgs a{};
+    a.images = states_img;
+    a.gam = gam;
+    a.dg = dg;
+    a.dqf = dq;
+    a.BH = p.BH; a.L = p.L; a.C = p.C; a.N = p.N; a.CPS = p.C / kGT; a.d = p.d; a.mode = p.mode;
+    a.num_tiles = p.BH * p.N * a.CPS;
+    cudaError_t e = cudaFuncSetAttribute(bwd_cached_tc<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kCSmem);
+    if (e != cudaSuccess) return e;
+    int dev = 0, sms = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (sms <= 0) sms = 148;
+    const int grid = a.num_tiles < sms ? a.num_tiles : sms;
+    bwd_cached_tc<false><<<grid, kCThreads, kCSmem, s>>>(mQ, mQ, mQ, mY, a);
     return cudaGetLastError();
 }
 

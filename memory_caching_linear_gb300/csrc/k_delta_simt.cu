@@ -429,26 +429,57 @@ __global__ void __launch_bounds__(kGT) delta_grads_simt(DeltaArgs a)
 //               plus dkbar / segment length (the gradient), in place
 //   pool_score: r_on[t] = <u_t, keys of the segment up to t> / their number
 // ---------------------------------------------------------------------------
+// A chunk's rows in 16-byte pieces: thread (lane tl, piece pc) takes the TPL tokens from tl TPL on.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) pool_sums(DeltaArgs a, const T *x, const float *tok, float *out)
+struct PoolTile {
+    static constexpr int V = 16 / (int)sizeof(T), PC = D / V;
+    static constexpr int TL = 256 / PC < kCH ? 256 / PC : kCH;
+    static constexpr int TPL = kCH / TL;
+    static constexpr int NT = TL * PC;  // threads at work
+};
+template <typename T, int V>
+__device__ __forceinline__ void load_piece(float (&x)[V], const T *src)
 {
-    __shared__ float part[256];
-    const int ch = (int)blockIdx.x % a.NCH;
-    const int seg = (int)(blockIdx.x / a.NCH) % a.N, bh = (int)(blockIdx.x / a.NCH) / a.N;
-    const int t0 = seg * a.C, tb = t0 + ch * kCH, te = min(min(tb + kCH, t0 + a.C), a.L);
-    constexpr int ways = 256 / D;
-    const int c = threadIdx.x % D, w = threadIdx.x / D;
-    float s = 0.f;
-    for (int t = tb + w; t < te; t += ways) {
-        const size_t tt = (size_t)bh * a.L + t;
-        s = fmaf(tok ? tok[tt * kBwdTokWords + 4] : 1.f, to_f(x[tt * D + c]), s);
-    }
-    part[threadIdx.x] = s;
-    __syncthreads();
-    if (w == 0) {
+    const uint4 q = *reinterpret_cast<const uint4 *>(src);
+    const T *t = reinterpret_cast<const T *>(&q);
 #pragma unroll
-        for (int i = 1; i < ways; ++i) s += part[i * D + c];
-        out[(size_t)blockIdx.x * D + c] = s;
+    for (int i = 0; i < V; ++i) x[i] = to_f(t[i]);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(256) pool_sums(DeltaArgs a, const T *x, const float *pw, float *out)
+{
+    using P = PoolTile<T, D>;
+    __shared__ float part[P::TL * (D + 1)];
+    const int ch = (int)(blockIdx.x % a.NCH);
+    const int seg = (int)(blockIdx.x / a.NCH) % a.N, bh = (int)(blockIdx.x / a.NCH) / a.N;
+    const int t0 = seg * a.C, tb = t0 + ch * kCH, cnt = min(min(tb + kCH, t0 + a.C), a.L) - tb;
+    if (cnt <= 0) return;
+    const int tid = threadIdx.x, pc = tid % P::PC, tl = tid / P::PC;
+    const size_t row0 = (size_t)bh * a.L + tb;
+    if (tid < P::NT) {
+        float s[P::V];
+#pragma unroll
+        for (int i = 0; i < P::V; ++i) s[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < P::TPL; ++j) {
+            const int t = tl * P::TPL + j;
+            if (t >= cnt) break;
+            float v[P::V];
+            load_piece<T, P::V>(v, x + (row0 + t) * D + pc * P::V);
+            const float f = pw ? pw[(row0 + t) * a.gw_stride] : 1.f;
+#pragma unroll
+            for (int i = 0; i < P::V; ++i) s[i] = fmaf(f, v[i], s[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < P::V; ++i) part[tl * (D + 1) + pc * P::V + i] = s[i];
+    }
+    __syncthreads();
+    if (tid < D) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < P::TL; ++i) s += part[i * (D + 1) + tid];
+        out[(size_t)blockIdx.x * D + tid] = s;
     }
 }
 
@@ -479,32 +510,56 @@ __global__ void __launch_bounds__(D) pool_scan(DeltaArgs a, float *sums, float *
 template <typename T, int D>
 __global__ void __launch_bounds__(256) pool_score(DeltaArgs a, const float *kpre, float *r_on)
 {
-    constexpr int P = D + 1;
-    extern __shared__ float sm[];  // kCH x P running key sums
-    const int ch = (int)blockIdx.x % a.NCH;
+    using P = PoolTile<T, D>;
+    __shared__ float part[P::TL * (D + 1)];
+    const int ch = (int)(blockIdx.x % a.NCH);
     const int seg = (int)(blockIdx.x / a.NCH) % a.N, bh = (int)(blockIdx.x / a.NCH) / a.N;
-    const int t0 = seg * a.C, tb = t0 + ch * kCH, te = min(min(tb + kCH, t0 + a.C), a.L);
-    if (tb >= te) return;
-    const int cnt = te - tb, tid = threadIdx.x;
-    const size_t base = (size_t)bh * a.L * D;
-    const T *k = static_cast<const T *>(a.k) + base, *u = static_cast<const T *>(a.u) + base;
-    for (int e = tid; e < cnt * D; e += 256) sm[(e / D) * P + e % D] = to_f(k[(size_t)tb * D + e]);
+    const int t0 = seg * a.C, tb = t0 + ch * kCH, cnt = min(min(tb + kCH, t0 + a.C), a.L) - tb;
+    if (cnt <= 0) return;
+    const int tid = threadIdx.x, pc = tid % P::PC, tl = tid / P::PC;
+    const size_t row0 = (size_t)bh * a.L + tb;
+    const T *k = static_cast<const T *>(a.k), *u = static_cast<const T *>(a.u);
+    float x[P::TPL][P::V];  // running key sums over the lane's tokens
+#pragma unroll
+    for (int j = 0; j < P::TPL; ++j) {
+        const int t = tl * P::TPL + j;
+        if (tid < P::NT && t < cnt) {
+            load_piece<T, P::V>(x[j], k + (row0 + t) * D + pc * P::V);
+        } else {
+#pragma unroll
+            for (int i = 0; i < P::V; ++i) x[j][i] = 0.f;
+        }
+        if (j > 0)
+#pragma unroll
+            for (int i = 0; i < P::V; ++i) x[j][i] += x[j > 0 ? j - 1 : 0][i];
+    }
+    if (tid < P::NT)
+#pragma unroll
+        for (int i = 0; i < P::V; ++i) part[tl * (D + 1) + pc * P::V + i] = x[P::TPL - 1][i];
     __syncthreads();
-    if (tid < D) {
-        float acc = kpre[(size_t)blockIdx.x * D + tid];
-        for (int t = 0; t < cnt; ++t) {
-            acc += sm[t * P + tid];
-            sm[t * P + tid] = acc;
+    if (tid < D) {  // keys of the segment before each lane's tokens
+        float s = kpre[(size_t)blockIdx.x * D + tid];
+#pragma unroll
+        for (int i = 0; i < P::TL; ++i) {
+            const float own = part[i * (D + 1) + tid];
+            part[i * (D + 1) + tid] = s;
+            s += own;
         }
     }
     __syncthreads();
-    const int lane = tid % 32;
-    for (int t = tid / 32; t < cnt; t += 8) {
-        float s = 0.f;
-        for (int c = lane; c < D; c += 32) s = fmaf(to_f(u[(size_t)(tb + t) * D + c]), sm[t * P + c], s);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) r_on[(size_t)bh * a.L + tb + t] = s / (float)(tb + t - t0 + 1);
+    for (int j = 0; j < P::TPL; ++j) {
+        const int t = tl * P::TPL + j;
+        float s = 0.f;
+        if (tid < P::NT && t < cnt) {
+            float v[P::V];
+            load_piece<T, P::V>(v, u + (row0 + t) * D + pc * P::V);
+#pragma unroll
+            for (int i = 0; i < P::V; ++i) s = fmaf(v[i], x[j][i] + part[tl * (D + 1) + pc * P::V + i], s);
+        }
+#pragma unroll
+        for (int o = P::PC / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (pc == 0 && tid < P::NT && t < cnt) r_on[row0 + t] = s / (float)(tb + t - t0 + 1);
     }
 }
 
@@ -541,14 +596,14 @@ cudaError_t pool_impl(const Problem &p, const DeltaArgs &a, float *sums, float *
     const unsigned chunks = (unsigned)((long long)p.BH * p.N * a.NCH);
     pool_sums<T, D><<<chunks, 256, 0, s>>>(a, static_cast<const T *>(a.k), nullptr, sums);
     pool_scan<D><<<(unsigned)((long long)p.BH * p.N), D, 0, s>>>(a, sums, kbar, nullptr);
-    if (r_on) pool_score<T, D><<<chunks, 256, sizeof(float) * kCH * (D + 1), s>>>(a, sums, r_on);
+    if (r_on) pool_score<T, D><<<chunks, 256, 0, s>>>(a, sums, r_on);
     return cudaGetLastError();
 }
 
 template <typename T, int D>
-cudaError_t pool_grad_impl(const Problem &p, const DeltaArgs &a, float *rho, const float *dkbar, cudaStream_t s)
+cudaError_t pool_grad_impl(const Problem &p, const DeltaArgs &a, const float *pw, float *rho, const float *dkbar, cudaStream_t s)
 {
-    pool_sums<T, D><<<(unsigned)((long long)p.BH * p.N * a.NCH), 256, 0, s>>>(a, static_cast<const T *>(a.u), a.tok, rho);
+    pool_sums<T, D><<<(unsigned)((long long)p.BH * p.N * a.NCH), 256, 0, s>>>(a, static_cast<const T *>(a.u), pw, rho);
     pool_scan<D><<<(unsigned)((long long)p.BH * p.N), D, 0, s>>>(a, rho, nullptr, dkbar);
     return cudaGetLastError();
 }
@@ -573,9 +628,9 @@ cudaError_t launch_pool_simt(const Problem &p, const DeltaArgs &a, float *sums, 
 {
     MC_DELTA_DISPATCH(pool_impl, p, a, sums, kbar, r_on, s);
 }
-cudaError_t launch_pool_grad_simt(const Problem &p, const DeltaArgs &a, float *rho, const float *dkbar, cudaStream_t s)
+cudaError_t launch_pool_grad_simt(const Problem &p, const DeltaArgs &a, const float *pw, float *rho, const float *dkbar, cudaStream_t s)
 {
-    MC_DELTA_DISPATCH(pool_grad_impl, p, a, rho, dkbar, s);
+    MC_DELTA_DISPATCH(pool_grad_impl, p, a, pw, rho, dkbar, s);
 }
 
 }  // namespace mc

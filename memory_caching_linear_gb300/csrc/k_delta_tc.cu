@@ -264,6 +264,24 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_tc(DeltaTcArgs a)
     }
 }
 
+// A warp's 16 rows of f S into an operand image (D / 64 panels of D rows), through its 2 KB staging area.
+template <int NT>
+__device__ __forceinline__ void put_image(const float (&S)[NT][4], uint8_t *img, float f, uint8_t *outb, int row, int lane)
+{
+#pragma unroll
+    for (int h = 0; h < NT / 8; ++h) {
+#pragma unroll
+        for (int n = 8 * h; n < 8 * h + 8; n += 2)
+            stsm4(smem_addr(outb) + tile_off<128>(lane & 15, (n & 7) + (lane >> 4)), pack2(f * S[n][0], f * S[n][1]),
+                  pack2(f * S[n][2], f * S[n][3]), pack2(f * S[n + 1][0], f * S[n + 1][1]), pack2(f * S[n + 1][2], f * S[n + 1][3]));
+        __syncwarp();
+        uint4 *dst = reinterpret_cast<uint4 *>(img + h * (NT * 8 * 128) + row * 128);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) dst[32 * x + lane] = reinterpret_cast<const uint4 *>(outb)[32 * x + lane];
+        __syncwarp();
+    }
+}
+
 // ---------------------------------------------------------------------------
 // delta_walk_tc: one CTA per (bh, segment, 16 NW value rows); NW warps of 16 rows.  Two stages of
 // the chunk's K, V columns, (Q,) and record, filled by asynchronous copies one chunk ahead.
@@ -333,6 +351,9 @@ __global__ void __launch_bounds__(32 * NW) delta_walk_tc(DeltaTcArgs a)
         const int cnt = min(kCH, len - ch * kCH);
         const size_t cidx = (size_t)sid * a.NCH + ch;
 
+        // an image's panels: 64 columns of all D rows, rows of 128 bytes with their pieces exchanged by row % 8
+        if (a.spre_img && ch > 0 && !(ch & 1))
+            put_image(S, a.spre_img + ((size_t)sid * (a.C / 128) + ch / 2) * (D * D * 2), vec[0], outb, vbase + 16 * warp, lane);
         if (a.S_c) {  // the memory before the chunk, in bf16, through the warp's staging area
             __nv_bfloat16 *dst = a.S_c + (cidx * D + vbase + 16 * warp) * D;
 #pragma unroll
@@ -512,6 +533,7 @@ __global__ void __launch_bounds__(32 * NW) delta_walk_tc(DeltaTcArgs a)
                 mma16816(S[2 * n2 + 1], ul[k4], b[2], b[3]);
             }
     }
+    if (a.states_img) put_image(S, a.states_img + (size_t)sid * (D * D * 2), 1.f, outb, vbase + 16 * warp, lane);
     if (a.states) {
         float *dst = a.states + ((size_t)sid * D + vbase + 16 * warp) * D;
 #pragma unroll
@@ -574,7 +596,16 @@ __global__ void __launch_bounds__(32 * NW) delta_rwalk_tc(DeltaTcArgs a)
     };
 
     float R[2 * KS][4];
-    if (a.G && seg < a.N - 1) {
+    if (a.G_img && seg < a.N - 1) {  // 128 x 128 image: two panels of 128 rows
+        const uint8_t *img = a.G_img + (size_t)sid * 32768;
+        const int r = vbase + 16 * warp + g;
+#pragma unroll
+        for (int n = 0; n < 2 * KS; ++n) {
+            const uint8_t *at = img + (n / 8) * 16384 + r * 128 + (((n & 7) ^ (r & 7)) << 4) + 4 * c;
+            const uint32_t x = *reinterpret_cast<const uint32_t *>(at), y = *reinterpret_cast<const uint32_t *>(at + 8 * 128);
+            R[n][0] = low_f(x); R[n][1] = high_f(x); R[n][2] = low_f(y); R[n][3] = high_f(y);
+        }
+    } else if (a.G && seg < a.N - 1) {
         const float *src = a.G + ((size_t)sid * D + vbase + 16 * warp) * D;
 #pragma unroll
         for (int n = 0; n < 2 * KS; ++n) {
@@ -1244,6 +1275,23 @@ __global__ void __launch_bounds__(256) delta_scalars(const __nv_bfloat16 *la, fl
     one[i] = 1.f;
 }
 
+// dy_t . O_t per token (the gradient of the online gate): one warp per token.
+__global__ void __launch_bounds__(256) delta_dgon(const __nv_bfloat16 *dy, const float *O, float *dgon, long long tokens, int d)
+{
+    const long long t = (long long)blockIdx.x * 8 + threadIdx.x / 32;
+    if (t >= tokens) return;
+    const int lane = threadIdx.x % 32;
+    float s = 0.f;
+    for (int i = 2 * lane; i < d; i += 64) {
+        const uint32_t y = *reinterpret_cast<const uint32_t *>(dy + t * d + i);
+        const float2 o = *reinterpret_cast<const float2 *>(O + t * d + i);
+        s = fmaf(low_f(y), o.x, fmaf(high_f(y), o.y, s));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) dgon[t] = s;
+}
+
 template <int D, bool READ, bool REV>
 cudaError_t prep_impl(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
 {
@@ -1278,6 +1326,13 @@ cudaError_t walk_impl(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
 }
 
 }  // namespace
+
+cudaError_t launch_delta_dgon(const Problem &p, const void *dy, const float *O_on, float *dgon, cudaStream_t s)
+{
+    const long long n = (long long)p.BH * p.L;
+    delta_dgon<<<(unsigned)((n + 7) / 8), 256, 0, s>>>(static_cast<const __nv_bfloat16 *>(dy), O_on, dgon, n, p.d);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_delta_grads_tc(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
 {

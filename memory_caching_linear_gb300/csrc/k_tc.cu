@@ -194,6 +194,31 @@ __global__ void __launch_bounds__(kRouterThreads, 1) gate_tiles_tc(const __grid_
     if (threadIdx.x == 0 && abort_flag) atomicExch(&g_tc_abort, 1);
 }
 
+// Key means [BH][N][d] as image rows; one CTA per row of a head's blocks of 64.
+__global__ void __launch_bounds__(kD) kbar_rows(const float *__restrict__ kbar, uint8_t *img, int N, int NB, int d)
+{
+    const int rows = NB * 64, row = (int)(blockIdx.x % rows), bh = (int)(blockIdx.x / rows), col = threadIdx.x;
+    const float v = row < N && col < d ? kbar[((size_t)bh * N + row) * d + col] : 0.f;
+    store_kbar_terms(img + (size_t)bh * NB * kKbImg, row, col, v);
+}
+
+// fp32 states as 128 x 128 images: one CTA per state, 16 bytes (8 columns) per thread and step.
+__global__ void __launch_bounds__(256) state_rows(const float *__restrict__ states, uint8_t *img, int d)
+{
+    const float *src = states + (size_t)blockIdx.x * d * d;
+    uint8_t *dst = img + (size_t)blockIdx.x * kTile;
+    for (int e = threadIdx.x; e < kD * kD / 8; e += 256) {
+        const int r = e / (kD / 8), c8 = e % (kD / 8);
+        uint4 o = make_uint4(0u, 0u, 0u, 0u);
+        if (r < d && 8 * c8 < d) {
+            const float4 x = *reinterpret_cast<const float4 *>(src + (size_t)r * d + 8 * c8);
+            const float4 y = *reinterpret_cast<const float4 *>(src + (size_t)r * d + 8 * c8 + 4);
+            o = make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+        }
+        *reinterpret_cast<uint4 *>(dst + sw128_offset(r, 8 * c8, kD)) = o;
+    }
+}
+
 int g_num_sms = 0;
 
 }  // namespace
@@ -213,6 +238,30 @@ bool tc_supported(const Problem &p)
 bool tc_fused_gates(const Problem &p) { return tc_supported(p) && p.N <= 64; }
 
 size_t tc_scratch_bytes(const Problem &p) { return forward_scratch_bytes(p); }
+
+TcForwardImages tc_forward_images(const Problem &p, void *scratch)
+{
+    const size_t BH = p.BH, N = p.N, im = img_bytes(p);
+    TcForwardImages t;
+    t.states_img = static_cast<uint8_t *>(scratch);
+    t.spre_img = t.states_img + pad256(BH * N * im);
+    t.kbar_img = t.spre_img + pad256(BH * N * (p.C / kCT) * im);
+    t.r_on = reinterpret_cast<float *>(t.kbar_img + pad256(BH * ((N + 63) / 64) * kKbImg));
+    return t;
+}
+
+cudaError_t launch_kbar_images(const Problem &p, const float *kbar, uint8_t *kbar_img, cudaStream_t s)
+{
+    const int NB = (p.N + 63) / 64;
+    kbar_rows<<<(unsigned)((long long)p.BH * NB * 64), kD, 0, s>>>(kbar, kbar_img, p.N, NB, p.d);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_state_images(const Problem &p, const float *states, uint8_t *img, cudaStream_t s)
+{
+    state_rows<<<(unsigned)((long long)p.BH * p.N), 256, 0, s>>>(states, img, p.d);
+    return cudaGetLastError();
+}
 
 // SSC router alone (mc_ssc_select) on the tensor-core path's shapes: key-mean
 // images, then the router kernel.
@@ -325,7 +374,8 @@ cudaError_t launch_bwd_gates_tc(const Problem &p, const void *u, const TcImages 
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRouterSmem);
     if (e != cudaSuccess) return e;
     const int gtiles = p.BH * (p.L / kCT);
-    const int ggrid = gtiles < g_num_sms ? gtiles : g_num_sms;
+    const int sms = sm_count();
+    const int ggrid = gtiles < sms ? gtiles : sms;
     k<<<ggrid, kRouterThreads, kRouterSmem, s>>>(mU, a);
     return cudaGetLastError();
 }

@@ -121,14 +121,13 @@ int forward_delta_tc(const Call &c, const void *q, const void *k, const void *v,
             alpha = cv.take<float>(BH * L);
             zero = cv.take<float>(BH * L);
             ones = cv.take<float>(BH * L);
-            f.states = cv.take<float>(BH * N * d * d);
             tc_scratch = cv.take<char>(tc_scratch_bytes(p));
         } else if (!one) {
             t.O_on = cv.take<float>(BH * L * d);
-            kbar = cv.take<float>(BH * N * d, routed);
             r_on = cv.take<float>(BH * L, routed);
-            sums = cv.take<float>(BH * N * c.NCH * d, routed);
         }
+        kbar = cv.take<float>(BH * N * d, !one && routed);
+        sums = cv.take<float>(BH * N * c.NCH * d, !one && routed);
         if (pass == 0 && scratch_alloc(&scratch, cv.used, s) != cudaSuccess) {
             cudaGetLastError();
             return MC_ERR_ALLOC;
@@ -137,23 +136,33 @@ int forward_delta_tc(const Call &c, const void *q, const void *k, const void *v,
     if (one) t.y = static_cast<__nv_bfloat16 *>(y);
     f.q = q; f.k = k; f.u = routed ? u : nullptr; f.y = y;
     f.BH = p.BH; f.L = p.L; f.C = p.C; f.N = p.N; f.mode = p.mode; f.topk = p.topk;
+    TcForwardImages img{};
+    if (tc) {
+        img = tc_forward_images(p, tc_scratch);
+        t.spre_img = img.spre_img;
+        t.states_img = img.states_img;
+        r_on = img.r_on;
+    }
     profile_call_start(s);
     cudaError_t e = launch_delta_walk_tc(p, t, !tc, s);
+    if (e == cudaSuccess && !one && routed) {
+        DeltaArgs a = delta_args(c);
+        a.k = k; a.u = f.u;
+        e = launch_pool_simt(p, a, sums, kbar, r_on, s);
+        profile_after_kernel(s, "pool_simt");
+    }
+    f.states = t.states;
     if (e == cudaSuccess && tc) {
         f.v = t.U;
         f.alpha = alpha; f.beta = zero; f.lam = ones;
+        f.have_images = true;
         e = launch_delta_scalars(p, la, alpha, zero, ones, s);
+        if (e == cudaSuccess && routed) e = launch_kbar_images(p, kbar, img.kbar_img, s);
         profile_after_kernel(s, "delta_scalars");
         if (e == cudaSuccess) e = launch_forward_tc(p, f, tc_scratch, s);
     } else if (e == cudaSuccess && !one) {
-        DeltaArgs a = delta_args(c);
-        a.k = k; a.u = f.u;
-        if (routed) {
-            e = launch_pool_simt(p, a, sums, kbar, r_on, s);
-            profile_after_kernel(s, "pool_simt");
-        }
         f.states = t.states; f.O_on = t.O_on; f.r_on = r_on; f.kbar = kbar;
-        if (e == cudaSuccess) e = launch_readout_simt(p, f, s);
+        e = launch_readout_simt(p, f, s);
         profile_after_kernel(s, "readout_simt");
     }
     cudaError_t ef = cudaFreeAsync(scratch, s);
@@ -236,7 +245,7 @@ int backward_delta(const void *q, const void *k, const void *v, const void *u, c
     a.q = q; a.k = k; a.v = v; a.la = la; a.be = be; a.dy = dy;
     a.u = routed ? u : nullptr;
     a.dq = dq; a.dk = dk; a.dv = dv; a.dla = dla; a.dbe = dbe;
-    const bool tc = delta_tc_supported(p);
+    const bool tc = delta_tc_supported(p), rtc = tc && many && bwd_tc_supported(p);  // rtc: the gate work too
     DeltaTcArgs t = delta_tc_args(c, q, k, v, la, be);
     t.dy = static_cast<const __nv_bfloat16 *>(dy);
     t.u = static_cast<const __nv_bfloat16 *>(a.u);
@@ -247,7 +256,8 @@ int backward_delta(const void *q, const void *k, const void *v, const void *u, c
     t.dbe = static_cast<__nv_bfloat16 *>(dbe);
     BwdArgs b{};
     float *sums = nullptr, *kbar = nullptr, *r_on = nullptr, *G = nullptr, *dkbar = nullptr, *tok = nullptr,
-          *dq_add = nullptr;
+          *dq_add = nullptr, *gam = nullptr, *dg = nullptr, *dgon = nullptr;
+    uint8_t *states_img = nullptr, *G_img = nullptr, *kbar_img = nullptr;
     void *scratch = nullptr;
     for (int pass = 0; pass < 2; ++pass) {
         Carver cv{static_cast<char *>(scratch), 0};
@@ -262,15 +272,25 @@ int backward_delta(const void *q, const void *k, const void *v, const void *u, c
         t.R_c = cv.take<__nv_bfloat16>(BH * N * NCH * d * d, tc);
         a.states = cv.take<float>(BH * N * d * d, many);
         a.O_on = cv.take<float>(BH * L * d, many);
-        G = cv.take<float>(BH * N * d * d, many);
+        G = cv.take<float>(BH * N * d * d, many && !rtc);
         tok = cv.take<float>(BH * L * kBwdTokWords, many);
         dq_add = cv.take<float>(BH * L * d, many);
         kbar = cv.take<float>(BH * N * d, many);
         dkbar = cv.take<float>(BH * N * d, many);
         r_on = cv.take<float>(BH * L, routed);
         sums = cv.take<float>(BH * N * NCH * d, routed);
-        b.sel_idx = cv.take<int32_t>(BH * L * p.topk, routed && p.mode == MC_SSC);
-        b.sel_g = cv.take<float>(BH * L * p.topk, routed && p.mode == MC_SSC);
+        b.sel_idx = cv.take<int32_t>(BH * L * p.topk, routed && !rtc && p.mode == MC_SSC);
+        b.sel_g = cv.take<float>(BH * L * p.topk, routed && !rtc && p.mode == MC_SSC);
+        b.Np = (int)((N + 15) & ~(size_t)15);
+        states_img = cv.take<uint8_t>(BH * N * 32768, rtc);
+        G_img = cv.take<uint8_t>(BH * N * 32768, rtc);
+        kbar_img = cv.take<uint8_t>(BH * ((N + 63) / 64) * 49152, rtc && routed);
+        gam = cv.take<float>(BH * N * L, rtc && routed);
+        dg = cv.take<float>(2 * BH * N * L, rtc);
+        dgon = cv.take<float>(BH * L, rtc);
+        b.kv_gw = cv.take<float>(2 * BH * L, rtc);
+        b.dr_hi = cv.take<__nv_bfloat16>(BH * b.Np * L, rtc && routed);
+        b.dr_lo = cv.take<__nv_bfloat16>(BH * b.Np * L, rtc && routed);
         if (pass == 0 && scratch_alloc(&scratch, cv.used, s) != cudaSuccess) {
             cudaGetLastError();
             return MC_ERR_ALLOC;
@@ -298,22 +318,53 @@ int backward_delta(const void *q, const void *k, const void *v, const void *u, c
         b.states = a.states; b.kbar = kbar; b.r_on = r_on; b.O_on = a.O_on;
         b.G = G; b.dkbar = dkbar; b.tok = tok;
         b.BH = p.BH; b.L = L; b.C = p.C; b.N = p.N; b.mode = p.mode; b.topk = p.topk;
-        if (e == cudaSuccess) e = launch_bwd_router_simt(p, b, s);
+        t.gon = tok + 2;
+        t.gw_stride = kBwdTokWords;
+        const float *pw = tok + 4;
+        if (rtc) {
+            // the tensor-core backward's gate kernels over images of these states: gates, the cached memories' dg and
+            // dq, dg of the online reads, the score gradients, G
+            b.dq_f32 = nullptr;
+            b.gam = gam;
+            b.dg_in = dg; b.dg_in2 = dg + BH * N * L;
+            b.dgon_in = dgon;
+            b.kpre_tiles = sums;
+            TcImages img{};
+            img.states_img = states_img; img.kbar_img = kbar_img; img.r_on = r_on;
+            if (e == cudaSuccess) e = launch_state_images(p, a.states, states_img, s);
+            if (e == cudaSuccess && routed) e = launch_kbar_images(p, kbar, kbar_img, s);
+            profile_after_kernel(s, "images");
+            if (e == cudaSuccess && routed) {
+                e = launch_bwd_gates_tc(p, u, img, gam, tok, s);
+                profile_after_kernel(s, "gate_tiles_tc");
+            }
+            if (e == cudaSuccess) e = launch_bwd_cached_only_tc(p, q, dy, states_img, gam, dq_add, dg, s);
+            profile_after_kernel(s, "bwd_cached_tc");
+            if (e == cudaSuccess) e = launch_delta_dgon(p, dy, a.O_on, dgon, s);
+            profile_after_kernel(s, "delta_dgon");
+            if (e == cudaSuccess) e = launch_bwd_route(p, b, s);
+            if (e == cudaSuccess) e = launch_bwd_G_tc(p, dy, q, gam, G_img, s);
+            profile_after_kernel(s, "bwd_G_tc");
+            t.gon = b.kv_gw;
+            pw = b.kv_gw + BH * L;
+            t.gw_stride = 1;
+            t.G_img = G_img;
+        } else {
+            if (e == cudaSuccess) e = launch_bwd_router_simt(p, b, s);
+            t.G = G;
+        }
         if (e == cudaSuccess && routed) {
-            a.tok = tok;
-            e = launch_pool_grad_simt(p, a, sums, dkbar, s);
+            a.gw_stride = t.gw_stride;
+            e = launch_pool_grad_simt(p, a, pw, sums, dkbar, s);
             profile_after_kernel(s, "pool_grad_simt");
             a.rho = sums;
+            t.rho = sums;
+            t.pw = pw;
         }
         a.tok = tok;
         a.G = G;
         a.dq_add = dq_add;
-        t.gon = tok + 2;
-        t.gw_stride = kBwdTokWords;
-        t.G = G;
         t.dq_add = dq_add;
-        t.rho = a.rho;
-        t.pw = routed ? tok + 4 : nullptr;
     }
     if (tc) {
         if (e == cudaSuccess) e = launch_delta_grads_tc(p, t, s);

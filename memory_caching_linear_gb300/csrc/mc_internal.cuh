@@ -43,6 +43,8 @@ struct FwdArgs {
     float *kbar;                // [BH][N][d]   scratch
     int32_t *sel_out;           // [BH][L][topk] (ssc_select only)
     const float *alpha, *beta, *lam;  // SWLA per-token scalars [BH][L]; all null = plain update
+    bool have_images;           // tensor-core forward: the images and r_on are in the scratch already (v holds what the
+                                // memory wrote), the state kernel is skipped
     const int32_t *seg_off;     // optional [N+1] segment boundaries (device); then C is the longest segment
     float *kpre_tiles;          // backward state kernel only: keys before each 64-token tile [BH][N][C/64][d]
     // Optional split of long segments for the FFMA scan (null: one CTA walks a whole segment).
@@ -151,6 +153,18 @@ cudaError_t launch_state_tc_segments(const Problem &p, const FwdArgs &a, const T
 cudaError_t launch_readout_tc_segments(const Problem &p, const FwdArgs &a, const TcSegTables &tb, void *scratch,
                                        cudaStream_t s);
 size_t tc_scratch_bytes(const Problem &p);
+// Where the forward's readout expects its operands within the scratch (FwdArgs::have_images): the images of the
+// cached states [BH][N] and, decayed by each 128-token chunk's first token, of the states before the chunks
+// [BH][N][C/128] (d x d bf16, 64-column 128-byte-swizzled panels), the key-mean images, and r_on [BH][L].
+struct TcForwardImages {
+    uint8_t *states_img, *spre_img, *kbar_img;
+    float *r_on;
+};
+TcForwardImages tc_forward_images(const Problem &p, void *scratch);
+// Key-mean images of a head's N segments from fp32 means [BH][N][d] (rows past N and columns past d zero).
+cudaError_t launch_kbar_images(const Problem &p, const float *kbar, uint8_t *kbar_img, cudaStream_t s);
+// 128-wide images of the fp32 states (rows and columns past d zero), as the backward's kernels read them.
+cudaError_t launch_state_images(const Problem &p, const float *states, uint8_t *img, cudaStream_t s);
 cudaError_t launch_forward_tc(const Problem &p, const FwdArgs &a, void *scratch, cudaStream_t s);
 // The d = 64 instantiations of the forward and segment launchers (k_tc64.cu).
 cudaError_t launch_forward_tc64(const Problem &p, const FwdArgs &a, void *scratch, cudaStream_t s);
@@ -247,6 +261,11 @@ size_t bwd_cached_scratch_bytes(const Problem &p);
 cudaError_t launch_bwd_cached_tc(const Problem &p, const void *q, const void *k, const void *v, const void *dy,
                                  const TcImages &img, const float *gam, const float *tok, void *dq, void *scratch,
                                  float **dg_out, float **dgon_out, cudaStream_t s);
+// The cached memories' part alone: dg (two partial sums, as above) and dq in fp32 [BH][L][d].
+cudaError_t launch_bwd_cached_only_tc(const Problem &p, const void *q, const void *dy, const uint8_t *states_img,
+                                      const float *gam, float *dq, float *dg, cudaStream_t s);
+// The gate work of the tensor-core backward (delta, dr, du, the online gates and pooled-key weights kv_gw, dkbar).
+cudaError_t launch_bwd_route(const Problem &p, const BwdArgs &a, cudaStream_t s);
 cudaError_t take_bwd_abort(int *was_set);
 // The key-mean gradients on the tensor cores: dkbar [BH][N][d] += sum_t dr_{t,i} u_t from the
 // route kernel's hi / lo planes of dr.
@@ -275,6 +294,7 @@ struct DeltaArgs {
     const float *tok;                // [BH][L][kBwdTokWords] online gate (word 2), pooled-key weight (4), or null (1, 0)
     const float *dq_add;             // [BH][L][d] added to dq, or null
     const float *rho;                // [BH][N][NCH][d] later tokens' pooled-key gradient after every chunk, or null
+    int gw_stride;                   // floats from token to token of the pooled-key weights (launch_pool_grad_simt)
     int BH, L, C, N, NCH;            // NCH = ceil(C / 64)
 };
 cudaError_t launch_delta_scan_simt(const Problem &p, const DeltaArgs &a, cudaStream_t s);
@@ -282,8 +302,8 @@ cudaError_t launch_delta_rscan_simt(const Problem &p, const DeltaArgs &a, cudaSt
 cudaError_t launch_delta_grads_simt(const Problem &p, const DeltaArgs &a, cudaStream_t s);
 // Key sums before every 64-token chunk (sums [BH][N][NCH][d]), key means, online scores (r_on null: not formed).
 cudaError_t launch_pool_simt(const Problem &p, const DeltaArgs &a, float *sums, float *kbar, float *r_on, cudaStream_t s);
-// rho from tok's pooled-key weights, u and the key means' gradient.
-cudaError_t launch_pool_grad_simt(const Problem &p, const DeltaArgs &a, float *rho, const float *dkbar, cudaStream_t s);
+// rho from the pooled-key weights pw (token t at [t * gw_stride]), u and the key means' gradient.
+cudaError_t launch_pool_grad_simt(const Problem &p, const DeltaArgs &a, const float *pw, float *rho, const float *dkbar, cudaStream_t s);
 // The same on the tensor cores (k_delta_tc.cu): bf16, d = 64 or 128, any segment length.
 constexpr int kDeltaRecBytes = 16384;  // a chunk's record between its two kernels
 struct DeltaTcArgs {
@@ -295,18 +315,21 @@ struct DeltaTcArgs {
     __nv_bfloat16 *U;      // [BH][L][d] beta_t e_t, or null
     __nv_bfloat16 *E;      // [BH][L][d] e_t, or null
     __nv_bfloat16 *S_c;    // [BH][N][NCH][d][d] memory before every chunk, or null
+    uint8_t *spre_img, *states_img;  // the readout's images (tc_forward_images), or null
     // gradients
     const __nv_bfloat16 *dy, *u;
     uint8_t *rrec;         // [BH][N][NCH] x kDeltaRRecBytes scratch: the reverse walk's record, or null
     const float *gon, *pw; // online gate and pooled-key weight of token t at [t * gw_stride], or null (1; no pooled keys)
     int gw_stride;
     const float *G;        // [BH][N][d][d] adjoint of the cached states, or null
+    const uint8_t *G_img;  // the same as bf16 operand images (launch_bwd_G_tc), or null
     const float *dq_add;   // [BH][L][d] added to dq, or null
     const float *rho;      // [BH][N][NCH][d], with pw
     __nv_bfloat16 *R_c;    // [BH][N][NCH][d][d] adjoint after every chunk
     __nv_bfloat16 *dq, *dk, *dv, *dla, *dbe;
     int BH, L, C, N, NCH;
 };
+cudaError_t launch_delta_dgon(const Problem &p, const void *dy, const float *O_on, float *dgon, cudaStream_t s);
 constexpr int kDeltaRRecBytes = 11264;
 // After the walk with rrec, E and S_c: dv and R_c, then the other gradients.
 cudaError_t launch_delta_grads_tc(const Problem &p, const DeltaTcArgs &a, cudaStream_t s);

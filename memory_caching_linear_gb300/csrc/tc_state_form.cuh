@@ -1383,7 +1383,7 @@ cudaError_t forward_impl(const Problem &p, const FwdArgs &fa, void *scratch, cud
     a.alpha = fa.alpha;
     a.beta = fa.beta;
     a.lam = fa.lam;
-    {
+    if (!fa.have_images) {
         auto k1 = gated ? (decay ? seg_state_tc<true, true, false, D> : seg_state_tc<true, false, false, D>)
                         : (decay ? seg_state_tc<false, true, false, D> : seg_state_tc<false, false, false, D>);
         const size_t smem1 = decay ? t1_smem_bytes<true, D>() : t1_smem_bytes<false, D>();

@@ -42,7 +42,7 @@ SHAPES = [  # (d, C, L, dtype): whole, ragged and one-token segments, lengths ne
     (16, 16, 50, "f32"), (32, 37, 130, "f32"), (64, 64, 192, "f32"), (128, 100, 230, "f32"),
     (16, 20, 61, "bf16"), (32, 64, 129, "bf16"),
     (64, 64, 192, "bf16"), (64, 65, 200, "bf16"), (64, 128, 512, "bf16"), (64, 1, 5, "bf16"),
-    (128, 128, 384, "bf16"), (128, 63, 190, "bf16"), (128, 130, 300, "bf16"),
+    (128, 128, 384, "bf16"), (128, 63, 190, "bf16"), (128, 130, 300, "bf16"), (128, 256, 512, "bf16"), (64, 256, 768, "bf16"),
 ]
 UNCUT = [(16, 1, "f32"), (64, 63, "bf16"), (64, 300, "bf16"), (128, 1, "bf16"), (128, 64, "bf16"), (128, 257, "bf16"), (128, 200, "f32"), (64, 129, "f32")]
 
@@ -77,15 +77,15 @@ def test_lengths_past_many_chunks():
     assert rel(gy, y) <= TOL["bf16"] and rel(gst, st) <= STATE_TOL
 
 
-@pytest.mark.parametrize("dtype,d", [("f32", 32), ("bf16", 64), ("bf16", 128)])
-def test_the_ends_of_the_gates(dtype, d):
+@pytest.mark.parametrize("dtype,d,L,C", [("f32", 32, 150, 70), ("bf16", 64, 150, 70), ("bf16", 128, 150, 70), ("bf16", 64, 256, 128),
+                                         ("bf16", 128, 256, 128)])
+def test_the_ends_of_the_gates(dtype, d, L, C):
     """No decay, a full reset, no write, and writes past the value (beta = 2), next to one another."""
-    L, C = 150, 70
     q, k, v, u, la, be = make_delta_inputs(1, 2, L, d, C, 9, dtype)
     la[:, :, ::3] = 0.0
     la[:, :, 10::17] = -80.0
     la[:, :, 75] = -float("inf")
-    la[:, :, 70] = -float("inf")  # a segment's first token
+    la[:, :, C] = -float("inf")  # a segment's first token
     be[:, :, ::5] = 0.0
     be[:, :, 3::7] = 2.0
     x = [q, k, v, u, la, be]
