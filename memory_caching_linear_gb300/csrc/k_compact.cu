@@ -7,14 +7,15 @@
 // Kept are the `protect` newest complete segments and, of the others, those with the most mass
 // (equal mass: the newer), in order of time; the last, incomplete segment becomes the online memory.
 //
-// Kernels: the pooled-key sums (k_delta_simt.cu), gate_mass (per 64-token tile, the gates and their
-// sums over the tile's tokens), compact_select (per head: the tiles' sums in a fixed order, the
+// Kernels: the pooled-key sums (k_delta_simt.cu), gate_mass (per tile of 64 or 128 tokens, the gates and their
+// sums over the tile's tokens), mass_reduce (the tiles' sums in a fixed order), compact_select (per head, the
 // ranking), compact_gather (copies, bound by HBM).  Partial sums instead of atomics keep the mass,
 // and with it the choice, the same from run to run.
 #include <cfloat>
 #include <cstdint>
 
 #include "mc_internal.cuh"
+#include "mma_sync.cuh"
 
 namespace mc {
 namespace {
@@ -115,7 +116,185 @@ __global__ void __launch_bounds__(kMThreads) gate_mass_simt(CompactArgs a)
     for (int i = ((smax + kMS - 1) / kMS) * kMS + tid; i < a.N; i += kMThreads) out[i] = 0.f;
 }
 
-// One CTA per head: mass_i = the tiles' sums in order, then which complete segments are kept.
+// ---------------------------------------------------------------------------
+// gate_mass_tc: the same for bf16 inputs and the softmax gates.  A CTA takes 128 tokens, a warp 16; the scores
+// against 64 segments at a time are warp-level products of u with the key means as three bf16 terms
+// (launch_kbar_images: every product is exact, only the fp32 sum rounds).  Up to 128 segments the scores stay in
+// registers between the softmax's sums and the gates; beyond, they are formed a second time.
+// ---------------------------------------------------------------------------
+constexpr int kTM = 128;
+
+template <int D>
+__global__ void __launch_bounds__(256, 2) gate_mass_tc(CompactArgs a)
+{
+    using namespace mma;
+    constexpr int KS = D / 16, PN = D > 64 ? 2 : 1, UR = D * 2 < 128 ? 128 : D * 2;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    uint8_t *Ut = smem_raw, *Kt = smem_raw + kTM * UR;  // 3 terms x PN panels of 64 rows x 128 bytes
+    __shared__ float cols[8][64];
+    const int tile = a.tiles - 1 - (int)(blockIdx.x / a.BH), bh = (int)(blockIdx.x % a.BH);  // the longest first
+    const int tb = tile * kTM, cnt = min(kTM, a.L - tb);
+    const int smax = (tb + cnt - 1) / a.C, nblk = (smax + 63) / 64;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, c = lane % 4;
+    const size_t row0 = (size_t)bh * a.L + tb;
+    const __nv_bfloat16 *u = static_cast<const __nv_bfloat16 *>(a.u);
+    float *out = a.part + ((size_t)bh * a.tiles + tile) * a.N;
+    for (int e = tid; e < kTM * (D / 8); e += 256) {
+        const int r = e / (D / 8), pc = e % (D / 8);
+        cp16(smem_addr(Ut) + tile_off<UR>(r, pc), u + (row0 + (r < cnt ? r : 0)) * D + pc * 8, r < cnt);
+    }
+    cp_commit();
+    // rows g and g + 8 of the warp's tokens: cached segments, online score
+    const int t0 = 16 * warp + g, t1 = t0 + 8;
+    const int lim0 = t0 < cnt ? (tb + t0) / a.C : 0, lim1 = t1 < cnt ? (tb + t1) / a.C : 0;
+    float m0 = t0 < cnt ? a.r_on[row0 + t0] : 0.f, m1 = t1 < cnt ? a.r_on[row0 + t1] : 0.f, z0 = c == 0 ? 1.f : 0.f, z1 = z0;
+    uint32_t au[KS][4];
+
+    auto scores = [&](int b, float (&S)[8][4]) {  // block b: fills S, -inf where a token does not read the segment
+        __syncthreads();  // the last block has been read
+        const uint8_t *img = a.kbar_img + ((size_t)bh * ((a.N + 63) / 64) + b) * 49152;
+        for (int e = tid; e < 3 * PN * 512; e += 256) {
+            const int term = e / (PN * 512), r = e % (PN * 512);
+            cp16(smem_addr(Kt) + e * 16, img + term * 16384 + r * 16, true);
+        }
+        cp_commit();
+        cp_wait<0>();
+        __syncthreads();
+        if (b == 0) {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+                ldsm4(au[ks], smem_addr(Ut) + tile_off<UR>(16 * warp + (lane & 15), 2 * ks + (lane >> 4)));
+        }
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[n][e] = 0.f;
+        const int br = (lane >> 4) * 8 + (lane & 7), bc = (lane >> 3) & 1;
+#pragma unroll
+        for (int term = 2; term >= 0; --term)  // the small terms first
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int n2 = 0; n2 < 4; ++n2) {
+                    uint32_t bf[4];
+                    ldsm4(bf, smem_addr(Kt) + (term * PN + ks / 4) * 8192 + tile_off<128>(16 * n2 + br, 2 * (ks & 3) + bc));
+                    mma16816(S[2 * n2], au[ks], bf[0], bf[1]);
+                    mma16816(S[2 * n2 + 1], au[ks], bf[2], bf[3]);
+                }
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (64 * b + 8 * n + 2 * c + (e & 1) >= (e >> 1 ? lim1 : lim0)) S[n][e] = -INFINITY;
+    };
+    auto softmax = [&](const float (&S)[8][4]) {  // running maximum and sum (each lane its own columns)
+        float x0 = m0, x1 = m1;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            x0 = fmaxf(x0, fmaxf(S[n][0], S[n][1]));
+            x1 = fmaxf(x1, fmaxf(S[n][2], S[n][3]));
+        }
+        z0 *= expf(m0 - x0);
+        z1 *= expf(m1 - x1);
+        m0 = x0;
+        m1 = x1;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            z0 += expf(S[n][0] - m0) + expf(S[n][1] - m0);
+            z1 += expf(S[n][2] - m1) + expf(S[n][3] - m1);
+        }
+    };
+    auto join = [&]() {  // the four lanes of a row
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            const float y0 = __shfl_xor_sync(0xffffffffu, m0, o), y1 = __shfl_xor_sync(0xffffffffu, m1, o);
+            const float w0 = __shfl_xor_sync(0xffffffffu, z0, o), w1 = __shfl_xor_sync(0xffffffffu, z1, o);
+            const float x0 = fmaxf(m0, y0), x1 = fmaxf(m1, y1);
+            z0 = z0 * expf(m0 - x0) + w0 * expf(y0 - x0);
+            z1 = z1 * expf(m1 - x1) + w1 * expf(y1 - x1);
+            m0 = x0;
+            m1 = x1;
+        }
+        z0 = 1.f / z0;
+        z1 = 1.f / z1;
+    };
+    auto gates = [&](int b, const float (&S)[8][4]) {  // sums over the tile's tokens
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            float s0 = expf(S[n][0] - m0) * z0 + expf(S[n][2] - m1) * z1;
+            float s1 = expf(S[n][1] - m0) * z0 + expf(S[n][3] - m1) * z1;
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+                s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+                s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+            }
+            if (g == 0) {
+                cols[warp][8 * n + 2 * c] = s0;
+                cols[warp][8 * n + 2 * c + 1] = s1;
+            }
+        }
+        __syncthreads();
+        if (tid < 64 && 64 * b + tid < a.N) {
+            float s = 0.f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) s += cols[w][tid];
+            out[64 * b + tid] = s;
+        }
+        __syncthreads();
+    };
+    float S0[8][4];
+    if (nblk <= 2) {
+        float S1[8][4];
+        if (nblk > 0) {
+            scores(0, S0);
+            softmax(S0);
+        }
+        if (nblk > 1) {
+            scores(1, S1);
+            softmax(S1);
+        }
+        join();
+        if (nblk > 0) gates(0, S0);
+        if (nblk > 1) gates(1, S1);
+    } else {
+        for (int b = 0; b < nblk; ++b) {
+            scores(b, S0);
+            softmax(S0);
+        }
+        join();
+        for (int b = 0; b < nblk; ++b) {
+            scores(b, S0);
+            gates(b, S0);
+        }
+    }
+    for (int i = nblk * 64 + tid; i < a.N; i += 256) out[i] = 0.f;
+    cp_wait<0>();
+}
+
+// mass_i: the tiles' sums, 32 strided shares of the tiles, joined in a fixed order.
+__global__ void __launch_bounds__(1024) mass_reduce(CompactArgs a)
+{
+    __shared__ float part[32][33];
+    const int blocks = (a.N + 31) / 32, bh = (int)blockIdx.x / blocks, lane = threadIdx.x % 32, w = threadIdx.x / 32;
+    const int i = ((int)blockIdx.x % blocks) * 32 + lane;
+    float s = 0.f;
+    if (i < a.N) {
+        const float *p = a.part + (size_t)bh * a.tiles * a.N + i;
+        int t = (int)((long long)(i + 1) * a.C / a.tile_len);  // no token before the segment's end reads it
+        t += (w - t % 32 + 32) % 32;
+#pragma unroll 4
+        for (; t < a.tiles; t += 32) s += p[(size_t)t * a.N];
+    }
+    part[w][lane] = s;
+    __syncthreads();
+    if (w == 0 && i < a.N) {
+#pragma unroll
+        for (int x = 1; x < 32; ++x) s += part[x][lane];
+        a.mass_all[(size_t)bh * a.N + i] = s;
+    }
+}
+
+// One CTA per head: which complete segments are kept.
 // order[bh][slot] is the segment of each slot, -1 for an empty one.
 __global__ void __launch_bounds__(kMThreads) compact_select(CompactArgs a)
 {
@@ -124,17 +303,7 @@ __global__ void __launch_bounds__(kMThreads) compact_select(CompactArgs a)
     __shared__ int total;
     const int bh = (int)blockIdx.x, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     for (int i = tid; i < a.N; i += kMThreads) {
-        // four chains of tiles, joined in a fixed order
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-        const float *p = a.part + (size_t)bh * a.tiles * a.N + i;
-        int t = (int)((long long)(i + 1) * a.C / kMT);  // no token before the segment's end reads it
-        for (; t + 4 <= a.tiles; t += 4)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) s[x] += p[(size_t)(t + x) * a.N];
-        for (; t < a.tiles; ++t) s[0] += p[(size_t)t * a.N];
-        const float m = (s[0] + s[1]) + (s[2] + s[3]);
-        ms[i] = m;
-        if (a.mass_all) a.mass_all[(size_t)bh * a.N + i] = m;
+        ms[i] = a.mass_all[(size_t)bh * a.N + i];
     }
     __syncthreads();
     const int done = a.done, nkeep = min(a.nmax, done), loose = done - a.protect;  // segments below `loose` compete
@@ -205,10 +374,32 @@ cudaError_t mass_impl(const Problem &p, const CompactArgs &a, cudaStream_t s)
     return cudaGetLastError();
 }
 
+template <int D>
+cudaError_t mass_tc_impl(const Problem &p, const CompactArgs &a, cudaStream_t s)
+{
+    const size_t smem = kTM * (D * 2 < 128 ? 128 : D * 2) + 3 * (D > 64 ? 2 : 1) * 8192;
+    auto kern = gate_mass_tc<D>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)((long long)p.BH * a.tiles), 256, smem, s>>>(a);
+    return cudaGetLastError();
+}
+
 }  // namespace
+
+int gate_mass_tile(const Problem &p) { return p.bf16 && p.mode == MC_GRM ? kTM : kMT; }
 
 cudaError_t launch_gate_mass(const Problem &p, const CompactArgs &a, cudaStream_t s)
 {
+    if (p.bf16 && p.mode == MC_GRM) {
+        switch (p.d) {
+        case 16: return mass_tc_impl<16>(p, a, s);
+        case 32: return mass_tc_impl<32>(p, a, s);
+        case 64: return mass_tc_impl<64>(p, a, s);
+        case 128: return mass_tc_impl<128>(p, a, s);
+        default: return cudaErrorInvalidValue;
+        }
+    }
     switch (p.d) {
     case 16: return p.bf16 ? mass_impl<__nv_bfloat16, 16>(p, a, s) : mass_impl<float, 16>(p, a, s);
     case 32: return p.bf16 ? mass_impl<__nv_bfloat16, 32>(p, a, s) : mass_impl<float, 32>(p, a, s);
@@ -223,6 +414,8 @@ cudaError_t launch_compact(const Problem &p, const CompactArgs &a, cudaStream_t 
     const size_t smem = 2 * sizeof(float) * a.N;
     cudaError_t e = cudaFuncSetAttribute(compact_select, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
+    mass_reduce<<<(unsigned)((long long)p.BH * ((a.N + 31) / 32)), 1024, 0, s>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     compact_select<<<(unsigned)p.BH, kMThreads, smem, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     compact_gather<<<(unsigned)((long long)p.BH * (a.nmax + 1)), kMThreads, 0, s>>>(a);

@@ -563,6 +563,77 @@ __global__ void __launch_bounds__(256) pool_score(DeltaArgs a, const float *kpre
     }
 }
 
+// The three passes in one, for many segments: one CTA per (bh, segment) goes through the chunks with the running key
+// sum in shared memory, the next chunk's rows on their way in registers, so k and u come from HBM once.
+template <typename T, int D, bool SCORE>
+__global__ void __launch_bounds__(256) pool_walk(DeltaArgs a, float *kpre, float *kbar, float *r_on)
+{
+    using P = PoolTile<T, D>;
+    __shared__ float part[2][P::TL * (D + 1)];
+    __shared__ float run[2][D];
+    const int seg = (int)blockIdx.x % a.N, bh = (int)blockIdx.x / a.N;
+    const int t0 = seg * a.C, len = min((seg + 1) * a.C, a.L) - t0, nch = (len + kCH - 1) / kCH;
+    const int tid = threadIdx.x, pc = tid % P::PC, tl = tid / P::PC;
+    const size_t row0 = (size_t)bh * a.L + t0;
+    const T *k = static_cast<const T *>(a.k), *u = static_cast<const T *>(a.u);
+    const bool scored = SCORE && seg > 0;  // the first segment's gate is 1 whatever its score
+    uint4 kq[P::TPL], uq[P::TPL];
+    auto load = [&](int ch) {
+#pragma unroll
+        for (int j = 0; j < P::TPL; ++j) {
+            const int t = ch * kCH + tl * P::TPL + j;
+            const bool ok = tid < P::NT && t < len;
+            kq[j] = ok ? *reinterpret_cast<const uint4 *>(k + (row0 + t) * D + pc * P::V) : make_uint4(0u, 0u, 0u, 0u);
+            if (scored) uq[j] = ok ? *reinterpret_cast<const uint4 *>(u + (row0 + t) * D + pc * P::V) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    if (tid < D) run[0][tid] = 0.f;
+    load(0);
+    for (int ch = 0; ch < nch; ++ch) {
+        float *pt = part[ch & 1];
+        float x[P::TPL][P::V], v[P::TPL][P::V];
+#pragma unroll
+        for (int j = 0; j < P::TPL; ++j) {
+            const T *kt = reinterpret_cast<const T *>(&kq[j]), *ut = reinterpret_cast<const T *>(&uq[j]);
+#pragma unroll
+            for (int i = 0; i < P::V; ++i) {
+                x[j][i] = to_f(kt[i]) + (j > 0 ? x[j > 0 ? j - 1 : 0][i] : 0.f);
+                v[j][i] = scored ? to_f(ut[i]) : 0.f;
+            }
+        }
+        if (ch + 1 < nch) load(ch + 1);
+        if (tid < P::NT)
+#pragma unroll
+            for (int i = 0; i < P::V; ++i) pt[tl * (D + 1) + pc * P::V + i] = x[P::TPL - 1][i];
+        __syncthreads();
+        if (tid < D) {
+            float s = run[ch & 1][tid];
+            if (kpre) kpre[((size_t)blockIdx.x * a.NCH + ch) * D + tid] = s;
+#pragma unroll
+            for (int i = 0; i < P::TL; ++i) {
+                const float own = pt[i * (D + 1) + tid];
+                pt[i * (D + 1) + tid] = s;
+                s += own;
+            }
+            run[(ch + 1) & 1][tid] = s;
+            if (ch + 1 == nch) kbar[(size_t)blockIdx.x * D + tid] = s / (float)len;
+        }
+        if (!SCORE) continue;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < P::TPL; ++j) {
+            const int t = ch * kCH + tl * P::TPL + j;
+            float s = 0.f;
+            if (scored && tid < P::NT)
+#pragma unroll
+                for (int i = 0; i < P::V; ++i) s = fmaf(v[j][i], x[j][i] + pt[tl * (D + 1) + pc * P::V + i], s);
+#pragma unroll
+            for (int o = P::PC / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (pc == 0 && tid < P::NT && t < len) r_on[row0 + t] = s / (float)(t + 1);
+        }
+    }
+}
+
 template <typename T, int D>
 cudaError_t scan_impl(const Problem &p, const DeltaArgs &a, cudaStream_t s)
 {
@@ -594,6 +665,11 @@ template <typename T, int D>
 cudaError_t pool_impl(const Problem &p, const DeltaArgs &a, float *sums, float *kbar, float *r_on, cudaStream_t s)
 {
     const unsigned chunks = (unsigned)((long long)p.BH * p.N * a.NCH);
+    if ((long long)p.BH * p.N >= 304) {  // two segments per SM: one pass
+        if (r_on) pool_walk<T, D, true><<<(unsigned)(p.BH * p.N), 256, 0, s>>>(a, sums, kbar, r_on);
+        else pool_walk<T, D, false><<<(unsigned)(p.BH * p.N), 256, 0, s>>>(a, sums, kbar, nullptr);
+        return cudaGetLastError();
+    }
     pool_sums<T, D><<<chunks, 256, 0, s>>>(a, static_cast<const T *>(a.k), nullptr, sums);
     pool_scan<D><<<(unsigned)((long long)p.BH * p.N), D, 0, s>>>(a, sums, kbar, nullptr);
     if (r_on) pool_score<T, D><<<chunks, 256, 0, s>>>(a, sums, r_on);

@@ -416,8 +416,9 @@ int cache_compact(const void *k, const void *u, const float *states_all, int B, 
     if ((st = check_call(c, B, H, L, d, seg_len, agg_mode, topk, bf16)) != MC_OK) return st;
     if (!c.uses_u) return MC_ERR_MODE;  // constant gates tell no segment from another
     Problem &p = c.p;
-    const long long tiles = ((long long)L + 63) / 64;
-    if (p.N > 16384 || (long long)p.BH * tiles >= (1ll << 31) || (long long)p.BH * (n_max + 1) >= (1ll << 31))
+    const int tile_len = gate_mass_tile(p);
+    const long long tiles = ((long long)L + tile_len - 1) / tile_len;
+    if (p.N > 16384 || (long long)p.BH * ((p.N + 63) / 64) * 64 >= (1ll << 31) || (long long)p.BH * tiles >= (1ll << 31) || (long long)p.BH * (n_max + 1) >= (1ll << 31))
         return MC_ERR_SHAPE;
     if (any_null({k, u, states_all, states, kbar, mass, slot_seg, online, ksum})) return MC_ERR_NULL;
     if (any_misaligned({k, u, states_all, states, kbar, mass, slot_seg, online, ksum, mass_all})) return MC_ERR_ALIGN;
@@ -429,12 +430,17 @@ int cache_compact(const void *k, const void *u, const float *states_all, int B, 
     m.u = u; m.states_all = states_all; m.mass_all = mass_all;
     m.states = states; m.kbar = kbar; m.mass = mass; m.online = online; m.ksum = ksum; m.slot_seg = slot_seg;
     m.BH = p.BH; m.L = L; m.C = p.C; m.N = p.N; m.d = d; m.mode = p.mode; m.topk = p.topk; m.tiles = (int)tiles;
+    m.tile_len = tile_len;
+    const bool tc = tile_len == 128;
     m.done = L / seg_len; m.nmax = n_max;
     m.protect = protect < m.done ? protect : m.done;
     float *sums = nullptr, *kbar_all = nullptr, *r_on = nullptr;
+    uint8_t *kbar_img = nullptr;
     void *scratch = nullptr;
     for (int pass = 0; pass < 2; ++pass) {
         Carver cv{static_cast<char *>(scratch), 0};
+        if (!mass_all) m.mass_all = cv.take<float>(BH * N);
+        kbar_img = cv.take<uint8_t>(BH * ((N + 63) / 64) * 49152, tc);
         kbar_all = cv.take<float>(BH * N * d);
         r_on = cv.take<float>(BH * L);
         sums = cv.take<float>(BH * N * c.NCH * d);
@@ -450,6 +456,8 @@ int cache_compact(const void *k, const void *u, const float *states_all, int B, 
     profile_call_start(s);
     cudaError_t e = launch_pool_simt(p, a, sums, kbar_all, r_on, s);
     profile_after_kernel(s, "pool_simt");
+    if (e == cudaSuccess && tc) e = launch_kbar_images(p, kbar_all, kbar_img, s);
+    m.kbar_img = kbar_img;
     if (e == cudaSuccess) {
         e = launch_gate_mass(p, m, s);
         profile_after_kernel(s, "gate_mass");

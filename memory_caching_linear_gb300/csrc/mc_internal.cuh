@@ -359,12 +359,14 @@ struct CompactArgs {
     const float *kbar_all, *r_on;      // [BH][N][d], [BH][L]
     const float *states_all;           // [BH][N][d][d]
     float *part;                       // [BH][tiles][N] scratch
-    float *mass_all;                   // [BH][N], or null
+    float *mass_all;                   // [BH][N]
+    const uint8_t *kbar_img;           // key-mean images (tensor-core gates), or null
     int32_t *order;                    // [BH][nmax] scratch
     float *states, *kbar, *mass, *online, *ksum;
     int32_t *slot_seg;
-    int BH, L, C, N, d, mode, topk, tiles, done, nmax, protect;
+    int BH, L, C, N, d, mode, topk, tiles, tile_len, done, nmax, protect;
 };
+int gate_mass_tile(const Problem &p);  // tokens per tile of launch_gate_mass
 cudaError_t launch_gate_mass(const Problem &p, const CompactArgs &a, cudaStream_t s);
 cudaError_t launch_compact(const Problem &p, const CompactArgs &a, cudaStream_t s);
 
