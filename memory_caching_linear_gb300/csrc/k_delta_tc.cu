@@ -29,8 +29,6 @@ namespace {
 using namespace mma;
 
 constexpr int kCH = kDeltaChunk;
-constexpr int kPrepThreads = 128;
-constexpr int kAP = kCH + 1;  // padded row of the 64 x 64 matrices
 
 // Lower-triangular B operands by 16 x 8 tiles: column tile nt (8 tokens) needs row tiles kt <= nt / 2.
 constexpr int kTiles = 20;
@@ -46,12 +44,6 @@ static_assert(kRecT + kRecP + kRecV == kRec, "record");
 // The other way round, rows m >= columns i: column tile nt needs row tiles kt = nt / 2 .. 3.
 __host__ __device__ constexpr int rev_base(int nt) { return 8 * (nt / 2) - nt / 2 * (nt / 2 - 1) + (nt & 1) * (4 - nt / 2); }
 static_assert(rev_base(7) + 1 == kTiles, "tiles of an upper triangle");
-__device__ __forceinline__ void rev_tile(int t, int &nt, int &kt)
-{
-    nt = 0;
-    while (nt < 7 && rev_base(nt + 1) <= t) ++nt;
-    kt = nt / 2 + t - rev_base(nt);
-}
 // The reverse walk's record: T - 1 (one term), P, and exp(c_i), exp(c_end - c_i), beta_i, [192] exp(c_end).
 static_assert(2 * kRecP + kRecV == kDeltaRRecBytes, "record");
 
@@ -71,31 +63,42 @@ __device__ __forceinline__ Where chunk_at(const DeltaTcArgs &a, long long id)
 }
 
 // ---------------------------------------------------------------------------
-// delta_prep_tc: one CTA per chunk.  K K^T (exact bf16 products) on the tensor cores, 16 rows per
-// warp; (1 + A)^-1 in fp32 by 16 x 16 blocks: each warp inverts a diagonal block by substitution (a lane
-// per column), then X_ij = -X_ii sum_k A_ik X_kj, one block diagonal after the other.
+// delta_prep_tc: one warp per chunk, no barrier between warps.  K K^T (and Q K^T) in registers, exact bf16
+// products; then X = (1 + A)^-1 in fp32 by substitution over blocks of 16 rows, a lane holding the columns
+// lane and lane + 32.  A and X share one 64 x 64 array in shared memory: A_ik at [k][i] (above the diagonal), X_ij at
+// [i][j] (on and below it), so that a step reads A's column k as one broadcast row.  P goes from the accumulators
+// to the record without shared memory: a tile of P is the operand of rows j, columns i as it lies, and its 8 x 8
+// transposes are the other one.
 // ---------------------------------------------------------------------------
-template <int D, bool READ, bool REV>
-__global__ void __launch_bounds__(kPrepThreads) delta_prep_tc(DeltaTcArgs a)
+constexpr int kMP = 68;  // row of the 64 x 64 array, in words
+
+template <int D, bool QK>
+__host__ __device__ constexpr int prep_smem()
 {
-    constexpr int ROW = D * 2, PIECES = D / 8;
+    return ((QK ? 2 : 1) * kCH * D * 2 > kCH * kMP * 4 ? (QK ? 2 : 1) * kCH * D * 2 : kCH * kMP * 4) + 2 * kCH * 4;
+}
+
+template <int D, bool READ, bool REV>
+__global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a)
+{
+    constexpr int ROW = D * 2, PIECES = D / 8, KS = D / 16;
     constexpr bool QK = READ || REV;
     extern __shared__ __align__(16) uint8_t sm[];
-    uint8_t *Kt = sm, *Qt = Kt + kCH * ROW;
-    float *A = reinterpret_cast<float *>(Qt + (QK ? kCH * ROW : 0)), *X = A + kCH * kAP, *Y = X + kCH * kAP;
-    __shared__ float cum[kCH], bet[kCH];
+    float *M = reinterpret_cast<float *>(sm);  // over the tiles once these are read
+    float *cum = reinterpret_cast<float *>(sm + prep_smem<D, QK>() - 2 * kCH * 4), *bet = cum + kCH;
     const Where w = chunk_at(a, blockIdx.x);
     if (w.cnt <= 0) return;
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, c = lane % 4;
+    const int lane = threadIdx.x, g = lane / 4, c = lane % 4;
     const size_t row0 = (size_t)w.bh * a.L + w.tb;
-    for (int e = tid; e < kCH * PIECES; e += kPrepThreads) {
+    const uint32_t Kt = smem_addr(sm), Qt = Kt + kCH * ROW;
+    for (int e = lane; e < kCH * PIECES; e += 32) {
         const int r = e / PIECES, pc = e % PIECES;
         const size_t off = (row0 + (r < w.cnt ? r : 0)) * D + pc * 8;
-        cp16(smem_addr(Kt) + tile_off<ROW>(r, pc), a.k + off, r < w.cnt);
-        if (QK) cp16(smem_addr(Qt) + tile_off<ROW>(r, pc), a.q + off, r < w.cnt);
+        cp16(Kt + tile_off<ROW>(r, pc), a.k + off, r < w.cnt);
+        if (QK) cp16(Qt + tile_off<ROW>(r, pc), a.q + off, r < w.cnt);
     }
     cp_commit();
-    if (warp == 0) {  // running sums of the chunk's decays, two tokens per lane
+    {  // running sums of the chunk's decays, two tokens per lane
         const int i = 2 * lane;
         const float x0 = i < w.cnt ? delta_log(__bfloat162float(a.la[row0 + i])) : 0.f;
         const float x1 = i + 1 < w.cnt ? delta_log(__bfloat162float(a.la[row0 + i + 1])) : 0.f;
@@ -111,173 +114,224 @@ __global__ void __launch_bounds__(kPrepThreads) delta_prep_tc(DeltaTcArgs a)
         bet[i + 1] = i + 1 < w.cnt ? __bfloat162float(a.be[row0 + i + 1]) : 0.f;
     }
     cp_wait<0>();
-    __syncthreads();
-    uint8_t *rec = a.rec + (size_t)blockIdx.x * kRec;
+    __syncwarp();
+    uint8_t *rec = a.rec + (size_t)blockIdx.x * kRec, *rrec = REV ? a.rrec + (size_t)blockIdx.x * kDeltaRRecBytes : nullptr;
+    const float ce = cum[kCH - 1];  // tokens past the end add nothing
     {
-        // rows 16 warp .. + 15, columns up to the diagonal
-        float kk[8][4], qk[8][4];
-#pragma unroll
-        for (int n = 0; n < 8; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) kk[n][e] = qk[n][e] = 0.f;
-        const int ar = 16 * warp + (lane & 15), ac = lane >> 4;
-        const int br = (lane >> 4) * 8 + (lane & 7), bc = (lane >> 3) & 1;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-            uint32_t ak[4], aq[4];
-            ldsm4(ak, smem_addr(Kt) + tile_off<ROW>(ar, 2 * ks + ac));
-            if (QK) ldsm4(aq, smem_addr(Qt) + tile_off<ROW>(ar, 2 * ks + ac));
-#pragma unroll
-            for (int n2 = 0; n2 < 4; ++n2) {
-                if (n2 > warp) break;
-                uint32_t b[4];
-                ldsm4(b, smem_addr(Kt) + tile_off<ROW>(16 * n2 + br, 2 * ks + bc));
-                mma16816(kk[2 * n2], ak, b[0], b[1]);
-                mma16816(kk[2 * n2 + 1], ak, b[2], b[3]);
-                if (QK) {
-                    mma16816(qk[2 * n2], aq, b[0], b[1]);
-                    mma16816(qk[2 * n2 + 1], aq, b[2], b[3]);
-                }
-            }
-        }
-#pragma unroll
-        for (int n = 0; n < 8; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = 16 * warp + g + 8 * (e >> 1), j = 8 * n + 2 * c + (e & 1);
-                const float dec = j <= i ? expf(cum[i] - cum[j]) : 0.f;
-                A[i * kAP + j] = j < i ? kk[n][e] * dec * bet[j] : 0.f;
-                if (QK) Y[i * kAP + j] = qk[n][e] * dec;
-                X[i * kAP + j] = 0.f;
-            }
-    }
-    __syncthreads();
-    {  // diagonal blocks: lane j < 16 has column j
-        float *Xd = X + (16 * warp) * kAP + 16 * warp;
-        const float *Ad = A + (16 * warp) * kAP + 16 * warp;
-        if (lane < 16) {
-            float x[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float s0 = i == lane ? 1.f : 0.f, s1 = 0.f;
-#pragma unroll
-                for (int k = 0; k < i; ++k) {
-                    if (k & 1) s1 = fmaf(-Ad[i * kAP + k], x[k], s1);
-                    else s0 = fmaf(-Ad[i * kAP + k], x[k], s0);
-                }
-                x[i] = s0 + s1;
-                Xd[i * kAP + lane] = x[i];
-            }
-        }
-    }
-    __syncthreads();
-    if (REV) {  // the same P as an operand of rows i, columns j
-        uint2 *pt = reinterpret_cast<uint2 *>(a.rrec + (size_t)blockIdx.x * kDeltaRRecBytes + kRecP);
-        for (int e = tid; e < kTiles * 32; e += kPrepThreads) {
-            int nt, kt;
-            rev_tile(e / 32, nt, kt);
-            const int l = e % 32;
-            const float *y = Y + (16 * kt + 2 * (l % 4)) * kAP + 8 * nt + l / 4;
-            pt[e] = make_uint2(pack2(y[0], y[kAP]), pack2(y[8 * kAP], y[9 * kAP]));
-        }
-        if (!READ) __syncthreads();
-    }
-    if (READ) {  // P tiles (nothing below touches Y until the next barrier)
-        uint2 *pt = reinterpret_cast<uint2 *>(rec + kRecT);
-        for (int e = tid; e < kTiles * 32; e += kPrepThreads) {
-            const int t = e / 32, l = e % 32;
-            int nt = 0;
-            while (nt < 7 && tile_base(nt + 1) <= t) ++nt;
-            const float *y = Y + (8 * nt + l / 4) * kAP + 16 * (t - tile_base(nt)) + 2 * (l % 4);
-            pt[e] = make_uint2(pack2(y[0], y[1]), pack2(y[8], y[9]));
-        }
-        __syncthreads();
-    }
-    for (int diag = 1; diag < 4; ++diag) {
-        // blocks (i, j) with i - j = diag: Y_ij = sum_{j <= k < i} A_ik X_kj, then X_ij = -X_ii Y_ij
-        const int nb = 4 - diag;
-        for (int e = tid; e < nb * 64; e += kPrepThreads) {  // four entries of a row each
-            const int b = e / 64, r = (e % 64) / 4, cc = (e % 4) * 4, i = b + diag;
-            float s[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int k = 16 * b; k < 16 * i; ++k) {
-                const float av = A[(16 * i + r) * kAP + k];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) s[x] = fmaf(av, X[k * kAP + 16 * b + cc + x], s[x]);
-            }
-#pragma unroll
-            for (int x = 0; x < 4; ++x) Y[(16 * i + r) * kAP + 16 * b + cc + x] = s[x];
-        }
-        __syncthreads();
-        for (int e = tid; e < nb * 64; e += kPrepThreads) {
-            const int b = e / 64, r = (e % 64) / 4, cc = (e % 4) * 4, i = b + diag;
-            float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const float xv = X[(16 * i + r) * kAP + 16 * i + k];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) s[x] = fmaf(-xv, Y[(16 * i + k) * kAP + 16 * b + cc + x], s[x]);
-            }
-#pragma unroll
-            for (int x = 0; x < 4; ++x) X[(16 * i + r) * kAP + 16 * b + cc + x] = s[x];
-        }
-        __syncthreads();
-    }
-    uint4 *tt = reinterpret_cast<uint4 *>(rec);
-    for (int e = tid; e < kTiles * 32; e += kPrepThreads) {
-        const int t = e / 32, l = e % 32;
-        int nt = 0;
-        while (nt < 7 && tile_base(nt + 1) <= t) ++nt;
-        const int i = 8 * nt + l / 4, j = 16 * (t - tile_base(nt)) + 2 * (l % 4);
-        const float *x = X + i * kAP + j;
-        uint4 o;
-        split2(j < i ? x[0] : 0.f, j + 1 < i ? x[1] : 0.f, o.x, o.z);
-        split2(j + 8 < i ? x[8] : 0.f, j + 9 < i ? x[9] : 0.f, o.y, o.w);
-        tt[e] = o;
-    }
-    if (REV) {
-        uint8_t *rrec = a.rrec + (size_t)blockIdx.x * kDeltaRRecBytes;
-        uint2 *lt = reinterpret_cast<uint2 *>(rrec);
-        for (int e = tid; e < kTiles * 32; e += kPrepThreads) {
-            int nt, kt;
-            rev_tile(e / 32, nt, kt);
-            const int l = e % 32, i = 8 * nt + l / 4, m = 16 * kt + 2 * (l % 4);  // T_mi, m > i
-            const float *x = X + m * kAP + i;
-            lt[e] = make_uint2(pack2(m > i ? x[0] : 0.f, m + 1 > i ? x[kAP] : 0.f),
-                               pack2(m + 8 > i ? x[8 * kAP] : 0.f, m + 9 > i ? x[9 * kAP] : 0.f));
-        }
-        if (tid < kCH) {
-            float *vec = reinterpret_cast<float *>(rrec + 2 * kRecP);
-            const float ce = cum[kCH - 1];
-            vec[tid] = expf(cum[tid]);
-            vec[64 + tid] = expf(ce - cum[tid]);
-            vec[128 + tid] = bet[tid];
-            if (tid == 0) vec[192] = expf(ce);
-        }
-    }
-    if (tid < kCH) {
         float *vec = reinterpret_cast<float *>(rec + kRecT + kRecP);
-        const float ce = cum[kCH - 1];  // tokens past the end add nothing
-        vec[tid] = expf(cum[tid]);
-        vec[64 + tid] = bet[tid] * expf(ce - cum[tid]);
-        vec[128 + tid] = bet[tid];
-        if (tid == 0) vec[192] = expf(ce);
+        float *rvec = reinterpret_cast<float *>(rrec + 2 * kRecP);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int i = lane + 32 * x;
+            const float ea = __expf(cum[i]), eb = __expf(ce - cum[i]);
+            vec[i] = ea;
+            vec[64 + i] = bet[i] * eb;
+            vec[128 + i] = bet[i];
+            if (REV) {
+                rvec[i] = ea;
+                rvec[64 + i] = eb;
+                rvec[128 + i] = bet[i];
+            }
+        }
+        if (lane == 0) {
+            vec[192] = __expf(ce);
+            if (REV) rvec[192] = __expf(ce);
+        }
+    }
+    const int ar = lane & 15, ac = lane >> 4, br = (lane >> 4) * 8 + (lane & 7), bc = (lane >> 3) & 1;
+    float kk[10][2][4];  // 16 x 16 blocks (b, n2 <= b) of K K^T
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        float qk[4][2][4];
+#pragma unroll
+        for (int n2 = 0; n2 <= b; ++n2)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) kk[b * (b + 1) / 2 + n2][h][e] = qk[n2][h][e] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            uint32_t ak[4], aq[4];
+            ldsm4(ak, Kt + tile_off<ROW>(16 * b + ar, 2 * ks + ac));
+            if (QK) ldsm4(aq, Qt + tile_off<ROW>(16 * b + ar, 2 * ks + ac));
+#pragma unroll
+            for (int n2 = 0; n2 <= b; ++n2) {
+                uint32_t bf[4];
+                ldsm4(bf, Kt + tile_off<ROW>(16 * n2 + br, 2 * ks + bc));
+                mma16816(kk[b * (b + 1) / 2 + n2][0], ak, bf[0], bf[1]);
+                mma16816(kk[b * (b + 1) / 2 + n2][1], ak, bf[2], bf[3]);
+                if (QK) {
+                    mma16816(qk[n2][0], aq, bf[0], bf[1]);
+                    mma16816(qk[n2][1], aq, bf[2], bf[3]);
+                }
+            }
+        }
+        if (QK) {
+            const float c0 = cum[16 * b + g], c1 = cum[16 * b + g + 8];
+#pragma unroll
+            for (int n2 = 0; n2 <= b; ++n2) {
+                uint32_t p[2][2];  // [columns half][rows half] 8 x 8 tiles
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int j = 16 * n2 + 8 * h + 2 * c;
+                    float v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int i = 16 * b + g + 8 * (e >> 1), jj = j + (e & 1);
+                        v[e] = jj <= i ? qk[n2][h][e] * __expf((e >> 1 ? c1 : c0) - cum[jj]) : 0.f;
+                    }
+                    p[h][0] = pack2(v[0], v[1]);
+                    p[h][1] = pack2(v[2], v[3]);
+                }
+                if (READ) {
+                    uint2 *pt = reinterpret_cast<uint2 *>(rec + kRecT) + lane;
+                    pt[(tile_base(2 * b) + n2) * 32] = make_uint2(p[0][0], p[1][0]);
+                    pt[(tile_base(2 * b + 1) + n2) * 32] = make_uint2(p[0][1], p[1][1]);
+                }
+                if (REV) {
+                    uint2 *pt = reinterpret_cast<uint2 *>(rrec + kRecP) + lane;
+                    pt[(rev_base(2 * n2) + b - n2) * 32] = make_uint2(movm_t(p[0][0]), movm_t(p[0][1]));
+                    pt[(rev_base(2 * n2 + 1) + b - n2) * 32] = make_uint2(movm_t(p[1][0]), movm_t(p[1][1]));
+                }
+            }
+        }
+    }
+    __syncwarp();  // the tiles have been read
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int n2 = 0; n2 <= b; ++n2)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = 16 * b + g + 8 * (e >> 1), j = 16 * n2 + 8 * h + 2 * c + (e & 1);
+                    if (j < i) M[j * kMP + i] = kk[b * (b + 1) / 2 + n2][h][e] * __expf(cum[i] - cum[j]) * bet[j];
+                }
+    __syncwarp();
+#pragma unroll
+    for (int blk = 0; blk < 4; ++blk) {
+        float x0[16], x1[16];  // rows 16 blk .. of the columns lane and (from block 2 on) lane + 32
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            x0[r] = 16 * blk + r == lane ? 1.f : 0.f;
+            x1[r] = 16 * blk + r == lane + 32 ? 1.f : 0.f;
+        }
+#pragma unroll 2
+        for (int k = 0; k < 16 * blk; ++k) {
+            const float y0 = lane <= k ? M[k * kMP + lane] : 0.f;
+            const float y1 = blk == 3 && lane + 32 <= k ? M[k * kMP + lane + 32] : 0.f;
+#pragma unroll
+            for (int r4 = 0; r4 < 4; ++r4) {
+                const float4 av = *reinterpret_cast<const float4 *>(M + k * kMP + 16 * blk + 4 * r4);
+                x0[4 * r4] = fmaf(-av.x, y0, x0[4 * r4]);
+                x0[4 * r4 + 1] = fmaf(-av.y, y0, x0[4 * r4 + 1]);
+                x0[4 * r4 + 2] = fmaf(-av.z, y0, x0[4 * r4 + 2]);
+                x0[4 * r4 + 3] = fmaf(-av.w, y0, x0[4 * r4 + 3]);
+                if (blk == 3) {
+                    x1[4 * r4] = fmaf(-av.x, y1, x1[4 * r4]);
+                    x1[4 * r4 + 1] = fmaf(-av.y, y1, x1[4 * r4 + 1]);
+                    x1[4 * r4 + 2] = fmaf(-av.z, y1, x1[4 * r4 + 2]);
+                    x1[4 * r4 + 3] = fmaf(-av.w, y1, x1[4 * r4 + 3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+#pragma unroll
+            for (int r4 = (k + 1) / 4; r4 < 4; ++r4) {
+                const float4 av = *reinterpret_cast<const float4 *>(M + (16 * blk + k) * kMP + 16 * blk + 4 * r4);
+                const float al[4] = {av.x, av.y, av.z, av.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int r = 4 * r4 + q;
+                    if (r > k) {
+                        x0[r] = fmaf(-al[q], x0[k], x0[r]);
+                        if (blk >= 2) x1[r] = fmaf(-al[q], x1[k], x1[r]);
+                    }
+                }
+            }
+        }
+        __syncwarp();  // every lane has read the block's columns of A beside the rows written now
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int i = 16 * blk + r;
+            if (lane <= i) M[i * kMP + lane] = x0[r];
+            if (blk >= 2 && lane + 32 <= i) M[i * kMP + lane + 32] = x1[r];
+        }
+        __syncwarp();
+    }
+    uint4 *tt = reinterpret_cast<uint4 *>(rec) + lane;
+#pragma unroll
+    for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+        for (int kt = 0; kt <= nt / 2; ++kt) {
+            const int i = 8 * nt + g, j = 16 * kt + 2 * c;
+            const float *x = M + i * kMP + j;
+            uint4 o;
+            split2(j < i ? x[0] : 0.f, j + 1 < i ? x[1] : 0.f, o.x, o.z);
+            split2(j + 8 < i ? x[8] : 0.f, j + 9 < i ? x[9] : 0.f, o.y, o.w);
+            tt[(tile_base(nt) + kt) * 32] = o;
+        }
+    if (REV) {
+        uint2 *lt = reinterpret_cast<uint2 *>(rrec) + lane;
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+            for (int kt = nt / 2; kt < 4; ++kt) {
+                const int i = 8 * nt + g, m = 16 * kt + 2 * c;  // T_mi, m > i
+                const float *x = M + m * kMP + i;
+                lt[(rev_base(nt) + kt - nt / 2) * 32] = make_uint2(pack2(m > i ? x[0] : 0.f, m + 1 > i ? x[kMP] : 0.f),
+                                                                   pack2(m + 8 > i ? x[8 * kMP] : 0.f, m + 9 > i ? x[9 * kMP] : 0.f));
+            }
     }
 }
 
-// A warp's 16 rows of f S into an operand image (D / 64 panels of D rows), through its 2 KB staging area.
-template <int NT>
-__device__ __forceinline__ void put_image(const float (&S)[NT][4], uint8_t *img, float f, uint8_t *outb, int row, int lane)
+// A warp's own 32 bytes of every row of the V (or dy) tile: once read, its staging area for what it writes.
+template <int NW>
+__device__ __forceinline__ uint32_t own_off(int r, int pc, int warp)
 {
+    constexpr int VP = NW * 2;  // 16-byte pieces of a row; they turn with the row
+    return (uint32_t)(r * NW * 32 + (((2 * warp + pc) ^ (r & (VP < 8 ? VP - 1 : 7))) << 4));
+}
+
+// 16 values x 64 tokens in operand registers to rows of 16 values.
+template <int NW, int D>
+__device__ __forceinline__ void put_tokens(__nv_bfloat16 *dst, const uint32_t (&f)[4][4], uint8_t *vt, int cnt, int warp, int lane)
+{
+    const uint32_t at = smem_addr(vt);
+#pragma unroll
+    for (int k4 = 0; k4 < 4; ++k4)
+        stsm4t(at + own_off<NW>(16 * k4 + (lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1, warp), f[k4][0], f[k4][1], f[k4][2], f[k4][3]);
+    __syncwarp();
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const int r = 16 * x + lane / 2, pc = lane % 2;
+        if (r < cnt) *reinterpret_cast<uint4 *>(dst + (size_t)r * D + 8 * pc) = *reinterpret_cast<const uint4 *>(vt + own_off<NW>(r, pc, warp));
+    }
+    __syncwarp();
+}
+
+// f times a warp's 16 rows, 64 columns at a time: `put` takes (panel, row, piece, 16 bytes).  Row r's piece pc is
+// staged in row 16 (pc / 2) + r of the tile.
+template <int NW, int NT, typename F>
+__device__ __forceinline__ void put_rows(const float (&S)[NT][4], float f, uint8_t *vt, int warp, int lane, F put)
+{
+    const uint32_t at = smem_addr(vt);
 #pragma unroll
     for (int h = 0; h < NT / 8; ++h) {
 #pragma unroll
-        for (int n = 8 * h; n < 8 * h + 8; n += 2)
-            stsm4(smem_addr(outb) + tile_off<128>(lane & 15, (n & 7) + (lane >> 4)), pack2(f * S[n][0], f * S[n][1]),
-                  pack2(f * S[n][2], f * S[n][3]), pack2(f * S[n + 1][0], f * S[n + 1][1]), pack2(f * S[n + 1][2], f * S[n + 1][3]));
+        for (int n = 0; n < 8; n += 2) {
+            const float(&s0)[4] = S[8 * h + n], (&s1)[4] = S[8 * h + n + 1];
+            stsm4(at + own_off<NW>(8 * n + (lane & 15), lane >> 4, warp), pack2(f * s0[0], f * s0[1]), pack2(f * s0[2], f * s0[3]),
+                  pack2(f * s1[0], f * s1[1]), pack2(f * s1[2], f * s1[3]));
+        }
         __syncwarp();
-        uint4 *dst = reinterpret_cast<uint4 *>(img + h * (NT * 8 * 128) + row * 128);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) dst[32 * x + lane] = reinterpret_cast<const uint4 *>(outb)[32 * x + lane];
+        for (int x = 0; x < 4; ++x) {
+            const int r = 4 * x + lane / 8, pc = lane % 8;
+            put(h, r, pc, *reinterpret_cast<const uint4 *>(vt + own_off<NW>(16 * (pc / 2) + r, pc & 1, warp)));
+        }
         __syncwarp();
     }
 }
@@ -289,16 +343,16 @@ __device__ __forceinline__ void put_image(const float (&S)[NT][4], uint8_t *img,
 template <int D, int NW, bool READ>
 struct WalkSmem {
     static constexpr int kK = kCH * D * 2, kV = kCH * NW * 32;
-    static constexpr int kStage = kK * (READ ? 2 : 1) + kV + kRec;
-    static constexpr int kOut = NW * 2048;  // a warp's 64 tokens x 16 values on their way out
-    static constexpr int kTotal = 2 * kStage + kOut;
+    static constexpr int kR = READ ? kRec : kRec - kRecP;  // without reads the record's P stays out
+    static constexpr int kStage = kK * (READ ? 2 : 1) + kV + kR;
+    static constexpr int kTotal = 2 * kStage;
 };
 
 template <int D, int NW, bool READ>
-__global__ void __launch_bounds__(32 * NW) delta_walk_tc(DeltaTcArgs a)
+__global__ void __launch_bounds__(32 * NW, NW == 4 ? (READ ? 2 : 3) : 1) delta_walk_tc(DeltaTcArgs a)
 {
     using W = WalkSmem<D, NW, READ>;
-    constexpr int ROW = D * 2, PIECES = D / 8, NT = 32 * NW, KS = D / 16, VROW = NW * 32, VP = NW * 2;
+    constexpr int ROW = D * 2, PIECES = D / 8, NT = 32 * NW, KS = D / 16, VP = NW * 2;
     extern __shared__ __align__(16) uint8_t sm[];
     constexpr int splits = D / (16 * NW);
     const int rs = (int)blockIdx.x % splits;
@@ -320,14 +374,12 @@ __global__ void __launch_bounds__(32 * NW) delta_walk_tc(DeltaTcArgs a)
         }
         for (int e = tid; e < kCH * VP; e += NT) {
             const int r = e / VP, pc = e % VP;
-            // rows of VROW bytes; the pieces of a row turn with it
-            cp16(smem_addr(st) + W::kK + r * VROW + ((pc ^ (r & (VP < 8 ? VP - 1 : 7))) << 4),
-                 a.v + (row0 + (r < cnt ? r : 0)) * D + vbase + pc * 8, r < cnt);
+            cp16(smem_addr(st) + W::kK + own_off<NW>(r, pc, 0), a.v + (row0 + (r < cnt ? r : 0)) * D + vbase + pc * 8, r < cnt);
         }
         const uint8_t *rec = a.rec + ((size_t)sid * a.NCH + ch) * kRec;
-        const uint32_t dst = smem_addr(st) + W::kStage - kRec;
-        for (int e = tid; e < kRec / 16; e += NT)
-            if (READ || e < kRecT / 16 || e >= (kRecT + kRecP) / 16) cp16(dst + e * 16, rec + e * 16, true);
+        const uint32_t dst = smem_addr(st) + W::kStage - W::kR;
+        for (int e = tid; e < W::kR / 16; e += NT)
+            cp16(dst + e * 16, rec + (READ || e < kRecT / 16 ? e : e + kRecP / 16) * 16, true);
         cp_commit();
     };
 
@@ -337,42 +389,19 @@ __global__ void __launch_bounds__(32 * NW) delta_walk_tc(DeltaTcArgs a)
 #pragma unroll
         for (int e = 0; e < 4; ++e) S[n][e] = 0.f;
 
-    uint8_t *outb = sm + 2 * W::kStage + warp * 2048;
     load(0);
     for (int ch = 0; ch < nch; ++ch) {
         cp_wait<0>();
         __syncthreads();  // the chunk has come, and the stage of the one before is free
         if (ch + 1 < nch) load(ch + 1);
-        const uint8_t *st = sm + (ch & 1) * W::kStage;
+        uint8_t *st = sm + (ch & 1) * W::kStage, *vown = st + W::kK;
         const uint32_t kt = smem_addr(st), vt = kt + W::kK, qt = vt + W::kV;
-        const uint8_t *rec = st + W::kStage - kRec;
-        const float *vec = reinterpret_cast<const float *>(rec + kRecT + kRecP);
+        const uint8_t *rec = st + W::kStage - W::kR;
+        const float *vec = reinterpret_cast<const float *>(rec + W::kR - kRecV);
         const size_t row0 = (size_t)bh * a.L + t0 + ch * kCH;
         const int cnt = min(kCH, len - ch * kCH);
         const size_t cidx = (size_t)sid * a.NCH + ch;
 
-        // an image's panels: 64 columns of all D rows, rows of 128 bytes with their pieces exchanged by row % 8
-        if (a.spre_img && ch > 0 && !(ch & 1))
-            put_image(S, a.spre_img + ((size_t)sid * (a.C / 128) + ch / 2) * (D * D * 2), vec[0], outb, vbase + 16 * warp, lane);
-        if (a.S_c) {  // the memory before the chunk, in bf16, through the warp's staging area
-            __nv_bfloat16 *dst = a.S_c + (cidx * D + vbase + 16 * warp) * D;
-#pragma unroll
-            for (int h = 0; h < D / 64; ++h) {  // 64 keys at a time: 16 rows of 128 bytes
-#pragma unroll
-                for (int n = 0; n < 8; n += 2)
-                    stsm4(smem_addr(outb) + tile_off<128>(lane & 15, n + (lane >> 4)), pack2(S[8 * h + n][0], S[8 * h + n][1]),
-                          pack2(S[8 * h + n][2], S[8 * h + n][3]), pack2(S[8 * h + n + 1][0], S[8 * h + n + 1][1]),
-                          pack2(S[8 * h + n + 1][2], S[8 * h + n + 1][3]));
-                __syncwarp();
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int r = x * 4 + lane / 8, pc = lane % 8;
-                    *reinterpret_cast<uint4 *>(dst + (size_t)r * D + 64 * h + pc * 8) =
-                        *reinterpret_cast<const uint4 *>(outb + tile_off<128>(r, pc));
-                }
-                __syncwarp();
-            }
-        }
         // (S K^T) and (S Q^T): rows values, columns tokens
         float X[8][4], O[8][4];
 #pragma unroll
@@ -408,7 +437,7 @@ __global__ void __launch_bounds__(32 * NW) delta_walk_tc(DeltaTcArgs a)
             uint32_t v4[4];
             {
                 const int r = 16 * kt4 + (lane >> 4) * 8 + (lane & 7), pc = 2 * warp + ((lane >> 3) & 1);
-                ldsm4t(v4, vt + r * VROW + ((pc ^ (r & (VP < 8 ? VP - 1 : 7))) << 4));
+                ldsm4t(v4, vt + own_off<NW>(r, pc, 0));
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -425,6 +454,19 @@ __global__ void __launch_bounds__(32 * NW) delta_walk_tc(DeltaTcArgs a)
                     O[n][3] *= ga.y;
                 }
             }
+        }
+        __syncwarp();  // the warp's part of V is free
+        if (a.spre_img && ch > 0 && !(ch & 1)) {  // panels of 64 columns, their pieces exchanged by row % 8
+            uint8_t *img = a.spre_img + ((size_t)sid * (a.C / 128) + ch / 2) * (D * D * 2) + (vbase + 16 * warp) * 128;
+            put_rows<NW>(S, vec[0], vown, warp, lane, [&](int h, int r, int pc, const uint4 &x) {
+                *reinterpret_cast<uint4 *>(img + h * (D * 128) + tile_off<128>(r, pc)) = x;
+            });
+        }
+        if (a.S_c) {  // the memory before the chunk
+            __nv_bfloat16 *dst = a.S_c + (cidx * D + vbase + 16 * warp) * D;
+            put_rows<NW>(S, 1.f, vown, warp, lane, [&](int h, int r, int pc, const uint4 &x) {
+                *reinterpret_cast<uint4 *>(dst + (size_t)r * D + 64 * h + pc * 8) = x;
+            });
         }
         {
             uint32_t rh[4][4], rl[4][4];
@@ -466,21 +508,8 @@ __global__ void __launch_bounds__(32 * NW) delta_walk_tc(DeltaTcArgs a)
                     mma16816(O[n], uh[k4], b.x, b.y);
                 }
         }
-        auto put = [&](__nv_bfloat16 *dst, const uint32_t (&f)[4][4]) {  // f: an operand of values x tokens
-#pragma unroll
-            for (int k4 = 0; k4 < 4; ++k4) {
-                const int r = 16 * k4 + (lane >> 4) * 8 + (lane & 7), pc = (lane >> 3) & 1;
-                stsm4t(smem_addr(outb) + r * 32 + ((pc ^ ((r >> 2) & 1)) << 4), f[k4][0], f[k4][1], f[k4][2], f[k4][3]);
-            }
-            __syncwarp();
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int r = 16 * x + lane / 2, pc = lane % 2;
-                if (r < cnt)
-                    *reinterpret_cast<uint4 *>(dst + (row0 + r) * D + vbase + 16 * warp + 8 * pc) =
-                        *reinterpret_cast<const uint4 *>(outb + r * 32 + ((pc ^ ((r >> 2) & 1)) << 4));
-            }
-            __syncwarp();
+        auto put = [&](__nv_bfloat16 *dst, const uint32_t (&f)[4][4]) {
+            put_tokens<NW, D>(dst + row0 * D + vbase + 16 * warp, f, vown, cnt, warp, lane);
         };
         if (a.U) put(a.U, uh);
         if (READ) {
@@ -533,7 +562,12 @@ __global__ void __launch_bounds__(32 * NW) delta_walk_tc(DeltaTcArgs a)
                 mma16816(S[2 * n2 + 1], ul[k4], b[2], b[3]);
             }
     }
-    if (a.states_img) put_image(S, a.states_img + (size_t)sid * (D * D * 2), 1.f, outb, vbase + 16 * warp, lane);
+    if (a.states_img) {
+        uint8_t *img = a.states_img + (size_t)sid * (D * D * 2) + (vbase + 16 * warp) * 128;
+        put_rows<NW>(S, 1.f, sm + ((nch - 1) & 1) * W::kStage + W::kK, warp, lane, [&](int h, int r, int pc, const uint4 &x) {
+            *reinterpret_cast<uint4 *>(img + h * (D * 128) + tile_off<128>(r, pc)) = x;
+        });
+    }
     if (a.states) {
         float *dst = a.states + ((size_t)sid * D + vbase + 16 * warp) * D;
 #pragma unroll
@@ -555,14 +589,14 @@ template <int D, int NW>
 struct RWalkSmem {
     static constexpr int kK = kCH * D * 2, kV = kCH * NW * 32;
     static constexpr int kStage = 2 * kK + kV + kDeltaRRecBytes + 256;  // K, Q, dy columns, record, gates
-    static constexpr int kTotal = 2 * kStage + NW * 2048;
+    static constexpr int kTotal = 2 * kStage;
 };
 
 template <int D, int NW>
-__global__ void __launch_bounds__(32 * NW) delta_rwalk_tc(DeltaTcArgs a)
+__global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1) delta_rwalk_tc(DeltaTcArgs a)
 {
     using W = RWalkSmem<D, NW>;
-    constexpr int ROW = D * 2, PIECES = D / 8, NT = 32 * NW, KS = D / 16, VROW = NW * 32, VP = NW * 2;
+    constexpr int ROW = D * 2, PIECES = D / 8, NT = 32 * NW, KS = D / 16, VP = NW * 2;
     extern __shared__ __align__(16) uint8_t sm[];
     constexpr int splits = D / (16 * NW);
     const int rs = (int)blockIdx.x % splits;
@@ -584,8 +618,7 @@ __global__ void __launch_bounds__(32 * NW) delta_rwalk_tc(DeltaTcArgs a)
         }
         for (int e = tid; e < kCH * VP; e += NT) {
             const int r = e / VP, pc = e % VP;
-            cp16(smem_addr(st) + 2 * W::kK + r * VROW + ((pc ^ (r & (VP < 8 ? VP - 1 : 7))) << 4),
-                 a.dy + (row0 + (r < cnt ? r : 0)) * D + vbase + pc * 8, r < cnt);
+            cp16(smem_addr(st) + 2 * W::kK + own_off<NW>(r, pc, 0), a.dy + (row0 + (r < cnt ? r : 0)) * D + vbase + pc * 8, r < cnt);
         }
         const uint8_t *rec = a.rrec + ((size_t)sid * a.NCH + ch) * kDeltaRRecBytes;
         const uint32_t dst = smem_addr(st) + 2 * W::kK + W::kV;
@@ -620,38 +653,18 @@ __global__ void __launch_bounds__(32 * NW) delta_rwalk_tc(DeltaTcArgs a)
             for (int e = 0; e < 4; ++e) R[n][e] = 0.f;
     }
 
-    uint8_t *outb = sm + 2 * W::kStage + warp * 2048;
     load(nch - 1);
     for (int ch = nch - 1; ch >= 0; --ch) {
         cp_wait<0>();
         __syncthreads();
         if (ch > 0) load(ch - 1);
-        const uint8_t *st = sm + (ch & 1) * W::kStage;
+        uint8_t *st = sm + (ch & 1) * W::kStage, *vown = st + 2 * W::kK;
         const uint32_t kt = smem_addr(st), qt = kt + W::kK, vt = qt + W::kK;
         const uint8_t *rec = st + 2 * W::kK + W::kV;
         const float *vec = reinterpret_cast<const float *>(rec + 2 * kRecP);
         const float *gs = reinterpret_cast<const float *>(rec + kDeltaRRecBytes);
         const size_t row0 = (size_t)bh * a.L + t0 + ch * kCH;
         const int cnt = min(kCH, len - ch * kCH);
-        {
-            __nv_bfloat16 *dst = a.R_c + (((size_t)sid * a.NCH + ch) * D + vbase + 16 * warp) * D;
-#pragma unroll
-            for (int h = 0; h < D / 64; ++h) {
-#pragma unroll
-                for (int n = 0; n < 8; n += 2)
-                    stsm4(smem_addr(outb) + tile_off<128>(lane & 15, n + (lane >> 4)), pack2(R[8 * h + n][0], R[8 * h + n][1]),
-                          pack2(R[8 * h + n][2], R[8 * h + n][3]), pack2(R[8 * h + n + 1][0], R[8 * h + n + 1][1]),
-                          pack2(R[8 * h + n + 1][2], R[8 * h + n + 1][3]));
-                __syncwarp();
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int r = x * 4 + lane / 8, pc = lane % 8;
-                    *reinterpret_cast<uint4 *>(dst + (size_t)r * D + 64 * h + pc * 8) =
-                        *reinterpret_cast<const uint4 *>(outb + tile_off<128>(r, pc));
-                }
-                __syncwarp();
-            }
-        }
         float X[8][4];
 #pragma unroll
         for (int n = 0; n < 8; ++n)
@@ -680,7 +693,7 @@ __global__ void __launch_bounds__(32 * NW) delta_rwalk_tc(DeltaTcArgs a)
         for (int k4 = 0; k4 < 4; ++k4) {
             uint32_t v4[4];
             const int r = 16 * k4 + (lane >> 4) * 8 + (lane & 7), pc = 2 * warp + ((lane >> 3) & 1);
-            ldsm4t(v4, vt + r * VROW + ((pc ^ (r & (VP < 8 ? VP - 1 : 7))) << 4));
+            ldsm4t(v4, vt + own_off<NW>(r, pc, 0));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int n = 2 * k4 + h;
@@ -698,6 +711,13 @@ __global__ void __launch_bounds__(32 * NW) delta_rwalk_tc(DeltaTcArgs a)
                     pg[k4][2 * h + z] = pack2(ga.x * p0, ga.y * p1);
                 }
             }
+        }
+        __syncwarp();  // the warp's part of dy is free
+        {  // the adjoint after the chunk
+            __nv_bfloat16 *dst = a.R_c + (((size_t)sid * a.NCH + ch) * D + vbase + 16 * warp) * D;
+            put_rows<NW>(R, 1.f, vown, warp, lane, [&](int h, int r, int pc, const uint4 &x) {
+                *reinterpret_cast<uint4 *>(dst + (size_t)r * D + 64 * h + pc * 8) = x;
+            });
         }
         const uint2 *lt = reinterpret_cast<const uint2 *>(rec) + lane;
         const uint2 *pt = reinterpret_cast<const uint2 *>(rec + kRecP) + lane;
@@ -734,20 +754,7 @@ __global__ void __launch_bounds__(32 * NW) delta_rwalk_tc(DeltaTcArgs a)
             wf[n / 2][2 * (n & 1)] = pack2(X[n][0], X[n][1]);
             wf[n / 2][2 * (n & 1) + 1] = pack2(X[n][2], X[n][3]);
         }
-#pragma unroll
-        for (int k4 = 0; k4 < 4; ++k4) {
-            const int r = 16 * k4 + (lane >> 4) * 8 + (lane & 7), pc = (lane >> 3) & 1;
-            stsm4t(smem_addr(outb) + r * 32 + ((pc ^ ((r >> 2) & 1)) << 4), wf[k4][0], wf[k4][1], wf[k4][2], wf[k4][3]);
-        }
-        __syncwarp();
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const int r = 16 * x + lane / 2, pc = lane % 2;
-            if (r < cnt)
-                *reinterpret_cast<uint4 *>(a.dv + (row0 + r) * D + vbase + 16 * warp + 8 * pc) =
-                    *reinterpret_cast<const uint4 *>(outb + r * 32 + ((pc ^ ((r >> 2) & 1)) << 4));
-        }
-        __syncwarp();
+        put_tokens<NW, D>(a.dv + row0 * D + vbase + 16 * warp, wf, vown, cnt, warp, lane);
 #pragma unroll
         for (int n = 0; n < 8; ++n) {  // -exp(c) w
             const float2 ga = *reinterpret_cast<const float2 *>(vec + 8 * n + 2 * c);
@@ -778,24 +785,26 @@ __global__ void __launch_bounds__(32 * NW) delta_rwalk_tc(DeltaTcArgs a)
 // ---------------------------------------------------------------------------
 // delta_grads_tc: one CTA per chunk, everything that sums over value rows (k_delta_simt.cu's header).
 // Eight warps: warp % 4 takes 16 tokens, warp / 4 half of the dimensions.  B1, B2 and their transposes
-// are formed by each warp for its own tokens straight into operand registers.  S and R share a buffer,
-// so that two CTAs fit on an SM (d = 128) and one's loads run under the other's products.
+// are formed by each warp for its own tokens straight into operand registers.  A chunk is a chain of loads and
+// small products, so two CTAs share an SM: S and R come through one 16 KB buffer (64 rows at a time, the next
+// ones on their way under the products between), and at most three of the five 16 x 64 results are held at once.
 // ---------------------------------------------------------------------------
 constexpr int kGradThreads = 256;
 
 template <int D>
 struct GradSmem {
-    static constexpr int kT = kCH * D * 2;         // a 64-token tile
-    static constexpr int kM = D * D * 2;           // S, then R
+    static constexpr int kT = kCH * D * 2;   // a 64-token tile
+    static constexpr int kM = 64 * D * 2;    // 64 rows of S or R
     static constexpr int kVec = 4 * (22 * kCH + 16);
     static constexpr int kTotal = 5 * kT + kM + kVec;
 };
 
 template <int D>
-__global__ void __launch_bounds__(kGradThreads, D == 128 ? 1 : 2) delta_grads_tc(DeltaTcArgs a)
+__global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
 {
     using G = GradSmem<D>;
     constexpr int ROW = D * 2, PIECES = D / 8, KS = D / 16, HD = D / 2, HN = HD / 8;  // HN column tiles per warp
+    constexpr int MB = D / 64;                                                         // blocks of S and R
     extern __shared__ __align__(16) uint8_t sm[];
     uint8_t *Qt = sm, *Kt = Qt + G::kT, *Pt = Kt + G::kT, *Et = Pt + G::kT, *Wt = Et + G::kT, *Mt = Wt + G::kT;
     float *cum = reinterpret_cast<float *>(Mt + G::kM), *bet = cum + kCH, *gs = bet + kCH, *pw = gs + kCH;
@@ -805,24 +814,27 @@ __global__ void __launch_bounds__(kGradThreads, D == 128 ? 1 : 2) delta_grads_tc
     const Where w = chunk_at(a, blockIdx.x);
     if (w.cnt <= 0) return;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, c = lane % 4;
-    const int m0 = 16 * (warp & 3), half = warp >> 2, d0 = half * HD;
+    const int wm = warp & 3, m0 = 16 * wm, half = warp >> 2, d0 = half * HD;
     const size_t row0 = (size_t)w.bh * a.L + w.tb;
     const __nv_bfloat16 *S = a.S_c + (size_t)blockIdx.x * D * D, *R = a.R_c + (size_t)blockIdx.x * D * D;
 
+    auto load_rows = [&](const __nv_bfloat16 *src, int b) {  // rows 64 b .. of S or R
+        for (int e = tid; e < 64 * PIECES; e += kGradThreads)
+            cp16(smem_addr(Mt) + tile_off<ROW>(e / PIECES, e % PIECES), src + (size_t)(64 * b * PIECES + e) * 8, true);
+        cp_commit();
+    };
     for (int e = tid; e < kCH * PIECES; e += kGradThreads) {
         const int r = e / PIECES, pc = e % PIECES;
         const bool ok = r < w.cnt;
         const size_t off = (row0 + (ok ? r : 0)) * D + pc * 8;
         const uint32_t o = tile_off<ROW>(r, pc);
+        cp16(smem_addr(Pt) + o, a.dy + off, ok);
+        cp16(smem_addr(Wt) + o, a.dv + off, ok);
+        cp16(smem_addr(Et) + o, a.E + off, ok);
         cp16(smem_addr(Qt) + o, a.q + off, ok);
         cp16(smem_addr(Kt) + o, a.k + off, ok);
-        cp16(smem_addr(Pt) + o, a.dy + off, ok);
-        cp16(smem_addr(Et) + o, a.E + off, ok);
-        cp16(smem_addr(Wt) + o, a.dv + off, ok);
     }
-    for (int e = tid; e < D * PIECES; e += kGradThreads)
-        cp16(smem_addr(Mt) + tile_off<ROW>(e / PIECES, e % PIECES), S + (size_t)e * 8, true);
-    cp_commit();
+    load_rows(S, 0);
     if (warp == 0) {
         const int i = 2 * lane;
         const float x0 = i < w.cnt ? delta_log(__bfloat162float(a.la[row0 + i])) : 0.f;
@@ -854,58 +866,66 @@ __global__ void __launch_bounds__(kGradThreads, D == 128 ? 1 : 2) delta_grads_tc
             for (int z = 0; z < 4; ++z) yw[z] = pack2(gs[r] * low_f(yw[z]), gs[r] * high_f(yw[z]));
             *x = y;
         }
+        __syncthreads();
     }
-    auto inner = [](const uint4 &x, const uint4 &y, float s) {
-        const uint32_t *xw = reinterpret_cast<const uint32_t *>(&x), *yw = reinterpret_cast<const uint32_t *>(&y);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) s = fmaf(low_f(xw[q]), low_f(yw[q]), fmaf(high_f(xw[q]), high_f(yw[q]), s));
-        return s;
-    };
-    uint4 sk[D * PIECES / kGradThreads];  // this thread's pieces of S, for <R, S>
-#pragma unroll
-    for (int x = 0; x < D * PIECES / kGradThreads; ++x) {
-        const int e = tid + x * kGradThreads;
-        sk[x] = *reinterpret_cast<const uint4 *>(Mt + tile_off<ROW>(e / PIECES, e % PIECES));
-    }
-    __syncthreads();
 
     const int ar = m0 + (lane & 15), ac = lane >> 4;                       // A operand of a token tile
     const int br = (lane >> 4) * 8 + (lane & 7), bc = (lane >> 3) & 1;     // B, columns = rows of the tile
     const int tr = ((lane >> 3) & 1) * 8 + (lane & 7), tc = lane >> 4;     // B, rows = rows of the tile
-    float dq[HN][4], y[HN][4], z[HN][4];
-#pragma unroll
-    for (int n = 0; n < HN; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) dq[n][e] = y[n][e] = z[n][e] = 0.f;
-    // p S and w S
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-        uint32_t ap[4], aw[4];
-        ldsm4(ap, smem_addr(Pt) + tile_off<ROW>(ar, 2 * ks + ac));
-        ldsm4(aw, smem_addr(Wt) + tile_off<ROW>(ar, 2 * ks + ac));
-#pragma unroll
-        for (int n2 = 0; n2 < HN / 2; ++n2) {
-            uint32_t b[4];
-            ldsm4t(b, smem_addr(Mt) + tile_off<ROW>(16 * ks + tr, d0 / 8 + 2 * n2 + tc));
-            mma16816(dq[2 * n2], ap, b[0], b[1]);
-            mma16816(dq[2 * n2 + 1], ap, b[2], b[3]);
-            mma16816(z[2 * n2], aw, b[0], b[1]);
-            mma16816(z[2 * n2 + 1], aw, b[2], b[3]);
-        }
-    }
-    __syncthreads();  // S has been read
-    for (int e = tid; e < D * PIECES; e += kGradThreads)
-        cp16(smem_addr(Mt) + tile_off<ROW>(e / PIECES, e % PIECES), R + (size_t)e * 8, true);
-    cp_commit();
     const float c_lo = cum[m0 + g], c_hi = cum[m0 + g + 8], ce = cum[kCH - 1];
-    {
-        const float e0 = expf(c_lo), e1 = expf(c_hi);
+    auto zero = [](auto &x) {
+#pragma unroll
+        for (int n = 0; n < (int)(sizeof(x) / sizeof(x[0])); ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
+    };
+    auto scale = [&](float (&x)[HN][4], float e0, float e1) {
 #pragma unroll
         for (int n = 0; n < HN; ++n) {
-            dq[n][0] *= e0; dq[n][1] *= e0; dq[n][2] *= e1; dq[n][3] *= e1;
-            z[n][0] *= e0; z[n][1] *= e0; z[n][2] *= e1; z[n][3] *= e1;
+            x[n][0] *= e0; x[n][1] *= e0; x[n][2] *= e1; x[n][3] *= e1;
         }
-    }
+    };
+    // the warp's 16 rows of `tile` times the 64 rows of S or R in the buffer (block b of its columns)
+    auto times_rows = [&](float (&x)[HN][4], const uint8_t *tile, int b) {
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            uint32_t af[4];
+            ldsm4(af, smem_addr(tile) + tile_off<ROW>(ar, 2 * (4 * b + ks) + ac));
+#pragma unroll
+            for (int n2 = 0; n2 < HN / 2; ++n2) {
+                uint32_t bf[4];
+                ldsm4t(bf, smem_addr(Mt) + tile_off<ROW>(16 * ks + tr, d0 / 8 + 2 * n2 + tc));
+                mma16816(x[2 * n2], af, bf[0], bf[1]);
+                mma16816(x[2 * n2 + 1], af, bf[2], bf[3]);
+            }
+        }
+    };
+    // the warp's 16 rows of `rows` against the 64 tokens of `cols`; 16 x 16 blocks n2 with `want`
+    auto pairs = [&](float (&x)[8][4], const uint8_t *rows, const uint8_t *cols, auto want) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            uint32_t af[4];
+            ldsm4(af, smem_addr(rows) + tile_off<ROW>(ar, 2 * ks + ac));
+#pragma unroll
+            for (int n2 = 0; n2 < 4; ++n2) {
+                if (!want(n2)) continue;
+                uint32_t bf[4];
+                ldsm4(bf, smem_addr(cols) + tile_off<ROW>(16 * n2 + br, 2 * ks + bc));
+                mma16816(x[2 * n2], af, bf[0], bf[1]);
+                mma16816(x[2 * n2 + 1], af, bf[2], bf[3]);
+            }
+        }
+    };
+    // x += (the weighted pairs) times the tokens of `tile`
+    auto times_tokens = [&](float (&x)[HN][4], const uint32_t (&f)[4], const uint8_t *tile, int k4) {
+#pragma unroll
+        for (int n2 = 0; n2 < HN / 2; ++n2) {
+            uint32_t bf[4];
+            ldsm4t(bf, smem_addr(tile) + tile_off<ROW>(16 * k4 + tr, d0 / 8 + 2 * n2 + tc));
+            mma16816(x[2 * n2], f, bf[0], bf[1]);
+            mma16816(x[2 * n2 + 1], f, bf[2], bf[3]);
+        }
+    };
     auto row_dot = [&](const float (&x)[HN][4], const uint8_t *tile, int what) {  // per token, over this half
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
@@ -924,53 +944,25 @@ __global__ void __launch_bounds__(kGradThreads, D == 128 ? 1 : 2) delta_grads_tc
             rowsum[(2 * what + half) * kCH + m0 + g + 8] = s1;
         }
     };
-    row_dot(dq, Qt, 1);
-    row_dot(z, Kt, 3);
-    // rows i of B1 beta and B2 beta (columns j <= i): dq += B1 K, z += B2 K.  F_ij = beta_j (B1_ij q_i.k_j - B2_ij k_i.k_j)
-    // for j < i, the first term on the warps of half 0, the second on those of half 1
-    {
-        float b1[8][4], b2[8][4];
-#pragma unroll
-        for (int n = 0; n < 8; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) b1[n][e] = b2[n][e] = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            uint32_t ap[4], aw[4];
-            ldsm4(ap, smem_addr(Pt) + tile_off<ROW>(ar, 2 * ks + ac));
-            ldsm4(aw, smem_addr(Wt) + tile_off<ROW>(ar, 2 * ks + ac));
-#pragma unroll
-            for (int n2 = 0; n2 < 4; ++n2) {
-                if (n2 > (warp & 3)) break;
-                uint32_t b[4];
-                ldsm4(b, smem_addr(Et) + tile_off<ROW>(16 * n2 + br, 2 * ks + bc));
-                mma16816(b1[2 * n2], ap, b[0], b[1]);
-                mma16816(b1[2 * n2 + 1], ap, b[2], b[3]);
-                mma16816(b2[2 * n2], aw, b[0], b[1]);
-                mma16816(b2[2 * n2 + 1], aw, b[2], b[3]);
-            }
-        }
-        float f0 = 0.f, f1s = 0.f;  // row sums of F
+    // rows i, columns j < i of F_ij = beta_j D_ij B (rows . k): its row and column sums
+    auto pair_sums = [&](const float (&b)[8][4], const uint8_t *rows, float sign) {
+        float f0 = 0.f, f1 = 0.f;
 #pragma unroll
         for (int n2 = 0; n2 < 4; ++n2) {
-            float *cf = colf + (4 * half + (warp & 3)) * kCH + 16 * n2;
-            if (n2 > (warp & 3)) {
+            float *cf = colf + (4 * half + wm) * kCH + 16 * n2;
+            if (n2 > wm) {
                 if (lane < 16) cf[lane] = 0.f;
                 continue;
             }
             float kk[2][4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) kk[h][e] = 0.f;
-            const uint32_t at = smem_addr(half ? Kt : Qt);
+            zero(kk);
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                uint32_t aq[4], b[4];
-                ldsm4(aq, at + tile_off<ROW>(ar, 2 * ks + ac));
-                ldsm4(b, smem_addr(Kt) + tile_off<ROW>(16 * n2 + br, 2 * ks + bc));
-                mma16816(kk[0], aq, b[0], b[1]);
-                mma16816(kk[1], aq, b[2], b[3]);
+                uint32_t aq[4], bf[4];
+                ldsm4(aq, smem_addr(rows) + tile_off<ROW>(ar, 2 * ks + ac));
+                ldsm4(bf, smem_addr(Kt) + tile_off<ROW>(16 * n2 + br, 2 * ks + bc));
+                mma16816(kk[0], aq, bf[0], bf[1]);
+                mma16816(kk[1], aq, bf[2], bf[3]);
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -979,9 +971,9 @@ __global__ void __launch_bounds__(kGradThreads, D == 128 ? 1 : 2) delta_grads_tc
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int i = m0 + g + 8 * (e >> 1), jj = j + (e & 1);
-                    const float f = jj < i ? expf((e >> 1 ? c_hi : c_lo) - cum[jj]) * bet[jj] * kk[h][e] * (half ? -b2[n][e] : b1[n][e]) : 0.f;
+                    const float f = jj < i ? __expf((e >> 1 ? c_hi : c_lo) - cum[jj]) * bet[jj] * kk[h][e] * sign * b[n][e] : 0.f;
                     col[e & 1] += f;
-                    if (e >> 1) f1s += f;
+                    if (e >> 1) f1 += f;
                     else f0 += f;
                 }
 #pragma unroll
@@ -997,129 +989,160 @@ __global__ void __launch_bounds__(kGradThreads, D == 128 ? 1 : 2) delta_grads_tc
         }
         f0 += __shfl_xor_sync(0xffffffffu, f0, 1);
         f0 += __shfl_xor_sync(0xffffffffu, f0, 2);
-        f1s += __shfl_xor_sync(0xffffffffu, f1s, 1);
-        f1s += __shfl_xor_sync(0xffffffffu, f1s, 2);
+        f1 += __shfl_xor_sync(0xffffffffu, f1, 1);
+        f1 += __shfl_xor_sync(0xffffffffu, f1, 2);
         if (c == 0) {
             rowf[half * kCH + m0 + g] = f0;
-            rowf[half * kCH + m0 + g + 8] = f1s;
+            rowf[half * kCH + m0 + g + 8] = f1;
         }
+    };
+    // a block of weighted pairs as an operand: rows i, columns j <= i (j < i) with beta_j, or transposed (rows j,
+    // columns i >= j, i > j) without
+    auto weigh_rows = [&](uint32_t (&f)[4], const float (&b)[8][4], int k4, bool diag) {
 #pragma unroll
-        for (int k4 = 0; k4 < 4; ++k4) {
-            if (k4 > (warp & 3)) break;
-            uint32_t f1[4], f2[4];
+        for (int h = 0; h < 2; ++h) {
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = m0 + g + 8 * (e >> 1), j = 16 * k4 + 8 * h + 2 * c + (e & 1);
+                v[e] = j < i || (diag && j == i) ? b[2 * k4 + h][e] * __expf((e >> 1 ? c_hi : c_lo) - cum[j]) * bet[j] : 0.f;
+            }
+            f[2 * h] = pack2(v[0], v[1]);
+            f[2 * h + 1] = pack2(v[2], v[3]);
+        }
+    };
+    auto weigh_cols = [&](uint32_t (&f)[4], const float (&b)[8][4], int k4, bool diag, float sign) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int j = m0 + g + 8 * (e >> 1), i = 16 * k4 + 8 * h + 2 * c + (e & 1);
+                v[e] = i > j || (diag && i == j) ? sign * b[2 * k4 + h][e] * __expf(cum[i] - (e >> 1 ? c_hi : c_lo)) : 0.f;
+            }
+            f[2 * h] = pack2(v[0], v[1]);
+            f[2 * h + 1] = pack2(v[2], v[3]);
+        }
+    };
+    // 16 x HD results to global memory: neighbouring lanes exchange halves of two tiles, so that a row's four lanes
+    // write 32 bytes in a run
+    auto store = [&](__nv_bfloat16 *dst, const float (&x)[HN][4]) {
+#pragma unroll
+        for (int n = 0; n < HN; n += 2)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int n = 2 * k4 + h;
+                const uint32_t p0 = pack2(x[n][2 * h], x[n][2 * h + 1]), p1 = pack2(x[n + 1][2 * h], x[n + 1][2 * h + 1]);
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, c & 1 ? p0 : p1, 1);
+                const int t = m0 + g + 8 * h;
+                if (t < w.cnt)
+                    *reinterpret_cast<uint2 *>(dst + (row0 + t) * D + d0 + 8 * (n + (c & 1)) + 4 * (c >> 1)) =
+                        c & 1 ? make_uint2(got, p1) : make_uint2(p0, got);
+            }
+    };
+    const auto lower = [&](int n2) { return n2 <= wm; };
+    const auto upper = [&](int n2) { return n2 >= wm; };
+
+    float z[HN][4], b[8][4];
+    zero(z);
+    zero(b);
+    {
+        float dq[HN][4];
+        zero(dq);
+        times_rows(dq, Pt, 0);
+        times_rows(z, Wt, 0);
+        __syncthreads();  // the rows have been read
+        if (MB > 1) load_rows(S, 1);
+        else load_rows(R, 0);
+        pairs(b, Pt, Et, lower);
+        if (MB > 1) {
+            cp_wait<0>();
+            __syncthreads();
+            times_rows(dq, Pt, 1);
+            times_rows(z, Wt, 1);
+            __syncthreads();
+            load_rows(R, 0);
+        }
+        const float e0 = __expf(c_lo), e1 = __expf(c_hi);
+        scale(dq, e0, e1);
+        scale(z, e0, e1);
+        row_dot(dq, Qt, 1);
+        row_dot(z, Kt, 3);
+        if (half == 0) pair_sums(b, Qt, 1.f);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = m0 + g + 8 * (e >> 1), j = 8 * n + 2 * c + (e & 1);
-                    const float f = j <= i ? expf((e >> 1 ? c_hi : c_lo) - cum[j]) * bet[j] : 0.f;
-                    b1[n][e] *= f;
-                    b2[n][e] *= j < i ? f : 0.f;
+        for (int k4 = 0; k4 < 4; ++k4) {
+            if (!lower(k4)) continue;
+            uint32_t f[4];
+            weigh_rows(f, b, k4, true);
+            times_tokens(dq, f, Kt, k4);
+        }
+        if (a.dq_add) {
+#pragma unroll
+            for (int n = 0; n < HN; ++n)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int t = m0 + g + 8 * x;
+                    if (t >= w.cnt) continue;
+                    const float2 f = *reinterpret_cast<const float2 *>(a.dq_add + (row0 + t) * D + d0 + 8 * n + 2 * c);
+                    dq[n][2 * x] += f.x;
+                    dq[n][2 * x + 1] += f.y;
                 }
-                f1[2 * h] = pack2(b1[n][0], b1[n][1]);
-                f1[2 * h + 1] = pack2(b1[n][2], b1[n][3]);
-                f2[2 * h] = pack2(b2[n][0], b2[n][1]);
-                f2[2 * h + 1] = pack2(b2[n][2], b2[n][3]);
-            }
+        }
+        store(a.dq, dq);
+    }
+    zero(b);
+    pairs(b, Wt, Et, lower);
+    if (half == 1) pair_sums(b, Kt, -1.f);
 #pragma unroll
-            for (int n2 = 0; n2 < HN / 2; ++n2) {
-                uint32_t b[4];
-                ldsm4t(b, smem_addr(Kt) + tile_off<ROW>(16 * k4 + tr, d0 / 8 + 2 * n2 + tc));
-                mma16816(dq[2 * n2], f1, b[0], b[1]);
-                mma16816(dq[2 * n2 + 1], f1, b[2], b[3]);
-                mma16816(z[2 * n2], f2, b[0], b[1]);
-                mma16816(z[2 * n2 + 1], f2, b[2], b[3]);
-            }
+    for (int k4 = 0; k4 < 4; ++k4) {
+        if (!lower(k4)) continue;
+        uint32_t f[4];
+        weigh_rows(f, b, k4, false);
+        times_tokens(z, f, Kt, k4);
+    }
+    float y[HN][4];
+    zero(y);
+    float in = 0.f;  // <R, S>
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+        cp_wait<0>();
+        __syncthreads();
+        for (int e = tid; e < 64 * PIECES; e += kGradThreads) {
+            const uint4 r4 = *reinterpret_cast<const uint4 *>(Mt + tile_off<ROW>(e / PIECES, e % PIECES));
+            const uint4 s4 = *reinterpret_cast<const uint4 *>(S + (size_t)(64 * mb * PIECES + e) * 8);
+            const uint32_t *rw = reinterpret_cast<const uint32_t *>(&r4), *sw = reinterpret_cast<const uint32_t *>(&s4);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) in = fmaf(low_f(rw[q]), low_f(sw[q]), fmaf(high_f(rw[q]), high_f(sw[q]), in));
+        }
+        times_rows(y, Et, mb);
+        if (mb + 1 < MB) {
+            __syncthreads();
+            load_rows(R, mb + 1);
+        }
+        if (mb == 0) {
+            zero(b);
+            pairs(b, Et, Pt, upper);
         }
     }
-    cp_wait<0>();
-    __syncthreads();  // R has come
-    {
-        float in = 0.f;
 #pragma unroll
-        for (int x = 0; x < D * PIECES / kGradThreads; ++x) {
-            const int e = tid + x * kGradThreads;
-            in = inner(sk[x], *reinterpret_cast<const uint4 *>(Mt + tile_off<ROW>(e / PIECES, e % PIECES)), in);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) in += __shfl_xor_sync(0xffffffffu, in, o);
-        if (lane == 0) red[warp] = in;
-    }
-    // E R
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-        uint32_t ae[4];
-        ldsm4(ae, smem_addr(Et) + tile_off<ROW>(ar, 2 * ks + ac));
-#pragma unroll
-        for (int n2 = 0; n2 < HN / 2; ++n2) {
-            uint32_t b[4];
-            ldsm4t(b, smem_addr(Mt) + tile_off<ROW>(16 * ks + tr, d0 / 8 + 2 * n2 + tc));
-            mma16816(y[2 * n2], ae, b[0], b[1]);
-            mma16816(y[2 * n2 + 1], ae, b[2], b[3]);
-        }
-    }
-    {
-        const float e0 = expf(ce - c_lo), e1 = expf(ce - c_hi);
-#pragma unroll
-        for (int n = 0; n < HN; ++n) {
-            y[n][0] *= e0; y[n][1] *= e0; y[n][2] *= e1; y[n][3] *= e1;
-        }
-    }
+    for (int o = 16; o > 0; o >>= 1) in += __shfl_xor_sync(0xffffffffu, in, o);
+    if (lane == 0) red[warp] = in;
+    scale(y, __expf(ce - c_lo), __expf(ce - c_hi));
     row_dot(y, Kt, 2);
-    // rows j of B1^T and B2^T (columns i >= j): y += B1^T Q - B2^T K
-    {
-        float b1[8][4], b2[8][4];
 #pragma unroll
-        for (int n = 0; n < 8; ++n)
+    for (int k4 = 0; k4 < 4; ++k4) {
+        if (!upper(k4)) continue;
+        uint32_t f[4];
+        weigh_cols(f, b, k4, true, 1.f);
+        times_tokens(y, f, Qt, k4);
+    }
+    zero(b);
+    pairs(b, Et, Wt, upper);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) b1[n][e] = b2[n][e] = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            uint32_t ae[4];
-            ldsm4(ae, smem_addr(Et) + tile_off<ROW>(ar, 2 * ks + ac));
-#pragma unroll
-            for (int n2 = 0; n2 < 4; ++n2) {
-                if (n2 < (warp & 3)) continue;
-                uint32_t b[4];
-                ldsm4(b, smem_addr(Pt) + tile_off<ROW>(16 * n2 + br, 2 * ks + bc));
-                mma16816(b1[2 * n2], ae, b[0], b[1]);
-                mma16816(b1[2 * n2 + 1], ae, b[2], b[3]);
-                ldsm4(b, smem_addr(Wt) + tile_off<ROW>(16 * n2 + br, 2 * ks + bc));
-                mma16816(b2[2 * n2], ae, b[0], b[1]);
-                mma16816(b2[2 * n2 + 1], ae, b[2], b[3]);
-            }
-        }
-#pragma unroll
-        for (int k4 = 0; k4 < 4; ++k4) {
-            if (k4 < (warp & 3)) continue;
-            uint32_t f1[4], f2[4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int n = 2 * k4 + h;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = m0 + g + 8 * (e >> 1), i = 8 * n + 2 * c + (e & 1);
-                    const float f = i >= j ? expf(cum[i] - (e >> 1 ? c_hi : c_lo)) : 0.f;
-                    b1[n][e] *= f;
-                    b2[n][e] *= i > j ? -f : 0.f;
-                }
-                f1[2 * h] = pack2(b1[n][0], b1[n][1]);
-                f1[2 * h + 1] = pack2(b1[n][2], b1[n][3]);
-                f2[2 * h] = pack2(b2[n][0], b2[n][1]);
-                f2[2 * h + 1] = pack2(b2[n][2], b2[n][3]);
-            }
-#pragma unroll
-            for (int n2 = 0; n2 < HN / 2; ++n2) {
-                uint32_t b[4];
-                ldsm4t(b, smem_addr(Qt) + tile_off<ROW>(16 * k4 + tr, d0 / 8 + 2 * n2 + tc));
-                mma16816(y[2 * n2], f1, b[0], b[1]);
-                mma16816(y[2 * n2 + 1], f1, b[2], b[3]);
-                ldsm4t(b, smem_addr(Kt) + tile_off<ROW>(16 * k4 + tr, d0 / 8 + 2 * n2 + tc));
-                mma16816(y[2 * n2], f2, b[0], b[1]);
-                mma16816(y[2 * n2 + 1], f2, b[2], b[3]);
-            }
-        }
+    for (int k4 = 0; k4 < 4; ++k4) {
+        if (!upper(k4)) continue;
+        uint32_t f[4];
+        weigh_cols(f, b, k4, false, -1.f);
+        times_tokens(y, f, Kt, k4);
     }
     row_dot(y, Kt, 0);
     {
@@ -1132,7 +1155,7 @@ __global__ void __launch_bounds__(kGradThreads, D == 128 ? 1 : 2) delta_grads_tc
             y[n][3] = fmaf(be1, y[n][3], -z[n][3]);
         }
     }
-    __syncthreads();  // the tiles have been read
+    __syncthreads();  // the tiles have been read, the sums are there
     if (a.pw) {  // the pooled keys' share: rho after the chunk + sum over the chunk's tokens t >= j of pw_t u_t
         for (int e = tid; e < kCH * PIECES; e += kGradThreads) {
             const int r = e / PIECES, pc = e % PIECES;
@@ -1143,7 +1166,7 @@ __global__ void __launch_bounds__(kGradThreads, D == 128 ? 1 : 2) delta_grads_tc
         __syncthreads();
 #pragma unroll
         for (int k4 = 0; k4 < 4; ++k4) {
-            if (k4 < (warp & 3)) continue;
+            if (!upper(k4)) continue;
             uint32_t fh[4], fl[4];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -1152,15 +1175,8 @@ __global__ void __launch_bounds__(kGradThreads, D == 128 ? 1 : 2) delta_grads_tc
                     const int j = m0 + g + 8 * x, t = 8 * (2 * k4 + h) + 2 * c;
                     split2(t >= j ? pw[t] : 0.f, t + 1 >= j ? pw[t + 1] : 0.f, fh[2 * h + x], fl[2 * h + x]);
                 }
-#pragma unroll
-            for (int n2 = 0; n2 < HN / 2; ++n2) {
-                uint32_t b[4];
-                ldsm4t(b, smem_addr(Et) + tile_off<ROW>(16 * k4 + tr, d0 / 8 + 2 * n2 + tc));
-                mma16816(y[2 * n2], fh, b[0], b[1]);
-                mma16816(y[2 * n2 + 1], fh, b[2], b[3]);
-                mma16816(y[2 * n2], fl, b[0], b[1]);
-                mma16816(y[2 * n2 + 1], fl, b[2], b[3]);
-            }
+            times_tokens(y, fh, Et, k4);
+            times_tokens(y, fl, Et, k4);
         }
         const float *rho = a.rho + (size_t)blockIdx.x * D + d0 + 2 * c;
 #pragma unroll
@@ -1169,36 +1185,7 @@ __global__ void __launch_bounds__(kGradThreads, D == 128 ? 1 : 2) delta_grads_tc
             y[n][0] += x.x; y[n][1] += x.y; y[n][2] += x.x; y[n][3] += x.y;
         }
     }
-    if (a.dq_add) {
-#pragma unroll
-        for (int n = 0; n < HN; ++n)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int t = m0 + g + 8 * x;
-                if (t >= w.cnt) continue;
-                const float2 f = *reinterpret_cast<const float2 *>(a.dq_add + (row0 + t) * D + d0 + 8 * n + 2 * c);
-                dq[n][2 * x] += f.x;
-                dq[n][2 * x + 1] += f.y;
-            }
-    }
-    // out through this warp's own part of two tiles
-#pragma unroll
-    for (int n = 0; n < HN; n += 2) {
-        const uint32_t o = tile_off<ROW>(m0 + (lane & 15), d0 / 8 + n + (lane >> 4));
-        stsm4(smem_addr(Qt) + o, pack2(dq[n][0], dq[n][1]), pack2(dq[n][2], dq[n][3]), pack2(dq[n + 1][0], dq[n + 1][1]),
-              pack2(dq[n + 1][2], dq[n + 1][3]));
-        stsm4(smem_addr(Kt) + o, pack2(y[n][0], y[n][1]), pack2(y[n][2], y[n][3]), pack2(y[n + 1][0], y[n + 1][1]),
-              pack2(y[n + 1][2], y[n + 1][3]));
-    }
-    __syncwarp();
-#pragma unroll
-    for (int x = 0; x < 16 * (HD / 8) / 32; ++x) {
-        const int e = x * 32 + lane, r = m0 + e / (HD / 8), pc = d0 / 8 + e % (HD / 8);
-        if (r < w.cnt) {
-            *reinterpret_cast<uint4 *>(a.dq + (row0 + r) * D + pc * 8) = *reinterpret_cast<const uint4 *>(Qt + tile_off<ROW>(r, pc));
-            *reinterpret_cast<uint4 *>(a.dk + (row0 + r) * D + pc * 8) = *reinterpret_cast<const uint4 *>(Kt + tile_off<ROW>(r, pc));
-        }
-    }
+    store(a.dk, y);
     if (warp == 0) {
         // dbeta, and h_t = <adjoint, memory> before token t: exp(c_end) <R, S>, the reads of S by tokens i >= t, the
         // writes of tokens j < t into R, and the pairs F_ij on either side of t.  As a running sum from the end every
@@ -1227,7 +1214,7 @@ __global__ void __launch_bounds__(kGradThreads, D == 128 ? 1 : 2) delta_grads_tc
             const float n = __shfl_down_sync(0xffffffffu, s, o);
             if (lane + o < 32) s += n;
         }
-        const float end = expf(ce) * in + fr;
+        const float end = __expf(ce) * in + fr;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             if (i + x >= w.cnt) continue;
@@ -1295,11 +1282,11 @@ __global__ void __launch_bounds__(256) delta_dgon(const __nv_bfloat16 *dy, const
 template <int D, bool READ, bool REV>
 cudaError_t prep_impl(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
 {
-    const size_t smem = (READ || REV ? 2 : 1) * kCH * D * 2 + 3 * sizeof(float) * kCH * kAP;
+    constexpr int smem = prep_smem<D, READ || REV>();
     auto kern = delta_prep_tc<D, READ, REV>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)((long long)p.BH * p.N * a.NCH), kPrepThreads, smem, s>>>(a);
+    kern<<<(unsigned)((long long)p.BH * p.N * a.NCH), 32, smem, s>>>(a);
     return cudaGetLastError();
 }
 

@@ -51,6 +51,14 @@ __device__ __forceinline__ void stsm4(uint32_t addr, uint32_t r0, uint32_t r1, u
                  : "memory");
 }
 
+// The transpose of an 8 x 8 matrix of 16-bit values held as an accumulator tile in bf16 (row g, columns 2c, 2c + 1).
+__device__ __forceinline__ uint32_t movm_t(uint32_t x)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
 // Copy 16 bytes to shared memory, or write zeros where `ok` is false (src is then not read).
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool ok)
 {
