@@ -13,6 +13,7 @@ q, k, v, u are CUDA tensors [B, H, L, d] (bf16 -> ``mc_forward``; fp32 ->
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -108,13 +109,21 @@ def num_segments(L: int, seg_len: int) -> int:
     return (L + seg_len - 1) // seg_len
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle alone, without a Stream object
+
+
 def _stream_handle(stream, device) -> int:
     if stream is None:
+        if _raw_stream is not None and device.index is not None:
+            return _raw_stream(device.index)
         stream = torch.cuda.current_stream(device)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _check(t, name, dtype, shape=None, device=None):
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_contiguous() and (shape is None or t.shape == shape)
+            and (device is None or t.device == device)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype != dtype:
@@ -324,16 +333,17 @@ def _ptr(t):
 
 def _sequence_args(q, named, dims):
     """Check that q has ``dims`` dimensions and a supported dtype and that the ``named`` tensors
-    (name, tensor, shape or None for q's) match it; returns (shape, device, dtype)."""
+    (name, tensor) match it; returns (shape, device, dtype)."""
     if not isinstance(q, torch.Tensor) or q.dim() != dims:
         raise ValueError("q must be [B, H, L, d]" if dims == 4 else "q must be [B, H, d]")
     if q.device.type != "cuda":
         raise ValueError("inputs must be CUDA tensors")
     if q.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("inputs must be bf16 or fp32")
-    for name, t, shape in named:
-        _check(t, name, q.dtype, q.shape if shape is None else shape, q.device)
-    return q.shape, q.device, q.dtype
+    shape, dev, dtype = q.shape, q.device, q.dtype
+    for name, t in named:
+        _check(t, name, dtype, shape, dev)
+    return shape, dev, dtype
 
 
 def _new(t, name, dtype, shape, dev):
@@ -342,9 +352,12 @@ def _new(t, name, dtype, shape, dev):
     return t
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(device):
     """The library works on the current device: make it the tensors'."""
-    return torch.cuda.device(device)
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def mc_forward_delta(q, k, v, u, log_alpha, beta, seg_len: int, agg_mode: int, topk: int = 0, *, y=None, states=None,
@@ -353,7 +366,7 @@ def mc_forward_delta(q, k, v, u, log_alpha, beta, seg_len: int, agg_mode: int, t
     and beta [B, H, L] of the same dtype.  u may be None for Residual and Mean, and when one segment
     covers the sequence with one of these.  Returns (y, states); states is None when ``want_states`` is
     False and none was given."""
-    (B, H, L, d), dev, dtype = _sequence_args(q, [("q", q, None), ("k", k, None), ("v", v, None)], 4)
+    (B, H, L, d), dev, dtype = _sequence_args(q, [("q", q), ("k", k), ("v", v)], 4)
     if u is not None:
         _check(u, "u", dtype, q.shape, dev)
     _check(log_alpha, "log_alpha", dtype, (B, H, L), dev)
@@ -378,7 +391,7 @@ def mc_backward_delta(q, k, v, u, log_alpha, beta, dy, seg_len: int, agg_mode: i
     (``mc_backward_delta`` in mc.h).  du is None for Residual and Mean unless a buffer is given (then it
     is zeroed)."""
     (B, H, L, d), dev, dtype = _sequence_args(
-        q, [("q", q, None), ("k", k, None), ("v", v, None), ("dy", dy, None)], 4)
+        q, [("q", q), ("k", k), ("v", v), ("dy", dy)], 4)
     if u is not None:
         _check(u, "u", dtype, q.shape, dev)
     _check(log_alpha, "log_alpha", dtype, (B, H, L), dev)
@@ -436,31 +449,38 @@ class EvictingCache(DecodeCache):
         """Take over another cache's contents and position (to go on from one prompt several times)."""
         if (other.seg_len, other.n_max, other.protect) != (self.seg_len, self.n_max, self.protect):
             raise ValueError("the caches differ in seg_len, n_max or protect")
-        for name in ("states", "kbar", "online", "ksum", "mass", "slot_seg"):
-            getattr(self, name).copy_(getattr(other, name))
+        names = ("states", "kbar", "online", "ksum", "mass", "slot_seg")
+        torch._foreach_copy_([getattr(self, n) for n in names], [getattr(other, n) for n in names])
         self.t = other.t
         return self
 
 
 def _cache_args(cache, B, H, d, dev):
-    n = cache.n_max
-    f32 = [("states", (B, H, n, d, d)), ("kbar", (B, H, n, d)), ("online", (B, H, d, d)), ("ksum", (B, H, d))]
+    n, f32 = cache.n_max, torch.float32
+    _check(cache.states, "states", f32, (B, H, n, d, d), dev)
+    _check(cache.kbar, "kbar", f32, (B, H, n, d), dev)
+    _check(cache.online, "online", f32, (B, H, d, d), dev)
+    _check(cache.ksum, "ksum", f32, (B, H, d), dev)
     if isinstance(cache, EvictingCache):
-        f32.append(("mass", (B, H, n)))
+        _check(cache.mass, "mass", f32, (B, H, n), dev)
         _check(cache.slot_seg, "slot_seg", torch.int32, (B, H, n), dev)
-    for name, shape in f32:
-        _check(getattr(cache, name), name, torch.float32, shape, dev)
 
 
 def _token_args(cache, q, k, v, u, log_alpha, beta, y):
-    (B, H, d), dev, dtype = _sequence_args(q, [("q", q, None), ("k", k, None), ("v", v, None)], 3)
+    shape, dev, dtype = _sequence_args(q, (("q", q), ("k", k), ("v", v)), 3)
+    B, H, d = shape
     if u is not None:
-        _check(u, "u", dtype, (B, H, d), dev)
-    for t, n in ((log_alpha, "log_alpha"), (beta, "beta")):
-        if t is not None:
-            _check(t, n, dtype, (B, H), dev)
+        _check(u, "u", dtype, shape, dev)
+    if log_alpha is not None:
+        _check(log_alpha, "log_alpha", dtype, (B, H), dev)
+    if beta is not None:
+        _check(beta, "beta", dtype, (B, H), dev)
     _cache_args(cache, B, H, d, dev)
-    return B, H, d, dev, _new(y, "y", dtype, (B, H, d), dev)
+    if y is None:
+        y = torch.empty_like(q)
+    else:
+        _check(y, "y", dtype, shape, dev)
+    return B, H, d, dev, y
 
 
 def mc_decode_step_delta(cache: DecodeCache, q, k, v, u, log_alpha, beta, agg_mode: int, topk: int = 0, *, y=None,
@@ -505,7 +525,7 @@ def mc_cache_compact(cache: EvictingCache, k, u, states, agg_mode: int, topk: in
     segment of the prefill, [B, H, N]."""
     if not isinstance(cache, EvictingCache):
         raise TypeError("cache must be an EvictingCache")
-    (B, H, L, d), dev, dtype = _sequence_args(k, [("k", k, None), ("u", u, None)], 4)
+    (B, H, L, d), dev, dtype = _sequence_args(k, [("k", k), ("u", u)], 4)
     N = num_segments(L, cache.seg_len)
     _check(states, "states", torch.float32, (B, H, N, d, d), dev)
     _cache_args(cache, B, H, d, dev)

@@ -27,7 +27,7 @@ constexpr int kMThreads = 256;
 template <typename T, int D>
 __global__ void __launch_bounds__(kMThreads) gate_mass_simt(CompactArgs a)
 {
-    constexpr int P = D + 1;
+    constexpr int P = D + 4;  // rows stay 16-byte aligned; eight rows apart by 4 words touch every bank
     extern __shared__ float sm[];
     float *Us = sm;               // kMT x P
     float *Kb = Us + kMT * P;     // kMS x P
@@ -52,13 +52,36 @@ __global__ void __launch_bounds__(kMThreads) gate_mass_simt(CompactArgs a)
         zs[tid] = 1.f;
         nsel[tid] = 0;
     }
+    // Four tokens (tx + 16 x) by four segments (ty + 16 y) per thread, each score in gate_score's order of sums, so that
+    // the router ranks as everywhere else.  Columns past the last segment that the tile reads are left out.
     auto scores = [&](int s0) {
         __syncthreads();
         for (int e = tid; e < kMS * D; e += kMThreads)
             Kb[(e / D) * P + e % D] = s0 + e / D < smax ? kbar[(size_t)s0 * D + e] : 0.f;
         __syncthreads();
-        for (int e = tid; e < kMT * kMS; e += kMThreads)
-            Sc[(e / kMS) * (kMS + 1) + e % kMS] = gate_score(Us + (e / kMS) * P, Kb + (e % kMS) * P, D);
+        const int tx = tid % 16, ty = tid / 16;
+#pragma unroll 1
+        for (int y = 0; y < 4; ++y) {
+            const int i = ty + 16 * y;
+            if (s0 + 16 * y >= smax) break;
+            float p[4][4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) p[x][0] = p[x][1] = p[x][2] = p[x][3] = 0.f;
+#pragma unroll 4
+            for (int c = 0; c < D; c += 4) {
+                const float4 kv = *reinterpret_cast<const float4 *>(Kb + i * P + c);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float4 uv = *reinterpret_cast<const float4 *>(Us + (tx + 16 * x) * P + c);
+                    p[x][0] = fmaf(uv.x, kv.x, p[x][0]);
+                    p[x][1] = fmaf(uv.y, kv.y, p[x][1]);
+                    p[x][2] = fmaf(uv.z, kv.z, p[x][2]);
+                    p[x][3] = fmaf(uv.w, kv.w, p[x][3]);
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) Sc[(tx + 16 * x) * (kMS + 1) + i] = (p[x][0] + p[x][1]) + (p[x][2] + p[x][3]);
+        }
         __syncthreads();
     };
     for (int s0 = 0; s0 < smax; s0 += kMS) {
@@ -99,19 +122,22 @@ __global__ void __launch_bounds__(kMThreads) gate_mass_simt(CompactArgs a)
         thr[tid] = c > 0 ? vals[c - 1] : FLT_MAX;  // a segment is selected if its score is above the last one's,
         thi[tid] = c > 0 ? seli[(size_t)tid * a.topk + c - 1] : -1;  // or equal with an index up to it
     }
+    __shared__ float part[4][kMS];
     for (int s0 = 0; s0 < smax; s0 += kMS) {
-        scores(s0);
-        if (tid < kMS && s0 + tid < a.N) {
-            const int i = s0 + tid;
-            float sum = 0.f;
-            for (int t = 0; t < cnt; ++t) {
+        if (smax > kMS) scores(s0);  // a single block's scores are still there
+        else __syncthreads();
+        const int q = tid / kMS, i = s0 + tid % kMS;  // a quarter of the tokens
+        float sum = 0.f;
+        if (i < smax)
+            for (int t = q * (kMT / 4); t < min(cnt, (q + 1) * (kMT / 4)); ++t) {
                 if (i >= (tb + t) / a.C) continue;
-                const float r = Sc[t * (kMS + 1) + tid];
+                const float r = Sc[t * (kMS + 1) + tid % kMS];
                 if (ssc && !(r > thr[t] || (r == thr[t] && i <= thi[t]))) continue;
                 sum += expf(r - mx[t]) / zs[t];
             }
-            out[i] = sum;
-        }
+        part[q][tid % kMS] = sum;
+        __syncthreads();
+        if (tid < kMS && s0 + tid < a.N) out[s0 + tid] = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
     }
     for (int i = ((smax + kMS - 1) / kMS) * kMS + tid; i < a.N; i += kMThreads) out[i] = 0.f;
 }
@@ -366,7 +392,7 @@ __global__ void __launch_bounds__(kMThreads) compact_gather(CompactArgs a)
 template <typename T, int D>
 cudaError_t mass_impl(const Problem &p, const CompactArgs &a, cudaStream_t s)
 {
-    const size_t smem = sizeof(float) * ((kMT + kMS) * (D + 1) + kMT * (kMS + 1) + 5 * kMT + 2 * (size_t)kMT * a.topk);
+    const size_t smem = sizeof(float) * ((kMT + kMS) * (D + 4) + kMT * (kMS + 1) + 5 * kMT + 2 * (size_t)kMT * a.topk);
     auto kern = gate_mass_simt<T, D>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;

@@ -40,7 +40,7 @@ __device__ __forceinline__ float dot4(const float4 &a, const float4 &b)
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) decode_slots(SlotArgs a)
+__global__ void __launch_bounds__(kThreads, 5) decode_slots(SlotArgs a)
 {
     constexpr int LPR = D / 4;                   // lanes per row (a 16-byte piece each)
     constexpr int RPW = 32 / LPR;                // rows of a warp at once
@@ -58,6 +58,18 @@ __global__ void __launch_bounds__(kThreads) decode_slots(SlotArgs a)
     __shared__ int gi[kMaxN], ids[kMaxN];
     __shared__ float g_on, red[kRows][kWarps];
     __shared__ int n_list, put;
+
+    // This warp's rows, and its share of the memories where several warps share a row.  Every slot is read in its
+    // order, the first four already while the gates are worked out, unless the router keeps a few only.
+    const int part = SPLIT == 1 ? 0 : (warp * RPW) / kRows;
+    const int rl0 = SPLIT == 1 ? warp * RPW * PASS + lane / LPR : (warp * RPW) % kRows + lane / LPR;
+    const float4 *st = reinterpret_cast<const float4 *>(a.states + ((size_t)bh * a.nmax * D + rb * kRows + rl0) * D) + lane % LPR;
+    const bool all = a.mode != MC_SSC;
+    float4 m4[4];
+    if (all && part + 3 * SPLIT < n) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) m4[y] = __ldcs(st + (size_t)(part + y * SPLIT) * (D * D / 4));
+    }
 
     for (int i = tid; i < D; i += kThreads) {
         const size_t at = (size_t)bh * D + i;
@@ -128,11 +140,14 @@ __global__ void __launch_bounds__(kThreads) decode_slots(SlotArgs a)
         }
         const unsigned b0 = __ballot_sync(0xffffffffu, c0), b1 = __ballot_sync(0xffffffffu, c1);
         const unsigned below = (1u << lane) - 1;
-        if (c0) {
+        if (all) {
+            gv[i0] = c0 ? g0 : 0.f;
+            gv[i1] = c1 ? g1 : 0.f;
+        } else if (c0) {
             gv[__popc(b0 & below)] = g0;
             gi[__popc(b0 & below)] = i0;
         }
-        if (c1) {
+        if (!all && c1) {
             const int at = __popc(b0) + __popc(b1 & below);
             gv[at] = g1;
             gi[at] = i1;
@@ -168,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) decode_slots(SlotArgs a)
         }
         if (lane == 0) {
             g_on = go;
-            n_list = __popc(b0) + __popc(b1);
+            n_list = all ? n : __popc(b0) + __popc(b1);
             put = where;
         }
     }
@@ -176,18 +191,15 @@ __global__ void __launch_bounds__(kThreads) decode_slots(SlotArgs a)
     asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // this CTA has read the head's key sum, key means, masses and slots
 
     // the rows
-    const int part = SPLIT == 1 ? 0 : (warp * RPW) / kRows;  // this warp's share of the memories
     const int nl = n_list;
     const float4 qv = reinterpret_cast<const float4 *>(qs)[lane % LPR];
     const float4 kv = reinterpret_cast<const float4 *>(ks)[lane % LPR];
     const float dec = delta ? delta_decay(to_f(static_cast<const T *>(a.la)[bh])) : 1.f;
     const float bet = delta ? to_f(static_cast<const T *>(a.be)[bh]) : 1.f;
-    const float *st = a.states + (size_t)bh * a.nmax * D * D;
     float4 on[PASS];
 #pragma unroll
     for (int x = 0; x < PASS; ++x) {
-        const int rl = SPLIT == 1 ? warp * RPW * PASS + x * RPW + lane / LPR : (warp * RPW) % kRows + lane / LPR;
-        const int r = rb * kRows + rl;
+        const int rl = rl0 + x * RPW, r = rb * kRows + rl;
         float acc = 0.f;
         if (part == 0) {
             float4 *row = reinterpret_cast<float4 *>(a.online + ((size_t)bh * D + r) * D) + lane % LPR;
@@ -208,16 +220,25 @@ __global__ void __launch_bounds__(kThreads) decode_slots(SlotArgs a)
             on[x] = m;
             acc = g_on * dot4(m, qv);
         }
-        const float4 *src = reinterpret_cast<const float4 *>(st + (size_t)r * D) + lane % LPR;
+        const float4 *src = st + x * RPW * (D / 4);
+        // an empty slot's gate is 0 and its memory anything, so a gate of 0 is not multiplied
+        auto add = [&](int j, const float4 &m) {
+            const float gj = gv[j];
+            if (gj != 0.f) acc = fmaf(gj, dot4(m, qv), acc);
+        };
         int j = part;
-        for (; j + 7 * SPLIT < nl; j += 8 * SPLIT) {  // eight rows in flight
-            float4 m[8];
+        for (; j + 3 * SPLIT < nl; j += 4 * SPLIT) {  // four rows in flight
+            if (!(all && x == 0 && j == part)) {
 #pragma unroll
-            for (int y = 0; y < 8; ++y) m[y] = src[(size_t)gi[j + y * SPLIT] * (D * D / 4)];
+                for (int y = 0; y < 4; ++y) {
+                    const int i = j + y * SPLIT;
+                    m4[y] = __ldcs(src + (size_t)(all ? i : gi[i]) * (D * D / 4));
+                }
+            }
 #pragma unroll
-            for (int y = 0; y < 8; ++y) acc = fmaf(gv[j + y * SPLIT], dot4(m[y], qv), acc);
+            for (int y = 0; y < 4; ++y) add(j + y * SPLIT, m4[y]);
         }
-        for (; j < nl; j += SPLIT) acc = fmaf(gv[j], dot4(src[(size_t)gi[j] * (D * D / 4)], qv), acc);
+        for (; j < nl; j += SPLIT) add(j, __ldcs(src + (size_t)(all ? j : gi[j]) * (D * D / 4)));
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
         if (lane % LPR == 0) red[rl][part] = acc;
@@ -232,8 +253,8 @@ __global__ void __launch_bounds__(kThreads) decode_slots(SlotArgs a)
     if (seg_end && part == 0) {
 #pragma unroll
         for (int x = 0; x < PASS; ++x) {
-            const int rl = SPLIT == 1 ? warp * RPW * PASS + x * RPW + lane / LPR : (warp * RPW) % kRows + lane / LPR;
-            reinterpret_cast<float4 *>(a.states + (((size_t)bh * a.nmax + put) * D + rb * kRows + rl) * D)[lane % LPR] = on[x];
+            const int r = rb * kRows + rl0 + x * RPW;
+            reinterpret_cast<float4 *>(a.states + (((size_t)bh * a.nmax + put) * D + r) * D)[lane % LPR] = on[x];
         }
     }
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");

@@ -104,21 +104,50 @@ __global__ void __launch_bounds__(32 * RowSplit<D>::W) delta_scan_simt(DeltaArgs
     float M[R::KPL], x[R::KPL];
 #pragma unroll
     for (int i = 0; i < R::KPL; ++i) M[i] = 0.f;
+    constexpr int NL = (R::TT * D + NT - 1) / NT, NV = (R::TT * R::RC + NT - 1) / NT;
+    T kn[NL], qn[NL], vn[NV], an, bn;  // the next tile, on its way while this one is worked on
+    auto fetch = [&](int c0) {
+        const int cnt = min(R::TT, t1 - c0);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const int e = tid + i * NT;
+            if (e < cnt * D) {
+                kn[i] = k[(size_t)c0 * D + e];
+                qn[i] = q[(size_t)c0 * D + e];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = tid + i * NT;
+            if (e < cnt * R::RC) vn[i] = v[(size_t)(c0 + e / R::RC) * D + rs * R::RC + e % R::RC];
+        }
+        if (tid < cnt) {
+            an = la[c0 + tid];
+            bn = be[c0 + tid];
+        }
+    };
+    fetch(t0);
     for (int c0 = t0; c0 < t1; c0 += R::TT) {
         const int cnt = min(R::TT, t1 - c0);
         if (a.S_c && (c0 - t0) % kCH == 0)
             store_keys<D>(a.S_c + (((size_t)bh * a.N + seg) * a.NCH + (c0 - t0) / kCH) * D * D + (size_t)row * D, M, g);
         __syncthreads();
-        for (int e = tid; e < cnt * D; e += NT) {
-            Ks[e] = to_f(k[(size_t)c0 * D + e]);
-            Qs[e] = to_f(q[(size_t)c0 * D + e]);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const int e = tid + i * NT;
+            if (e < cnt * D) {
+                Ks[e] = to_f(kn[i]);
+                Qs[e] = to_f(qn[i]);
+            }
         }
-        for (int e = tid; e < cnt * R::RC; e += NT)
-            Vs[e] = to_f(v[(size_t)(c0 + e / R::RC) * D + rs * R::RC + e % R::RC]);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (tid + i * NT < cnt * R::RC) Vs[tid + i * NT] = to_f(vn[i]);
         if (tid < cnt) {
-            As[tid] = delta_decay(to_f(la[c0 + tid]));
-            Bs[tid] = to_f(be[c0 + tid]);
+            As[tid] = delta_decay(to_f(an));
+            Bs[tid] = to_f(bn);
         }
+        if (c0 + R::TT < t1) fetch(c0 + R::TT);
         __syncthreads();
         for (int t = 0; t < cnt; ++t) {
             const float at = As[t];
@@ -167,22 +196,53 @@ __global__ void __launch_bounds__(32 * RowSplit<D>::W) delta_rscan_simt(DeltaArg
         for (int i = 0; i < R::KPL; ++i) N[i] = 0.f;
     }
     const int nt = (t1 - t0 + R::TT - 1) / R::TT;
+    constexpr int NL = (R::TT * D + NT - 1) / NT, NV = (R::TT * R::RC + NT - 1) / NT;
+    T kn[NL], qn[NL], pn[NV], an, bn;
+    float gn = 1.f;
+    auto fetch = [&](int c0) {
+        const int cnt = min(R::TT, t1 - c0);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const int e = tid + i * NT;
+            if (e < cnt * D) {
+                kn[i] = k[(size_t)c0 * D + e];
+                qn[i] = q[(size_t)c0 * D + e];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = tid + i * NT;
+            if (e < cnt * R::RC) pn[i] = dy[(size_t)(c0 + e / R::RC) * D + rs * R::RC + e % R::RC];
+        }
+        if (tid < cnt) {
+            an = la[c0 + tid];
+            bn = be[c0 + tid];
+            if (a.tok) gn = a.tok[(sbase + c0 + tid) * kBwdTokWords + 2];
+        }
+    };
+    fetch(t0 + (nt - 1) * R::TT);
     for (int ti = nt - 1; ti >= 0; --ti) {
         const int c0 = t0 + ti * R::TT, cnt = min(R::TT, t1 - c0);
         if (c0 + cnt == t1 || (c0 + cnt - t0) % kCH == 0)
             store_keys<D>(a.R_c + (((size_t)bh * a.N + seg) * a.NCH + (c0 - t0) / kCH) * D * D + (size_t)row * D, N, g);
         __syncthreads();
-        for (int e = tid; e < cnt * D; e += NT) {
-            Ks[e] = to_f(k[(size_t)c0 * D + e]);
-            Qs[e] = to_f(q[(size_t)c0 * D + e]);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const int e = tid + i * NT;
+            if (e < cnt * D) {
+                Ks[e] = to_f(kn[i]);
+                Qs[e] = to_f(qn[i]);
+            }
         }
-        for (int e = tid; e < cnt * R::RC; e += NT)
-            Ps[e] = to_f(dy[(size_t)(c0 + e / R::RC) * D + rs * R::RC + e % R::RC]);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (tid + i * NT < cnt * R::RC) Ps[tid + i * NT] = to_f(pn[i]);
         if (tid < cnt) {
-            As[tid] = delta_decay(to_f(la[c0 + tid]));
-            Bs[tid] = to_f(be[c0 + tid]);
-            Gs[tid] = a.tok ? a.tok[(sbase + c0 + tid) * kBwdTokWords + 2] : 1.f;
+            As[tid] = delta_decay(to_f(an));
+            Bs[tid] = to_f(bn);
+            Gs[tid] = gn;
         }
+        if (ti > 0) fetch(c0 - R::TT);
         __syncthreads();
         for (int t = cnt - 1; t >= 0; --t) {
             load_keys<D>(qx, Qs + t * D, g);
