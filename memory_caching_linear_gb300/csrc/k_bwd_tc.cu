@@ -16,6 +16,7 @@
 //   by the two gates in shared memory, and one thread issues D_i += (g_i o dy)^T q
 //   for both states, alternating eight 128x128x16 MMAs each, with both operands read
 //   MN-major from shared memory.
+#include <algorithm>
 #include <cstdint>
 
 #include "mc_internal.cuh"
@@ -47,6 +48,8 @@ constexpr size_t kGSmem = kGStages * kGStage + 1024;
 struct GArgs {
     const float *gam;  // [BH][N][L]: g_{t,i} of the cached segments (routed aggregations)
     uint8_t *G;        // [BH][N] x 32 KB: G_i as a bf16 operand image (rows = value dim, as a state image)
+    float *Gf;         // instead: parts x [BH][N][d][d] fp32 summands, each over a share of the later tiles
+    int parts;
     int BH, L, C, N, d, mode, pairs;
 };
 
@@ -69,11 +72,13 @@ __global__ void __launch_bounds__(kGThreads, 2)
     __shared__ int abort_flag;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int pr = (int)blockIdx.x / a.BH, bh = (int)blockIdx.x % a.BH;
+    const int bh = (int)blockIdx.x % a.BH, part = (int)(blockIdx.x / a.BH) % a.parts, pr = (int)(blockIdx.x / a.BH) / a.parts;
     const int i0 = 2 * pr, i1 = 2 * pr + 1;
     const bool two = i1 < a.N - 1;  // segment N-1 has no later tokens
     const int t_begin = (i0 + 1) * a.C;
-    const int ntiles = (a.L - t_begin) / kG2;
+    const int all_tiles = (a.L - t_begin) / kG2;
+    const int lo_tile = (int)((long long)all_tiles * part / a.parts), end_tile = (int)((long long)all_tiles * (part + 1) / a.parts);
+    const int ntiles = end_tile - lo_tile;  // this CTA's, walked from end_tile - 1 down
     const int split = a.C / kG2;  // tiles of segment i1: the second state starts after them
     const bool routed = a.mode == MC_GRM || a.mode == MC_SOUP || a.mode == MC_SSC;
 
@@ -106,7 +111,7 @@ __global__ void __launch_bounds__(kGThreads, 2)
                 const int s = j % kGStages;
                 if (!mbar_wait(&empty[s], ((j / kGStages) & 1) ^ 1, &abort_flag)) break;
                 uint8_t *st = sm + s * kGStage;
-                const int jt = ntiles - 1 - j;  // the tile, from the end
+                const int jt = end_tile - 1 - j;  // the tile, from the end
                 const int row = bh * a.L + t_begin + jt * kG2;
                 const bool g0 = routed, g1 = routed && two && jt >= split;  // gates to bring along
                 mbar_arrive_expect_tx(&full[s], 2 * kG2Tile + (g0 ? 256 : 0) + (g1 ? 256 : 0));
@@ -134,7 +139,7 @@ __global__ void __launch_bounds__(kGThreads, 2)
                 if (!(ok = mbar_wait(&scaled[s], (j / kGStages) & 1, &abort_flag))) break;
                 tc_fence_after();
                 const uint32_t y0 = smem_u32(sm + s * kGStage), q0 = y0 + kG2Tile, y1 = y0 + 2 * kG2Tile;
-                const bool second = two && ntiles - 1 - j >= split;  // segment i1's tiles come last
+                const bool second = two && end_tile - 1 - j >= split;  // segment i1's tiles come last
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {  // 16 tokens per step: 16 rows of 128 bytes; the 64-column halves 8 KB apart
                     const uint64_t bq = make_desc_sw128(q0 + kk * 2048u, kG2Tile / 2, 1024);
@@ -154,7 +159,7 @@ __global__ void __launch_bounds__(kGThreads, 2)
         const int trow = r & 63, h = r >> 6;  // token row of the tile, 64-column panel
         for (int j = 0; j < ntiles; ++j) {
             const int s = j % kGStages;
-            const int jt = ntiles - 1 - j;  // the tile, from the end
+            const int jt = end_tile - 1 - j;  // the tile, from the end
             const bool second = two && jt >= split;
             if (!mbar_wait(&full[s], (j / kGStages) & 1, &abort_flag)) break;
             // the gates came with the tile (routed); Residual 1, Mean 1 / (n(t) + 1)
@@ -190,6 +195,23 @@ __global__ void __launch_bounds__(kGThreads, 2)
         const bool got = mbar_wait(&done, 0, &abort_flag);
         tc_fence_after();
         for (int which = 0; which < (two ? 2 : 1); ++which) {
+            if (a.Gf) {
+                const bool any = ntiles > 0 && (which == 0 || end_tile - 1 >= split);  // the accumulator was written
+                float *dst = a.Gf + ((((size_t)part * a.BH + bh) * a.N + (which ? i1 : i0)) * a.d + r) * a.d;
+                for (int c0 = 0; c0 < a.d; c0 += 32) {
+                    uint32_t x[32];
+                    tmem_ld32(tD + 128 * which + ((uint32_t)(32 * q4) << 16) + c0, x);
+                    tmem_wait_ld();
+                    if (!got || r >= a.d) continue;
+#pragma unroll
+                    for (int q = 0; q < 32; q += 4)
+                        *reinterpret_cast<float4 *>(dst + c0 + q) =
+                            any ? make_float4(__uint_as_float(x[q]), __uint_as_float(x[q + 1]), __uint_as_float(x[q + 2]),
+                                              __uint_as_float(x[q + 3]))
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+                continue;
+            }
             uint8_t *img = a.G + ((size_t)bh * a.N + (which ? i1 : i0)) * kGTile + r * 128;
             for (int c0 = 0; c0 < 128; c0 += 32) {
                 uint32_t x[32];
@@ -994,9 +1016,36 @@ cudaError_t launch_bwd_G_tc(const Problem &p, const void *dy, const void *q, con
     a.G = G;
     a.BH = p.BH; a.L = p.L; a.C = p.C; a.N = p.N; a.d = p.d; a.mode = p.mode;
     a.pairs = p.N / 2;  // pairs of the cached segments 0 .. N-2
+    a.parts = 1;
     cudaError_t e = cudaFuncSetAttribute(bwd_G_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGSmem);
     if (e != cudaSuccess) return e;
     bwd_G_tc<<<(unsigned)(p.BH * a.pairs), kGThreads, kGSmem, s>>>(mY, mQ, a);
+    return cudaGetLastError();
+}
+
+// Two CTAs fit on an SM: enough shares of the tokens that every SM has two.
+int bwd_G_parts(const Problem &p)
+{
+    const int ctas = p.BH * (p.N / 2);
+    return ctas < 1 ? 1 : std::min(8, (304 + ctas - 1) / ctas);
+}
+
+cudaError_t launch_bwd_G_parts_tc(const Problem &p, const void *dy, const void *q, const float *gam, float *G, cudaStream_t s)
+{
+    if (p.N < 2) return cudaSuccess;
+    CUtensorMap mY, mQ;
+    const unsigned long long rows = (unsigned long long)p.BH * p.L;
+    if (!make_tmap_bf16_sw128(&mY, dy, rows, p.d, kG2) || !make_tmap_bf16_sw128(&mQ, q, rows, p.d, kG2))
+        return cudaErrorInvalidValue;
+    GArgs a{};
+    a.gam = gam;
+    a.Gf = G;
+    a.BH = p.BH; a.L = p.L; a.C = p.C; a.N = p.N; a.d = p.d; a.mode = p.mode;
+    a.pairs = p.N / 2;
+    a.parts = bwd_G_parts(p);
+    cudaError_t e = cudaFuncSetAttribute(bwd_G_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGSmem);
+    if (e != cudaSuccess) return e;
+    bwd_G_tc<<<(unsigned)(p.BH * a.pairs * a.parts), kGThreads, kGSmem, s>>>(mY, mQ, a);
     return cudaGetLastError();
 }
 

@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(256, 2) gate_mass_tc(CompactArgs a)
             for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                 for (int n2 = 0; n2 < 4; ++n2) {
+                    if (64 * b + 16 * n2 >= smax) break;
                     uint32_t bf[4];
                     ldsm4(bf, smem_addr(Kt) + (term * PN + ks / 4) * 8192 + tile_off<128>(16 * n2 + br, 2 * (ks & 3) + bc));
                     mma16816(S[2 * n2], au[ks], bf[0], bf[1]);
@@ -220,14 +221,14 @@ __global__ void __launch_bounds__(256, 2) gate_mass_tc(CompactArgs a)
             x0 = fmaxf(x0, fmaxf(S[n][0], S[n][1]));
             x1 = fmaxf(x1, fmaxf(S[n][2], S[n][3]));
         }
-        z0 *= expf(m0 - x0);
-        z1 *= expf(m1 - x1);
+        z0 *= __expf(m0 - x0);
+        z1 *= __expf(m1 - x1);
         m0 = x0;
         m1 = x1;
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
-            z0 += expf(S[n][0] - m0) + expf(S[n][1] - m0);
-            z1 += expf(S[n][2] - m1) + expf(S[n][3] - m1);
+            z0 += __expf(S[n][0] - m0) + __expf(S[n][1] - m0);
+            z1 += __expf(S[n][2] - m1) + __expf(S[n][3] - m1);
         }
     };
     auto join = [&]() {  // the four lanes of a row
@@ -236,8 +237,8 @@ __global__ void __launch_bounds__(256, 2) gate_mass_tc(CompactArgs a)
             const float y0 = __shfl_xor_sync(0xffffffffu, m0, o), y1 = __shfl_xor_sync(0xffffffffu, m1, o);
             const float w0 = __shfl_xor_sync(0xffffffffu, z0, o), w1 = __shfl_xor_sync(0xffffffffu, z1, o);
             const float x0 = fmaxf(m0, y0), x1 = fmaxf(m1, y1);
-            z0 = z0 * expf(m0 - x0) + w0 * expf(y0 - x0);
-            z1 = z1 * expf(m1 - x1) + w1 * expf(y1 - x1);
+            z0 = z0 * __expf(m0 - x0) + w0 * __expf(y0 - x0);
+            z1 = z1 * __expf(m1 - x1) + w1 * __expf(y1 - x1);
             m0 = x0;
             m1 = x1;
         }
@@ -247,8 +248,8 @@ __global__ void __launch_bounds__(256, 2) gate_mass_tc(CompactArgs a)
     auto gates = [&](int b, const float (&S)[8][4]) {  // sums over the tile's tokens
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
-            float s0 = expf(S[n][0] - m0) * z0 + expf(S[n][2] - m1) * z1;
-            float s1 = expf(S[n][1] - m0) * z0 + expf(S[n][3] - m1) * z1;
+            float s0 = __expf(S[n][0] - m0) * z0 + __expf(S[n][2] - m1) * z1;
+            float s1 = __expf(S[n][1] - m0) * z0 + __expf(S[n][3] - m1) * z1;
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) {
                 s0 += __shfl_xor_sync(0xffffffffu, s0, o);

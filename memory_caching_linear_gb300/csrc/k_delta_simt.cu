@@ -23,6 +23,7 @@
 #include <cstdint>
 
 #include "mc_internal.cuh"
+#include "mma_sync.cuh"
 
 namespace mc {
 namespace {
@@ -624,47 +625,58 @@ __global__ void __launch_bounds__(256) pool_score(DeltaArgs a, const float *kpre
 }
 
 // The three passes in one, for many segments: one CTA per (bh, segment) goes through the chunks with the running key
-// sum in shared memory, the next chunk's rows on their way in registers, so k and u come from HBM once.
+// sum in shared memory, so k and u come from HBM once.  A thread copies the pieces that it will read itself, the
+// next chunks' asynchronously (two ahead in bf16, one in fp32), so the copies need no barrier.
+template <typename T, int D>
+constexpr int pool_stages() { return sizeof(T) == 2 ? 3 : 2; }
+template <typename T, int D>
+constexpr int pool_walk_smem(bool score) { return pool_stages<T, D>() * (score ? 2 : 1) * PoolTile<T, D>::TPL * 256 * 16; }
+
 template <typename T, int D, bool SCORE>
 __global__ void __launch_bounds__(256) pool_walk(DeltaArgs a, float *kpre, float *kbar, float *r_on)
 {
     using P = PoolTile<T, D>;
+    constexpr int NS = pool_stages<T, D>(), OPS = SCORE ? 2 : 1;
+    extern __shared__ __align__(16) uint8_t fifo[];
     __shared__ float part[2][P::TL * (D + 1)];
     __shared__ float run[2][D];
     const int seg = (int)blockIdx.x % a.N, bh = (int)blockIdx.x / a.N;
     const int t0 = seg * a.C, len = min((seg + 1) * a.C, a.L) - t0, nch = (len + kCH - 1) / kCH;
     const int tid = threadIdx.x, pc = tid % P::PC, tl = tid / P::PC;
     const size_t row0 = (size_t)bh * a.L + t0;
-    const T *k = static_cast<const T *>(a.k), *u = static_cast<const T *>(a.u);
+    const T *k = static_cast<const T *>(a.k) + row0 * D + pc * P::V, *u = SCORE ? static_cast<const T *>(a.u) + row0 * D + pc * P::V : nullptr;
     const bool scored = SCORE && seg > 0;  // the first segment's gate is 1 whatever its score
-    uint4 kq[P::TPL], uq[P::TPL];
+    auto slot = [&](int ch, int op, int j) { return fifo + ((((ch % NS) * OPS + op) * P::TPL + j) * 256 + tid) * 16; };
     auto load = [&](int ch) {
+        if (ch < nch && tid < P::NT) {
 #pragma unroll
-        for (int j = 0; j < P::TPL; ++j) {
-            const int t = ch * kCH + tl * P::TPL + j;
-            const bool ok = tid < P::NT && t < len;
-            kq[j] = ok ? *reinterpret_cast<const uint4 *>(k + (row0 + t) * D + pc * P::V) : make_uint4(0u, 0u, 0u, 0u);
-            if (scored) uq[j] = ok ? *reinterpret_cast<const uint4 *>(u + (row0 + t) * D + pc * P::V) : make_uint4(0u, 0u, 0u, 0u);
-        }
-    };
-    if (tid < D) run[0][tid] = 0.f;
-    load(0);
-    for (int ch = 0; ch < nch; ++ch) {
-        float *pt = part[ch & 1];
-        float x[P::TPL][P::V], v[P::TPL][P::V];
-#pragma unroll
-        for (int j = 0; j < P::TPL; ++j) {
-            const T *kt = reinterpret_cast<const T *>(&kq[j]), *ut = reinterpret_cast<const T *>(&uq[j]);
-#pragma unroll
-            for (int i = 0; i < P::V; ++i) {
-                x[j][i] = to_f(kt[i]) + (j > 0 ? x[j > 0 ? j - 1 : 0][i] : 0.f);
-                v[j][i] = scored ? to_f(ut[i]) : 0.f;
+            for (int j = 0; j < P::TPL; ++j) {
+                const int t = ch * kCH + tl * P::TPL + j;
+                mma::cp16(mma::smem_addr(slot(ch, 0, j)), k + (size_t)(t < len ? t : 0) * D, t < len);
+                if (scored) mma::cp16(mma::smem_addr(slot(ch, 1, j)), u + (size_t)(t < len ? t : 0) * D, t < len);
             }
         }
-        if (ch + 1 < nch) load(ch + 1);
-        if (tid < P::NT)
+        mma::cp_commit();
+    };
+    if (tid < D) run[0][tid] = 0.f;
+#pragma unroll
+    for (int ch = 0; ch < NS - 1; ++ch) load(ch);
+    for (int ch = 0; ch < nch; ++ch) {
+        load(ch + NS - 1);
+        mma::cp_wait<NS - 1>();
+        float *pt = part[ch & 1];
+        float x[P::TPL][P::V];
+        if (tid < P::NT) {
+#pragma unroll
+            for (int j = 0; j < P::TPL; ++j) {
+                load_piece<T, P::V>(x[j], reinterpret_cast<const T *>(slot(ch, 0, j)));
+                if (j > 0)
+#pragma unroll
+                    for (int i = 0; i < P::V; ++i) x[j][i] += x[j > 0 ? j - 1 : 0][i];
+            }
 #pragma unroll
             for (int i = 0; i < P::V; ++i) pt[tl * (D + 1) + pc * P::V + i] = x[P::TPL - 1][i];
+        }
         __syncthreads();
         if (tid < D) {
             float s = run[ch & 1][tid];
@@ -680,18 +692,26 @@ __global__ void __launch_bounds__(256) pool_walk(DeltaArgs a, float *kpre, float
         }
         if (!SCORE) continue;
         __syncthreads();
+        float before[P::V];
+        if (tid < P::NT)
+#pragma unroll
+            for (int i = 0; i < P::V; ++i) before[i] = pt[tl * (D + 1) + pc * P::V + i];
 #pragma unroll
         for (int j = 0; j < P::TPL; ++j) {
             const int t = ch * kCH + tl * P::TPL + j;
             float s = 0.f;
-            if (scored && tid < P::NT)
+            if (scored && tid < P::NT) {
+                float v[P::V];
+                load_piece<T, P::V>(v, reinterpret_cast<const T *>(slot(ch, 1, j)));
 #pragma unroll
-                for (int i = 0; i < P::V; ++i) s = fmaf(v[j][i], x[j][i] + pt[tl * (D + 1) + pc * P::V + i], s);
+                for (int i = 0; i < P::V; ++i) s = fmaf(v[i], x[j][i] + before[i], s);
+            }
 #pragma unroll
             for (int o = P::PC / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
             if (pc == 0 && tid < P::NT && t < len) r_on[row0 + t] = s / (float)(t + 1);
         }
     }
+    mma::cp_wait<0>();
 }
 
 template <typename T, int D>
@@ -725,9 +745,12 @@ template <typename T, int D>
 cudaError_t pool_impl(const Problem &p, const DeltaArgs &a, float *sums, float *kbar, float *r_on, cudaStream_t s)
 {
     const unsigned chunks = (unsigned)((long long)p.BH * p.N * a.NCH);
-    if ((long long)p.BH * p.N >= 304) {  // two segments per SM: one pass
-        if (r_on) pool_walk<T, D, true><<<(unsigned)(p.BH * p.N), 256, 0, s>>>(a, sums, kbar, r_on);
-        else pool_walk<T, D, false><<<(unsigned)(p.BH * p.N), 256, 0, s>>>(a, sums, kbar, nullptr);
+    if ((long long)p.BH * p.N >= 152) {  // a segment per SM: one pass
+        auto kern = r_on ? pool_walk<T, D, true> : pool_walk<T, D, false>;
+        const int smem = pool_walk_smem<T, D>(r_on != nullptr);
+        cudaError_t e = set_smem(kern, smem);
+        if (e != cudaSuccess) return e;
+        kern<<<(unsigned)(p.BH * p.N), 256, smem, s>>>(a, sums, kbar, r_on);
         return cudaGetLastError();
     }
     pool_sums<T, D><<<chunks, 256, 0, s>>>(a, static_cast<const T *>(a.k), nullptr, sums);

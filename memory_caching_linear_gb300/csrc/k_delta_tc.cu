@@ -14,10 +14,11 @@
 // short and each is small, and an accumulator in tensor memory would have to be read back, split and
 // written to shared memory between any two of them.
 //
-// Precision: the memory, the errors and T carry fp32 accuracy (every operand that is not an input is
-// split into two bf16 terms, products of two lows left out: 2^-17 of a term); rounding T, R or S to
-// one bf16 would put 2^-9 of the memory into every later error.  P is one bf16 term, since it only
-// reaches the bf16 output.
+// Precision: the memory is held in fp32.  A call that returns the fp32 states (FULL) takes every operand that is
+// not an input as two bf16 terms (products of two lows left out: 2^-17 of a term), which leaves the states 4e-6
+// off; one term would put 2^-9 of the memory into every later error.  Where only bf16 results come out (y alone, the
+// gradients) one term each is enough: errors against 64 bits grow from 3.2e-3 to 3.5e-3 of y and from 4.0e-3 to
+// 4.1e-3 of the worst gradient, and the walk takes 0.35 instead of 0.46 ms at the long workload.
 #include <cstdint>
 
 #include "mc_internal.cuh"
@@ -348,7 +349,7 @@ struct WalkSmem {
     static constexpr int kTotal = 2 * kStage;
 };
 
-template <int D, int NW, bool READ>
+template <int D, int NW, bool READ, bool FULL>
 __global__ void __launch_bounds__(32 * NW, NW == 4 ? (READ ? 2 : 3) : 1) delta_walk_tc(DeltaTcArgs a)
 {
     using W = WalkSmem<D, NW, READ>;
@@ -422,8 +423,10 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? (READ ? 2 : 3) : 1) delta_w
                 ldsm4(b, kt + tile_off<ROW>(16 * n2 + br, 2 * ks + bc));
                 mma16816(X[2 * n2], hi, b[0], b[1]);
                 mma16816(X[2 * n2 + 1], hi, b[2], b[3]);
-                mma16816(X[2 * n2], lo, b[0], b[1]);
-                mma16816(X[2 * n2 + 1], lo, b[2], b[3]);
+                if (FULL) {
+                    mma16816(X[2 * n2], lo, b[0], b[1]);
+                    mma16816(X[2 * n2 + 1], lo, b[2], b[3]);
+                }
                 if (READ) {  // the output is bf16: one term
                     ldsm4(b, qt + tile_off<ROW>(16 * n2 + br, 2 * ks + bc));
                     mma16816(O[2 * n2], hi, b[0], b[1]);
@@ -484,8 +487,10 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? (READ ? 2 : 3) : 1) delta_w
                 for (int n = 2 * k4; n < 8; ++n) {
                     const uint4 b = tt[(tile_base(n) + k4) * 32];
                     mma16816(X[n], rh[k4], b.x, b.y);
-                    mma16816(X[n], rl[k4], b.x, b.y);
-                    mma16816(X[n], rh[k4], b.z, b.w);
+                    if (FULL) {
+                        mma16816(X[n], rl[k4], b.x, b.y);
+                        mma16816(X[n], rh[k4], b.z, b.w);
+                    }
                 }
         }
         // U = diag(beta) E for the read and the readout; U' = diag(beta exp(c_end - c)) E for the memory
@@ -558,8 +563,10 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? (READ ? 2 : 3) : 1) delta_w
                 ldsm4t(b, kt + tile_off<ROW>(16 * k4 + tr, 2 * n2 + tc));
                 mma16816(S[2 * n2], uh[k4], b[0], b[1]);
                 mma16816(S[2 * n2 + 1], uh[k4], b[2], b[3]);
-                mma16816(S[2 * n2], ul[k4], b[0], b[1]);
-                mma16816(S[2 * n2 + 1], ul[k4], b[2], b[3]);
+                if (FULL) {
+                    mma16816(S[2 * n2], ul[k4], b[0], b[1]);
+                    mma16816(S[2 * n2 + 1], ul[k4], b[2], b[3]);
+                }
             }
     }
     if (a.states_img) {
@@ -583,7 +590,7 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? (READ ? 2 : 3) : 1) delta_w
 // with p_i = g_i dy_i and R the adjoint after the chunk:
 //   X   = diag(exp(c_end - c)) K R^T + P^T p,   W = T^T diag(beta) X            (dv = W)
 //   R' = exp(c_end) R + sum_i exp(c_i) (p_i q_i^T - w_i k_i^T)
-// R itself enters the products in two bf16 terms, the rest in one: the results are bf16 gradients.
+// R is held in fp32 and enters the products in one bf16 term, as all the rest: the results are bf16 gradients.
 // ---------------------------------------------------------------------------
 template <int D, int NW>
 struct RWalkSmem {
@@ -629,22 +636,17 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1) delta_rwalk_tc(Delta
     };
 
     float R[2 * KS][4];
-    if (a.G_img && seg < a.N - 1) {  // 128 x 128 image: two panels of 128 rows
-        const uint8_t *img = a.G_img + (size_t)sid * 32768;
-        const int r = vbase + 16 * warp + g;
+    if (a.G && seg < a.N - 1) {  // partial sums, in order
 #pragma unroll
-        for (int n = 0; n < 2 * KS; ++n) {
-            const uint8_t *at = img + (n / 8) * 16384 + r * 128 + (((n & 7) ^ (r & 7)) << 4) + 4 * c;
-            const uint32_t x = *reinterpret_cast<const uint32_t *>(at), y = *reinterpret_cast<const uint32_t *>(at + 8 * 128);
-            R[n][0] = low_f(x); R[n][1] = high_f(x); R[n][2] = low_f(y); R[n][3] = high_f(y);
-        }
-    } else if (a.G && seg < a.N - 1) {
-        const float *src = a.G + ((size_t)sid * D + vbase + 16 * warp) * D;
+        for (int n = 0; n < 2 * KS; ++n) R[n][0] = R[n][1] = R[n][2] = R[n][3] = 0.f;
+        for (int part = 0; part < a.g_parts; ++part) {
+            const float *src = a.G + (((size_t)part * a.BH * a.N + sid) * D + vbase + 16 * warp) * D;
 #pragma unroll
-        for (int n = 0; n < 2 * KS; ++n) {
-            const float2 x = *reinterpret_cast<const float2 *>(src + (size_t)g * D + 8 * n + 2 * c);
-            const float2 y = *reinterpret_cast<const float2 *>(src + (size_t)(g + 8) * D + 8 * n + 2 * c);
-            R[n][0] = x.x; R[n][1] = x.y; R[n][2] = y.x; R[n][3] = y.y;
+            for (int n = 0; n < 2 * KS; ++n) {
+                const float2 x = *reinterpret_cast<const float2 *>(src + (size_t)g * D + 8 * n + 2 * c);
+                const float2 y = *reinterpret_cast<const float2 *>(src + (size_t)(g + 8) * D + 8 * n + 2 * c);
+                R[n][0] += x.x; R[n][1] += x.y; R[n][2] += y.x; R[n][3] += y.y;
+            }
         }
     } else {
 #pragma unroll
@@ -673,19 +675,14 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1) delta_rwalk_tc(Delta
         const int br = (lane >> 4) * 8 + (lane & 7), bc = (lane >> 3) & 1;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-            uint32_t hi[4], lo[4];
-            split2(R[2 * ks][0], R[2 * ks][1], hi[0], lo[0]);
-            split2(R[2 * ks][2], R[2 * ks][3], hi[1], lo[1]);
-            split2(R[2 * ks + 1][0], R[2 * ks + 1][1], hi[2], lo[2]);
-            split2(R[2 * ks + 1][2], R[2 * ks + 1][3], hi[3], lo[3]);
+            const uint32_t rf[4] = {pack2(R[2 * ks][0], R[2 * ks][1]), pack2(R[2 * ks][2], R[2 * ks][3]),
+                                    pack2(R[2 * ks + 1][0], R[2 * ks + 1][1]), pack2(R[2 * ks + 1][2], R[2 * ks + 1][3])};
 #pragma unroll
             for (int n2 = 0; n2 < 4; ++n2) {
                 uint32_t b[4];
                 ldsm4(b, kt + tile_off<ROW>(16 * n2 + br, 2 * ks + bc));
-                mma16816(X[2 * n2], hi, b[0], b[1]);
-                mma16816(X[2 * n2 + 1], hi, b[2], b[3]);
-                mma16816(X[2 * n2], lo, b[0], b[1]);
-                mma16816(X[2 * n2 + 1], lo, b[2], b[3]);
+                mma16816(X[2 * n2], rf, b[0], b[1]);
+                mma16816(X[2 * n2 + 1], rf, b[2], b[3]);
             }
         }
         uint32_t pf[4][4], pg[4][4];  // p, and exp(c) p
@@ -784,10 +781,11 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1) delta_rwalk_tc(Delta
 
 // ---------------------------------------------------------------------------
 // delta_grads_tc: one CTA per chunk, everything that sums over value rows (k_delta_simt.cu's header).
-// Eight warps: warp % 4 takes 16 tokens, warp / 4 half of the dimensions.  B1, B2 and their transposes
-// are formed by each warp for its own tokens straight into operand registers.  A chunk is a chain of loads and
-// small products, so two CTAs share an SM: S and R come through one 16 KB buffer (64 rows at a time, the next
-// ones on their way under the products between), and at most three of the five 16 x 64 results are held at once.
+// Eight warps: warp % 4 takes 16 tokens, warp / 4 half of the dimensions.  The warps of one half form B1, those of the
+// other B2 (16 rows each), and leave them in shared memory as 16 x 16 blocks of the lower triangle, from which both
+// read them as they lie (with beta_j) and transposed.  A chunk is a chain of loads and small products, so two CTAs
+// share an SM: S and R come through one 16 KB buffer (64 rows at a time, the next ones on their way under the
+// products between), and at most three of the 16 x 64 results are held at once.
 // ---------------------------------------------------------------------------
 constexpr int kGradThreads = 256;
 
@@ -796,7 +794,8 @@ struct GradSmem {
     static constexpr int kT = kCH * D * 2;   // a 64-token tile
     static constexpr int kM = 64 * D * 2;    // 64 rows of S or R
     static constexpr int kVec = 4 * (22 * kCH + 16);
-    static constexpr int kTotal = 5 * kT + kM + kVec;
+    static constexpr int kB = 2 * 10 * 512;  // B1 and B2: ten 16 x 16 blocks each
+    static constexpr int kTotal = 5 * kT + kM + kB + kVec;
 };
 
 template <int D>
@@ -807,7 +806,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
     constexpr int MB = D / 64;                                                         // blocks of S and R
     extern __shared__ __align__(16) uint8_t sm[];
     uint8_t *Qt = sm, *Kt = Qt + G::kT, *Pt = Kt + G::kT, *Et = Pt + G::kT, *Wt = Et + G::kT, *Mt = Wt + G::kT;
-    float *cum = reinterpret_cast<float *>(Mt + G::kM), *bet = cum + kCH, *gs = bet + kCH, *pw = gs + kCH;
+    uint8_t *Bt = Mt + G::kM;
+    float *cum = reinterpret_cast<float *>(Bt + G::kB), *bet = cum + kCH, *gs = bet + kCH, *pw = gs + kCH;
     float *rowsum = pw + kCH;                      // [4][2][64] by half: Y.k, exp(c) p S q, D R e k, exp(c) w S k
     float *rowf = rowsum + 8 * kCH, *colf = rowf + 2 * kCH;  // [2][64], [2][4][64]: sums of F over its rows, columns
     float *red = colf + 8 * kCH;
@@ -900,15 +900,15 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
             }
         }
     };
-    // the warp's 16 rows of `rows` against the 64 tokens of `cols`; 16 x 16 blocks n2 with `want`
-    auto pairs = [&](float (&x)[8][4], const uint8_t *rows, const uint8_t *cols, auto want) {
+    // the warp's 16 rows of `rows` against the tokens of `cols` up to them
+    auto pairs = [&](float (&x)[8][4], const uint8_t *rows, const uint8_t *cols) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             uint32_t af[4];
             ldsm4(af, smem_addr(rows) + tile_off<ROW>(ar, 2 * ks + ac));
 #pragma unroll
             for (int n2 = 0; n2 < 4; ++n2) {
-                if (!want(n2)) continue;
+                if (n2 > wm) continue;
                 uint32_t bf[4];
                 ldsm4(bf, smem_addr(cols) + tile_off<ROW>(16 * n2 + br, 2 * ks + bc));
                 mma16816(x[2 * n2], af, bf[0], bf[1]);
@@ -996,32 +996,43 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
             rowf[half * kCH + m0 + g + 8] = f1;
         }
     };
-    // a block of weighted pairs as an operand: rows i, columns j <= i (j < i) with beta_j, or transposed (rows j,
-    // columns i >= j, i > j) without
-    auto weigh_rows = [&](uint32_t (&f)[4], const float (&b)[8][4], int k4, bool diag) {
+    // Block (r, q) of B1 (which = 0) or B2: 16 rows of 32 bytes, their two pieces exchanged every four rows.
+    auto block = [&](int which, int r, int q) { return smem_addr(Bt) + (which * 10 + r * (r + 1) / 2 + q) * 512; };
+    auto block_off = [](int r, int pc) { return (uint32_t)(r * 32 + ((pc ^ ((r >> 2) & 1)) << 4)); };
+    // this warp's rows, weighted with D_ij, into their blocks
+    auto put_blocks = [&](const float (&x)[8][4]) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float v[4];
+        for (int k4 = 0; k4 < 4; ++k4) {
+            if (k4 > wm) continue;
+            uint32_t f[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = m0 + g + 8 * (e >> 1), j = 16 * k4 + 8 * h + 2 * c + (e & 1);
-                v[e] = j < i || (diag && j == i) ? b[2 * k4 + h][e] * __expf((e >> 1 ? c_hi : c_lo) - cum[j]) * bet[j] : 0.f;
+            for (int h = 0; h < 2; ++h) {
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = m0 + g + 8 * (e >> 1), j = 16 * k4 + 8 * h + 2 * c + (e & 1);
+                    v[e] = j < i || (half == 0 && j == i) ? x[2 * k4 + h][e] * __expf((e >> 1 ? c_hi : c_lo) - cum[j]) : 0.f;
+                }
+                f[2 * h] = pack2(v[0], v[1]);
+                f[2 * h + 1] = pack2(v[2], v[3]);
             }
-            f[2 * h] = pack2(v[0], v[1]);
-            f[2 * h + 1] = pack2(v[2], v[3]);
+            stsm4(block(half, wm, k4) + block_off(lane & 15, lane >> 4), f[0], f[1], f[2], f[3]);
         }
     };
-    auto weigh_cols = [&](uint32_t (&f)[4], const float (&b)[8][4], int k4, bool diag, float sign) {
+    // x += (this warp's rows of B, with beta_j) times the keys
+    auto times_keys = [&](float (&x)[HN][4], int which) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int j = m0 + g + 8 * (e >> 1), i = 16 * k4 + 8 * h + 2 * c + (e & 1);
-                v[e] = i > j || (diag && i == j) ? sign * b[2 * k4 + h][e] * __expf(cum[i] - (e >> 1 ? c_hi : c_lo)) : 0.f;
-            }
-            f[2 * h] = pack2(v[0], v[1]);
-            f[2 * h + 1] = pack2(v[2], v[3]);
+        for (int k4 = 0; k4 < 4; ++k4) {
+            if (k4 > wm) continue;
+            uint32_t f[4];
+            ldsm4(f, block(which, wm, k4) + block_off(lane & 15, lane >> 4));
+            const float2 be0 = *reinterpret_cast<const float2 *>(bet + 16 * k4 + 2 * c);
+            const float2 be1 = *reinterpret_cast<const float2 *>(bet + 16 * k4 + 8 + 2 * c);
+            f[0] = pack2(low_f(f[0]) * be0.x, high_f(f[0]) * be0.y);
+            f[1] = pack2(low_f(f[1]) * be0.x, high_f(f[1]) * be0.y);
+            f[2] = pack2(low_f(f[2]) * be1.x, high_f(f[2]) * be1.y);
+            f[3] = pack2(low_f(f[3]) * be1.x, high_f(f[3]) * be1.y);
+            times_tokens(x, f, Kt, k4);
         }
     };
     // 16 x HD results to global memory: neighbouring lanes exchange halves of two tiles, so that a row's four lanes
@@ -1039,21 +1050,21 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
                         c & 1 ? make_uint2(got, p1) : make_uint2(p0, got);
             }
     };
-    const auto lower = [&](int n2) { return n2 <= wm; };
-    const auto upper = [&](int n2) { return n2 >= wm; };
 
-    float z[HN][4], b[8][4];
+    float z[HN][4];
     zero(z);
-    zero(b);
     {
-        float dq[HN][4];
+        float dq[HN][4], b[8][4];
+        zero(b);
         zero(dq);
         times_rows(dq, Pt, 0);
         times_rows(z, Wt, 0);
         __syncthreads();  // the rows have been read
         if (MB > 1) load_rows(S, 1);
         else load_rows(R, 0);
-        pairs(b, Pt, Et, lower);
+        pairs(b, half ? Wt : Pt, Et);
+        pair_sums(b, half ? Kt : Qt, half ? -1.f : 1.f);
+        put_blocks(b);
         if (MB > 1) {
             cp_wait<0>();
             __syncthreads();
@@ -1067,14 +1078,9 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
         scale(z, e0, e1);
         row_dot(dq, Qt, 1);
         row_dot(z, Kt, 3);
-        if (half == 0) pair_sums(b, Qt, 1.f);
-#pragma unroll
-        for (int k4 = 0; k4 < 4; ++k4) {
-            if (!lower(k4)) continue;
-            uint32_t f[4];
-            weigh_rows(f, b, k4, true);
-            times_tokens(dq, f, Kt, k4);
-        }
+        if (MB == 1) __syncthreads();  // (else the barrier above) the blocks are there
+        times_keys(dq, 0);
+        times_keys(z, 1);
         if (a.dq_add) {
 #pragma unroll
             for (int n = 0; n < HN; ++n)
@@ -1088,16 +1094,6 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
                 }
         }
         store(a.dq, dq);
-    }
-    zero(b);
-    pairs(b, Wt, Et, lower);
-    if (half == 1) pair_sums(b, Kt, -1.f);
-#pragma unroll
-    for (int k4 = 0; k4 < 4; ++k4) {
-        if (!lower(k4)) continue;
-        uint32_t f[4];
-        weigh_rows(f, b, k4, false);
-        times_tokens(z, f, Kt, k4);
     }
     float y[HN][4];
     zero(y);
@@ -1118,10 +1114,6 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
             __syncthreads();
             load_rows(R, mb + 1);
         }
-        if (mb == 0) {
-            zero(b);
-            pairs(b, Et, Pt, upper);
-        }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) in += __shfl_xor_sync(0xffffffffu, in, o);
@@ -1129,19 +1121,15 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
     scale(y, __expf(ce - c_lo), __expf(ce - c_hi));
     row_dot(y, Kt, 2);
 #pragma unroll
-    for (int k4 = 0; k4 < 4; ++k4) {
-        if (!upper(k4)) continue;
+    for (int k4 = 0; k4 < 4; ++k4) {  // the transposed blocks: rows j, columns i >= j
+        if (k4 < wm) continue;
+        const uint32_t off = block_off(((lane >> 4) << 3) + (lane & 7), (lane >> 3) & 1);
         uint32_t f[4];
-        weigh_cols(f, b, k4, true, 1.f);
+        ldsm4t(f, block(0, k4, wm) + off);
         times_tokens(y, f, Qt, k4);
-    }
-    zero(b);
-    pairs(b, Et, Wt, upper);
+        ldsm4t(f, block(1, k4, wm) + off);
 #pragma unroll
-    for (int k4 = 0; k4 < 4; ++k4) {
-        if (!upper(k4)) continue;
-        uint32_t f[4];
-        weigh_cols(f, b, k4, false, -1.f);
+        for (int q = 0; q < 4; ++q) f[q] ^= 0x80008000u;
         times_tokens(y, f, Kt, k4);
     }
     row_dot(y, Kt, 0);
@@ -1166,7 +1154,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
         __syncthreads();
 #pragma unroll
         for (int k4 = 0; k4 < 4; ++k4) {
-            if (!upper(k4)) continue;
+            if (k4 < wm) continue;
             uint32_t fh[4], fl[4];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -1262,21 +1250,21 @@ __global__ void __launch_bounds__(256) delta_scalars(const __nv_bfloat16 *la, fl
     one[i] = 1.f;
 }
 
-// dy_t . O_t per token (the gradient of the online gate): one warp per token.
-__global__ void __launch_bounds__(256) delta_dgon(const __nv_bfloat16 *dy, const float *O, float *dgon, long long tokens, int d)
+// dy_t . O_t per token (the gradient of the online gate): d / 8 lanes per token.
+__global__ void __launch_bounds__(256) delta_dgon(const __nv_bfloat16 *dy, const __nv_bfloat16 *O, float *dgon, long long tokens, int d)
 {
-    const long long t = (long long)blockIdx.x * 8 + threadIdx.x / 32;
-    if (t >= tokens) return;
-    const int lane = threadIdx.x % 32;
+    const int pieces = d / 8;
+    const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
+    const bool ok = e / pieces < tokens;
     float s = 0.f;
-    for (int i = 2 * lane; i < d; i += 64) {
-        const uint32_t y = *reinterpret_cast<const uint32_t *>(dy + t * d + i);
-        const float2 o = *reinterpret_cast<const float2 *>(O + t * d + i);
-        s = fmaf(low_f(y), o.x, fmaf(high_f(y), o.y, s));
-    }
+    if (ok) {
+        const uint4 y = reinterpret_cast<const uint4 *>(dy)[e], o = reinterpret_cast<const uint4 *>(O)[e];
+        const uint32_t *yw = reinterpret_cast<const uint32_t *>(&y), *ow = reinterpret_cast<const uint32_t *>(&o);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) dgon[t] = s;
+        for (int q = 0; q < 4; ++q) s = fmaf(low_f(yw[q]), low_f(ow[q]), fmaf(high_f(yw[q]), high_f(ow[q]), s));
+    }
+    for (int o = pieces / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (ok && e % pieces == 0) dgon[e / pieces] = s;
 }
 
 template <int D, bool READ, bool REV>
@@ -1290,11 +1278,11 @@ cudaError_t prep_impl(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
     return cudaGetLastError();
 }
 
-template <int D, int NW, bool READ>
+template <int D, int NW, bool READ, bool FULL>
 cudaError_t walk_launch(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
 {
     constexpr int smem = WalkSmem<D, NW, READ>::kTotal;
-    auto kern = delta_walk_tc<D, NW, READ>;
+    auto kern = delta_walk_tc<D, NW, READ, FULL>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)((long long)p.BH * p.N * (D / (16 * NW))), 32 * NW, smem, s>>>(a);
@@ -1307,17 +1295,18 @@ cudaError_t walk_impl(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
     cudaError_t e = a.rrec ? prep_impl<D, READ, true>(p, a, s) : prep_impl<D, READ, false>(p, a, s);
     if (e != cudaSuccess) return e;
     profile_after_kernel(s, "delta_prep_tc");
-    e = walk_launch<D, 4, READ>(p, a, s);
+    e = a.full ? walk_launch<D, 4, READ, true>(p, a, s) : walk_launch<D, 4, READ, false>(p, a, s);
     profile_after_kernel(s, "delta_walk_tc");
     return e;
 }
 
 }  // namespace
 
-cudaError_t launch_delta_dgon(const Problem &p, const void *dy, const float *O_on, float *dgon, cudaStream_t s)
+cudaError_t launch_delta_dgon(const Problem &p, const void *dy, const void *O, float *dgon, cudaStream_t s)
 {
     const long long n = (long long)p.BH * p.L;
-    delta_dgon<<<(unsigned)((n + 7) / 8), 256, 0, s>>>(static_cast<const __nv_bfloat16 *>(dy), O_on, dgon, n, p.d);
+    delta_dgon<<<(unsigned)((n * (p.d / 8) + 255) / 256), 256, 0, s>>>(static_cast<const __nv_bfloat16 *>(dy),
+                                                                   static_cast<const __nv_bfloat16 *>(O), dgon, n, p.d);
     return cudaGetLastError();
 }
 

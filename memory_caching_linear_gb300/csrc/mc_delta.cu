@@ -105,6 +105,7 @@ int forward_delta_tc(const Call &c, const void *q, const void *k, const void *v,
     const bool one = N == 1, routed = mode_uses_u(p.mode), tc = !one && tc_fused_gates(p);
     DeltaTcArgs t = delta_tc_args(c, q, k, v, la, be);
     t.states = states;
+    t.full = states != nullptr;
     FwdArgs f{};
     float *kbar = nullptr, *r_on = nullptr, *sums = nullptr, *alpha = nullptr, *zero = nullptr, *ones = nullptr;
     char *tc_scratch = nullptr;
@@ -257,7 +258,7 @@ int backward_delta(const void *q, const void *k, const void *v, const void *u, c
     BwdArgs b{};
     float *sums = nullptr, *kbar = nullptr, *r_on = nullptr, *G = nullptr, *dkbar = nullptr, *tok = nullptr,
           *dq_add = nullptr, *gam = nullptr, *dg = nullptr, *dgon = nullptr;
-    uint8_t *states_img = nullptr, *G_img = nullptr, *kbar_img = nullptr;
+    uint8_t *states_img = nullptr, *kbar_img = nullptr;
     void *scratch = nullptr;
     for (int pass = 0; pass < 2; ++pass) {
         Carver cv{static_cast<char *>(scratch), 0};
@@ -271,8 +272,10 @@ int backward_delta(const void *q, const void *k, const void *v, const void *u, c
         t.S_c = cv.take<__nv_bfloat16>(BH * N * NCH * d * d, tc);
         t.R_c = cv.take<__nv_bfloat16>(BH * N * NCH * d * d, tc);
         a.states = cv.take<float>(BH * N * d * d, many);
-        a.O_on = cv.take<float>(BH * L * d, many);
-        G = cv.take<float>(BH * N * d * d, many && !rtc);
+        a.O_on = cv.take<float>(BH * L * d, many && !rtc);
+        t.y = cv.take<__nv_bfloat16>(BH * L * d, rtc);
+        t.g_parts = rtc ? bwd_G_parts(p) : 1;
+        G = cv.take<float>(t.g_parts * BH * N * d * d, many);
         tok = cv.take<float>(BH * L * kBwdTokWords, many);
         dq_add = cv.take<float>(BH * L * d, many);
         kbar = cv.take<float>(BH * N * d, many);
@@ -283,7 +286,6 @@ int backward_delta(const void *q, const void *k, const void *v, const void *u, c
         b.sel_g = cv.take<float>(BH * L * p.topk, routed && !rtc && p.mode == MC_SSC);
         b.Np = (int)((N + 15) & ~(size_t)15);
         states_img = cv.take<uint8_t>(BH * N * 32768, rtc);
-        G_img = cv.take<uint8_t>(BH * N * 32768, rtc);
         kbar_img = cv.take<uint8_t>(BH * ((N + 63) / 64) * 49152, rtc && routed);
         gam = cv.take<float>(BH * N * L, rtc && routed);
         dg = cv.take<float>(2 * BH * N * L, rtc);
@@ -340,19 +342,18 @@ int backward_delta(const void *q, const void *k, const void *v, const void *u, c
             }
             if (e == cudaSuccess) e = launch_bwd_cached_only_tc(p, q, dy, states_img, gam, dq_add, dg, s);
             profile_after_kernel(s, "bwd_cached_tc");
-            if (e == cudaSuccess) e = launch_delta_dgon(p, dy, a.O_on, dgon, s);
+            if (e == cudaSuccess) e = launch_delta_dgon(p, dy, t.y, dgon, s);
             profile_after_kernel(s, "delta_dgon");
             if (e == cudaSuccess) e = launch_bwd_route(p, b, s);
-            if (e == cudaSuccess) e = launch_bwd_G_tc(p, dy, q, gam, G_img, s);
+            if (e == cudaSuccess) e = launch_bwd_G_parts_tc(p, dy, q, gam, G, s);
             profile_after_kernel(s, "bwd_G_tc");
             t.gon = b.kv_gw;
             pw = b.kv_gw + BH * L;
             t.gw_stride = 1;
-            t.G_img = G_img;
         } else {
             if (e == cudaSuccess) e = launch_bwd_router_simt(p, b, s);
-            t.G = G;
         }
+        t.G = G;
         if (e == cudaSuccess && routed) {
             a.gw_stride = t.gw_stride;
             e = launch_pool_grad_simt(p, a, pw, sums, dkbar, s);

@@ -252,6 +252,9 @@ size_t backward_scratch_bytes(const Problem &p);
 // L % seg_len == 0, N <= 64.
 bool bwd_tc_supported(const Problem &p);
 cudaError_t launch_bwd_G_tc(const Problem &p, const void *dy, const void *q, const float *gam, uint8_t *G, cudaStream_t s);
+// G as bwd_G_parts(p) fp32 summands [BH][N][d][d] each (segments < N - 1), over shares of the later tokens.
+int bwd_G_parts(const Problem &p);
+cudaError_t launch_bwd_G_parts_tc(const Problem &p, const void *dy, const void *q, const float *gam, float *G, cudaStream_t s);
 // gw: [2][BH][L], the online gate of every token, then its pooled-key weight w (routed aggregations).
 cudaError_t launch_bwd_kv_tc(const Problem &p, const void *q, const void *k, const void *v, const void *u, const void *dy,
                              const uint8_t *G, const float *gw, const float *dkbar, void *dk, void *dv, cudaStream_t s);
@@ -309,6 +312,7 @@ constexpr int kDeltaRecBytes = 16384;  // a chunk's record between its two kerne
 struct DeltaTcArgs {
     const __nv_bfloat16 *q, *k, *v, *la, *be;
     uint8_t *rec;          // [BH][N][NCH] x kDeltaRecBytes scratch
+    bool full;             // states with fp32 accuracy
     __nv_bfloat16 *y;      // online reads in bf16 (one segment), or null
     float *O_on;           // online reads in fp32, or null
     float *states;         // [BH][N][d][d], or null
@@ -321,15 +325,15 @@ struct DeltaTcArgs {
     uint8_t *rrec;         // [BH][N][NCH] x kDeltaRRecBytes scratch: the reverse walk's record, or null
     const float *gon, *pw; // online gate and pooled-key weight of token t at [t * gw_stride], or null (1; no pooled keys)
     int gw_stride;
-    const float *G;        // [BH][N][d][d] adjoint of the cached states, or null
-    const uint8_t *G_img;  // the same as bf16 operand images (launch_bwd_G_tc), or null
+    const float *G;        // g_parts x [BH][N][d][d]: the adjoint of the cached states as a sum, or null
+    int g_parts;
     const float *dq_add;   // [BH][L][d] added to dq, or null
     const float *rho;      // [BH][N][NCH][d], with pw
     __nv_bfloat16 *R_c;    // [BH][N][NCH][d][d] adjoint after every chunk
     __nv_bfloat16 *dq, *dk, *dv, *dla, *dbe;
     int BH, L, C, N, NCH;
 };
-cudaError_t launch_delta_dgon(const Problem &p, const void *dy, const float *O_on, float *dgon, cudaStream_t s);
+cudaError_t launch_delta_dgon(const Problem &p, const void *dy, const void *O, float *dgon, cudaStream_t s);
 constexpr int kDeltaRRecBytes = 11264;
 // After the walk with rrec, E and S_c: dv and R_c, then the other gradients.
 cudaError_t launch_delta_grads_tc(const Problem &p, const DeltaTcArgs &a, cudaStream_t s);

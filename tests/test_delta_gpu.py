@@ -57,7 +57,9 @@ def test_forward(d, C, L, dtype, mode, topk):
     assert rel(gy, y) <= TOL[dtype]
     assert rel(gst, st) <= STATE_TOL
     again, none = mcl.mc_forward_delta(*cuda(x), C, mode, topk, want_states=False)
-    assert none is None and torch.equal(again, gy)
+    assert none is None and rel(again, y) <= TOL[dtype]
+    if dtype == "f32" or d < 64:  # the tensor-core kernels hold the states to more terms when they are returned
+        assert torch.equal(again, gy)
 
 
 @pytest.mark.parametrize("d,L,dtype", UNCUT)
