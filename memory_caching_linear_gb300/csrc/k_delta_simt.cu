@@ -626,20 +626,18 @@ __global__ void __launch_bounds__(256) pool_score(DeltaArgs a, const float *kpre
 
 // The three passes in one, for many segments: one CTA per (bh, segment) goes through the chunks with the running key
 // sum in shared memory, so k and u come from HBM once.  A thread copies the pieces that it will read itself, the
-// next chunks' asynchronously (two ahead in bf16, one in fp32), so the copies need no barrier.
+// next chunk's asynchronously, so the copies need no barrier; three CTAs on an SM (bf16, d = 128) keep 96 KB on their way.
+constexpr int kPoolStages = 2;
 template <typename T, int D>
-constexpr int pool_stages() { return sizeof(T) == 2 ? 3 : 2; }
-template <typename T, int D>
-constexpr int pool_walk_smem(bool score) { return pool_stages<T, D>() * (score ? 2 : 1) * PoolTile<T, D>::TPL * 256 * 16; }
+constexpr int pool_walk_smem(bool score) { return kPoolStages * (score ? 2 : 1) * PoolTile<T, D>::TPL * 256 * 16; }
 
 template <typename T, int D, bool SCORE>
 __global__ void __launch_bounds__(256) pool_walk(DeltaArgs a, float *kpre, float *kbar, float *r_on)
 {
     using P = PoolTile<T, D>;
-    constexpr int NS = pool_stages<T, D>(), OPS = SCORE ? 2 : 1;
+    constexpr int NS = kPoolStages, OPS = SCORE ? 2 : 1;
     extern __shared__ __align__(16) uint8_t fifo[];
-    __shared__ float part[2][P::TL * (D + 1)];
-    __shared__ float run[2][D];
+    __shared__ float part[P::TL * (D + 1)];
     const int seg = (int)blockIdx.x % a.N, bh = (int)blockIdx.x / a.N;
     const int t0 = seg * a.C, len = min((seg + 1) * a.C, a.L) - t0, nch = (len + kCH - 1) / kCH;
     const int tid = threadIdx.x, pc = tid % P::PC, tl = tid / P::PC;
@@ -658,13 +656,12 @@ __global__ void __launch_bounds__(256) pool_walk(DeltaArgs a, float *kpre, float
         }
         mma::cp_commit();
     };
-    if (tid < D) run[0][tid] = 0.f;
+    float run = 0.f;  // (threads below D) the segment's sum of column tid so far
 #pragma unroll
     for (int ch = 0; ch < NS - 1; ++ch) load(ch);
     for (int ch = 0; ch < nch; ++ch) {
         load(ch + NS - 1);
         mma::cp_wait<NS - 1>();
-        float *pt = part[ch & 1];
         float x[P::TPL][P::V];
         if (tid < P::NT) {
 #pragma unroll
@@ -675,27 +672,29 @@ __global__ void __launch_bounds__(256) pool_walk(DeltaArgs a, float *kpre, float
                     for (int i = 0; i < P::V; ++i) x[j][i] += x[j > 0 ? j - 1 : 0][i];
             }
 #pragma unroll
-            for (int i = 0; i < P::V; ++i) pt[tl * (D + 1) + pc * P::V + i] = x[P::TPL - 1][i];
+            for (int i = 0; i < P::V; ++i) part[tl * (D + 1) + pc * P::V + i] = x[P::TPL - 1][i];
         }
         __syncthreads();
         if (tid < D) {
-            float s = run[ch & 1][tid];
+            float own[P::TL], s = run;
+#pragma unroll
+            for (int i = 0; i < P::TL; ++i) own[i] = part[i * (D + 1) + tid];
             if (kpre) kpre[((size_t)blockIdx.x * a.NCH + ch) * D + tid] = s;
 #pragma unroll
             for (int i = 0; i < P::TL; ++i) {
-                const float own = pt[i * (D + 1) + tid];
-                pt[i * (D + 1) + tid] = s;
-                s += own;
+                part[i * (D + 1) + tid] = s;
+                s += own[i];
             }
-            run[(ch + 1) & 1][tid] = s;
+            run = s;
             if (ch + 1 == nch) kbar[(size_t)blockIdx.x * D + tid] = s / (float)len;
         }
-        if (!SCORE) continue;
         __syncthreads();
+        if (!SCORE) continue;
         float before[P::V];
         if (tid < P::NT)
 #pragma unroll
-            for (int i = 0; i < P::V; ++i) before[i] = pt[tl * (D + 1) + pc * P::V + i];
+            for (int i = 0; i < P::V; ++i) before[i] = part[tl * (D + 1) + pc * P::V + i];
+        __syncthreads();
 #pragma unroll
         for (int j = 0; j < P::TPL; ++j) {
             const int t = ch * kCH + tl * P::TPL + j;
