@@ -65,18 +65,54 @@ __device__ __forceinline__ Where chunk_at(const DeltaTcArgs &a, long long id)
 
 // ---------------------------------------------------------------------------
 // delta_prep_tc: one warp per chunk, no barrier between warps.  K K^T (and Q K^T) in registers, exact bf16
-// products; then X = (1 + A)^-1 in fp32 by substitution over blocks of 16 rows, a lane holding the columns
-// lane and lane + 32.  A and X share one 64 x 64 array in shared memory: A_ik at [k][i] (above the diagonal), X_ij at
-// [i][j] (on and below it), so that a step reads A's column k as one broadcast row.  P goes from the accumulators
-// to the record without shared memory: a tile of P is the operand of rows j, columns i as it lies, and its 8 x 8
-// transposes are the other one.
+// products; then X = (1 + A)^-1 by 16 x 16 blocks: the four diagonal blocks by substitution in fp32, all at once (a lane
+// per column, two blocks on each half of the warp), and the others from them as products of 16 x 16 blocks with every
+// operand in two bf16 terms (2^-17):
+//   X10 = -X11 A10 X00, X32 = -X33 A32 X22, and [X20 X21; X30 X31] = -[X22 0; X32 X33] [A20 A21; A30 A31] [X00 0; X10 X11].
+// A product's result is a left operand as it lies, its 8 x 8 transposes are a right one, and a block of X (or P) is, as it
+// lies, also the walk's operand of rows j, columns i: nothing but the diagonal blocks passes through shared memory.
+// (Substitution over all 64 rows, two columns a lane: 156 us at the long workload.)
 // ---------------------------------------------------------------------------
-constexpr int kMP = 68;  // row of the 64 x 64 array, in words
+constexpr int kXP = 20, kXB = 16 * kXP + 8;  // row and block pitch of the diagonal blocks, in words
+
+struct Terms {  // an operand in two bf16 terms: left 4 registers each, right 2 x 2
+    uint32_t h[4], l[4];
+};
+// 16 x 16 results: [column half][accumulator]
+__device__ __forceinline__ Terms left_of(const float (&x)[2][4])
+{
+    Terms t;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) split2(x[h][2 * r], x[h][2 * r + 1], t.h[2 * h + r], t.l[2 * h + r]);
+    return t;
+}
+__device__ __forceinline__ Terms right_of(const Terms &left)
+{
+    Terms t;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        t.h[q] = movm_t(left.h[q]);
+        t.l[q] = movm_t(left.l[q]);
+    }
+    return t;
+}
+// acc += left x right
+__device__ __forceinline__ void block_mma(float (&acc)[2][4], const Terms &a, const Terms &b)
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        mma16816(acc[h], a.l, b.h[2 * h], b.h[2 * h + 1]);
+        mma16816(acc[h], a.h, b.l[2 * h], b.l[2 * h + 1]);
+        mma16816(acc[h], a.h, b.h[2 * h], b.h[2 * h + 1]);
+    }
+}
 
 template <int D, bool QK>
 __host__ __device__ constexpr int prep_smem()
 {
-    return ((QK ? 2 : 1) * kCH * D * 2 > kCH * kMP * 4 ? (QK ? 2 : 1) * kCH * D * 2 : kCH * kMP * 4) + 2 * kCH * 4;
+    return ((QK ? 2 : 1) * kCH * D * 2 > 8 * kXB * 4 ? (QK ? 2 : 1) * kCH * D * 2 : 8 * kXB * 4) + 2 * kCH * 4;
 }
 
 template <int D, bool READ, bool REV>
@@ -85,7 +121,7 @@ __global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a)
     constexpr int ROW = D * 2, PIECES = D / 8, KS = D / 16;
     constexpr bool QK = READ || REV;
     extern __shared__ __align__(16) uint8_t sm[];
-    float *M = reinterpret_cast<float *>(sm);  // over the tiles once these are read
+    float *Ad = reinterpret_cast<float *>(sm), *Xd = Ad + 4 * kXB;  // over the tiles once these are read
     float *cum = reinterpret_cast<float *>(sm + prep_smem<D, QK>() - 2 * kCH * 4), *bet = cum + kCH;
     const Where w = chunk_at(a, blockIdx.x);
     if (w.cnt <= 0) return;
@@ -206,85 +242,131 @@ __global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a)
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int i = 16 * b + g + 8 * (e >> 1), j = 16 * n2 + 8 * h + 2 * c + (e & 1);
-                    if (j < i) M[j * kMP + i] = kk[b * (b + 1) / 2 + n2][h][e] * __expf(cum[i] - cum[j]) * bet[j];
+                    const int il = g + 8 * (e >> 1), jl = 8 * h + 2 * c + (e & 1), i = 16 * b + il, j = 16 * n2 + jl;
+                    float &x = kk[b * (b + 1) / 2 + n2][h][e];
+                    x *= j < i ? __expf(cum[i] - cum[j]) * bet[j] : 0.f;
+                    if (b == n2) Ad[b * kXB + jl * kXP + il] = x;  // column j of A as a row
                 }
     __syncwarp();
+    {
+        const int hw = lane / 16, col = lane % 16;
+        float x[2][16];
 #pragma unroll
-    for (int blk = 0; blk < 4; ++blk) {
-        float x0[16], x1[16];  // rows 16 blk .. of the columns lane and (from block 2 on) lane + 32
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            x0[r] = 16 * blk + r == lane ? 1.f : 0.f;
-            x1[r] = 16 * blk + r == lane + 32 ? 1.f : 0.f;
-        }
-#pragma unroll 2
-        for (int k = 0; k < 16 * blk; ++k) {
-            const float y0 = lane <= k ? M[k * kMP + lane] : 0.f;
-            const float y1 = blk == 3 && lane + 32 <= k ? M[k * kMP + lane + 32] : 0.f;
+            for (int r = 0; r < 16; ++r) x[s][r] = r == col ? 1.f : 0.f;
 #pragma unroll
-            for (int r4 = 0; r4 < 4; ++r4) {
-                const float4 av = *reinterpret_cast<const float4 *>(M + k * kMP + 16 * blk + 4 * r4);
-                x0[4 * r4] = fmaf(-av.x, y0, x0[4 * r4]);
-                x0[4 * r4 + 1] = fmaf(-av.y, y0, x0[4 * r4 + 1]);
-                x0[4 * r4 + 2] = fmaf(-av.z, y0, x0[4 * r4 + 2]);
-                x0[4 * r4 + 3] = fmaf(-av.w, y0, x0[4 * r4 + 3]);
-                if (blk == 3) {
-                    x1[4 * r4] = fmaf(-av.x, y1, x1[4 * r4]);
-                    x1[4 * r4 + 1] = fmaf(-av.y, y1, x1[4 * r4 + 1]);
-                    x1[4 * r4 + 2] = fmaf(-av.z, y1, x1[4 * r4 + 2]);
-                    x1[4 * r4 + 3] = fmaf(-av.w, y1, x1[4 * r4 + 3]);
+        for (int k = 0; k < 15; ++k)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int r4 = (k + 1) / 4; r4 < 4; ++r4) {
+                    const float4 av = *reinterpret_cast<const float4 *>(Ad + (2 * s + hw) * kXB + k * kXP + 4 * r4);
+                    const float al[4] = {av.x, av.y, av.z, av.w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (4 * r4 + q > k) x[s][4 * r4 + q] = fmaf(-al[q], x[s][k], x[s][4 * r4 + q]);
                 }
-            }
-        }
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int r4 = (k + 1) / 4; r4 < 4; ++r4) {
-                const float4 av = *reinterpret_cast<const float4 *>(M + (16 * blk + k) * kMP + 16 * blk + 4 * r4);
-                const float al[4] = {av.x, av.y, av.z, av.w};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int r = 4 * r4 + q;
-                    if (r > k) {
-                        x0[r] = fmaf(-al[q], x0[k], x0[r]);
-                        if (blk >= 2) x1[r] = fmaf(-al[q], x1[k], x1[r]);
-                    }
-                }
-            }
-        }
-        __syncwarp();  // every lane has read the block's columns of A beside the rows written now
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int i = 16 * blk + r;
-            if (lane <= i) M[i * kMP + lane] = x0[r];
-            if (blk >= 2 && lane + 32 <= i) M[i * kMP + lane + 32] = x1[r];
-        }
-        __syncwarp();
+            for (int r = 0; r < 16; ++r) Xd[(2 * s + hw) * kXB + r * kXP + col] = x[s][r];
     }
-    uint4 *tt = reinterpret_cast<uint4 *>(rec) + lane;
+    __syncwarp();
+    auto diag = [&](int b, float (&x)[2][4]) {  // a diagonal block as a result
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int kt = 0; kt <= nt / 2; ++kt) {
-            const int i = 8 * nt + g, j = 16 * kt + 2 * c;
-            const float *x = M + i * kMP + j;
-            uint4 o;
-            split2(j < i ? x[0] : 0.f, j + 1 < i ? x[1] : 0.f, o.x, o.z);
-            split2(j + 8 < i ? x[8] : 0.f, j + 9 < i ? x[9] : 0.f, o.y, o.w);
-            tt[(tile_base(nt) + kt) * 32] = o;
-        }
-    if (REV) {
-        uint2 *lt = reinterpret_cast<uint2 *>(rrec) + lane;
-#pragma unroll
-        for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-            for (int kt = nt / 2; kt < 4; ++kt) {
-                const int i = 8 * nt + g, m = 16 * kt + 2 * c;  // T_mi, m > i
-                const float *x = M + m * kMP + i;
-                lt[(rev_base(nt) + kt - nt / 2) * 32] = make_uint2(pack2(m > i ? x[0] : 0.f, m + 1 > i ? x[kMP] : 0.f),
-                                                                   pack2(m + 8 > i ? x[8 * kMP] : 0.f, m + 9 > i ? x[9 * kMP] : 0.f));
+            for (int r = 0; r < 2; ++r) {
+                const float2 v = *reinterpret_cast<const float2 *>(Xd + b * kXB + (g + 8 * r) * kXP + 8 * h + 2 * c);
+                x[h][2 * r] = v.x;
+                x[h][2 * r + 1] = v.y;
             }
+    };
+    auto out = [&](int bi, int bj, const Terms &t) {  // block (bi, bj) of T - 1
+        uint4 *tt = reinterpret_cast<uint4 *>(rec) + lane;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) tt[(tile_base(2 * bi + r) + bj) * 32] = make_uint4(t.h[r], t.h[2 + r], t.l[r], t.l[2 + r]);
+        if (REV) {
+            uint2 *lt = reinterpret_cast<uint2 *>(rrec) + lane;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                lt[(rev_base(2 * bj + h) + bi - bj) * 32] = make_uint2(movm_t(t.h[2 * h]), movm_t(t.h[2 * h + 1]));
+        }
+    };
+    auto negate = [](float (&x)[2][4]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[h][e] = -x[h][e];
+    };
+    auto clear = [](float (&x)[2][4]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[h][e] = 0.f;
+    };
+    Terms D0, D1, D2, D3;
+    {
+        float x[2][4];
+        Terms *const to[4] = {&D0, &D1, &D2, &D3};
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            diag(b, x);
+            *to[b] = left_of(x);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)  // T - 1: the diagonal out
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (8 * h + 2 * c + (e & 1) >= g + 8 * (e >> 1)) x[h][e] = 0.f;
+            out(b, b, left_of(x));
+        }
+    }
+    // A_bn is kk[b (b + 1) / 2 + n]
+    Terms X10r, X32l;
+    {
+        float y[2][4], x[2][4];
+        clear(y);
+        block_mma(y, left_of(kk[1]), right_of(D0));
+        clear(x);
+        block_mma(x, D1, right_of(left_of(y)));
+        negate(x);
+        const Terms t = left_of(x);
+        out(1, 0, t);
+        X10r = right_of(t);
+        clear(y);
+        block_mma(y, left_of(kk[8]), right_of(D2));
+        clear(x);
+        block_mma(x, D3, right_of(left_of(y)));
+        negate(x);
+        X32l = left_of(x);
+        out(3, 2, X32l);
+    }
+    const Terms D0r = right_of(D0), D1r = right_of(D1);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {  // block columns 0 and 1
+        float y2[2][4], y3[2][4], x[2][4];
+        clear(y2);
+        clear(y3);
+        if (j == 0) {
+            block_mma(y2, left_of(kk[3]), D0r);
+            block_mma(y3, left_of(kk[6]), D0r);
+            block_mma(y2, left_of(kk[4]), X10r);
+            block_mma(y3, left_of(kk[7]), X10r);
+        } else {
+            block_mma(y2, left_of(kk[4]), D1r);
+            block_mma(y3, left_of(kk[7]), D1r);
+        }
+        const Terms y2r = right_of(left_of(y2)), y3r = right_of(left_of(y3));
+        clear(x);
+        block_mma(x, D2, y2r);
+        negate(x);
+        out(2, j, left_of(x));
+        clear(x);
+        block_mma(x, X32l, y2r);
+        block_mma(x, D3, y3r);
+        negate(x);
+        out(3, j, left_of(x));
     }
 }
 
