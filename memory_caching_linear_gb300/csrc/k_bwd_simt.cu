@@ -784,7 +784,9 @@ __global__ void __launch_bounds__(kThreads) bwd_G_simt(BwdArgs a)
     float *Us = Qs + kTG * P;  // kTG x P
     float *gb = Us + kTG * P;  // kTG
 
-    const int i = (int)blockIdx.x / a.BH, bh = (int)blockIdx.x % a.BH;
+    const int per = a.BH * (a.N - 1);
+    const int part = (int)blockIdx.x / per, i = (int)blockIdx.x % per / a.BH, bh = (int)blockIdx.x % a.BH;
+    const int parts = a.g_parts > 1 ? a.g_parts : 1;
     const int mode = a.mode;
     const bool gated = gated_mode(mode);
     const size_t base = (size_t)bh * a.L * D;
@@ -799,7 +801,10 @@ __global__ void __launch_bounds__(kThreads) bwd_G_simt(BwdArgs a)
 #pragma unroll
         for (int y = 0; y < RB; ++y) G[x][y] = 0.f;
 
-    for (int c0 = (i + 1) * a.C; c0 < a.L; c0 += kTG) {
+    // this CTA's share of the later tokens, in whole steps
+    const int first = (i + 1) * a.C, steps = (a.L - first + kTG - 1) / kTG;
+    const int c_end = min(a.L, first + (int)((long long)steps * (part + 1) / parts) * kTG);
+    for (int c0 = first + (int)((long long)steps * part / parts) * kTG; c0 < c_end; c0 += kTG) {
         const int cnt = min(kTG, a.L - c0);
         __syncthreads();
         for (int e = tid; e < kTG * D; e += kThreads) {
@@ -844,7 +849,7 @@ __global__ void __launch_bounds__(kThreads) bwd_G_simt(BwdArgs a)
                 for (int y = 0; y < RB; ++y) G[x][y] = fmaf(yv[x], qv[y], G[x][y]);
         }
     }
-    float *Go = a.G + ((size_t)bh * a.N + i) * D * D;
+    float *Go = a.G + (((size_t)part * a.BH + bh) * a.N + i) * D * D;
 #pragma unroll
     for (int x = 0; x < RB; ++x)
 #pragma unroll
@@ -1039,7 +1044,7 @@ cudaError_t router_impl(const Problem &p, const BwdArgs &a, cudaStream_t s)
         const size_t smem = sizeof(float) * (3 * kTG * P + kTG);
         auto kern = bwd_G_simt<T, D>;
         if ((e = set_smem(kern, smem)) != cudaSuccess) return e;
-        kern<<<(unsigned)((long long)p.BH * (p.N - 1)), kThreads, smem, s>>>(a);
+        kern<<<(unsigned)((long long)p.BH * (p.N - 1) * (a.g_parts > 1 ? a.g_parts : 1)), kThreads, smem, s>>>(a);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         profile_after_kernel(s, "bwd_G_simt");
     }

@@ -144,55 +144,75 @@ __global__ void __launch_bounds__(kMThreads) gate_mass_simt(CompactArgs a)
 
 // ---------------------------------------------------------------------------
 // gate_mass_tc: the same for bf16 inputs and the softmax gates.  A CTA takes 128 tokens, a warp 16; the scores
-// against 64 segments at a time are warp-level products of u with the key means as three bf16 terms
-// (launch_kbar_images: every product is exact, only the fp32 sum rounds).  Up to 128 segments the scores stay in
-// registers between the softmax's sums and the gates; beyond, they are formed a second time.
+// against 32 segments at a time are warp-level products of u with the key means as three bf16 terms
+// (launch_kbar_images: every product is exact, only the fp32 sum rounds), the next 32 segments' means on their way
+// meanwhile.  Up to 128 segments the scores stay in registers between the softmax's sums and the gates; beyond, they are
+// formed a second time.
 // ---------------------------------------------------------------------------
 constexpr int kTM = 128;
+
+template <int D>
+struct MassSmem {
+    static constexpr int PN = D > 64 ? 2 : 1;                   // 64-column panels
+    static constexpr int UR = D * 2 < 128 ? 128 : D * 2;        // row of the token tile
+    static constexpr int kHalf = 3 * PN * 32 * 128;             // three terms of 32 segments
+    static constexpr int kTotal = kTM * UR + 2 * kHalf;
+};
 
 template <int D>
 __global__ void __launch_bounds__(256, 2) gate_mass_tc(CompactArgs a)
 {
     using namespace mma;
-    constexpr int KS = D / 16, PN = D > 64 ? 2 : 1, UR = D * 2 < 128 ? 128 : D * 2;
+    using M = MassSmem<D>;
+    constexpr int KS = D / 16, PN = M::PN, UR = M::UR;
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    uint8_t *Ut = smem_raw, *Kt = smem_raw + kTM * UR;  // 3 terms x PN panels of 64 rows x 128 bytes
-    __shared__ float cols[8][64];
+    uint8_t *Ut = smem_raw, *Kt = smem_raw + kTM * UR;
+    __shared__ float cols[8][32];
     const int tile = a.tiles - 1 - (int)(blockIdx.x / a.BH), bh = (int)(blockIdx.x % a.BH);  // the longest first
     const int tb = tile * kTM, cnt = min(kTM, a.L - tb);
-    const int smax = (tb + cnt - 1) / a.C, nblk = (smax + 63) / 64;
+    const int smax = (tb + cnt - 1) / a.C, nh = (smax + 31) / 32;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, c = lane % 4;
     const size_t row0 = (size_t)bh * a.L + tb;
     const __nv_bfloat16 *u = static_cast<const __nv_bfloat16 *>(a.u);
     float *out = a.part + ((size_t)bh * a.tiles + tile) * a.N;
+    for (int i = nh * 32 + tid; i < a.N; i += 256) out[i] = 0.f;
+    if (nh == 0) return;
+    const uint8_t *img = a.kbar_img + (size_t)bh * ((a.N + 63) / 64) * 49152;
+    int it = 0;  // loads so far: half h goes to buffer it % 2
+    auto issue = [&](int h) {
+        const uint32_t dst = smem_addr(Kt) + (it & 1) * M::kHalf;
+        const uint8_t *src = img + (size_t)(h / 2) * 49152 + (h & 1) * 32 * 128;
+        for (int e = tid; e < 3 * PN * 256; e += 256) {
+            const int tp = e / 256, r = e % 256;  // term and panel; 16-byte piece
+            cp16(dst + e * 16, src + (tp / PN) * 16384 + (tp % PN) * 8192 + r * 16, true);
+        }
+        cp_commit();
+        ++it;
+    };
     for (int e = tid; e < kTM * (D / 8); e += 256) {
         const int r = e / (D / 8), pc = e % (D / 8);
         cp16(smem_addr(Ut) + tile_off<UR>(r, pc), u + (row0 + (r < cnt ? r : 0)) * D + pc * 8, r < cnt);
     }
-    cp_commit();
+    issue(0);
     // rows g and g + 8 of the warp's tokens: cached segments, online score
     const int t0 = 16 * warp + g, t1 = t0 + 8;
     const int lim0 = t0 < cnt ? (tb + t0) / a.C : 0, lim1 = t1 < cnt ? (tb + t1) / a.C : 0;
     float m0 = t0 < cnt ? a.r_on[row0 + t0] : 0.f, m1 = t1 < cnt ? a.r_on[row0 + t1] : 0.f, z0 = c == 0 ? 1.f : 0.f, z1 = z0;
     uint32_t au[KS][4];
 
-    auto scores = [&](int b, float (&S)[8][4]) {  // block b: fills S, -inf where a token does not read the segment
-        __syncthreads();  // the last block has been read
-        const uint8_t *img = a.kbar_img + ((size_t)bh * ((a.N + 63) / 64) + b) * 49152;
-        for (int e = tid; e < 3 * PN * 512; e += 256) {
-            const int term = e / (PN * 512), r = e % (PN * 512);
-            cp16(smem_addr(Kt) + e * 16, img + term * 16384 + r * 16, true);
-        }
-        cp_commit();
+    // Half h's scores, -inf where a token does not read the segment; `next` is loaded meanwhile (-1: nothing).
+    auto scores = [&](int h, int next, float (&S)[4][4]) {
         cp_wait<0>();
-        __syncthreads();
-        if (b == 0) {
+        __syncthreads();  // the half has come, and the other buffer has been read
+        const uint32_t kt = smem_addr(Kt) + ((it - 1) & 1) * M::kHalf;
+        if (it == 1) {
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
                 ldsm4(au[ks], smem_addr(Ut) + tile_off<UR>(16 * warp + (lane & 15), 2 * ks + (lane >> 4)));
         }
+        if (next >= 0) issue(next);
 #pragma unroll
-        for (int n = 0; n < 8; ++n)
+        for (int n = 0; n < 4; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) S[n][e] = 0.f;
         const int br = (lane >> 4) * 8 + (lane & 7), bc = (lane >> 3) & 1;
@@ -201,23 +221,23 @@ __global__ void __launch_bounds__(256, 2) gate_mass_tc(CompactArgs a)
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-                for (int n2 = 0; n2 < 4; ++n2) {
-                    if (64 * b + 16 * n2 >= smax) break;
+                for (int n2 = 0; n2 < 2; ++n2) {
+                    if (32 * h + 16 * n2 >= smax) break;
                     uint32_t bf[4];
-                    ldsm4(bf, smem_addr(Kt) + (term * PN + ks / 4) * 8192 + tile_off<128>(16 * n2 + br, 2 * (ks & 3) + bc));
+                    ldsm4(bf, kt + (term * PN + ks / 4) * 4096 + tile_off<128>(16 * n2 + br, 2 * (ks & 3) + bc));
                     mma16816(S[2 * n2], au[ks], bf[0], bf[1]);
                     mma16816(S[2 * n2 + 1], au[ks], bf[2], bf[3]);
                 }
 #pragma unroll
-        for (int n = 0; n < 8; ++n)
+        for (int n = 0; n < 4; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (64 * b + 8 * n + 2 * c + (e & 1) >= (e >> 1 ? lim1 : lim0)) S[n][e] = -INFINITY;
+                if (32 * h + 8 * n + 2 * c + (e & 1) >= (e >> 1 ? lim1 : lim0)) S[n][e] = -INFINITY;
     };
-    auto softmax = [&](const float (&S)[8][4]) {  // running maximum and sum (each lane its own columns)
+    auto softmax = [&](const float (&S)[4][4]) {  // running maximum and sum (each lane its own columns)
         float x0 = m0, x1 = m1;
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
+        for (int n = 0; n < 4; ++n) {
             x0 = fmaxf(x0, fmaxf(S[n][0], S[n][1]));
             x1 = fmaxf(x1, fmaxf(S[n][2], S[n][3]));
         }
@@ -226,7 +246,7 @@ __global__ void __launch_bounds__(256, 2) gate_mass_tc(CompactArgs a)
         m0 = x0;
         m1 = x1;
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
+        for (int n = 0; n < 4; ++n) {
             z0 += __expf(S[n][0] - m0) + __expf(S[n][1] - m0);
             z1 += __expf(S[n][2] - m1) + __expf(S[n][3] - m1);
         }
@@ -245,9 +265,9 @@ __global__ void __launch_bounds__(256, 2) gate_mass_tc(CompactArgs a)
         z0 = 1.f / z0;
         z1 = 1.f / z1;
     };
-    auto gates = [&](int b, const float (&S)[8][4]) {  // sums over the tile's tokens
+    auto gates = [&](int h, const float (&S)[4][4]) {  // sums over the tile's tokens
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
+        for (int n = 0; n < 4; ++n) {
             float s0 = __expf(S[n][0] - m0) * z0 + __expf(S[n][2] - m1) * z1;
             float s1 = __expf(S[n][1] - m0) * z0 + __expf(S[n][3] - m1) * z1;
 #pragma unroll
@@ -261,41 +281,38 @@ __global__ void __launch_bounds__(256, 2) gate_mass_tc(CompactArgs a)
             }
         }
         __syncthreads();
-        if (tid < 64 && 64 * b + tid < a.N) {
+        if (tid < 32 && 32 * h + tid < a.N) {
             float s = 0.f;
 #pragma unroll
             for (int w = 0; w < 8; ++w) s += cols[w][tid];
-            out[64 * b + tid] = s;
+            out[32 * h + tid] = s;
         }
         __syncthreads();
     };
-    float S0[8][4];
-    if (nblk <= 2) {
-        float S1[8][4];
-        if (nblk > 0) {
-            scores(0, S0);
-            softmax(S0);
-        }
-        if (nblk > 1) {
-            scores(1, S1);
-            softmax(S1);
-        }
+    if (nh <= 4) {
+        float S[4][4][4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+            if (h < nh) {
+                scores(h, h + 1 < nh ? h + 1 : -1, S[h]);
+                softmax(S[h]);
+            }
         join();
-        if (nblk > 0) gates(0, S0);
-        if (nblk > 1) gates(1, S1);
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+            if (h < nh) gates(h, S[h]);
     } else {
-        for (int b = 0; b < nblk; ++b) {
-            scores(b, S0);
-            softmax(S0);
+        float S[4][4];
+        for (int h = 0; h < nh; ++h) {
+            scores(h, h + 1 < nh ? h + 1 : 0, S);
+            softmax(S);
         }
         join();
-        for (int b = 0; b < nblk; ++b) {
-            scores(b, S0);
-            gates(b, S0);
+        for (int h = 0; h < nh; ++h) {
+            scores(h, h + 1 < nh ? h + 1 : -1, S);
+            gates(h, S);
         }
     }
-    for (int i = nblk * 64 + tid; i < a.N; i += 256) out[i] = 0.f;
-    cp_wait<0>();
 }
 
 // mass_i: the tiles' sums, 32 strided shares of the tiles, joined in a fixed order.
@@ -404,9 +421,9 @@ cudaError_t mass_impl(const Problem &p, const CompactArgs &a, cudaStream_t s)
 template <int D>
 cudaError_t mass_tc_impl(const Problem &p, const CompactArgs &a, cudaStream_t s)
 {
-    const size_t smem = kTM * (D * 2 < 128 ? 128 : D * 2) + 3 * (D > 64 ? 2 : 1) * 8192;
+    constexpr int smem = MassSmem<D>::kTotal;
     auto kern = gate_mass_tc<D>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)((long long)p.BH * a.tiles), 256, smem, s>>>(a);
     return cudaGetLastError();

@@ -190,12 +190,14 @@ __global__ void __launch_bounds__(32 * RowSplit<D>::W) delta_rscan_simt(DeltaArg
     const T *la = static_cast<const T *>(a.la) + sbase, *be = static_cast<const T *>(a.be) + sbase;
     T *dv = static_cast<T *>(a.dv) + base;
     float N[R::KPL], kx[R::KPL], qx[R::KPL];
-    if (a.G && seg < a.N - 1)
-        load_keys<D>(N, a.G + ((size_t)bh * a.N + seg) * D * D + (size_t)row * D, g);
-    else {
 #pragma unroll
-        for (int i = 0; i < R::KPL; ++i) N[i] = 0.f;
-    }
+    for (int i = 0; i < R::KPL; ++i) N[i] = 0.f;
+    if (a.G && seg < a.N - 1)
+        for (int part = 0; part < a.g_parts; ++part) {
+            load_keys<D>(kx, a.G + (((size_t)part * a.BH + bh) * a.N + seg) * D * D + (size_t)row * D, g);
+#pragma unroll
+            for (int i = 0; i < R::KPL; ++i) N[i] += kx[i];
+        }
     const int nt = (t1 - t0 + R::TT - 1) / R::TT;
     constexpr int NL = (R::TT * D + NT - 1) / NT, NV = (R::TT * R::RC + NT - 1) / NT;
     T kn[NL], qn[NL], pn[NV], an, bn;

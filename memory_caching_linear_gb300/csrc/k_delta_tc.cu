@@ -1182,12 +1182,17 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
     float in = 0.f;  // <R, S>
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
+        uint4 s4[64 * PIECES / kGradThreads];  // this thread's pieces of S again, for <R, S>, while R comes
+#pragma unroll
+        for (int x = 0; x < 64 * PIECES / kGradThreads; ++x)
+            s4[x] = *reinterpret_cast<const uint4 *>(S + (size_t)(64 * mb * PIECES + tid + x * kGradThreads) * 8);
         cp_wait<0>();
         __syncthreads();
-        for (int e = tid; e < 64 * PIECES; e += kGradThreads) {
+#pragma unroll
+        for (int x = 0; x < 64 * PIECES / kGradThreads; ++x) {
+            const int e = tid + x * kGradThreads;
             const uint4 r4 = *reinterpret_cast<const uint4 *>(Mt + tile_off<ROW>(e / PIECES, e % PIECES));
-            const uint4 s4 = *reinterpret_cast<const uint4 *>(S + (size_t)(64 * mb * PIECES + e) * 8);
-            const uint32_t *rw = reinterpret_cast<const uint32_t *>(&r4), *sw = reinterpret_cast<const uint32_t *>(&s4);
+            const uint32_t *rw = reinterpret_cast<const uint32_t *>(&r4), *sw = reinterpret_cast<const uint32_t *>(&s4[x]);
 #pragma unroll
             for (int q = 0; q < 4; ++q) in = fmaf(low_f(rw[q]), low_f(sw[q]), fmaf(high_f(rw[q]), high_f(sw[q]), in));
         }

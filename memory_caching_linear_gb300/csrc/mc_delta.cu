@@ -1,5 +1,6 @@
 // mc_delta.cu -- the entry points of the gated delta memory and of the evicting decode cache
 // (include/mc.h): argument checks, scratch, and the choice of kernels.
+#include <algorithm>
 #include <cstdint>
 
 #include "mc_internal.cuh"
@@ -229,6 +230,13 @@ int forward_delta(const void *q, const void *k, const void *v, const void *u, co
     return e == cudaSuccess && ef == cudaSuccess ? MC_OK : fail(e != cudaSuccess ? e : ef);
 }
 
+// Shares of the tokens for the CUDA-core G: two CTAs for every SM where there are few heads and segments.
+int simt_G_parts(const Problem &p)
+{
+    const long long ctas = (long long)p.BH * (p.N - 1);
+    return ctas >= 304 ? 1 : (int)std::min<long long>(8, (304 + ctas - 1) / ctas);
+}
+
 int backward_delta(const void *q, const void *k, const void *v, const void *u, const void *la, const void *be,
                    const void *dy, int B, int H, int L, int d, int seg_len, int agg_mode, int topk, void *dq, void *dk,
                    void *dv, void *du, void *dla, void *dbe, bool bf16, cudaStream_t s)
@@ -274,7 +282,7 @@ int backward_delta(const void *q, const void *k, const void *v, const void *u, c
         a.states = cv.take<float>(BH * N * d * d, many);
         a.O_on = cv.take<float>(BH * L * d, many && !rtc);
         t.y = cv.take<__nv_bfloat16>(BH * L * d, rtc);
-        t.g_parts = rtc ? bwd_G_parts(p) : 1;
+        b.g_parts = a.g_parts = t.g_parts = rtc ? bwd_G_parts(p) : many ? simt_G_parts(p) : 1;
         G = cv.take<float>(t.g_parts * BH * N * d * d, many);
         tok = cv.take<float>(BH * L * kBwdTokWords, many);
         dq_add = cv.take<float>(BH * L * d, many);

@@ -245,6 +245,7 @@ struct BwdArgs {
     int Np;               // N rounded up to a multiple of 16
     float *kpre_tiles;    // [BH][N][ceil(C/64)][d] keys of each segment before each 64-token tile, or null
     float *kv_gw;         // [2][BH][L] the online gate and the pooled-key weight w per token (tensor-core path)
+    int g_parts;          // CUDA-core path: G as that many summands, one after the other, over shares of the later tokens (0: one)
     int BH, L, C, N, mode, topk;
 };
 size_t backward_scratch_bytes(const Problem &p);
@@ -293,7 +294,8 @@ struct DeltaArgs {
     void *dq, *dk, *dv, *dla, *dbe;  // gradients
     float *E, *W;                    // [BH][L][d] e_t, w_t (fp32 scratch; E null: not kept)
     float *S_c, *R_c;                // [BH][N][NCH][d][d] memory before / adjoint after every chunk (S_c null: not kept)
-    const float *G;                  // [BH][N][d][d] adjoint of the cached states, or null
+    const float *G;                  // g_parts x [BH][N][d][d]: the adjoint of the cached states as a sum, or null
+    int g_parts;
     const float *tok;                // [BH][L][kBwdTokWords] online gate (word 2), pooled-key weight (4), or null (1, 0)
     const float *dq_add;             // [BH][L][d] added to dq, or null
     const float *rho;                // [BH][N][NCH][d] later tokens' pooled-key gradient after every chunk, or null
