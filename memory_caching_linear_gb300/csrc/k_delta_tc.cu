@@ -378,45 +378,56 @@ __device__ __forceinline__ uint32_t own_off(int r, int pc, int warp)
     return (uint32_t)(r * NW * 32 + (((2 * warp + pc) ^ (r & (VP < 8 ? VP - 1 : 7))) << 4));
 }
 
-// 16 values x 64 tokens in operand registers to rows of 16 values.
-template <int NW, int D>
-__device__ __forceinline__ void put_tokens(__nv_bfloat16 *dst, const uint32_t (&f)[4][4], uint8_t *vt, int cnt, int warp, int lane)
+// 16 values x 64 tokens in operand registers to rows of 16 values.  Where two warps hold the same values (KP = 2), each
+// writes half of the tokens.
+template <int NW, int KP, int D>
+__device__ __forceinline__ void put_tokens(__nv_bfloat16 *dst, const uint32_t (&f)[4][4], uint8_t *vt, int cnt, int wr, int kp, int lane)
 {
     const uint32_t at = smem_addr(vt);
 #pragma unroll
     for (int k4 = 0; k4 < 4; ++k4)
-        stsm4t(at + own_off<NW>(16 * k4 + (lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1, warp), f[k4][0], f[k4][1], f[k4][2], f[k4][3]);
+        if (KP == 1 || k4 / 2 == kp)
+            stsm4t(at + own_off<NW>(16 * k4 + (lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1, wr), f[k4][0], f[k4][1], f[k4][2], f[k4][3]);
     __syncwarp();
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
         const int r = 16 * x + lane / 2, pc = lane % 2;
-        if (r < cnt) *reinterpret_cast<uint4 *>(dst + (size_t)r * D + 8 * pc) = *reinterpret_cast<const uint4 *>(vt + own_off<NW>(r, pc, warp));
+        if ((KP == 1 || x / 2 == kp) && r < cnt)
+            *reinterpret_cast<uint4 *>(dst + (size_t)r * D + 8 * pc) = *reinterpret_cast<const uint4 *>(vt + own_off<NW>(r, pc, wr));
     }
     __syncwarp();
 }
 
-// f times a warp's 16 rows, 64 columns at a time: `put` takes (panel, row, piece, 16 bytes).  Row r's piece pc is
-// staged in row 16 (pc / 2) + r of the tile.
-template <int NW, int NT, typename F>
-__device__ __forceinline__ void put_rows(const float (&S)[NT][4], float f, uint8_t *vt, int warp, int lane, F put)
+// f times a warp's 16 rows in bf16: neighbouring lanes exchange halves of two tiles, so that a row's four lanes hold 32
+// bytes in a run.  `put` takes (row, tile of 8 columns, byte within the tile's 16, 8 bytes).
+template <int NT, typename F>
+__device__ __forceinline__ void put_rows(const float (&S)[NT][4], float f, int lane, F put)
 {
-    const uint32_t at = smem_addr(vt);
+    const int g = lane / 4, c = lane % 4;
 #pragma unroll
-    for (int h = 0; h < NT / 8; ++h) {
+    for (int n = 0; n < NT; n += 2)
 #pragma unroll
-        for (int n = 0; n < 8; n += 2) {
-            const float(&s0)[4] = S[8 * h + n], (&s1)[4] = S[8 * h + n + 1];
-            stsm4(at + own_off<NW>(8 * n + (lane & 15), lane >> 4, warp), pack2(f * s0[0], f * s0[1]), pack2(f * s0[2], f * s0[3]),
-                  pack2(f * s1[0], f * s1[1]), pack2(f * s1[2], f * s1[3]));
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t p0 = pack2(f * S[n][2 * h], f * S[n][2 * h + 1]), p1 = pack2(f * S[n + 1][2 * h], f * S[n + 1][2 * h + 1]);
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, c & 1 ? p0 : p1, 1);
+            put(g + 8 * h, n + (c & 1), 8 * (c >> 1), c & 1 ? make_uint2(got, p1) : make_uint2(p0, got));
         }
-        __syncwarp();
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const int r = 4 * x + lane / 8, pc = lane % 8;
-            put(h, r, pc, *reinterpret_cast<const uint4 *>(vt + own_off<NW>(16 * (pc / 2) + r, pc & 1, warp)));
-        }
-        __syncwarp();
-    }
+}
+
+// Two warps that hold the two halves of the keys of 16 rows add their partial products: each leaves its own in xb,
+// and adds the other's (tiles with `mine` only).
+template <typename F, typename G>
+__device__ __forceinline__ void pair_sum(float4 *xb, int warp, int lane, F each, G add)
+{
+    each([&](int i, const float (&x)[4]) { xb[(warp * 16 + i) * 32 + lane] = make_float4(x[0], x[1], x[2], x[3]); });
+    asm volatile("bar.sync %0, 64;" ::"r"(1 + warp / 2) : "memory");
+    add([&](int i, float (&x)[4]) {
+        const float4 y = xb[((warp ^ 1) * 16 + i) * 32 + lane];
+        x[0] += y.x;
+        x[1] += y.y;
+        x[2] += y.z;
+        x[3] += y.w;
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -431,11 +442,11 @@ struct WalkSmem {
     static constexpr int kTotal = 2 * kStage;
 };
 
-template <int D, int NW, bool READ, bool FULL>
-__global__ void __launch_bounds__(32 * NW, NW == 4 ? (READ ? 2 : 3) : 1) delta_walk_tc(DeltaTcArgs a)
+template <int D, int NW, int KP, bool READ, bool FULL>
+__global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) delta_walk_tc(DeltaTcArgs a)
 {
     using W = WalkSmem<D, NW, READ>;
-    constexpr int ROW = D * 2, PIECES = D / 8, NT = 32 * NW, KS = D / 16, VP = NW * 2;
+    constexpr int ROW = D * 2, PIECES = D / 8, NT = 32 * NW * KP, KS = D / 16 / KP, VP = NW * 2;
     extern __shared__ __align__(16) uint8_t sm[];
     constexpr int splits = D / (16 * NW);
     const int rs = (int)blockIdx.x % splits;
@@ -444,6 +455,7 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? (READ ? 2 : 3) : 1) delta_w
     const int t0 = seg * a.C, len = min((seg + 1) * a.C, a.L) - t0, nch = (len + kCH - 1) / kCH;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, c = lane % 4;
     const int vbase = rs * 16 * NW;  // the CTA's first value row
+    const int wr = warp / KP, kp = KP == 1 ? 0 : warp % KP, k0 = kp * KS;  // the warp's rows, its share of the keys
 
     auto load = [&](int ch) {
         uint8_t *st = sm + (ch & 1) * W::kStage;
@@ -466,7 +478,7 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? (READ ? 2 : 3) : 1) delta_w
         cp_commit();
     };
 
-    float S[2 * KS][4];  // 16 rows x D keys: tile n holds keys 8n ..
+    float S[2 * KS][4];  // 16 rows x D / KP keys: tile n holds keys 16 k0 + 8 n ..
 #pragma unroll
     for (int n = 0; n < 2 * KS; ++n)
 #pragma unroll
@@ -502,7 +514,7 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? (READ ? 2 : 3) : 1) delta_w
 #pragma unroll
             for (int n2 = 0; n2 < 4; ++n2) {
                 uint32_t b[4];
-                ldsm4(b, kt + tile_off<ROW>(16 * n2 + br, 2 * ks + bc));
+                ldsm4(b, kt + tile_off<ROW>(16 * n2 + br, 2 * (k0 + ks) + bc));
                 mma16816(X[2 * n2], hi, b[0], b[1]);
                 mma16816(X[2 * n2 + 1], hi, b[2], b[3]);
                 if (FULL) {
@@ -510,48 +522,58 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? (READ ? 2 : 3) : 1) delta_w
                     mma16816(X[2 * n2 + 1], lo, b[2], b[3]);
                 }
                 if (READ) {  // the output is bf16: one term
-                    ldsm4(b, qt + tile_off<ROW>(16 * n2 + br, 2 * ks + bc));
+                    ldsm4(b, qt + tile_off<ROW>(16 * n2 + br, 2 * (k0 + ks) + bc));
                     mma16816(O[2 * n2], hi, b[0], b[1]);
                     mma16816(O[2 * n2 + 1], hi, b[2], b[3]);
                 }
             }
         }
+        uint32_t v4[4][4];
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4)
+            ldsm4t(v4[k4], vt + own_off<NW>(16 * k4 + (lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1, wr));
+        if (KP == 2)
+            pair_sum(reinterpret_cast<float4 *>(sm + 2 * W::kStage), warp, lane,
+                     [&](auto leave) {
+#pragma unroll
+                         for (int n = 0; n < 8; ++n) {
+                             leave(n, X[n]);
+                             if (READ && n / 4 != kp) leave(8 + n % 4, O[n]);
+                         }
+                     },
+                     [&](auto add) {
+#pragma unroll
+                         for (int n = 0; n < 8; ++n) {
+                             add(n, X[n]);
+                             if (READ && n / 4 == kp) add(8 + n % 4, O[n]);
+                         }
+                     });
+        else __syncwarp();  // the warp's part of V is free
         // R = V - diag(exp c) K S^T, then E = R + (T - 1) R
 #pragma unroll
-        for (int kt4 = 0; kt4 < 4; ++kt4) {
-            uint32_t v4[4];
-            {
-                const int r = 16 * kt4 + (lane >> 4) * 8 + (lane & 7), pc = 2 * warp + ((lane >> 3) & 1);
-                ldsm4t(v4, vt + own_off<NW>(r, pc, 0));
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int n = 2 * kt4 + h;
-                const float2 ga = *reinterpret_cast<const float2 *>(vec + 8 * n + 2 * c);
-                X[n][0] = low_f(v4[2 * h]) - ga.x * X[n][0];
-                X[n][1] = high_f(v4[2 * h]) - ga.y * X[n][1];
-                X[n][2] = low_f(v4[2 * h + 1]) - ga.x * X[n][2];
-                X[n][3] = high_f(v4[2 * h + 1]) - ga.y * X[n][3];
-                if (READ) {
-                    O[n][0] *= ga.x;
-                    O[n][1] *= ga.y;
-                    O[n][2] *= ga.x;
-                    O[n][3] *= ga.y;
-                }
+        for (int n = 0; n < 8; ++n) {
+            const uint32_t lo2 = v4[n / 2][2 * (n & 1)], hi2 = v4[n / 2][2 * (n & 1) + 1];
+            const float2 ga = *reinterpret_cast<const float2 *>(vec + 8 * n + 2 * c);
+            X[n][0] = low_f(lo2) - ga.x * X[n][0];
+            X[n][1] = high_f(lo2) - ga.y * X[n][1];
+            X[n][2] = low_f(hi2) - ga.x * X[n][2];
+            X[n][3] = high_f(hi2) - ga.y * X[n][3];
+            if (READ) {
+                O[n][0] *= ga.x;
+                O[n][1] *= ga.y;
+                O[n][2] *= ga.x;
+                O[n][3] *= ga.y;
             }
         }
-        __syncwarp();  // the warp's part of V is free
         if (a.spre_img && ch > 0 && !(ch & 1)) {  // panels of 64 columns, their pieces exchanged by row % 8
-            uint8_t *img = a.spre_img + ((size_t)sid * (a.C / 128) + ch / 2) * (D * D * 2) + (vbase + 16 * warp) * 128;
-            put_rows<NW>(S, vec[0], vown, warp, lane, [&](int h, int r, int pc, const uint4 &x) {
-                *reinterpret_cast<uint4 *>(img + h * (D * 128) + tile_off<128>(r, pc)) = x;
+            uint8_t *img = a.spre_img + ((size_t)sid * (a.C / 128) + ch / 2) * (D * D * 2) + (vbase + 16 * wr) * 128;
+            put_rows(S, vec[0], lane, [&](int r, int n, int at, const uint2 &x) {
+                *reinterpret_cast<uint2 *>(img + (2 * k0 + n) / 8 * (D * 128) + tile_off<128>(r, (2 * k0 + n) % 8) + at) = x;
             });
         }
         if (a.S_c) {  // the memory before the chunk
-            __nv_bfloat16 *dst = a.S_c + (cidx * D + vbase + 16 * warp) * D;
-            put_rows<NW>(S, 1.f, vown, warp, lane, [&](int h, int r, int pc, const uint4 &x) {
-                *reinterpret_cast<uint4 *>(dst + (size_t)r * D + 64 * h + pc * 8) = x;
-            });
+            __nv_bfloat16 *dst = a.S_c + (cidx * D + vbase + 16 * wr) * D + 16 * k0;
+            put_rows(S, 1.f, lane, [&](int r, int n, int at, const uint2 &x) { *reinterpret_cast<uint2 *>(dst + (size_t)r * D + 8 * n + at / 2) = x; });
         }
         {
             uint32_t rh[4][4], rl[4][4];
@@ -591,12 +613,13 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? (READ ? 2 : 3) : 1) delta_w
             for (int k4 = 0; k4 < 4; ++k4)
 #pragma unroll
                 for (int n = 2 * k4; n < 8; ++n) {
+                    if (KP == 2 && n / 4 != kp) continue;
                     const uint2 b = pt[(tile_base(n) + k4) * 32];
                     mma16816(O[n], uh[k4], b.x, b.y);
                 }
         }
         auto put = [&](__nv_bfloat16 *dst, const uint32_t (&f)[4][4]) {
-            put_tokens<NW, D>(dst + row0 * D + vbase + 16 * warp, f, vown, cnt, warp, lane);
+            put_tokens<NW, KP, D>(dst + row0 * D + vbase + 16 * wr, f, vown, cnt, wr, kp, lane);
         };
         if (a.U) put(a.U, uh);
         if (READ) {
@@ -612,8 +635,8 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? (READ ? 2 : 3) : 1) delta_w
                 for (int n = 0; n < 8; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int t = 8 * n + 2 * c + (e & 1), r = vbase + 16 * warp + g + 8 * (e >> 1);
-                        if (t < cnt) a.O_on[(row0 + t) * D + r] = O[n][e];
+                        const int t = 8 * n + 2 * c + (e & 1), r = vbase + 16 * wr + g + 8 * (e >> 1);
+                        if ((KP == 1 || n / 4 == kp) && t < cnt) a.O_on[(row0 + t) * D + r] = O[n][e];
                     }
             }
         }
@@ -642,7 +665,7 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? (READ ? 2 : 3) : 1) delta_w
 #pragma unroll
             for (int n2 = 0; n2 < KS; ++n2) {
                 uint32_t b[4];
-                ldsm4t(b, kt + tile_off<ROW>(16 * k4 + tr, 2 * n2 + tc));
+                ldsm4t(b, kt + tile_off<ROW>(16 * k4 + tr, 2 * (k0 + n2) + tc));
                 mma16816(S[2 * n2], uh[k4], b[0], b[1]);
                 mma16816(S[2 * n2 + 1], uh[k4], b[2], b[3]);
                 if (FULL) {
@@ -652,13 +675,13 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? (READ ? 2 : 3) : 1) delta_w
             }
     }
     if (a.states_img) {
-        uint8_t *img = a.states_img + (size_t)sid * (D * D * 2) + (vbase + 16 * warp) * 128;
-        put_rows<NW>(S, 1.f, sm + ((nch - 1) & 1) * W::kStage + W::kK, warp, lane, [&](int h, int r, int pc, const uint4 &x) {
-            *reinterpret_cast<uint4 *>(img + h * (D * 128) + tile_off<128>(r, pc)) = x;
+        uint8_t *img = a.states_img + (size_t)sid * (D * D * 2) + (vbase + 16 * wr) * 128;
+        put_rows(S, 1.f, lane, [&](int r, int n, int at, const uint2 &x) {
+            *reinterpret_cast<uint2 *>(img + (2 * k0 + n) / 8 * (D * 128) + tile_off<128>(r, (2 * k0 + n) % 8) + at) = x;
         });
     }
     if (a.states) {
-        float *dst = a.states + ((size_t)sid * D + vbase + 16 * warp) * D;
+        float *dst = a.states + ((size_t)sid * D + vbase + 16 * wr) * D + 16 * k0;
 #pragma unroll
         for (int n = 0; n < 2 * KS; ++n) {
             *reinterpret_cast<float2 *>(dst + (size_t)g * D + 8 * n + 2 * c) = make_float2(S[n][0], S[n][1]);
@@ -681,11 +704,11 @@ struct RWalkSmem {
     static constexpr int kTotal = 2 * kStage;
 };
 
-template <int D, int NW>
-__global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1) delta_rwalk_tc(DeltaTcArgs a)
+template <int D, int NW, int KP>
+__global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(DeltaTcArgs a)
 {
     using W = RWalkSmem<D, NW>;
-    constexpr int ROW = D * 2, PIECES = D / 8, NT = 32 * NW, KS = D / 16, VP = NW * 2;
+    constexpr int ROW = D * 2, PIECES = D / 8, NT = 32 * NW * KP, KS = D / 16 / KP, VP = NW * 2;
     extern __shared__ __align__(16) uint8_t sm[];
     constexpr int splits = D / (16 * NW);
     const int rs = (int)blockIdx.x % splits;
@@ -694,6 +717,7 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1) delta_rwalk_tc(Delta
     const int t0 = seg * a.C, len = min((seg + 1) * a.C, a.L) - t0, nch = (len + kCH - 1) / kCH;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, c = lane % 4;
     const int vbase = rs * 16 * NW;
+    const int wr = warp / KP, kp = KP == 1 ? 0 : warp % KP, k0 = kp * KS;
 
     auto load = [&](int ch) {
         uint8_t *st = sm + (ch & 1) * W::kStage;
@@ -722,7 +746,7 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1) delta_rwalk_tc(Delta
 #pragma unroll
         for (int n = 0; n < 2 * KS; ++n) R[n][0] = R[n][1] = R[n][2] = R[n][3] = 0.f;
         for (int part = 0; part < a.g_parts; ++part) {
-            const float *src = a.G + (((size_t)part * a.BH * a.N + sid) * D + vbase + 16 * warp) * D;
+            const float *src = a.G + (((size_t)part * a.BH * a.N + sid) * D + vbase + 16 * wr) * D + 16 * k0;
 #pragma unroll
             for (int n = 0; n < 2 * KS; ++n) {
                 const float2 x = *reinterpret_cast<const float2 *>(src + (size_t)g * D + 8 * n + 2 * c);
@@ -762,41 +786,47 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1) delta_rwalk_tc(Delta
 #pragma unroll
             for (int n2 = 0; n2 < 4; ++n2) {
                 uint32_t b[4];
-                ldsm4(b, kt + tile_off<ROW>(16 * n2 + br, 2 * ks + bc));
+                ldsm4(b, kt + tile_off<ROW>(16 * n2 + br, 2 * (k0 + ks) + bc));
                 mma16816(X[2 * n2], rf, b[0], b[1]);
                 mma16816(X[2 * n2 + 1], rf, b[2], b[3]);
             }
         }
+        uint32_t v4[4][4];
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4)
+            ldsm4t(v4[k4], vt + own_off<NW>(16 * k4 + (lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1, wr));
+        if (KP == 2)
+            pair_sum(reinterpret_cast<float4 *>(sm + 2 * W::kStage), warp, lane,
+                     [&](auto leave) {
+#pragma unroll
+                         for (int n = 0; n < 8; ++n) leave(n, X[n]);
+                     },
+                     [&](auto add) {
+#pragma unroll
+                         for (int n = 0; n < 8; ++n) add(n, X[n]);
+                     });
+        else __syncwarp();  // the warp's part of dy is free
         uint32_t pf[4][4], pg[4][4];  // p, and exp(c) p
 #pragma unroll
-        for (int k4 = 0; k4 < 4; ++k4) {
-            uint32_t v4[4];
-            const int r = 16 * k4 + (lane >> 4) * 8 + (lane & 7), pc = 2 * warp + ((lane >> 3) & 1);
-            ldsm4t(v4, vt + own_off<NW>(r, pc, 0));
+        for (int n = 0; n < 8; ++n) {
+            const float2 re = *reinterpret_cast<const float2 *>(vec + 64 + 8 * n + 2 * c);
+            const float2 ga = *reinterpret_cast<const float2 *>(vec + 8 * n + 2 * c);
+            const float2 go = *reinterpret_cast<const float2 *>(gs + 8 * n + 2 * c);
+            X[n][0] *= re.x;
+            X[n][1] *= re.y;
+            X[n][2] *= re.x;
+            X[n][3] *= re.y;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int n = 2 * k4 + h;
-                const float2 re = *reinterpret_cast<const float2 *>(vec + 64 + 8 * n + 2 * c);
-                const float2 ga = *reinterpret_cast<const float2 *>(vec + 8 * n + 2 * c);
-                const float2 go = *reinterpret_cast<const float2 *>(gs + 8 * n + 2 * c);
-                X[n][0] *= re.x;
-                X[n][1] *= re.y;
-                X[n][2] *= re.x;
-                X[n][3] *= re.y;
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    const float p0 = go.x * low_f(v4[2 * h + z]), p1 = go.y * high_f(v4[2 * h + z]);
-                    pf[k4][2 * h + z] = pack2(p0, p1);
-                    pg[k4][2 * h + z] = pack2(ga.x * p0, ga.y * p1);
-                }
+            for (int z = 0; z < 2; ++z) {
+                const int q = 2 * (n & 1) + z;
+                const float p0 = go.x * low_f(v4[n / 2][q]), p1 = go.y * high_f(v4[n / 2][q]);
+                pf[n / 2][q] = pack2(p0, p1);
+                pg[n / 2][q] = pack2(ga.x * p0, ga.y * p1);
             }
         }
-        __syncwarp();  // the warp's part of dy is free
         {  // the adjoint after the chunk
-            __nv_bfloat16 *dst = a.R_c + (((size_t)sid * a.NCH + ch) * D + vbase + 16 * warp) * D;
-            put_rows<NW>(R, 1.f, vown, warp, lane, [&](int h, int r, int pc, const uint4 &x) {
-                *reinterpret_cast<uint4 *>(dst + (size_t)r * D + 64 * h + pc * 8) = x;
-            });
+            __nv_bfloat16 *dst = a.R_c + (((size_t)sid * a.NCH + ch) * D + vbase + 16 * wr) * D + 16 * k0;
+            put_rows(R, 1.f, lane, [&](int r, int n, int at, const uint2 &x) { *reinterpret_cast<uint2 *>(dst + (size_t)r * D + 8 * n + at / 2) = x; });
         }
         const uint2 *lt = reinterpret_cast<const uint2 *>(rec) + lane;
         const uint2 *pt = reinterpret_cast<const uint2 *>(rec + kRecP) + lane;
@@ -833,7 +863,7 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1) delta_rwalk_tc(Delta
             wf[n / 2][2 * (n & 1)] = pack2(X[n][0], X[n][1]);
             wf[n / 2][2 * (n & 1) + 1] = pack2(X[n][2], X[n][3]);
         }
-        put_tokens<NW, D>(a.dv + row0 * D + vbase + 16 * warp, wf, vown, cnt, warp, lane);
+        put_tokens<NW, KP, D>(a.dv + row0 * D + vbase + 16 * wr, wf, vown, cnt, wr, kp, lane);
 #pragma unroll
         for (int n = 0; n < 8; ++n) {  // -exp(c) w
             const float2 ga = *reinterpret_cast<const float2 *>(vec + 8 * n + 2 * c);
@@ -851,10 +881,10 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1) delta_rwalk_tc(Delta
 #pragma unroll
             for (int n2 = 0; n2 < KS; ++n2) {
                 uint32_t b[4];
-                ldsm4t(b, kt + tile_off<ROW>(16 * k4 + tr, 2 * n2 + tc));
+                ldsm4t(b, kt + tile_off<ROW>(16 * k4 + tr, 2 * (k0 + n2) + tc));
                 mma16816(R[2 * n2], wf[k4], b[0], b[1]);
                 mma16816(R[2 * n2 + 1], wf[k4], b[2], b[3]);
-                ldsm4t(b, qt + tile_off<ROW>(16 * k4 + tr, 2 * n2 + tc));
+                ldsm4t(b, qt + tile_off<ROW>(16 * k4 + tr, 2 * (k0 + n2) + tc));
                 mma16816(R[2 * n2], pg[k4], b[0], b[1]);
                 mma16816(R[2 * n2 + 1], pg[k4], b[2], b[3]);
             }
@@ -1300,21 +1330,26 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
     }
 }
 
-template <int D, int NW>
+// Few walkers leave most of the card idle, and a chunk's products on a walker's way to the next chunk are what counts: then
+// two warps share 16 rows, half of the keys each.  KP = 2 with two row groups per CTA where all its CTAs fit at two
+// per SM (L = 4096, 32 heads, d = 128: see the measurements at the launch), else four row groups and whole rows.
+inline bool split_keys(const Problem &p) { return (long long)p.BH * p.N * (p.d / 32) <= 304; }
+
+template <int D, int NW, int KP>
 cudaError_t rwalk_launch(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
 {
-    constexpr int smem = RWalkSmem<D, NW>::kTotal;
-    auto kern = delta_rwalk_tc<D, NW>;
+    constexpr int smem = RWalkSmem<D, NW>::kTotal + (KP == 2 ? 2 * NW * 8192 : 0);
+    auto kern = delta_rwalk_tc<D, NW, KP>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)((long long)p.BH * p.N * (D / (16 * NW))), 32 * NW, smem, s>>>(a);
+    kern<<<(unsigned)((long long)p.BH * p.N * (D / (16 * NW))), 32 * NW * KP, smem, s>>>(a);
     return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t grads_tc_impl(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
 {
-    cudaError_t e = rwalk_launch<D, 4>(p, a, s);
+    cudaError_t e = split_keys(p) ? rwalk_launch<D, 2, 2>(p, a, s) : rwalk_launch<D, 4, 1>(p, a, s);
     if (e != cudaSuccess) return e;
     profile_after_kernel(s, "delta_rwalk_tc");
     constexpr int smem = GradSmem<D>::kTotal;
@@ -1365,15 +1400,21 @@ cudaError_t prep_impl(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
     return cudaGetLastError();
 }
 
-template <int D, int NW, bool READ, bool FULL>
+template <int D, int NW, int KP, bool READ, bool FULL>
 cudaError_t walk_launch(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
 {
-    constexpr int smem = WalkSmem<D, NW, READ>::kTotal;
-    auto kern = delta_walk_tc<D, NW, READ, FULL>;
+    constexpr int smem = WalkSmem<D, NW, READ>::kTotal + (KP == 2 ? 2 * NW * 8192 : 0);
+    auto kern = delta_walk_tc<D, NW, KP, READ, FULL>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)((long long)p.BH * p.N * (D / (16 * NW))), 32 * NW, smem, s>>>(a);
+    kern<<<(unsigned)((long long)p.BH * p.N * (D / (16 * NW))), 32 * NW * KP, smem, s>>>(a);
     return cudaGetLastError();
+}
+
+template <int D, bool READ, bool FULL>
+cudaError_t walk_kp(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
+{
+    return split_keys(p) ? walk_launch<D, 2, 2, READ, FULL>(p, a, s) : walk_launch<D, 4, 1, READ, FULL>(p, a, s);
 }
 
 template <int D, bool READ>
@@ -1382,7 +1423,7 @@ cudaError_t walk_impl(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
     cudaError_t e = a.rrec ? prep_impl<D, READ, true>(p, a, s) : prep_impl<D, READ, false>(p, a, s);
     if (e != cudaSuccess) return e;
     profile_after_kernel(s, "delta_prep_tc");
-    e = a.full ? walk_launch<D, 4, READ, true>(p, a, s) : walk_launch<D, 4, READ, false>(p, a, s);
+    e = a.full ? walk_kp<D, READ, true>(p, a, s) : walk_kp<D, READ, false>(p, a, s);
     profile_after_kernel(s, "delta_walk_tc");
     return e;
 }

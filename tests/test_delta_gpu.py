@@ -233,3 +233,18 @@ def test_nothing_is_written_behind_the_outputs():
     mcl.mc_backward_delta(*x, torch.ones_like(x[0]), C, GRM, **outs)
     for b, t in zip(big, x):
         assert (b[t.numel():] == 3.0).all()
+
+
+@pytest.mark.parametrize("d,C,L", [(64, 30, 310), (128, 70, 350), (128, 128, 640), (64, 128, 1280)])
+def test_many_heads_and_segments(d, C, L):
+    """Enough walkers to fill the card: one warp per 16 rows instead of two."""
+    x = make_delta_inputs(2, 8, L, d, C, 61, "bf16")
+    y, st = forward(*x, C, GRM)
+    gy, gst = mcl.mc_forward_delta(*cuda(x), C, GRM)
+    assert rel(gy, y) <= TOL["bf16"] and rel(gst, st) <= STATE_TOL
+    assert rel(mcl.mc_forward_delta(*cuda(x), C, GRM, want_states=False)[0], y) <= TOL["bf16"]
+    dy = torch.randn(x[0].shape, generator=torch.Generator().manual_seed(8)).to(x[0].dtype)
+    got = mcl.mc_backward_delta(*cuda(x), dy.cuda(), C, GRM)
+    assert mcl.mc_check_device() == mcl.MC_OK
+    for name, g, w in zip(("dq", "dk", "dv", "du", "dlog_alpha", "dbeta"), got, backward(*x, dy, C, GRM)):
+        assert rel(g, w) <= TOL["bf16"], name
