@@ -14,11 +14,11 @@
 // short and each is small, and an accumulator in tensor memory would have to be read back, split and
 // written to shared memory between any two of them.
 //
-// Precision: the memory is held in fp32.  A call that returns the fp32 states (FULL) takes every operand that is
-// not an input as two bf16 terms (products of two lows left out: 2^-17 of a term), which leaves the states 4e-6
-// off; one term would put 2^-9 of the memory into every later error.  Where only bf16 results come out (y alone, the
-// gradients) one term each is enough: errors against 64 bits grow from 3.2e-3 to 3.5e-3 of y and from 4.0e-3 to
-// 4.1e-3 of the worst gradient, and the walk takes 0.35 instead of 0.46 ms at the long workload.
+// Precision: the memory is held in fp32, and every operand that is not an input enters the products in two bf16
+// terms, products of two lows left out: 2^-17 of a term (the inverse in three, 2^-25).  The errors e_j of keys that
+// resemble each other are large and cancel in S and in O, so one term (2^-9) would show: at keys with a cosine of 0.8 it
+// leaves the memory 7e-3 and y 9e-3 off, as against 2e-5 and 1.4e-3, the last bf16 rounding.  The gradients' own walk reads
+// S in one term (S 4e-4 off there): they pass through bf16 states and errors anyway.
 #include <cstdint>
 
 #include "mc_internal.cuh"
@@ -36,17 +36,17 @@ constexpr int kTiles = 20;
 __host__ __device__ constexpr int tile_base(int nt) { return nt / 2 * (nt / 2 + 1) + (nt & 1) * (nt / 2 + 1); }
 static_assert(tile_base(7) + 4 == kTiles, "tiles of a lower triangle");
 
-// A chunk's record (DeltaTcArgs::rec): T - 1 as {hi, lo} operand tiles, P tiles, and 256 floats:
-// exp(c_i), beta_i exp(c_end - c_i), beta_i, and [192] exp(c_end).
-constexpr int kRecT = kTiles * 32 * 16, kRecP = kTiles * 32 * 8, kRecV = 1024;
+// A chunk's record (DeltaTcArgs::rec): T - 1 as {hi, lo} operand tiles; 256 floats: exp(c_i), beta_i exp(c_end - c_i),
+// beta_i, and [192] exp(c_end); P as {hi, lo} tiles.
+constexpr int kRecT = kTiles * 32 * 16, kRecV = 1024;
 constexpr int kRec = kDeltaRecBytes;
-static_assert(kRecT + kRecP + kRecV == kRec, "record");
+static_assert(2 * kRecT + kRecV == kRec, "record");
 
 // The other way round, rows m >= columns i: column tile nt needs row tiles kt = nt / 2 .. 3.
 __host__ __device__ constexpr int rev_base(int nt) { return 8 * (nt / 2) - nt / 2 * (nt / 2 - 1) + (nt & 1) * (4 - nt / 2); }
 static_assert(rev_base(7) + 1 == kTiles, "tiles of an upper triangle");
-// The reverse walk's record: T - 1 (one term), P, and exp(c_i), exp(c_end - c_i), beta_i, [192] exp(c_end).
-static_assert(2 * kRecP + kRecV == kDeltaRRecBytes, "record");
+// The reverse walk's record: exp(c_i), exp(c_end - c_i), beta_i, [192] exp(c_end); T - 1 and P as {hi, lo} tiles.
+static_assert(2 * kRecT + kRecV == kDeltaRRecBytes, "record");
 
 struct Where {
     int bh, seg, ch, tb, cnt;
@@ -67,7 +67,7 @@ __device__ __forceinline__ Where chunk_at(const DeltaTcArgs &a, long long id)
 // delta_prep_tc: one warp per chunk, no barrier between warps.  K K^T (and Q K^T) in registers, exact bf16
 // products; then X = (1 + A)^-1 by 16 x 16 blocks: the four diagonal blocks by substitution in fp32, all at once (a lane
 // per column, two blocks on each half of the warp), and the others from them as products of 16 x 16 blocks with every
-// operand in two bf16 terms (2^-17):
+// operand in three bf16 terms (2^-25):
 //   X10 = -X11 A10 X00, X32 = -X33 A32 X22, and [X20 X21; X30 X31] = -[X22 0; X32 X33] [A20 A21; A30 A31] [X00 0; X10 X11].
 // A product's result is a left operand as it lies, its 8 x 8 transposes are a right one, and a block of X (or P) is, as it
 // lies, also the walk's operand of rows j, columns i: nothing but the diagonal blocks passes through shared memory.
@@ -75,8 +75,8 @@ __device__ __forceinline__ Where chunk_at(const DeltaTcArgs &a, long long id)
 // ---------------------------------------------------------------------------
 constexpr int kXP = 20, kXB = 16 * kXP + 8;  // row and block pitch of the diagonal blocks, in words
 
-struct Terms {  // an operand in two bf16 terms: left 4 registers each, right 2 x 2
-    uint32_t h[4], l[4];
+struct Terms {  // an operand in three bf16 terms: left 4 registers each, right 2 x 2
+    uint32_t h[4], m[4], l[4];
 };
 // 16 x 16 results: [column half][accumulator]
 __device__ __forceinline__ Terms left_of(const float (&x)[2][4])
@@ -85,7 +85,7 @@ __device__ __forceinline__ Terms left_of(const float (&x)[2][4])
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) split2(x[h][2 * r], x[h][2 * r + 1], t.h[2 * h + r], t.l[2 * h + r]);
+        for (int r = 0; r < 2; ++r) split3(x[h][2 * r], x[h][2 * r + 1], t.h[2 * h + r], t.m[2 * h + r], t.l[2 * h + r]);
     return t;
 }
 __device__ __forceinline__ Terms right_of(const Terms &left)
@@ -94,6 +94,7 @@ __device__ __forceinline__ Terms right_of(const Terms &left)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         t.h[q] = movm_t(left.h[q]);
+        t.m[q] = movm_t(left.m[q]);
         t.l[q] = movm_t(left.l[q]);
     }
     return t;
@@ -105,6 +106,9 @@ __device__ __forceinline__ void block_mma(float (&acc)[2][4], const Terms &a, co
     for (int h = 0; h < 2; ++h) {
         mma16816(acc[h], a.l, b.h[2 * h], b.h[2 * h + 1]);
         mma16816(acc[h], a.h, b.l[2 * h], b.l[2 * h + 1]);
+        mma16816(acc[h], a.m, b.m[2 * h], b.m[2 * h + 1]);
+        mma16816(acc[h], a.m, b.h[2 * h], b.h[2 * h + 1]);
+        mma16816(acc[h], a.h, b.m[2 * h], b.m[2 * h + 1]);
         mma16816(acc[h], a.h, b.h[2 * h], b.h[2 * h + 1]);
     }
 }
@@ -155,8 +159,8 @@ __global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a)
     uint8_t *rec = a.rec + (size_t)blockIdx.x * kRec, *rrec = REV ? a.rrec + (size_t)blockIdx.x * kDeltaRRecBytes : nullptr;
     const float ce = cum[kCH - 1];  // tokens past the end add nothing
     {
-        float *vec = reinterpret_cast<float *>(rec + kRecT + kRecP);
-        float *rvec = reinterpret_cast<float *>(rrec + 2 * kRecP);
+        float *vec = reinterpret_cast<float *>(rec + kRecT);
+        float *rvec = reinterpret_cast<float *>(rrec);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const int i = lane + 32 * x;
@@ -207,7 +211,7 @@ __global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a)
             const float c0 = cum[16 * b + g], c1 = cum[16 * b + g + 8];
 #pragma unroll
             for (int n2 = 0; n2 <= b; ++n2) {
-                uint32_t p[2][2];  // [columns half][rows half] 8 x 8 tiles
+                uint32_t p[2][2], pl[2][2];  // [columns half][rows half] 8 x 8 tiles, two terms
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int j = 16 * n2 + 8 * h + 2 * c;
@@ -217,18 +221,20 @@ __global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a)
                         const int i = 16 * b + g + 8 * (e >> 1), jj = j + (e & 1);
                         v[e] = jj <= i ? qk[n2][h][e] * __expf((e >> 1 ? c1 : c0) - cum[jj]) : 0.f;
                     }
-                    p[h][0] = pack2(v[0], v[1]);
-                    p[h][1] = pack2(v[2], v[3]);
+                    split2(v[0], v[1], p[h][0], pl[h][0]);
+                    split2(v[2], v[3], p[h][1], pl[h][1]);
                 }
                 if (READ) {
-                    uint2 *pt = reinterpret_cast<uint2 *>(rec + kRecT) + lane;
-                    pt[(tile_base(2 * b) + n2) * 32] = make_uint2(p[0][0], p[1][0]);
-                    pt[(tile_base(2 * b + 1) + n2) * 32] = make_uint2(p[0][1], p[1][1]);
+                    uint4 *pt = reinterpret_cast<uint4 *>(rec + kRecT + kRecV) + lane;
+                    pt[(tile_base(2 * b) + n2) * 32] = make_uint4(p[0][0], p[1][0], pl[0][0], pl[1][0]);
+                    pt[(tile_base(2 * b + 1) + n2) * 32] = make_uint4(p[0][1], p[1][1], pl[0][1], pl[1][1]);
                 }
                 if (REV) {
-                    uint2 *pt = reinterpret_cast<uint2 *>(rrec + kRecP) + lane;
-                    pt[(rev_base(2 * n2) + b - n2) * 32] = make_uint2(movm_t(p[0][0]), movm_t(p[0][1]));
-                    pt[(rev_base(2 * n2 + 1) + b - n2) * 32] = make_uint2(movm_t(p[1][0]), movm_t(p[1][1]));
+                    uint4 *pt = reinterpret_cast<uint4 *>(rrec + kRecV + kRecT) + lane;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        pt[(rev_base(2 * n2 + h) + b - n2) * 32] =
+                            make_uint4(movm_t(p[h][0]), movm_t(p[h][1]), movm_t(pl[h][0]), movm_t(pl[h][1]));
                 }
             }
         }
@@ -286,12 +292,13 @@ __global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a)
     auto out = [&](int bi, int bj, const Terms &t) {  // block (bi, bj) of T - 1
         uint4 *tt = reinterpret_cast<uint4 *>(rec) + lane;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) tt[(tile_base(2 * bi + r) + bj) * 32] = make_uint4(t.h[r], t.h[2 + r], t.l[r], t.l[2 + r]);
+        for (int r = 0; r < 2; ++r) tt[(tile_base(2 * bi + r) + bj) * 32] = make_uint4(t.h[r], t.h[2 + r], t.m[r], t.m[2 + r]);
         if (REV) {
-            uint2 *lt = reinterpret_cast<uint2 *>(rrec) + lane;
+            uint4 *lt = reinterpret_cast<uint4 *>(rrec + kRecV) + lane;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                lt[(rev_base(2 * bj + h) + bi - bj) * 32] = make_uint2(movm_t(t.h[2 * h]), movm_t(t.h[2 * h + 1]));
+                lt[(rev_base(2 * bj + h) + bi - bj) * 32] =
+                    make_uint4(movm_t(t.h[2 * h]), movm_t(t.h[2 * h + 1]), movm_t(t.m[2 * h]), movm_t(t.m[2 * h + 1]));
         }
     };
     auto negate = [](float (&x)[2][4]) {
@@ -437,9 +444,10 @@ __device__ __forceinline__ void pair_sum(float4 *xb, int warp, int lane, F each,
 template <int D, int NW, bool READ>
 struct WalkSmem {
     static constexpr int kK = kCH * D * 2, kV = kCH * NW * 32;
-    static constexpr int kR = READ ? kRec : kRec - kRecP;  // without reads the record's P stays out
+    static constexpr int kR = kRecT + kRecV;
     static constexpr int kStage = kK * (READ ? 2 : 1) + kV + kR;
-    static constexpr int kTotal = 2 * kStage;
+    static constexpr int kP = READ ? kRecT : 0;  // P of the present chunk, needed late in it: one buffer
+    static constexpr int kTotal = 2 * kStage + kP;
 };
 
 template <int D, int NW, int KP, bool READ, bool FULL>
@@ -474,7 +482,7 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
         const uint8_t *rec = a.rec + ((size_t)sid * a.NCH + ch) * kRec;
         const uint32_t dst = smem_addr(st) + W::kStage - W::kR;
         for (int e = tid; e < W::kR / 16; e += NT)
-            cp16(dst + e * 16, rec + (READ || e < kRecT / 16 ? e : e + kRecP / 16) * 16, true);
+            cp16(dst + e * 16, rec + e * 16, true);
         cp_commit();
     };
 
@@ -488,7 +496,13 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
     for (int ch = 0; ch < nch; ++ch) {
         cp_wait<0>();
         __syncthreads();  // the chunk has come, and the stage of the one before is free
+        if (READ) {
+            const uint8_t *src = a.rec + ((size_t)sid * a.NCH + ch) * kRec + kRecT + kRecV;
+            for (int e = tid; e < kRecT / 16; e += NT) cp16(smem_addr(sm) + 2 * W::kStage + e * 16, src + e * 16, true);
+            cp_commit();
+        }
         if (ch + 1 < nch) load(ch + 1);
+        else cp_commit();
         uint8_t *st = sm + (ch & 1) * W::kStage, *vown = st + W::kK;
         const uint32_t kt = smem_addr(st), vt = kt + W::kK, qt = vt + W::kV;
         const uint8_t *rec = st + W::kStage - W::kR;
@@ -521,7 +535,7 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
                     mma16816(X[2 * n2], lo, b[0], b[1]);
                     mma16816(X[2 * n2 + 1], lo, b[2], b[3]);
                 }
-                if (READ) {  // the output is bf16: one term
+                if (READ) {  // the output is bf16 and nothing cancels here: one term
                     ldsm4(b, qt + tile_off<ROW>(16 * n2 + br, 2 * (k0 + ks) + bc));
                     mma16816(O[2 * n2], hi, b[0], b[1]);
                     mma16816(O[2 * n2 + 1], hi, b[2], b[3]);
@@ -533,7 +547,7 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
         for (int k4 = 0; k4 < 4; ++k4)
             ldsm4t(v4[k4], vt + own_off<NW>(16 * k4 + (lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1, wr));
         if (KP == 2)
-            pair_sum(reinterpret_cast<float4 *>(sm + 2 * W::kStage), warp, lane,
+            pair_sum(reinterpret_cast<float4 *>(sm + W::kTotal), warp, lane,
                      [&](auto leave) {
 #pragma unroll
                          for (int n = 0; n < 8; ++n) {
@@ -591,10 +605,8 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
                 for (int n = 2 * k4; n < 8; ++n) {
                     const uint4 b = tt[(tile_base(n) + k4) * 32];
                     mma16816(X[n], rh[k4], b.x, b.y);
-                    if (FULL) {
-                        mma16816(X[n], rl[k4], b.x, b.y);
-                        mma16816(X[n], rh[k4], b.z, b.w);
-                    }
+                    mma16816(X[n], rl[k4], b.x, b.y);
+                    mma16816(X[n], rh[k4], b.z, b.w);
                 }
         }
         // U = diag(beta) E for the read and the readout; U' = diag(beta exp(c_end - c)) E for the memory
@@ -603,18 +615,21 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
             const float2 be = *reinterpret_cast<const float2 *>(vec + 128 + 8 * n + 2 * c);
-            const uint32_t u0 = pack2(be.x * X[n][0], be.y * X[n][1]), u1 = pack2(be.x * X[n][2], be.y * X[n][3]);
-            uh[n / 2][2 * (n & 1)] = u0;
-            uh[n / 2][2 * (n & 1) + 1] = u1;
+            split2(be.x * X[n][0], be.y * X[n][1], uh[n / 2][2 * (n & 1)], ul[n / 2][2 * (n & 1)]);
+            split2(be.x * X[n][2], be.y * X[n][3], uh[n / 2][2 * (n & 1) + 1], ul[n / 2][2 * (n & 1) + 1]);
         }
         if (READ) {
-            const uint2 *pt = reinterpret_cast<const uint2 *>(rec + kRecT) + lane;
+            cp_wait<1>();  // (the next chunk may still be on its way)
+            __syncthreads();
+            const uint4 *pt = reinterpret_cast<const uint4 *>(sm + 2 * W::kStage) + lane;
 #pragma unroll
             for (int k4 = 0; k4 < 4; ++k4)
 #pragma unroll
                 for (int n = 2 * k4; n < 8; ++n) {
                     if (KP == 2 && n / 4 != kp) continue;
-                    const uint2 b = pt[(tile_base(n) + k4) * 32];
+                    const uint4 b = pt[(tile_base(n) + k4) * 32];
+                    mma16816(O[n], ul[k4], b.x, b.y);
+                    mma16816(O[n], uh[k4], b.z, b.w);
                     mma16816(O[n], uh[k4], b.x, b.y);
                 }
         }
@@ -668,10 +683,8 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
                 ldsm4t(b, kt + tile_off<ROW>(16 * k4 + tr, 2 * (k0 + n2) + tc));
                 mma16816(S[2 * n2], uh[k4], b[0], b[1]);
                 mma16816(S[2 * n2 + 1], uh[k4], b[2], b[3]);
-                if (FULL) {
-                    mma16816(S[2 * n2], ul[k4], b[0], b[1]);
-                    mma16816(S[2 * n2 + 1], ul[k4], b[2], b[3]);
-                }
+                mma16816(S[2 * n2], ul[k4], b[0], b[1]);
+                mma16816(S[2 * n2 + 1], ul[k4], b[2], b[3]);
             }
     }
     if (a.states_img) {
@@ -695,13 +708,15 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
 // with p_i = g_i dy_i and R the adjoint after the chunk:
 //   X   = diag(exp(c_end - c)) K R^T + P^T p,   W = T^T diag(beta) X            (dv = W)
 //   R' = exp(c_end) R + sum_i exp(c_i) (p_i q_i^T - w_i k_i^T)
-// R is held in fp32 and enters the products in one bf16 term, as all the rest: the results are bf16 gradients.
+// R is held in fp32 and read in one bf16 term; T, P, X and w take part in two, as in the walk forwards: for keys that
+// resemble each other X gathers what later tokens ask of every one of them, and w is the small difference that is left
+// (one term: dv 3e-2 off at all but parallel keys).  T and P are needed late in a chunk: one buffer for the present one's.
 // ---------------------------------------------------------------------------
 template <int D, int NW>
 struct RWalkSmem {
     static constexpr int kK = kCH * D * 2, kV = kCH * NW * 32;
-    static constexpr int kStage = 2 * kK + kV + kDeltaRRecBytes + 256;  // K, Q, dy columns, record, gates
-    static constexpr int kTotal = 2 * kStage;
+    static constexpr int kStage = 2 * kK + kV + kRecV + 256;  // K, Q, dy columns, vectors, gates
+    static constexpr int kTotal = 2 * kStage + 2 * kRecT;
 };
 
 template <int D, int NW, int KP>
@@ -735,8 +750,8 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
         }
         const uint8_t *rec = a.rrec + ((size_t)sid * a.NCH + ch) * kDeltaRRecBytes;
         const uint32_t dst = smem_addr(st) + 2 * W::kK + W::kV;
-        for (int e = tid; e < kDeltaRRecBytes / 16; e += NT) cp16(dst + e * 16, rec + e * 16, true);
-        float *gs = reinterpret_cast<float *>(st + 2 * W::kK + W::kV + kDeltaRRecBytes);
+        for (int e = tid; e < kRecV / 16; e += NT) cp16(dst + e * 16, rec + e * 16, true);
+        float *gs = reinterpret_cast<float *>(st + 2 * W::kK + W::kV + kRecV);
         for (int e = tid; e < kCH; e += NT) gs[e] = a.gon && e < cnt ? a.gon[(row0 + e) * a.gw_stride] : 1.f;
         cp_commit();
     };
@@ -765,12 +780,18 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
     for (int ch = nch - 1; ch >= 0; --ch) {
         cp_wait<0>();
         __syncthreads();
+        {
+            const uint8_t *src = a.rrec + ((size_t)sid * a.NCH + ch) * kDeltaRRecBytes + kRecV;
+            for (int e = tid; e < 2 * kRecT / 16; e += NT) cp16(smem_addr(sm) + 2 * W::kStage + e * 16, src + e * 16, true);
+            cp_commit();
+        }
         if (ch > 0) load(ch - 1);
+        else cp_commit();
         uint8_t *st = sm + (ch & 1) * W::kStage, *vown = st + 2 * W::kK;
         const uint32_t kt = smem_addr(st), qt = kt + W::kK, vt = qt + W::kK;
         const uint8_t *rec = st + 2 * W::kK + W::kV;
-        const float *vec = reinterpret_cast<const float *>(rec + 2 * kRecP);
-        const float *gs = reinterpret_cast<const float *>(rec + kDeltaRRecBytes);
+        const float *vec = reinterpret_cast<const float *>(rec);
+        const float *gs = reinterpret_cast<const float *>(rec + kRecV);
         const size_t row0 = (size_t)bh * a.L + t0 + ch * kCH;
         const int cnt = min(kCH, len - ch * kCH);
         float X[8][4];
@@ -796,7 +817,7 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
         for (int k4 = 0; k4 < 4; ++k4)
             ldsm4t(v4[k4], vt + own_off<NW>(16 * k4 + (lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1, wr));
         if (KP == 2)
-            pair_sum(reinterpret_cast<float4 *>(sm + 2 * W::kStage), warp, lane,
+            pair_sum(reinterpret_cast<float4 *>(sm + W::kTotal), warp, lane,
                      [&](auto leave) {
 #pragma unroll
                          for (int n = 0; n < 8; ++n) leave(n, X[n]);
@@ -828,36 +849,38 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
             __nv_bfloat16 *dst = a.R_c + (((size_t)sid * a.NCH + ch) * D + vbase + 16 * wr) * D + 16 * k0;
             put_rows(R, 1.f, lane, [&](int r, int n, int at, const uint2 &x) { *reinterpret_cast<uint2 *>(dst + (size_t)r * D + 8 * n + at / 2) = x; });
         }
-        const uint2 *lt = reinterpret_cast<const uint2 *>(rec) + lane;
-        const uint2 *pt = reinterpret_cast<const uint2 *>(rec + kRecP) + lane;
+        cp_wait<1>();  // T and P (the next chunk may still be on its way)
+        __syncthreads();
+        const uint4 *lt = reinterpret_cast<const uint4 *>(sm + 2 * W::kStage) + lane;
+        const uint4 *pt = reinterpret_cast<const uint4 *>(sm + 2 * W::kStage + kRecT) + lane;
 #pragma unroll
         for (int k4 = 0; k4 < 4; ++k4)
 #pragma unroll
             for (int n = 0; n < 2 * k4 + 2; ++n) {
-                const uint2 b = pt[(rev_base(n) + k4 - n / 2) * 32];
+                const uint4 b = pt[(rev_base(n) + k4 - n / 2) * 32];
+                mma16816(X[n], pf[k4], b.z, b.w);
                 mma16816(X[n], pf[k4], b.x, b.y);
             }
-        {
-            uint32_t yh[4][4];
+        uint32_t wf[4][4], wl[4][4];
 #pragma unroll
-            for (int n = 0; n < 8; ++n) {
-                const float2 be = *reinterpret_cast<const float2 *>(vec + 128 + 8 * n + 2 * c);
-                X[n][0] *= be.x;
-                X[n][1] *= be.y;
-                X[n][2] *= be.x;
-                X[n][3] *= be.y;
-                yh[n / 2][2 * (n & 1)] = pack2(X[n][0], X[n][1]);
-                yh[n / 2][2 * (n & 1) + 1] = pack2(X[n][2], X[n][3]);
-            }
-#pragma unroll
-            for (int k4 = 0; k4 < 4; ++k4)
-#pragma unroll
-                for (int n = 0; n < 2 * k4 + 2; ++n) {
-                    const uint2 b = lt[(rev_base(n) + k4 - n / 2) * 32];
-                    mma16816(X[n], yh[k4], b.x, b.y);
-                }
+        for (int n = 0; n < 8; ++n) {
+            const float2 be = *reinterpret_cast<const float2 *>(vec + 128 + 8 * n + 2 * c);
+            X[n][0] *= be.x;
+            X[n][1] *= be.y;
+            X[n][2] *= be.x;
+            X[n][3] *= be.y;
+            split2(X[n][0], X[n][1], wf[n / 2][2 * (n & 1)], wl[n / 2][2 * (n & 1)]);
+            split2(X[n][2], X[n][3], wf[n / 2][2 * (n & 1) + 1], wl[n / 2][2 * (n & 1) + 1]);
         }
-        uint32_t wf[4][4];
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4)
+#pragma unroll
+            for (int n = 0; n < 2 * k4 + 2; ++n) {
+                const uint4 b = lt[(rev_base(n) + k4 - n / 2) * 32];
+                mma16816(X[n], wf[k4], b.x, b.y);
+                mma16816(X[n], wl[k4], b.x, b.y);
+                mma16816(X[n], wf[k4], b.z, b.w);
+            }
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
             wf[n / 2][2 * (n & 1)] = pack2(X[n][0], X[n][1]);
@@ -867,8 +890,8 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
 #pragma unroll
         for (int n = 0; n < 8; ++n) {  // -exp(c) w
             const float2 ga = *reinterpret_cast<const float2 *>(vec + 8 * n + 2 * c);
-            wf[n / 2][2 * (n & 1)] = pack2(-ga.x * X[n][0], -ga.y * X[n][1]);
-            wf[n / 2][2 * (n & 1) + 1] = pack2(-ga.x * X[n][2], -ga.y * X[n][3]);
+            split2(-ga.x * X[n][0], -ga.y * X[n][1], wf[n / 2][2 * (n & 1)], wl[n / 2][2 * (n & 1)]);
+            split2(-ga.x * X[n][2], -ga.y * X[n][3], wf[n / 2][2 * (n & 1) + 1], wl[n / 2][2 * (n & 1) + 1]);
         }
         const float dec = vec[192];
 #pragma unroll
@@ -884,6 +907,8 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
                 ldsm4t(b, kt + tile_off<ROW>(16 * k4 + tr, 2 * (k0 + n2) + tc));
                 mma16816(R[2 * n2], wf[k4], b[0], b[1]);
                 mma16816(R[2 * n2 + 1], wf[k4], b[2], b[3]);
+                mma16816(R[2 * n2], wl[k4], b[0], b[1]);
+                mma16816(R[2 * n2 + 1], wl[k4], b[2], b[3]);
                 ldsm4t(b, qt + tile_off<ROW>(16 * k4 + tr, 2 * (k0 + n2) + tc));
                 mma16816(R[2 * n2], pg[k4], b[0], b[1]);
                 mma16816(R[2 * n2 + 1], pg[k4], b[2], b[3]);

@@ -106,7 +106,7 @@ int forward_delta_tc(const Call &c, const void *q, const void *k, const void *v,
     const bool one = N == 1, routed = mode_uses_u(p.mode), tc = !one && tc_fused_gates(p);
     DeltaTcArgs t = delta_tc_args(c, q, k, v, la, be);
     t.states = states;
-    t.full = states != nullptr;
+    t.full = true;
     FwdArgs f{};
     float *kbar = nullptr, *r_on = nullptr, *sums = nullptr, *alpha = nullptr, *zero = nullptr, *ones = nullptr;
     char *tc_scratch = nullptr;

@@ -310,11 +310,11 @@ cudaError_t launch_pool_simt(const Problem &p, const DeltaArgs &a, float *sums, 
 // rho from the pooled-key weights pw (token t at [t * gw_stride]), u and the key means' gradient.
 cudaError_t launch_pool_grad_simt(const Problem &p, const DeltaArgs &a, const float *pw, float *rho, const float *dkbar, cudaStream_t s);
 // The same on the tensor cores (k_delta_tc.cu): bf16, d = 64 or 128, any segment length.
-constexpr int kDeltaRecBytes = 16384;  // a chunk's record between its two kernels
+constexpr int kDeltaRecBytes = 21504;  // a chunk's record between its two kernels
 struct DeltaTcArgs {
     const __nv_bfloat16 *q, *k, *v, *la, *be;
     uint8_t *rec;          // [BH][N][NCH] x kDeltaRecBytes scratch
-    bool full;             // states with fp32 accuracy
+    bool full;             // the walk reads the memory in two bf16 terms (else one)
     __nv_bfloat16 *y;      // online reads in bf16 (one segment), or null
     float *O_on;           // online reads in fp32, or null
     float *states;         // [BH][N][d][d], or null
@@ -336,7 +336,7 @@ struct DeltaTcArgs {
     int BH, L, C, N, NCH;
 };
 cudaError_t launch_delta_dgon(const Problem &p, const void *dy, const void *O, float *dgon, cudaStream_t s);
-constexpr int kDeltaRRecBytes = 11264;
+constexpr int kDeltaRRecBytes = 21504;
 // After the walk with rrec, E and S_c: dv and R_c, then the other gradients.
 cudaError_t launch_delta_grads_tc(const Problem &p, const DeltaTcArgs &a, cudaStream_t s);
 bool delta_tc_supported(const Problem &p);

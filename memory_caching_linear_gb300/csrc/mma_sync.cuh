@@ -84,6 +84,13 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
     lo = pack2(x - low_f(hi), y - high_f(hi));
 }
 
+// The same in three terms, up to 2^-25.
+__device__ __forceinline__ void split3(float x, float y, uint32_t &hi, uint32_t &mid, uint32_t &lo)
+{
+    hi = pack2(x, y);
+    split2(x - low_f(hi), y - high_f(hi), mid, lo);
+}
+
 // Byte offset of 16-byte piece c of row r in a tile of rows of ROW bytes (a multiple of 128): pieces are
 // exchanged within their 128 bytes by the row, so that eight rows of a column touch every bank once.
 template <int ROW>

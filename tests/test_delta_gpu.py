@@ -248,3 +248,40 @@ def test_many_heads_and_segments(d, C, L):
     assert mcl.mc_check_device() == mcl.MC_OK
     for name, g, w in zip(("dq", "dk", "dv", "du", "dlog_alpha", "dbeta"), got, backward(*x, dy, C, GRM)):
         assert rel(g, w) <= TOL["bf16"], name
+
+
+@pytest.mark.parametrize("beta", [1.0, 1.9])
+@pytest.mark.parametrize("d,dtype", [(32, "f32"), (64, "bf16"), (128, "bf16")])
+def test_keys_that_resemble_each_other(d, dtype, beta):
+    """Neighbouring keys all but parallel: the inverse within a chunk is far from the identity, and every write undoes
+    the one before, so the values e_j beta_j that a chunk writes are of the size of the result and cancel.
+
+    States from bf16 inputs: an operand of two bf16 terms is off by 2^-17 of itself, and the 64 products of a chunk's
+    sum by the root of that, 8 * 2^-17 = 6e-5 of the largest; the memory forgets a write by |1 - beta| per token, so at
+    beta = 1.9 the errors of 1 / (1 - 0.9) = 10 tokens stand together: 6e-4, and at beta = 1 of one.  Over two chunks and
+    the decay of a maximum over 2 d^2 entries (four standard deviations), 2.5e-4 and 2.5e-3.
+    y with cached segments: the readout's tensor-core kernels round the written values and their weights to bf16, 2^-9 in
+    the mean, and a token's read has 128 products of a chunk of which each counts: 2^-9 * sqrt(2 * 128) = 3e-2, times
+    four standard deviations over values of which the largest is at four, too.  One memory is read in two terms: 1e-2.
+    Gradients pass through bf16 e, w and states the same way: chunks of 64, three roundings, 2^-9 * sqrt(3 * 64) = 2.7e-2,
+    times |beta| of the write that they go through twice."""
+    L, C = 260, 128
+    q, k, v, u, la, be = make_delta_inputs(1, 2, L, d, C, 71, dtype, decay=0.001)
+    k = k.float() * 0.05 + k[:, :, :1].float()
+    k = (k / k.norm(dim=-1, keepdim=True)).to(q.dtype)
+    be = torch.full_like(be, beta)
+    x = [q, k, v, u, la, be]
+    dy = torch.randn(q.shape, generator=torch.Generator().manual_seed(9)).to(q.dtype)
+    y1, st1 = forward(*x, L, RESIDUAL)
+    gy1, gst1 = mcl.mc_forward_delta(*cuda(x), L, RESIDUAL)
+    y, st = forward(*x, C, GRM)
+    gy, gst = mcl.mc_forward_delta(*cuda(x), C, GRM)
+    b16 = dtype == "bf16"
+    state_tol = STATE_TOL if not b16 else 2.5e-4 if beta == 1.0 else 2.5e-3
+    print("states", rel(gst, st), rel(gst1, st1), "y", rel(gy, y), rel(gy1, y1))
+    assert rel(gy1, y1) <= TOL[dtype] and rel(gst1, st1) <= state_tol
+    assert rel(gst, st) <= state_tol and rel(gy, y) <= (3e-2 if b16 else TOL[dtype])
+    for name, g, w in zip(("dq", "dk", "dv", "du", "dlog_alpha", "dbeta"), mcl.mc_backward_delta(*cuda(x), dy.cuda(), C, GRM),
+                          backward(*x, dy, C, GRM)):
+        print(name, rel(g, w))
+        assert rel(g, w) <= (2.7e-2 * max(1.0, beta) ** 2 if b16 else TOL[dtype]), name
