@@ -414,7 +414,8 @@ def mc_backward_delta(q, k, v, u, log_alpha, beta, dy, seg_len: int, agg_mode: i
 class DeltaMemoryCaching(torch.autograd.Function):
     """Autograd wrapper of the gated delta memory: y = DeltaMemoryCaching.apply(q, k, v, u, log_alpha,
     beta, seg_len, agg_mode, topk) runs ``mc_forward_delta`` and, on backward, ``mc_backward_delta``
-    (u may be None for Residual and Mean)."""
+    (u may be None for Residual and Mean).  The gradients have none of their own.  Work captured into a graph is better
+    written with the two functions: autograd ties a leaf's gradient to the stream of every graph that lives."""
 
     @staticmethod
     def forward(ctx, q, k, v, u, log_alpha, beta, seg_len: int, agg_mode: int, topk: int = 0):
@@ -424,6 +425,7 @@ class DeltaMemoryCaching(torch.autograd.Function):
         return y
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         q, k, v, u, log_alpha, beta = ctx.saved_tensors
         dq, dk, dv, du, dla, dbe = mc_backward_delta(q, k, v, u, log_alpha, beta, dy.contiguous(), *ctx.cfg)
@@ -447,8 +449,8 @@ class EvictingCache(DecodeCache):
 
     def copy_(self, other: "EvictingCache") -> "EvictingCache":
         """Take over another cache's contents and position (to go on from one prompt several times)."""
-        if (other.seg_len, other.n_max, other.protect) != (self.seg_len, self.n_max, self.protect):
-            raise ValueError("the caches differ in seg_len, n_max or protect")
+        if (other.seg_len, other.protect, other.states.shape) != (self.seg_len, self.protect, self.states.shape):
+            raise ValueError("the caches differ in seg_len, protect or shape")
         names = ("states", "kbar", "online", "ksum", "mass", "slot_seg")
         torch._foreach_copy_([getattr(self, n) for n in names], [getattr(other, n) for n in names])
         self.t = other.t

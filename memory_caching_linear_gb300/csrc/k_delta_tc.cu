@@ -14,11 +14,12 @@
 // short and each is small, and an accumulator in tensor memory would have to be read back, split and
 // written to shared memory between any two of them.
 //
-// Precision: the memory is held in fp32, and every operand that is not an input enters the products in two bf16
-// terms, products of two lows left out: 2^-17 of a term (the inverse in three, 2^-25).  The errors e_j of keys that
-// resemble each other are large and cancel in S and in O, so one term (2^-9) would show: at keys with a cosine of 0.8 it
-// leaves the memory 7e-3 and y 9e-3 off, as against 2e-5 and 1.4e-3, the last bf16 rounding.  The gradients' own walk reads
-// S in one term (S 4e-4 off there): they pass through bf16 states and errors anyway.
+// Precision: the memory is held in fp32, and what is not an input enters the products in two bf16 terms, products of two
+// lows left out: 2^-17 of a term (the inverse in three, 2^-25).  The errors e_j of keys that resemble each other are large
+// and cancel in S and in O, so one term (2^-9) would show: at keys with a cosine of 0.8 it leaves the memory 7e-3 and y 9e-3
+// off, as against 2e-5 and 1.4e-3, the last bf16 rounding.  Two readings are one term's: O's of S, where nothing cancels and
+// the result is bf16, and E's of S in the gradients' own walk (S 4e-4 off there; 132 instead of 181 us at L = 4096, 32
+// heads, d = 128): what they yield passes through bf16 states and errors anyway.
 #include <cstdint>
 
 #include "mc_internal.cuh"
@@ -423,13 +424,13 @@ __device__ __forceinline__ void put_rows(const float (&S)[NT][4], float f, int l
 
 // Two warps that hold the two halves of the keys of 16 rows add their partial products: each leaves its own in xb,
 // and adds the other's (tiles with `mine` only).
-template <typename F, typename G>
+template <int TILES, typename F, typename G>
 __device__ __forceinline__ void pair_sum(float4 *xb, int warp, int lane, F each, G add)
 {
-    each([&](int i, const float (&x)[4]) { xb[(warp * 16 + i) * 32 + lane] = make_float4(x[0], x[1], x[2], x[3]); });
+    each([&](int i, const float (&x)[4]) { xb[(warp * TILES + i) * 32 + lane] = make_float4(x[0], x[1], x[2], x[3]); });
     asm volatile("bar.sync %0, 64;" ::"r"(1 + warp / 2) : "memory");
     add([&](int i, float (&x)[4]) {
-        const float4 y = xb[((warp ^ 1) * 16 + i) * 32 + lane];
+        const float4 y = xb[((warp ^ 1) * TILES + i) * 32 + lane];
         x[0] += y.x;
         x[1] += y.y;
         x[2] += y.z;
@@ -547,7 +548,7 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
         for (int k4 = 0; k4 < 4; ++k4)
             ldsm4t(v4[k4], vt + own_off<NW>(16 * k4 + (lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1, wr));
         if (KP == 2)
-            pair_sum(reinterpret_cast<float4 *>(sm + W::kTotal), warp, lane,
+            pair_sum<READ ? 12 : 8>(reinterpret_cast<float4 *>(sm + W::kTotal), warp, lane,
                      [&](auto leave) {
 #pragma unroll
                          for (int n = 0; n < 8; ++n) {
@@ -817,7 +818,7 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
         for (int k4 = 0; k4 < 4; ++k4)
             ldsm4t(v4[k4], vt + own_off<NW>(16 * k4 + (lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1, wr));
         if (KP == 2)
-            pair_sum(reinterpret_cast<float4 *>(sm + W::kTotal), warp, lane,
+            pair_sum<8>(reinterpret_cast<float4 *>(sm + W::kTotal), warp, lane,
                      [&](auto leave) {
 #pragma unroll
                          for (int n = 0; n < 8; ++n) leave(n, X[n]);
@@ -1356,14 +1357,15 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
 }
 
 // Few walkers leave most of the card idle, and a chunk's products on a walker's way to the next chunk are what counts: then
-// two warps share 16 rows, half of the keys each.  KP = 2 with two row groups per CTA where all its CTAs fit at two
-// per SM (L = 4096, 32 heads, d = 128: see the measurements at the launch), else four row groups and whole rows.
-inline bool split_keys(const Problem &p) { return (long long)p.BH * p.N * (p.d / 32) <= 304; }
+// two warps share 16 rows, half of the keys each.  KP = 2 with two row groups per CTA as long as every CTA has an SM to
+// itself, else four row groups and whole rows.  L = 2048, d = 128, one memory (forward, recomputed, reverse walk), KP = 2
+// against 1: 32 heads (128 CTAs) 89 68 82 against 111 93 102 us; 48 heads (192 CTAs) 171 101 129 against 111 93 102 us.
+inline bool split_keys(const Problem &p) { return (long long)p.BH * p.N * (p.d / 32) <= 152; }
 
 template <int D, int NW, int KP>
 cudaError_t rwalk_launch(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
 {
-    constexpr int smem = RWalkSmem<D, NW>::kTotal + (KP == 2 ? 2 * NW * 8192 : 0);
+    constexpr int smem = RWalkSmem<D, NW>::kTotal + (KP == 2 ? 2 * NW * 8 * 512 : 0);
     auto kern = delta_rwalk_tc<D, NW, KP>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -1428,7 +1430,7 @@ cudaError_t prep_impl(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
 template <int D, int NW, int KP, bool READ, bool FULL>
 cudaError_t walk_launch(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
 {
-    constexpr int smem = WalkSmem<D, NW, READ>::kTotal + (KP == 2 ? 2 * NW * 8192 : 0);
+    constexpr int smem = WalkSmem<D, NW, READ>::kTotal + (KP == 2 ? 2 * NW * (READ ? 12 : 8) * 512 : 0);
     auto kern = delta_walk_tc<D, NW, KP, READ, FULL>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;

@@ -285,3 +285,36 @@ def test_keys_that_resemble_each_other(d, dtype, beta):
                           backward(*x, dy, C, GRM)):
         print(name, rel(g, w))
         assert rel(g, w) <= (2.7e-2 * max(1.0, beta) ** 2 if b16 else TOL[dtype]), name
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements in every tensor and in the chunk states: copies of one head, the last as the first."""
+    if torch.cuda.mem_get_info()[0] < 170e9:
+        pytest.skip("needs 170 GB")
+    BH, L, d, C = 33000, 1024, 64, 128
+    assert BH * L * d > 2**31 and BH * (L // 64) * d * d > 2**31
+    one = make_delta_inputs(1, 1, L, d, C, 81, "bf16")
+    dy1 = torch.randn(one[0].shape, generator=torch.Generator().manual_seed(10)).to(one[0].dtype)
+    y, st = forward(*one, C, GRM)
+    want = backward(*one, dy1, C, GRM)
+    x = [t.cuda().expand(1, BH, *t.shape[2:]).contiguous() for t in one]
+    dy = dy1.cuda().expand(1, BH, L, d).contiguous()
+    gy, gst = mcl.mc_forward_delta(*x, C, GRM)
+    for h in (0, BH - 1):
+        assert rel(gy[:, h], y[:, 0]) <= TOL["bf16"] and rel(gst[:, h], st[:, 0]) <= STATE_TOL
+    assert torch.equal(gy[:, 0], gy[:, -1]) and torch.equal(gst[:, 0], gst[:, -1])
+    del gy, gst
+    got = mcl.mc_backward_delta(*x, dy, C, GRM)
+    for name, g, w in zip(("dq", "dk", "dv", "du", "dlog_alpha", "dbeta"), got, want):
+        assert rel(g[:, 0], w[:, 0]) <= TOL["bf16"] and rel(g[:, -1], w[:, 0]) <= TOL["bf16"], name
+    del x, dy, got, g
+    mcl.mc_trim_scratch()
+    torch.cuda.empty_cache()
+
+
+def test_second_gradients_are_refused():
+    x = [t.requires_grad_() for t in cuda(make_delta_inputs(1, 1, 20, 16, 10, 4, "f32"))]
+    y = mcl.DeltaMemoryCaching.apply(*x, 10, GRM, 0)
+    dq, = torch.autograd.grad(y.square().sum(), x[0], create_graph=True)
+    with pytest.raises(RuntimeError):
+        dq.sum().backward()

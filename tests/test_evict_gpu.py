@@ -181,3 +181,35 @@ def test_constant_gates_are_refused(mode):
     with pytest.raises(mcl.MCError) as e:
         mcl.mc_decode_step_evict(cache, z, z, z, z, mode)
     assert e.value.status == mcl.MC_ERR_MODE and cache.t == 0
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 numbers in the cache and in the prefill's states: copies of one head, the last as the first."""
+    if torch.cuda.mem_get_info()[0] < 60e9:
+        pytest.skip("needs 60 GB")
+    BH, d, C, n_max = 8400, 64, 4, 63
+    L = 66 * C + 2
+    assert BH * n_max * d * d > 2**31
+    one = make_delta_inputs(1, 1, L + 4, d, C, 91, "bf16")
+    st1 = torch.randn(1, 1, 67, d, d, generator=torch.Generator().manual_seed(3))
+    head = [t[:, :, :L].contiguous() for t in one]
+    ref, mass = compact(head[1], head[3], st1, C, GRM, 0, n_max, 2)
+    cache = mcl.EvictingCache(1, BH, d, C, n_max, protect=2)
+    wide = lambda t: t.cuda().expand(1, BH, *t.shape[2:]).contiguous()
+    got = mcl.mc_cache_compact(cache, wide(head[1]), wide(head[3]), wide(st1), GRM)
+    assert torch.equal(got[:, 0], got[:, -1]) and rel(got[:, :1], mass) <= 1e-4
+    for j in range(L, L + 4):  # over a segment's end
+        tok = [t[:, :, j].contiguous() for t in one]
+        w = [t.cuda().expand(1, BH, *t.shape[2:]).contiguous() for t in tok]
+        y = mcl.mc_decode_step_evict(cache, *w[:4], GRM, log_alpha=w[4], beta=w[5])
+        want = ref.step(*tok[:4], GRM, 0, *tok[4:])
+        assert torch.equal(y[:, 0], y[:, -1]) and rel(y[:, :1], want) <= TOL["bf16"]
+    assert torch.equal(cache.slot_seg[:, 0], cache.slot_seg[:, -1]) and torch.equal(cache.states[:, 0], cache.states[:, -1])
+    assert torch.equal(cache.slot_seg[:, :1].cpu().long(), ref.slot_seg) and rel(cache.states[:, :1], ref.states) <= 1e-4
+
+
+def test_caches_of_different_shapes_are_not_copied():
+    a = mcl.EvictingCache(1, 2, 32, 4, 3)
+    for b in (mcl.EvictingCache(1, 1, 32, 4, 3), mcl.EvictingCache(1, 2, 32, 4, 2), mcl.EvictingCache(1, 2, 32, 5, 3)):
+        with pytest.raises(ValueError):
+            a.copy_(b)
