@@ -922,8 +922,9 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
 // Eight warps: warp % 4 takes 16 tokens, warp / 4 half of the dimensions.  The warps of one half form B1, those of the
 // other B2 (16 rows each), and leave them in shared memory as 16 x 16 blocks of the lower triangle, from which both
 // read them as they lie (with beta_j) and transposed.  A chunk is a chain of loads and small products, so two CTAs
-// share an SM: S and R come through one 16 KB buffer (64 rows at a time, the next ones on their way under the
-// products between), and at most three of the 16 x 64 results are held at once.
+// share an SM: S comes through one buffer (64 rows at a time, the next ones on their way under the products
+// between), R into the tiles of p and w once these have been read, u into S's, and at most three of the 16 x 64
+// results are held at once.
 // ---------------------------------------------------------------------------
 constexpr int kGradThreads = 256;
 
@@ -956,9 +957,9 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
     const size_t row0 = (size_t)w.bh * a.L + w.tb;
     const __nv_bfloat16 *S = a.S_c + (size_t)blockIdx.x * D * D, *R = a.R_c + (size_t)blockIdx.x * D * D;
 
-    auto load_rows = [&](const __nv_bfloat16 *src, int b) {  // rows 64 b .. of S or R
+    auto load_rows = [&](uint8_t *dst, const __nv_bfloat16 *src, int b) {  // rows 64 b .. of S or R
         for (int e = tid; e < 64 * PIECES; e += kGradThreads)
-            cp16(smem_addr(Mt) + tile_off<ROW>(e / PIECES, e % PIECES), src + (size_t)(64 * b * PIECES + e) * 8, true);
+            cp16(smem_addr(dst) + tile_off<ROW>(e / PIECES, e % PIECES), src + (size_t)(64 * b * PIECES + e) * 8, true);
         cp_commit();
     };
     for (int e = tid; e < kCH * PIECES; e += kGradThreads) {
@@ -972,7 +973,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
         cp16(smem_addr(Qt) + o, a.q + off, ok);
         cp16(smem_addr(Kt) + o, a.k + off, ok);
     }
-    load_rows(S, 0);
+    load_rows(Mt, S, 0);
     if (warp == 0) {
         const int i = 2 * lane;
         const float x0 = i < w.cnt ? delta_log(__bfloat162float(a.la[row0 + i])) : 0.f;
@@ -1023,8 +1024,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
             x[n][0] *= e0; x[n][1] *= e0; x[n][2] *= e1; x[n][3] *= e1;
         }
     };
-    // the warp's 16 rows of `tile` times the 64 rows of S or R in the buffer (block b of its columns)
-    auto times_rows = [&](float (&x)[HN][4], const uint8_t *tile, int b) {
+    // the warp's 16 rows of `tile` times 64 rows of S or R (block b of its columns)
+    auto times_rows = [&](float (&x)[HN][4], const uint8_t *tile, const uint8_t *rows, int b) {
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
             uint32_t af[4];
@@ -1032,7 +1033,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
 #pragma unroll
             for (int n2 = 0; n2 < HN / 2; ++n2) {
                 uint32_t bf[4];
-                ldsm4t(bf, smem_addr(Mt) + tile_off<ROW>(16 * ks + tr, d0 / 8 + 2 * n2 + tc));
+                ldsm4t(bf, smem_addr(rows) + tile_off<ROW>(16 * ks + tr, d0 / 8 + 2 * n2 + tc));
                 mma16816(x[2 * n2], af, bf[0], bf[1]);
                 mma16816(x[2 * n2 + 1], af, bf[2], bf[3]);
             }
@@ -1195,28 +1196,29 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
         float dq[HN][4], b[8][4];
         zero(b);
         zero(dq);
-        times_rows(dq, Pt, 0);
-        times_rows(z, Wt, 0);
-        __syncthreads();  // the rows have been read
-        if (MB > 1) load_rows(S, 1);
-        else load_rows(R, 0);
+        times_rows(dq, Pt, Mt, 0);
+        times_rows(z, Wt, Mt, 0);
+        if (MB > 1) {
+            __syncthreads();  // the rows have been read
+            load_rows(Mt, S, 1);
+        }
         pairs(b, half ? Wt : Pt, Et);
         pair_sums(b, half ? Kt : Qt, half ? -1.f : 1.f);
         put_blocks(b);
         if (MB > 1) {
             cp_wait<0>();
             __syncthreads();
-            times_rows(dq, Pt, 1);
-            times_rows(z, Wt, 1);
-            __syncthreads();
-            load_rows(R, 0);
+            times_rows(dq, Pt, Mt, 1);
+            times_rows(z, Wt, Mt, 1);
         }
+        __syncthreads();  // p and w have been read: their tiles take R; the blocks are there
+        load_rows(Wt, R, 0);
+        if (MB > 1) load_rows(Pt, R, 1);
         const float e0 = __expf(c_lo), e1 = __expf(c_hi);
         scale(dq, e0, e1);
         scale(z, e0, e1);
         row_dot(dq, Qt, 1);
         row_dot(z, Kt, 3);
-        if (MB == 1) __syncthreads();  // (else the barrier above) the blocks are there
         times_keys(dq, 0);
         times_keys(z, 1);
         if (a.dq_add) {
@@ -1235,29 +1237,36 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
     }
     float y[HN][4];
     zero(y);
-    float in = 0.f;  // <R, S>
+    float in = 0.f;  // <R, S>, of which S's last rows are still there
+    constexpr int X4 = 64 * PIECES / kGradThreads;
+    uint4 s4[X4];
+    if (MB > 1)
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb) {
-        uint4 s4[64 * PIECES / kGradThreads];  // this thread's pieces of S again, for <R, S>, while R comes
+        for (int x = 0; x < X4; ++x) s4[x] = *reinterpret_cast<const uint4 *>(S + (size_t)(tid + x * kGradThreads) * 8);
+    cp_wait<0>();
+    __syncthreads();
 #pragma unroll
-        for (int x = 0; x < 64 * PIECES / kGradThreads; ++x)
-            s4[x] = *reinterpret_cast<const uint4 *>(S + (size_t)(64 * mb * PIECES + tid + x * kGradThreads) * 8);
-        cp_wait<0>();
-        __syncthreads();
+    for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-        for (int x = 0; x < 64 * PIECES / kGradThreads; ++x) {
+        for (int x = 0; x < X4; ++x) {
             const int e = tid + x * kGradThreads;
-            const uint4 r4 = *reinterpret_cast<const uint4 *>(Mt + tile_off<ROW>(e / PIECES, e % PIECES));
-            const uint32_t *rw = reinterpret_cast<const uint32_t *>(&r4), *sw = reinterpret_cast<const uint32_t *>(&s4[x]);
+            const uint32_t o = tile_off<ROW>(e / PIECES, e % PIECES);
+            const uint4 r4 = *reinterpret_cast<const uint4 *>((mb ? Pt : Wt) + o);
+            const uint4 m4 = mb + 1 < MB ? s4[x] : *reinterpret_cast<const uint4 *>(Mt + o);
+            const uint32_t *rw = reinterpret_cast<const uint32_t *>(&r4), *sw = reinterpret_cast<const uint32_t *>(&m4);
 #pragma unroll
             for (int q = 0; q < 4; ++q) in = fmaf(low_f(rw[q]), low_f(sw[q]), fmaf(high_f(rw[q]), high_f(sw[q]), in));
         }
-        times_rows(y, Et, mb);
-        if (mb + 1 < MB) {
-            __syncthreads();
-            load_rows(R, mb + 1);
+    if (a.pw) {  // u for the pooled keys' share, into the last rows' place
+        __syncthreads();
+        for (int e = tid; e < kCH * PIECES; e += kGradThreads) {
+            const int r = e / PIECES, pc = e % PIECES;
+            cp16(smem_addr(Mt) + tile_off<ROW>(r, pc), a.u + (row0 + (r < w.cnt ? r : 0)) * D + pc * 8, r < w.cnt);
         }
+        cp_commit();
     }
+    times_rows(y, Et, Wt, 0);
+    if (MB > 1) times_rows(y, Et, Pt, 1);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) in += __shfl_xor_sync(0xffffffffu, in, o);
     if (lane == 0) red[warp] = in;
@@ -1286,15 +1295,9 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
             y[n][3] = fmaf(be1, y[n][3], -z[n][3]);
         }
     }
-    __syncthreads();  // the tiles have been read, the sums are there
+    cp_wait<0>();
+    __syncthreads();  // u and the sums are there
     if (a.pw) {  // the pooled keys' share: rho after the chunk + sum over the chunk's tokens t >= j of pw_t u_t
-        for (int e = tid; e < kCH * PIECES; e += kGradThreads) {
-            const int r = e / PIECES, pc = e % PIECES;
-            cp16(smem_addr(Et) + tile_off<ROW>(r, pc), a.u + (row0 + (r < w.cnt ? r : 0)) * D + pc * 8, r < w.cnt);
-        }
-        cp_commit();
-        cp_wait<0>();
-        __syncthreads();
 #pragma unroll
         for (int k4 = 0; k4 < 4; ++k4) {
             if (k4 < wm) continue;
@@ -1306,8 +1309,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
                     const int j = m0 + g + 8 * x, t = 8 * (2 * k4 + h) + 2 * c;
                     split2(t >= j ? pw[t] : 0.f, t + 1 >= j ? pw[t + 1] : 0.f, fh[2 * h + x], fl[2 * h + x]);
                 }
-            times_tokens(y, fh, Et, k4);
-            times_tokens(y, fl, Et, k4);
+            times_tokens(y, fh, Mt, k4);
+            times_tokens(y, fl, Mt, k4);
         }
         const float *rho = a.rho + (size_t)blockIdx.x * D + d0 + 2 * c;
 #pragma unroll
