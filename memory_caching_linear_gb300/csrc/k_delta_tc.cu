@@ -922,9 +922,8 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
 // Eight warps: warp % 4 takes 16 tokens, warp / 4 half of the dimensions.  The warps of one half form B1, those of the
 // other B2 (16 rows each), and leave them in shared memory as 16 x 16 blocks of the lower triangle, from which both
 // read them as they lie (with beta_j) and transposed.  A chunk is a chain of loads and small products, so two CTAs
-// share an SM: S comes through one buffer (64 rows at a time, the next ones on their way under the products
-// between), R into the tiles of p and w once these have been read, u into S's, and at most three of the 16 x 64
-// results are held at once.
+// share an SM, no load is waited for that could have been under way before, and tiles that have been read make room:
+// S's second block takes e's tile, R those of p and w, e comes again in S's first block, u in its second.
 // ---------------------------------------------------------------------------
 constexpr int kGradThreads = 256;
 
@@ -948,8 +947,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
     uint8_t *Bt = Mt + G::kM;
     float *cum = reinterpret_cast<float *>(Bt + G::kB), *bet = cum + kCH, *gs = bet + kCH, *pw = gs + kCH;
     float *rowsum = pw + kCH;                      // [4][2][64] by half: Y.k, exp(c) p S q, D R e k, exp(c) w S k
-    float *rowf = rowsum + 8 * kCH, *colf = rowf + 2 * kCH;  // [2][64], [2][4][64]: sums of F over its rows, columns
-    float *red = colf + 8 * kCH;
+    float *rowf = rowsum + 8 * kCH, *colf = rowf + 5 * kCH;  // [2][10][16] sums of F's blocks over their columns, rows
+    float *red = colf + 5 * kCH;
     const Where w = chunk_at(a, blockIdx.x);
     if (w.cnt <= 0) return;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, c = lane % 4;
@@ -960,40 +959,48 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
     auto load_rows = [&](uint8_t *dst, const __nv_bfloat16 *src, int b) {  // rows 64 b .. of S or R
         for (int e = tid; e < 64 * PIECES; e += kGradThreads)
             cp16(smem_addr(dst) + tile_off<ROW>(e / PIECES, e % PIECES), src + (size_t)(64 * b * PIECES + e) * 8, true);
-        cp_commit();
     };
-    for (int e = tid; e < kCH * PIECES; e += kGradThreads) {
-        const int r = e / PIECES, pc = e % PIECES;
-        const bool ok = r < w.cnt;
-        const size_t off = (row0 + (ok ? r : 0)) * D + pc * 8;
-        const uint32_t o = tile_off<ROW>(r, pc);
-        cp16(smem_addr(Pt) + o, a.dy + off, ok);
-        cp16(smem_addr(Wt) + o, a.dv + off, ok);
-        cp16(smem_addr(Et) + o, a.E + off, ok);
-        cp16(smem_addr(Qt) + o, a.q + off, ok);
-        cp16(smem_addr(Kt) + o, a.k + off, ok);
-    }
-    load_rows(Mt, S, 0);
+    // the gates' loads first, or they would queue behind the tiles
+    const int gt = warp == 0 ? 2 * lane : tid - kCH;
+    const bool in_chunk = gt >= 0 && gt < w.cnt;
+    float g0 = 0.f, g1 = 1.f, g2 = 0.f;
     if (warp == 0) {
-        const int i = 2 * lane;
-        const float x0 = i < w.cnt ? delta_log(__bfloat162float(a.la[row0 + i])) : 0.f;
-        const float x1 = i + 1 < w.cnt ? delta_log(__bfloat162float(a.la[row0 + i + 1])) : 0.f;
-        float s = x0 + x1;
+        if (in_chunk) g0 = delta_log(__bfloat162float(a.la[row0 + gt]));
+        g1 = gt + 1 < w.cnt ? delta_log(__bfloat162float(a.la[row0 + gt + 1])) : 0.f;
+    } else if (in_chunk) {
+        g0 = __bfloat162float(a.be[row0 + gt]);
+        if (a.gon) g1 = a.gon[(row0 + gt) * a.gw_stride];
+        if (a.pw) g2 = a.pw[(row0 + gt) * a.gw_stride];
+    }
+    auto load_tokens = [&](uint8_t *dst, const __nv_bfloat16 *src) {
+        for (int e = tid; e < kCH * PIECES; e += kGradThreads) {
+            const int r = e / PIECES, pc = e % PIECES;
+            cp16(smem_addr(dst) + tile_off<ROW>(r, pc), src + (row0 + (r < w.cnt ? r : 0)) * D + pc * 8, r < w.cnt);
+        }
+    };
+    load_tokens(Pt, a.dy);
+    load_tokens(Et, a.E);
+    load_tokens(Wt, a.dv);
+    load_tokens(Qt, a.q);
+    load_tokens(Kt, a.k);
+    cp_commit();
+    load_rows(Mt, S, 0);
+    cp_commit();
+    if (warp == 0) {
+        float s = g0 + g1;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const float n = __shfl_up_sync(0xffffffffu, s, o);
             if (lane >= o) s += n;
         }
-        cum[i] = s - x1;
-        cum[i + 1] = s;
+        cum[gt] = s - g1;
+        cum[gt + 1] = s;
+    } else if (gt >= 0 && gt < kCH) {
+        bet[gt] = g0;
+        gs[gt] = g1;
+        pw[gt] = g2;
     }
-    if (tid < kCH) {
-        const bool ok = tid < w.cnt;
-        bet[tid] = ok ? __bfloat162float(a.be[row0 + tid]) : 0.f;
-        gs[tid] = ok && a.gon ? a.gon[(row0 + tid) * a.gw_stride] : 1.f;
-        pw[tid] = ok && a.pw ? a.pw[(row0 + tid) * a.gw_stride] : 0.f;
-    }
-    cp_wait<0>();
+    cp_wait<1>();
     __syncthreads();
     if (a.gon) {  // p = g dy, in place
         for (int e = tid; e < kCH * PIECES; e += kGradThreads) {
@@ -1039,22 +1046,6 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
             }
         }
     };
-    // the warp's 16 rows of `rows` against the tokens of `cols` up to them
-    auto pairs = [&](float (&x)[8][4], const uint8_t *rows, const uint8_t *cols) {
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            uint32_t af[4];
-            ldsm4(af, smem_addr(rows) + tile_off<ROW>(ar, 2 * ks + ac));
-#pragma unroll
-            for (int n2 = 0; n2 < 4; ++n2) {
-                if (n2 > wm) continue;
-                uint32_t bf[4];
-                ldsm4(bf, smem_addr(cols) + tile_off<ROW>(16 * n2 + br, 2 * ks + bc));
-                mma16816(x[2 * n2], af, bf[0], bf[1]);
-                mma16816(x[2 * n2 + 1], af, bf[2], bf[3]);
-            }
-        }
-    };
     // x += (the weighted pairs) times the tokens of `tile`
     auto times_tokens = [&](float (&x)[HN][4], const uint32_t (&f)[4], const uint8_t *tile, int k4) {
 #pragma unroll
@@ -1083,80 +1074,85 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
             rowsum[(2 * what + half) * kCH + m0 + g + 8] = s1;
         }
     };
-    // rows i, columns j < i of F_ij = beta_j D_ij B (rows . k): its row and column sums
-    auto pair_sums = [&](const float (&b)[8][4], const uint8_t *rows, float sign) {
-        float f0 = 0.f, f1 = 0.f;
-#pragma unroll
-        for (int n2 = 0; n2 < 4; ++n2) {
-            float *cf = colf + (4 * half + wm) * kCH + 16 * n2;
-            if (n2 > wm) {
-                if (lane < 16) cf[lane] = 0.f;
-                continue;
-            }
-            float kk[2][4];
-            zero(kk);
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                uint32_t aq[4], bf[4];
-                ldsm4(aq, smem_addr(rows) + tile_off<ROW>(ar, 2 * ks + ac));
-                ldsm4(bf, smem_addr(Kt) + tile_off<ROW>(16 * n2 + br, 2 * ks + bc));
-                mma16816(kk[0], aq, bf[0], bf[1]);
-                mma16816(kk[1], aq, bf[2], bf[3]);
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int n = 2 * n2 + h, j = 8 * n + 2 * c;
-                float col[2] = {0.f, 0.f};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = m0 + g + 8 * (e >> 1), jj = j + (e & 1);
-                    const float f = jj < i ? __expf((e >> 1 ? c_hi : c_lo) - cum[jj]) * bet[jj] * kk[h][e] * sign * b[n][e] : 0.f;
-                    col[e & 1] += f;
-                    if (e >> 1) f1 += f;
-                    else f0 += f;
-                }
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) {
-                    col[0] += __shfl_xor_sync(0xffffffffu, col[0], o);
-                    col[1] += __shfl_xor_sync(0xffffffffu, col[1], o);
-                }
-                if (g == 0) {
-                    cf[8 * h + 2 * c] = col[0];
-                    cf[8 * h + 2 * c + 1] = col[1];
-                }
-            }
-        }
-        f0 += __shfl_xor_sync(0xffffffffu, f0, 1);
-        f0 += __shfl_xor_sync(0xffffffffu, f0, 2);
-        f1 += __shfl_xor_sync(0xffffffffu, f1, 1);
-        f1 += __shfl_xor_sync(0xffffffffu, f1, 2);
-        if (c == 0) {
-            rowf[half * kCH + m0 + g] = f0;
-            rowf[half * kCH + m0 + g + 8] = f1;
-        }
-    };
     // Block (r, q) of B1 (which = 0) or B2: 16 rows of 32 bytes, their two pieces exchanged every four rows.
     auto block = [&](int which, int r, int q) { return smem_addr(Bt) + (which * 10 + r * (r + 1) / 2 + q) * 512; };
     auto block_off = [](int r, int pc) { return (uint32_t)(r * 32 + ((pc ^ ((r >> 2) & 1)) << 4)); };
-    // this warp's rows, weighted with D_ij, into their blocks
-    auto put_blocks = [&](const float (&x)[8][4]) {
+    // The ten blocks of a half go round its warps, three or two to each, five to an SM's quarter.
+    auto block_at = [&](int x, int &r, int &q) {
+        const int blk = (half ? 3 - wm : wm) + 4 * x;
+        r = (blk >= 1) + (blk >= 3) + (blk >= 6);
+        q = blk - r * (r + 1) / 2;
+        return blk;
+    };
+    // 16 tokens of `rows` against 16 of `cols`
+    auto pairs = [&](float (&x)[2][4], const uint8_t *rows, int r, const uint8_t *cols, int q) {
+        zero(x);
 #pragma unroll
-        for (int k4 = 0; k4 < 4; ++k4) {
-            if (k4 > wm) continue;
-            uint32_t f[4];
+        for (int ks = 0; ks < KS; ++ks) {
+            uint32_t af[4], bf[4];
+            ldsm4(af, smem_addr(rows) + tile_off<ROW>(16 * r + (lane & 15), 2 * ks + ac));
+            ldsm4(bf, smem_addr(cols) + tile_off<ROW>(16 * q + br, 2 * ks + bc));
+            mma16816(x[0], af, bf[0], bf[1]);
+            mma16816(x[1], af, bf[2], bf[3]);
+        }
+    };
+    // a block of B, weighted with D_ij: kept, and in bf16 into shared memory
+    auto put_block = [&](float (&x)[2][4], int r, int q) {
+        uint32_t f[4];
+        const float c0 = cum[16 * r + g], c1 = cum[16 * r + g + 8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float2 cj = *reinterpret_cast<const float2 *>(cum + 16 * q + 8 * h + 2 * c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int il = g + 8 * (e >> 1), jl = 8 * h + 2 * c + (e & 1);
+                x[h][e] = r > q || jl < il || (half == 0 && jl == il) ? x[h][e] * __expf((e >> 1 ? c1 : c0) - (e & 1 ? cj.y : cj.x)) : 0.f;
+            }
+            f[2 * h] = pack2(x[h][0], x[h][1]);
+            f[2 * h + 1] = pack2(x[h][2], x[h][3]);
+        }
+        stsm4(block(half, r, q) + block_off(lane & 15, lane >> 4), f[0], f[1], f[2], f[3]);
+    };
+    // F_ij = beta_j B_ij (rows_i . k_j) for j < i: the sums over a block's columns and rows
+    auto pair_sums = [&](const float (&b)[2][4], const uint8_t *rows, float sign, int blk, int r, int q) {
+        float kk[2][4], f0 = 0.f, f1 = 0.f, col[2][2];
+        pairs(kk, rows, r, Kt, q);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float2 bj = *reinterpret_cast<const float2 *>(bet + 16 * q + 8 * h + 2 * c);
+            col[h][0] = col[h][1] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int il = g + 8 * (e >> 1), jl = 8 * h + 2 * c + (e & 1);
+                const float f = r > q || jl < il ? sign * (e & 1 ? bj.y : bj.x) * kk[h][e] * b[h][e] : 0.f;
+                col[h][e & 1] += f;
+                if (e >> 1) f1 += f;
+                else f0 += f;
+            }
+        }
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = m0 + g + 8 * (e >> 1), j = 16 * k4 + 8 * h + 2 * c + (e & 1);
-                    v[e] = j < i || (half == 0 && j == i) ? x[2 * k4 + h][e] * __expf((e >> 1 ? c_hi : c_lo) - cum[j]) : 0.f;
-                }
-                f[2 * h] = pack2(v[0], v[1]);
-                f[2 * h + 1] = pack2(v[2], v[3]);
+                col[h][0] += __shfl_xor_sync(0xffffffffu, col[h][0], o);
+                col[h][1] += __shfl_xor_sync(0xffffffffu, col[h][1], o);
             }
-            stsm4(block(half, wm, k4) + block_off(lane & 15, lane >> 4), f[0], f[1], f[2], f[3]);
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            f0 += __shfl_xor_sync(0xffffffffu, f0, o);
+            f1 += __shfl_xor_sync(0xffffffffu, f1, o);
         }
+        float *rf = rowf + (half * 10 + blk) * 16, *cf = colf + (half * 10 + blk) * 16;
+        if (c == 0) {
+            rf[g] = f0;
+            rf[g + 8] = f1;
+        }
+        if (g == 0)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                cf[8 * h + 2 * c] = col[h][0];
+                cf[8 * h + 2 * c + 1] = col[h][1];
+            }
     };
     // x += (this warp's rows of B, with beta_j) times the keys
     auto times_keys = [&](float (&x)[HN][4], int which) {
@@ -1190,49 +1186,79 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
             }
     };
 
+    // Where S comes in two blocks: the second takes e's place once the pairs have read it, and e comes again with R.
+    uint8_t *const Sl = MB > 1 ? Et : Mt, *const E2 = MB > 1 ? Mt : Et;
+    {
+        float b[3][2][4];
+        int r, q;
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+            if (block_at(x, r, q) < 10) {
+                pairs(b[x], half ? Wt : Pt, r, Et, q);
+                put_block(b[x], r, q);
+            }
+        __syncthreads();  // the blocks are there, e has been read
+        if (MB > 1) load_rows(Et, S, 1);
+        cp_commit();
+#pragma unroll
+        for (int x = 0; x < 3; ++x) {
+            const int blk = block_at(x, r, q);
+            if (blk < 10) pair_sums(b[x], half ? Kt : Qt, half ? -1.f : 1.f, blk, r, q);
+        }
+    }
+    cp_wait<0>();
+    __syncthreads();
     float z[HN][4];
     zero(z);
     {
-        float dq[HN][4], b[8][4];
-        zero(b);
+        float dq[HN][4];
         zero(dq);
         times_rows(dq, Pt, Mt, 0);
         times_rows(z, Wt, Mt, 0);
         if (MB > 1) {
-            __syncthreads();  // the rows have been read
-            load_rows(Mt, S, 1);
+            times_rows(dq, Pt, Et, 1);
+            times_rows(z, Wt, Et, 1);
         }
-        pairs(b, half ? Wt : Pt, Et);
-        pair_sums(b, half ? Kt : Qt, half ? -1.f : 1.f);
-        put_blocks(b);
-        if (MB > 1) {
-            cp_wait<0>();
-            __syncthreads();
-            times_rows(dq, Pt, Mt, 1);
-            times_rows(z, Wt, Mt, 1);
-        }
-        __syncthreads();  // p and w have been read: their tiles take R; the blocks are there
+        __syncthreads();  // p and w have been read: their tiles take R
         load_rows(Wt, R, 0);
-        if (MB > 1) load_rows(Pt, R, 1);
+        if (MB > 1) {
+            load_rows(Pt, R, 1);
+            load_tokens(Mt, a.E);
+        }
+        cp_commit();
         const float e0 = __expf(c_lo), e1 = __expf(c_hi);
         scale(dq, e0, e1);
         scale(z, e0, e1);
         row_dot(dq, Qt, 1);
         row_dot(z, Kt, 3);
-        times_keys(dq, 0);
-        times_keys(z, 1);
-        if (a.dq_add) {
+        float2 add[HN / 2][2];  // half of the cached memories' share at once, on its way under the products
+        auto fetch = [&](int hf) {
 #pragma unroll
-            for (int n = 0; n < HN; ++n)
+            for (int n = 0; n < HN / 2; ++n)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const int t = m0 + g + 8 * x;
-                    if (t >= w.cnt) continue;
-                    const float2 f = *reinterpret_cast<const float2 *>(a.dq_add + (row0 + t) * D + d0 + 8 * n + 2 * c);
-                    dq[n][2 * x] += f.x;
-                    dq[n][2 * x + 1] += f.y;
+                    add[n][x] = t < w.cnt ? *reinterpret_cast<const float2 *>(a.dq_add + (row0 + t) * D + d0 + 8 * (hf * (HN / 2) + n) + 2 * c)
+                                          : make_float2(0.f, 0.f);
                 }
+        };
+        auto join = [&](int hf) {
+#pragma unroll
+            for (int n = 0; n < HN / 2; ++n)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    dq[hf * (HN / 2) + n][2 * x] += add[n][x].x;
+                    dq[hf * (HN / 2) + n][2 * x + 1] += add[n][x].y;
+                }
+        };
+        if (a.dq_add) fetch(0);
+        times_keys(z, 1);
+        if (a.dq_add) {
+            join(0);
+            fetch(1);
         }
+        times_keys(dq, 0);
+        if (a.dq_add) join(1);
         store(a.dq, dq);
     }
     float y[HN][4];
@@ -1252,21 +1278,18 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
             const int e = tid + x * kGradThreads;
             const uint32_t o = tile_off<ROW>(e / PIECES, e % PIECES);
             const uint4 r4 = *reinterpret_cast<const uint4 *>((mb ? Pt : Wt) + o);
-            const uint4 m4 = mb + 1 < MB ? s4[x] : *reinterpret_cast<const uint4 *>(Mt + o);
+            const uint4 m4 = mb + 1 < MB ? s4[x] : *reinterpret_cast<const uint4 *>(Sl + o);
             const uint32_t *rw = reinterpret_cast<const uint32_t *>(&r4), *sw = reinterpret_cast<const uint32_t *>(&m4);
 #pragma unroll
             for (int q = 0; q < 4; ++q) in = fmaf(low_f(rw[q]), low_f(sw[q]), fmaf(high_f(rw[q]), high_f(sw[q]), in));
         }
-    if (a.pw) {  // u for the pooled keys' share, into the last rows' place
+    if (a.pw) {  // u for the pooled keys' share, into their place
         __syncthreads();
-        for (int e = tid; e < kCH * PIECES; e += kGradThreads) {
-            const int r = e / PIECES, pc = e % PIECES;
-            cp16(smem_addr(Mt) + tile_off<ROW>(r, pc), a.u + (row0 + (r < w.cnt ? r : 0)) * D + pc * 8, r < w.cnt);
-        }
+        load_tokens(Sl, a.u);
         cp_commit();
     }
-    times_rows(y, Et, Wt, 0);
-    if (MB > 1) times_rows(y, Et, Pt, 1);
+    times_rows(y, E2, Wt, 0);
+    if (MB > 1) times_rows(y, E2, Pt, 1);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) in += __shfl_xor_sync(0xffffffffu, in, o);
     if (lane == 0) red[warp] = in;
@@ -1309,8 +1332,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
                     const int j = m0 + g + 8 * x, t = 8 * (2 * k4 + h) + 2 * c;
                     split2(t >= j ? pw[t] : 0.f, t + 1 >= j ? pw[t + 1] : 0.f, fh[2 * h + x], fl[2 * h + x]);
                 }
-            times_tokens(y, fh, Mt, k4);
-            times_tokens(y, fl, Mt, k4);
+            times_tokens(y, fh, Sl, k4);
+            times_tokens(y, fl, Sl, k4);
         }
         const float *rho = a.rho + (size_t)blockIdx.x * D + d0 + 2 * c;
 #pragma unroll
@@ -1334,9 +1357,12 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
             const int t = i + x;
             const float f = bet[t] * (rowsum[4 * kCH + t] + rowsum[5 * kCH + t]);
             float r = (rowsum[2 * kCH + t] + rowsum[3 * kCH + t]) - (rowsum[6 * kCH + t] + rowsum[7 * kCH + t]) - f;
-            r += rowf[t] + rowf[kCH + t];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) r -= colf[q * kCH + t];
+            for (int y = 0; y < 8; ++y) {  // block (t's, y) of its row, (y, t's) of its column, of B1 and B2
+                const int b0 = t / 16, b1 = y % 4, base = y / 4 * 10;
+                if (b1 <= b0) r += rowf[(base + b0 * (b0 + 1) / 2 + b1) * 16 + t % 16];
+                if (b1 >= b0) r -= colf[(base + b1 * (b1 + 1) / 2 + b0) * 16 + t % 16];
+            }
             (x ? h1 : h0) = r;
             fr += f;
         }
