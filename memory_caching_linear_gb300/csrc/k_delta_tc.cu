@@ -24,11 +24,16 @@
 
 #include "mc_internal.cuh"
 #include "mma_sync.cuh"
+#include "sm100.cuh"
+#include "tensormap.cuh"
 
 namespace mc {
 namespace {
 
 using namespace mma;
+using namespace sm100;
+
+__device__ int g_delta_abort;
 
 constexpr int kCH = kDeltaChunk;
 
@@ -378,12 +383,43 @@ __global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a)
     }
 }
 
+// The walks' tiles of tokens come by TMA: 64 x 64 panels of q and k, and the CTA's columns of v (or dy).
+struct DeltaMaps {
+    CUtensorMap k, q, v;
+};
+constexpr int kPanel = kCH * 128;
+__device__ __forceinline__ uint32_t panel_off(int r, int c) { return (uint32_t)((c >> 3) * kPanel) + tile_off<128>(r, c & 7); }
+
+// What follows the tiles in shared memory: a barrier per stage, one for the single buffer, and whether a wait gave up.
+struct WalkSync {
+    uint64_t full[2], single;
+    int abort_flag, pad;
+};
+__device__ __forceinline__ bool walk_sync_init(WalkSync *y, const void *sm, int tid)
+{
+    if (tid == 0) {
+        y->abort_flag = (smem_addr(sm) & 1023) != 0;  // (the panels' swizzle counts from 1024-byte boundaries)
+        mbar_init(&y->full[0], 1);
+        mbar_init(&y->full[1], 1);
+        mbar_init(&y->single, 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    return y->abort_flag == 0;
+}
+// Rows from cnt on of a tile of ROW bytes a row: a chunk's last tokens may be another segment's.
+template <int ROW, int NT>
+__device__ __forceinline__ void clear_rows(uint8_t *tile, int cnt, int tid)
+{
+    for (int e = cnt * (ROW / 16) + tid; e < kCH * (ROW / 16); e += NT) reinterpret_cast<uint4 *>(tile)[e] = make_uint4(0, 0, 0, 0);
+}
+
 // A warp's own 32 bytes of every row of the V (or dy) tile: once read, its staging area for what it writes.
 template <int NW>
 __device__ __forceinline__ uint32_t own_off(int r, int pc, int warp)
 {
-    constexpr int VP = NW * 2;  // 16-byte pieces of a row; they turn with the row
-    return (uint32_t)(r * NW * 32 + (((2 * warp + pc) ^ (r & (VP < 8 ? VP - 1 : 7))) << 4));
+    // 16-byte pieces of a row, exchanged as the copies of 64-byte and of 128-byte rows leave them
+    return (uint32_t)(r * NW * 32 + (((2 * warp + pc) ^ (NW == 4 ? r & 7 : r >> 1 & 3)) << 4));
 }
 
 // 16 values x 64 tokens in operand registers to rows of 16 values.  Where two warps hold the same values (KP = 2), each
@@ -440,7 +476,8 @@ __device__ __forceinline__ void pair_sum(float4 *xb, int warp, int lane, F each,
 
 // ---------------------------------------------------------------------------
 // delta_walk_tc: one CTA per (bh, segment, 16 NW value rows); NW warps of 16 rows.  Two stages of
-// the chunk's K, V columns, (Q,) and record, filled by asynchronous copies one chunk ahead.
+// the chunk's K, V columns, (Q,) and record, filled by TMA one chunk ahead: copied by the threads, 16 bytes at a
+// time, they took a fifth of the time (shared memory's pipe is what the products wait for, too).
 // ---------------------------------------------------------------------------
 template <int D, int NW, bool READ>
 struct WalkSmem {
@@ -452,11 +489,12 @@ struct WalkSmem {
 };
 
 template <int D, int NW, int KP, bool READ, bool FULL>
-__global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) delta_walk_tc(DeltaTcArgs a)
+__global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) delta_walk_tc(DeltaTcArgs a, const __grid_constant__ DeltaMaps maps)
 {
     using W = WalkSmem<D, NW, READ>;
-    constexpr int ROW = D * 2, PIECES = D / 8, NT = 32 * NW * KP, KS = D / 16 / KP, VP = NW * 2;
-    extern __shared__ __align__(16) uint8_t sm[];
+    constexpr int NT = 32 * NW * KP, KS = D / 16 / KP;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    WalkSync *sync = reinterpret_cast<WalkSync *>(sm + W::kTotal);
     constexpr int splits = D / (16 * NW);
     const int rs = (int)blockIdx.x % splits;
     const long long sid = blockIdx.x / splits;
@@ -466,26 +504,19 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
     const int vbase = rs * 16 * NW;  // the CTA's first value row
     const int wr = warp / KP, kp = KP == 1 ? 0 : warp % KP, k0 = kp * KS;  // the warp's rows, its share of the keys
 
-    auto load = [&](int ch) {
+    auto load = [&](int ch) {  // one thread
         uint8_t *st = sm + (ch & 1) * W::kStage;
-        const int cnt = min(kCH, len - ch * kCH);
-        const size_t row0 = (size_t)bh * a.L + t0 + ch * kCH;
-        for (int e = tid; e < kCH * PIECES; e += NT) {
-            const int r = e / PIECES, pc = e % PIECES;
-            const size_t off = (row0 + (r < cnt ? r : 0)) * D + pc * 8;
-            cp16(smem_addr(st) + tile_off<ROW>(r, pc), a.k + off, r < cnt);
-            if (READ) cp16(smem_addr(st) + W::kK + W::kV + tile_off<ROW>(r, pc), a.q + off, r < cnt);
+        uint64_t *bar = &sync->full[ch & 1];
+        mbar_arrive_expect_tx(bar, W::kStage);
+#pragma unroll
+        for (int p = 0; p < D / 64; ++p) {
+            tma_load_3d(st + p * kPanel, &maps.k, 64 * p, t0 + ch * kCH, bh, bar);
+            if (READ) tma_load_3d(st + W::kK + W::kV + p * kPanel, &maps.q, 64 * p, t0 + ch * kCH, bh, bar);
         }
-        for (int e = tid; e < kCH * VP; e += NT) {
-            const int r = e / VP, pc = e % VP;
-            cp16(smem_addr(st) + W::kK + own_off<NW>(r, pc, 0), a.v + (row0 + (r < cnt ? r : 0)) * D + vbase + pc * 8, r < cnt);
-        }
-        const uint8_t *rec = a.rec + ((size_t)sid * a.NCH + ch) * kRec;
-        const uint32_t dst = smem_addr(st) + W::kStage - W::kR;
-        for (int e = tid; e < W::kR / 16; e += NT)
-            cp16(dst + e * 16, rec + e * 16, true);
-        cp_commit();
+        tma_load_3d(st + W::kK, &maps.v, vbase, t0 + ch * kCH, bh, bar);
+        bulk_load(st + W::kStage - W::kR, a.rec + ((size_t)sid * a.NCH + ch) * kRec, W::kR, bar);
     };
+    bool ok = walk_sync_init(sync, sm, tid);
 
     float S[2 * KS][4];  // 16 rows x D / KP keys: tile n holds keys 16 k0 + 8 n ..
 #pragma unroll
@@ -493,17 +524,22 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
 #pragma unroll
         for (int e = 0; e < 4; ++e) S[n][e] = 0.f;
 
-    load(0);
+    if (ok && tid == 0) load(0);
     for (int ch = 0; ch < nch; ++ch) {
-        cp_wait<0>();
-        __syncthreads();  // the chunk has come, and the stage of the one before is free
-        if (READ) {
-            const uint8_t *src = a.rec + ((size_t)sid * a.NCH + ch) * kRec + kRecT + kRecV;
-            for (int e = tid; e < kRecT / 16; e += NT) cp16(smem_addr(sm) + 2 * W::kStage + e * 16, src + e * 16, true);
-            cp_commit();
+        if (ok) ok = mbar_wait(&sync->full[ch & 1], ch / 2 & 1, &sync->abort_flag);
+        fence_async_smem();  // what was staged in the other stage goes before what will come there
+        if (__syncthreads_or(!ok)) {
+            if (tid == 0) atomicExch(&g_delta_abort, 1);
+            return;
         }
-        if (ch + 1 < nch) load(ch + 1);
-        else cp_commit();
+        if (tid == 0) {
+            if (READ) {
+                mbar_arrive_expect_tx(&sync->single, kRecT);
+                bulk_load(sm + 2 * W::kStage, a.rec + ((size_t)sid * a.NCH + ch) * kRec + kRecT + kRecV, kRecT, &sync->single);
+            }
+            if (ch + 1 < nch) load(ch + 1);
+        }
+        __syncwarp();
         uint8_t *st = sm + (ch & 1) * W::kStage, *vown = st + W::kK;
         const uint32_t kt = smem_addr(st), vt = kt + W::kK, qt = vt + W::kV;
         const uint8_t *rec = st + W::kStage - W::kR;
@@ -511,6 +547,15 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
         const size_t row0 = (size_t)bh * a.L + t0 + ch * kCH;
         const int cnt = min(kCH, len - ch * kCH);
         const size_t cidx = (size_t)sid * a.NCH + ch;
+        if (cnt < kCH) {
+#pragma unroll
+            for (int p = 0; p < D / 64; ++p) {
+                clear_rows<128, NT>(st + p * kPanel, cnt, tid);
+                if (READ) clear_rows<128, NT>(st + W::kK + W::kV + p * kPanel, cnt, tid);
+            }
+            clear_rows<NW * 32, NT>(vown, cnt, tid);
+            __syncthreads();
+        }
 
         // (S K^T) and (S Q^T): rows values, columns tokens
         float X[8][4], O[8][4];
@@ -529,7 +574,7 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
 #pragma unroll
             for (int n2 = 0; n2 < 4; ++n2) {
                 uint32_t b[4];
-                ldsm4(b, kt + tile_off<ROW>(16 * n2 + br, 2 * (k0 + ks) + bc));
+                ldsm4(b, kt + panel_off(16 * n2 + br, 2 * (k0 + ks) + bc));
                 mma16816(X[2 * n2], hi, b[0], b[1]);
                 mma16816(X[2 * n2 + 1], hi, b[2], b[3]);
                 if (FULL) {
@@ -537,7 +582,7 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
                     mma16816(X[2 * n2 + 1], lo, b[2], b[3]);
                 }
                 if (READ) {  // the output is bf16 and nothing cancels here: one term
-                    ldsm4(b, qt + tile_off<ROW>(16 * n2 + br, 2 * (k0 + ks) + bc));
+                    ldsm4(b, qt + panel_off(16 * n2 + br, 2 * (k0 + ks) + bc));
                     mma16816(O[2 * n2], hi, b[0], b[1]);
                     mma16816(O[2 * n2 + 1], hi, b[2], b[3]);
                 }
@@ -548,7 +593,7 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
         for (int k4 = 0; k4 < 4; ++k4)
             ldsm4t(v4[k4], vt + own_off<NW>(16 * k4 + (lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1, wr));
         if (KP == 2)
-            pair_sum<READ ? 12 : 8>(reinterpret_cast<float4 *>(sm + W::kTotal), warp, lane,
+            pair_sum<READ ? 12 : 8>(reinterpret_cast<float4 *>(sm + W::kTotal + sizeof(WalkSync)), warp, lane,
                      [&](auto leave) {
 #pragma unroll
                          for (int n = 0; n < 8; ++n) {
@@ -620,8 +665,8 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
             split2(be.x * X[n][2], be.y * X[n][3], uh[n / 2][2 * (n & 1) + 1], ul[n / 2][2 * (n & 1) + 1]);
         }
         if (READ) {
-            cp_wait<1>();  // (the next chunk may still be on its way)
-            __syncthreads();
+            if (ok) ok = mbar_wait(&sync->single, ch & 1, &sync->abort_flag);
+            __syncwarp();
             const uint4 *pt = reinterpret_cast<const uint4 *>(sm + 2 * W::kStage) + lane;
 #pragma unroll
             for (int k4 = 0; k4 < 4; ++k4)
@@ -681,7 +726,7 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
 #pragma unroll
             for (int n2 = 0; n2 < KS; ++n2) {
                 uint32_t b[4];
-                ldsm4t(b, kt + tile_off<ROW>(16 * k4 + tr, 2 * (k0 + n2) + tc));
+                ldsm4t(b, kt + panel_off(16 * k4 + tr, 2 * (k0 + n2) + tc));
                 mma16816(S[2 * n2], uh[k4], b[0], b[1]);
                 mma16816(S[2 * n2 + 1], uh[k4], b[2], b[3]);
                 mma16816(S[2 * n2], ul[k4], b[0], b[1]);
@@ -716,16 +761,18 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
 template <int D, int NW>
 struct RWalkSmem {
     static constexpr int kK = kCH * D * 2, kV = kCH * NW * 32;
-    static constexpr int kStage = 2 * kK + kV + kRecV + 256;  // K, Q, dy columns, vectors, gates
-    static constexpr int kTotal = 2 * kStage + 2 * kRecT;
+    static constexpr int kStage = 2 * kK + kV + kRecV;  // K, Q, dy columns, vectors
+    static constexpr int kTotal = 2 * kStage + 2 * kRecT + 2 * kCH * 4;  // T and P, two chunks' gates
 };
 
 template <int D, int NW, int KP>
-__global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(DeltaTcArgs a)
+__global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(DeltaTcArgs a, const __grid_constant__ DeltaMaps maps)
 {
     using W = RWalkSmem<D, NW>;
-    constexpr int ROW = D * 2, PIECES = D / 8, NT = 32 * NW * KP, KS = D / 16 / KP, VP = NW * 2;
-    extern __shared__ __align__(16) uint8_t sm[];
+    constexpr int NT = 32 * NW * KP, KS = D / 16 / KP;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    WalkSync *sync = reinterpret_cast<WalkSync *>(sm + W::kTotal);
+    float *gates = reinterpret_cast<float *>(sm + 2 * W::kStage + 2 * kRecT);
     constexpr int splits = D / (16 * NW);
     const int rs = (int)blockIdx.x % splits;
     const long long sid = blockIdx.x / splits;
@@ -735,27 +782,25 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
     const int vbase = rs * 16 * NW;
     const int wr = warp / KP, kp = KP == 1 ? 0 : warp % KP, k0 = kp * KS;
 
-    auto load = [&](int ch) {
+    auto load = [&](int ch) {  // one thread
         uint8_t *st = sm + (ch & 1) * W::kStage;
-        const int cnt = min(kCH, len - ch * kCH);
-        const size_t row0 = (size_t)bh * a.L + t0 + ch * kCH;
-        for (int e = tid; e < kCH * PIECES; e += NT) {
-            const int r = e / PIECES, pc = e % PIECES;
-            const size_t off = (row0 + (r < cnt ? r : 0)) * D + pc * 8;
-            cp16(smem_addr(st) + tile_off<ROW>(r, pc), a.k + off, r < cnt);
-            cp16(smem_addr(st) + W::kK + tile_off<ROW>(r, pc), a.q + off, r < cnt);
+        uint64_t *bar = &sync->full[ch & 1];
+        mbar_arrive_expect_tx(bar, W::kStage);
+#pragma unroll
+        for (int p = 0; p < D / 64; ++p) {
+            tma_load_3d(st + p * kPanel, &maps.k, 64 * p, t0 + ch * kCH, bh, bar);
+            tma_load_3d(st + W::kK + p * kPanel, &maps.q, 64 * p, t0 + ch * kCH, bh, bar);
         }
-        for (int e = tid; e < kCH * VP; e += NT) {
-            const int r = e / VP, pc = e % VP;
-            cp16(smem_addr(st) + 2 * W::kK + own_off<NW>(r, pc, 0), a.dy + (row0 + (r < cnt ? r : 0)) * D + vbase + pc * 8, r < cnt);
-        }
-        const uint8_t *rec = a.rrec + ((size_t)sid * a.NCH + ch) * kDeltaRRecBytes;
-        const uint32_t dst = smem_addr(st) + 2 * W::kK + W::kV;
-        for (int e = tid; e < kRecV / 16; e += NT) cp16(dst + e * 16, rec + e * 16, true);
-        float *gs = reinterpret_cast<float *>(st + 2 * W::kK + W::kV + kRecV);
-        for (int e = tid; e < kCH; e += NT) gs[e] = a.gon && e < cnt ? a.gon[(row0 + e) * a.gw_stride] : 1.f;
-        cp_commit();
+        tma_load_3d(st + 2 * W::kK, &maps.v, vbase, t0 + ch * kCH, bh, bar);
+        bulk_load(st + 2 * W::kK + W::kV, a.rrec + ((size_t)sid * a.NCH + ch) * kDeltaRRecBytes, kRecV, bar);
     };
+    auto gate = [&](int ch) {
+        return a.gon && ch * kCH + tid < len ? a.gon[((size_t)bh * a.L + t0 + ch * kCH + tid) * a.gw_stride] : 1.f;
+    };
+    bool ok = walk_sync_init(sync, sm, tid);
+    if (ok && tid == 0) load(nch - 1);
+    __syncwarp();
+    if (tid < kCH) gates[(nch - 1 & 1) * kCH + tid] = gate(nch - 1);
 
     float R[2 * KS][4];
     if (a.G && seg < a.N - 1) {  // partial sums, in order
@@ -777,24 +822,34 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
             for (int e = 0; e < 4; ++e) R[n][e] = 0.f;
     }
 
-    load(nch - 1);
     for (int ch = nch - 1; ch >= 0; --ch) {
-        cp_wait<0>();
-        __syncthreads();
-        {
-            const uint8_t *src = a.rrec + ((size_t)sid * a.NCH + ch) * kDeltaRRecBytes + kRecV;
-            for (int e = tid; e < 2 * kRecT / 16; e += NT) cp16(smem_addr(sm) + 2 * W::kStage + e * 16, src + e * 16, true);
-            cp_commit();
+        const int turn = nch - 1 - ch;
+        if (ok) ok = mbar_wait(&sync->full[ch & 1], turn / 2 & 1, &sync->abort_flag);
+        fence_async_smem();  // what was staged in the other stage goes before what will come there
+        if (__syncthreads_or(!ok)) {
+            if (tid == 0) atomicExch(&g_delta_abort, 1);
+            return;
         }
-        if (ch > 0) load(ch - 1);
-        else cp_commit();
+        if (tid == 0) {
+            mbar_arrive_expect_tx(&sync->single, 2 * kRecT);
+            bulk_load(sm + 2 * W::kStage, a.rrec + ((size_t)sid * a.NCH + ch) * kDeltaRRecBytes + kRecV, 2 * kRecT, &sync->single);
+            if (ch > 0) load(ch - 1);
+        }
+        __syncwarp();
+        const float next_gate = ch > 0 && tid < kCH ? gate(ch - 1) : 1.f;
         uint8_t *st = sm + (ch & 1) * W::kStage, *vown = st + 2 * W::kK;
         const uint32_t kt = smem_addr(st), qt = kt + W::kK, vt = qt + W::kK;
         const uint8_t *rec = st + 2 * W::kK + W::kV;
         const float *vec = reinterpret_cast<const float *>(rec);
-        const float *gs = reinterpret_cast<const float *>(rec + kRecV);
+        const float *gs = gates + (ch & 1) * kCH;
         const size_t row0 = (size_t)bh * a.L + t0 + ch * kCH;
         const int cnt = min(kCH, len - ch * kCH);
+        if (cnt < kCH) {
+#pragma unroll
+            for (int p = 0; p < 2 * (D / 64); ++p) clear_rows<128, NT>(st + p * kPanel, cnt, tid);
+            clear_rows<NW * 32, NT>(vown, cnt, tid);
+            __syncthreads();
+        }
         float X[8][4];
 #pragma unroll
         for (int n = 0; n < 8; ++n)
@@ -808,7 +863,7 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
 #pragma unroll
             for (int n2 = 0; n2 < 4; ++n2) {
                 uint32_t b[4];
-                ldsm4(b, kt + tile_off<ROW>(16 * n2 + br, 2 * (k0 + ks) + bc));
+                ldsm4(b, kt + panel_off(16 * n2 + br, 2 * (k0 + ks) + bc));
                 mma16816(X[2 * n2], rf, b[0], b[1]);
                 mma16816(X[2 * n2 + 1], rf, b[2], b[3]);
             }
@@ -818,7 +873,7 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
         for (int k4 = 0; k4 < 4; ++k4)
             ldsm4t(v4[k4], vt + own_off<NW>(16 * k4 + (lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1, wr));
         if (KP == 2)
-            pair_sum<8>(reinterpret_cast<float4 *>(sm + W::kTotal), warp, lane,
+            pair_sum<8>(reinterpret_cast<float4 *>(sm + W::kTotal + sizeof(WalkSync)), warp, lane,
                      [&](auto leave) {
 #pragma unroll
                          for (int n = 0; n < 8; ++n) leave(n, X[n]);
@@ -850,8 +905,8 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
             __nv_bfloat16 *dst = a.R_c + (((size_t)sid * a.NCH + ch) * D + vbase + 16 * wr) * D + 16 * k0;
             put_rows(R, 1.f, lane, [&](int r, int n, int at, const uint2 &x) { *reinterpret_cast<uint2 *>(dst + (size_t)r * D + 8 * n + at / 2) = x; });
         }
-        cp_wait<1>();  // T and P (the next chunk may still be on its way)
-        __syncthreads();
+        if (ok) ok = mbar_wait(&sync->single, turn & 1, &sync->abort_flag);  // T and P
+        __syncwarp();
         const uint4 *lt = reinterpret_cast<const uint4 *>(sm + 2 * W::kStage) + lane;
         const uint4 *pt = reinterpret_cast<const uint4 *>(sm + 2 * W::kStage + kRecT) + lane;
 #pragma unroll
@@ -905,15 +960,16 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
 #pragma unroll
             for (int n2 = 0; n2 < KS; ++n2) {
                 uint32_t b[4];
-                ldsm4t(b, kt + tile_off<ROW>(16 * k4 + tr, 2 * (k0 + n2) + tc));
+                ldsm4t(b, kt + panel_off(16 * k4 + tr, 2 * (k0 + n2) + tc));
                 mma16816(R[2 * n2], wf[k4], b[0], b[1]);
                 mma16816(R[2 * n2 + 1], wf[k4], b[2], b[3]);
                 mma16816(R[2 * n2], wl[k4], b[0], b[1]);
                 mma16816(R[2 * n2 + 1], wl[k4], b[2], b[3]);
-                ldsm4t(b, qt + tile_off<ROW>(16 * k4 + tr, 2 * (k0 + n2) + tc));
+                ldsm4t(b, qt + panel_off(16 * k4 + tr, 2 * (k0 + n2) + tc));
                 mma16816(R[2 * n2], pg[k4], b[0], b[1]);
                 mma16816(R[2 * n2 + 1], pg[k4], b[2], b[3]);
             }
+        if (ch > 0 && tid < kCH) gates[(ch - 1 & 1) * kCH + tid] = next_gate;
     }
 }
 
@@ -1391,14 +1447,24 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
 // against 1: 32 heads (128 CTAs) 89 68 82 against 111 93 102 us; 48 heads (192 CTAs) 171 101 129 against 111 93 102 us.
 inline bool split_keys(const Problem &p) { return (long long)p.BH * p.N * (p.d / 32) <= 152; }
 
+template <int D, int NW>
+bool make_maps(DeltaMaps *m, const Problem &p, const DeltaTcArgs &a, const void *v)
+{
+    const auto sw = NW == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    return make_tmap_bf16_3d_sw128(&m->k, a.k, p.BH, p.L, D, kCH) && make_tmap_bf16_3d_sw128(&m->q, a.q, p.BH, p.L, D, kCH) &&
+           make_tmap_bf16_3d(&m->v, v, p.BH, p.L, D, 16 * NW, kCH, sw);
+}
+
 template <int D, int NW, int KP>
 cudaError_t rwalk_launch(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
 {
-    constexpr int smem = RWalkSmem<D, NW>::kTotal + (KP == 2 ? 2 * NW * 8 * 512 : 0);
+    constexpr int smem = RWalkSmem<D, NW>::kTotal + (int)sizeof(WalkSync) + (KP == 2 ? 2 * NW * 8 * 512 : 0);
+    DeltaMaps maps;
+    if (!make_maps<D, NW>(&maps, p, a, a.dy)) return cudaErrorUnknown;
     auto kern = delta_rwalk_tc<D, NW, KP>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)((long long)p.BH * p.N * (D / (16 * NW))), 32 * NW * KP, smem, s>>>(a);
+    kern<<<(unsigned)((long long)p.BH * p.N * (D / (16 * NW))), 32 * NW * KP, smem, s>>>(a, maps);
     return cudaGetLastError();
 }
 
@@ -1459,11 +1525,13 @@ cudaError_t prep_impl(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
 template <int D, int NW, int KP, bool READ, bool FULL>
 cudaError_t walk_launch(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
 {
-    constexpr int smem = WalkSmem<D, NW, READ>::kTotal + (KP == 2 ? 2 * NW * (READ ? 12 : 8) * 512 : 0);
+    constexpr int smem = WalkSmem<D, NW, READ>::kTotal + (int)sizeof(WalkSync) + (KP == 2 ? 2 * NW * (READ ? 12 : 8) * 512 : 0);
+    DeltaMaps maps;
+    if (!make_maps<D, NW>(&maps, p, a, a.v)) return cudaErrorUnknown;
     auto kern = delta_walk_tc<D, NW, KP, READ, FULL>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)((long long)p.BH * p.N * (D / (16 * NW))), 32 * NW * KP, smem, s>>>(a);
+    kern<<<(unsigned)((long long)p.BH * p.N * (D / (16 * NW))), 32 * NW * KP, smem, s>>>(a, maps);
     return cudaGetLastError();
 }
 
@@ -1485,6 +1553,19 @@ cudaError_t walk_impl(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
 }
 
 }  // namespace
+
+cudaError_t take_delta_abort(int *was_set)
+{
+    int v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_delta_abort, sizeof(int));
+    if (e != cudaSuccess) return e;
+    *was_set = v;
+    if (v) {
+        v = 0;
+        e = cudaMemcpyToSymbol(g_delta_abort, &v, sizeof(int));
+    }
+    return e;
+}
 
 cudaError_t launch_delta_dgon(const Problem &p, const void *dy, const void *O, float *dgon, cudaStream_t s)
 {

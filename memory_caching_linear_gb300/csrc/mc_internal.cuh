@@ -271,6 +271,7 @@ cudaError_t launch_bwd_cached_only_tc(const Problem &p, const void *q, const voi
 // The gate work of the tensor-core backward (delta, dr, du, the online gates and pooled-key weights kv_gw, dkbar).
 cudaError_t launch_bwd_route(const Problem &p, const BwdArgs &a, cudaStream_t s);
 cudaError_t take_bwd_abort(int *was_set);
+cudaError_t take_delta_abort(int *was_set);
 // The key-mean gradients on the tensor cores: dkbar [BH][N][d] += sum_t dr_{t,i} u_t from the
 // route kernel's hi / lo planes of dr.
 cudaError_t launch_bwd_dkbar_tc(const Problem &p, const void *u, const __nv_bfloat16 *dr_hi,

@@ -51,22 +51,29 @@ inline bool make_tmap_bf16_sw128(CUtensorMap *map, const void *base, unsigned lo
 }
 
 // A [heads][rows][cols] bf16 tensor (row-major, contiguous) moved in boxes of
-// box_rows x 64 elements of one head, 128-byte swizzled.  Coordinates are (column,
+// box_rows x box_cols elements of one head with the given swizzle.  Coordinates are (column,
 // row, head); rows at or past `rows` read as zeros (the TMA's out-of-bounds fill), so
 // a box that runs past a head's last row never touches the next head.
-inline bool make_tmap_bf16_3d_sw128(CUtensorMap *map, const void *base, unsigned long long heads,
-                                    unsigned long long rows, unsigned long long cols, unsigned box_rows)
+inline bool make_tmap_bf16_3d(CUtensorMap *map, const void *base, unsigned long long heads, unsigned long long rows,
+                              unsigned long long cols, unsigned box_cols, unsigned box_rows, CUtensorMapSwizzle swizzle)
 {
     auto enc = tensor_map_encoder();
     if (enc == nullptr) return false;
     cuuint64_t dims[3] = {cols, rows, heads};
     cuuint64_t strides[2] = {cols * 2, rows * cols * 2};
-    cuuint32_t box[3] = {64, box_rows, 1};
+    cuuint32_t box[3] = {box_cols, box_rows, 1};
     cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
+}
+
+// Boxes of box_rows x 64 elements, 128-byte swizzled.
+inline bool make_tmap_bf16_3d_sw128(CUtensorMap *map, const void *base, unsigned long long heads,
+                                    unsigned long long rows, unsigned long long cols, unsigned box_rows)
+{
+    return make_tmap_bf16_3d(map, base, heads, rows, cols, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace mc
