@@ -479,19 +479,20 @@ __device__ __forceinline__ void pair_sum(float4 *xb, int warp, int lane, F each,
 // the chunk's K, V columns, (Q,) and record, filled by TMA one chunk ahead: copied by the threads, 16 bytes at a
 // time, they took a fifth of the time (shared memory's pipe is what the products wait for, too).
 // ---------------------------------------------------------------------------
-template <int D, int NW, bool READ>
+template <int D, int NW, int KP, bool READ>
 struct WalkSmem {
     static constexpr int kK = kCH * D * 2, kV = kCH * NW * 32;
-    static constexpr int kR = kRecT + kRecV;
+    static constexpr bool kLate = READ && KP == 1;  // P is needed late in a chunk: one buffer, where two CTAs share an SM
+    static constexpr int kR = kRecT + kRecV + (READ && !kLate ? kRecT : 0);
     static constexpr int kStage = kK * (READ ? 2 : 1) + kV + kR;
-    static constexpr int kP = READ ? kRecT : 0;  // P of the present chunk, needed late in it: one buffer
+    static constexpr int kP = kLate ? kRecT : 0;
     static constexpr int kTotal = 2 * kStage + kP;
 };
 
 template <int D, int NW, int KP, bool READ, bool FULL>
 __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) delta_walk_tc(DeltaTcArgs a, const __grid_constant__ DeltaMaps maps)
 {
-    using W = WalkSmem<D, NW, READ>;
+    using W = WalkSmem<D, NW, KP, READ>;
     constexpr int NT = 32 * NW * KP, KS = D / 16 / KP;
     extern __shared__ __align__(1024) uint8_t sm[];
     WalkSync *sync = reinterpret_cast<WalkSync *>(sm + W::kTotal);
@@ -533,7 +534,7 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
             return;
         }
         if (tid == 0) {
-            if (READ) {
+            if (W::kLate) {
                 mbar_arrive_expect_tx(&sync->single, kRecT);
                 bulk_load(sm + 2 * W::kStage, a.rec + ((size_t)sid * a.NCH + ch) * kRec + kRecT + kRecV, kRecT, &sync->single);
             }
@@ -543,7 +544,7 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
         uint8_t *st = sm + (ch & 1) * W::kStage, *vown = st + W::kK;
         const uint32_t kt = smem_addr(st), vt = kt + W::kK, qt = vt + W::kV;
         const uint8_t *rec = st + W::kStage - W::kR;
-        const float *vec = reinterpret_cast<const float *>(rec + W::kR - kRecV);
+        const float *vec = reinterpret_cast<const float *>(rec + kRecT);
         const size_t row0 = (size_t)bh * a.L + t0 + ch * kCH;
         const int cnt = min(kCH, len - ch * kCH);
         const size_t cidx = (size_t)sid * a.NCH + ch;
@@ -665,9 +666,11 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
             split2(be.x * X[n][2], be.y * X[n][3], uh[n / 2][2 * (n & 1) + 1], ul[n / 2][2 * (n & 1) + 1]);
         }
         if (READ) {
-            if (ok) ok = mbar_wait(&sync->single, ch & 1, &sync->abort_flag);
-            __syncwarp();
-            const uint4 *pt = reinterpret_cast<const uint4 *>(sm + 2 * W::kStage) + lane;
+            if (W::kLate) {
+                if (ok) ok = mbar_wait(&sync->single, ch & 1, &sync->abort_flag);
+                __syncwarp();
+            }
+            const uint4 *pt = reinterpret_cast<const uint4 *>(W::kLate ? sm + 2 * W::kStage : rec + kRecT + kRecV) + lane;
 #pragma unroll
             for (int k4 = 0; k4 < 4; ++k4)
 #pragma unroll
@@ -756,23 +759,26 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
 //   R' = exp(c_end) R + sum_i exp(c_i) (p_i q_i^T - w_i k_i^T)
 // R is held in fp32 and read in one bf16 term; T, P, X and w take part in two, as in the walk forwards: for keys that
 // resemble each other X gathers what later tokens ask of every one of them, and w is the small difference that is left
-// (one term: dv 3e-2 off at all but parallel keys).  T and P are needed late in a chunk: one buffer for the present one's.
+// (one term: dv 3e-2 off at all but parallel keys).
 // ---------------------------------------------------------------------------
-template <int D, int NW>
+template <int D, int NW, int KP>
 struct RWalkSmem {
     static constexpr int kK = kCH * D * 2, kV = kCH * NW * 32;
-    static constexpr int kStage = 2 * kK + kV + kRecV;  // K, Q, dy columns, vectors
-    static constexpr int kTotal = 2 * kStage + 2 * kRecT + 2 * kCH * 4;  // T and P, two chunks' gates
+    static constexpr bool kLate = KP == 1;  // T and P are needed late in a chunk, as P above
+    static constexpr int kR = kRecV + (kLate ? 0 : 2 * kRecT);
+    static constexpr int kStage = 2 * kK + kV + kR;  // K, Q, dy columns, record
+    static constexpr int kGates = 2 * kStage + (kLate ? 2 * kRecT : 0);
+    static constexpr int kTotal = kGates + 2 * kCH * 4;  // two chunks' gates
 };
 
 template <int D, int NW, int KP>
 __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(DeltaTcArgs a, const __grid_constant__ DeltaMaps maps)
 {
-    using W = RWalkSmem<D, NW>;
+    using W = RWalkSmem<D, NW, KP>;
     constexpr int NT = 32 * NW * KP, KS = D / 16 / KP;
     extern __shared__ __align__(1024) uint8_t sm[];
     WalkSync *sync = reinterpret_cast<WalkSync *>(sm + W::kTotal);
-    float *gates = reinterpret_cast<float *>(sm + 2 * W::kStage + 2 * kRecT);
+    float *gates = reinterpret_cast<float *>(sm + W::kGates);
     constexpr int splits = D / (16 * NW);
     const int rs = (int)blockIdx.x % splits;
     const long long sid = blockIdx.x / splits;
@@ -792,7 +798,7 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
             tma_load_3d(st + W::kK + p * kPanel, &maps.q, 64 * p, t0 + ch * kCH, bh, bar);
         }
         tma_load_3d(st + 2 * W::kK, &maps.v, vbase, t0 + ch * kCH, bh, bar);
-        bulk_load(st + 2 * W::kK + W::kV, a.rrec + ((size_t)sid * a.NCH + ch) * kDeltaRRecBytes, kRecV, bar);
+        bulk_load(st + 2 * W::kK + W::kV, a.rrec + ((size_t)sid * a.NCH + ch) * kDeltaRRecBytes, W::kR, bar);
     };
     auto gate = [&](int ch) {
         return a.gon && ch * kCH + tid < len ? a.gon[((size_t)bh * a.L + t0 + ch * kCH + tid) * a.gw_stride] : 1.f;
@@ -831,8 +837,10 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
             return;
         }
         if (tid == 0) {
-            mbar_arrive_expect_tx(&sync->single, 2 * kRecT);
-            bulk_load(sm + 2 * W::kStage, a.rrec + ((size_t)sid * a.NCH + ch) * kDeltaRRecBytes + kRecV, 2 * kRecT, &sync->single);
+            if (W::kLate) {
+                mbar_arrive_expect_tx(&sync->single, 2 * kRecT);
+                bulk_load(sm + 2 * W::kStage, a.rrec + ((size_t)sid * a.NCH + ch) * kDeltaRRecBytes + kRecV, 2 * kRecT, &sync->single);
+            }
             if (ch > 0) load(ch - 1);
         }
         __syncwarp();
@@ -905,10 +913,12 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
             __nv_bfloat16 *dst = a.R_c + (((size_t)sid * a.NCH + ch) * D + vbase + 16 * wr) * D + 16 * k0;
             put_rows(R, 1.f, lane, [&](int r, int n, int at, const uint2 &x) { *reinterpret_cast<uint2 *>(dst + (size_t)r * D + 8 * n + at / 2) = x; });
         }
-        if (ok) ok = mbar_wait(&sync->single, turn & 1, &sync->abort_flag);  // T and P
-        __syncwarp();
-        const uint4 *lt = reinterpret_cast<const uint4 *>(sm + 2 * W::kStage) + lane;
-        const uint4 *pt = reinterpret_cast<const uint4 *>(sm + 2 * W::kStage + kRecT) + lane;
+        if (W::kLate) {
+            if (ok) ok = mbar_wait(&sync->single, turn & 1, &sync->abort_flag);
+            __syncwarp();
+        }
+        const uint4 *lt = reinterpret_cast<const uint4 *>(W::kLate ? sm + 2 * W::kStage : rec + kRecV) + lane;
+        const uint4 *pt = lt + kRecT / 16;
 #pragma unroll
         for (int k4 = 0; k4 < 4; ++k4)
 #pragma unroll
@@ -1458,7 +1468,7 @@ bool make_maps(DeltaMaps *m, const Problem &p, const DeltaTcArgs &a, const void 
 template <int D, int NW, int KP>
 cudaError_t rwalk_launch(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
 {
-    constexpr int smem = RWalkSmem<D, NW>::kTotal + (int)sizeof(WalkSync) + (KP == 2 ? 2 * NW * 8 * 512 : 0);
+    constexpr int smem = RWalkSmem<D, NW, KP>::kTotal + (int)sizeof(WalkSync) + (KP == 2 ? 2 * NW * 8 * 512 : 0);
     DeltaMaps maps;
     if (!make_maps<D, NW>(&maps, p, a, a.dy)) return cudaErrorUnknown;
     auto kern = delta_rwalk_tc<D, NW, KP>;
@@ -1525,7 +1535,7 @@ cudaError_t prep_impl(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
 template <int D, int NW, int KP, bool READ, bool FULL>
 cudaError_t walk_launch(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
 {
-    constexpr int smem = WalkSmem<D, NW, READ>::kTotal + (int)sizeof(WalkSync) + (KP == 2 ? 2 * NW * (READ ? 12 : 8) * 512 : 0);
+    constexpr int smem = WalkSmem<D, NW, KP, READ>::kTotal + (int)sizeof(WalkSync) + (KP == 2 ? 2 * NW * (READ ? 12 : 8) * 512 : 0);
     DeltaMaps maps;
     if (!make_maps<D, NW>(&maps, p, a, a.v)) return cudaErrorUnknown;
     auto kern = delta_walk_tc<D, NW, KP, READ, FULL>;
