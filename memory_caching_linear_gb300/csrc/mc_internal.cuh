@@ -311,7 +311,7 @@ cudaError_t launch_pool_simt(const Problem &p, const DeltaArgs &a, float *sums, 
 // rho from the pooled-key weights pw (token t at [t * gw_stride]), u and the key means' gradient.
 cudaError_t launch_pool_grad_simt(const Problem &p, const DeltaArgs &a, const float *pw, float *rho, const float *dkbar, cudaStream_t s);
 // The same on the tensor cores (k_delta_tc.cu): bf16, d = 64 or 128, any segment length.
-constexpr int kDeltaRecBytes = 21504;  // a chunk's record between its two kernels
+constexpr int kDeltaRecBytes = 21504, kDeltaRRecBytes = 21504;  // a chunk's records for the walk and for the reverse walk
 struct DeltaTcArgs {
     const __nv_bfloat16 *q, *k, *v, *la, *be;
     uint8_t *rec;          // [BH][N][NCH] x kDeltaRecBytes scratch
@@ -336,13 +336,13 @@ struct DeltaTcArgs {
     __nv_bfloat16 *dq, *dk, *dv, *dla, *dbe;
     int BH, L, C, N, NCH;
 };
+// dy_t . O_t of every token.
 cudaError_t launch_delta_dgon(const Problem &p, const void *dy, const void *O, float *dgon, cudaStream_t s);
-constexpr int kDeltaRRecBytes = 21504;
 // After the walk with rrec, E and S_c: dv and R_c, then the other gradients.
 cudaError_t launch_delta_grads_tc(const Problem &p, const DeltaTcArgs &a, cudaStream_t s);
 bool delta_tc_supported(const Problem &p);
-// read: q is read and y or O_on written.
 cudaError_t launch_delta_scalars(const Problem &p, const void *la, float *alpha, float *zero, float *one, cudaStream_t s);
+// read: q is read and y or O_on written.
 cudaError_t launch_delta_walk_tc(const Problem &p, const DeltaTcArgs &a, bool read, cudaStream_t s);
 
 // The gates, the cached reads' gradients and G of the FFMA backward alone (k_bwd_simt.cu): tok, dq_f32, du, dkbar, G.
