@@ -880,17 +880,7 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
 #pragma unroll
         for (int k4 = 0; k4 < 4; ++k4)
             ldsm4t(v4[k4], vt + own_off<NW>(16 * k4 + (lane >> 4) * 8 + (lane & 7), (lane >> 3) & 1, wr));
-        if (KP == 2)
-            pair_sum<8>(reinterpret_cast<float4 *>(sm + W::kTotal + sizeof(WalkSync)), warp, lane,
-                     [&](auto leave) {
-#pragma unroll
-                         for (int n = 0; n < 8; ++n) leave(n, X[n]);
-                     },
-                     [&](auto add) {
-#pragma unroll
-                         for (int n = 0; n < 8; ++n) add(n, X[n]);
-                     });
-        else __syncwarp();  // the warp's part of dy is free
+        if (KP == 1) __syncwarp();  // the warp's part of dy is free
         uint32_t pf[4][4], pg[4][4];  // p, and exp(c) p
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
@@ -920,13 +910,25 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
         const uint4 *lt = reinterpret_cast<const uint4 *>(W::kLate ? sm + 2 * W::kStage : rec + kRecV) + lane;
         const uint4 *pt = lt + kRecT / 16;
 #pragma unroll
-        for (int k4 = 0; k4 < 4; ++k4)
+        for (int k4 = 0; k4 < 4; ++k4) {
+            if (KP == 2 && (k4 == 1 || k4 == 2) != (kp == 1)) continue;  // ten of the twenty tiles to each of two warps
 #pragma unroll
             for (int n = 0; n < 2 * k4 + 2; ++n) {
                 const uint4 b = pt[(rev_base(n) + k4 - n / 2) * 32];
                 mma16816(X[n], pf[k4], b.z, b.w);
                 mma16816(X[n], pf[k4], b.x, b.y);
             }
+        }
+        if (KP == 2)
+            pair_sum<8>(reinterpret_cast<float4 *>(sm + W::kTotal + sizeof(WalkSync)), warp, lane,
+                     [&](auto leave) {
+#pragma unroll
+                         for (int n = 0; n < 8; ++n) leave(n, X[n]);
+                     },
+                     [&](auto add) {
+#pragma unroll
+                         for (int n = 0; n < 8; ++n) add(n, X[n]);
+                     });
         uint32_t wf[4][4], wl[4][4];
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
