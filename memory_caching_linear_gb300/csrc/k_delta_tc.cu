@@ -69,6 +69,37 @@ __device__ __forceinline__ Where chunk_at(const DeltaTcArgs &a, long long id)
     return w;
 }
 
+// Tiles of tokens come by TMA: 64 x 64 panels of q and k, and a walk's columns of v (or dy).
+struct DeltaMaps {
+    CUtensorMap k, q, v;
+};
+constexpr int kPanel = kCH * 128;
+__device__ __forceinline__ uint32_t panel_off(int r, int c) { return (uint32_t)((c >> 3) * kPanel) + tile_off<128>(r, c & 7); }
+
+// What follows the tiles in shared memory: a barrier per stage, one for the single buffer, and whether a wait gave up.
+struct WalkSync {
+    uint64_t full[2], single;
+    int abort_flag, pad;
+};
+__device__ __forceinline__ bool walk_sync_init(WalkSync *y, const void *sm, int tid)
+{
+    if (tid == 0) {
+        y->abort_flag = (smem_addr(sm) & 1023) != 0;  // (the panels' swizzle counts from 1024-byte boundaries)
+        mbar_init(&y->full[0], 1);
+        mbar_init(&y->full[1], 1);
+        mbar_init(&y->single, 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    return y->abort_flag == 0;
+}
+// Rows from cnt on of a tile of ROW bytes a row: a chunk's last tokens may be another segment's.
+template <int ROW, int NT>
+__device__ __forceinline__ void clear_rows(uint8_t *tile, int cnt, int tid)
+{
+    for (int e = cnt * (ROW / 16) + tid; e < kCH * (ROW / 16); e += NT) reinterpret_cast<uint4 *>(tile)[e] = make_uint4(0, 0, 0, 0);
+}
+
 // ---------------------------------------------------------------------------
 // delta_prep_tc: one warp per chunk, no barrier between warps.  K K^T (and Q K^T) in registers, exact bf16
 // products; then X = (1 + A)^-1 by 16 x 16 blocks: the four diagonal blocks by substitution in fp32, all at once (a lane
@@ -122,29 +153,33 @@ __device__ __forceinline__ void block_mma(float (&acc)[2][4], const Terms &a, co
 template <int D, bool QK>
 __host__ __device__ constexpr int prep_smem()
 {
-    return ((QK ? 2 : 1) * kCH * D * 2 > 8 * kXB * 4 ? (QK ? 2 : 1) * kCH * D * 2 : 8 * kXB * 4) + 2 * kCH * 4;
+    return ((QK ? 2 : 1) * kCH * D * 2 > 8 * kXB * 4 ? (QK ? 2 : 1) * kCH * D * 2 : 8 * kXB * 4) + 2 * kCH * 4 + (int)sizeof(WalkSync);
 }
 
 template <int D, bool READ, bool REV>
-__global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a)
+__global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a, const __grid_constant__ DeltaMaps maps)
 {
-    constexpr int ROW = D * 2, PIECES = D / 8, KS = D / 16;
+    constexpr int KS = D / 16;
     constexpr bool QK = READ || REV;
-    extern __shared__ __align__(16) uint8_t sm[];
+    extern __shared__ __align__(1024) uint8_t sm[];
     float *Ad = reinterpret_cast<float *>(sm), *Xd = Ad + 4 * kXB;  // over the tiles once these are read
-    float *cum = reinterpret_cast<float *>(sm + prep_smem<D, QK>() - 2 * kCH * 4), *bet = cum + kCH;
+    WalkSync *sync = reinterpret_cast<WalkSync *>(sm + prep_smem<D, QK>() - sizeof(WalkSync));
+    float *bet = reinterpret_cast<float *>(sync) - kCH, *cum = bet - kCH;
     const Where w = chunk_at(a, blockIdx.x);
     if (w.cnt <= 0) return;
     const int lane = threadIdx.x, g = lane / 4, c = lane % 4;
     const size_t row0 = (size_t)w.bh * a.L + w.tb;
-    const uint32_t Kt = smem_addr(sm), Qt = Kt + kCH * ROW;
-    for (int e = lane; e < kCH * PIECES; e += 32) {
-        const int r = e / PIECES, pc = e % PIECES;
-        const size_t off = (row0 + (r < w.cnt ? r : 0)) * D + pc * 8;
-        cp16(Kt + tile_off<ROW>(r, pc), a.k + off, r < w.cnt);
-        if (QK) cp16(Qt + tile_off<ROW>(r, pc), a.q + off, r < w.cnt);
+    const uint32_t Kt = smem_addr(sm), Qt = Kt + kCH * D * 2;
+    bool ok = walk_sync_init(sync, sm, lane);
+    if (ok && lane == 0) {
+        mbar_arrive_expect_tx(&sync->single, (QK ? 2 : 1) * kCH * D * 2);
+#pragma unroll
+        for (int p = 0; p < D / 64; ++p) {
+            tma_load_3d(sm + p * kPanel, &maps.k, 64 * p, w.tb, w.bh, &sync->single);
+            if (QK) tma_load_3d(sm + kCH * D * 2 + p * kPanel, &maps.q, 64 * p, w.tb, w.bh, &sync->single);
+        }
     }
-    cp_commit();
+    __syncwarp();
     {  // running sums of the chunk's decays, two tokens per lane
         const int i = 2 * lane;
         const float x0 = i < w.cnt ? delta_log(__bfloat162float(a.la[row0 + i])) : 0.f;
@@ -160,7 +195,14 @@ __global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a)
         bet[i] = i < w.cnt ? __bfloat162float(a.be[row0 + i]) : 0.f;
         bet[i + 1] = i + 1 < w.cnt ? __bfloat162float(a.be[row0 + i + 1]) : 0.f;
     }
-    cp_wait<0>();
+    if (ok) ok = mbar_wait(&sync->single, 0, &sync->abort_flag);
+    if (__any_sync(0xffffffffu, !ok)) {
+        if (lane == 0) atomicExch(&g_delta_abort, 1);
+        return;
+    }
+    if (w.cnt < kCH)
+#pragma unroll
+        for (int p = 0; p < (QK ? 2 : 1) * (D / 64); ++p) clear_rows<128, 32>(sm + p * kPanel, w.cnt, lane);
     __syncwarp();
     uint8_t *rec = a.rec + (size_t)blockIdx.x * kRec, *rrec = REV ? a.rrec + (size_t)blockIdx.x * kDeltaRRecBytes : nullptr;
     const float ce = cum[kCH - 1];  // tokens past the end add nothing
@@ -199,12 +241,12 @@ __global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a)
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             uint32_t ak[4], aq[4];
-            ldsm4(ak, Kt + tile_off<ROW>(16 * b + ar, 2 * ks + ac));
-            if (QK) ldsm4(aq, Qt + tile_off<ROW>(16 * b + ar, 2 * ks + ac));
+            ldsm4(ak, Kt + panel_off(16 * b + ar, 2 * ks + ac));
+            if (QK) ldsm4(aq, Qt + panel_off(16 * b + ar, 2 * ks + ac));
 #pragma unroll
             for (int n2 = 0; n2 <= b; ++n2) {
                 uint32_t bf[4];
-                ldsm4(bf, Kt + tile_off<ROW>(16 * n2 + br, 2 * ks + bc));
+                ldsm4(bf, Kt + panel_off(16 * n2 + br, 2 * ks + bc));
                 mma16816(kk[b * (b + 1) / 2 + n2][0], ak, bf[0], bf[1]);
                 mma16816(kk[b * (b + 1) / 2 + n2][1], ak, bf[2], bf[3]);
                 if (QK) {
@@ -213,35 +255,39 @@ __global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a)
                 }
             }
         }
-        if (QK) {
-            const float c0 = cum[16 * b + g], c1 = cum[16 * b + g + 8];
+        const float c0 = cum[16 * b + g], c1 = cum[16 * b + g + 8];
 #pragma unroll
-            for (int n2 = 0; n2 <= b; ++n2) {
-                uint32_t p[2][2], pl[2][2];  // [columns half][rows half] 8 x 8 tiles, two terms
+        for (int n2 = 0; n2 <= b; ++n2) {
+            uint32_t p[2][2], pl[2][2];  // [columns half][rows half] 8 x 8 tiles of P, two terms
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int j = 16 * n2 + 8 * h + 2 * c;
-                    float v[4];
+            for (int h = 0; h < 2; ++h) {
+                const float2 cj = *reinterpret_cast<const float2 *>(cum + 16 * n2 + 8 * h + 2 * c);
+                const float2 bj = *reinterpret_cast<const float2 *>(bet + 16 * n2 + 8 * h + 2 * c);
+                float v[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int i = 16 * b + g + 8 * (e >> 1), jj = j + (e & 1);
-                        v[e] = jj <= i ? qk[n2][h][e] * __expf((e >> 1 ? c1 : c0) - cum[jj]) : 0.f;
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const int il = g + 8 * (e >> 1), jl = 8 * h + 2 * c + (e & 1);
+                    const float dec = __expf((e >> 1 ? c1 : c0) - (e & 1 ? cj.y : cj.x));
+                    float &x = kk[b * (b + 1) / 2 + n2][h][e];
+                    x = n2 < b || jl < il ? x * (dec * (e & 1 ? bj.y : bj.x)) : 0.f;  // A
+                    v[e] = n2 < b || jl <= il ? qk[n2][h][e] * dec : 0.f;
+                }
+                if (QK) {
                     split2(v[0], v[1], p[h][0], pl[h][0]);
                     split2(v[2], v[3], p[h][1], pl[h][1]);
                 }
-                if (READ) {
-                    uint4 *pt = reinterpret_cast<uint4 *>(rec + kRecT + kRecV) + lane;
-                    pt[(tile_base(2 * b) + n2) * 32] = make_uint4(p[0][0], p[1][0], pl[0][0], pl[1][0]);
-                    pt[(tile_base(2 * b + 1) + n2) * 32] = make_uint4(p[0][1], p[1][1], pl[0][1], pl[1][1]);
-                }
-                if (REV) {
-                    uint4 *pt = reinterpret_cast<uint4 *>(rrec + kRecV + kRecT) + lane;
+            }
+            if (READ) {
+                uint4 *pt = reinterpret_cast<uint4 *>(rec + kRecT + kRecV) + lane;
+                pt[(tile_base(2 * b) + n2) * 32] = make_uint4(p[0][0], p[1][0], pl[0][0], pl[1][0]);
+                pt[(tile_base(2 * b + 1) + n2) * 32] = make_uint4(p[0][1], p[1][1], pl[0][1], pl[1][1]);
+            }
+            if (REV) {
+                uint4 *pt = reinterpret_cast<uint4 *>(rrec + kRecV + kRecT) + lane;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        pt[(rev_base(2 * n2 + h) + b - n2) * 32] =
-                            make_uint4(movm_t(p[h][0]), movm_t(p[h][1]), movm_t(pl[h][0]), movm_t(pl[h][1]));
-                }
+                for (int h = 0; h < 2; ++h)
+                    pt[(rev_base(2 * n2 + h) + b - n2) * 32] =
+                        make_uint4(movm_t(p[h][0]), movm_t(p[h][1]), movm_t(pl[h][0]), movm_t(pl[h][1]));
             }
         }
     }
@@ -249,16 +295,10 @@ __global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a)
 #pragma unroll
     for (int b = 0; b < 4; ++b)
 #pragma unroll
-        for (int n2 = 0; n2 <= b; ++n2)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int il = g + 8 * (e >> 1), jl = 8 * h + 2 * c + (e & 1), i = 16 * b + il, j = 16 * n2 + jl;
-                    float &x = kk[b * (b + 1) / 2 + n2][h][e];
-                    x *= j < i ? __expf(cum[i] - cum[j]) * bet[j] : 0.f;
-                    if (b == n2) Ad[b * kXB + jl * kXP + il] = x;  // column j of A as a row
-                }
+            for (int e = 0; e < 4; ++e)  // the diagonal blocks of A: column j as a row
+                Ad[b * kXB + (8 * h + 2 * c + (e & 1)) * kXP + g + 8 * (e >> 1)] = kk[b * (b + 3) / 2][h][e];
     __syncwarp();
     {
         const int hw = lane / 16, col = lane % 16;
@@ -381,37 +421,6 @@ __global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a)
         negate(x);
         out(3, j, left_of(x));
     }
-}
-
-// The walks' tiles of tokens come by TMA: 64 x 64 panels of q and k, and the CTA's columns of v (or dy).
-struct DeltaMaps {
-    CUtensorMap k, q, v;
-};
-constexpr int kPanel = kCH * 128;
-__device__ __forceinline__ uint32_t panel_off(int r, int c) { return (uint32_t)((c >> 3) * kPanel) + tile_off<128>(r, c & 7); }
-
-// What follows the tiles in shared memory: a barrier per stage, one for the single buffer, and whether a wait gave up.
-struct WalkSync {
-    uint64_t full[2], single;
-    int abort_flag, pad;
-};
-__device__ __forceinline__ bool walk_sync_init(WalkSync *y, const void *sm, int tid)
-{
-    if (tid == 0) {
-        y->abort_flag = (smem_addr(sm) & 1023) != 0;  // (the panels' swizzle counts from 1024-byte boundaries)
-        mbar_init(&y->full[0], 1);
-        mbar_init(&y->full[1], 1);
-        mbar_init(&y->single, 1);
-        fence_mbar_init();
-    }
-    __syncthreads();
-    return y->abort_flag == 0;
-}
-// Rows from cnt on of a tile of ROW bytes a row: a chunk's last tokens may be another segment's.
-template <int ROW, int NT>
-__device__ __forceinline__ void clear_rows(uint8_t *tile, int cnt, int tid)
-{
-    for (int e = cnt * (ROW / 16) + tid; e < kCH * (ROW / 16); e += NT) reinterpret_cast<uint4 *>(tile)[e] = make_uint4(0, 0, 0, 0);
 }
 
 // A warp's own 32 bytes of every row of the V (or dy) tile: once read, its staging area for what it writes.
@@ -1453,12 +1462,6 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
     }
 }
 
-// Few walkers leave most of the card idle, and a chunk's products on a walker's way to the next chunk are what counts: then
-// two warps share 16 rows, half of the keys each.  KP = 2 with two row groups per CTA as long as every CTA has an SM to
-// itself, else four row groups and whole rows.  L = 2048, d = 128, one memory (forward, recomputed, reverse walk), KP = 2
-// against 1: 32 heads (128 CTAs) 89 68 82 against 111 93 102 us; 48 heads (192 CTAs) 171 101 129 against 111 93 102 us.
-inline bool split_keys(const Problem &p) { return (long long)p.BH * p.N * (p.d / 32) <= 152; }
-
 template <int D, int NW>
 bool make_maps(DeltaMaps *m, const Problem &p, const DeltaTcArgs &a, const void *v)
 {
@@ -1466,6 +1469,12 @@ bool make_maps(DeltaMaps *m, const Problem &p, const DeltaTcArgs &a, const void 
     return make_tmap_bf16_3d_sw128(&m->k, a.k, p.BH, p.L, D, kCH) && make_tmap_bf16_3d_sw128(&m->q, a.q, p.BH, p.L, D, kCH) &&
            make_tmap_bf16_3d(&m->v, v, p.BH, p.L, D, 16 * NW, kCH, sw);
 }
+
+// Few walkers leave most of the card idle, and a chunk's products on a walker's way to the next chunk are what counts: then
+// two warps share 16 rows, half of the keys each.  KP = 2 with two row groups per CTA as long as every CTA has an SM to
+// itself, else four row groups and whole rows.  L = 2048, d = 128, one memory (forward, recomputed, reverse walk), KP = 2
+// against 1: 32 heads (128 CTAs) 89 68 82 against 111 93 102 us; 48 heads (192 CTAs) 171 101 129 against 111 93 102 us.
+inline bool split_keys(const Problem &p) { return (long long)p.BH * p.N * (p.d / 32) <= 152; }
 
 template <int D, int NW, int KP>
 cudaError_t rwalk_launch(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
@@ -1527,10 +1536,12 @@ template <int D, bool READ, bool REV>
 cudaError_t prep_impl(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
 {
     constexpr int smem = prep_smem<D, READ || REV>();
+    DeltaMaps maps;
+    if (!make_maps<D, 4>(&maps, p, a, a.v)) return cudaErrorUnknown;
     auto kern = delta_prep_tc<D, READ, REV>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)((long long)p.BH * p.N * a.NCH), 32, smem, s>>>(a);
+    kern<<<(unsigned)((long long)p.BH * p.N * a.NCH), 32, smem, s>>>(a, maps);
     return cudaGetLastError();
 }
 
