@@ -1004,22 +1004,31 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
 // ---------------------------------------------------------------------------
 constexpr int kGradThreads = 256;
 
+struct GradMaps {
+    CUtensorMap dy, e, w, q, k, u, S, R;  // tokens; the memories and adjoints by chunk
+};
+struct GradSync {
+    uint64_t tiles, S0, S1, R, u;
+    int abort_flag, pad;
+};
+
 template <int D>
 struct GradSmem {
     static constexpr int kT = kCH * D * 2;   // a 64-token tile
     static constexpr int kM = 64 * D * 2;    // 64 rows of S or R
     static constexpr int kVec = 4 * (22 * kCH + 16);
     static constexpr int kB = 2 * 10 * 512;  // B1 and B2: ten 16 x 16 blocks each
-    static constexpr int kTotal = 5 * kT + kM + kB + kVec;
+    static constexpr int kSync = 5 * kT + kM + kB + kVec;
+    static constexpr int kTotal = kSync + (int)sizeof(GradSync);
 };
 
 template <int D>
-__global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
+__global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a, const __grid_constant__ GradMaps maps)
 {
     using G = GradSmem<D>;
-    constexpr int ROW = D * 2, PIECES = D / 8, KS = D / 16, HD = D / 2, HN = HD / 8;  // HN column tiles per warp
+    constexpr int PIECES = D / 8, KS = D / 16, HD = D / 2, HN = HD / 8;  // HN column tiles per warp
     constexpr int MB = D / 64;                                                         // blocks of S and R
-    extern __shared__ __align__(16) uint8_t sm[];
+    extern __shared__ __align__(1024) uint8_t sm[];
     uint8_t *Qt = sm, *Kt = Qt + G::kT, *Pt = Kt + G::kT, *Et = Pt + G::kT, *Wt = Et + G::kT, *Mt = Wt + G::kT;
     uint8_t *Bt = Mt + G::kM;
     float *cum = reinterpret_cast<float *>(Bt + G::kB), *bet = cum + kCH, *gs = bet + kCH, *pw = gs + kCH;
@@ -1031,12 +1040,32 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, c = lane % 4;
     const int wm = warp & 3, m0 = 16 * wm, half = warp >> 2, d0 = half * HD;
     const size_t row0 = (size_t)w.bh * a.L + w.tb;
-    const __nv_bfloat16 *S = a.S_c + (size_t)blockIdx.x * D * D, *R = a.R_c + (size_t)blockIdx.x * D * D;
+    const __nv_bfloat16 *S = a.S_c + (size_t)blockIdx.x * D * D;
+    GradSync *sync = reinterpret_cast<GradSync *>(sm + G::kSync);
 
-    auto load_rows = [&](uint8_t *dst, const __nv_bfloat16 *src, int b) {  // rows 64 b .. of S or R
-        for (int e = tid; e < 64 * PIECES; e += kGradThreads)
-            cp16(smem_addr(dst) + tile_off<ROW>(e / PIECES, e % PIECES), src + (size_t)(64 * b * PIECES + e) * 8, true);
+    // one thread's
+    auto load_tokens = [&](uint8_t *dst, const CUtensorMap &map, uint64_t *bar) {
+#pragma unroll
+        for (int p = 0; p < D / 64; ++p) tma_load_3d(dst + p * kPanel, &map, 64 * p, w.tb, w.bh, bar);
     };
+    auto load_rows = [&](uint8_t *dst, const CUtensorMap &map, int b, uint64_t *bar) {  // rows 64 b .. of S or R
+#pragma unroll
+        for (int p = 0; p < D / 64; ++p) tma_load_3d(dst + p * kPanel, &map, 64 * p, 64 * b, (int)blockIdx.x, bar);
+    };
+    // the chunk's last tokens may be another segment's
+    auto clear_tokens = [&](uint8_t *tile) {
+#pragma unroll
+        for (int p = 0; p < D / 64; ++p) clear_rows<128, kGradThreads>(tile + p * kPanel, w.cnt, tid);
+    };
+    if (tid == 0) {
+        sync->abort_flag = (smem_addr(sm) & 1023) != 0;
+        mbar_init(&sync->tiles, 1);
+        mbar_init(&sync->S0, 1);
+        mbar_init(&sync->S1, 1);
+        mbar_init(&sync->R, 1);
+        mbar_init(&sync->u, 1);
+        fence_mbar_init();
+    }
     // the gates' loads first, or they would queue behind the tiles
     const int gt = warp == 0 ? 2 * lane : tid - kCH;
     const bool in_chunk = gt >= 0 && gt < w.cnt;
@@ -1049,20 +1078,22 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
         if (a.gon) g1 = a.gon[(row0 + gt) * a.gw_stride];
         if (a.pw) g2 = a.pw[(row0 + gt) * a.gw_stride];
     }
-    auto load_tokens = [&](uint8_t *dst, const __nv_bfloat16 *src) {
-        for (int e = tid; e < kCH * PIECES; e += kGradThreads) {
-            const int r = e / PIECES, pc = e % PIECES;
-            cp16(smem_addr(dst) + tile_off<ROW>(r, pc), src + (row0 + (r < w.cnt ? r : 0)) * D + pc * 8, r < w.cnt);
-        }
+    __syncthreads();
+    bool ok = sync->abort_flag == 0;
+    auto wait = [&](uint64_t *bar) {
+        if (ok) ok = mbar_wait(bar, 0, &sync->abort_flag);
     };
-    load_tokens(Pt, a.dy);
-    load_tokens(Et, a.E);
-    load_tokens(Wt, a.dv);
-    load_tokens(Qt, a.q);
-    load_tokens(Kt, a.k);
-    cp_commit();
-    load_rows(Mt, S, 0);
-    cp_commit();
+    if (ok && tid == 0) {
+        mbar_arrive_expect_tx(&sync->tiles, 5 * G::kT);
+        load_tokens(Pt, maps.dy, &sync->tiles);
+        load_tokens(Et, maps.e, &sync->tiles);
+        load_tokens(Wt, maps.w, &sync->tiles);
+        load_tokens(Qt, maps.q, &sync->tiles);
+        load_tokens(Kt, maps.k, &sync->tiles);
+        mbar_arrive_expect_tx(&sync->S0, G::kM);
+        load_rows(Mt, maps.S, 0, &sync->S0);
+    }
+    __syncwarp();
     if (warp == 0) {
         float s = g0 + g1;
 #pragma unroll
@@ -1077,12 +1108,19 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
         gs[gt] = g1;
         pw[gt] = g2;
     }
-    cp_wait<1>();
-    __syncthreads();
+    wait(&sync->tiles);
+    if (__syncthreads_or(!ok)) {
+        if (tid == 0) atomicExch(&g_delta_abort, 1);
+        return;
+    }
+    if (w.cnt < kCH) {
+        for (uint8_t *t : {Qt, Kt, Pt, Et, Wt}) clear_tokens(t);
+        __syncthreads();
+    }
     if (a.gon) {  // p = g dy, in place
         for (int e = tid; e < kCH * PIECES; e += kGradThreads) {
             const int r = e / PIECES;
-            uint4 *x = reinterpret_cast<uint4 *>(Pt + tile_off<ROW>(r, e % PIECES));
+            uint4 *x = reinterpret_cast<uint4 *>(Pt + panel_off(r, e % PIECES));
             uint4 y = *x;
             uint32_t *yw = reinterpret_cast<uint32_t *>(&y);
 #pragma unroll
@@ -1113,11 +1151,11 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
             uint32_t af[4];
-            ldsm4(af, smem_addr(tile) + tile_off<ROW>(ar, 2 * (4 * b + ks) + ac));
+            ldsm4(af, smem_addr(tile) + panel_off(ar, 2 * (4 * b + ks) + ac));
 #pragma unroll
             for (int n2 = 0; n2 < HN / 2; ++n2) {
                 uint32_t bf[4];
-                ldsm4t(bf, smem_addr(rows) + tile_off<ROW>(16 * ks + tr, d0 / 8 + 2 * n2 + tc));
+                ldsm4t(bf, smem_addr(rows) + panel_off(16 * ks + tr, d0 / 8 + 2 * n2 + tc));
                 mma16816(x[2 * n2], af, bf[0], bf[1]);
                 mma16816(x[2 * n2 + 1], af, bf[2], bf[3]);
             }
@@ -1128,7 +1166,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
 #pragma unroll
         for (int n2 = 0; n2 < HN / 2; ++n2) {
             uint32_t bf[4];
-            ldsm4t(bf, smem_addr(tile) + tile_off<ROW>(16 * k4 + tr, d0 / 8 + 2 * n2 + tc));
+            ldsm4t(bf, smem_addr(tile) + panel_off(16 * k4 + tr, d0 / 8 + 2 * n2 + tc));
             mma16816(x[2 * n2], f, bf[0], bf[1]);
             mma16816(x[2 * n2 + 1], f, bf[2], bf[3]);
         }
@@ -1137,8 +1175,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int n = 0; n < HN; ++n) {
-            const uint32_t a0 = *reinterpret_cast<const uint32_t *>(tile + tile_off<ROW>(m0 + g, d0 / 8 + n) + 4 * c);
-            const uint32_t a1 = *reinterpret_cast<const uint32_t *>(tile + tile_off<ROW>(m0 + g + 8, d0 / 8 + n) + 4 * c);
+            const uint32_t a0 = *reinterpret_cast<const uint32_t *>(tile + panel_off(m0 + g, d0 / 8 + n) + 4 * c);
+            const uint32_t a1 = *reinterpret_cast<const uint32_t *>(tile + panel_off(m0 + g + 8, d0 / 8 + n) + 4 * c);
             s0 = fmaf(x[n][0], low_f(a0), fmaf(x[n][1], high_f(a0), s0));
             s1 = fmaf(x[n][2], low_f(a1), fmaf(x[n][3], high_f(a1), s1));
         }
@@ -1167,8 +1205,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             uint32_t af[4], bf[4];
-            ldsm4(af, smem_addr(rows) + tile_off<ROW>(16 * r + (lane & 15), 2 * ks + ac));
-            ldsm4(bf, smem_addr(cols) + tile_off<ROW>(16 * q + br, 2 * ks + bc));
+            ldsm4(af, smem_addr(rows) + panel_off(16 * r + (lane & 15), 2 * ks + ac));
+            ldsm4(bf, smem_addr(cols) + panel_off(16 * q + br, 2 * ks + bc));
             mma16816(x[0], af, bf[0], bf[1]);
             mma16816(x[1], af, bf[2], bf[3]);
         }
@@ -1274,17 +1312,22 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
                 pairs(b[x], half ? Wt : Pt, r, Et, q);
                 put_block(b[x], r, q);
             }
-        __syncthreads();  // the blocks are there, e has been read
-        if (MB > 1) load_rows(Et, S, 1);
-        cp_commit();
+        fence_async_smem();  // (what was cleared or scaled in the tiles, before the copies over them)
+        __syncthreads();     // the blocks are there, e has been read
+        if (MB > 1 && tid == 0) {
+            mbar_arrive_expect_tx(&sync->S1, G::kM);
+            load_rows(Et, maps.S, 1, &sync->S1);
+        }
+        __syncwarp();
 #pragma unroll
         for (int x = 0; x < 3; ++x) {
             const int blk = block_at(x, r, q);
             if (blk < 10) pair_sums(b[x], half ? Kt : Qt, half ? -1.f : 1.f, blk, r, q);
         }
     }
-    cp_wait<0>();
-    __syncthreads();
+    wait(&sync->S0);
+    if (MB > 1) wait(&sync->S1);
+    __syncwarp();
     float z[HN][4];
     zero(z);
     {
@@ -1296,13 +1339,19 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
             times_rows(dq, Pt, Et, 1);
             times_rows(z, Wt, Et, 1);
         }
-        __syncthreads();  // p and w have been read: their tiles take R
-        load_rows(Wt, R, 0);
-        if (MB > 1) {
-            load_rows(Pt, R, 1);
-            load_tokens(Mt, a.E);
+        if (__syncthreads_or(!ok)) {  // p and w have been read: their tiles take R
+            if (tid == 0) atomicExch(&g_delta_abort, 1);
+            return;
         }
-        cp_commit();
+        if (tid == 0) {
+            mbar_arrive_expect_tx(&sync->R, MB * G::kM + (MB > 1 ? G::kT : 0));
+            load_rows(Wt, maps.R, 0, &sync->R);
+            if (MB > 1) {
+                load_rows(Pt, maps.R, 1, &sync->R);
+                load_tokens(Mt, maps.e, &sync->R);
+            }
+        }
+        __syncwarp();
         const float e0 = __expf(c_lo), e1 = __expf(c_hi);
         scale(dq, e0, e1);
         scale(z, e0, e1);
@@ -1346,14 +1395,18 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
     if (MB > 1)
 #pragma unroll
         for (int x = 0; x < X4; ++x) s4[x] = *reinterpret_cast<const uint4 *>(S + (size_t)(tid + x * kGradThreads) * 8);
-    cp_wait<0>();
-    __syncthreads();
+    wait(&sync->R);
+    __syncwarp();
+    if (MB > 1 && w.cnt < kCH) {
+        clear_tokens(E2);
+        __syncthreads();
+    }
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
         for (int x = 0; x < X4; ++x) {
             const int e = tid + x * kGradThreads;
-            const uint32_t o = tile_off<ROW>(e / PIECES, e % PIECES);
+            const uint32_t o = panel_off(e / PIECES, e % PIECES);
             const uint4 r4 = *reinterpret_cast<const uint4 *>((mb ? Pt : Wt) + o);
             const uint4 m4 = mb + 1 < MB ? s4[x] : *reinterpret_cast<const uint4 *>(Sl + o);
             const uint32_t *rw = reinterpret_cast<const uint32_t *>(&r4), *sw = reinterpret_cast<const uint32_t *>(&m4);
@@ -1362,8 +1415,11 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
         }
     if (a.pw) {  // u for the pooled keys' share, into their place
         __syncthreads();
-        load_tokens(Sl, a.u);
-        cp_commit();
+        if (ok && tid == 0) {
+            mbar_arrive_expect_tx(&sync->u, G::kT);
+            load_tokens(Sl, maps.u, &sync->u);
+        }
+        __syncwarp();
     }
     times_rows(y, E2, Wt, 0);
     if (MB > 1) times_rows(y, E2, Pt, 1);
@@ -1395,8 +1451,15 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a)
             y[n][3] = fmaf(be1, y[n][3], -z[n][3]);
         }
     }
-    cp_wait<0>();
-    __syncthreads();  // u and the sums are there
+    if (a.pw) wait(&sync->u);
+    if (__syncthreads_or(!ok)) {  // the sums are there
+        if (tid == 0) atomicExch(&g_delta_abort, 1);
+        return;
+    }
+    if (a.pw && w.cnt < kCH) {
+        clear_tokens(Sl);
+        __syncthreads();
+    }
     if (a.pw) {  // the pooled keys' share: rho after the chunk + sum over the chunk's tokens t >= j of pw_t u_t
 #pragma unroll
         for (int k4 = 0; k4 < 4; ++k4) {
@@ -1496,9 +1559,16 @@ cudaError_t grads_tc_impl(const Problem &p, const DeltaTcArgs &a, cudaStream_t s
     if (e != cudaSuccess) return e;
     profile_after_kernel(s, "delta_rwalk_tc");
     constexpr int smem = GradSmem<D>::kTotal;
+    GradMaps maps;
+    const unsigned long long chunks = (unsigned long long)p.BH * p.N * a.NCH;
+    auto tokens = [&](CUtensorMap *m, const void *x) { return make_tmap_bf16_3d_sw128(m, x, p.BH, p.L, D, kCH); };
+    if (!tokens(&maps.dy, a.dy) || !tokens(&maps.e, a.E) || !tokens(&maps.w, a.dv) || !tokens(&maps.q, a.q) || !tokens(&maps.k, a.k) ||
+        !tokens(&maps.u, a.pw ? a.u : a.k) || !make_tmap_bf16_3d_sw128(&maps.S, a.S_c, chunks, D, D, 64) ||
+        !make_tmap_bf16_3d_sw128(&maps.R, a.R_c, chunks, D, D, 64))
+        return cudaErrorUnknown;
     auto kern = delta_grads_tc<D>;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-    kern<<<(unsigned)((long long)p.BH * p.N * a.NCH), kGradThreads, smem, s>>>(a);
+    kern<<<(unsigned)((long long)p.BH * p.N * a.NCH), kGradThreads, smem, s>>>(a, maps);
     e = cudaGetLastError();
     profile_after_kernel(s, "delta_grads_tc");
     return e;
