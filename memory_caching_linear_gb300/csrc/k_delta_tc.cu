@@ -108,7 +108,9 @@ __device__ __forceinline__ void clear_rows(uint8_t *tile, int cnt, int tid)
 //   X10 = -X11 A10 X00, X32 = -X33 A32 X22, and [X20 X21; X30 X31] = -[X22 0; X32 X33] [A20 A21; A30 A31] [X00 0; X10 X11].
 // A product's result is a left operand as it lies, its 8 x 8 transposes are a right one, and a block of X (or P) is, as it
 // lies, also the walk's operand of rows j, columns i: nothing but the diagonal blocks passes through shared memory.
-// (Substitution over all 64 rows, two columns a lane: 156 us at the long workload.)
+// 16 heads of 65536 tokens, d = 128: 111 us for 0.45 GB of keys read and records written, 4.1 TB/s (substitution over all
+// 64 rows, two columns a lane: 156 us); the gradients' form with P and the reverse record 44 us for 2048 chunks, where a
+// chunk's own chain of small products, 8 us, is what a warp waits for.
 // ---------------------------------------------------------------------------
 constexpr int kXP = 20, kXB = 16 * kXP + 8;  // row and block pitch of the diagonal blocks, in words
 
@@ -486,7 +488,10 @@ __device__ __forceinline__ void pair_sum(float4 *xb, int warp, int lane, F each,
 // ---------------------------------------------------------------------------
 // delta_walk_tc: one CTA per (bh, segment, 16 NW value rows); NW warps of 16 rows.  Two stages of
 // the chunk's K, V columns, (Q,) and record, filled by TMA one chunk ahead: copied by the threads, 16 bytes at a
-// time, they took a fifth of the time (shared memory's pipe is what the products wait for, too).
+// time, they took a fifth of the time (shared memory's pipe is what the products wait for, too).  16 heads of 65536
+// tokens, segments of 1024, d = 128: 421 us, 404 TFLOP/s of warp-level products against 600 that these reach when nothing
+// else is done; 512 CTAs share 456 places.  One memory of 4096 tokens, 32 heads (recomputed, one term): 121 us, 1.9 us for a
+// chunk, half of which are one warp's own products one after the other.
 // ---------------------------------------------------------------------------
 template <int D, int NW, int KP, bool READ>
 struct WalkSmem {
@@ -768,7 +773,8 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
 //   R' = exp(c_end) R + sum_i exp(c_i) (p_i q_i^T - w_i k_i^T)
 // R is held in fp32 and read in one bf16 term; T, P, X and w take part in two, as in the walk forwards: for keys that
 // resemble each other X gathers what later tokens ask of every one of them, and w is the small difference that is left
-// (one term: dv 3e-2 off at all but parallel keys).
+// (one term: dv 3e-2 off at all but parallel keys).  One memory of 4096 tokens, 32 heads, d = 128: 139 us, 2.2 us for a chunk,
+// its chain as in delta_walk_tc; 16 heads of 16384, segments of 1024: 170 us.
 // ---------------------------------------------------------------------------
 template <int D, int NW, int KP>
 struct RWalkSmem {
@@ -1000,7 +1006,9 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
 // other B2 (16 rows each), and leave them in shared memory as 16 x 16 blocks of the lower triangle, from which both
 // read them as they lie (with beta_j) and transposed.  A chunk is a chain of loads and small products, so two CTAs
 // share an SM, no load is waited for that could have been under way before, and tiles that have been read make room:
-// S's second block takes e's tile, R those of p and w, e comes again in S's first block, u in its second.
+// S's second block takes e's tile, R those of p and w, e comes again in S's first block, u in its second.  2048 chunks, d = 128:
+// 117 us for 0.40 GB (3.4 TB/s) and 33 GFLOP of products; 4096 chunks with gates and pooled keys 260 us.  Bound by the
+// latency of loads and products within a chunk, with 16 warps on an SM.
 // ---------------------------------------------------------------------------
 constexpr int kGradThreads = 256;
 

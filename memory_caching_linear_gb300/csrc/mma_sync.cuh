@@ -1,6 +1,6 @@
 // mma_sync.cuh -- warp-level matrix helpers of the gated delta kernels: m16n8k16 bf16 products with
 // fp32 accumulation, 8x8 matrix loads, 16-byte asynchronous copies, and the split of an fp32
-// value into two bf16 terms.
+// value into two or three bf16 terms.
 //
 // Fragments, with g = lane / 4 and c = lane % 4: an accumulator holds (row g, columns 2c, 2c+1) and
 // (row g + 8, the same); operand A (16 x 16) is two such tiles side by side in bf16, and B (16 x 8)
