@@ -1023,7 +1023,8 @@ cudaError_t launch_bwd_G_tc(const Problem &p, const void *dy, const void *q, con
     return cudaGetLastError();
 }
 
-// Two CTAs fit on an SM: enough shares of the tokens that every SM has two.
+// Two CTAs fit on an SM: enough shares of the tokens that every SM has two (16 heads, 16 segments of 1024, d = 128: 104 us in
+// three shares against 223 in one; reading the summands takes 8 us more).
 int bwd_G_parts(const Problem &p)
 {
     const int ctas = p.BH * (p.N / 2);

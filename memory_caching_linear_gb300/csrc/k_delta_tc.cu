@@ -94,10 +94,10 @@ __device__ __forceinline__ bool walk_sync_init(WalkSync *y, const void *sm, int 
     return y->abort_flag == 0;
 }
 // Rows from cnt on of a tile of ROW bytes a row: a chunk's last tokens may be another segment's.
-template <int ROW, int NT>
+template <int ROW, int ROWS, int NT>
 __device__ __forceinline__ void clear_rows(uint8_t *tile, int cnt, int tid)
 {
-    for (int e = cnt * (ROW / 16) + tid; e < kCH * (ROW / 16); e += NT) reinterpret_cast<uint4 *>(tile)[e] = make_uint4(0, 0, 0, 0);
+    for (int e = cnt * (ROW / 16) + tid; e < ROWS * (ROW / 16); e += NT) reinterpret_cast<uint4 *>(tile)[e] = make_uint4(0, 0, 0, 0);
 }
 
 // ---------------------------------------------------------------------------
@@ -109,8 +109,8 @@ __device__ __forceinline__ void clear_rows(uint8_t *tile, int cnt, int tid)
 // A product's result is a left operand as it lies, its 8 x 8 transposes are a right one, and a block of X (or P) is, as it
 // lies, also the walk's operand of rows j, columns i: nothing but the diagonal blocks passes through shared memory.
 // 16 heads of 65536 tokens, d = 128: 111 us for 0.45 GB of keys read and records written, 4.1 TB/s (substitution over all
-// 64 rows, two columns a lane: 156 us); the gradients' form with P and the reverse record 44 us for 2048 chunks, where a
-// chunk's own chain of small products, 8 us, is what a warp waits for.
+// 64 rows, two columns a lane: 156 us); with P and the reverse record 67 us for 4096 chunks, 4.6 TB/s, without P 40 us for
+// 2048 chunks, where a chunk's own chain of small products, 8 us, is what a warp waits for.
 // ---------------------------------------------------------------------------
 constexpr int kXP = 20, kXB = 16 * kXP + 8;  // row and block pitch of the diagonal blocks, in words
 
@@ -155,7 +155,8 @@ __device__ __forceinline__ void block_mma(float (&acc)[2][4], const Terms &a, co
 template <int D, bool QK>
 __host__ __device__ constexpr int prep_smem()
 {
-    return ((QK ? 2 : 1) * kCH * D * 2 > 8 * kXB * 4 ? (QK ? 2 : 1) * kCH * D * 2 : 8 * kXB * 4) + 2 * kCH * 4 + (int)sizeof(WalkSync);
+    constexpr int tiles = (kCH + (QK ? 32 : 0)) * D * 2;
+    return (tiles > 8 * kXB * 4 ? tiles : 8 * kXB * 4) + 2 * kCH * 4 + (int)sizeof(WalkSync);
 }
 
 template <int D, bool READ, bool REV>
@@ -171,14 +172,24 @@ __global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a, const __grid_
     if (w.cnt <= 0) return;
     const int lane = threadIdx.x, g = lane / 4, c = lane % 4;
     const size_t row0 = (size_t)w.bh * a.L + w.tb;
-    const uint32_t Kt = smem_addr(sm), Qt = Kt + kCH * D * 2;
+    // K, and 16 rows of Q at a time in two buffers: with all of Q an SM would hold six chunks, not eight
+    constexpr int QB = 16 * D * 2;
+    uint8_t *Qs = sm + kCH * D * 2;
+    const uint32_t Kt = smem_addr(sm);
+    auto load_q = [&](int b) {
+        mbar_arrive_expect_tx(&sync->full[b & 1], QB);
+#pragma unroll
+        for (int p = 0; p < D / 64; ++p)
+            tma_load_3d(Qs + (b & 1) * QB + p * 2048, &maps.q, 64 * p, w.tb + 16 * b, w.bh, &sync->full[b & 1]);
+    };
     bool ok = walk_sync_init(sync, sm, lane);
     if (ok && lane == 0) {
-        mbar_arrive_expect_tx(&sync->single, (QK ? 2 : 1) * kCH * D * 2);
+        mbar_arrive_expect_tx(&sync->single, kCH * D * 2);
 #pragma unroll
-        for (int p = 0; p < D / 64; ++p) {
-            tma_load_3d(sm + p * kPanel, &maps.k, 64 * p, w.tb, w.bh, &sync->single);
-            if (QK) tma_load_3d(sm + kCH * D * 2 + p * kPanel, &maps.q, 64 * p, w.tb, w.bh, &sync->single);
+        for (int p = 0; p < D / 64; ++p) tma_load_3d(sm + p * kPanel, &maps.k, 64 * p, w.tb, w.bh, &sync->single);
+        if (QK) {
+            load_q(0);
+            load_q(1);
         }
     }
     __syncwarp();
@@ -204,7 +215,7 @@ __global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a, const __grid_
     }
     if (w.cnt < kCH)
 #pragma unroll
-        for (int p = 0; p < (QK ? 2 : 1) * (D / 64); ++p) clear_rows<128, 32>(sm + p * kPanel, w.cnt, lane);
+        for (int p = 0; p < D / 64; ++p) clear_rows<128, kCH, 32>(sm + p * kPanel, w.cnt, lane);
     __syncwarp();
     uint8_t *rec = a.rec + (size_t)blockIdx.x * kRec, *rrec = REV ? a.rrec + (size_t)blockIdx.x * kDeltaRRecBytes : nullptr;
     const float ce = cum[kCH - 1];  // tokens past the end add nothing
@@ -233,6 +244,18 @@ __global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a, const __grid_
     float kk[10][2][4];  // 16 x 16 blocks (b, n2 <= b) of K K^T
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
+        uint8_t *Qb = Qs + (b & 1) * QB;
+        if (QK) {
+            if (ok) ok = mbar_wait(&sync->full[b & 1], b / 2, &sync->abort_flag);
+            if (__any_sync(0xffffffffu, !ok)) {
+                if (lane == 0) atomicExch(&g_delta_abort, 1);
+                return;
+            }
+            if (w.cnt < 16 * b + 16)
+#pragma unroll
+                for (int p = 0; p < D / 64; ++p) clear_rows<128, 16, 32>(Qb + p * 2048, max(w.cnt - 16 * b, 0), lane);
+            __syncwarp();
+        }
         float qk[4][2][4];
 #pragma unroll
         for (int n2 = 0; n2 <= b; ++n2)
@@ -244,7 +267,7 @@ __global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a, const __grid_
         for (int ks = 0; ks < KS; ++ks) {
             uint32_t ak[4], aq[4];
             ldsm4(ak, Kt + panel_off(16 * b + ar, 2 * ks + ac));
-            if (QK) ldsm4(aq, Qt + panel_off(16 * b + ar, 2 * ks + ac));
+            if (QK) ldsm4(aq, smem_addr(Qb) + (2 * ks + ac) / 8 * 2048 + tile_off<128>(ar, (2 * ks + ac) & 7));
 #pragma unroll
             for (int n2 = 0; n2 <= b; ++n2) {
                 uint32_t bf[4];
@@ -256,6 +279,11 @@ __global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a, const __grid_
                     mma16816(qk[n2][1], aq, bf[2], bf[3]);
                 }
             }
+        }
+        if (QK && b < 2) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) load_q(b + 2);
         }
         const float c0 = cum[16 * b + g], c1 = cum[16 * b + g + 8];
 #pragma unroll
@@ -565,10 +593,10 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
         if (cnt < kCH) {
 #pragma unroll
             for (int p = 0; p < D / 64; ++p) {
-                clear_rows<128, NT>(st + p * kPanel, cnt, tid);
-                if (READ) clear_rows<128, NT>(st + W::kK + W::kV + p * kPanel, cnt, tid);
+                clear_rows<128, kCH, NT>(st + p * kPanel, cnt, tid);
+                if (READ) clear_rows<128, kCH, NT>(st + W::kK + W::kV + p * kPanel, cnt, tid);
             }
-            clear_rows<NW * 32, NT>(vown, cnt, tid);
+            clear_rows<NW * 32, kCH, NT>(vown, cnt, tid);
             __syncthreads();
         }
 
@@ -869,8 +897,8 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
         const int cnt = min(kCH, len - ch * kCH);
         if (cnt < kCH) {
 #pragma unroll
-            for (int p = 0; p < 2 * (D / 64); ++p) clear_rows<128, NT>(st + p * kPanel, cnt, tid);
-            clear_rows<NW * 32, NT>(vown, cnt, tid);
+            for (int p = 0; p < 2 * (D / 64); ++p) clear_rows<128, kCH, NT>(st + p * kPanel, cnt, tid);
+            clear_rows<NW * 32, kCH, NT>(vown, cnt, tid);
             __syncthreads();
         }
         float X[8][4];
@@ -1063,7 +1091,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
     // the chunk's last tokens may be another segment's
     auto clear_tokens = [&](uint8_t *tile) {
 #pragma unroll
-        for (int p = 0; p < D / 64; ++p) clear_rows<128, kGradThreads>(tile + p * kPanel, w.cnt, tid);
+        for (int p = 0; p < D / 64; ++p) clear_rows<128, kCH, kGradThreads>(tile + p * kPanel, w.cnt, tid);
     };
     if (tid == 0) {
         sync->abort_flag = (smem_addr(sm) & 1023) != 0;
@@ -1534,10 +1562,10 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
 }
 
 template <int D, int NW>
-bool make_maps(DeltaMaps *m, const Problem &p, const DeltaTcArgs &a, const void *v)
+bool make_maps(DeltaMaps *m, const Problem &p, const DeltaTcArgs &a, const void *v, int q_rows = kCH)
 {
     const auto sw = NW == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-    return make_tmap_bf16_3d_sw128(&m->k, a.k, p.BH, p.L, D, kCH) && make_tmap_bf16_3d_sw128(&m->q, a.q, p.BH, p.L, D, kCH) &&
+    return make_tmap_bf16_3d_sw128(&m->k, a.k, p.BH, p.L, D, kCH) && make_tmap_bf16_3d_sw128(&m->q, a.q, p.BH, p.L, D, q_rows) &&
            make_tmap_bf16_3d(&m->v, v, p.BH, p.L, D, 16 * NW, kCH, sw);
 }
 
@@ -1615,7 +1643,7 @@ cudaError_t prep_impl(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
 {
     constexpr int smem = prep_smem<D, READ || REV>();
     DeltaMaps maps;
-    if (!make_maps<D, 4>(&maps, p, a, a.v)) return cudaErrorUnknown;
+    if (!make_maps<D, 4>(&maps, p, a, a.v, 16)) return cudaErrorUnknown;
     auto kern = delta_prep_tc<D, READ, REV>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;

@@ -230,7 +230,8 @@ int forward_delta(const void *q, const void *k, const void *v, const void *u, co
     return e == cudaSuccess && ef == cudaSuccess ? MC_OK : fail(e != cudaSuccess ? e : ef);
 }
 
-// Shares of the tokens for the CUDA-core G: two CTAs for every SM where there are few heads and segments.
+// Shares of the tokens for the CUDA-core G: two CTAs for every SM where there are few heads and segments (4 heads of 1000
+// tokens, 4 segments, d = 64: 18 us in eight shares, 100 in one).  The summands are added in their order.
 int simt_G_parts(const Problem &p)
 {
     const long long ctas = (long long)p.BH * (p.N - 1);
