@@ -318,3 +318,43 @@ def test_second_gradients_are_refused():
     dq, = torch.autograd.grad(y.square().sum(), x[0], create_graph=True)
     with pytest.raises(RuntimeError):
         dq.sum().backward()
+
+
+@pytest.mark.parametrize("d,dtype", [(32, "f32"), (64, "bf16"), (128, "bf16")])
+def test_neighbours_do_not_leak(d, dtype):
+    """NaN in another segment or another head: tiles of 64 tokens reach over a segment's end and must not use what is there."""
+    L, C = 290, 100
+    clean = cuda(make_delta_inputs(1, 2, L, d, C, 95, dtype))
+    bad = [t.clone() for t in clean]
+    for t in bad:
+        t[:, :, C:] = float("nan")
+    for mode in (RESIDUAL, GRM):
+        y, st = mcl.mc_forward_delta(*clean, C, mode)
+        yb, stb = mcl.mc_forward_delta(*bad, C, mode)
+        assert torch.equal(yb[:, :, :C], y[:, :, :C]) and torch.equal(stb[:, :, 0], st[:, :, 0])
+        assert torch.isnan(yb[:, :, C:]).all()
+    bad = [t.clone() for t in clean]
+    for t in bad:
+        t[:, 1] = float("nan")
+    dy = torch.randn(clean[0].shape, generator=torch.Generator().manual_seed(11)).to(clean[0])
+    dyb = dy.clone()
+    dyb[:, 1] = float("nan")
+    for C in (100, 70, L):
+        assert torch.equal(mcl.mc_forward_delta(*bad, C, GRM)[0][:, 0], mcl.mc_forward_delta(*clean, C, GRM)[0][:, 0])
+        want, got = mcl.mc_backward_delta(*clean, dy, C, GRM), mcl.mc_backward_delta(*bad, dyb, C, GRM)
+        for name, g, w in zip(("dq", "dk", "dv", "du", "dlog_alpha", "dbeta"), got, want):
+            assert rel(g[:, 0], w[:, 0].cpu()) <= TOL[dtype] / 10, name
+
+
+@pytest.mark.parametrize("d,C,L,dtype,mode,topk", [(16, 1, 300, "f32", GRM, 0), (64, 1, 300, "bf16", GRM, 0), (64, 2, 301, "bf16", SSC, 3),
+                                                   (64, 128, 2560, "bf16", SSC, 17), (128, 128, 2560, "bf16", SSC, 1)])
+def test_many_short_segments_and_wide_routers(d, C, L, dtype, mode, topk):
+    x = make_delta_inputs(1, 1, L, d, C, 97, dtype)
+    y, st = forward(*x, C, mode, topk)
+    gy, gst = mcl.mc_forward_delta(*cuda(x), C, mode, topk)
+    assert rel(gy, y) <= TOL[dtype] and rel(gst, st) <= STATE_TOL
+    dy = torch.randn(x[0].shape, generator=torch.Generator().manual_seed(12)).to(x[0].dtype)
+    got = mcl.mc_backward_delta(*cuda(x), dy.cuda(), C, mode, topk)
+    assert mcl.mc_check_device() == mcl.MC_OK
+    for name, g, w in zip(("dq", "dk", "dv", "du", "dlog_alpha", "dbeta"), got, backward(*x, dy, C, mode, topk)):
+        assert rel(g, w) <= TOL[dtype], name
