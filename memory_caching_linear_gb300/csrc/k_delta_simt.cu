@@ -80,19 +80,39 @@ __device__ __forceinline__ float dot_keys(const float (&x)[RowSplit<D>::KPL], co
     return s;
 }
 
+// The row with two vectors at once: their lanes' sums go side by side.
+template <int D>
+__device__ __forceinline__ float2 dot2_keys(const float (&m)[RowSplit<D>::KPL], const float (&x)[RowSplit<D>::KPL],
+                                            const float (&y)[RowSplit<D>::KPL])
+{
+    float p[4] = {0.f, 0.f, 0.f, 0.f}, q[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < RowSplit<D>::KPL; ++i) {
+        p[i & 3] = fmaf(m[i], x[i], p[i & 3]);
+        q[i & 3] = fmaf(m[i], y[i], q[i & 3]);
+    }
+    float2 s = make_float2((p[0] + p[1]) + (p[2] + p[3]), (q[0] + q[1]) + (q[2] + q[3]));
+#pragma unroll
+    for (int o = RowSplit<D>::G / 2; o > 0; o >>= 1) {
+        const float a = __shfl_xor_sync(0xffffffffu, s.x, o), b = __shfl_xor_sync(0xffffffffu, s.y, o);
+        s.x += a;
+        s.y += b;
+    }
+    return s;
+}
+
 // ---------------------------------------------------------------------------
-// delta_scan_simt: one CTA per (bh, segment, RC value rows).  Bound by the chain of one token
-// to the next (two dot products of a row, about 0.2 us a token: 60 us for segments of 250, fp32,
-// d = 64); it keeps the row in registers and the rows, heads and segments run side by side.  (A token's
-// read and the next one's first product taken together: the same; the reverse scan's next vectors
-// loaded ahead: 45 -> 53 us.)
+// delta_scan_simt: one CTA per (bh, segment, RC value rows).  Bound by the chain of one token to the next; the row
+// stays in registers, its read by q_t and by the next key go side by side, and the rows, heads and segments run in
+// parallel.  4 heads of 1024 tokens, fp32, d = 64: 186 us, 0.18 us a token (208 with the two reads one after the other; a
+// row over twice as many lanes 202; the reverse scan with its next vectors loaded ahead 171 instead of 162).
 // ---------------------------------------------------------------------------
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * RowSplit<D>::W) delta_scan_simt(DeltaArgs a)
 {
     using R = RowSplit<D>;
     constexpr int NT = 32 * R::W;
-    __shared__ __align__(16) float Ks[R::TT * D], Qs[R::TT * D], Vs[R::TT * R::RC];
+    __shared__ __align__(16) float Ks[(R::TT + 1) * D], Qs[R::TT * D], Vs[R::TT * R::RC];
     __shared__ float As[R::TT], Bs[R::TT];
     constexpr int splits = D / R::RC;
     const int rs = blockIdx.x % splits;
@@ -129,6 +149,7 @@ __global__ void __launch_bounds__(32 * RowSplit<D>::W) delta_scan_simt(DeltaArgs
             bn = be[c0 + tid];
         }
     };
+    for (int e = tid; e < D; e += NT) Ks[R::TT * D + e] = 0.f;  // (read, not used)
     fetch(t0);
     for (int c0 = t0; c0 < t1; c0 += R::TT) {
         const int cnt = min(R::TT, t1 - c0);
@@ -152,21 +173,30 @@ __global__ void __launch_bounds__(32 * RowSplit<D>::W) delta_scan_simt(DeltaArgs
         }
         if (c0 + R::TT < t1) fetch(c0 + R::TT);
         __syncthreads();
-        for (int t = 0; t < cnt; ++t) {
+        float z[R::KPL], y[R::KPL];
+        load_keys<D>(x, Ks, g);
+        float mk = dot_keys<D>(M, x);  // M_{t-1} k_t
+        size_t at_ = base + (size_t)c0 * D + row;
+        auto token = [&](int t, const float (&kt)[R::KPL], float (&kn)[R::KPL]) {
             const float at = As[t];
-            load_keys<D>(x, Ks + t * D, g);
-            const float e = Vs[t * R::RC + rl] - at * dot_keys<D>(M, x);
+            load_keys<D>(y, Qs + t * D, g);
+            load_keys<D>(kn, Ks + (t + 1) * D, g);
+            const float e = Vs[t * R::RC + rl] - at * mk;
             const float ue = Bs[t] * e;
 #pragma unroll
-            for (int i = 0; i < R::KPL; ++i) M[i] = fmaf(ue, x[i], at * M[i]);
-            load_keys<D>(x, Qs + t * D, g);
-            const float o = dot_keys<D>(M, x);
+            for (int i = 0; i < R::KPL; ++i) M[i] = fmaf(ue, kt[i], at * M[i]);
+            const float2 oz = dot2_keys<D>(M, y, kn);
+            mk = oz.y;
             if (g == 0) {
-                const size_t at_ = base + (size_t)(c0 + t) * D + row;
-                if (a.y) static_cast<T *>(a.y)[at_] = from_f<T>(o);
-                if (a.O_on) a.O_on[at_] = o;
+                if (a.y) static_cast<T *>(a.y)[at_] = from_f<T>(oz.x);
+                if (a.O_on) a.O_on[at_] = oz.x;
                 if (a.E) a.E[at_] = e;
             }
+            at_ += D;
+        };
+        for (int t = 0; t < cnt; t += 2) {
+            token(t, x, z);
+            if (t + 1 < cnt) token(t + 1, z, x);
         }
     }
     if (a.states) store_keys<D>(a.states + ((size_t)bh * a.N + seg) * D * D + (size_t)row * D, M, g);
