@@ -18,7 +18,7 @@
 // lows left out: 2^-17 of a term (the inverse in three, 2^-25).  The errors e_j of keys that resemble each other are large
 // and cancel in S and in O, so one term (2^-9) would show: at keys with a cosine of 0.8 it leaves the memory 7e-3 and y 9e-3
 // off, as against 2e-5 and 1.4e-3, the last bf16 rounding.  Two readings are one term's: O's of S, where nothing cancels and
-// the result is bf16, and E's of S in the gradients' own walk (S 4e-4 off there; 132 instead of 181 us at L = 4096, 32
+// the result is bf16, and E's of S in the gradients' own walk (S 4e-4 off there; 122 instead of 140 us at L = 2048, 96
 // heads, d = 128): what they yield passes through bf16 states and errors anyway.
 #include <cstdint>
 
@@ -1603,7 +1603,7 @@ bool make_maps(DeltaMaps *m, const Problem &p, const DeltaTcArgs &a, const void 
 // Few walkers leave most of the card idle, and a chunk's products on a walker's way to the next chunk are what counts: then
 // two warps share 16 rows, half of the keys each.  KP = 2 with two row groups per CTA as long as every CTA has an SM to
 // itself, else four row groups and whole rows.  L = 2048, d = 128, one memory (forward, recomputed, reverse walk), KP = 2
-// against 1: 32 heads (128 CTAs) 89 68 82 against 111 93 102 us; 48 heads (192 CTAs) 171 101 129 against 111 93 102 us.
+// against 1: 32 heads (128 CTAs) 81 64 74 against 103 77 96 us; 48 heads (192 CTAs) 156 93 139 against 103 76 96 us.
 inline bool split_keys(const Problem &p) { return (long long)p.BH * p.N * (p.d / 32) <= 152; }
 
 template <int D, int NW, int KP>
