@@ -38,6 +38,18 @@ int mc_selftest_umma(const void *X, const void *W, float *D, int form, mc_stream
  */
 int mc_selftest_wait_timeout(int limit_ms, mc_stream_t stream);
 
+/*
+ * mc_selftest_delta_give_up -- from the next launch on, the gated delta memory's
+ * tensor-core kernels take the chosen waits for ones that gave up: they abandon
+ * their work as after a time-out (the copies under way still land first), and
+ * mc_check_device reports MC_ERR_DEVICE_TIMEOUT.  Host state of the process; 0
+ * goes back to normal.
+ *   waits : a sum of 1 (a kernel's first tiles), 2 (what a kernel needs later:
+ *           the walks' single-buffered records, the gradients' S) and 4 (the
+ *           gradients' R and u).  MC_ERR_MODE for anything else.
+ */
+int mc_selftest_delta_give_up(int waits);
+
 #ifdef __cplusplus
 }
 #endif

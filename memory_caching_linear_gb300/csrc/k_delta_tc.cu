@@ -20,6 +20,7 @@
 // off, as against 2e-5 and 1.4e-3, the last bf16 rounding.  Two readings are one term's: O's of S, where nothing cancels and
 // the result is bf16, and E's of S in the gradients' own walk (S 4e-4 off there; 122 instead of 140 us at L = 2048, 96
 // heads, d = 128): what they yield passes through bf16 states and errors anyway.
+#include <atomic>
 #include <cstdint>
 
 #include "mc_internal.cuh"
@@ -34,6 +35,7 @@ using namespace mma;
 using namespace sm100;
 
 __device__ int g_delta_abort;
+std::atomic<int> g_give_up{0};  // waits to be taken for ones that gave up, in later launches
 
 constexpr int kCH = kDeltaChunk;
 
@@ -99,6 +101,19 @@ cudaError_t launch_early(K *kern, long long grid, int block, int smem, cudaStrea
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// A bounded wait; `refused` says that the caller is to take it for one that gave up (mc_selftest_delta_give_up).
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int *abort_flag, bool refused)
+{
+    return !refused && mbar_wait(bar, parity, abort_flag);
+}
+// A CTA that gives up: the thread that issued the copies waits (with a limit again) until those under way have landed, so
+// that none writes shared memory that is another CTA's by then.
+__device__ __forceinline__ void wait_out(uint64_t *bar, uint32_t parity)
+{
+    int gave_up = 0;
+    mbar_wait_limit(bar, parity, &gave_up, kWaitLimitNs);
+}
+
 // What follows the tiles in shared memory: a barrier per stage, one for the single buffer, and whether a wait gave up.
 struct WalkSync {
     uint64_t full[2], single;
@@ -115,6 +130,17 @@ __device__ __forceinline__ bool walk_sync_init(WalkSync *y, const void *sm, int 
     }
     __syncthreads();
     return y->abort_flag == 0;
+}
+// A walk that gives up after `stages` loads of stages (number j went to full[b(j)], its use j / 2 of that barrier) and
+// `singles` of the single buffer: none was issued where walk_sync_init said no.
+template <typename F>
+__device__ __forceinline__ void walk_gives_up(WalkSync *y, const void *sm, int stages, int singles, F b)
+{
+    if ((smem_addr(sm) & 1023) == 0) {
+        for (int j = max(stages - 2, 0); j < stages; ++j) wait_out(&y->full[b(j)], j / 2 & 1);
+        if (singles > 0) wait_out(&y->single, (singles - 1) & 1);
+    }
+    atomicExch(&g_delta_abort, 1);
 }
 // Rows from cnt on of a tile of ROW bytes a row: a chunk's last tokens may be another segment's.
 template <int ROW, int ROWS, int NT>
@@ -199,14 +225,24 @@ __global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a, const __grid_
     constexpr int QB = 16 * D * 2;
     uint8_t *Qs = sm + kCH * D * 2;
     const uint32_t Kt = smem_addr(sm);
+    const bool refused = a.give_up & kGiveUpTiles;
+    int under_way = 0;  // (lane 0) K and how many blocks of Q
     auto load_q = [&](int b) {
+        ++under_way;
         mbar_arrive_expect_tx(&sync->full[b & 1], QB);
 #pragma unroll
         for (int p = 0; p < D / 64; ++p)
             tma_load_3d(Qs + (b & 1) * QB + p * 2048, &maps.q, 64 * p, w.tb + 16 * b, w.bh, &sync->full[b & 1]);
     };
     bool ok = walk_sync_init(sync, sm, lane);
+    auto give_up = [&]() {
+        if (lane != 0) return;
+        if (under_way > 0) wait_out(&sync->single, 0);
+        for (int b = max(under_way - 3, 0); b < under_way - 1; ++b) wait_out(&sync->full[b & 1], b / 2);
+        atomicExch(&g_delta_abort, 1);
+    };
     if (ok && lane == 0) {
+        under_way = 1;
         mbar_arrive_expect_tx(&sync->single, kCH * D * 2);
 #pragma unroll
         for (int p = 0; p < D / 64; ++p) tma_load_3d(sm + p * kPanel, &maps.k, 64 * p, w.tb, w.bh, &sync->single);
@@ -231,9 +267,9 @@ __global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a, const __grid_
         bet[i] = i < w.cnt ? __bfloat162float(a.be[row0 + i]) : 0.f;
         bet[i + 1] = i + 1 < w.cnt ? __bfloat162float(a.be[row0 + i + 1]) : 0.f;
     }
-    if (ok) ok = mbar_wait(&sync->single, 0, &sync->abort_flag);
+    if (ok) ok = wait_for(&sync->single, 0, &sync->abort_flag, refused);
     if (__any_sync(0xffffffffu, !ok)) {
-        if (lane == 0) atomicExch(&g_delta_abort, 1);
+        give_up();
         return;
     }
     if (w.cnt < kCH)
@@ -269,9 +305,9 @@ __global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a, const __grid_
     for (int b = 0; b < 4; ++b) {
         uint8_t *Qb = Qs + (b & 1) * QB;
         if (QK) {
-            if (ok) ok = mbar_wait(&sync->full[b & 1], b / 2, &sync->abort_flag);
+            if (ok) ok = wait_for(&sync->full[b & 1], b / 2, &sync->abort_flag, refused);
             if (__any_sync(0xffffffffu, !ok)) {
-                if (lane == 0) atomicExch(&g_delta_abort, 1);
+                give_up();
                 return;
             }
             if (w.cnt < 16 * b + 16)
@@ -584,6 +620,9 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
         bulk_load(st + W::kStage - W::kR, a.rec + ((size_t)sid * a.NCH + ch) * kRec, W::kR, bar);
     };
     bool ok = walk_sync_init(sync, sm, tid);
+    auto give_up = [&](int stages, int singles) {
+        if (tid == 0) walk_gives_up(sync, sm, stages, W::kLate ? singles : 0, [](int j) { return j & 1; });
+    };
 
     float S[2 * KS][4];  // 16 rows x D / KP keys: tile n holds keys 16 k0 + 8 n ..
 #pragma unroll
@@ -594,10 +633,10 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
     after_previous();
     if (ok && tid == 0) load(0);
     for (int ch = 0; ch < nch; ++ch) {
-        if (ok) ok = mbar_wait(&sync->full[ch & 1], ch / 2 & 1, &sync->abort_flag);
+        if (ok) ok = wait_for(&sync->full[ch & 1], ch / 2 & 1, &sync->abort_flag, a.give_up & kGiveUpTiles);
         fence_async_smem();  // what was staged in the other stage goes before what will come there
         if (__syncthreads_or(!ok)) {
-            if (tid == 0) atomicExch(&g_delta_abort, 1);
+            give_up(ch + 1, ch);
             return;
         }
         if (tid == 0) {
@@ -734,7 +773,7 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
         }
         if (READ) {
             if (W::kLate) {
-                if (ok) ok = mbar_wait(&sync->single, ch & 1, &sync->abort_flag);
+                if (ok) ok = wait_for(&sync->single, ch & 1, &sync->abort_flag, a.give_up & kGiveUpLate);
                 __syncwarp();
             }
             const uint4 *pt = reinterpret_cast<const uint4 *>(W::kLate ? sm + 2 * W::kStage : rec + kRecT + kRecV) + lane;
@@ -802,6 +841,10 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
                 mma16816(S[2 * n2], ul[k4], b[0], b[1]);
                 mma16816(S[2 * n2 + 1], ul[k4], b[2], b[3]);
             }
+    }
+    if (W::kLate && __syncthreads_or(!ok)) {  // the last chunk's wait
+        give_up(nch, nch);
+        return;
     }
     let_next_start();
     if (a.states_img) {
@@ -873,6 +916,9 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
         return a.gon && ch * kCH + tid < len ? a.gon[((size_t)bh * a.L + t0 + ch * kCH + tid) * a.gw_stride] : 1.f;
     };
     bool ok = walk_sync_init(sync, sm, tid);
+    auto give_up = [&](int stages, int singles) {
+        if (tid == 0) walk_gives_up(sync, sm, stages, W::kLate ? singles : 0, [&](int j) { return (nch - 1 - j) & 1; });
+    };
     after_previous();
     if (ok && tid == 0) load(nch - 1);
     __syncwarp();
@@ -900,10 +946,10 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
 
     for (int ch = nch - 1; ch >= 0; --ch) {
         const int turn = nch - 1 - ch;
-        if (ok) ok = mbar_wait(&sync->full[ch & 1], turn / 2 & 1, &sync->abort_flag);
+        if (ok) ok = wait_for(&sync->full[ch & 1], turn / 2 & 1, &sync->abort_flag, a.give_up & kGiveUpTiles);
         fence_async_smem();  // what was staged in the other stage goes before what will come there
         if (__syncthreads_or(!ok)) {
-            if (tid == 0) atomicExch(&g_delta_abort, 1);
+            give_up(turn + 1, turn);
             return;
         }
         if (tid == 0) {
@@ -974,7 +1020,7 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
             put_rows(R, 1.f, lane, [&](int r, int n, int at, const uint2 &x) { *reinterpret_cast<uint2 *>(dst + (size_t)r * D + 8 * n + at / 2) = x; });
         }
         if (W::kLate) {
-            if (ok) ok = mbar_wait(&sync->single, turn & 1, &sync->abort_flag);
+            if (ok) ok = wait_for(&sync->single, turn & 1, &sync->abort_flag, a.give_up & kGiveUpLate);
             __syncwarp();
         }
         const uint4 *lt = reinterpret_cast<const uint4 *>(W::kLate ? sm + 2 * W::kStage : rec + kRecV) + lane;
@@ -1053,6 +1099,10 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
             }
         if (ch > 0 && tid < kCH) gates[(ch - 1 & 1) * kCH + tid] = next_gate;
     }
+    if (W::kLate && __syncthreads_or(!ok)) {  // the last chunk's wait
+        give_up(nch, nch);
+        return;
+    }
     let_next_start();
 }
 
@@ -1075,7 +1125,7 @@ struct GradMaps {
 };
 struct GradSync {
     uint64_t tiles, S0, S1, R, u;
-    int abort_flag, pad;
+    int abort_flag, used;  // used: the barriers, in this order, that copies were sent to
 };
 
 template <int D>
@@ -1125,6 +1175,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
     };
     if (tid == 0) {
         sync->abort_flag = (smem_addr(sm) & 1023) != 0;
+        sync->used = 0;
         mbar_init(&sync->tiles, 1);
         mbar_init(&sync->S0, 1);
         mbar_init(&sync->S1, 1);
@@ -1147,10 +1198,17 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
     }
     __syncthreads();
     bool ok = sync->abort_flag == 0;
-    auto wait = [&](uint64_t *bar) {
-        if (ok) ok = mbar_wait(bar, 0, &sync->abort_flag);
+    auto wait = [&](uint64_t *bar, int kind) {
+        if (ok) ok = wait_for(bar, 0, &sync->abort_flag, a.give_up & kind);
+    };
+    auto give_up = [&]() {
+        if (tid != 0) return;
+        for (uint64_t *bar : {&sync->tiles, &sync->S0, &sync->S1, &sync->R, &sync->u})
+            if (sync->used >> (bar - &sync->tiles) & 1) wait_out(bar, 0);
+        atomicExch(&g_delta_abort, 1);
     };
     if (ok && tid == 0) {
+        sync->used = 3;
         mbar_arrive_expect_tx(&sync->tiles, 5 * G::kT);
         load_tokens(Pt, maps.dy, &sync->tiles);
         load_tokens(Et, maps.e, &sync->tiles);
@@ -1175,9 +1233,9 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
         gs[gt] = g1;
         pw[gt] = g2;
     }
-    wait(&sync->tiles);
+    wait(&sync->tiles, kGiveUpTiles);
     if (__syncthreads_or(!ok)) {
-        if (tid == 0) atomicExch(&g_delta_abort, 1);
+        give_up();
         return;
     }
     if (w.cnt < kCH) {
@@ -1382,6 +1440,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
         fence_async_smem();  // (what was cleared or scaled in the tiles, before the copies over them)
         __syncthreads();     // the blocks are there, e has been read
         if (MB > 1 && tid == 0) {
+            sync->used |= 4;
             mbar_arrive_expect_tx(&sync->S1, G::kM);
             load_rows(Et, maps.S, 1, &sync->S1);
         }
@@ -1392,8 +1451,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
             if (blk < 10) pair_sums(b[x], half ? Kt : Qt, half ? -1.f : 1.f, blk, r, q);
         }
     }
-    wait(&sync->S0);
-    if (MB > 1) wait(&sync->S1);
+    wait(&sync->S0, kGiveUpLate);
+    if (MB > 1) wait(&sync->S1, kGiveUpLate);
     __syncwarp();
     float z[HN][4];
     zero(z);
@@ -1407,10 +1466,11 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
             times_rows(z, Wt, Et, 1);
         }
         if (__syncthreads_or(!ok)) {  // p and w have been read: their tiles take R
-            if (tid == 0) atomicExch(&g_delta_abort, 1);
+            give_up();
             return;
         }
         if (tid == 0) {
+            sync->used |= 8;
             mbar_arrive_expect_tx(&sync->R, MB * G::kM + (MB > 1 ? G::kT : 0));
             load_rows(Wt, maps.R, 0, &sync->R);
             if (MB > 1) {
@@ -1462,7 +1522,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
     if (MB > 1)
 #pragma unroll
         for (int x = 0; x < X4; ++x) s4[x] = *reinterpret_cast<const uint4 *>(S + (size_t)(tid + x * kGradThreads) * 8);
-    wait(&sync->R);
+    wait(&sync->R, kGiveUpEnd);
     __syncwarp();
     if (MB > 1 && w.cnt < kCH) {
         clear_tokens(E2);
@@ -1483,6 +1543,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
     if (a.pw) {  // u for the pooled keys' share, into their place
         __syncthreads();
         if (ok && tid == 0) {
+            sync->used |= 16;
             mbar_arrive_expect_tx(&sync->u, G::kT);
             load_tokens(Sl, maps.u, &sync->u);
         }
@@ -1518,9 +1579,9 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
             y[n][3] = fmaf(be1, y[n][3], -z[n][3]);
         }
     }
-    if (a.pw) wait(&sync->u);
+    if (a.pw) wait(&sync->u, kGiveUpEnd);
     if (__syncthreads_or(!ok)) {  // the sums are there
-        if (tid == 0) atomicExch(&g_delta_abort, 1);
+        give_up();
         return;
     }
     if (a.pw && w.cnt < kCH) {
@@ -1727,8 +1788,12 @@ cudaError_t launch_delta_dgon(const Problem &p, const void *dy, const void *O, f
     return cudaGetLastError();
 }
 
-cudaError_t launch_delta_grads_tc(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
+void set_delta_give_up(int waits) { g_give_up = waits; }
+
+cudaError_t launch_delta_grads_tc(const Problem &p, const DeltaTcArgs &args, cudaStream_t s)
 {
+    DeltaTcArgs a = args;
+    a.give_up = g_give_up;
     return p.d == 64 ? grads_tc_impl<64>(p, a, s) : grads_tc_impl<128>(p, a, s);
 }
 
@@ -1741,8 +1806,10 @@ cudaError_t launch_delta_scalars(const Problem &p, const void *la, float *alpha,
     return cudaGetLastError();
 }
 
-cudaError_t launch_delta_walk_tc(const Problem &p, const DeltaTcArgs &a, bool read, cudaStream_t s)
+cudaError_t launch_delta_walk_tc(const Problem &p, const DeltaTcArgs &args, bool read, cudaStream_t s)
 {
+    DeltaTcArgs a = args;
+    a.give_up = g_give_up;
     if (p.d == 64) return read ? walk_impl<64, true>(p, a, s) : walk_impl<64, false>(p, a, s);
     return read ? walk_impl<128, true>(p, a, s) : walk_impl<128, false>(p, a, s);
 }

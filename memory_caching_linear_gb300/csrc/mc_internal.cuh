@@ -335,7 +335,10 @@ struct DeltaTcArgs {
     __nv_bfloat16 *R_c;    // [BH][N][NCH][d][d] adjoint after every chunk
     __nv_bfloat16 *dq, *dk, *dv, *dla, *dbe;
     int BH, L, C, N, NCH;
+    int give_up;           // kGiveUp*: waits that are taken for ones that gave up (set by the launchers)
 };
+constexpr int kGiveUpTiles = 1, kGiveUpLate = 2, kGiveUpEnd = 4;
+void set_delta_give_up(int waits);
 // dy_t . O_t of every token.
 cudaError_t launch_delta_dgon(const Problem &p, const void *dy, const void *O, float *dgon, cudaStream_t s);
 // After the walk with rrec, E and S_c: dv and R_c, then the other gradients.

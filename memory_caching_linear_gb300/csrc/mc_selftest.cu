@@ -191,3 +191,10 @@ extern "C" int mc_selftest_wait_timeout(int limit_ms, mc_stream_t stream_)
     if (e != cudaSuccess || es != cudaSuccess) return MC_ERR_CUDA;
     return h == 1 ? MC_ERR_DEVICE_TIMEOUT : MC_OK;
 }
+
+extern "C" int mc_selftest_delta_give_up(int waits)
+{
+    if (waits & ~(mc::kGiveUpTiles | mc::kGiveUpLate | mc::kGiveUpEnd)) return MC_ERR_MODE;
+    mc::set_delta_give_up(waits);
+    return MC_OK;
+}
