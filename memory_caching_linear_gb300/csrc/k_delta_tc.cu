@@ -205,7 +205,7 @@ template <int D, bool QK>
 __host__ __device__ constexpr int prep_smem()
 {
     constexpr int tiles = (kCH + (QK ? 32 : 0)) * D * 2;
-    return (tiles > 8 * kXB * 4 ? tiles : 8 * kXB * 4) + 2 * kCH * 4 + (int)sizeof(WalkSync);
+    return (tiles > 8 * kXB * 4 ? tiles : 8 * kXB * 4) + 3 * kCH * 4 + (int)sizeof(WalkSync);
 }
 
 template <int D, bool READ, bool REV>
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a, const __grid_
     extern __shared__ __align__(1024) uint8_t sm[];
     float *Ad = reinterpret_cast<float *>(sm), *Xd = Ad + 4 * kXB;  // over the tiles once these are read
     WalkSync *sync = reinterpret_cast<WalkSync *>(sm + prep_smem<D, QK>() - sizeof(WalkSync));
-    float *bet = reinterpret_cast<float *>(sync) - kCH, *cum = bet - kCH;
+    float *bet = reinterpret_cast<float *>(sync) - kCH, *cum = bet - kCH, *cul = cum - kCH;
     const Where w = chunk_at(a, blockIdx.x);
     if (w.cnt <= 0) return;
     const int lane = threadIdx.x, g = lane / 4, c = lane % 4;
@@ -252,18 +252,23 @@ __global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a, const __grid_
         }
     }
     __syncwarp();
-    {  // running sums of the chunk's decays, two tokens per lane
+    {  // running sums of the chunk's decays as cum + cul (delta_parts), two tokens per lane
         const int i = 2 * lane;
-        const float x0 = i < w.cnt ? delta_log(__bfloat162float(a.la[row0 + i])) : 0.f;
-        const float x1 = i + 1 < w.cnt ? delta_log(__bfloat162float(a.la[row0 + i + 1])) : 0.f;
-        float s = x0 + x1;
+        const float2 x0 = delta_parts(i < w.cnt ? delta_log(__bfloat162float(a.la[row0 + i])) : 0.f);
+        const float2 x1 = delta_parts(i + 1 < w.cnt ? delta_log(__bfloat162float(a.la[row0 + i + 1])) : 0.f);
+        float s = x0.x + x1.x, r = x0.y + x1.y;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const float n = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += n;
+            const float n = __shfl_up_sync(0xffffffffu, s, o), m = __shfl_up_sync(0xffffffffu, r, o);
+            if (lane >= o) {
+                s += n;
+                r += m;
+            }
         }
-        cum[i] = s - x1;
+        cum[i] = s - x1.x;
         cum[i + 1] = s;
+        cul[i] = r - x1.y;
+        cul[i + 1] = r;
         bet[i] = i < w.cnt ? __bfloat162float(a.be[row0 + i]) : 0.f;
         bet[i + 1] = i + 1 < w.cnt ? __bfloat162float(a.be[row0 + i + 1]) : 0.f;
     }
@@ -277,14 +282,14 @@ __global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a, const __grid_
         for (int p = 0; p < D / 64; ++p) clear_rows<128, kCH, 32>(sm + p * kPanel, w.cnt, lane);
     __syncwarp();
     uint8_t *rec = a.rec + (size_t)blockIdx.x * kRec, *rrec = REV ? a.rrec + (size_t)blockIdx.x * kDeltaRRecBytes : nullptr;
-    const float ce = cum[kCH - 1];  // tokens past the end add nothing
+    const float ce = cum[kCH - 1], cel = cul[kCH - 1];  // tokens past the end add nothing
     {
         float *vec = reinterpret_cast<float *>(rec + kRecT);
         float *rvec = reinterpret_cast<float *>(rrec);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const int i = lane + 32 * x;
-            const float ea = __expf(cum[i]), eb = __expf(ce - cum[i]);
+            const float ea = __expf(cum[i] + cul[i]), eb = __expf((ce - cum[i]) + (cel - cul[i]));
             vec[i] = ea;
             vec[64 + i] = bet[i] * eb;
             vec[128 + i] = bet[i];
@@ -295,8 +300,8 @@ __global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a, const __grid_
             }
         }
         if (lane == 0) {
-            vec[192] = __expf(ce);
-            if (REV) rvec[192] = __expf(ce);
+            vec[192] = __expf(ce + cel);
+            if (REV) rvec[192] = __expf(ce + cel);
         }
     }
     const int ar = lane & 15, ac = lane >> 4, br = (lane >> 4) * 8 + (lane & 7), bc = (lane >> 3) & 1;
@@ -344,19 +349,20 @@ __global__ void __launch_bounds__(32) delta_prep_tc(DeltaTcArgs a, const __grid_
             __syncwarp();
             if (lane == 0) load_q(b + 2);
         }
-        const float c0 = cum[16 * b + g], c1 = cum[16 * b + g + 8];
+        const float c0 = cum[16 * b + g], c1 = cum[16 * b + g + 8], r0 = cul[16 * b + g], r1 = cul[16 * b + g + 8];
 #pragma unroll
         for (int n2 = 0; n2 <= b; ++n2) {
             uint32_t p[2][2], pl[2][2];  // [columns half][rows half] 8 x 8 tiles of P, two terms
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const float2 cj = *reinterpret_cast<const float2 *>(cum + 16 * n2 + 8 * h + 2 * c);
+                const float2 rj = *reinterpret_cast<const float2 *>(cul + 16 * n2 + 8 * h + 2 * c);
                 const float2 bj = *reinterpret_cast<const float2 *>(bet + 16 * n2 + 8 * h + 2 * c);
                 float v[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int il = g + 8 * (e >> 1), jl = 8 * h + 2 * c + (e & 1);
-                    const float dec = __expf((e >> 1 ? c1 : c0) - (e & 1 ? cj.y : cj.x));
+                    const float dec = __expf(((e >> 1 ? c1 : c0) - (e & 1 ? cj.y : cj.x)) + ((e >> 1 ? r1 : r0) - (e & 1 ? rj.y : rj.x)));
                     float &x = kk[b * (b + 1) / 2 + n2][h][e];
                     x = n2 < b || jl < il ? x * (dec * (e & 1 ? bj.y : bj.x)) : 0.f;  // A
                     v[e] = n2 < b || jl <= il ? qk[n2][h][e] * dec : 0.f;

@@ -286,6 +286,14 @@ constexpr int kDeltaChunk = 64;  // tokens of a chunk
 // Decays below exp(-60) (one part in 1e26) count as that: differences of their running sums stay finite.
 __device__ __forceinline__ float delta_log(float x) { return x < -60.f ? -60.f : x; }
 __device__ __forceinline__ float delta_decay(float x) { return expf(delta_log(x)); }
+// A running sum of decays loses |sum| 2^-24, which a difference of two sums far from zero shows (2e-4 after a chunk of
+// resets).  So a logarithm is split: a multiple of 2^-11, whose sums over a chunk (below 2^12) are exact, and the rest, below
+// 2^-12; c_i - c_j is then the difference of the first sums, exact, and of the second, 2^-30 off.
+__device__ __forceinline__ float2 delta_parts(float x)
+{
+    const float m = rintf(x * 2048.f) * (1.f / 2048.f);
+    return make_float2(m, x - m);
+}
 struct DeltaArgs {
     const void *q, *k, *v, *u, *dy;  // [BH][L][d], element type per Problem::bf16
     const void *la, *be;             // log_alpha, beta [BH][L], the same type

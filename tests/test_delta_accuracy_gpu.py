@@ -1,0 +1,51 @@
+"""How exact the gated delta memory is where its gates or keys make that hard, against the 64-bit form (delta_ref).
+
+Errors are relative to the largest reference value of an output, as in test_delta_gpu.py, and so are the tolerances that
+these tests share with it: 1e-4 for fp32 results and for states, 1e-2 for bf16 results."""
+import pytest
+import torch
+
+import memory_caching_linear_gb300 as mcl
+from delta_ref import GRM, MEAN, RESIDUAL, SSC, backward, forward, make_delta_inputs
+
+pytestmark = pytest.mark.gpu
+
+NAMES = ("dq", "dk", "dv", "du", "dlog_alpha", "dbeta")
+TOL = {"f32": 1e-4, "bf16": 1e-2}
+STATE_TOL = 1e-4
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from memory_caching_linear_gb300 import build
+    build.build()
+    mcl.load_library()
+
+
+def rel(got, ref):
+    ref = ref.double()
+    scale = float(ref.abs().max())
+    return float((got.double().cpu() - ref).abs().max()) / (scale if scale > 0 else 1.0)
+
+
+def cuda(xs):
+    return [x.cuda() if x is not None else None for x in xs]
+
+
+def after_resets(H, L, d, C, dtype, resets):
+    """Every chunk of 64 tokens starts with so many full resets and goes on with ordinary decays; the ends of the segments
+    lie in such a stretch."""
+    x = make_delta_inputs(1, H, L, d, C, d + resets, dtype, decay=0.05)
+    for s in range(0, L, 64):
+        x[4][:, :, s:s + resets] = -float("inf")
+    return x, [*x[:4], x[4].double().clamp_min(-60.0), x[5]]
+
+
+@pytest.mark.parametrize("resets", [48, 56, 60])
+@pytest.mark.parametrize("d,C,L", [(64, 128, 256), (64, 64, 64), (128, 128, 128), (128, 192, 384)])
+def test_states_after_many_resets(d, C, L, resets):
+    """The decay between two neighbouring tokens is one number whatever came before them."""
+    x, floor = after_resets(4, L, d, C, "bf16", resets)
+    y, st = forward(*floor, C, GRM)
+    gy, gst = mcl.mc_forward_delta(*cuda(x), C, GRM)
+    assert rel(gst, st) <= STATE_TOL and rel(gy, y) <= TOL["bf16"]
