@@ -310,7 +310,7 @@ constexpr int kGB = 32;  // rows of S and R at once (16 for d = 16)
 template <int D>
 constexpr size_t grads_smem()
 {
-    return sizeof(float) * (5 * kCH * (D + 1) + 2 * kCH * (kCH + 1) + (D < kGB ? D : kGB) * (D + 1) + 6 * kCH + 32);
+    return sizeof(float) * (5 * kCH * (D + 1) + 2 * kCH * (kCH + 1) + (D < kGB ? D : kGB) * (D + 1) + 7 * kCH + 32);
 }
 
 template <typename T, int D>
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kGT) delta_grads_simt(DeltaArgs a)
     extern __shared__ float sm[];
     float *Qs = sm, *Ks = Qs + kCH * P, *Ps = Ks + kCH * P, *Es = Ps + kCH * P, *Ws = Es + kCH * P;
     float *B1 = Ws + kCH * P, *B2 = B1 + kCH * BP, *Ms = B2 + kCH * BP;
-    float *cum = Ms + GB * P, *bet = cum + kCH, *hd = bet + kCH, *hb = hd + kCH, *dbe = hb + kCH, *red = dbe + kCH;
+    float *cum = Ms + GB * P, *bet = cum + kCH, *hd = bet + kCH, *hb = hd + kCH, *dbe = hb + kCH, *cul = dbe + kCH, *red = cul + kCH;
 
     const int ch = (int)blockIdx.x % a.NCH;
     const int seg = (int)(blockIdx.x / a.NCH) % a.N, bh = (int)(blockIdx.x / a.NCH) / a.N;
@@ -348,15 +348,20 @@ __global__ void __launch_bounds__(kGT) delta_grads_simt(DeltaArgs a)
         Ws[r * P + c] = ok ? a.W[base + gi] : 0.f;
     }
     if (tid < kCH) {
-        cum[tid] = tid < cnt ? delta_log(to_f(la[tb + tid])) : 0.f;
+        const float2 x = delta_parts(tid < cnt ? delta_log(to_f(la[tb + tid])) : 0.f);
+        cum[tid] = x.x;
+        cul[tid] = x.y;
         bet[tid] = tid < cnt ? to_f(be[tb + tid]) : 0.f;
         hd[tid] = hb[tid] = dbe[tid] = 0.f;
     }
     __syncthreads();
     if (tid == 0)
-        for (int i = 1; i < kCH; ++i) cum[i] += cum[i - 1];
+        for (int i = 1; i < kCH; ++i) {
+            cum[i] += cum[i - 1];
+            cul[i] += cul[i - 1];
+        }
     __syncthreads();
-    const float cend = cum[last];
+    auto decay = [&](int i, int j) { return expf((cum[i] - cum[j]) + (cul[i] - cul[j])); };  // D_ij
     for (int e = tid; e < kCH * kCH; e += kGT) {
         const int i = e / kCH, j = e % kCH;
         float b1 = 0.f, b2 = 0.f;
@@ -365,7 +370,7 @@ __global__ void __launch_bounds__(kGT) delta_grads_simt(DeltaArgs a)
                 b1 = fmaf(Ps[i * P + c], Es[j * P + c], b1);
                 b2 = fmaf(Ws[i * P + c], Es[j * P + c], b2);
             }
-            const float dec = expf(cum[i] - cum[j]);
+            const float dec = decay(i, j);
             b1 *= dec;
             b2 = j < i ? b2 * dec : 0.f;
         }
@@ -425,7 +430,7 @@ __global__ void __launch_bounds__(kGT) delta_grads_simt(DeltaArgs a)
 #pragma unroll
     for (int p = 0; p < TP; ++p) {
         const int t = ty + 16 * p;
-        const float ge = expf(cum[t]), gr = expf(cend - cum[t]);
+        const float ge = expf(cum[t] + cul[t]), gr = decay(last, t);
         float dq[RB], y[RB], kk[RB];
 #pragma unroll
         for (int r = 0; r < RB; ++r) {
@@ -481,7 +486,7 @@ __global__ void __launch_bounds__(kGT) delta_grads_simt(DeltaArgs a)
     if (tid == 0) {  // h backwards over the chunk
         float in = 0.f;
         for (int w = 0; w < kGT / 32; ++w) in += red[w];
-        float h = expf(cend) * in;
+        float h = expf(cum[last] + cul[last]) * in;
         for (int t = 0; t < cnt; ++t) h += hb[t];
         for (int t = last; t >= 0; --t) {
             h += hd[t];

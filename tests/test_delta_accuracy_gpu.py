@@ -49,3 +49,13 @@ def test_states_after_many_resets(d, C, L, resets):
     y, st = forward(*floor, C, GRM)
     gy, gst = mcl.mc_forward_delta(*cuda(x), C, GRM)
     assert rel(gst, st) <= STATE_TOL and rel(gy, y) <= TOL["bf16"]
+
+
+@pytest.mark.parametrize("resets", [40, 60])
+@pytest.mark.parametrize("d,C,L,mode", [(16, 64, 128, GRM), (32, 64, 64, RESIDUAL), (64, 128, 256, GRM), (128, 64, 64, RESIDUAL)])
+def test_fp32_gradients_after_many_resets(d, C, L, mode, resets):
+    x, floor = after_resets(2, L, d, C, "f32", resets)
+    dy = torch.randn(x[0].shape, generator=torch.Generator().manual_seed(3))
+    for name, g, w in zip(NAMES, mcl.mc_backward_delta(*cuda(x), dy.cuda(), C, mode), backward(*floor, dy, C, mode)):
+        if g is not None:
+            assert rel(g, w) <= TOL["f32"], name
