@@ -157,9 +157,9 @@ __device__ __forceinline__ void clear_rows(uint8_t *tile, int cnt, int tid)
 //   X10 = -X11 A10 X00, X32 = -X33 A32 X22, and [X20 X21; X30 X31] = -[X22 0; X32 X33] [A20 A21; A30 A31] [X00 0; X10 X11].
 // A product's result is a left operand as it lies, its 8 x 8 transposes are a right one, and a block of X (or P) is, as it
 // lies, also the walk's operand of rows j, columns i: nothing but the diagonal blocks passes through shared memory.
-// 16 heads of 65536 tokens, d = 128: 111 us for 0.45 GB of keys read and records written, 4.1 TB/s (substitution over all
-// 64 rows, two columns a lane: 156 us); with P and the reverse record 67 us for 4096 chunks, 4.6 TB/s, without P 40 us for
-// 2048 chunks, where a chunk's own chain of small products, 8 us, is what a warp waits for.
+// 16 heads of 65536 tokens, d = 128: 164 us for 0.89 GB of keys and queries read and records written, 5.4 TB/s (without P
+// 102 us; substitution over all 64 rows, two columns a lane: 156); with P and the reverse record 62 us for 4096 chunks,
+// 5.0 TB/s, without P 34 us for 2048 chunks, where a chunk's own chain of small products, 8 us, is what a warp waits for.
 // ---------------------------------------------------------------------------
 constexpr int kXP = 20, kXB = 16 * kXP + 8;  // row and block pitch of the diagonal blocks, in words
 
@@ -583,9 +583,10 @@ __device__ __forceinline__ void pair_sum(float4 *xb, int warp, int lane, F each,
 // delta_walk_tc: one CTA per (bh, segment, 16 NW value rows); NW warps of 16 rows.  Two stages of
 // the chunk's K, V columns, (Q,) and record, filled by TMA one chunk ahead: copied by the threads, 16 bytes at a
 // time, they took a fifth of the time (shared memory's pipe is what the products wait for, too).  16 heads of 65536
-// tokens, segments of 1024, d = 128: 421 us, 404 TFLOP/s of warp-level products against 600 that these reach when nothing
-// else is done; 512 CTAs share 456 places.  One memory of 4096 tokens, 32 heads (recomputed, one term): 121 us, 1.9 us for a
-// chunk, half of which are one warp's own products one after the other.
+// tokens, segments of 1024, d = 128: 571 us, 413 TFLOP/s of warp-level products against 600 that these reach when nothing
+// else is done (420 us without the online reads, which the readout would then form in one term).  One memory of 4096
+// tokens, 32 heads (recomputed, one term): 117 us, 1.8 us for a chunk, half of which are one warp's own products one after
+// the other.
 // ---------------------------------------------------------------------------
 template <int D, int NW, int KP, bool READ>
 struct WalkSmem {
@@ -738,12 +739,6 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
                 O[n][3] *= ga.y;
             }
         }
-        if (a.spre_img && ch > 0 && !(ch & 1)) {  // panels of 64 columns, their pieces exchanged by row % 8
-            uint8_t *img = a.spre_img + ((size_t)sid * (a.C / 128) + ch / 2) * (D * D * 2) + (vbase + 16 * wr) * 128;
-            put_rows(S, vec[0], lane, [&](int r, int n, int at, const uint2 &x) {
-                *reinterpret_cast<uint2 *>(img + (2 * k0 + n) / 8 * (D * 128) + tile_off<128>(r, (2 * k0 + n) % 8) + at) = x;
-            });
-        }
         if (a.S_c) {  // the memory before the chunk
             __nv_bfloat16 *dst = a.S_c + (cidx * D + vbase + 16 * wr) * D + 16 * k0;
             put_rows(S, 1.f, lane, [&](int r, int n, int at, const uint2 &x) { *reinterpret_cast<uint2 *>(dst + (size_t)r * D + 8 * n + at / 2) = x; });
@@ -768,7 +763,7 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
                     mma16816(X[n], rh[k4], b.z, b.w);
                 }
         }
-        // U = diag(beta) E for the read and the readout; U' = diag(beta exp(c_end - c)) E for the memory
+        // U = diag(beta) E for the read; U' = diag(beta exp(c_end - c)) E for the memory
         const float dec = vec[192];
         uint32_t uh[4][4], ul[4][4];
 #pragma unroll
@@ -797,7 +792,6 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
         auto put = [&](__nv_bfloat16 *dst, const uint32_t (&f)[4][4]) {
             put_tokens<NW, KP, D>(dst + row0 * D + vbase + 16 * wr, f, vown, cnt, wr, kp, lane);
         };
-        if (a.U) put(a.U, uh);
         if (READ) {
             uint32_t of[4][4];
 #pragma unroll
@@ -1703,17 +1697,6 @@ cudaError_t grads_tc_impl(const Problem &p, const DeltaTcArgs &a, cudaStream_t s
     return e;
 }
 
-// The scalars of the window update that the readout's kernels take (mc_forward_swla's alpha, beta, lambda):
-// over the written values beta_t e_t the delta memory is the one with alpha = exp(log_alpha), beta = 0, lambda = 1.
-__global__ void __launch_bounds__(256) delta_scalars(const __nv_bfloat16 *la, float *alpha, float *zero, float *one, long long n)
-{
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n) return;
-    alpha[i] = delta_decay(__bfloat162float(la[i]));
-    zero[i] = 0.f;
-    one[i] = 1.f;
-}
-
 // dy_t . O_t per token (the gradient of the online gate): d / 8 lanes per token.
 __global__ void __launch_bounds__(256) delta_dgon(const __nv_bfloat16 *dy, const __nv_bfloat16 *O, float *dgon, long long tokens, int d)
 {
@@ -1763,10 +1746,11 @@ cudaError_t walk_kp(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
 template <int D, bool READ>
 cudaError_t walk_impl(const Problem &p, const DeltaTcArgs &a, cudaStream_t s)
 {
-    cudaError_t e = a.rrec ? prep_impl<D, READ, true>(p, a, s) : prep_impl<D, READ, false>(p, a, s);
+    // (the forward always reads, and only it walks in full terms and without the reverse walk's record)
+    cudaError_t e = !READ || a.rrec ? prep_impl<D, READ, true>(p, a, s) : prep_impl<D, true, false>(p, a, s);
     if (e != cudaSuccess) return e;
     profile_after_kernel(s, "delta_prep_tc");
-    e = a.full ? walk_kp<D, READ, true>(p, a, s) : walk_kp<D, READ, false>(p, a, s);
+    e = READ && a.full ? walk_kp<D, true, true>(p, a, s) : walk_kp<D, READ, false>(p, a, s);
     profile_after_kernel(s, "delta_walk_tc");
     return e;
 }
@@ -1804,13 +1788,6 @@ cudaError_t launch_delta_grads_tc(const Problem &p, const DeltaTcArgs &args, cud
 }
 
 bool delta_tc_supported(const Problem &p) { return p.bf16 && (p.d == 64 || p.d == 128); }
-
-cudaError_t launch_delta_scalars(const Problem &p, const void *la, float *alpha, float *zero, float *one, cudaStream_t s)
-{
-    const long long n = (long long)p.BH * p.L;
-    delta_scalars<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(static_cast<const __nv_bfloat16 *>(la), alpha, zero, one, n);
-    return cudaGetLastError();
-}
 
 cudaError_t launch_delta_walk_tc(const Problem &p, const DeltaTcArgs &args, bool read, cudaStream_t s)
 {

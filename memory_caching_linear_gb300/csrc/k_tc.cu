@@ -237,15 +237,14 @@ bool tc_supported(const Problem &p)
 
 bool tc_fused_gates(const Problem &p) { return tc_supported(p) && p.N <= 64; }
 
-size_t tc_scratch_bytes(const Problem &p) { return forward_scratch_bytes(p); }
+size_t tc_scratch_bytes(const Problem &p, bool given) { return forward_scratch_bytes(p, given); }
 
 TcForwardImages tc_forward_images(const Problem &p, void *scratch)
 {
     const size_t BH = p.BH, N = p.N, im = img_bytes(p);
     TcForwardImages t;
     t.states_img = static_cast<uint8_t *>(scratch);
-    t.spre_img = t.states_img + pad256(BH * N * im);
-    t.kbar_img = t.spre_img + pad256(BH * N * (p.C / kCT) * im);
+    t.kbar_img = t.states_img + pad256(BH * N * im);
     t.r_on = reinterpret_cast<float *>(t.kbar_img + pad256(BH * ((N + 63) / 64) * kKbImg));
     return t;
 }

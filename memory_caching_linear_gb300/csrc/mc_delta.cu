@@ -95,9 +95,9 @@ DeltaTcArgs delta_tc_args(const Call &c, const void *q, const void *k, const voi
     return t;
 }
 
-// bf16, d = 64 or 128.  One memory: the walk writes y.  Several, where the readout's tensor-core kernels take
-// the shape: the walk writes the states and the written values beta_t e_t, and the readout runs over these
-// with the decay.  Otherwise the walk writes the online reads for the CUDA-core readout.
+// bf16, d = 64 or 128.  One memory: the walk writes y.  Several: the walk writes the states and, in fp32, the online reads,
+// whose terms may cancel and which it forms in two bf16 terms (at all but parallel keys one term left y 4e-2 off); the
+// readout adds the cached memories, on the tensor cores where it takes the shape.
 int forward_delta_tc(const Call &c, const void *q, const void *k, const void *v, const void *u, const void *la,
                      const void *be, void *y, float *states, cudaStream_t s)
 {
@@ -108,7 +108,7 @@ int forward_delta_tc(const Call &c, const void *q, const void *k, const void *v,
     t.states = states;
     t.full = true;
     FwdArgs f{};
-    float *kbar = nullptr, *r_on = nullptr, *sums = nullptr, *alpha = nullptr, *zero = nullptr, *ones = nullptr;
+    float *kbar = nullptr, *r_on = nullptr, *sums = nullptr;
     char *tc_scratch = nullptr;
     void *scratch = nullptr;
     for (int pass = 0; pass < 2; ++pass) {
@@ -118,16 +118,9 @@ int forward_delta_tc(const Call &c, const void *q, const void *k, const void *v,
             float *own_states = cv.take<float>(BH * N * d * d, !states);
             t.states = states ? states : own_states;
         }
-        if (tc) {
-            t.U = cv.take<__nv_bfloat16>(BH * L * d);
-            alpha = cv.take<float>(BH * L);
-            zero = cv.take<float>(BH * L);
-            ones = cv.take<float>(BH * L);
-            tc_scratch = cv.take<char>(tc_scratch_bytes(p));
-        } else if (!one) {
-            t.O_on = cv.take<float>(BH * L * d);
-            r_on = cv.take<float>(BH * L, routed);
-        }
+        t.O_on = cv.take<float>(BH * L * d, !one);
+        tc_scratch = cv.take<char>(tc ? tc_scratch_bytes(p, true) : 0, tc);
+        r_on = cv.take<float>(BH * L, !one && !tc && routed);
         kbar = cv.take<float>(BH * N * d, !one && routed);
         sums = cv.take<float>(BH * N * c.NCH * d, !one && routed);
         if (pass == 0 && scratch_alloc(&scratch, cv.used, s) != cudaSuccess) {
@@ -141,12 +134,11 @@ int forward_delta_tc(const Call &c, const void *q, const void *k, const void *v,
     TcForwardImages img{};
     if (tc) {
         img = tc_forward_images(p, tc_scratch);
-        t.spre_img = img.spre_img;
         t.states_img = img.states_img;
         r_on = img.r_on;
     }
     profile_call_start(s);
-    cudaError_t e = launch_delta_walk_tc(p, t, !tc, s);
+    cudaError_t e = launch_delta_walk_tc(p, t, true, s);
     if (e == cudaSuccess && !one && routed) {
         DeltaArgs a = delta_args(c);
         a.k = k; a.u = f.u;
@@ -154,16 +146,17 @@ int forward_delta_tc(const Call &c, const void *q, const void *k, const void *v,
         profile_after_kernel(s, "pool_simt");
     }
     f.states = t.states;
+    f.O_on = t.O_on;
     if (e == cudaSuccess && tc) {
-        f.v = t.U;
-        f.alpha = alpha; f.beta = zero; f.lam = ones;
-        f.have_images = true;
-        e = launch_delta_scalars(p, la, alpha, zero, ones, s);
-        if (e == cudaSuccess && routed) e = launch_kbar_images(p, kbar, img.kbar_img, s);
-        profile_after_kernel(s, "delta_scalars");
+        f.v = v;
+        f.given = true;
+        if (routed) {
+            e = launch_kbar_images(p, kbar, img.kbar_img, s);
+            profile_after_kernel(s, "kbar_images");
+        }
         if (e == cudaSuccess) e = launch_forward_tc(p, f, tc_scratch, s);
     } else if (e == cudaSuccess && !one) {
-        f.states = t.states; f.O_on = t.O_on; f.r_on = r_on; f.kbar = kbar;
+        f.r_on = r_on; f.kbar = kbar;
         e = launch_readout_simt(p, f, s);
         profile_after_kernel(s, "readout_simt");
     }

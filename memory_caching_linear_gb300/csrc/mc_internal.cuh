@@ -43,8 +43,8 @@ struct FwdArgs {
     float *kbar;                // [BH][N][d]   scratch
     int32_t *sel_out;           // [BH][L][topk] (ssc_select only)
     const float *alpha, *beta, *lam;  // SWLA per-token scalars [BH][L]; all null = plain update
-    bool have_images;           // tensor-core forward: the images and r_on are in the scratch already (v holds what the
-                                // memory wrote), the state kernel is skipped
+    bool given;                 // tensor-core forward: O_on holds the online reads, the images and r_on are in the scratch
+                                // already; the state kernel is skipped
     const int32_t *seg_off;     // optional [N+1] segment boundaries (device); then C is the longest segment
     float *kpre_tiles;          // backward state kernel only: keys before each 64-token tile [BH][N][C/64][d]
     // Optional split of long segments for the FFMA scan (null: one CTA walks a whole segment).
@@ -152,12 +152,11 @@ cudaError_t launch_state_tc_segments(const Problem &p, const FwdArgs &a, const T
                                      cudaStream_t s);
 cudaError_t launch_readout_tc_segments(const Problem &p, const FwdArgs &a, const TcSegTables &tb, void *scratch,
                                        cudaStream_t s);
-size_t tc_scratch_bytes(const Problem &p);
-// Where the forward's readout expects its operands within the scratch (FwdArgs::have_images): the images of the
-// cached states [BH][N] and, decayed by each 128-token chunk's first token, of the states before the chunks
-// [BH][N][C/128] (d x d bf16, 64-column 128-byte-swizzled panels), the key-mean images, and r_on [BH][L].
+size_t tc_scratch_bytes(const Problem &p, bool given = false);
+// Where the forward's readout expects its operands within the scratch (FwdArgs::given): the images of the cached
+// states [BH][N] (d x d bf16, 64-column 128-byte-swizzled panels), the key-mean images, and r_on [BH][L].
 struct TcForwardImages {
-    uint8_t *states_img, *spre_img, *kbar_img;
+    uint8_t *states_img, *kbar_img;
     float *r_on;
 };
 TcForwardImages tc_forward_images(const Problem &p, void *scratch);
@@ -327,10 +326,9 @@ struct DeltaTcArgs {
     __nv_bfloat16 *y;      // online reads in bf16 (one segment), or null
     float *O_on;           // online reads in fp32, or null
     float *states;         // [BH][N][d][d], or null
-    __nv_bfloat16 *U;      // [BH][L][d] beta_t e_t, or null
     __nv_bfloat16 *E;      // [BH][L][d] e_t, or null
     __nv_bfloat16 *S_c;    // [BH][N][NCH][d][d] memory before every chunk, or null
-    uint8_t *spre_img, *states_img;  // the readout's images (tc_forward_images), or null
+    uint8_t *states_img;   // the readout's images (tc_forward_images), or null
     // gradients
     const __nv_bfloat16 *dy, *u;
     uint8_t *rrec;         // [BH][N][NCH] x kDeltaRRecBytes scratch: the reverse walk's record, or null
@@ -352,7 +350,6 @@ cudaError_t launch_delta_dgon(const Problem &p, const void *dy, const void *O, f
 // After the walk with rrec, E and S_c: dv and R_c, then the other gradients.
 cudaError_t launch_delta_grads_tc(const Problem &p, const DeltaTcArgs &a, cudaStream_t s);
 bool delta_tc_supported(const Problem &p);
-cudaError_t launch_delta_scalars(const Problem &p, const void *la, float *alpha, float *zero, float *one, cudaStream_t s);
 // read: q is read and y or O_on written.
 cudaError_t launch_delta_walk_tc(const Problem &p, const DeltaTcArgs &a, bool read, cudaStream_t s);
 

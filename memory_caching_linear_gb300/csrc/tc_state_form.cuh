@@ -73,6 +73,7 @@ struct TcArgs {
     float *kpre_out;      // backward: keys of the segment before each 64-token tile [BH][N][2 CPS][d], or null
     int32_t *sel_out;     // SSC: optional [BH][L][topk] router output (rank order, -1 padded)
     const __nv_bfloat16 *gates;  // gates from HBM (more than 64 segments): [BH][N][L] bf16, or null
+    const float *o_on;    // [BH][L][d] online reads of another memory's own kernels (ON), or null
     int topk;             // SSC: cached segments selected per token
     int mean;             // Mean aggregation: the Residual path with every weight 1 / (n + 1)
     const float *alpha, *beta, *lam;  // SWLA per-token scalars [BH][L] (SWLA kernels only)
@@ -758,20 +759,27 @@ __device__ __forceinline__ TileInfo decode_tile(const TcArgs &a, int id)
     return t;
 }
 
-// Cached operands a tile reads, in order: the chunk's prefix state (c > 0), then
-// the cached states M^(0..n-1) (GRM) or their prefix sum P_n (Residual, n > 0).
-template <bool GATED>
-__device__ __forceinline__ int tile_items(const TileInfo &t)
+// Cached operands a tile reads, in order: the chunk's prefix state (c > 0; not where the
+// online reads are given), then the cached states M^(0..n-1) (GRM) or their prefix sum P_n
+// (Residual, n > 0).
+template <bool ON>
+__device__ __forceinline__ bool has_prefix(const TileInfo &t)
 {
-    return GATED ? t.n + (t.c > 0 ? 1 : 0) : (t.n > 0 ? 1 : 0) + (t.c > 0 ? 1 : 0);
+    return !ON && t.c > 0;
 }
 
-template <bool GATED, bool VAR, int D>
+template <bool GATED, bool ON>
+__device__ __forceinline__ int tile_items(const TileInfo &t)
+{
+    return (GATED ? t.n : t.n > 0 ? 1 : 0) + (has_prefix<ON>(t) ? 1 : 0);
+}
+
+template <bool GATED, bool VAR, int D, bool ON>
 __device__ __forceinline__ const uint8_t *item_image(const TcArgs &a, const TileInfo &t, int k)
 {
     constexpr size_t kImg = D * D * 2;
     const size_t sb = (size_t)t.bh * a.N;
-    if (t.c > 0) {
+    if (has_prefix<ON>(t)) {
         const size_t nch_head = VAR ? (size_t)a.NC : (size_t)a.N * a.CPS;
         if (k == 0) return a.spre_img + ((size_t)t.bh * nch_head + t.cbase + t.c) * kImg;
         --k;
@@ -794,13 +802,19 @@ __device__ __forceinline__ const uint8_t *item_image(const TcArgs &a, const Tile
 // GG: the gates come from HBM (gates[bh][i][t], the online gate at i = n), written by
 // the gate kernel, instead of being formed here from scores in tensor memory; the tile then
 // reads no U or key-mean panels, and any number of cached segments works.
-template <bool GATED, bool DECAY, bool SSC, bool GG = false, bool VAR = false, int D = 128>
+// ON: the online reads M_t q_t come in fp32 (o_on) from a memory whose own kernels formed them, as
+// exactly as it needs; D then takes the cached memories alone (no K, no V, no prefix state), and
+// the drain adds g_n o_on.  16 heads of 65536 tokens, segments of 1024, d = 128: 790 us, 0.54 GB of
+// it the online reads, against 868 where G, P V and the prefix state are formed here.
+template <bool GATED, bool DECAY, bool SSC, bool GG = false, bool VAR = false, int D = 128, bool ON = false>
 __global__ void __launch_bounds__(kT2Threads, kT2CtasPerSm)
     readout_tc(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mU, TcArgs a)
 {
     static_assert(D == 64 || D == 128, "head dimension");
+    static_assert(!ON || (!DECAY && !GG && !VAR), "given online reads");
     constexpr int NP = D / 64;  // 64-column panels of a Q, K, U tile or of an image
+    constexpr int QS = ON ? 1 : 2;  // ring slots from one Q panel to the next
     constexpr uint32_t kImg = D * D * 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = align1024(smem_raw);
@@ -849,11 +863,13 @@ __global__ void __launch_bounds__(kT2Threads, kT2CtasPerSm)
         // ---------------------------------------------------------- TMA producer
         // Panel sequence of a tile: (gated) U0 U1 KBhi KBmid KBlo (gate scores), Q0 K0 Q1 K1
         // (G), V0 V1 (P V), then both K panels of every cached operand.  The workers
-        // release the Q panels.
+        // release the Q panels.  ON: no K and V panels.
         if (lane == 0 && my_tiles > 0) {
             prefetch_tensormap(&mQ);
-            prefetch_tensormap(&mK);
-            prefetch_tensormap(&mV);
+            if (!ON) {
+                prefetch_tensormap(&mK);
+                prefetch_tensormap(&mV);
+            }
             if (GATED && !GG) prefetch_tensormap(&mU);
             uint32_t g = 0;
             bool ok = true;
@@ -866,10 +882,11 @@ __global__ void __launch_bounds__(kT2Threads, kT2CtasPerSm)
             for (int j = 0; j < my_tiles && ok; ++j) {
                 const TileInfo t = decode_tile<VAR>(a, tile_id(j));
                 const int rr = t.bh * a.L + t.off + t.c * kCT;
-                if (((GATED && !GG) || DECAY) && j + 1 < my_tiles) {  // rows the workers read directly
+                if (((GATED && !GG) || DECAY || ON) && j + 1 < my_tiles) {  // rows the workers read directly
                     const TileInfo tn = decode_tile<VAR>(a, tile_id(j + 1));
                     const size_t tn_id = ((size_t)tn.bh * a.L + (size_t)tn.off + (size_t)tn.c * kCT) / kCT;
                     if (GATED && !GG) prefetch_l2(a.r_on + tn_id * kCT, kCT * 4);
+                    if (ON) prefetch_l2(a.o_on + tn_id * kCT * D, kCT * D * 4);
                     if (DECAY) {
                         prefetch_l2(a.alpha + tn_id * kCT, kCT * 4);
                         prefetch_l2(a.beta + tn_id * kCT, kCT * 4);
@@ -897,11 +914,13 @@ __global__ void __launch_bounds__(kT2Threads, kT2CtasPerSm)
                     if (!(ok = (dst = slot(kPanel)) != nullptr)) break;
                     tma_load_2d(dst, &mQ, 64 * h, rr, &ring_full[g % kRing]);
                     ++g;
+                    if (ON) continue;
                     if (!(ok = (dst = slot(kPanel)) != nullptr)) break;
                     tma_load_2d(dst, &mK, 64 * h, rr, &ring_full[g % kRing]);
                     ++g;
                 }
-                if (D == 128) {
+                if (ON) {
+                } else if (D == 128) {
                     for (int h = 0; h < 2 && ok; ++h) {  // keys 64h .. 64h + 63, both 64-wide halves of v
                         if (!(ok = (dst = slot(kPanel)) != nullptr)) break;
                         tma_load_2d(dst, &mV, 0, rr + 64 * h, &ring_full[g % kRing]);
@@ -915,9 +934,9 @@ __global__ void __launch_bounds__(kT2Threads, kT2CtasPerSm)
                         ++g;
                     }
                 }
-                const int items = tile_items<GATED>(t);
+                const int items = tile_items<GATED, ON>(t);
                 for (int k = 0; k < items && ok; ++k) {
-                    const uint8_t *src = item_image<GATED, VAR, D>(a, t, k);
+                    const uint8_t *src = item_image<GATED, VAR, D, ON>(a, t, k);
                     for (int h = 0; h < NP && ok; ++h) {
                         if (!(ok = (dst = slot(kImg / NP)) != nullptr)) break;
                         bulk_load(dst, src + h * (kImg / NP), kImg / NP, &ring_full[g % kRing]);
@@ -971,6 +990,9 @@ __global__ void __launch_bounds__(kT2Threads, kT2CtasPerSm)
                     g += NP + 3;
                 }
                 if (!(ok = mbar_wait(&y_empty, (j & 1) ^ 1, &abort_flag))) break;  // D of tile j-1 drained
+                if (ON) {
+                    g += NP;  // the Q panels, released by the workers
+                } else {
                 // G = Q K^T
                 for (int h = 0; h < NP; ++h) {
                     const uint32_t sq = g % kRing, sk = (g + 1) % kRing;
@@ -1002,8 +1024,9 @@ __global__ void __launch_bounds__(kT2Threads, kT2CtasPerSm)
                 if (!ok) break;
                 mma_commit(&a_empty[ps]);
                 ++ac;
+                }
                 // D += (g_i o Q) X_i^T
-                const int items = tile_items<GATED>(t);
+                const int items = tile_items<GATED, ON>(t);
                 for (int k = 0; k < items && ok; ++k) {
                     const uint32_t as = ac % 2;
                     if (!(ok = mbar_wait(&a_full[as], (ac / 2) & 1, &abort_flag))) break;
@@ -1013,7 +1036,7 @@ __global__ void __launch_bounds__(kT2Threads, kT2CtasPerSm)
                         tc_fence_after();
                         const uint64_t db = make_desc_sw128(s_base + s * kPanel, 0, 1024);
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) mma_ts(tD, tA0 + as * 64 + (4 * h + kk) * 8, db + 2 * kk, idX, 1);
+                        for (int kk = 0; kk < 4; ++kk) mma_ts(tD, tA0 + as * 64 + (4 * h + kk) * 8, db + 2 * kk, idX, !ON || (k | h | kk) != 0);
                         mma_commit(&ring_empty[s]);
                         ++g;
                     }
@@ -1053,7 +1076,7 @@ __global__ void __launch_bounds__(kT2Threads, kT2CtasPerSm)
         float *dsm = reinterpret_cast<float *>(sm + kRing * kPanel) + q4 * 5 * kCT;  // SWLA: ell | lambda | beta_{j+1} | E | F
         for (int j = 0; j < my_tiles && ok; ++j) {
             const TileInfo t = decode_tile<VAR>(a, tile_id(j));
-            const int items = tile_items<GATED>(t);
+            const int items = tile_items<GATED, ON>(t);
             float gn = a.mean ? 1.f / (float)(t.n + 1) : 1.f;  // Residual: 1
             // GG: this token's gates in HBM, gcol[i L] for memory i (the online one at i = n)
             const __nv_bfloat16 *gcol =
@@ -1081,7 +1104,7 @@ __global__ void __launch_bounds__(kT2Threads, kT2CtasPerSm)
                 const float inv = token_gates<SSC>(sc, t.n, ron, a.topk, nullptr);
 #pragma unroll
                 for (int k = 0; k < 32; ++k) gm2[k] = pack_bf16x2(sc[2 * k] * inv, sc[2 * k + 1] * inv);
-                gn = __bfloat162float(__high2bfloat16(*reinterpret_cast<const __nv_bfloat162 *>(&gm2[31])));
+                gn = ON ? sc[63] * inv : __bfloat162float(__high2bfloat16(*reinterpret_cast<const __nv_bfloat162 *>(&gm2[31])));
             }
             float ellt = 0.f;  // SWLA: log of A(t_c, t) for this token row
             if (DECAY) {
@@ -1111,11 +1134,11 @@ __global__ void __launch_bounds__(kT2Threads, kT2CtasPerSm)
             // row r sits at chunk c ^ (r % 8)), read while G runs
             uint32_t qp[32 * NP];
             if (!(ok = mbar_wait(&ring_full[g % kRing], (g / kRing) & 1, &abort_flag) &&
-                       (NP == 1 || mbar_wait(&ring_full[(g + 2) % kRing], ((g + 2) / kRing) & 1, &abort_flag))))
+                       (NP == 1 || mbar_wait(&ring_full[(g + QS) % kRing], ((g + QS) / kRing) & 1, &abort_flag))))
                 break;
 #pragma unroll
             for (int h = 0; h < NP; ++h) {
-                const uint8_t *pq = sm + ((g + 2 * h) % kRing) * kPanel + row * 128;
+                const uint8_t *pq = sm + ((g + QS * h) % kRing) * kPanel + row * 128;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     const uint4 x = *reinterpret_cast<const uint4 *>(pq + ((c ^ (row & 7)) << 4));
@@ -1126,16 +1149,18 @@ __global__ void __launch_bounds__(kT2Threads, kT2CtasPerSm)
                 }
             }
             mbar_arrive(&q_read);
-            if (!(ok = mbar_wait(&g_full, j & 1, &abort_flag))) break;
-            tc_fence_after();
+            if (!ON) {
+                if (!(ok = mbar_wait(&g_full, j & 1, &abort_flag))) break;
+                tc_fence_after();
+            }
             if (leader) {  // G and every worker are done with the Q panels
                 if (!(ok = mbar_wait(&q_read, j & 1, &abort_flag))) break;
                 mbar_arrive(&ring_empty[g % kRing]);
-                if (NP == 2) mbar_arrive(&ring_empty[(g + 2) % kRing]);
+                if (NP == 2) mbar_arrive(&ring_empty[(g + QS) % kRing]);
             }
             // P = g_n * mask(G), key column c <= token row
-            if (!(ok = claim())) break;
-            {
+            if (!ON) {
+                if (!(ok = claim())) break;
                 const uint32_t ta = tA0 + (ac % 2) * 64 + lane_base;
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
@@ -1188,8 +1213,8 @@ __global__ void __launch_bounds__(kT2Threads, kT2CtasPerSm)
                     }
                     tmem_st16(ta + 16 * h, o);
                 }
+                publish();
             }
-            publish();
             // cached operands: g_i o Q
             const __nv_bfloat16 *gl = reinterpret_cast<const __nv_bfloat16 *>(gm2);
             // GG: item k's gate from HBM, loaded one item ahead
@@ -1201,12 +1226,12 @@ __global__ void __launch_bounds__(kT2Threads, kT2CtasPerSm)
 #pragma unroll 1
             for (int k = 0; k < items; ++k) {
                 __nv_bfloat162 gam2 = __float2bfloat162_rn(gn);  // Residual: 1, Mean: 1 / (n + 1)
-                const bool prefix = t.c > 0 && k == 0;  // item 0 of a chunk c > 0 is its prefix state (gate g_n)
+                const bool prefix = has_prefix<ON>(t) && k == 0;  // item 0 of a chunk c > 0 is its prefix state (gate g_n)
                 if (GG) {
                     gam2 = __bfloat162bfloat162(gnext);
                     if (k + 1 < items) gnext = item_gate(k + 1);
                 } else if (GATED) {
-                    const int i = t.c > 0 ? k - 1 : k;
+                    const int i = has_prefix<ON>(t) ? k - 1 : k;
                     gam2 = __bfloat162bfloat162(i < 0 ? __float2bfloat16_rn(gn) : gl[i]);
                 }
                 if (DECAY && prefix) gam2 = __float2bfloat162_rn(gn * __expf(ellt));  // A(t_c, t) S^_c q_t
@@ -1231,10 +1256,21 @@ __global__ void __launch_bounds__(kT2Threads, kT2CtasPerSm)
                 publish();
             }
             if (!ok) break;
-            g += NP * (3 + items);  // Q, K, V and the cached operands
+            g += NP * ((ON ? 1 : 3) + items);  // Q, (K, V) and the cached operands
             // drain: read D in the 16x256b layout (a quad of threads holds 8 consecutive
             // columns of a row), release it, then transpose within each quad by shuffles
             // so that every thread stores 16 contiguous bytes: 8 rows x 64 bytes per store
+            // ON: the quad's columns of the online reads (whole 32-byte sectors), the first ones under way with the MMAs
+            const float *ot = ON ? a.o_on + ((size_t)t.bh * a.L + (size_t)t.off + (size_t)t.c * kCT + 32 * q4 + (lane >> 2)) * D + 2 * (lane & 3) : nullptr;
+            float2 oa[ON ? 8 : 1], ob[ON ? 8 : 1];
+            auto fetch = [&](int hl, int ch) {
+#pragma unroll
+                for (int b = 0; b < (ON ? 8 : 0); ++b) {
+                    oa[b] = __ldcs(reinterpret_cast<const float2 *>(ot + (16 * hl) * D + 64 * ch + 8 * b));
+                    ob[b] = __ldcs(reinterpret_cast<const float2 *>(ot + (16 * hl + 8) * D + 64 * ch + 8 * b));
+                }
+            };
+            fetch(0, 0);
             if (!(ok = mbar_wait(&y_full, j & 1, &abort_flag))) break;
             tc_fence_after();
             uint32_t yb[64];  // [lane half][column half]: 8 pairs of row A, then 8 of row B
@@ -1245,6 +1281,21 @@ __global__ void __launch_bounds__(kT2Threads, kT2CtasPerSm)
                     uint32_t x[32];
                     tmem_ld_16x256b_x8(tD + ((uint32_t)(32 * q4 + 16 * hl) << 16) + 64 * ch, x);
                     tmem_wait_ld();
+                    if (ON) {
+                        const float ga = __shfl_sync(0xffffffffu, gn, 16 * hl + (lane >> 2));
+                        const float gb = __shfl_sync(0xffffffffu, gn, 16 * hl + 8 + (lane >> 2));
+#pragma unroll
+                        for (int b = 0; b < (ON ? 8 : 0); ++b) {  // (nothing was accumulated for a first segment's tile)
+                            const float z[4] = {items > 0 ? __uint_as_float(x[4 * b]) : 0.f, items > 0 ? __uint_as_float(x[4 * b + 1]) : 0.f,
+                                                items > 0 ? __uint_as_float(x[4 * b + 2]) : 0.f, items > 0 ? __uint_as_float(x[4 * b + 3]) : 0.f};
+                            x[4 * b] = __float_as_uint(fmaf(ga, oa[b].x, z[0]));
+                            x[4 * b + 1] = __float_as_uint(fmaf(ga, oa[b].y, z[1]));
+                            x[4 * b + 2] = __float_as_uint(fmaf(gb, ob[b].x, z[2]));
+                            x[4 * b + 3] = __float_as_uint(fmaf(gb, ob[b].y, z[3]));
+                        }
+                        if (ch + 1 < NP) fetch(hl, ch + 1);
+                        else if (hl == 0) fetch(1, 0);
+                    }
 #pragma unroll
                     for (int b = 0; b < 8; ++b) {
                         yb[16 * (2 * hl + ch) + b] = pack_bf16x2(__uint_as_float(x[4 * b]), __uint_as_float(x[4 * b + 1]));
@@ -1303,9 +1354,10 @@ inline size_t img_bytes(const Problem &p) { return (size_t)p.d * p.d * 2; }
 // Scratch of the forward over constant segments: state images [BH][N], prefix-state
 // images [BH][N][CPS], key-mean images [BH][NB], r_on [BH][L], then the prefix sums of
 // the states [BH][N] (Residual / Mean) or the gates [BH][N][L] bf16 (more than 64 segments).
-inline size_t forward_scratch_bytes(const Problem &p)
+// With given online reads there are no prefix-state images.
+inline size_t forward_scratch_bytes(const Problem &p, bool given)
 {
-    const size_t BH = p.BH, N = p.N, CPS = p.C / kCT, NB = (N + 63) / 64, im = img_bytes(p);
+    const size_t BH = p.BH, N = p.N, CPS = given ? 0 : p.C / kCT, NB = (N + 63) / 64, im = img_bytes(p);
     size_t b = pad256(BH * N * im) + pad256(BH * N * CPS * im) + pad256(BH * NB * kKbImg) +
                pad256(sizeof(float) * BH * p.L);
     if (!mode_uses_u(p.mode)) b += pad256(BH * N * im);
@@ -1343,7 +1395,8 @@ cudaError_t forward_impl(const Problem &p, const FwdArgs &fa, void *scratch, cud
     a.states_img = base;
     base += pad256(BH * N * im);
     a.spre_img = base;
-    base += pad256(BH * N * CPS * im);
+    a.o_on = fa.given ? fa.O_on : nullptr;
+    if (!fa.given) base += pad256(BH * N * CPS * im);
     a.kbar_img = base;
     base += pad256(BH * ((N + 63) / 64) * kKbImg);
     a.r_on = reinterpret_cast<float *>(base);
@@ -1378,12 +1431,12 @@ cudaError_t forward_impl(const Problem &p, const FwdArgs &fa, void *scratch, cud
     const int sms = sm_count();
     cudaError_t e;
 
-    profile_call_start(s);
+    if (!fa.given) profile_call_start(s);
     const bool decay = fa.alpha != nullptr;
     a.alpha = fa.alpha;
     a.beta = fa.beta;
     a.lam = fa.lam;
-    if (!fa.have_images) {
+    if (!fa.given) {
         auto k1 = gated ? (decay ? seg_state_tc<true, true, false, D> : seg_state_tc<true, false, false, D>)
                         : (decay ? seg_state_tc<false, true, false, D> : seg_state_tc<false, false, false, D>);
         const size_t smem1 = decay ? t1_smem_bytes<true, D>() : t1_smem_bytes<false, D>();
@@ -1407,7 +1460,10 @@ cudaError_t forward_impl(const Problem &p, const FwdArgs &fa, void *scratch, cud
     }
     {
         const bool ssc = p.mode == MC_SSC;
-        auto k2 = !gated ? (decay ? readout_tc<false, true, false, false, false, D> : readout_tc<false, false, false, false, false, D>)
+        auto k2 = fa.given ? (!gated ? readout_tc<false, false, false, false, false, D, true>
+                              : ssc  ? readout_tc<true, false, true, false, false, D, true>
+                                     : readout_tc<true, false, false, false, false, D, true>)
+                  : !gated ? (decay ? readout_tc<false, true, false, false, false, D> : readout_tc<false, false, false, false, false, D>)
                   : gg   ? (ssc ? readout_tc<true, false, true, true, false, D> : readout_tc<true, false, false, true, false, D>)
                   : ssc  ? (decay ? readout_tc<true, true, true, false, false, D> : readout_tc<true, false, true, false, false, D>)
                          : (decay ? readout_tc<true, true, false, false, false, D> : readout_tc<true, false, false, false, false, D>);

@@ -59,3 +59,23 @@ def test_fp32_gradients_after_many_resets(d, C, L, mode, resets):
     for name, g, w in zip(NAMES, mcl.mc_backward_delta(*cuda(x), dy.cuda(), C, mode), backward(*floor, dy, C, mode)):
         if g is not None:
             assert rel(g, w) <= TOL["f32"], name
+
+
+def resembling(L, d, spread, beta, seed=71):
+    """Neighbouring keys that share one direction: every write undoes the one before, so what a chunk writes is of the size of
+    the result and cancels."""
+    q, k, v, u, la, be = make_delta_inputs(1, 2, L, d, 128, seed, "bf16", decay=0.001)
+    k = k.float() * spread + k[:, :, :1].float()
+    return [q, (k / k.norm(dim=-1, keepdim=True)).to(q.dtype), v, u, la, torch.full_like(be, beta)]
+
+
+@pytest.mark.parametrize("mode,topk", [(RESIDUAL, 0), (GRM, 0), (SSC, 1), (MEAN, 0)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("spread,beta", [(0.05, 1.0), (0.05, 1.9), (0.3, 1.9)])
+@pytest.mark.parametrize("C,L", [(128, 384), (130, 384), (192, 384), (384, 384), (128, 380)])
+def test_reads_of_resembling_keys(C, L, spread, beta, d, mode, topk):
+    """y is as exact for one segment length as for another: whatever kernels read the cached memories, the online read is
+    formed in two bf16 terms, 2^-17 of the terms that cancel, and what remains of the 1e-2 are roundings of results."""
+    x = resembling(L, d, spread, beta)
+    y, _ = forward(*x, C, mode, topk)
+    assert rel(mcl.mc_forward_delta(*cuda(x), C, mode, topk)[0], y) <= TOL["bf16"]
