@@ -306,7 +306,8 @@ int mc_decode_step_evict(const void *q, const void *k, const void *v, const void
  *   prefill_mass   : fp32 [B][H][N], every segment's mass (0 for the last one); may be NULL.
  *   agg_mode, topk : the prefill's; MC_GRM, MC_SOUP or MC_SSC, else MC_ERR_MODE.
  *   protect        : 0 .. n_max; n_max: 1 .. 64.
- *   The cache shares no memory with the prefill's states.  Errors as mc_forward.
+ *   The cache shares no memory with the prefill's states.  Errors as mc_forward.  Scratch: at most
+ *   about twice the prefill's states, and a float per token.
  */
 int mc_cache_compact(const void *k, const void *u, const float *prefill_states, int B, int H, int L,
                      int d, int seg_len, int agg_mode, int topk, int protect, float *states,

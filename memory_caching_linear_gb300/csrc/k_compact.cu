@@ -10,7 +10,10 @@
 // Kernels: the pooled-key sums (k_delta_simt.cu), gate_mass (per tile of 64 or 128 tokens, the gates and their
 // sums over the tile's tokens), mass_reduce (the tiles' sums in a fixed order), compact_select (per head, the
 // ranking), compact_gather (copies, bound by HBM).  Partial sums instead of atomics keep the mass,
-// and with it the choice, the same from run to run.
+// and with it the choice, the same from run to run.  A head has at most 512 of them (and no more than a state has
+// numbers): row r of `part` takes tile tiles - shares + r and every shares-th one before it, summed in that order, so the
+// scratch grows with the number of segments alone; up to 32768 tokens (65536 in gate_mass_tc; half of that
+// for d = 16) a row is a tile.
 #include <cfloat>
 #include <cstdint>
 
@@ -36,110 +39,118 @@ __global__ void __launch_bounds__(kMThreads) gate_mass_simt(CompactArgs a)
     int *thi = reinterpret_cast<int *>(thr + kMT), *nsel = thi + kMT;
     float *selv = reinterpret_cast<float *>(nsel + kMT);            // SSC: kMT x topk
     int *seli = reinterpret_cast<int *>(selv + (size_t)kMT * a.topk);
-    const int tile = (int)blockIdx.x % a.tiles, bh = (int)blockIdx.x / a.tiles;
-    const int tb = tile * kMT, cnt = min(kMT, a.L - tb);
-    const int smax = (tb + cnt - 1) / a.C;  // the newest segment in the tile: segments before it are read
+    const int last = a.tiles - a.shares + (int)blockIdx.x % a.shares, bh = (int)blockIdx.x / a.shares;
     const size_t base = (size_t)bh * a.L * D;
     const T *u = static_cast<const T *>(a.u) + base;
     const float *kbar = a.kbar_all + (size_t)bh * a.N * D;
     float *out = a.part + (size_t)blockIdx.x * a.N;
     const int tid = threadIdx.x;
-    for (int e = tid; e < kMT * D; e += kMThreads)
-        Us[(e / D) * P + e % D] = e / D < cnt ? to_f(u[(size_t)tb * D + e]) : 0.f;
-    const bool ssc = a.mode == MC_SSC;
-    if (tid < kMT) {
-        mx[tid] = tid < cnt ? a.r_on[(size_t)bh * a.L + tb + tid] : 0.f;
-        zs[tid] = 1.f;
-        nsel[tid] = 0;
-    }
-    // Four tokens (tx + 16 x) by four segments (ty + 16 y) per thread, each score in gate_score's order of sums, so that
-    // the router ranks as everywhere else.  Columns past the last segment that the tile reads are left out.
-    auto scores = [&](int s0) {
+    for (int tile = last; tile >= 0; tile -= a.shares) {
+        const bool first = tile == last;  // (a tile reads no segment that a later one does not)
+        const int tb = tile * kMT, cnt = min(kMT, a.L - tb);
+        const int smax = (tb + cnt - 1) / a.C;  // the newest segment in the tile: segments before it are read
         __syncthreads();
-        for (int e = tid; e < kMS * D; e += kMThreads)
-            Kb[(e / D) * P + e % D] = s0 + e / D < smax ? kbar[(size_t)s0 * D + e] : 0.f;
-        __syncthreads();
-        const int tx = tid % 16, ty = tid / 16;
-#pragma unroll 1
-        for (int y = 0; y < 4; ++y) {
-            const int i = ty + 16 * y;
-            if (s0 + 16 * y >= smax) break;
-            float p[4][4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) p[x][0] = p[x][1] = p[x][2] = p[x][3] = 0.f;
-#pragma unroll 4
-            for (int c = 0; c < D; c += 4) {
-                const float4 kv = *reinterpret_cast<const float4 *>(Kb + i * P + c);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const float4 uv = *reinterpret_cast<const float4 *>(Us + (tx + 16 * x) * P + c);
-                    p[x][0] = fmaf(uv.x, kv.x, p[x][0]);
-                    p[x][1] = fmaf(uv.y, kv.y, p[x][1]);
-                    p[x][2] = fmaf(uv.z, kv.z, p[x][2]);
-                    p[x][3] = fmaf(uv.w, kv.w, p[x][3]);
-                }
-            }
-#pragma unroll
-            for (int x = 0; x < 4; ++x) Sc[(tx + 16 * x) * (kMS + 1) + i] = (p[x][0] + p[x][1]) + (p[x][2] + p[x][3]);
+        for (int e = tid; e < kMT * D; e += kMThreads)
+            Us[(e / D) * P + e % D] = e / D < cnt ? to_f(u[(size_t)tb * D + e]) : 0.f;
+        const bool ssc = a.mode == MC_SSC;
+        if (tid < kMT) {
+            mx[tid] = tid < cnt ? a.r_on[(size_t)bh * a.L + tb + tid] : 0.f;
+            zs[tid] = 1.f;
+            nsel[tid] = 0;
         }
-        __syncthreads();
-    };
-    for (int s0 = 0; s0 < smax; s0 += kMS) {
-        scores(s0);
-        if (tid < cnt) {
-            const int n = min((tb + tid) / a.C - s0, kMS);  // cached segments of this token in the block
-            if (ssc) {
-                int c = nsel[tid];
-                for (int i = 0; i < n; ++i)
-                    topk_insert(selv + (size_t)tid * a.topk, seli + (size_t)tid * a.topk, c, a.topk, Sc[tid * (kMS + 1) + i], s0 + i);
-                nsel[tid] = c;
-            } else {
-                float m = mx[tid], z = zs[tid];
-                for (int i = 0; i < n; ++i) {
-                    const float r = Sc[tid * (kMS + 1) + i];
-                    if (r > m) {
-                        z = z * expf(m - r) + 1.f;
-                        m = r;
-                    } else {
-                        z += expf(r - m);
+        // Four tokens (tx + 16 x) by four segments (ty + 16 y) per thread, each score in gate_score's order of sums, so that
+        // the router ranks as everywhere else.  Columns past the last segment that the tile reads are left out.
+        auto scores = [&](int s0) {
+            __syncthreads();
+            for (int e = tid; e < kMS * D; e += kMThreads)
+                Kb[(e / D) * P + e % D] = s0 + e / D < smax ? kbar[(size_t)s0 * D + e] : 0.f;
+            __syncthreads();
+            const int tx = tid % 16, ty = tid / 16;
+#pragma unroll 1
+            for (int y = 0; y < 4; ++y) {
+                const int i = ty + 16 * y;
+                if (s0 + 16 * y >= smax) break;
+                float p[4][4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) p[x][0] = p[x][1] = p[x][2] = p[x][3] = 0.f;
+#pragma unroll 4
+                for (int c = 0; c < D; c += 4) {
+                    const float4 kv = *reinterpret_cast<const float4 *>(Kb + i * P + c);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const float4 uv = *reinterpret_cast<const float4 *>(Us + (tx + 16 * x) * P + c);
+                        p[x][0] = fmaf(uv.x, kv.x, p[x][0]);
+                        p[x][1] = fmaf(uv.y, kv.y, p[x][1]);
+                        p[x][2] = fmaf(uv.z, kv.z, p[x][2]);
+                        p[x][3] = fmaf(uv.w, kv.w, p[x][3]);
                     }
                 }
-                mx[tid] = m;
-                zs[tid] = z;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) Sc[(tx + 16 * x) * (kMS + 1) + i] = (p[x][0] + p[x][1]) + (p[x][2] + p[x][3]);
+            }
+            __syncthreads();
+        };
+        for (int s0 = 0; s0 < smax; s0 += kMS) {
+            scores(s0);
+            if (tid < cnt) {
+                const int n = min((tb + tid) / a.C - s0, kMS);  // cached segments of this token in the block
+                if (ssc) {
+                    int c = nsel[tid];
+                    for (int i = 0; i < n; ++i)
+                        topk_insert(selv + (size_t)tid * a.topk, seli + (size_t)tid * a.topk, c, a.topk, Sc[tid * (kMS + 1) + i], s0 + i);
+                    nsel[tid] = c;
+                } else {
+                    float m = mx[tid], z = zs[tid];
+                    for (int i = 0; i < n; ++i) {
+                        const float r = Sc[tid * (kMS + 1) + i];
+                        if (r > m) {
+                            z = z * expf(m - r) + 1.f;
+                            m = r;
+                        } else {
+                            z += expf(r - m);
+                        }
+                    }
+                    mx[tid] = m;
+                    zs[tid] = z;
+                }
             }
         }
-    }
-    if (ssc && tid < cnt) {
-        const float ron = mx[tid];
-        const int c = nsel[tid];
-        const float *vals = selv + (size_t)tid * a.topk;
-        float m = ron;
-        if (c > 0) m = fmaxf(m, vals[0]);
-        float z = expf(ron - m);
-        for (int i = 0; i < c; ++i) z += expf(vals[i] - m);
-        mx[tid] = m;
-        zs[tid] = z;
-        thr[tid] = c > 0 ? vals[c - 1] : FLT_MAX;  // a segment is selected if its score is above the last one's,
-        thi[tid] = c > 0 ? seli[(size_t)tid * a.topk + c - 1] : -1;  // or equal with an index up to it
-    }
-    __shared__ float part[4][kMS];
-    for (int s0 = 0; s0 < smax; s0 += kMS) {
-        if (smax > kMS) scores(s0);  // a single block's scores are still there
-        else __syncthreads();
-        const int q = tid / kMS, i = s0 + tid % kMS;  // a quarter of the tokens
-        float sum = 0.f;
-        if (i < smax)
-            for (int t = q * (kMT / 4); t < min(cnt, (q + 1) * (kMT / 4)); ++t) {
-                if (i >= (tb + t) / a.C) continue;
-                const float r = Sc[t * (kMS + 1) + tid % kMS];
-                if (ssc && !(r > thr[t] || (r == thr[t] && i <= thi[t]))) continue;
-                sum += expf(r - mx[t]) / zs[t];
+        if (ssc && tid < cnt) {
+            const float ron = mx[tid];
+            const int c = nsel[tid];
+            const float *vals = selv + (size_t)tid * a.topk;
+            float m = ron;
+            if (c > 0) m = fmaxf(m, vals[0]);
+            float z = expf(ron - m);
+            for (int i = 0; i < c; ++i) z += expf(vals[i] - m);
+            mx[tid] = m;
+            zs[tid] = z;
+            thr[tid] = c > 0 ? vals[c - 1] : FLT_MAX;  // a segment is selected if its score is above the last one's,
+            thi[tid] = c > 0 ? seli[(size_t)tid * a.topk + c - 1] : -1;  // or equal with an index up to it
+        }
+        __shared__ float part[4][kMS];
+        for (int s0 = 0; s0 < smax; s0 += kMS) {
+            if (smax > kMS) scores(s0);  // a single block's scores are still there
+            else __syncthreads();
+            const int q = tid / kMS, i = s0 + tid % kMS;  // a quarter of the tokens
+            float sum = 0.f;
+            if (i < smax)
+                for (int t = q * (kMT / 4); t < min(cnt, (q + 1) * (kMT / 4)); ++t) {
+                    if (i >= (tb + t) / a.C) continue;
+                    const float r = Sc[t * (kMS + 1) + tid % kMS];
+                    if (ssc && !(r > thr[t] || (r == thr[t] && i <= thi[t]))) continue;
+                    sum += expf(r - mx[t]) / zs[t];
+                }
+            part[q][tid % kMS] = sum;
+            __syncthreads();
+            if (tid < kMS && s0 + tid < a.N) {
+                const float x = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
+                out[s0 + tid] = first ? x : out[s0 + tid] + x;
             }
-        part[q][tid % kMS] = sum;
-        __syncthreads();
-        if (tid < kMS && s0 + tid < a.N) out[s0 + tid] = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
+        }
+        if (first)
+            for (int i = ((smax + kMS - 1) / kMS) * kMS + tid; i < a.N; i += kMThreads) out[i] = 0.f;
     }
-    for (int i = ((smax + kMS - 1) / kMS) * kMS + tid; i < a.N; i += kMThreads) out[i] = 0.f;
 }
 
 // ---------------------------------------------------------------------------
@@ -170,154 +181,159 @@ __global__ void __launch_bounds__(256, 2) gate_mass_tc(CompactArgs a)
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t *Ut = smem_raw, *Kt = smem_raw + kTM * UR;
     __shared__ float cols[8][32];
-    const int tile = a.tiles - 1 - (int)(blockIdx.x / a.BH), bh = (int)(blockIdx.x % a.BH);  // the longest first
-    const int tb = tile * kTM, cnt = min(kTM, a.L - tb);
-    const int smax = (tb + cnt - 1) / a.C, nh = (smax + 31) / 32;
+    const int row = a.shares - 1 - (int)(blockIdx.x / a.BH), bh = (int)(blockIdx.x % a.BH);  // the longest first
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, c = lane % 4;
-    const size_t row0 = (size_t)bh * a.L + tb;
     const __nv_bfloat16 *u = static_cast<const __nv_bfloat16 *>(a.u);
-    float *out = a.part + ((size_t)bh * a.tiles + tile) * a.N;
-    for (int i = nh * 32 + tid; i < a.N; i += 256) out[i] = 0.f;
-    if (nh == 0) return;
-    const uint8_t *img = a.kbar_img + (size_t)bh * ((a.N + 63) / 64) * 49152;
-    int it = 0;  // loads so far: half h goes to buffer it % 2
-    auto issue = [&](int h) {
-        const uint32_t dst = smem_addr(Kt) + (it & 1) * M::kHalf;
-        const uint8_t *src = img + (size_t)(h / 2) * 49152 + (h & 1) * 32 * 128;
-        for (int e = tid; e < 3 * PN * 256; e += 256) {
-            const int tp = e / 256, r = e % 256;  // term and panel; 16-byte piece
-            cp16(dst + e * 16, src + (tp / PN) * 16384 + (tp % PN) * 8192 + r * 16, true);
+    float *out = a.part + ((size_t)bh * a.shares + row) * a.N;
+    for (int tile = a.tiles - a.shares + row; tile >= 0; tile -= a.shares) {
+        const bool first = tile == a.tiles - a.shares + row;  // (a tile reads no segment that a later one does not)
+        const int tb = tile * kTM, cnt = min(kTM, a.L - tb);
+        const int smax = (tb + cnt - 1) / a.C, nh = (smax + 31) / 32;
+        const size_t row0 = (size_t)bh * a.L + tb;
+        if (first)
+            for (int i = nh * 32 + tid; i < a.N; i += 256) out[i] = 0.f;
+        if (nh == 0) break;  // (nor do the tiles before it read any)
+        if (!first) __syncthreads();
+        const uint8_t *img = a.kbar_img + (size_t)bh * ((a.N + 63) / 64) * 49152;
+        int it = 0;  // loads so far: half h goes to buffer it % 2
+        auto issue = [&](int h) {
+            const uint32_t dst = smem_addr(Kt) + (it & 1) * M::kHalf;
+            const uint8_t *src = img + (size_t)(h / 2) * 49152 + (h & 1) * 32 * 128;
+            for (int e = tid; e < 3 * PN * 256; e += 256) {
+                const int tp = e / 256, r = e % 256;  // term and panel; 16-byte piece
+                cp16(dst + e * 16, src + (tp / PN) * 16384 + (tp % PN) * 8192 + r * 16, true);
+            }
+            cp_commit();
+            ++it;
+        };
+        for (int e = tid; e < kTM * (D / 8); e += 256) {
+            const int r = e / (D / 8), pc = e % (D / 8);
+            cp16(smem_addr(Ut) + tile_off<UR>(r, pc), u + (row0 + (r < cnt ? r : 0)) * D + pc * 8, r < cnt);
         }
-        cp_commit();
-        ++it;
-    };
-    for (int e = tid; e < kTM * (D / 8); e += 256) {
-        const int r = e / (D / 8), pc = e % (D / 8);
-        cp16(smem_addr(Ut) + tile_off<UR>(r, pc), u + (row0 + (r < cnt ? r : 0)) * D + pc * 8, r < cnt);
-    }
-    issue(0);
-    // rows g and g + 8 of the warp's tokens: cached segments, online score
-    const int t0 = 16 * warp + g, t1 = t0 + 8;
-    const int lim0 = t0 < cnt ? (tb + t0) / a.C : 0, lim1 = t1 < cnt ? (tb + t1) / a.C : 0;
-    float m0 = t0 < cnt ? a.r_on[row0 + t0] : 0.f, m1 = t1 < cnt ? a.r_on[row0 + t1] : 0.f, z0 = c == 0 ? 1.f : 0.f, z1 = z0;
-    uint32_t au[KS][4];
+        issue(0);
+        // rows g and g + 8 of the warp's tokens: cached segments, online score
+        const int t0 = 16 * warp + g, t1 = t0 + 8;
+        const int lim0 = t0 < cnt ? (tb + t0) / a.C : 0, lim1 = t1 < cnt ? (tb + t1) / a.C : 0;
+        float m0 = t0 < cnt ? a.r_on[row0 + t0] : 0.f, m1 = t1 < cnt ? a.r_on[row0 + t1] : 0.f, z0 = c == 0 ? 1.f : 0.f, z1 = z0;
+        uint32_t au[KS][4];
 
-    // Half h's scores, -inf where a token does not read the segment; `next` is loaded meanwhile (-1: nothing).
-    auto scores = [&](int h, int next, float (&S)[4][4]) {
-        cp_wait<0>();
-        __syncthreads();  // the half has come, and the other buffer has been read
-        const uint32_t kt = smem_addr(Kt) + ((it - 1) & 1) * M::kHalf;
-        if (it == 1) {
+        // Half h's scores, -inf where a token does not read the segment; `next` is loaded meanwhile (-1: nothing).
+        auto scores = [&](int h, int next, float (&S)[4][4]) {
+            cp_wait<0>();
+            __syncthreads();  // the half has come, and the other buffer has been read
+            const uint32_t kt = smem_addr(Kt) + ((it - 1) & 1) * M::kHalf;
+            if (it == 1) {
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-                ldsm4(au[ks], smem_addr(Ut) + tile_off<UR>(16 * warp + (lane & 15), 2 * ks + (lane >> 4)));
-        }
-        if (next >= 0) issue(next);
+                for (int ks = 0; ks < KS; ++ks)
+                    ldsm4(au[ks], smem_addr(Ut) + tile_off<UR>(16 * warp + (lane & 15), 2 * ks + (lane >> 4)));
+            }
+            if (next >= 0) issue(next);
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+            for (int n = 0; n < 4; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) S[n][e] = 0.f;
-        const int br = (lane >> 4) * 8 + (lane & 7), bc = (lane >> 3) & 1;
+                for (int e = 0; e < 4; ++e) S[n][e] = 0.f;
+            const int br = (lane >> 4) * 8 + (lane & 7), bc = (lane >> 3) & 1;
 #pragma unroll
-        for (int term = 2; term >= 0; --term)  // the small terms first
+            for (int term = 2; term >= 0; --term)  // the small terms first
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
+                for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-                for (int n2 = 0; n2 < 2; ++n2) {
-                    if (32 * h + 16 * n2 >= smax) break;
-                    uint32_t bf[4];
-                    ldsm4(bf, kt + (term * PN + ks / 4) * 4096 + tile_off<128>(16 * n2 + br, 2 * (ks & 3) + bc));
-                    mma16816(S[2 * n2], au[ks], bf[0], bf[1]);
-                    mma16816(S[2 * n2 + 1], au[ks], bf[2], bf[3]);
-                }
+                    for (int n2 = 0; n2 < 2; ++n2) {
+                        if (32 * h + 16 * n2 >= smax) break;
+                        uint32_t bf[4];
+                        ldsm4(bf, kt + (term * PN + ks / 4) * 4096 + tile_off<128>(16 * n2 + br, 2 * (ks & 3) + bc));
+                        mma16816(S[2 * n2], au[ks], bf[0], bf[1]);
+                        mma16816(S[2 * n2 + 1], au[ks], bf[2], bf[3]);
+                    }
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+            for (int n = 0; n < 4; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (32 * h + 8 * n + 2 * c + (e & 1) >= (e >> 1 ? lim1 : lim0)) S[n][e] = -INFINITY;
-    };
-    auto softmax = [&](const float (&S)[4][4]) {  // running maximum and sum (each lane its own columns)
-        float x0 = m0, x1 = m1;
+                for (int e = 0; e < 4; ++e)
+                    if (32 * h + 8 * n + 2 * c + (e & 1) >= (e >> 1 ? lim1 : lim0)) S[n][e] = -INFINITY;
+        };
+        auto softmax = [&](const float (&S)[4][4]) {  // running maximum and sum (each lane its own columns)
+            float x0 = m0, x1 = m1;
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            x0 = fmaxf(x0, fmaxf(S[n][0], S[n][1]));
-            x1 = fmaxf(x1, fmaxf(S[n][2], S[n][3]));
-        }
-        z0 *= __expf(m0 - x0);
-        z1 *= __expf(m1 - x1);
-        m0 = x0;
-        m1 = x1;
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            z0 += __expf(S[n][0] - m0) + __expf(S[n][1] - m0);
-            z1 += __expf(S[n][2] - m1) + __expf(S[n][3] - m1);
-        }
-    };
-    auto join = [&]() {  // the four lanes of a row
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-            const float y0 = __shfl_xor_sync(0xffffffffu, m0, o), y1 = __shfl_xor_sync(0xffffffffu, m1, o);
-            const float w0 = __shfl_xor_sync(0xffffffffu, z0, o), w1 = __shfl_xor_sync(0xffffffffu, z1, o);
-            const float x0 = fmaxf(m0, y0), x1 = fmaxf(m1, y1);
-            z0 = z0 * __expf(m0 - x0) + w0 * __expf(y0 - x0);
-            z1 = z1 * __expf(m1 - x1) + w1 * __expf(y1 - x1);
+            for (int n = 0; n < 4; ++n) {
+                x0 = fmaxf(x0, fmaxf(S[n][0], S[n][1]));
+                x1 = fmaxf(x1, fmaxf(S[n][2], S[n][3]));
+            }
+            z0 *= __expf(m0 - x0);
+            z1 *= __expf(m1 - x1);
             m0 = x0;
             m1 = x1;
-        }
-        z0 = 1.f / z0;
-        z1 = 1.f / z1;
-    };
-    auto gates = [&](int h, const float (&S)[4][4]) {  // sums over the tile's tokens
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            float s0 = __expf(S[n][0] - m0) * z0 + __expf(S[n][2] - m1) * z1;
-            float s1 = __expf(S[n][1] - m0) * z0 + __expf(S[n][3] - m1) * z1;
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-                s0 += __shfl_xor_sync(0xffffffffu, s0, o);
-                s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+            for (int n = 0; n < 4; ++n) {
+                z0 += __expf(S[n][0] - m0) + __expf(S[n][1] - m0);
+                z1 += __expf(S[n][2] - m1) + __expf(S[n][3] - m1);
             }
-            if (g == 0) {
-                cols[warp][8 * n + 2 * c] = s0;
-                cols[warp][8 * n + 2 * c + 1] = s1;
+        };
+        auto join = [&]() {  // the four lanes of a row
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+                const float y0 = __shfl_xor_sync(0xffffffffu, m0, o), y1 = __shfl_xor_sync(0xffffffffu, m1, o);
+                const float w0 = __shfl_xor_sync(0xffffffffu, z0, o), w1 = __shfl_xor_sync(0xffffffffu, z1, o);
+                const float x0 = fmaxf(m0, y0), x1 = fmaxf(m1, y1);
+                z0 = z0 * __expf(m0 - x0) + w0 * __expf(y0 - x0);
+                z1 = z1 * __expf(m1 - x1) + w1 * __expf(y1 - x1);
+                m0 = x0;
+                m1 = x1;
             }
-        }
-        __syncthreads();
-        if (tid < 32 && 32 * h + tid < a.N) {
-            float s = 0.f;
+            z0 = 1.f / z0;
+            z1 = 1.f / z1;
+        };
+        auto gates = [&](int h, const float (&S)[4][4]) {  // sums over the tile's tokens
 #pragma unroll
-            for (int w = 0; w < 8; ++w) s += cols[w][tid];
-            out[32 * h + tid] = s;
-        }
-        __syncthreads();
-    };
-    if (nh <= 4) {
-        float S[4][4][4];
+            for (int n = 0; n < 4; ++n) {
+                float s0 = __expf(S[n][0] - m0) * z0 + __expf(S[n][2] - m1) * z1;
+                float s1 = __expf(S[n][1] - m0) * z0 + __expf(S[n][3] - m1) * z1;
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
-            if (h < nh) {
-                scores(h, h + 1 < nh ? h + 1 : -1, S[h]);
-                softmax(S[h]);
+                for (int o = 4; o < 32; o <<= 1) {
+                    s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+                    s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+                }
+                if (g == 0) {
+                    cols[warp][8 * n + 2 * c] = s0;
+                    cols[warp][8 * n + 2 * c + 1] = s1;
+                }
             }
-        join();
+            __syncthreads();
+            if (tid < 32 && 32 * h + tid < a.N) {
+                float s = 0.f;
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
-            if (h < nh) gates(h, S[h]);
-    } else {
-        float S[4][4];
-        for (int h = 0; h < nh; ++h) {
-            scores(h, h + 1 < nh ? h + 1 : 0, S);
-            softmax(S);
-        }
-        join();
-        for (int h = 0; h < nh; ++h) {
-            scores(h, h + 1 < nh ? h + 1 : -1, S);
-            gates(h, S);
+                for (int w = 0; w < 8; ++w) s += cols[w][tid];
+                out[32 * h + tid] = first ? s : out[32 * h + tid] + s;
+            }
+            __syncthreads();
+        };
+        if (nh <= 4) {
+            float S[4][4][4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                if (h < nh) {
+                    scores(h, h + 1 < nh ? h + 1 : -1, S[h]);
+                    softmax(S[h]);
+                }
+            join();
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                if (h < nh) gates(h, S[h]);
+        } else {
+            float S[4][4];
+            for (int h = 0; h < nh; ++h) {
+                scores(h, h + 1 < nh ? h + 1 : 0, S);
+                softmax(S);
+            }
+            join();
+            for (int h = 0; h < nh; ++h) {
+                scores(h, h + 1 < nh ? h + 1 : -1, S);
+                gates(h, S);
+            }
         }
     }
 }
 
-// mass_i: the tiles' sums, 32 strided shares of the tiles, joined in a fixed order.
+// mass_i: the rows' sums, 32 strided shares of the rows, joined in a fixed order.
 __global__ void __launch_bounds__(1024) mass_reduce(CompactArgs a)
 {
     __shared__ float part[32][33];
@@ -325,11 +341,12 @@ __global__ void __launch_bounds__(1024) mass_reduce(CompactArgs a)
     const int i = ((int)blockIdx.x % blocks) * 32 + lane;
     float s = 0.f;
     if (i < a.N) {
-        const float *p = a.part + (size_t)bh * a.tiles * a.N + i;
-        int t = (int)((long long)(i + 1) * a.C / a.tile_len);  // no token before the segment's end reads it
+        const float *p = a.part + (size_t)bh * a.shares * a.N + i;
+        // no token before the segment's end reads it: the first row with a tile that does
+        int t = max(0, (int)((long long)(i + 1) * a.C / a.tile_len) - (a.tiles - a.shares));
         t += (w - t % 32 + 32) % 32;
 #pragma unroll 4
-        for (; t < a.tiles; t += 32) s += p[(size_t)t * a.N];
+        for (; t < a.shares; t += 32) s += p[(size_t)t * a.N];
     }
     part[w][lane] = s;
     __syncthreads();
@@ -416,7 +433,7 @@ cudaError_t mass_impl(const Problem &p, const CompactArgs &a, cudaStream_t s)
     auto kern = gate_mass_simt<T, D>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)((long long)p.BH * a.tiles), kMThreads, smem, s>>>(a);
+    kern<<<(unsigned)((long long)p.BH * a.shares), kMThreads, smem, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -427,7 +444,7 @@ cudaError_t mass_tc_impl(const Problem &p, const CompactArgs &a, cudaStream_t s)
     auto kern = gate_mass_tc<D>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)((long long)p.BH * a.tiles), 256, smem, s>>>(a);
+    kern<<<(unsigned)((long long)p.BH * a.shares), 256, smem, s>>>(a);
     return cudaGetLastError();
 }
 

@@ -434,6 +434,7 @@ int cache_compact(const void *k, const void *u, const float *states_all, int B, 
     m.states = states; m.kbar = kbar; m.mass = mass; m.online = online; m.ksum = ksum; m.slot_seg = slot_seg;
     m.BH = p.BH; m.L = L; m.C = p.C; m.N = p.N; m.d = d; m.mode = p.mode; m.topk = p.topk; m.tiles = (int)tiles;
     m.tile_len = tile_len;
+    m.shares = (int)std::min<long long>(tiles, std::min(512, d * d));
     const bool tc = tile_len == 128;
     m.done = L / seg_len; m.nmax = n_max;
     m.protect = protect < m.done ? protect : m.done;
@@ -447,7 +448,7 @@ int cache_compact(const void *k, const void *u, const float *states_all, int B, 
         kbar_all = cv.take<float>(BH * N * d);
         r_on = cv.take<float>(BH * L);
         sums = cv.take<float>(BH * N * c.NCH * d);
-        m.part = cv.take<float>(BH * m.tiles * N);
+        m.part = cv.take<float>(BH * m.shares * N);
         m.order = cv.take<int32_t>(BH * n_max);
         if (pass == 0 && scratch_alloc(&scratch, cv.used, s) != cudaSuccess) {
             cudaGetLastError();

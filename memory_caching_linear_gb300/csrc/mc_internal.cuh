@@ -373,13 +373,13 @@ struct CompactArgs {
     const void *u;                     // [BH][L][d]
     const float *kbar_all, *r_on;      // [BH][N][d], [BH][L]
     const float *states_all;           // [BH][N][d][d]
-    float *part;                       // [BH][tiles][N] scratch
+    float *part;                       // [BH][shares][N] scratch
     float *mass_all;                   // [BH][N]
     const uint8_t *kbar_img;           // key-mean images (tensor-core gates), or null
     int32_t *order;                    // [BH][nmax] scratch
     float *states, *kbar, *mass, *online, *ksum;
     int32_t *slot_seg;
-    int BH, L, C, N, d, mode, topk, tiles, tile_len, done, nmax, protect;
+    int BH, L, C, N, d, mode, topk, tiles, tile_len, shares, done, nmax, protect;
 };
 int gate_mass_tile(const Problem &p);  // tokens per tile of launch_gate_mass
 cudaError_t launch_gate_mass(const Problem &p, const CompactArgs &a, cudaStream_t s);
