@@ -198,9 +198,17 @@ class DecodeCache:
         self.ksum = torch.zeros((B, H, d), **f32)
 
 
+def _in_order(cache):
+    """Segment s in slot s: the steps that keep no record of what a slot holds take no other cache."""
+    if isinstance(cache, EvictingCache):
+        raise TypeError("an EvictingCache is for mc_decode_step_evict")
+
+
 def mc_decode_step(cache: DecodeCache, q, k, v, u, agg_mode: int, topk: int = 0, *, y=None, stream=None):
     """One decoding step (``mc_decode_step`` in mc.h) for tokens q, k, v, u of shape
-    [B, H, d] at position ``cache.t``; advances ``cache.t`` and returns y [B, H, d]."""
+    [B, H, d] at position ``cache.t``; advances ``cache.t`` and returns y [B, H, d].
+    Not for an :class:`EvictingCache`."""
+    _in_order(cache)
     lib = load_library()
     if q.dim() != 3:
         raise ValueError("q must be [B, H, d]")
@@ -439,7 +447,8 @@ class DeltaMemoryCaching(torch.autograd.Function):
 class EvictingCache(DecodeCache):
     """A :class:`DecodeCache` of ``n_max`` slots that never fills up: each slot also has the gate weight
     that its segment gathered (``mass`` [B, H, n_max], fp32) and the segment it holds (``slot_seg``,
-    int32, -1 empty).  The ``protect`` newest completed segments are never evicted."""
+    int32, -1 empty).  The ``protect`` newest completed segments are never evicted.  It is for
+    ``mc_decode_step_evict``: the other steps would not say which segment a slot holds, and refuse it."""
 
     def __init__(self, B: int, H: int, d: int, seg_len: int, n_max: int, protect: int = 1, device="cuda"):
         super().__init__(B, H, d, seg_len, n_max, device)
@@ -488,7 +497,9 @@ def _token_args(cache, q, k, v, u, log_alpha, beta, y):
 def mc_decode_step_delta(cache: DecodeCache, q, k, v, u, log_alpha, beta, agg_mode: int, topk: int = 0, *, y=None,
                          stream=None):
     """One decoding step over the gated delta memory (``mc_decode_step_delta`` in mc.h): q, k, v, u
-    [B, H, d], log_alpha and beta [B, H]; advances ``cache.t`` and returns y [B, H, d]."""
+    [B, H, d], log_alpha and beta [B, H]; advances ``cache.t`` and returns y [B, H, d].  Not for an
+    :class:`EvictingCache`."""
+    _in_order(cache)
     B, H, d, dev, y = _token_args(cache, q, k, v, u, log_alpha, beta, y)
     with _on(dev):
         st = load_library().mc_decode_step_delta(
