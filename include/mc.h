@@ -272,7 +272,8 @@ int mc_decode_step_delta(const void *q, const void *k, const void *v, const void
  * mc_decode_step_evict -- a decoding step that never runs out of cache.  The n_max slots of
  * every head hold the segments that slot_seg names, in any order, and each gathers the gate
  * weight of the tokens that read it:
- *   mass     : fp32 [B][H][n_max] (in/out), mass_i += g_{t,i}.
+ *   mass     : fp32 [B][H][n_max] (in/out), mass_i += g_{t,i}: rounded up or down as t says, so that gates far
+ *              below a mass's last place count too (the sum stays within a few last places).
  *   slot_seg : int32 [B][H][n_max] (in/out), the segment a slot holds, -1 if it is empty.
  * At a segment's last token its memory and mean key go to the first empty slot or, if there is
  * none, replace the segment with the least mass (this token's weight included; equal mass: the

@@ -7,7 +7,7 @@
 //   gates:   as mc_decode_step over the cached segments: the first s slots, or with eviction
 //            every slot that holds a segment (slot_seg >= 0)
 //   read:    y = g_on M q + sum_i g_i M_i q
-//   mass:    mass_i += g_i (eviction only)
+//   mass:    mass_i += g_i (eviction only), rounded up or down so that small gates count in a large mass (add_mass)
 //   at the segment's last token M and the mean key become a cached segment: in slot s, or with
 //   eviction in the first empty slot, else in that of the segment with the least mass (this
 //   token's weight included) among those that are not the `protect` newest; equal mass: the oldest.
@@ -39,6 +39,20 @@ __device__ __forceinline__ float4 fma4(float s, const float4 &a, const float4 &b
 __device__ __forceinline__ float dot4(const float4 &a, const float4 &b)
 {
     return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, a.w * b.w)));
+}
+
+// m + g for a sum without end.  To the nearest fp32, a gate below half a unit in the last place would add nothing from some
+// mass on (0.004 at 65536), and the ranking would go by what was lost.  So the sum goes to the fp32 below it or above it:
+// above if its distance from the one below, in units, exceeds r.  With r the multiples of the golden ratio modulo 1, which are
+// spread as evenly as a sequence can be, the sum of n gates is a few units off, not n halves.  r is a function of the
+// position alone, so that runs repeat and equal masses with equal gates stay equal.
+__device__ __forceinline__ float add_mass(float m, float g, float r)
+{
+    const float s = m + g, b = s - m, e = (m - (s - b)) + (g - b);  // m + g = s + e exactly
+    if (!(e != 0.f) || !(s < FLT_MAX)) return s;
+    const float o = __int_as_float(__float_as_int(s) + (e > 0.f ? 1 : -1));  // the fp32 on the other side of m + g (s > 0)
+    const float up = e / (o - s);  // how far towards it
+    return e > 0.f ? (up > r ? o : s) : (1.f - up > r ? s : o);
 }
 
 template <typename T, int D>
@@ -157,7 +171,8 @@ __global__ void __launch_bounds__(kThreads, 5) decode_slots(SlotArgs a)
         int where = s;
         if (evict) {
             float *mass = a.mass + (size_t)bh * a.nmax;
-            const float m0 = i0 < n ? mass[i0] + (c0 ? g0 : 0.f) : 0.f, m1 = i1 < n ? mass[i1] + (c1 ? g1 : 0.f) : 0.f;
+            const float r = (float)((unsigned)a.t * 2654435769u >> 8) * 0x1p-24f;  // 2^32 / golden ratio
+            const float m0 = i0 < n ? add_mass(mass[i0], c0 ? g0 : 0.f, r) : 0.f, m1 = i1 < n ? add_mass(mass[i1], c1 ? g1 : 0.f, r) : 0.f;
             sc[lane] = m0;  // the head's new masses (the scores are spent)
             if (i1 < n) sc[i1] = m1;
             if (seg_end) {
