@@ -228,7 +228,7 @@ int mc_decode_step(const void *q, const void *k, const void *v, const void *u,
  *     M_t = a_t M_{t-1} + beta_t e_t k_t^T,   a_t = exp(log_alpha_t),
  * and everything else -- the cached states, the gates, the aggregations -- as mc_forward.
  * One segment (seg_len >= L) is the plain gated delta rule, whatever the aggregation; then
- * u is not read.
+ * u is not read and may be NULL.
  *   log_alpha, beta : [B][H][L], of q's element type.  log_alpha <= 0 (values below -60, and
  *                     -inf, count as -60: a decay by one part in 1e26); a segment's first one
  *                     meets an empty memory.  beta is any number; with unit keys the memory
@@ -248,8 +248,8 @@ int mc_forward_delta(const void *q, const void *k, const void *v, const void *u,
  * mc_backward_delta -- gradients of <y, dy> for mc_forward_delta: dq, dk, dv, du as
  * mc_backward, and dlog_alpha, dbeta [B][H][L] (written, of the element type; dlog_alpha is
  * zero at a segment's first token).  The states have no gradient of their own (a loss reads
- * them through y).  du may be NULL for MC_RESIDUAL and MC_MEAN; if given it is zeroed.  No
- * input may share memory with an output.  The call recomputes the forward in scratch: per 64
+ * them through y).  du may be NULL for MC_RESIDUAL and MC_MEAN and where one segment covers the
+ * sequence; if given it is zeroed.  No input may share memory with an output.  The call recomputes the forward in scratch: per 64
  * tokens and head two d x d states (of the element type; fp32 for d < 64) and, for bf16 with
  * d >= 64, 42 KB of pair products, and about 4 L d floats.
  */

@@ -371,8 +371,8 @@ def _on(device):
 def mc_forward_delta(q, k, v, u, log_alpha, beta, seg_len: int, agg_mode: int, topk: int = 0, *, y=None, states=None,
                      want_states: bool = True, stream=None):
     """Forward over the gated delta memory (``mc_forward_delta`` in mc.h); bf16 or fp32 inputs, log_alpha
-    and beta [B, H, L] of the same dtype.  u may be None for Residual and Mean, and when one segment
-    covers the sequence with one of these.  Returns (y, states); states is None when ``want_states`` is
+    and beta [B, H, L] of the same dtype.  u may be None for Residual and Mean, and where one segment
+    covers the sequence.  Returns (y, states); states is None when ``want_states`` is
     False and none was given."""
     (B, H, L, d), dev, dtype = _sequence_args(q, [("q", q), ("k", k), ("v", v)], 4)
     if u is not None:
@@ -422,7 +422,7 @@ def mc_backward_delta(q, k, v, u, log_alpha, beta, dy, seg_len: int, agg_mode: i
 class DeltaMemoryCaching(torch.autograd.Function):
     """Autograd wrapper of the gated delta memory: y = DeltaMemoryCaching.apply(q, k, v, u, log_alpha,
     beta, seg_len, agg_mode, topk) runs ``mc_forward_delta`` and, on backward, ``mc_backward_delta``
-    (u may be None for Residual and Mean).  The gradients have none of their own.  Work captured into a graph is better
+    (u may be None for Residual and Mean, and where one segment covers the sequence).  The gradients have none of their own.  Work captured into a graph is better
     written with the two functions: autograd ties a leaf's gradient to the stream of every graph that lives."""
 
     @staticmethod

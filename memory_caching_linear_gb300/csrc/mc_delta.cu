@@ -50,7 +50,7 @@ int check_call(Call &c, int B, int H, int L, int d, int seg_len, int agg_mode, i
     // one CTA per 64-token chunk, up to eight per segment
     if ((long long)p.BH * p.N * (c.NCH > 8 ? c.NCH : 8) >= (1ll << 31)) return MC_ERR_SHAPE;
     if (agg_mode < MC_RESIDUAL || agg_mode > MC_MEAN) return MC_ERR_MODE;
-    c.uses_u = mode_uses_u(agg_mode);
+    c.uses_u = mode_uses_u(agg_mode) && p.N > 1;  // a single memory has nothing to weigh
     p.mode = agg_mode == MC_SOUP ? MC_GRM : agg_mode;  // the same function for a matrix memory
     if (agg_mode == MC_SSC) {
         if (topk < 0) return MC_ERR_TOPK;
@@ -417,7 +417,7 @@ int cache_compact(const void *k, const void *u, const float *states_all, int B, 
     if (st != MC_OK) return st;
     if (n_max < 1 || n_max > kDecMaxN - 1 || protect < 0 || protect > n_max) return MC_ERR_SHAPE;
     if ((st = check_call(c, B, H, L, d, seg_len, agg_mode, topk, bf16)) != MC_OK) return st;
-    if (!c.uses_u) return MC_ERR_MODE;  // constant gates tell no segment from another
+    if (!mode_uses_u(agg_mode)) return MC_ERR_MODE;  // constant gates tell no segment from another
     Problem &p = c.p;
     const int tile_len = gate_mass_tile(p);
     const long long tiles = ((long long)L + tile_len - 1) / tile_len;

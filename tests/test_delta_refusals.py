@@ -20,3 +20,26 @@ def test_steps_without_slots_refuse_an_evicting_cache():
     with pytest.raises(TypeError):
         mcl.mc_decode_step_delta(cache, z, z, z, z, g, g, mcl.MC_GRM)
     assert cache.t == 0
+
+
+FAKE = 1 << 20  # an aligned address that is never read
+
+
+@pytest.mark.parametrize("mode", [mcl.MC_GRM, mcl.MC_SOUP, mcl.MC_SSC])
+def test_one_segment_needs_no_router_input(mode):
+    """A single memory has nothing to weigh: u is not read, and du, if it is there, only zeroed.  (The misaligned q keeps the
+    calls from going on.)"""
+    lib = mcl.load_library()
+
+    def forward(u, L, seg):
+        return lib.mc_forward_delta(FAKE + 4, FAKE, FAKE, u, FAKE, FAKE, 1, 1, L, 16, seg, mode, 2, FAKE, None, 1, None)
+
+    def backward(u, du, L, seg):
+        return lib.mc_backward_delta(FAKE + 4, FAKE, FAKE, u, FAKE, FAKE, FAKE, 1, 1, L, 16, seg, mode, 2, FAKE, FAKE, FAKE, du,
+                                     FAKE, FAKE, 1, None)
+
+    for seg in (64, 65, 1 << 20):
+        assert forward(None, 64, seg) == mcl.MC_ERR_ALIGN
+        assert backward(None, None, 64, seg) == mcl.MC_ERR_ALIGN and backward(None, FAKE, 64, seg) == mcl.MC_ERR_ALIGN
+    assert forward(None, 64, 63) == mcl.MC_ERR_NULL
+    assert backward(None, FAKE, 64, 63) == mcl.MC_ERR_NULL and backward(FAKE, None, 64, 63) == mcl.MC_ERR_NULL
