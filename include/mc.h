@@ -235,7 +235,7 @@ int mc_decode_step(const void *q, const void *k, const void *v, const void *u,
  *                     stays bounded for beta in [0, 2].
  *   states          : as mc_forward (fp32 whatever the element type); may be NULL.
  *   is_bf16         : q, k, v, u, log_alpha, beta and y are bf16 if non-zero, fp32 otherwise.
- *   Every d of mc_forward and any seg_len; errors as mc_forward.  No input may share memory
+ *   Every d of mc_forward, any seg_len, L up to 2^30; errors as mc_forward.  No input may share memory
  *   with an output.  With bf16 inputs the states come out to a few parts in 1e5 (1e4 where
  *   all keys of a segment are nearly parallel and beta is close to 2).
  */

@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kThreads, 5) decode_slots(SlotArgs a)
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const bool evict = a.mass != nullptr, delta = a.la != nullptr;
     const int s = a.t / a.C, t0 = s * a.C;
-    const bool seg_start = a.t == t0, seg_end = a.t == t0 + a.C - 1;
+    const bool seg_start = a.t == t0, seg_end = a.t - t0 == a.C - 1;
     const int n = evict ? a.nmax : s;  // slots looked at
     const bool routed = a.mode == MC_GRM || a.mode == MC_SSC;
     __shared__ __align__(16) float qs[D], ks[D], us[D], ps[D];

@@ -39,6 +39,7 @@ int check_call(Call &c, int B, int H, int L, int d, int seg_len, int agg_mode, i
 {
     int st = check_shape(B, H, L, d, seg_len);
     if (st != MC_OK) return st;
+    if (L > (1 << 30)) return MC_ERR_SHAPE;  // a segment's end, up to L + seg_len, is an int in the kernels
     if (seg_len > L) seg_len = L;
     Problem &p = c.p;
     p = Problem{};

@@ -43,3 +43,17 @@ def test_one_segment_needs_no_router_input(mode):
         assert backward(None, None, 64, seg) == mcl.MC_ERR_ALIGN and backward(None, FAKE, 64, seg) == mcl.MC_ERR_ALIGN
     assert forward(None, 64, 63) == mcl.MC_ERR_NULL
     assert backward(None, FAKE, 64, 63) == mcl.MC_ERR_NULL and backward(FAKE, None, 64, 63) == mcl.MC_ERR_NULL
+
+
+def test_lengths_whose_segment_ends_pass_an_int():
+    lib = mcl.load_library()
+
+    def forward(L, seg):
+        return lib.mc_forward_delta(FAKE + 4, FAKE, FAKE, None, FAKE, FAKE, 1, 1, L, 16, seg, mcl.MC_RESIDUAL, 0, FAKE, None, 1, None)
+
+    def compact(L, seg):
+        return lib.mc_cache_compact(FAKE + 4, FAKE, FAKE, 1, 1, L, 16, seg, mcl.MC_GRM, 0, 1, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 4, None, 1, None)
+
+    for call in (forward, compact):
+        assert call(1 << 30, (1 << 31) - 1) == mcl.MC_ERR_ALIGN and call(1 << 30, (1 << 30) - 1) == mcl.MC_ERR_ALIGN
+        assert call((1 << 30) + 1, 1 << 30) == mcl.MC_ERR_SHAPE and call((1 << 31) - 1, (1 << 31) - 1) == mcl.MC_ERR_SHAPE
