@@ -360,6 +360,12 @@ def _new(t, name, dtype, shape, dev):
     return t
 
 
+def _c_ints(seg_len, topk, L):
+    """seg_len and topk for the library, whose ints are of 32 bits: a segment longer than the sequence is the sequence, and
+    no more segments than tokens can be selected."""
+    return min(int(seg_len), L), min(int(topk), L)
+
+
 _HERE = contextlib.nullcontext()
 
 
@@ -379,6 +385,7 @@ def mc_forward_delta(q, k, v, u, log_alpha, beta, seg_len: int, agg_mode: int, t
         _check(u, "u", dtype, q.shape, dev)
     _check(log_alpha, "log_alpha", dtype, (B, H, L), dev)
     _check(beta, "beta", dtype, (B, H, L), dev)
+    seg_len, topk = _c_ints(seg_len, topk, L)
     y = _new(y, "y", dtype, q.shape, dev)
     if states is not None or want_states:
         N = num_segments(L, seg_len) if seg_len >= 1 else 1
@@ -404,6 +411,7 @@ def mc_backward_delta(q, k, v, u, log_alpha, beta, dy, seg_len: int, agg_mode: i
         _check(u, "u", dtype, q.shape, dev)
     _check(log_alpha, "log_alpha", dtype, (B, H, L), dev)
     _check(beta, "beta", dtype, (B, H, L), dev)
+    seg_len, topk = _c_ints(seg_len, topk, L)
     dq, dk, dv = (_new(t, n, dtype, q.shape, dev) for t, n in ((dq, "dq"), (dk, "dk"), (dv, "dv")))
     if du is not None or agg_mode in (MC_GRM, MC_SOUP, MC_SSC):
         du = _new(du, "du", dtype, q.shape, dev)
@@ -539,6 +547,9 @@ def mc_cache_compact(cache: EvictingCache, k, u, states, agg_mode: int, topk: in
     if not isinstance(cache, EvictingCache):
         raise TypeError("cache must be an EvictingCache")
     (B, H, L, d), dev, dtype = _sequence_args(k, [("k", k), ("u", u)], 4)
+    if not 1 <= cache.seg_len < 1 << 31:
+        raise ValueError("seg_len must be in 1 .. 2^31 - 1")
+    topk = _c_ints(cache.seg_len, topk, L)[1]
     N = num_segments(L, cache.seg_len)
     _check(states, "states", torch.float32, (B, H, N, d, d), dev)
     _cache_args(cache, B, H, d, dev)

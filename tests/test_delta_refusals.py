@@ -57,3 +57,10 @@ def test_lengths_whose_segment_ends_pass_an_int():
     for call in (forward, compact):
         assert call(1 << 30, (1 << 31) - 1) == mcl.MC_ERR_ALIGN and call(1 << 30, (1 << 30) - 1) == mcl.MC_ERR_ALIGN
         assert call((1 << 30) + 1, 1 << 30) == mcl.MC_ERR_SHAPE and call((1 << 31) - 1, (1 << 31) - 1) == mcl.MC_ERR_SHAPE
+
+
+def test_numbers_past_32_bits_do_not_wrap():
+    """One segment asked for as 2^32 + 5 tokens is not one of 5, nor are 2^32 + 1 selected segments one."""
+    from memory_caching_linear_gb300 import _c_ints
+    assert _c_ints((1 << 32) + 5, (1 << 32) + 1, 100) == (100, 100)
+    assert _c_ints(7, 3, 100) == (7, 3) and _c_ints(0, -1, 100) == (0, -1) and _c_ints(100, 100, 100) == (100, 100)
