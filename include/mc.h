@@ -235,9 +235,11 @@ int mc_decode_step(const void *q, const void *k, const void *v, const void *u,
  *                     stays bounded for beta in [0, 2].
  *   states          : as mc_forward (fp32 whatever the element type); may be NULL.
  *   is_bf16         : q, k, v, u, log_alpha, beta and y are bf16 if non-zero, fp32 otherwise.
- *   Every d of mc_forward, any seg_len, L up to 2^30; errors as mc_forward.  No input may share memory
- *   with an output.  With bf16 inputs the states come out to a few parts in 1e5 (1e4 where
- *   all keys of a segment are nearly parallel and beta is close to 2).
+ *   Every d of mc_forward, any seg_len, L up to 2^30; errors as mc_forward.  No
+ *   input may share memory with an output.  With bf16 inputs the states come out to a few parts in 1e5 (1e4 where
+ *   all keys of a segment are nearly parallel and beta is close to 2), and y, relative to its
+ *   largest value, to 1e-2: its rounding to bf16, and that of the gates and cached states.  With fp32
+ *   inputs both are within 1e-4.
  */
 int mc_forward_delta(const void *q, const void *k, const void *v, const void *u,
                      const void *log_alpha, const void *beta, int B, int H, int L, int d,
@@ -249,9 +251,14 @@ int mc_forward_delta(const void *q, const void *k, const void *v, const void *u,
  * mc_backward, and dlog_alpha, dbeta [B][H][L] (written, of the element type; dlog_alpha is
  * zero at a segment's first token).  The states have no gradient of their own (a loss reads
  * them through y).  du may be NULL for MC_RESIDUAL and MC_MEAN and where one segment covers the
- * sequence; if given it is zeroed.  No input may share memory with an output.  The call recomputes the forward in scratch: per 64
- * tokens and head two d x d states (of the element type; fp32 for d < 64) and, for bf16 with
- * d >= 64, 42 KB of pair products, and about 4 L d floats.
+ * sequence; if given it is zeroed.  No input may share memory with an output.  The call recomputes
+ * the forward in scratch: for every chunk of 64 tokens that a segment begins (a segment of 16
+ * tokens is one) two d x d states (of the element type; fp32 for d < 64) and, for bf16 with
+ * d >= 64, 42 KB of pair products; and about 4 L d floats.
+ *   Accuracy, relative to a gradient's largest value: fp32 inputs 1e-4; bf16 ones, rounded to bf16
+ * at the end, 1e-2.  Where all keys of a segment are nearly parallel what a token writes undoes what
+ * the one before wrote, and with bf16 inputs and d >= 64 dlog_alpha, a difference of large terms,
+ * can be several 1e-2 off.
  */
 int mc_backward_delta(const void *q, const void *k, const void *v, const void *u,
                       const void *log_alpha, const void *beta, const void *dy, int B, int H, int L,

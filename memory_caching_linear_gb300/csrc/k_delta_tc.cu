@@ -16,10 +16,11 @@
 //
 // Precision: the memory is held in fp32, and what is not an input enters the products in two bf16 terms, products of two
 // lows left out: 2^-17 of a term (the inverse in three, 2^-25).  The errors e_j of keys that resemble each other are large
-// and cancel in S and in O, so one term (2^-9) would show: at keys with a cosine of 0.8 it leaves the memory 7e-3 and y 9e-3
-// off, as against 2e-5 and 1.4e-3, the last bf16 rounding.  Two readings are one term's: O's of S, where nothing cancels and
-// the result is bf16, and E's of S in the gradients' own walk (S 4e-4 off there; 122 instead of 140 us at L = 2048, 96
-// heads, d = 128): what they yield passes through bf16 states and errors anyway.
+// and cancel in S, in O and in the gradients' sums over pairs, so one term (2^-9) would show: at keys with a cosine of 0.8 it
+// leaves the memory 7e-3 and y 9e-3 off, as against 2e-5 and 1.4e-3, the last bf16 rounding, and at all but parallel ones
+// dq and dbeta 5e-2.  One term's are readings in which nothing cancels and whose results are bf16: O's of S, and in the
+// gradients' kernels S and R at a chunk's ends; E's of S in their own walk leaves S 4e-4 off there (122 instead of 140 us at
+// L = 2048, 96 heads, d = 128).
 #include <atomic>
 #include <cstdint>
 
@@ -585,7 +586,7 @@ __device__ __forceinline__ void pair_sum(float4 *xb, int warp, int lane, F each,
 // time, they took a fifth of the time (shared memory's pipe is what the products wait for, too).  16 heads of 65536
 // tokens, segments of 1024, d = 128: 571 us, 413 TFLOP/s of warp-level products against 600 that these reach when nothing
 // else is done (420 us without the online reads, which the readout would then form in one term).  One memory of 4096
-// tokens, 32 heads (recomputed, one term): 117 us, 1.8 us for a chunk, half of which are one warp's own products one after
+// tokens, 32 heads (recomputed, one term, e in two for the gradients): 126 us, 2.0 us for a chunk, half of which are one warp's own products one after
 // the other.
 // ---------------------------------------------------------------------------
 template <int D, int NW, int KP, bool READ>
@@ -811,13 +812,14 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
             }
         }
         if (a.E) {
-            uint32_t ef[4][4];
+            uint32_t eh[4][4], el[4][4];
 #pragma unroll
             for (int n = 0; n < 8; ++n) {
-                ef[n / 2][2 * (n & 1)] = pack2(X[n][0], X[n][1]);
-                ef[n / 2][2 * (n & 1) + 1] = pack2(X[n][2], X[n][3]);
+                split2(X[n][0], X[n][1], eh[n / 2][2 * (n & 1)], el[n / 2][2 * (n & 1)]);
+                split2(X[n][2], X[n][3], eh[n / 2][2 * (n & 1) + 1], el[n / 2][2 * (n & 1) + 1]);
             }
-            put(a.E, ef);
+            put(a.E, eh);
+            put(a.E_lo, el);
         }
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
@@ -868,10 +870,10 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) de
 // with p_i = g_i dy_i and R the adjoint after the chunk:
 //   X   = diag(exp(c_end - c)) K R^T + P^T p,   W = T^T diag(beta) X            (dv = W)
 //   R' = exp(c_end) R + sum_i exp(c_i) (p_i q_i^T - w_i k_i^T)
-// R is held in fp32 and read in one bf16 term; T, P, X and w take part in two, as in the walk forwards: for keys that
-// resemble each other X gathers what later tokens ask of every one of them, and w is the small difference that is left
-// (one term: dv 3e-2 off at all but parallel keys).  One memory of 4096 tokens, 32 heads, d = 128: 139 us, 2.2 us for a chunk,
-// its chain as in delta_walk_tc; 16 heads of 16384, segments of 1024: 170 us.
+// R is held in fp32 and read in two bf16 terms, as T, P, X and w are: for keys that resemble each other X gathers what later
+// tokens ask of every one of them, and w is the small difference that is left (all in one term: dv 3e-2 off at all but
+// parallel keys; R alone: dv and dbeta 1.2e-2).  p is rounded once.  One memory of 4096 tokens, 32 heads, d = 128: 155 us,
+// 2.4 us for a chunk, its chain as in delta_walk_tc; 16 heads of 16384, segments of 1024: 199 us.
 // ---------------------------------------------------------------------------
 template <int D, int NW, int KP>
 struct RWalkSmem {
@@ -982,14 +984,19 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
         const int br = (lane >> 4) * 8 + (lane & 7), bc = (lane >> 3) & 1;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-            const uint32_t rf[4] = {pack2(R[2 * ks][0], R[2 * ks][1]), pack2(R[2 * ks][2], R[2 * ks][3]),
-                                    pack2(R[2 * ks + 1][0], R[2 * ks + 1][1]), pack2(R[2 * ks + 1][2], R[2 * ks + 1][3])};
+            uint32_t rf[4], rl[4];
+            split2(R[2 * ks][0], R[2 * ks][1], rf[0], rl[0]);
+            split2(R[2 * ks][2], R[2 * ks][3], rf[1], rl[1]);
+            split2(R[2 * ks + 1][0], R[2 * ks + 1][1], rf[2], rl[2]);
+            split2(R[2 * ks + 1][2], R[2 * ks + 1][3], rf[3], rl[3]);
 #pragma unroll
             for (int n2 = 0; n2 < 4; ++n2) {
                 uint32_t b[4];
                 ldsm4(b, kt + panel_off(16 * n2 + br, 2 * (k0 + ks) + bc));
                 mma16816(X[2 * n2], rf, b[0], b[1]);
                 mma16816(X[2 * n2 + 1], rf, b[2], b[3]);
+                mma16816(X[2 * n2], rl, b[0], b[1]);
+                mma16816(X[2 * n2 + 1], rl, b[2], b[3]);
             }
         }
         uint32_t v4[4][4];
@@ -1067,10 +1074,11 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
             }
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
-            wf[n / 2][2 * (n & 1)] = pack2(X[n][0], X[n][1]);
-            wf[n / 2][2 * (n & 1) + 1] = pack2(X[n][2], X[n][3]);
+            split2(X[n][0], X[n][1], wf[n / 2][2 * (n & 1)], wl[n / 2][2 * (n & 1)]);
+            split2(X[n][2], X[n][3], wf[n / 2][2 * (n & 1) + 1], wl[n / 2][2 * (n & 1) + 1]);
         }
         put_tokens<NW, KP, D>(a.dv + row0 * D + vbase + 16 * wr, wf, vown, cnt, wr, kp, lane);
+        put_tokens<NW, KP, D>(a.W_lo + row0 * D + vbase + 16 * wr, wl, vown, cnt, wr, kp, lane);
 #pragma unroll
         for (int n = 0; n < 8; ++n) {  // -exp(c) w
             const float2 ga = *reinterpret_cast<const float2 *>(vec + 8 * n + 2 * c);
@@ -1109,22 +1117,24 @@ __global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_rwalk_tc(
 // ---------------------------------------------------------------------------
 // delta_grads_tc: one CTA per chunk, everything that sums over value rows (k_delta_simt.cu's header).
 // Eight warps: warp % 4 takes 16 tokens, warp / 4 half of the dimensions.  The warps of one half form B1, those of the
-// other B2 (16 rows each), and leave them in shared memory as 16 x 16 blocks of the lower triangle, from which both
-// read them as they lie (with beta_j) and transposed.  A chunk is a chain of loads and small products, so two CTAs
-// share an SM, no load is waited for that could have been under way before, and tiles that have been read make room:
-// S's second block takes e's tile, R those of p and w, e comes again in S's first block, u in its second.  2048 chunks, d = 128:
-// 115 us for 0.40 GB (3.4 TB/s) and 33 GFLOP of products; 4096 chunks with gates and pooled keys 260 us.  Bound by the
-// latency of loads and products within a chunk, with 16 warps on an SM.
-// e, w, p, S, R and the weighted pairs enter in one bf16 term each, sums are fp32: the gradients come out 2.7e-3 to 3.9e-3 off
-// in the 2-norm, of which their own last rounding is 1.7e-3.  The pair sums behind the decay's gradient cancel and use fp32 pairs.
-// ---------------------------------------------------------------------------
+// other B2 (16 rows each), and leave them in shared memory as 16 x 16 blocks of the lower triangle in two bf16 terms, from
+// which both read them as they lie (with beta_j) and transposed.  A chunk is a chain of loads and small products, so two
+// CTAs share an SM, a load is under way while what is there is worked on, and tiles that have been read make room: q and k
+// come where the second terms of e and w were, the pairs' second terms go where e was (d = 128), S's second block where the
+// first was, R where p and w were, e comes again in S's place, u in R's.  2048 chunks, d = 128: 147 us for 0.52 GB (3.5 TB/s)
+// and 33 GFLOP of products; 4096 chunks with gates and pooled keys 317 us.  Bound by the latency of loads and products
+// within a chunk, with 16 warps on an SM.
+// e, w and the weighted pairs enter the sums over pairs in two terms: for keys that resemble each other these sums cancel
+// (one term: dq and dbeta up to 5e-2 off, 117 us).  p, S, R and e's and w's products with these are one term's: the gradients
+// come out 1.7e-3 to 2.5e-3 off in the 2-norm, of which their own last rounding is 1.7e-3.
+// The decay's gradient is a running sum of pair terms of which each enters and leaves with the same value.
 constexpr int kGradThreads = 256;
 
 struct GradMaps {
-    CUtensorMap dy, e, w, q, k, u, S, R;  // tokens; the memories and adjoints by chunk
+    CUtensorMap dy, e, e_lo, w, w_lo, q, k, u, S, R;  // tokens (e and w in two terms); the memories and adjoints by chunk
 };
 struct GradSync {
-    uint64_t tiles, S0, S1, R, u;
+    uint64_t tiles, S0, qk, S1, R, u;
     int abort_flag, used;  // used: the barriers, in this order, that copies were sent to
 };
 
@@ -1133,8 +1143,9 @@ struct GradSmem {
     static constexpr int kT = kCH * D * 2;   // a 64-token tile
     static constexpr int kM = 64 * D * 2;    // 64 rows of S or R
     static constexpr int kVec = 4 * (22 * kCH + 16);
-    static constexpr int kB = 2 * 10 * 512;  // B1 and B2: ten 16 x 16 blocks each
-    static constexpr int kSync = 5 * kT + kM + kB + kVec;
+    static constexpr int kB = 2 * 10 * 512;  // B1 and B2: ten 16 x 16 blocks each, their first terms
+    static constexpr int kBl = kT < kB ? kB : 0;  // their second terms (else over e's tile)
+    static constexpr int kSync = 5 * kT + kM + kB + kBl + kVec;
     static constexpr int kTotal = kSync + (int)sizeof(GradSync);
 };
 
@@ -1146,8 +1157,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
     constexpr int MB = D / 64;                                                         // blocks of S and R
     extern __shared__ __align__(1024) uint8_t sm[];
     uint8_t *Qt = sm, *Kt = Qt + G::kT, *Pt = Kt + G::kT, *Et = Pt + G::kT, *Wt = Et + G::kT, *Mt = Wt + G::kT;
-    uint8_t *Bt = Mt + G::kM;
-    float *cum = reinterpret_cast<float *>(Bt + G::kB), *bet = cum + kCH, *gs = bet + kCH, *pw = gs + kCH;
+    uint8_t *Bt = Mt + G::kM, *Bl = G::kBl ? Bt + G::kB : Et;
+    float *cum = reinterpret_cast<float *>(Bt + G::kB + G::kBl), *bet = cum + kCH, *gs = bet + kCH, *pw = gs + kCH;
     float *rowsum = pw + kCH;                      // [4][2][64] by half: Y.k, exp(c) p S q, D R e k, exp(c) w S k
     float *rowf = rowsum + 8 * kCH, *colf = rowf + 5 * kCH;  // [2][10][16] sums of F's blocks over their columns, rows
     float *red = colf + 5 * kCH;
@@ -1178,6 +1189,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
         sync->used = 0;
         mbar_init(&sync->tiles, 1);
         mbar_init(&sync->S0, 1);
+        mbar_init(&sync->qk, 1);
         mbar_init(&sync->S1, 1);
         mbar_init(&sync->R, 1);
         mbar_init(&sync->u, 1);
@@ -1203,7 +1215,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
     };
     auto give_up = [&]() {
         if (tid != 0) return;
-        for (uint64_t *bar : {&sync->tiles, &sync->S0, &sync->S1, &sync->R, &sync->u})
+        for (uint64_t *bar : {&sync->tiles, &sync->S0, &sync->qk, &sync->S1, &sync->R, &sync->u})
             if (sync->used >> (bar - &sync->tiles) & 1) wait_out(bar, 0);
         atomicExch(&g_delta_abort, 1);
     };
@@ -1213,8 +1225,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
         load_tokens(Pt, maps.dy, &sync->tiles);
         load_tokens(Et, maps.e, &sync->tiles);
         load_tokens(Wt, maps.w, &sync->tiles);
-        load_tokens(Qt, maps.q, &sync->tiles);
-        load_tokens(Kt, maps.k, &sync->tiles);
+        load_tokens(Kt, maps.e_lo, &sync->tiles);  // (q and k take the places of the second terms, which the pairs alone need)
+        load_tokens(Qt, maps.w_lo, &sync->tiles);
         mbar_arrive_expect_tx(&sync->S0, G::kM);
         load_rows(Mt, maps.S, 0, &sync->S0);
     }
@@ -1315,7 +1327,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
         }
     };
     // Block (r, q) of B1 (which = 0) or B2: 16 rows of 32 bytes, their two pieces exchanged every four rows.
-    auto block = [&](int which, int r, int q) { return smem_addr(Bt) + (which * 10 + r * (r + 1) / 2 + q) * 512; };
+    auto block = [&](int which, int r, int q) { return (uint32_t)((which * 10 + r * (r + 1) / 2 + q) * 512); };
+    const uint32_t bh_at = smem_addr(Bt), bl_at = smem_addr(Bl);  // first, second terms
     auto block_off = [](int r, int pc) { return (uint32_t)(r * 32 + ((pc ^ ((r >> 2) & 1)) << 4)); };
     // The ten blocks of a half go round its warps, three or two to each, five to an SM's quarter.
     auto block_at = [&](int x, int &r, int &q) {
@@ -1324,9 +1337,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
         q = blk - r * (r + 1) / 2;
         return blk;
     };
-    // 16 tokens of `rows` against 16 of `cols`
+    // x += 16 tokens of `rows` against 16 of `cols`
     auto pairs = [&](float (&x)[2][4], const uint8_t *rows, int r, const uint8_t *cols, int q) {
-        zero(x);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             uint32_t af[4], bf[4];
@@ -1336,9 +1348,9 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
             mma16816(x[1], af, bf[2], bf[3]);
         }
     };
-    // a block of B, weighted with D_ij: kept, and in bf16 into shared memory
-    auto put_block = [&](float (&x)[2][4], int r, int q) {
-        uint32_t f[4];
+    // a block of B weighted with D_ij; w_i . e_i is kept
+    float *we = gs;  // (the gates have been read)
+    auto weigh = [&](float (&x)[2][4], int r, int q) {
         const float c0 = cum[16 * r + g], c1 = cum[16 * r + g + 8];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -1346,17 +1358,39 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int il = g + 8 * (e >> 1), jl = 8 * h + 2 * c + (e & 1);
+                if (half == 1 && r == q && jl == il) we[16 * r + il] = x[h][e];
                 x[h][e] = r > q || jl < il || (half == 0 && jl == il) ? x[h][e] * __expf((e >> 1 ? c1 : c0) - (e & 1 ? cj.y : cj.x)) : 0.f;
             }
-            f[2 * h] = pack2(x[h][0], x[h][1]);
-            f[2 * h + 1] = pack2(x[h][2], x[h][3]);
         }
-        stsm4(block(half, r, q) + block_off(lane & 15, lane >> 4), f[0], f[1], f[2], f[3]);
+    };
+    // into shared memory in two terms, and back
+    auto put_block = [&](const float (&x)[2][4], int r, int q) {
+        uint32_t f[4], l[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            split2(x[h][0], x[h][1], f[2 * h], l[2 * h]);
+            split2(x[h][2], x[h][3], f[2 * h + 1], l[2 * h + 1]);
+        }
+        const uint32_t at = block(half, r, q) + block_off(lane & 15, lane >> 4);
+        stsm4(bh_at + at, f[0], f[1], f[2], f[3]);
+        stsm4(bl_at + at, l[0], l[1], l[2], l[3]);
+    };
+    // block (r, q) of B as pairs of values: register x holds (row g + 8 (x % 2), columns 8 (x / 2) + 2 c, + 1)
+    auto get_block = [&](float2 (&v)[4], int which, int r, int q) {
+        uint32_t f[4], l[4];
+        const uint32_t at = block(which, r, q) + block_off(lane & 15, lane >> 4);
+        ldsm4(f, bh_at + at);
+        ldsm4(l, bl_at + at);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) v[x] = make_float2(low_f(f[x]) + low_f(l[x]), high_f(f[x]) + high_f(l[x]));
     };
     // F_ij = beta_j B_ij (rows_i . k_j) for j < i: the sums over a block's columns and rows
-    auto pair_sums = [&](const float (&b)[2][4], const uint8_t *rows, float sign, int blk, int r, int q) {
+    auto pair_sums = [&](const uint8_t *rows, float sign, int blk, int r, int q) {
         float kk[2][4], f0 = 0.f, f1 = 0.f, col[2][2];
+        float2 b[4];
+        zero(kk);
         pairs(kk, rows, r, Kt, q);
+        get_block(b, half, r, q);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const float2 bj = *reinterpret_cast<const float2 *>(bet + 16 * q + 8 * h + 2 * c);
@@ -1364,7 +1398,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int il = g + 8 * (e >> 1), jl = 8 * h + 2 * c + (e & 1);
-                const float f = r > q || jl < il ? sign * (e & 1 ? bj.y : bj.x) * kk[h][e] * b[h][e] : 0.f;
+                const float f = r > q || jl < il ? sign * (e & 1 ? bj.y : bj.x) * kk[h][e] * (e & 1 ? b[2 * h + (e >> 1)].y : b[2 * h + (e >> 1)].x) : 0.f;
                 col[h][e & 1] += f;
                 if (e >> 1) f1 += f;
                 else f0 += f;
@@ -1399,14 +1433,15 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
 #pragma unroll
         for (int k4 = 0; k4 < 4; ++k4) {
             if (k4 > wm) continue;
-            uint32_t f[4];
-            ldsm4(f, block(which, wm, k4) + block_off(lane & 15, lane >> 4));
-            const float2 be0 = *reinterpret_cast<const float2 *>(bet + 16 * k4 + 2 * c);
-            const float2 be1 = *reinterpret_cast<const float2 *>(bet + 16 * k4 + 8 + 2 * c);
-            f[0] = pack2(low_f(f[0]) * be0.x, high_f(f[0]) * be0.y);
-            f[1] = pack2(low_f(f[1]) * be0.x, high_f(f[1]) * be0.y);
-            f[2] = pack2(low_f(f[2]) * be1.x, high_f(f[2]) * be1.y);
-            f[3] = pack2(low_f(f[3]) * be1.x, high_f(f[3]) * be1.y);
+            float2 v[4];
+            get_block(v, which, wm, k4);
+            uint32_t f[4], l[4];
+#pragma unroll
+            for (int x2 = 0; x2 < 4; ++x2) {
+                const float2 be = *reinterpret_cast<const float2 *>(bet + 16 * k4 + 8 * (x2 / 2) + 2 * c);
+                split2(v[x2].x * be.x, v[x2].y * be.y, f[x2], l[x2]);
+            }
+            times_tokens(x, l, Kt, k4);
             times_tokens(x, f, Kt, k4);
         }
     };
@@ -1426,33 +1461,32 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
             }
     };
 
-    // Where S comes in two blocks: the second takes e's place once the pairs have read it, and e comes again with R.
-    uint8_t *const Sl = MB > 1 ? Et : Mt, *const E2 = MB > 1 ? Mt : Et;
     {
         float b[3][2][4];
         int r, q;
 #pragma unroll
         for (int x = 0; x < 3; ++x)
             if (block_at(x, r, q) < 10) {
+                zero(b[x]);
+                pairs(b[x], half ? Wt : Pt, r, Kt, q);  // e's second term
+                if (half) pairs(b[x], Qt, r, Et, q);    // w's second term
                 pairs(b[x], half ? Wt : Pt, r, Et, q);
-                put_block(b[x], r, q);
+                weigh(b[x], r, q);
             }
-        fence_async_smem();  // (what was cleared or scaled in the tiles, before the copies over them)
-        __syncthreads();     // the blocks are there, e has been read
-        if (MB > 1 && tid == 0) {
+        fence_async_smem();  // (what was cleared in the tiles, before the copies over them)
+        __syncthreads();     // the second terms have been read, and e
+        if (tid == 0) {
             sync->used |= 4;
-            mbar_arrive_expect_tx(&sync->S1, G::kM);
-            load_rows(Et, maps.S, 1, &sync->S1);
+            mbar_arrive_expect_tx(&sync->qk, 2 * G::kT);
+            load_tokens(Qt, maps.q, &sync->qk);
+            load_tokens(Kt, maps.k, &sync->qk);
         }
         __syncwarp();
 #pragma unroll
-        for (int x = 0; x < 3; ++x) {
-            const int blk = block_at(x, r, q);
-            if (blk < 10) pair_sums(b[x], half ? Kt : Qt, half ? -1.f : 1.f, blk, r, q);
-        }
+        for (int x = 0; x < 3; ++x)
+            if (block_at(x, r, q) < 10) put_block(b[x], r, q);
     }
     wait(&sync->S0, kGiveUpLate);
-    if (MB > 1) wait(&sync->S1, kGiveUpLate);
     __syncwarp();
     float z[HN][4];
     zero(z);
@@ -1461,16 +1495,43 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
         zero(dq);
         times_rows(dq, Pt, Mt, 0);
         times_rows(z, Wt, Mt, 0);
-        if (MB > 1) {
-            times_rows(dq, Pt, Et, 1);
-            times_rows(z, Wt, Et, 1);
+        wait(&sync->qk, kGiveUpLate);
+        if (__syncthreads_or(!ok)) {  // the blocks are there, S's first rows have been read
+            give_up();
+            return;
         }
-        if (__syncthreads_or(!ok)) {  // p and w have been read: their tiles take R
+        if (MB > 1 && tid == 0) {
+            sync->used |= 8;
+            mbar_arrive_expect_tx(&sync->S1, G::kM);
+            load_rows(Mt, maps.S, 1, &sync->S1);
+        }
+        __syncwarp();
+        if (w.cnt < kCH) {
+            clear_tokens(Qt);
+            clear_tokens(Kt);
+            __syncthreads();
+        }
+        {
+            int r, q;
+#pragma unroll
+            for (int x = 0; x < 3; ++x) {
+                const int blk = block_at(x, r, q);
+                if (blk < 10) pair_sums(half ? Kt : Qt, half ? -1.f : 1.f, blk, r, q);
+            }
+        }
+        if (MB > 1) {
+            wait(&sync->S1, kGiveUpLate);
+            __syncwarp();
+            times_rows(dq, Pt, Mt, 1);
+            times_rows(z, Wt, Mt, 1);
+        }
+        fence_async_smem();
+        if (__syncthreads_or(!ok)) {  // p and w have been read: their tiles take R, and S's takes e
             give_up();
             return;
         }
         if (tid == 0) {
-            sync->used |= 8;
+            sync->used |= 16;
             mbar_arrive_expect_tx(&sync->R, MB * G::kM + (MB > 1 ? G::kT : 0));
             load_rows(Wt, maps.R, 0, &sync->R);
             if (MB > 1) {
@@ -1516,12 +1577,15 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
     }
     float y[HN][4];
     zero(y);
-    float in = 0.f;  // <R, S>, of which S's last rows are still there
+    uint8_t *const E2 = MB > 1 ? Mt : Et;
+    float in = 0.f;  // <R, S>; S's rows are still there where they are one block
     constexpr int X4 = 64 * PIECES / kGradThreads;
-    uint4 s4[X4];
+    uint4 s4[MB][X4];
     if (MB > 1)
 #pragma unroll
-        for (int x = 0; x < X4; ++x) s4[x] = *reinterpret_cast<const uint4 *>(S + (size_t)(tid + x * kGradThreads) * 8);
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+            for (int x = 0; x < X4; ++x) s4[mb][x] = *reinterpret_cast<const uint4 *>(S + (size_t)(tid + (mb * X4 + x) * kGradThreads) * 8);
     wait(&sync->R, kGiveUpEnd);
     __syncwarp();
     if (MB > 1 && w.cnt < kCH) {
@@ -1535,22 +1599,22 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
             const int e = tid + x * kGradThreads;
             const uint32_t o = panel_off(e / PIECES, e % PIECES);
             const uint4 r4 = *reinterpret_cast<const uint4 *>((mb ? Pt : Wt) + o);
-            const uint4 m4 = mb + 1 < MB ? s4[x] : *reinterpret_cast<const uint4 *>(Sl + o);
+            const uint4 m4 = MB > 1 ? s4[mb][x] : *reinterpret_cast<const uint4 *>(Mt + o);
             const uint32_t *rw = reinterpret_cast<const uint32_t *>(&r4), *sw = reinterpret_cast<const uint32_t *>(&m4);
 #pragma unroll
             for (int q = 0; q < 4; ++q) in = fmaf(low_f(rw[q]), low_f(sw[q]), fmaf(high_f(rw[q]), high_f(sw[q]), in));
         }
-    if (a.pw) {  // u for the pooled keys' share, into their place
+    times_rows(y, E2, Wt, 0);
+    if (MB > 1) times_rows(y, E2, Pt, 1);
+    if (a.pw) {  // u for the pooled keys' share, in R's place
         __syncthreads();
         if (ok && tid == 0) {
-            sync->used |= 16;
+            sync->used |= 32;
             mbar_arrive_expect_tx(&sync->u, G::kT);
-            load_tokens(Sl, maps.u, &sync->u);
+            load_tokens(Wt, maps.u, &sync->u);
         }
         __syncwarp();
     }
-    times_rows(y, E2, Wt, 0);
-    if (MB > 1) times_rows(y, E2, Pt, 1);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) in += __shfl_xor_sync(0xffffffffu, in, o);
     if (lane == 0) red[warp] = in;
@@ -1560,13 +1624,17 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
     for (int k4 = 0; k4 < 4; ++k4) {  // the transposed blocks: rows j, columns i >= j
         if (k4 < wm) continue;
         const uint32_t off = block_off(((lane >> 4) << 3) + (lane & 7), (lane >> 3) & 1);
-        uint32_t f[4];
-        ldsm4t(f, block(0, k4, wm) + off);
-        times_tokens(y, f, Qt, k4);
-        ldsm4t(f, block(1, k4, wm) + off);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) f[q] ^= 0x80008000u;
-        times_tokens(y, f, Kt, k4);
+        for (int term = 1; term >= 0; --term) {
+            const uint32_t at = (term ? bl_at : bh_at) + off;
+            uint32_t f[4];
+            ldsm4t(f, at + block(0, k4, wm));
+            times_tokens(y, f, Qt, k4);
+            ldsm4t(f, at + block(1, k4, wm));
+#pragma unroll
+            for (int q = 0; q < 4; ++q) f[q] ^= 0x80008000u;
+            times_tokens(y, f, Kt, k4);
+        }
     }
     row_dot(y, Kt, 0);
     {
@@ -1585,7 +1653,7 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
         return;
     }
     if (a.pw && w.cnt < kCH) {
-        clear_tokens(Sl);
+        clear_tokens(Wt);
         __syncthreads();
     }
     if (a.pw) {  // the pooled keys' share: rho after the chunk + sum over the chunk's tokens t >= j of pw_t u_t
@@ -1600,8 +1668,8 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
                     const int j = m0 + g + 8 * x, t = 8 * (2 * k4 + h) + 2 * c;
                     split2(t >= j ? pw[t] : 0.f, t + 1 >= j ? pw[t + 1] : 0.f, fh[2 * h + x], fl[2 * h + x]);
                 }
-            times_tokens(y, fh, Sl, k4);
-            times_tokens(y, fl, Sl, k4);
+            times_tokens(y, fh, Wt, k4);
+            times_tokens(y, fl, Wt, k4);
         }
         const float *rho = a.rho + (size_t)blockIdx.x * D + d0 + 2 * c;
 #pragma unroll
@@ -1648,7 +1716,9 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grads_tc(DeltaTcArgs a,
             if (i + x >= w.cnt) continue;
             const float h = end + s - (x ? h0 : 0.f);
             a.dla[row0 + i + x] = __float2bfloat16_rn(w.ch == 0 && i + x == 0 ? 0.f : h);  // the first decay meets an empty memory
-            a.dbe[row0 + i + x] = __float2bfloat16_rn(rowsum[i + x] + rowsum[kCH + i + x]);
+            // w_t . e_t / beta_t; without a beta_t, e_t . (N_t k_t) through the pairs, whose terms may cancel
+            const int t = i + x;
+            a.dbe[row0 + t] = __float2bfloat16_rn(fabsf(bet[t]) > 1e-20f ? we[t] / bet[t] : rowsum[t] + rowsum[kCH + t]);
         }
     }
 }
@@ -1687,7 +1757,8 @@ cudaError_t grads_tc_impl(const Problem &p, const DeltaTcArgs &a, cudaStream_t s
     GradMaps maps;
     const unsigned long long chunks = (unsigned long long)p.BH * p.N * a.NCH;
     auto tokens = [&](CUtensorMap *m, const void *x) { return make_tmap_bf16_3d_sw128(m, x, p.BH, p.L, D, kCH); };
-    if (!tokens(&maps.dy, a.dy) || !tokens(&maps.e, a.E) || !tokens(&maps.w, a.dv) || !tokens(&maps.q, a.q) || !tokens(&maps.k, a.k) ||
+    if (!tokens(&maps.dy, a.dy) || !tokens(&maps.e, a.E) || !tokens(&maps.w, a.dv) || !tokens(&maps.e_lo, a.E_lo) ||
+        !tokens(&maps.w_lo, a.W_lo) || !tokens(&maps.q, a.q) || !tokens(&maps.k, a.k) ||
         !tokens(&maps.u, a.pw ? a.u : a.k) || !make_tmap_bf16_3d_sw128(&maps.S, a.S_c, chunks, D, D, 64) ||
         !make_tmap_bf16_3d_sw128(&maps.R, a.R_c, chunks, D, D, 64))
         return cudaErrorUnknown;

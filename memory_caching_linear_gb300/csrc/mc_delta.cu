@@ -272,6 +272,8 @@ int backward_delta(const void *q, const void *k, const void *v, const void *u, c
         t.rec = cv.take<uint8_t>(BH * N * NCH * kDeltaRecBytes, tc);
         t.rrec = cv.take<uint8_t>(BH * N * NCH * kDeltaRRecBytes, tc);
         t.E = cv.take<__nv_bfloat16>(BH * L * d, tc);
+        t.E_lo = cv.take<__nv_bfloat16>(BH * L * d, tc);
+        t.W_lo = cv.take<__nv_bfloat16>(BH * L * d, tc);
         t.S_c = cv.take<__nv_bfloat16>(BH * N * NCH * d * d, tc);
         t.R_c = cv.take<__nv_bfloat16>(BH * N * NCH * d * d, tc);
         a.states = cv.take<float>(BH * N * d * d, many);

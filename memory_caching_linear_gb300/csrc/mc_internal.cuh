@@ -326,7 +326,7 @@ struct DeltaTcArgs {
     __nv_bfloat16 *y;      // online reads in bf16 (one segment), or null
     float *O_on;           // online reads in fp32, or null
     float *states;         // [BH][N][d][d], or null
-    __nv_bfloat16 *E;      // [BH][L][d] e_t, or null
+    __nv_bfloat16 *E, *E_lo;  // [BH][L][d] e_t in two terms, or null
     __nv_bfloat16 *S_c;    // [BH][N][NCH][d][d] memory before every chunk, or null
     uint8_t *states_img;   // the readout's images (tc_forward_images), or null
     // gradients
@@ -339,6 +339,7 @@ struct DeltaTcArgs {
     const float *dq_add;   // [BH][L][d] added to dq, or null
     const float *rho;      // [BH][N][NCH][d], with pw
     __nv_bfloat16 *R_c;    // [BH][N][NCH][d][d] adjoint after every chunk
+    __nv_bfloat16 *W_lo;   // [BH][L][d] what the rounding of dv = w_t leaves
     __nv_bfloat16 *dq, *dk, *dv, *dla, *dbe;
     int BH, L, C, N, NCH;
     int give_up;           // kGiveUp*: waits that are taken for ones that gave up (set by the launchers)

@@ -79,3 +79,39 @@ def test_reads_of_resembling_keys(C, L, spread, beta, d, mode, topk):
     x = resembling(L, d, spread, beta)
     y, _ = forward(*x, C, mode, topk)
     assert rel(mcl.mc_forward_delta(*cuda(x), C, mode, topk)[0], y) <= TOL["bf16"]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("spread,beta", [(0.05, 1.0), (0.05, 1.9), (0.3, 1.9)])
+@pytest.mark.parametrize("C,L", [(128, 256), (130, 260), (192, 256), (256, 256)])
+def test_gradients_of_resembling_keys(C, L, spread, beta, d):
+    """Sums over pairs of tokens cancel here; formed in two bf16 terms, 2^-17, as is the adjoint's read, they leave the 1e-2 of
+    bf16 results (in one term dq and dbeta were 5e-2 off).  dlog_alpha is a difference of reads and writes: its bound is that
+    of test_keys_that_resemble_each_other."""
+    x = resembling(L, d, spread, beta)
+    dy = torch.randn(x[0].shape, generator=torch.Generator().manual_seed(9)).to(x[0].dtype)
+    tol = {"dlog_alpha": 2.7e-2 * max(1.0, beta) ** 2}
+    for name, g, w in zip(NAMES, mcl.mc_backward_delta(*cuda(x), dy.cuda(), C, GRM), backward(*x, dy, C, GRM)):
+        assert rel(g, w) <= tol.get(name, TOL["bf16"]), name
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("C,L,mode", [(128, 256, GRM), (128, 256, RESIDUAL), (130, 260, GRM), (256, 256, GRM)])
+def test_gradients_in_the_mean(C, L, mode, d):
+    """In the 2-norm a rounding to bf16 is 1.7e-3 (2^-8 / sqrt(3) times the mean of a value over its power of two, 0.74).  A
+    gradient has its own, that of the state or adjoint it reads, and, behind gates, theirs: 1.7e-3 * sqrt(3) = 2.9e-3."""
+    x = make_delta_inputs(2, 3, L, d, C, 7 + d, "bf16")
+    dy = torch.randn(x[0].shape, generator=torch.Generator().manual_seed(9)).to(x[0].dtype)
+    for name, g, w in zip(NAMES, mcl.mc_backward_delta(*cuda(x), dy.cuda(), C, mode), backward(*x, dy, C, mode)):
+        if g is not None and name != "dlog_alpha" and w.any():
+            assert float((g.double().cpu() - w).norm() / w.norm()) <= 2.9e-3, name
+
+
+@pytest.mark.parametrize("d,C,L", [(16, 20, 61), (32, 64, 129), (64, 64, 192), (64, 128, 512), (128, 130, 300), (128, 128, 384), (128, 257, 257)])
+@pytest.mark.parametrize("mode,topk", [(RESIDUAL, 0), (GRM, 0), (SSC, 1)])
+def test_states_or_not_the_same_y(d, C, L, mode, topk):
+    """A call that returns no states, as the autograd function makes it, forms the same y, bit for bit."""
+    x = cuda(make_delta_inputs(2, 2, L, d, C, d + C, "bf16"))
+    y, st = mcl.mc_forward_delta(*x, C, mode, topk)
+    again, none = mcl.mc_forward_delta(*x, C, mode, topk, want_states=False)
+    assert none is None and torch.equal(again, y)
