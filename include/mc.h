@@ -235,11 +235,12 @@ int mc_decode_step(const void *q, const void *k, const void *v, const void *u,
  *                     stays bounded for beta in [0, 2].
  *   states          : as mc_forward (fp32 whatever the element type); may be NULL.
  *   is_bf16         : q, k, v, u, log_alpha, beta and y are bf16 if non-zero, fp32 otherwise.
- *   Every d of mc_forward, any seg_len, L up to 2^30; errors as mc_forward.  No
- *   input may share memory with an output.  With bf16 inputs the states come out to a few parts in 1e5 (1e4 where
- *   all keys of a segment are nearly parallel and beta is close to 2), and y, relative to its
- *   largest value, to 1e-2: its rounding to bf16, and that of the gates and cached states.  With fp32
- *   inputs both are within 1e-4.
+ *   Every d of mc_forward, any seg_len, L up to 2^30; errors as mc_forward.  No input may share
+ *   memory with an output.
+ *   Accuracy, relative to an output's largest value: with bf16 inputs the states come out to a few
+ *   parts in 1e5 (1e4 where all keys of a segment are nearly parallel and beta is close to 2) and y to
+ *   1e-2: its rounding to bf16, and that of the gates and cached states.  With fp32 inputs both are
+ *   within 1e-4.
  */
 int mc_forward_delta(const void *q, const void *k, const void *v, const void *u,
                      const void *log_alpha, const void *beta, int B, int H, int L, int d,
@@ -258,7 +259,8 @@ int mc_forward_delta(const void *q, const void *k, const void *v, const void *u,
  *   Accuracy, relative to a gradient's largest value: fp32 inputs 1e-4; bf16 ones, rounded to bf16
  * at the end, 1e-2.  Where all keys of a segment are nearly parallel what a token writes undoes what
  * the one before wrote, and with bf16 inputs and d >= 64 dlog_alpha, a difference of large terms,
- * can be several 1e-2 off.
+ * can be several 1e-2 off.  With a router dk can differ from run to run by an fp32 rounding of its
+ * part through the pooled keys.
  */
 int mc_backward_delta(const void *q, const void *k, const void *v, const void *u,
                       const void *log_alpha, const void *beta, const void *dy, int B, int H, int L,

@@ -1,0 +1,57 @@
+"""Calls of the gated delta memory that are allowed and easily overlooked."""
+import pytest
+import torch
+
+import memory_caching_linear_gb300 as mcl
+from delta_ref import GRM, RESIDUAL, SOUP, SSC, make_delta_inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from memory_caching_linear_gb300 import build
+    build.build()
+    mcl.load_library()
+
+
+@pytest.mark.parametrize("mode", [GRM, SOUP, SSC])
+@pytest.mark.parametrize("d,dtype", [(32, "f32"), (64, "bf16"), (128, "bf16")])
+def test_one_segment_without_router_input(d, dtype, mode):
+    L = 150
+    q, k, v, _, la, be = (t.cuda() for t in make_delta_inputs(1, 2, L, d, L, d, dtype))
+    dy = torch.randn_like(q)
+    want, st = mcl.mc_forward_delta(q, k, v, None, la, be, L, RESIDUAL)
+    for seg_len in (L, (1 << 32) + 5):  # a segment of more tokens than there are, past 32 bits too
+        got, gst = mcl.mc_forward_delta(q, k, v, None, la, be, seg_len, mode, 2)
+        assert torch.equal(got, want) and torch.equal(gst, st)
+    grads = mcl.mc_backward_delta(q, k, v, None, la, be, dy, L, RESIDUAL)
+    got = mcl.mc_backward_delta(q, k, v, None, la, be, dy, (1 << 32) + 5, mode, 2)
+    assert not got[3].any()
+    for g, w in zip(got[:3] + got[4:], grads[:3] + grads[4:]):
+        assert torch.equal(g, w)
+    leaf = [t.clone().requires_grad_() for t in (q, k, v, la, be)]
+    mcl.DeltaMemoryCaching.apply(*leaf[:3], None, *leaf[3:], L, mode, 2).backward(dy)
+    for t, w in zip(leaf, grads[:3] + grads[4:]):
+        assert torch.equal(t.grad, w)
+
+
+@pytest.mark.parametrize("C", [128, 70, 300])
+def test_two_streams_at_once(C):
+    """Calls on two streams share nothing: each has its own scratch."""
+    xs = [[t.cuda() for t in make_delta_inputs(1, 4, 300 if C != 128 else 384, 64, C, s, "bf16")] for s in (1, 2)]
+    dys = [torch.randn_like(x[0]) for x in xs]
+    want = [mcl.mc_forward_delta(*x, C, GRM) for x in xs]
+    grads = [mcl.mc_backward_delta(*x, dy, C, RESIDUAL) for x, dy in zip(xs, dys)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    out = [[], []]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                out[i].append((mcl.mc_forward_delta(*xs[i], C, GRM), mcl.mc_backward_delta(*xs[i], dys[i], C, RESIDUAL)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for fwd, bwd in out[i]:
+            assert all(torch.equal(a, b) for a, b in zip(fwd, want[i]))
+            assert all(a is b or torch.equal(a, b) for a, b in zip(bwd, grads[i]))
