@@ -19,7 +19,7 @@
 // and cancel in S, in O and in the gradients' sums over pairs, so one term (2^-9) would show: at keys with a cosine of 0.8 it
 // leaves the memory 7e-3 and y 9e-3 off, as against 2e-5 and 1.4e-3, the last bf16 rounding, and at all but parallel ones
 // dq and dbeta 5e-2.  One term's are readings in which nothing cancels and whose results are bf16: O's of S, and in the
-// gradients' kernels S and R at a chunk's ends; E's of S in their own walk leaves S 4e-4 off there (122 instead of 140 us at
+// gradients' kernels S and R at a chunk's ends; E's of S in their own walk leaves S 4e-4 off there (135 instead of 150 us at
 // L = 2048, 96 heads, d = 128).
 #include <atomic>
 #include <cstdint>
@@ -600,7 +600,7 @@ struct WalkSmem {
 };
 
 template <int D, int NW, int KP, bool READ, bool FULL>
-__global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? (READ ? 2 : 3) : 1) delta_walk_tc(DeltaTcArgs a, const __grid_constant__ DeltaMaps maps)
+__global__ void __launch_bounds__(32 * NW * KP, KP == 1 ? 2 : 1) delta_walk_tc(DeltaTcArgs a, const __grid_constant__ DeltaMaps maps)
 {
     using W = WalkSmem<D, NW, KP, READ>;
     constexpr int NT = 32 * NW * KP, KS = D / 16 / KP;
@@ -1734,7 +1734,7 @@ bool make_maps(DeltaMaps *m, const Problem &p, const DeltaTcArgs &a, const void 
 // Few walkers leave most of the card idle, and a chunk's products on a walker's way to the next chunk are what counts: then
 // two warps share 16 rows, half of the keys each.  KP = 2 with two row groups per CTA as long as every CTA has an SM to
 // itself, else four row groups and whole rows.  L = 2048, d = 128, one memory (forward, recomputed, reverse walk), KP = 2
-// against 1: 32 heads (128 CTAs) 81 64 74 against 103 77 96 us; 48 heads (192 CTAs) 156 93 139 against 103 76 96 us.
+// against 1: 32 heads (128 CTAs) 80 66 82 against 103 83 113 us; 48 heads (192 CTAs) 155 97 156 against 103 82 113 us.
 inline bool split_keys(const Problem &p) { return (long long)p.BH * p.N * (p.d / 32) <= 152; }
 
 template <int D, int NW, int KP>
