@@ -271,7 +271,7 @@ int mc_backward_delta(const void *q, const void *k, const void *v, const void *u
 
 /*
  * mc_decode_step_delta -- mc_decode_step over the gated delta memory: log_alpha and beta are
- * the token's, [B][H], of q's element type; caches, rules and errors as mc_decode_step.  Run
+ * the token's, [B][H], of q's element type and aligned to it; caches, rules and errors as mc_decode_step.  Run
  * from t = 0 it reproduces mc_forward_delta token by token.
  */
 int mc_decode_step_delta(const void *q, const void *k, const void *v, const void *u,
@@ -292,7 +292,8 @@ int mc_decode_step_delta(const void *q, const void *k, const void *v, const void
  * 0.  Heads choose independently.  The token still reads the segment that it drives out.
  *   t        : the token's position, any number >= 0.  Start from empty slots (slot_seg = -1,
  *              mass = 0) at t = 0, or from mc_cache_compact's cache at t = L.
- *   log_alpha, beta : the token's, for the gated delta memory; both NULL for the linear one.
+ *   log_alpha, beta : the token's, as in mc_decode_step_delta, for the gated delta memory; both NULL
+ *              for the linear one.
  *   agg_mode : MC_GRM, MC_SOUP or MC_SSC (equal scores: the older segment first); the
  *              aggregations with constant gates return MC_ERR_MODE.
  *   protect  : 0 .. n_max - 1; n_max: 1 .. 64.

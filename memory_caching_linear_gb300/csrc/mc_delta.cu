@@ -397,8 +397,9 @@ int decode_slots(SlotArgs a, int B, int H, int seg_len, int agg_mode, int topk, 
     if (any_null({a.q, a.k, a.v, a.y, a.states, a.kbar, a.online, a.ksum}) || (routed && !a.u)) return MC_ERR_NULL;
     if (evict && any_null({a.mass, a.slot_seg})) return MC_ERR_NULL;
     if (evict ? !a.la != !a.be : !a.la || !a.be) return MC_ERR_NULL;
-    if (any_misaligned({a.q, a.k, a.v, a.u, a.la, a.be, a.y, a.states, a.kbar, a.online, a.ksum, a.mass, a.slot_seg}))
-        return MC_ERR_ALIGN;
+    if (any_misaligned({a.q, a.k, a.v, a.u, a.y, a.states, a.kbar, a.online, a.ksum, a.mass, a.slot_seg})) return MC_ERR_ALIGN;
+    // one number per head: a token's, wherever it lies in a sequence's [B][H][L]
+    if ((reinterpret_cast<uintptr_t>(a.la) | reinterpret_cast<uintptr_t>(a.be)) & (a.bf16 ? 1u : 3u)) return MC_ERR_ALIGN;
     if ((st = check_device()) != MC_OK) return st;
     a.BH = B * H;
     a.C = seg_len;

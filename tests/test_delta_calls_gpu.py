@@ -55,3 +55,19 @@ def test_two_streams_at_once(C):
         for fwd, bwd in out[i]:
             assert all(torch.equal(a, b) for a, b in zip(fwd, want[i]))
             assert all(a is b or torch.equal(a, b) for a, b in zip(bwd, grads[i]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_one_head_decodes_from_slices_of_its_sequence(dtype):
+    """With B = H = 1 a token's slice is contiguous where it lies: log_alpha and beta at any element."""
+    L, d, C = 9, 32, 4
+    x = [t.cuda() for t in make_delta_inputs(1, 1, L, d, C, 17, dtype)]
+    a, b = mcl.DecodeCache(1, 1, d, C, 4), mcl.DecodeCache(1, 1, d, C, 4)
+    e, f = mcl.EvictingCache(1, 1, d, C, 2), mcl.EvictingCache(1, 1, d, C, 2)
+    for j in range(L):
+        tok = [t[:, :, j] for t in x]
+        own = [t.clone() for t in tok]
+        assert tok[4].is_contiguous() and (j == 0 or tok[4].data_ptr() != own[4].data_ptr())
+        assert torch.equal(mcl.mc_decode_step_delta(a, *tok, GRM), mcl.mc_decode_step_delta(b, *own, GRM))
+        got = mcl.mc_decode_step_evict(e, *tok[:4], GRM, log_alpha=tok[4], beta=tok[5])
+        assert torch.equal(got, mcl.mc_decode_step_evict(f, *own[:4], GRM, log_alpha=own[4], beta=own[5]))
