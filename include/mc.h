@@ -259,9 +259,9 @@ int mc_forward_delta(const void *q, const void *k, const void *v, const void *u,
  * tokens is one) two d x d states (of the element type; fp32 for d < 64) and, for bf16 with
  * d >= 64, 42 KB of pair products; and about 4 L d floats.
  *   Accuracy, relative to a gradient's largest value: fp32 inputs 1e-4; bf16 ones, rounded to bf16
- * at the end, 1e-2.  Where all keys of a segment are nearly parallel what a token writes undoes what
- * the one before wrote, and with bf16 inputs and d >= 64 dlog_alpha, a difference of large terms,
- * can be several 1e-2 off.  With a router dk can differ from run to run by an fp32 rounding of its
+ * at the end, 1e-2.  dlog_alpha is a difference of larger terms: with bf16 inputs and d >= 64 2e-2,
+ * and several 1e-2 where all keys of a segment are nearly parallel and what a token writes undoes
+ * what the one before wrote.  With a router dk can differ from run to run by an fp32 rounding of its
  * part through the pooled keys.
  */
 int mc_backward_delta(const void *q, const void *k, const void *v, const void *u,

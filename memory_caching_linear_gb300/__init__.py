@@ -366,6 +366,13 @@ def _c_ints(seg_len, topk, L):
     return min(int(seg_len), L), min(int(topk), L)
 
 
+def _gate(t, name, dtype, shape, dev, stream):
+    """log_alpha or beta of a sequence.  The library wants 16-byte aligned arrays, and a part of a batch, t[b:b + 1], begins
+    at any element: such a one is copied (on the current stream: not where another is asked for)."""
+    _check(t, name, dtype, shape, dev)
+    return t.clone() if stream is None and t.data_ptr() % 16 else t
+
+
 _HERE = contextlib.nullcontext()
 
 
@@ -383,8 +390,8 @@ def mc_forward_delta(q, k, v, u, log_alpha, beta, seg_len: int, agg_mode: int, t
     (B, H, L, d), dev, dtype = _sequence_args(q, [("q", q), ("k", k), ("v", v)], 4)
     if u is not None:
         _check(u, "u", dtype, q.shape, dev)
-    _check(log_alpha, "log_alpha", dtype, (B, H, L), dev)
-    _check(beta, "beta", dtype, (B, H, L), dev)
+    log_alpha = _gate(log_alpha, "log_alpha", dtype, (B, H, L), dev, stream)
+    beta = _gate(beta, "beta", dtype, (B, H, L), dev, stream)
     seg_len, topk = _c_ints(seg_len, topk, L)
     y = _new(y, "y", dtype, q.shape, dev)
     if states is not None or want_states:
@@ -409,8 +416,8 @@ def mc_backward_delta(q, k, v, u, log_alpha, beta, dy, seg_len: int, agg_mode: i
         q, [("q", q), ("k", k), ("v", v), ("dy", dy)], 4)
     if u is not None:
         _check(u, "u", dtype, q.shape, dev)
-    _check(log_alpha, "log_alpha", dtype, (B, H, L), dev)
-    _check(beta, "beta", dtype, (B, H, L), dev)
+    log_alpha = _gate(log_alpha, "log_alpha", dtype, (B, H, L), dev, stream)
+    beta = _gate(beta, "beta", dtype, (B, H, L), dev, stream)
     seg_len, topk = _c_ints(seg_len, topk, L)
     dq, dk, dv = (_new(t, n, dtype, q.shape, dev) for t, n in ((dq, "dq"), (dk, "dk"), (dv, "dv")))
     if du is not None or agg_mode in (MC_GRM, MC_SOUP, MC_SSC):

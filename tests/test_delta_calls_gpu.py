@@ -71,3 +71,22 @@ def test_one_head_decodes_from_slices_of_its_sequence(dtype):
         assert torch.equal(mcl.mc_decode_step_delta(a, *tok, GRM), mcl.mc_decode_step_delta(b, *own, GRM))
         got = mcl.mc_decode_step_evict(e, *tok[:4], GRM, log_alpha=tok[4], beta=tok[5])
         assert torch.equal(got, mcl.mc_decode_step_evict(f, *own[:4], GRM, log_alpha=own[4], beta=own[5]))
+
+
+@pytest.mark.parametrize("C", [33, 11])
+def test_parts_of_a_batch(C):
+    """x[b:b + 1] of a batch is contiguous; its log_alpha and beta begin at any element."""
+    x = [t.cuda() for t in make_delta_inputs(3, 1, 33, 64, C, 19, "bf16")]
+    dy = torch.randn_like(x[0])
+    y, st = mcl.mc_forward_delta(*x, C, GRM)
+    grads = mcl.mc_backward_delta(*x, dy, C, RESIDUAL)
+    for b in range(3):
+        part = [t[b:b + 1] for t in x]
+        assert b == 0 or part[4].data_ptr() % 16
+        gy, gst = mcl.mc_forward_delta(*part, C, GRM)
+        assert torch.equal(gy, y[b:b + 1]) and torch.equal(gst, st[b:b + 1])
+        for g, w in zip(mcl.mc_backward_delta(*part, dy[b:b + 1], C, RESIDUAL), grads):
+            assert w is None or torch.equal(g, w[b:b + 1])
+        leaf = [t.clone().requires_grad_() for t in part[:3]]
+        mcl.DeltaMemoryCaching.apply(*leaf, None, part[4], part[5], C, RESIDUAL, 0).backward(dy[b:b + 1])
+        assert torch.equal(leaf[0].grad, grads[0][b:b + 1])
