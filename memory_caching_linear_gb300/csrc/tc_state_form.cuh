@@ -919,15 +919,14 @@ __global__ void __launch_bounds__(kT2Threads, kT2CtasPerSm)
                     tma_load_2d(dst, &mK, 64 * h, rr, &ring_full[g % kRing]);
                     ++g;
                 }
-                if (ON) {
-                } else if (D == 128) {
+                if (!ON && D == 128) {
                     for (int h = 0; h < 2 && ok; ++h) {  // keys 64h .. 64h + 63, both 64-wide halves of v
                         if (!(ok = (dst = slot(kPanel)) != nullptr)) break;
                         tma_load_2d(dst, &mV, 0, rr + 64 * h, &ring_full[g % kRing]);
                         tma_load_2d(dst + kPanel / 2, &mV, 64, rr + 64 * h, &ring_full[g % kRing]);
                         ++g;
                     }
-                } else if (ok) {  // all 128 keys of the 64-wide v in one panel
+                } else if (!ON && ok) {  // all 128 keys of the 64-wide v in one panel
                     if ((ok = (dst = slot(kPanel)) != nullptr)) {
                         tma_load_2d(dst, &mV, 0, rr, &ring_full[g % kRing]);
                         tma_load_2d(dst + kPanel / 2, &mV, 0, rr + 64, &ring_full[g % kRing]);
@@ -993,37 +992,37 @@ __global__ void __launch_bounds__(kT2Threads, kT2CtasPerSm)
                 if (ON) {
                     g += NP;  // the Q panels, released by the workers
                 } else {
-                // G = Q K^T
-                for (int h = 0; h < NP; ++h) {
-                    const uint32_t sq = g % kRing, sk = (g + 1) % kRing;
-                    if (!(ok = ring_ready(g) && ring_ready(g + 1))) break;
-                    tc_fence_after();
-                    const uint64_t dq = make_desc_sw128(s_base + sq * kPanel, 0, 1024);
-                    const uint64_t dk = make_desc_sw128(s_base + sk * kPanel, 0, 1024);
+                    // G = Q K^T
+                    for (int h = 0; h < NP; ++h) {
+                        const uint32_t sq = g % kRing, sk = (g + 1) % kRing;
+                        if (!(ok = ring_ready(g) && ring_ready(g + 1))) break;
+                        tc_fence_after();
+                        const uint64_t dq = make_desc_sw128(s_base + sq * kPanel, 0, 1024);
+                        const uint64_t dk = make_desc_sw128(s_base + sk * kPanel, 0, 1024);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) mma_ss(tD, dq + 2 * kk, dk + 2 * kk, idKm, (h | kk) != 0);
-                    mma_commit(&ring_empty[sk]);  // the Q panel is released by the workers
-                    g += 2;
-                }
-                if (!ok) break;
-                mma_commit(&g_full);
-                // D = P V once the workers have read G and written P
-                const uint32_t ps = ac % 2;
-                if (!(ok = mbar_wait(&a_full[ps], (ac / 2) & 1, &abort_flag))) break;
-                for (int h = 0; h < NP; ++h) {  // V panels: 128 / NP keys each
-                    const uint32_t s = g % kRing;
-                    if (!(ok = ring_ready(g))) break;
-                    tc_fence_after();
-                    const uint64_t dv = make_desc_sw128(s_base + s * kPanel, kPanel / 2, 1024);
+                        for (int kk = 0; kk < 4; ++kk) mma_ss(tD, dq + 2 * kk, dk + 2 * kk, idKm, (h | kk) != 0);
+                        mma_commit(&ring_empty[sk]);  // the Q panel is released by the workers
+                        g += 2;
+                    }
+                    if (!ok) break;
+                    mma_commit(&g_full);
+                    // D = P V once the workers have read G and written P
+                    const uint32_t ps = ac % 2;
+                    if (!(ok = mbar_wait(&a_full[ps], (ac / 2) & 1, &abort_flag))) break;
+                    for (int h = 0; h < NP; ++h) {  // V panels: 128 / NP keys each
+                        const uint32_t s = g % kRing;
+                        if (!(ok = ring_ready(g))) break;
+                        tc_fence_after();
+                        const uint64_t dv = make_desc_sw128(s_base + s * kPanel, kPanel / 2, 1024);
 #pragma unroll
-                    for (int kk = 0; kk < 8 / NP; ++kk)
-                        mma_ts(tD, tA0 + ps * 64 + ((8 / NP) * h + kk) * 8, dv + kk * (2048u >> 4), idPV, (h | kk) != 0);
-                    mma_commit(&ring_empty[s]);
-                    ++g;
-                }
-                if (!ok) break;
-                mma_commit(&a_empty[ps]);
-                ++ac;
+                        for (int kk = 0; kk < 8 / NP; ++kk)
+                            mma_ts(tD, tA0 + ps * 64 + ((8 / NP) * h + kk) * 8, dv + kk * (2048u >> 4), idPV, (h | kk) != 0);
+                        mma_commit(&ring_empty[s]);
+                        ++g;
+                    }
+                    if (!ok) break;
+                    mma_commit(&a_empty[ps]);
+                    ++ac;
                 }
                 // D += (g_i o Q) X_i^T
                 const int items = tile_items<GATED, ON>(t);
