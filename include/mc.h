@@ -328,6 +328,109 @@ int mc_cache_compact(const void *k, const void *u, const float *prefill_states, 
                      int n_max, float *prefill_mass, int is_bf16, mc_stream_t stream);
 
 /*
+ * A paged cache: the decoding caches of up to n_seqs sequences, each at a position of its own, over one pool of pages.  A
+ * page holds one completed segment of one sequence (every head's memory and mean key); sequences that went on from the same
+ * prompt name the same pages.  All memory is the caller's, on the device; a library call works on it in stream order.
+ *   pages, kbar  : fp32 [n_pages][H][d][d] and [n_pages][H][d].
+ *   refs         : int32 [n_pages], how many tables name a page; 0 is a free one, whose contents are anything.
+ *   online, ksum : fp32 [n_seqs][H][d][d] and [n_seqs][H][d], the begun segment's memory and key sum; anything where pos is a
+ *                  multiple of seg_len.
+ *   table        : int32 [n_seqs][n_max], page of segment i; -1 from segment pos / seg_len on, and for one that found no
+ *                  page (it is not there: no gate, no read).
+ *   pos          : int32 [n_seqs], tokens seen, 0 .. 2^30.  An empty slot is a sequence at 0.
+ *   row          : int32 [n_seqs], a permutation: slot x's online, ksum, table and pos lie in row row[x].
+ *   status       : int32 [1], an OR of MC_PAGES_* that calls set and nobody clears but the caller:
+ *                    MC_PAGES_INDEX      a slot, parent, node, count, row or position out of range, or a slot that two
+ *                                        rows of one writing call name: taken as said below, never followed
+ *                    MC_PAGES_NONE_FREE  a segment found no free page and is lost
+ *                    MC_PAGES_TABLE_FULL a sequence has more than n_max segments; those after are lost
+ *   n_seqs, n_max: 1 .. 1024; n_pages: 1 .. 2^20; seg_len >= 1; d as for every call.
+ * An empty cache has refs, pos and status zero, table -1 and row the identity.  New pages are the lowest free ones, given out
+ * in the order of the batch's rows and of time.  The batch of a call is B <= n_seqs rows of tokens; slots (int32 [B],
+ * device, NULL: row b is slot b) says whose they are, -1 (a row to pad with) nobody's: such a row is not read and its outputs
+ * stay as they are.  Every call returns without synchronising, takes positions from the device, and may be captured
+ * into a graph and replayed.  Two calls on one cache are ordered by the caller unless both only read it (mc_decode_tree, and
+ * mc_pages_compact of its source).  Integer arrays are aligned to 4 bytes, log_alpha and beta to their element, all others
+ * to 16.  No input shares memory with an output.
+ */
+typedef struct {
+    float *pages, *kbar;
+    int32_t *refs;
+    float *online, *ksum;
+    int32_t *table, *pos, *row, *status;
+    int32_t n_pages, n_seqs, H, d, seg_len, n_max;
+} mc_paged_cache;
+
+enum { MC_PAGES_INDEX = 1, MC_PAGES_NONE_FREE = 2, MC_PAGES_TABLE_FULL = 4 };
+
+/*
+ * mc_decode_step_paged -- one decoding step of every sequence in the batch, as mc_decode_step treats its token; a segment that it
+ * completes gets a page.
+ *   q, k, v, u      : the tokens, [B][H][d] (u may be NULL for Residual and Mean); y: the same, written.
+ *   log_alpha, beta : [B][H] for the gated delta memory, both NULL for the linear one.
+ *   slots           : as above; a slot that comes twice is the first row's alone.
+ *   agg_mode        : every mc_agg_mode.  topk (SSC): any number >= 0; equal scores: the older segment.
+ * Errors as mc_decode_step.
+ */
+int mc_decode_step_paged(const mc_paged_cache *cache, const void *q, const void *k, const void *v, const void *u,
+                         const void *log_alpha, const void *beta, const int32_t *slots, int B, int agg_mode, int topk,
+                         void *y, int is_bf16, mc_stream_t stream);
+
+/*
+ * mc_decode_tree -- what T drafted tokens of every sequence would read, the cache left as it is.  Node n goes on from node
+ * parent[n] < n, or from the cache (-1): it reads what mc_decode_step_paged would read after the tokens on its path, segments
+ * that the path itself completes among it.
+ *   q, k, v, u, y   : [B][H][T][d]; log_alpha, beta [B][H][T] or both NULL.
+ *   parent          : int32 [B][T], device (NULL only for T = 1).  A parent out of range is taken as -1.
+ *   count           : int32 [B], device: sequence b's nodes are 0 .. count[b] - 1; the others are not read (nor their parents)
+ *                     and their y stays as it is.  NULL: T.  Numbers outside 0 .. T are taken as the nearest in it.
+ *   slots           : as above; a slot may come any number of times.
+ *   T               : 1 .. 64.  Other arguments and errors as mc_decode_step_paged.
+ * Accuracy as mc_decode_step: fp32 inputs 1e-4, bf16 ones 1e-2 of the largest value.  With bf16 inputs, d >= 64, T > 8 and no
+ * SSC the cached memories are rounded to the tensor cores' 11 significant bits on the way (2^-11 of their values, against
+ * the 2^-9 of y's own rounding).
+ */
+int mc_decode_tree(const mc_paged_cache *cache, const void *q, const void *k, const void *v, const void *u,
+                   const void *log_alpha, const void *beta, const int32_t *parent, const int32_t *count,
+                   const int32_t *slots, int B, int T, int agg_mode, int topk, void *y, int is_bf16, mc_stream_t stream);
+
+/*
+ * mc_tree_accept -- the tokens on the path to node last[b] join sequence b (none for -1): its memory, key sum, position and,
+ * where segments are completed, pages, as mc_decode_step_paged over them one by one.
+ *   k, v, log_alpha, beta, parent, slots, T : the draft's, as mc_decode_tree was given (a slot that comes twice is the first
+ *                     row's alone).  last: int32 [B], device; out of range is taken as -1, a parent out of range ends the path.
+ */
+int mc_tree_accept(const mc_paged_cache *cache, const void *k, const void *v, const void *log_alpha, const void *beta,
+                   const int32_t *parent, const int32_t *last, const int32_t *slots, int B, int T, int is_bf16,
+                   mc_stream_t stream);
+
+/*
+ * mc_pages_fork -- every slot x goes on from what slot src[x] held before the call: src[x] = x stays, src[x] = -1 frees the
+ * slot, and one src may come any number of times (beams that swap, samples of one prompt).  Pages are shared, not copied;
+ * those that no table names any more are free.  A row that somebody goes on from stays in place and is that slot's (its own
+ * if it stays, else the lowest's); the other slots get copies in, or keep, the rows left over, both in ascending order.
+ *   src : int32 [n_seqs], device.  A number out of range is taken as x.
+ */
+int mc_pages_fork(const mc_paged_cache *cache, const int32_t *src, mc_stream_t stream);
+
+/*
+ * mc_pages_compact -- everything in src to dst, another cache: the live pages come first, in their order, and row becomes the
+ * identity.  What dst held is gone; slots and pages past those of src are empty.  dst has H, d and seg_len of src and at least
+ * its n_seqs and n_max; its pages may be fewer (a live page that has no place is lost: MC_PAGES_NONE_FREE in dst's status).
+ */
+int mc_pages_compact(const mc_paged_cache *dst, const mc_paged_cache *src, mc_stream_t stream);
+
+/*
+ * mc_pages_load -- a prompt into a slot: its complete segments get pages, an incomplete last one becomes the online memory
+ * (zeros if there is none).  What the slot held is released first.
+ *   k      : the prompt's keys [H][L][d], bf16 if is_bf16 != 0 else fp32.
+ *   states : its prefill's states, fp32 [H][N][d][d], N = ceil(L / seg_len).
+ *   slot   : 0 .. n_seqs - 1.  L: 1 .. 2^30 with L / seg_len <= n_max, else MC_ERR_SHAPE.
+ */
+int mc_pages_load(const mc_paged_cache *cache, int slot, const void *k, const float *states, int L, int is_bf16,
+                  mc_stream_t stream);
+
+/*
  * mc_ssc_select -- the SSC router alone ([MC-sum §3.4]), for inspection and tests.
  *   k, u     : [B][H][L][d], bf16 if is_bf16 != 0 else fp32, device.
  *   idx      : int32 [B][H][L][topk], written: for token t of segment s, the

@@ -26,7 +26,8 @@ MC_ERR_ALLOC, MC_ERR_CUDA, MC_ERR_DEVICE_TIMEOUT, MC_ERR_ALIGN, MC_ERR_DEVICE = 
 MC_ERR_SCRATCH = -10
 
 EXPORTED = ("mc_forward", "mc_forward_f32", "mc_forward_swla", "mc_forward_segments", "mc_log_segments", "mc_backward", "mc_backward_f32", "mc_decode_step", "mc_forward_delta", "mc_backward_delta",
-            "mc_decode_step_delta", "mc_decode_step_evict", "mc_cache_compact", "mc_ssc_select", "mc_forward_host", "mc_forward_noalloc",
+            "mc_decode_step_delta", "mc_decode_step_evict", "mc_cache_compact", "mc_decode_step_paged",
+            "mc_decode_tree", "mc_tree_accept", "mc_pages_fork", "mc_pages_compact", "mc_pages_load", "mc_ssc_select", "mc_forward_host", "mc_forward_noalloc",
             "mc_check_device", "mc_trim_scratch", "mc_set_readout_form", "mc_profile_begin", "mc_profile_end",
             "mc_profile_stage", "mc_status_string")
 MC_READOUT_AUTO, MC_READOUT_FACTORISED = 0, 1
@@ -77,6 +78,18 @@ def load_library():
     lib.mc_decode_step_evict.restype = i
     lib.mc_cache_compact.argtypes = [vp] * 3 + [i] * 8 + [vp] * 6 + [i, vp, i, vp]
     lib.mc_cache_compact.restype = i
+    lib.mc_decode_step_paged.argtypes = [vp] * 8 + [i] * 3 + [vp, i, vp]
+    lib.mc_decode_step_paged.restype = i
+    lib.mc_decode_tree.argtypes = [vp] * 10 + [i] * 4 + [vp, i, vp]
+    lib.mc_decode_tree.restype = i
+    lib.mc_tree_accept.argtypes = [vp] * 8 + [i] * 3 + [vp]
+    lib.mc_tree_accept.restype = i
+    lib.mc_pages_fork.argtypes = [vp, vp, vp]
+    lib.mc_pages_fork.restype = i
+    lib.mc_pages_compact.argtypes = [vp, vp, vp]
+    lib.mc_pages_compact.restype = i
+    lib.mc_pages_load.argtypes = [vp, i, vp, vp, i, i, vp]
+    lib.mc_pages_load.restype = i
     lib.mc_ssc_select.argtypes = [vp, vp, i, i, i, i, i, i, vp, i, vp]
     lib.mc_ssc_select.restype = i
     lib.mc_forward_host.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, i, vp, vp, i, vp]
@@ -571,6 +584,192 @@ def mc_cache_compact(cache: EvictingCache, k, u, states, agg_mode: int, topk: in
         raise MCError(st, "mc_cache_compact")
     cache.t = L
     return mass
+
+
+MC_PAGES_INDEX, MC_PAGES_NONE_FREE, MC_PAGES_TABLE_FULL = 1, 2, 4
+
+
+class _CPagedCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("pages", "kbar", "refs", "online", "ksum", "table", "pos", "row", "status")] + \
+               [(n, ctypes.c_int32) for n in ("n_pages", "n_seqs", "H", "d", "seg_len", "n_max")]
+
+
+class PagedCache:
+    """Decoding caches of up to ``n_seqs`` sequences, each at its own position, over one pool of ``n_pages`` pages (a page: one
+    completed segment's memory and mean key for every head), in which sequences share the pages of what they have in common
+    (``mc_paged_cache`` in mc.h).  ``pages`` [n_pages, H, d, d], ``kbar`` [n_pages, H, d], ``online`` [n_seqs, H, d, d] and
+    ``ksum`` [n_seqs, H, d] are fp32; ``refs`` [n_pages], ``table`` [n_seqs, n_max], ``pos``, ``row`` [n_seqs] and
+    ``status`` [1] int32, all on the device: slot x's online, ksum, table and pos lie in row ``row[x]``.  The tensors are filled
+    in place, never replaced.  A new cache is empty: every slot is a sequence at position 0."""
+
+    def __init__(self, n_seqs: int, H: int, d: int, seg_len: int, n_max: int, n_pages: int, device="cuda"):
+        self.seg_len, self.n_max, self.n_pages, self.n_seqs, self.H, self.d = \
+            int(seg_len), int(n_max), int(n_pages), int(n_seqs), int(H), int(d)
+        if not 1 <= self.seg_len < 1 << 31:
+            raise ValueError("seg_len must be in 1 .. 2^31 - 1")
+        f32, i32 = dict(dtype=torch.float32, device=device), dict(dtype=torch.int32, device=device)
+        self._t = {"pages": torch.zeros((n_pages, H, d, d), **f32), "kbar": torch.zeros((n_pages, H, d), **f32),
+                   "refs": torch.zeros((n_pages,), **i32), "online": torch.zeros((n_seqs, H, d, d), **f32),
+                   "ksum": torch.zeros((n_seqs, H, d), **f32), "table": torch.full((n_seqs, n_max), -1, **i32),
+                   "pos": torch.zeros((n_seqs,), **i32), "row": torch.arange(n_seqs, **i32), "status": torch.zeros((1,), **i32)}
+        self.device = self._t["pages"].device
+        self._c = _CPagedCache(*[t.data_ptr() for t in self._t.values()], self.n_pages, self.n_seqs, self.H, self.d,
+                               self.seg_len, self.n_max)
+        self._ref = ctypes.addressof(self._c)
+
+    pages, kbar, refs, online, ksum, table, pos, row, status = (
+        property(lambda self, n=n: self._t[n]) for n in
+        ("pages", "kbar", "refs", "online", "ksum", "table", "pos", "row", "status"))
+
+    def check(self):
+        """Wait for the device and raise if a call met a bad index, an empty pool or a full table since the last check
+        (``status``, which is cleared)."""
+        bits = int(self.status.item())
+        if bits:
+            self.status.zero_()
+            raise RuntimeError("paged cache: " + ", ".join(t for b, t in (
+                (MC_PAGES_INDEX, "an index out of range or named twice"), (MC_PAGES_NONE_FREE, "no free page"),
+                (MC_PAGES_TABLE_FULL, "more segments than n_max")) if bits & b))
+
+
+def _paged(cache, dev=None):
+    if not isinstance(cache, PagedCache):
+        raise TypeError("cache must be a PagedCache")
+    if cache.device.type != "cuda":
+        raise ValueError("the cache must be on a CUDA device")
+    if dev is not None and cache.device != dev:
+        raise ValueError(f"the cache must be on {dev}")
+
+
+def _paged_batch(cache, first, name, dims):
+    """The batch size of a call whose first token tensor is [B, H, (T,) d]; its checks."""
+    if not isinstance(first, torch.Tensor) or first.dim() != dims:
+        raise ValueError(f"{name} must be [B, H, d]" if dims == 3 else f"{name} must be [B, H, T, d]")
+    if first.device.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    if first.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("inputs must be bf16 or fp32")
+    _paged(cache, first.device)
+    shape = first.shape
+    if shape[1] != cache.H or shape[-1] != cache.d:
+        raise ValueError(f"{name} must have the cache's H = {cache.H} and d = {cache.d}")
+    if not 1 <= shape[0] <= cache.n_seqs:
+        raise ValueError(f"a batch is 1 .. {cache.n_seqs} rows")
+    if dims == 4 and not 1 <= shape[2] <= 64:
+        raise ValueError("a draft has 1 .. 64 nodes")
+
+
+def _tokens_match(first, others, gates, indexes):
+    shape, dev, dtype = first.shape, first.device, first.dtype
+    for t, n in others:
+        if t is not None:
+            _check(t, n, dtype, shape, dev)
+    for t, n in gates:
+        if t is not None:
+            _check(t, n, dtype, shape[:-1], dev)
+    for t, n, want in indexes:
+        if t is not None:
+            _check(t, n, torch.int32, want, dev)
+
+
+def mc_decode_step_paged(cache: PagedCache, q, k, v, u, agg_mode: int, topk: int = 0, *, log_alpha=None, beta=None,
+                         slots=None, y=None, stream=None):
+    """One decoding step of every sequence of the batch (``mc_decode_step_paged`` in mc.h): q, k, v, u [B, H, d], for the
+    gated delta memory log_alpha and beta [B, H]; ``slots`` int32 [B] says whose tokens they are (-1: nobody's; None: row b is slot
+    b).  Positions advance on the device, so the call may be captured and replayed.  Returns y [B, H, d]; rows of nobody stay
+    as they are in a y that is given, and are anything in a new one."""
+    _paged_batch(cache, q, "q", 3)
+    _tokens_match(q, ((q, "q"), (k, "k"), (v, "v"), (u, "u")), ((log_alpha, "log_alpha"), (beta, "beta")),
+                  ((slots, "slots", q.shape[:1]),))
+    y = _new(y, "y", q.dtype, q.shape, q.device)
+    with _on(q.device):
+        st = load_library().mc_decode_step_paged(
+            cache._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(u), _ptr(log_alpha), _ptr(beta), _ptr(slots),
+            q.shape[0], int(agg_mode), max(-1, min(int(topk), 1 << 30)), y.data_ptr(), int(q.dtype == torch.bfloat16),
+            _stream_handle(stream, q.device))
+    if st != MC_OK:
+        raise MCError(st, "mc_decode_step_paged")
+    return y
+
+
+def mc_decode_tree(cache: PagedCache, q, k, v, u, parent, agg_mode: int, topk: int = 0, *, log_alpha=None, beta=None,
+                   count=None, slots=None, y=None, stream=None):
+    """What a tree of T drafted tokens of every sequence would read (``mc_decode_tree`` in mc.h); the cache stays as it is.  q, k,
+    v, u [B, H, T, d], for the gated delta memory log_alpha and beta [B, H, T]; ``parent`` int32 [B, T] (-1: the cache),
+    ``count`` int32 [B] nodes of each sequence (None: T), ``slots`` as in :func:`mc_decode_step_paged`.  Returns y [B, H, T,
+    d]; what is beyond count, and rows of nobody, stay as they are in a y that is given, and are anything in a new one."""
+    _paged_batch(cache, q, "q", 4)
+    B, _, T, _ = q.shape
+    _tokens_match(q, ((q, "q"), (k, "k"), (v, "v"), (u, "u")), ((log_alpha, "log_alpha"), (beta, "beta")),
+                  ((parent, "parent", (B, T)), (count, "count", (B,)), (slots, "slots", (B,))))
+    y = _new(y, "y", q.dtype, q.shape, q.device)
+    with _on(q.device):
+        st = load_library().mc_decode_tree(
+            cache._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(u), _ptr(log_alpha), _ptr(beta), _ptr(parent), _ptr(count),
+            _ptr(slots), B, T, int(agg_mode), max(-1, min(int(topk), 1 << 30)), y.data_ptr(), int(q.dtype == torch.bfloat16),
+            _stream_handle(stream, q.device))
+    if st != MC_OK:
+        raise MCError(st, "mc_decode_tree")
+    return y
+
+
+def mc_tree_accept(cache: PagedCache, k, v, parent, last, *, log_alpha=None, beta=None, slots=None, stream=None):
+    """The drafted tokens on the path to node ``last`` (int32 [B], -1: none) join their sequences (``mc_tree_accept`` in mc.h);
+    the other arguments as :func:`mc_decode_tree` was given them."""
+    _paged_batch(cache, k, "k", 4)
+    B, _, T, _ = k.shape
+    _tokens_match(k, ((k, "k"), (v, "v")), ((log_alpha, "log_alpha"), (beta, "beta")),
+                  ((parent, "parent", (B, T)), (last, "last", (B,)), (slots, "slots", (B,))))
+    with _on(k.device):
+        st = load_library().mc_tree_accept(
+            cache._ref, k.data_ptr(), v.data_ptr(), _ptr(log_alpha), _ptr(beta), _ptr(parent), _ptr(last), _ptr(slots), B, T,
+            int(k.dtype == torch.bfloat16), _stream_handle(stream, k.device))
+    if st != MC_OK:
+        raise MCError(st, "mc_tree_accept")
+
+
+def mc_pages_fork(cache: PagedCache, src, *, stream=None):
+    """Every slot x goes on from what slot src[x] held (``mc_pages_fork`` in mc.h): src int32 [n_seqs] on the device, x to stay, -1
+    to be freed.  Pages are shared; pages that no sequence names any more are free."""
+    _paged(cache)
+    _check(src, "src", torch.int32, (cache.n_seqs,), cache.device)
+    with _on(cache.device):
+        st = load_library().mc_pages_fork(cache._ref, src.data_ptr(), _stream_handle(stream, cache.device))
+    if st != MC_OK:
+        raise MCError(st, "mc_pages_fork")
+
+
+def mc_pages_compact(into: PagedCache, cache: PagedCache, *, stream=None):
+    """Everything of ``cache`` into another one, the live pages first (``mc_pages_compact`` in mc.h): a pool of another size,
+    a copy to go on from, or a pool without holes."""
+    _paged(cache)
+    _paged(into, cache.device)
+    with _on(cache.device):
+        st = load_library().mc_pages_compact(into._ref, cache._ref, _stream_handle(stream, cache.device))
+    if st != MC_OK:
+        raise MCError(st, "mc_pages_compact")
+
+
+def mc_pages_load(cache: PagedCache, slot: int, k, states, *, stream=None):
+    """A prompt into a slot (``mc_pages_load`` in mc.h): its keys [H, L, d] and its prefill's states [H, N, d, d] (one batch
+    entry of what the forward took and returned)."""
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be [H, L, d]")
+    if k.device.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    if k.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("inputs must be bf16 or fp32")
+    _paged(cache, k.device)
+    L = k.shape[1]
+    _check(k, "k", k.dtype, (cache.H, L, cache.d), k.device)
+    _check(states, "states", torch.float32, (cache.H, num_segments(L, cache.seg_len), cache.d, cache.d), k.device)
+    if not 0 <= int(slot) < cache.n_seqs:
+        raise ValueError(f"slot must be 0 .. {cache.n_seqs - 1}")
+    with _on(k.device):
+        st = load_library().mc_pages_load(cache._ref, int(slot), k.data_ptr(), states.data_ptr(), L,
+                                          int(k.dtype == torch.bfloat16), _stream_handle(stream, k.device))
+    if st != MC_OK:
+        raise MCError(st, "mc_pages_load")
 
 
 class MemoryCaching(torch.autograd.Function):

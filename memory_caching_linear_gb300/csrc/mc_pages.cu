@@ -1,0 +1,234 @@
+// mc_pages.cu -- the entry points of decoding over a paged cache (include/mc.h): argument checks, scratch, and the
+// kernels of each call.
+#include <algorithm>
+#include <cstdint>
+#include <initializer_list>
+
+#include "paged.cuh"
+
+namespace mc {
+namespace {
+
+constexpr int kSms = 152;
+
+// A block of stream-ordered scratch handed out in 256-byte aligned pieces (a first walk with a null base adds the sizes up).
+struct Carver {
+    char *base;
+    size_t used;
+    template <typename T>
+    T *take(size_t count)
+    {
+        char *p = base ? base + used : nullptr;
+        used += round_up(sizeof(T) * count);
+        return reinterpret_cast<T *>(p);
+    }
+};
+
+int fail(cudaError_t e)
+{
+    cudaGetLastError();
+    return e == cudaErrorMemoryAllocation ? MC_ERR_ALLOC : MC_ERR_CUDA;
+}
+
+bool aligned(const void *p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
+
+int check_cache(const mc_paged_cache *c, Paged &p)
+{
+    if (!c) return MC_ERR_NULL;
+    if (c->d != 16 && c->d != 32 && c->d != 64 && c->d != 128) return MC_ERR_SHAPE;
+    if (c->H < 1 || c->seg_len < 1 || c->n_seqs < 1 || c->n_seqs > kMaxRows || c->n_max < 1 || c->n_max > kMaxPaged ||
+        c->n_pages < 1 || c->n_pages > (1 << 20))
+        return MC_ERR_SHAPE;
+    // a CTA for every 32 KB of the pool and of the rows, and one for every head of a sequence's segments
+    const long long pieces = ((long long)c->H * c->d * c->d + 8191) / 8192;
+    if (c->H > (1 << 20) || pieces * (c->n_pages + c->n_seqs) >= (1ll << 31) || (long long)c->H * kMaxRows * 8 >= (1ll << 31))
+        return MC_ERR_SHAPE;
+    p = Paged{c->pages, c->kbar, c->refs, c->online, c->ksum, c->table, c->pos, c->row, c->status,
+              c->n_pages, c->n_seqs, c->H, c->d, c->seg_len, c->n_max};
+    return MC_OK;
+}
+
+int check_cache_pointers(const Paged &p)
+{
+    for (const void *x : {(const void *)p.pages, (const void *)p.kbar, (const void *)p.refs, (const void *)p.online,
+                          (const void *)p.ksum, (const void *)p.table, (const void *)p.pos, (const void *)p.row, (const void *)p.status})
+        if (!x) return MC_ERR_NULL;
+    for (const void *x : {p.pages, p.kbar, p.online, p.ksum})
+        if (!aligned(x, 16)) return MC_ERR_ALIGN;
+    for (const void *x : {p.refs, p.table, p.pos, p.row, p.status})
+        if (!aligned(x, 4)) return MC_ERR_ALIGN;
+    return MC_OK;
+}
+
+int check_pointers(std::initializer_list<const void *> wanted, std::initializer_list<const void *> words,
+                   std::initializer_list<const void *> elements, size_t element)
+{
+    for (const void *x : wanted)
+        if (!x) return MC_ERR_NULL;
+    for (const void *x : wanted)
+        if (!aligned(x, 16)) return MC_ERR_ALIGN;
+    for (const void *x : words)
+        if (!aligned(x, 4)) return MC_ERR_ALIGN;
+    for (const void *x : elements)
+        if (!aligned(x, element)) return MC_ERR_ALIGN;
+    return MC_OK;
+}
+
+// A step (T = 1), a tree's reads, or the acceptance of a path (y null).
+int run_batch(const mc_paged_cache *cache, TreeArgs a, int agg_mode, cudaStream_t s)
+{
+    int st = check_cache(cache, a.c);
+    if (st != MC_OK) return st;
+    const Paged &c = a.c;
+    const bool accept = a.accept;
+    if (a.B < 1 || a.B > c.S || a.T < 1 || a.T > kMaxTree) return MC_ERR_SHAPE;
+    if (agg_mode < MC_RESIDUAL || agg_mode > MC_MEAN) return MC_ERR_MODE;
+    a.mode = agg_mode == MC_SOUP ? MC_GRM : agg_mode;  // the same function for a matrix memory
+    if (a.mode == MC_SSC && a.topk < 0) return MC_ERR_TOPK;
+    if ((st = check_cache_pointers(c)) != MC_OK) return st;
+    if ((a.la == nullptr) != (a.be == nullptr)) return MC_ERR_NULL;
+    a.delta = a.la != nullptr;
+    const bool routed = !accept && mode_uses_u(a.mode);
+    if ((!a.parent && (a.T > 1 || accept)) || (accept && !a.last)) return MC_ERR_NULL;
+    const size_t element = a.bf16 ? 2 : 4;
+    st = accept ? check_pointers({a.k, a.v}, {a.parent, a.last, a.slots}, {a.la, a.be}, element)
+                : check_pointers({a.q, a.k, a.v, routed ? a.u : a.q, a.y}, {a.parent, a.count, a.slots}, {a.la, a.be}, element);
+    if (st != MC_OK) return st;
+    if ((st = check_device()) != MC_OK) return st;
+    const size_t BH = (size_t)a.B * c.H, T = a.T, B = a.B;
+    a.Tp = (a.T + 7) / 8 * 8;
+    a.groups = a.Tp / 8;
+    a.ranges = std::max(1, 4 * kSms / a.groups);
+    void *scratch = nullptr;
+    for (int pass = 0; pass < 2; ++pass) {
+        Carver cv{static_cast<char *>(scratch), 0};
+        a.p.path = cv.take<uint64_t>(B);
+        a.p.act = cv.take<int32_t>(B);
+        a.p.pos = cv.take<int32_t>(B);
+        a.p.len = cv.take<int32_t>(B);
+        a.p.fresh = cv.take<int32_t>(B + 1);
+        a.p.units = cv.take<int32_t>(B + 1);
+        a.p.list = cv.take<int32_t>(B * T);
+        if (!accept) {
+            a.gates = cv.take<float>(BH * (c.nmax + 1) * a.Tp);
+            a.f0 = cv.take<float>(BH * a.Tp);
+            a.P = cv.take<float>(BH * T * a.Tp);
+            a.A = cv.take<float>(a.delta ? BH * T * a.Tp : 0);
+            a.part = cv.take<float>((a.ranges + BH) * a.Tp * c.d);
+        }
+        if (pass == 0 && scratch_alloc(&scratch, cv.used, s) != cudaSuccess) {
+            cudaGetLastError();
+            return MC_ERR_ALLOC;
+        }
+    }
+    profile_call_start(s);
+    cudaError_t e = launch_plan(a, s);
+    profile_after_kernel(s, "plan_rows");
+    if (e == cudaSuccess && accept) {
+        e = launch_accept(a, s);
+        profile_after_kernel(s, "accept_rows");
+    } else if (e == cudaSuccess) {
+        e = launch_tree_gates(a, s);
+        profile_after_kernel(s, "tree_gates");
+        if (e == cudaSuccess) e = launch_tree_read(a, s);
+        profile_after_kernel(s, "tree_read");
+        if (e == cudaSuccess) e = launch_tree_finish(a, s);
+        profile_after_kernel(s, a.step ? "step_finish" : "tree_finish");
+    }
+    cudaError_t ef = cudaFreeAsync(scratch, s);
+    return e == cudaSuccess && ef == cudaSuccess ? MC_OK : fail(e != cudaSuccess ? e : ef);
+}
+
+template <typename F>
+int with_plan(size_t ints, cudaStream_t s, F &&work)
+{
+    void *plan = nullptr;
+    if (scratch_alloc(&plan, sizeof(int32_t) * ints, s) != cudaSuccess) {
+        cudaGetLastError();
+        return MC_ERR_ALLOC;
+    }
+    cudaError_t e = work(static_cast<int32_t *>(plan)), ef = cudaFreeAsync(plan, s);
+    return e == cudaSuccess && ef == cudaSuccess ? MC_OK : fail(e != cudaSuccess ? e : ef);
+}
+
+}  // namespace
+}  // namespace mc
+
+extern "C" {
+
+int mc_decode_step_paged(const mc_paged_cache *cache, const void *q, const void *k, const void *v, const void *u,
+                         const void *log_alpha, const void *beta, const int32_t *slots, int B, int agg_mode, int topk,
+                         void *y, int is_bf16, mc_stream_t stream)
+{
+    mc::TreeArgs a{};
+    a.q = q; a.k = k; a.v = v; a.u = u; a.la = log_alpha; a.be = beta; a.slots = slots; a.y = y;
+    a.B = B; a.T = 1; a.topk = topk; a.bf16 = is_bf16 != 0; a.step = true;
+    return mc::run_batch(cache, a, agg_mode, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int mc_decode_tree(const mc_paged_cache *cache, const void *q, const void *k, const void *v, const void *u,
+                   const void *log_alpha, const void *beta, const int32_t *parent, const int32_t *count,
+                   const int32_t *slots, int B, int T, int agg_mode, int topk, void *y, int is_bf16, mc_stream_t stream)
+{
+    mc::TreeArgs a{};
+    a.q = q; a.k = k; a.v = v; a.u = u; a.la = log_alpha; a.be = beta; a.slots = slots; a.y = y;
+    a.parent = parent; a.count = count;
+    a.B = B; a.T = T; a.topk = topk; a.bf16 = is_bf16 != 0;
+    return mc::run_batch(cache, a, agg_mode, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int mc_tree_accept(const mc_paged_cache *cache, const void *k, const void *v, const void *log_alpha, const void *beta,
+                   const int32_t *parent, const int32_t *last, const int32_t *slots, int B, int T, int is_bf16,
+                   mc_stream_t stream)
+{
+    mc::TreeArgs a{};
+    a.k = k; a.v = v; a.la = log_alpha; a.be = beta; a.slots = slots; a.parent = parent; a.last = last; a.accept = true;
+    a.B = B; a.T = T; a.bf16 = is_bf16 != 0;
+    return mc::run_batch(cache, a, MC_RESIDUAL, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int mc_pages_fork(const mc_paged_cache *cache, const int32_t *src, mc_stream_t stream)
+{
+    mc::Paged c;
+    int st = mc::check_cache(cache, c);
+    if (st == MC_OK) st = mc::check_cache_pointers(c);
+    if (st != MC_OK) return st;
+    if (!src) return MC_ERR_NULL;
+    if (!mc::aligned(src, 4)) return MC_ERR_ALIGN;
+    if ((st = mc::check_device()) != MC_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return mc::with_plan(2 * (size_t)c.S, s, [&](int32_t *plan) { return mc::launch_fork(c, src, plan, s); });
+}
+
+int mc_pages_compact(const mc_paged_cache *dst, const mc_paged_cache *src, mc_stream_t stream)
+{
+    mc::Paged to, from;
+    int st = mc::check_cache(dst, to);
+    if (st == MC_OK) st = mc::check_cache(src, from);
+    if (st != MC_OK) return st;
+    if (to.H != from.H || to.d != from.d || to.C != from.C || to.S < from.S || to.nmax < from.nmax) return MC_ERR_SHAPE;
+    if ((st = mc::check_cache_pointers(to)) != MC_OK || (st = mc::check_cache_pointers(from)) != MC_OK) return st;
+    if (to.pages == from.pages || to.online == from.online || to.table == from.table || to.refs == from.refs) return MC_ERR_SHAPE;
+    if ((st = mc::check_device()) != MC_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return mc::with_plan(1 + (size_t)to.P + from.P, s, [&](int32_t *plan) { return mc::launch_pages_compact(to, from, plan, s); });
+}
+
+int mc_pages_load(const mc_paged_cache *cache, int slot, const void *k, const float *states, int L, int is_bf16,
+                  mc_stream_t stream)
+{
+    mc::Paged c;
+    int st = mc::check_cache(cache, c);
+    if (st != MC_OK) return st;
+    if (slot < 0 || slot >= c.S || L < 1 || L > mc::kMaxPos || L / c.C > c.nmax) return MC_ERR_SHAPE;
+    if ((long long)(L / c.C + 1) * c.H >= (1ll << 31)) return MC_ERR_SHAPE;
+    if ((st = mc::check_cache_pointers(c)) != MC_OK) return st;
+    if ((st = mc::check_pointers({k, states}, {}, {}, 4)) != MC_OK) return st;
+    if ((st = mc::check_device()) != MC_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return mc::with_plan((size_t)(L / c.C) + 1, s, [&](int32_t *plan) {
+        return mc::launch_pages_load(c, slot, k, states, L, is_bf16 != 0, plan, s);
+    });
+}
+
+}  // extern "C"
