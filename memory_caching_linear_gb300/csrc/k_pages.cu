@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_rows(TreeArgs a)
         a.p.len[tid] = len;
     }
     int units, want;
-    const int ub = block_scan(in && row >= 0 ? units_of(a, pos) : 0, &units);
+    const int ub = block_scan(in && row >= 0 && nodes_of(a, tid) > 0 ? units_of(a, pos) : 0, &units);
     if (in) a.p.units[tid] = ub;
     if (tid == 0) a.p.units[a.B] = units;
     if (!writes) return;

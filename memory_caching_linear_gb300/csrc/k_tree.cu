@@ -248,15 +248,15 @@ __global__ void __launch_bounds__(kGateThreads) tree_gates(TreeArgs a)
             if (a.delta) {
                 const float2 z = cum[63 - __clzll(mine & seg_set[0])];
                 into = expf(z.x + z.y);
-                a.f0[(size_t)bh * a.Tp + n] = in0 && last == 0 ? into : 0.f;
             }
+            s[nb + 1] = in0 && last == 0 ? into : 0.f;
             s[nb] = in0 ? gp[warp][0] * into : 0.f;
             if (a.step) a.f0[(size_t)bh * a.Tp] = gp[warp][0];  // a step's end reads the memory after the token
         }
     }
     __syncthreads();
-    float *out = a.gates + (size_t)bh * (c.nmax + 1) * a.Tp + n0;
-    for (int i = tid; i < (nb + 1) * kGroup; i += kGateThreads) {
+    float *out = a.gates + (size_t)bh * (c.nmax + 2) * a.Tp + n0;
+    for (int i = tid; i < (nb + 2) * kGroup; i += kGateThreads) {
         const int t = i % kGroup;
         out[(size_t)(i / kGroup) * a.Tp + t] = n0 + t < m ? sc[t * stride + i / kGroup] : 0.f;
     }
@@ -284,22 +284,25 @@ __global__ void __launch_bounds__(256) tree_read(TreeArgs a)
         while (x >= (long long)a.p.units[b + 1] * c.H) ++b;
         const int nu = a.p.units[b + 1] - a.p.units[b];
         const long long in_b = x - (long long)a.p.units[b] * c.H;
-        const int h = (int)(in_b / nu), i0 = (int)(in_b % nu), i1 = (int)(end - x < nu - i0 ? i0 + (end - x) : nu);
+        const int bh = b * c.H + (int)(in_b / nu), h = (int)(in_b / nu), row = a.p.act[b], nb = cached_segments(c, a.p.pos[b]);
+        const int i0 = (int)(in_b % nu);
+        const bool for_keys = i0 > nb;
+        const int stop = for_keys || nu <= nb + 1 ? nu : nb + 1;  // the keys' read is apart
+        const int i1 = (int)(end - x < stop - i0 ? i0 + (end - x) : stop);
         x += i1 - i0;
         const int m = nodes_of(a, b);
         if (n0 >= m) continue;
-        const int bh = b * c.H + h, row = a.p.act[b], nb = cached_segments(c, a.p.pos[b]);
         float4 q[TG];
 #pragma unroll
         for (int t = 0; t < TG; ++t)
-            q[t] = n0 + t < m ? load4(static_cast<const E *>(a.q) + ((size_t)bh * a.T + n0 + t) * D + c0) : make_float4(0.f, 0.f, 0.f, 0.f);
+            q[t] = n0 + t < m ? load4(static_cast<const E *>(for_keys ? a.k : a.q) + ((size_t)bh * a.T + n0 + t) * D + c0) : make_float4(0.f, 0.f, 0.f, 0.f);
         float acc[PASS][TG];
 #pragma unroll
         for (int y = 0; y < PASS; ++y)
 #pragma unroll
             for (int t = 0; t < TG; ++t) acc[y][t] = 0.f;
         for (int i = i0; i < i1; ++i) {
-            const float *g = a.gates + ((size_t)bh * (c.nmax + 1) + i) * a.Tp + n0;
+            const float *g = a.gates + ((size_t)bh * (c.nmax + 2) + i) * a.Tp + n0;
             float gv[TG];
             bool any = false;
 #pragma unroll
@@ -316,7 +319,7 @@ __global__ void __launch_bounds__(256) tree_read(TreeArgs a)
                     if (gv[t] != 0.f) acc[y][t] = fmaf(gv[t], dot4(w, q[t]), acc[y][t]);
             }
         }
-        float *out = a.part + ((size_t)range + bh) * a.Tp * D + (size_t)n0 * D;
+        float *out = (for_keys ? a.Z + (size_t)bh * a.Tp * D : a.part + ((size_t)range + bh) * a.Tp * D) + (size_t)n0 * D;
 #pragma unroll
         for (int y = 0; y < PASS; ++y) {
             sum_groups<TG, LPR>(acc[y], lane);
@@ -335,10 +338,11 @@ __global__ void __launch_bounds__(256) tree_read(TreeArgs a)
 __device__ __forceinline__ float sum_parts(const TreeArgs &a, int bh, int b, int h, int D, int n, int r)
 {
     const long long U = (long long)a.p.units[a.B] * a.c.H;
-    const int nu = a.p.units[b + 1] - a.p.units[b];
+    const int all = a.p.units[b + 1] - a.p.units[b];  // (the last of which, of a begun delta memory, is the keys' read)
+    const int nu = all - (a.delta && !a.step && a.p.pos[b] % a.c.C ? 1 : 0);
     float y = 0.f;
     if (nu == 0) return y;
-    const long long u0 = (long long)a.p.units[b] * a.c.H + (long long)h * nu;
+    const long long u0 = (long long)a.p.units[b] * a.c.H + (long long)h * all;
     const long long R = ranges_of(U, a.ranges);
     const int j0 = range_of(u0, U, R), j1 = range_of(u0 + nu - 1, U, R);
     for (int j = j0; j <= j1; ++j) y += a.part[(((size_t)j + bh) * a.Tp + n) * D + r];
@@ -359,41 +363,21 @@ __global__ void __launch_bounds__(256) tree_finish(TreeArgs a)
     const int in0 = a.p.pos[b] % c.C;
     extern __shared__ __align__(16) float dyn[];
     float *Ps = dyn, *As = Ps + kMaxTree * kMaxTree;  // [m][Tp]
-    float *M0 = As + kMaxTree * kMaxTree;             // [RB][D + 4]
-    float *ks = M0 + RB * (D + 4);                    // [m][D]
     __shared__ float es[kMaxTree][RB];
     const size_t at = (size_t)bh * a.T;
     for (int i = tid; i < m * a.Tp; i += 256) {
         Ps[i] = a.P[at * a.Tp + i];
         if (a.delta) As[i] = a.A[at * a.Tp + i];
     }
-    const bool met = a.delta && in0;
-    if (met) {
-        const float *mem = c.online + (((size_t)row * c.H + h) * D + rb * RB) * D;
-        for (int i = tid; i < RB * D; i += 256) M0[i / D * (D + 4) + i % D] = mem[i];
-        for (int i = tid; i < m * D; i += 256) ks[i] = to_f(static_cast<const E *>(a.k)[at * D + i]);
-    }
+    const float *into = a.gates + ((size_t)bh * (c.nmax + 2) + cached_segments(c, a.p.pos[b]) + 1) * a.Tp;
     float e[8];
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
         const int n = warp + 8 * x;
         e[x] = n < m ? to_f(static_cast<const E *>(a.v)[(at + n) * D + rb * RB + r]) : 0.f;
+        if (a.delta && in0 && n < m && into[n] != 0.f) e[x] -= a.Z[((size_t)bh * a.Tp + n) * D + rb * RB + r];
     }
     __syncthreads();
-    if (met) {
-        float z[8] = {};
-        for (int x4 = 0; x4 < D; x4 += 4) {
-            const float4 w = load4(M0 + r * (D + 4) + x4);
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-                if (warp + 8 * x < m) z[x] += dot4(w, load4(ks + (warp + 8 * x) * D + x4));
-        }
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            const float f = warp + 8 * x < m ? a.f0[(size_t)bh * a.Tp + warp + 8 * x] : 0.f;
-            if (f != 0.f) e[x] -= f * z[x];
-        }
-    }
     if (a.delta) {
 #pragma unroll 1
         for (int j = 0; j < m; ++j) {
@@ -517,7 +501,7 @@ cudaError_t finish_impl(const TreeArgs &a, cudaStream_t s)
         step_finish<E, D><<<grid, 256, 0, s>>>(a);
         return cudaGetLastError();
     }
-    const size_t smem = sizeof(float) * (2 * kMaxTree * kMaxTree + RB * (D + 4) + kMaxTree * D);
+    const size_t smem = sizeof(float) * 2 * kMaxTree * kMaxTree;
     cudaError_t e = cudaFuncSetAttribute(tree_finish<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     tree_finish<E, D><<<grid, 256, smem, s>>>(a);
@@ -543,7 +527,10 @@ cudaError_t run(const TreeArgs &a, cudaStream_t s, int what)
 }  // namespace
 
 cudaError_t launch_tree_gates(const TreeArgs &a, cudaStream_t s) { return run(a, s, 0); }
-cudaError_t launch_tree_read(const TreeArgs &a, cudaStream_t s) { return run(a, s, 1); }
+cudaError_t launch_tree_read(const TreeArgs &a, cudaStream_t s)
+{
+    return tree_tc_supported(a) ? launch_tree_read_tc(a, s) : run(a, s, 1);
+}
 cudaError_t launch_tree_finish(const TreeArgs &a, cudaStream_t s) { return run(a, s, 2); }
 
 }  // namespace mc

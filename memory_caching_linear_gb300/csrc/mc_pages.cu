@@ -98,7 +98,7 @@ int run_batch(const mc_paged_cache *cache, TreeArgs a, int agg_mode, cudaStream_
     const size_t BH = (size_t)a.B * c.H, T = a.T, B = a.B;
     a.Tp = (a.T + 7) / 8 * 8;
     a.groups = a.Tp / 8;
-    a.ranges = std::max(1, 4 * kSms / a.groups);
+    a.ranges = tree_tc_supported(a) ? kSms : std::max(1, 4 * kSms / a.groups);
     void *scratch = nullptr;
     for (int pass = 0; pass < 2; ++pass) {
         Carver cv{static_cast<char *>(scratch), 0};
@@ -110,7 +110,8 @@ int run_batch(const mc_paged_cache *cache, TreeArgs a, int agg_mode, cudaStream_
         a.p.units = cv.take<int32_t>(B + 1);
         a.p.list = cv.take<int32_t>(B * T);
         if (!accept) {
-            a.gates = cv.take<float>(BH * (c.nmax + 1) * a.Tp);
+            a.gates = cv.take<float>(BH * (c.nmax + 2) * a.Tp);
+            a.Z = cv.take<float>(a.delta && !a.step ? BH * a.Tp * c.d : 0);
             a.f0 = cv.take<float>(BH * a.Tp);
             a.P = cv.take<float>(BH * T * a.Tp);
             a.A = cv.take<float>(a.delta ? BH * T * a.Tp : 0);
@@ -131,7 +132,7 @@ int run_batch(const mc_paged_cache *cache, TreeArgs a, int agg_mode, cudaStream_
         e = launch_tree_gates(a, s);
         profile_after_kernel(s, "tree_gates");
         if (e == cudaSuccess) e = launch_tree_read(a, s);
-        profile_after_kernel(s, "tree_read");
+        profile_after_kernel(s, tree_tc_supported(a) ? "tree_read_tc" : "tree_read");
         if (e == cudaSuccess) e = launch_tree_finish(a, s);
         profile_after_kernel(s, a.step ? "step_finish" : "tree_finish");
     }

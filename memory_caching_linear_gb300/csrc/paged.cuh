@@ -47,10 +47,11 @@ struct TreeArgs {
     const int32_t *slots;                 // [B], or null (batch row b is slot b)
     const int32_t *last;                  // [B] accept: the last node of the path
     void *y;                              // [B][H][T][d]
-    float *gates;                         // [BH][nmax + 1][Tp] gates of the cached memories, then of the begun segment's
+    float *gates;                         // [BH][nmax + 2][Tp] gates of the cached memories, then what nodes read of the begun
+                                          // segment's with their queries (gate and decay) and with their keys (decay)
     float *P, *A;                         // [BH][T][Tp] what a node reads of what its ancestors wrote; what they meet in its key
-    float *f0;                            // [BH][Tp] decay from the cache to a node, 0 past the begun segment; in a step the
-                                          // online memory's gate
+    float *f0;                            // [BH][Tp] a step: the online memory's gate
+    float *Z;                             // [BH][Tp][d] the begun segment's memory read with the nodes' keys, decayed
     float *part;                          // [ranges + BH][Tp][d] partial reads
     int B, T, Tp, mode, topk;
     int ranges, groups;                   // shares of the memories; of the tokens
@@ -66,11 +67,11 @@ __device__ __forceinline__ int range_of(long long x, long long U, long long R) {
 __device__ __forceinline__ int valid_page(const Paged &c, int p) { return (unsigned)p < (unsigned)c.P ? p : -1; }
 
 // Completed segments of a sequence at pos that its table has room for, and the memories that a read goes over: those and,
-// in a tree's reads, that of a segment begun.
+// in a tree's reads, that of a segment begun, for the queries and (gated delta memory) for the keys.
 __device__ __forceinline__ int cached_segments(const Paged &c, int pos) { return min(pos / c.C, c.nmax); }
 __device__ __forceinline__ int units_of(const TreeArgs &a, int pos)
 {
-    return cached_segments(a.c, pos) + (!a.step && pos % a.c.C ? 1 : 0);
+    return cached_segments(a.c, pos) + (!a.step && pos % a.c.C ? (a.delta ? 2 : 1) : 0);
 }
 __device__ __forceinline__ int nodes_of(const TreeArgs &a, int b)
 {
@@ -139,6 +140,9 @@ __device__ __forceinline__ void sum_groups(float (&p)[N], int lane)
 cudaError_t launch_plan(const TreeArgs &a, cudaStream_t s);
 cudaError_t launch_tree_gates(const TreeArgs &a, cudaStream_t s);
 cudaError_t launch_tree_read(const TreeArgs &a, cudaStream_t s);
+bool tree_tc_supported(const TreeArgs &a);
+cudaError_t launch_tree_read_tc(const TreeArgs &a, cudaStream_t s);
+cudaError_t take_tree_abort(int *was_set);
 cudaError_t launch_tree_finish(const TreeArgs &a, cudaStream_t s);  // a step's end too
 cudaError_t launch_accept(const TreeArgs &a, cudaStream_t s);
 cudaError_t launch_fork(const Paged &c, const int32_t *src, int32_t *plan, cudaStream_t s);
