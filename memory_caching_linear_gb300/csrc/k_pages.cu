@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_rows(TreeArgs a)
 {
     const Paged &c = a.c;
     const int tid = threadIdx.x, lane = tid % 32;
-    const bool accept = a.accept, writes = a.step || accept;
+    const bool accept = a.accept;
     __shared__ int taker[kMaxRows], lens[kMaxRows];
     taker[tid] = 0x7fffffff;
     lens[tid] = 0;
@@ -90,11 +90,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_rows(TreeArgs a)
                 row = -1;
             }
         }
-        if (row >= 0 && writes) atomicMin(&taker[row], tid);
-        if (row >= 0 && a.count && (a.count[tid] < 0 || a.count[tid] > a.T)) report(c, MC_PAGES_INDEX);
+        if (row >= 0) atomicMin(&taker[row], tid);
     }
     __syncthreads();
-    if (row >= 0 && writes && taker[row] != tid) {
+    if (row >= 0 && taker[row] != tid) {
         report(c, MC_PAGES_INDEX);
         row = -1;
     }
@@ -130,11 +129,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_rows(TreeArgs a)
         a.p.pos[tid] = pos;
         a.p.len[tid] = len;
     }
-    int units, want;
-    const int ub = block_scan(in && row >= 0 && nodes_of(a, tid) > 0 ? units_of(a, pos) : 0, &units);
-    if (in) a.p.units[tid] = ub;
-    if (tid == 0) a.p.units[a.B] = units;
-    if (!writes) return;
+    int want;
     const int fb = block_scan(more, &want);
     if (in) a.p.fresh[tid] = fb;
     if (tid == 0) a.p.fresh[a.B] = want;

@@ -15,6 +15,7 @@
 #include <cstdint>
 
 #include "paged.cuh"
+#include "tree_nodes.cuh"
 
 namespace mc {
 namespace {
@@ -25,9 +26,10 @@ constexpr int kGroup = 8;  // tokens that a CTA of the gates and of the CUDA-cor
 
 constexpr int kGateThreads = 256;
 
-size_t gates_smem(const Paged &c)
+size_t gates_smem(const TreeArgs &a)
 {
-    return sizeof(float) * (kGroup * (size_t)(c.nmax + 1 + kMaxTree) + c.nmax);
+    const size_t ints = Line::ints(a.B), floats = kGroup * (size_t)(a.c.nmax + 1 + kMaxTree) + a.c.nmax;
+    return 4 * (ints > floats ? ints : floats);
 }
 
 template <typename E, int D>
@@ -35,43 +37,26 @@ __global__ void __launch_bounds__(kGateThreads) tree_gates(TreeArgs a)
 {
     constexpr int LPR = D / 4, RPW = 32 / LPR, WARPS = kGateThreads / 32;
     const Paged &c = a.c;
+    extern __shared__ __align__(16) float dyn[];
+    after_previous();
+    if (blockIdx.x == gridDim.x - 1) {  // one CTA more, for those that come after
+        leave_line(a, reinterpret_cast<int *>(dyn));
+        return;
+    }
     const int bh = (int)blockIdx.x / a.groups, n0 = (int)blockIdx.x % a.groups * kGroup, b = bh / c.H, h = bh % c.H;
-    const int row = a.p.act[b], m = nodes_of(a, b);
-    if (row < 0 || n0 >= m) return;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int pos = a.p.pos[b], nb = cached_segments(c, pos), in0 = pos % c.C;
+    const Seat seat = seat_of(a, b, false);
+    const int row = seat.row, m = seat.m;
+    if (row < 0 || n0 >= m) return;
+    const int nb = cached_segments(c, seat.pos), in0 = seat.pos % c.C;
     const bool routed = a.mode == MC_GRM || a.mode == MC_SSC;
     const int stride = c.nmax + 1 + kMaxTree;
-    extern __shared__ __align__(16) float dyn[];
     float *sc = dyn;                                         // [kGroup][stride] scores: cached, key sum, nodes; then gates
     int *page = reinterpret_cast<int *>(dyn + kGroup * stride);  // [nmax]
-    __shared__ uint64_t anc[kMaxTree], seg_set[kMaxTree];
-    __shared__ int up[kMaxTree], seg[kMaxTree];
+    __shared__ Nodes nodes;
     __shared__ __align__(16) float tok[3][kGroup][D];  // u, q, k of the group's tokens
     __shared__ float kq[kGroup][kMaxTree], kk[kGroup][kMaxTree], gp[kGroup][kMaxTree];
-    __shared__ float2 cum[kMaxTree];
-    __shared__ float la[kMaxTree], be[kMaxTree];
 
-    // ancestors by doubling: after turn x a node knows those up to 2^x above it
-    uint64_t set = 0;
-    int f = -1;
-    if (tid < kMaxTree) {
-        if (tid < m) {
-            set = 1ull << tid;
-            f = a.parent ? a.parent[(size_t)b * a.T + tid] : -1;
-            if (f < -1 || f >= tid) {
-                atomicOr(c.status, MC_PAGES_INDEX);
-                f = -1;
-            }
-            if (a.delta) {
-                la[tid] = delta_log(to_f(static_cast<const E *>(a.la)[(size_t)bh * a.T + tid]));
-                be[tid] = to_f(static_cast<const E *>(a.be)[(size_t)bh * a.T + tid]);
-            }
-        }
-        anc[tid] = set;
-        up[tid] = f;
-        seg_set[tid] = 0;
-    }
     for (int i = tid; i < nb; i += kGateThreads) page[i] = valid_page(c, c.table[(size_t)row * c.nmax + i]);
     for (int i = tid; i < kGroup * D; i += kGateThreads) {
         const int t = i / D, x = i % D;
@@ -81,35 +66,7 @@ __global__ void __launch_bounds__(kGateThreads) tree_gates(TreeArgs a)
         tok[1][t][x] = in ? to_f(static_cast<const E *>(a.q)[at]) : 0.f;
         if (a.delta) tok[2][t][x] = in ? to_f(static_cast<const E *>(a.k)[at]) : 0.f;
     }
-    __syncthreads();
-#pragma unroll 1
-    for (int x = 1; x < m; x *= 2) {
-        if (tid < m && f >= 0) {
-            set |= anc[f];
-            f = up[f];
-        }
-        __syncthreads();
-        if (tid < m) {
-            anc[tid] = set;
-            up[tid] = f;
-        }
-        __syncthreads();
-    }
-    if (tid < m) {
-        const int s = (in0 + __popcll(set) - 1) / c.C;
-        seg[tid] = s;
-        atomicOr(reinterpret_cast<unsigned long long *>(&seg_set[s]), 1ull << tid);
-    }
-    __syncthreads();
-    if (a.delta && tid < m) {
-        float2 s = make_float2(0.f, 0.f);
-        for (uint64_t w = set & seg_set[seg[tid]]; w; w &= w - 1) {
-            const float2 x = delta_parts(la[__ffsll(w) - 1]);
-            s.x += x.x;
-            s.y += x.y;
-        }
-        cum[tid] = s;
-    }
+    make_nodes<E>(a, nodes, b, bh, m, in0);
 
     // dot products of the group's tokens (tok[which]) with rows: LPR lanes to a row
     auto dots = [&](int which, int rows, auto load, auto store) {
@@ -150,13 +107,13 @@ __global__ void __launch_bounds__(kGateThreads) tree_gates(TreeArgs a)
     const int n = n0 + warp;
     if (n < m) {
         float *s = sc + warp * stride;
-        const uint64_t mine = anc[n];
-        const int last = seg[n];
+        const uint64_t mine = nodes.anc[n];
+        const int last = nodes.seg[n];
         float top = -FLT_MAX;
         if (routed) {
             for (int j = lane; j <= last; j += 32) {  // the path's segments: keys of the cache and of the path
                 float x = j == 0 && in0 ? s[nb] : 0.f;
-                for (uint64_t w = mine & seg_set[j]; w; w &= w - 1) x += s[nb + __ffsll(w)];
+                for (uint64_t w = mine & nodes.seg_set[j]; w; w &= w - 1) x += s[nb + __ffsll(w)];
                 gp[warp][j] = x / (float)(j < last ? c.C : (in0 + __popcll(mine) - 1) % c.C + 1);
             }
             __syncwarp();
@@ -225,30 +182,8 @@ __global__ void __launch_bounds__(kGateThreads) tree_gates(TreeArgs a)
             for (int j = lane; j <= last; j += 32) gp[warp][j] = g;
         }
         __syncwarp();
-        // what the node reads of what its ancestors wrote, and what they meet in its key
-        float *Pr = a.P + ((size_t)bh * a.T + n) * a.Tp, *Ar = a.delta ? a.A + ((size_t)bh * a.T + n) * a.Tp : nullptr;
-        auto decay = [&](int to, int from) { return expf((cum[to].x - cum[from].x) + (cum[to].y - cum[from].y)); };
-        for (int x = lane; x < a.Tp; x += 32) {
-            const bool above = x < m && (mine >> x) & 1;
-            float p = 0.f, q = 0.f;
-            if (above) {
-                const int sx = seg[x];
-                p = gp[warp][sx] * kq[warp][x];
-                if (a.delta) {
-                    const int deepest = 63 - __clzll(mine & seg_set[sx]);
-                    p *= decay(deepest, x) * be[x];
-                    if (sx == last && x != n) q = decay(n, x) * be[x] * kk[warp][x];
-                }
-            }
-            Pr[x] = p;
-            if (a.delta) Ar[x] = q;
-        }
         if (lane == 0) {
-            float into = 1.f;  // of the begun segment's memory
-            if (a.delta) {
-                const float2 z = cum[63 - __clzll(mine & seg_set[0])];
-                into = expf(z.x + z.y);
-            }
+            const float into = a.delta ? decay_from_cache(nodes, n) : 1.f;  // of the begun segment's memory
             s[nb + 1] = in0 && last == 0 ? into : 0.f;
             s[nb] = in0 ? gp[warp][0] * into : 0.f;
             if (a.step) a.f0[(size_t)bh * a.Tp] = gp[warp][0];  // a step's end reads the memory after the token
@@ -260,6 +195,9 @@ __global__ void __launch_bounds__(kGateThreads) tree_gates(TreeArgs a)
         const int t = i % kGroup;
         out[(size_t)(i / kGroup) * a.Tp + t] = n0 + t < m ? sc[t * stride + i / kGroup] : 0.f;
     }
+    if (!a.step)
+        write_path<kGroup>(a, nodes, bh, n0, m, [&](int t, int j) { return gp[t][j]; }, [&](int t, int x) { return kq[t][x]; },
+                           [&](int t, int x) { return kk[t][x]; });
 }
 
 // ------------------------------------------------------------------------------------------------ read
@@ -273,7 +211,10 @@ __global__ void __launch_bounds__(256) tree_read(TreeArgs a)
     const Paged &c = a.c;
     const int range = (int)blockIdx.x / a.groups, n0 = (int)blockIdx.x % a.groups * kGroup;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const long long U = (long long)a.p.units[a.B] * c.H;
+    extern __shared__ int space[];
+    after_previous();
+    const Line line = make_line(a, space, false);
+    const long long U = (long long)line.units[a.B] * c.H;
     const long long R = ranges_of(U, a.ranges);
     if (range >= R || warp * RPW * PASS >= D) return;
     long long x = range_begin(range, U, R);
@@ -281,16 +222,16 @@ __global__ void __launch_bounds__(256) tree_read(TreeArgs a)
     const int r0 = warp * RPW * PASS + lane / LPR, c0 = lane % LPR * 4;
     int b = 0;
     while (x < end) {
-        while (x >= (long long)a.p.units[b + 1] * c.H) ++b;
-        const int nu = a.p.units[b + 1] - a.p.units[b];
-        const long long in_b = x - (long long)a.p.units[b] * c.H;
-        const int bh = b * c.H + (int)(in_b / nu), h = (int)(in_b / nu), row = a.p.act[b], nb = cached_segments(c, a.p.pos[b]);
+        while (x >= (long long)line.units[b + 1] * c.H) ++b;
+        const int nu = line.units[b + 1] - line.units[b];
+        const long long in_b = x - (long long)line.units[b] * c.H;
+        const int bh = b * c.H + (int)(in_b / nu), h = (int)(in_b / nu), row = line.row[b], nb = cached_segments(c, line.pos[b]);
         const int i0 = (int)(in_b % nu);
         const bool for_keys = i0 > nb;
         const int stop = for_keys || nu <= nb + 1 ? nu : nb + 1;  // the keys' read is apart
         const int i1 = (int)(end - x < stop - i0 ? i0 + (end - x) : stop);
         x += i1 - i0;
-        const int m = nodes_of(a, b);
+        const int m = line.nodes[b];
         if (n0 >= m) continue;
         float4 q[TG];
 #pragma unroll
@@ -334,84 +275,201 @@ __global__ void __launch_bounds__(256) tree_read(TreeArgs a)
 
 // ------------------------------------------------------------------------------------------------ finish
 
-// The partial reads of head bh at (token, row), in their order.
-__device__ __forceinline__ float sum_parts(const TreeArgs &a, int bh, int b, int h, int D, int n, int r)
-{
-    const long long U = (long long)a.p.units[a.B] * a.c.H;
-    const int all = a.p.units[b + 1] - a.p.units[b];  // (the last of which, of a begun delta memory, is the keys' read)
-    const int nu = all - (a.delta && !a.step && a.p.pos[b] % a.c.C ? 1 : 0);
-    float y = 0.f;
-    if (nu == 0) return y;
-    const long long u0 = (long long)a.p.units[b] * a.c.H + (long long)h * all;
-    const long long R = ranges_of(U, a.ranges);
-    const int j0 = range_of(u0, U, R), j1 = range_of(u0 + nu - 1, U, R);
-    for (int j = j0; j <= j1; ++j) y += a.part[(((size_t)j + bh) * a.Tp + n) * D + r];
-    return y;
-}
+// The partial reads of a head's `count` memories lie in ranges j0 .. j1, in the order of the memories.
+struct Parts {
+    int j0, j1;
+    __device__ Parts(const TreeArgs &a, const Line &l, int b, int h, int count)
+    {
+        const int before = l.units[b], all = l.units[b + 1] - before;
+        const long long U = (long long)l.units[a.B] * a.c.H, R = ranges_of(U, a.ranges), u0 = (long long)before * a.c.H + (long long)h * all;
+        j0 = count > 0 ? range_of(u0, U, R) : 0;
+        j1 = count > 0 ? range_of(u0 + count - 1, U, R) : -1;
+    }
+};
 
-// Solves for e node by node (each node's is taken from all of its descendants' at once) and adds everything up: 32 rows of a
-// head, a lane to a row, a warp to every eighth node.
-template <typename E, int D>
+// Solves for e and adds everything up: up to 32 rows of a head, a lane to a row and a warp to eight nodes, whose e and y it
+// keeps in registers.  A row needs its own e alone, so lanes share nothing but P and A.  The warps' nodes come in turns:
+// the warp at hand works out its eight e (a triangle) and leaves them in shared memory, the later ones take them up: eight
+// products with A and with P for every e.  The linear memory's e are the values: no turns.
+//   SPLIT: a split read.  With s the scores, a part's largest L_p and sum z_p, top = max(L_p, path scores) and
+//   Z = sum_p z_p exp(L_p - top) + sum_j exp(s_j - top), a part counts exp(L_p - top) / Z and path segment j, whose P and (j = 0)
+//   read of the begun memory wait for it, exp(s_j - top) / Z (Residual: 1 and 1; Mean: all scores 0).
+// Latency bounds it: loads that do not hang on one another are all under way before the first is used.
+constexpr int kPartsAtOnce = 4;
+
+template <typename E, int D, bool SPLIT>
 __global__ void __launch_bounds__(256) tree_finish(TreeArgs a)
 {
     constexpr int RB = D < 32 ? D : 32;
     const Paged &c = a.c;
     const int bh = (int)blockIdx.x / (D / RB), rb = (int)blockIdx.x % (D / RB), b = bh / c.H, h = bh % c.H;
-    const int row = a.p.act[b], m = nodes_of(a, b);
-    if (row < 0 || m == 0) return;
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, r = lane % RB;
-    const int in0 = a.p.pos[b] % c.C;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, row = rb * RB + lane % RB, n0 = 8 * warp;
     extern __shared__ __align__(16) float dyn[];
-    float *Ps = dyn, *As = Ps + kMaxTree * kMaxTree;  // [m][Tp]
-    __shared__ float es[kMaxTree][RB];
+    float *Ps = dyn, *As = Ps + a.T * a.Tp;          // [m][Tp]
+    float *ws = As + (a.delta ? a.T * a.Tp : 0);     // SPLIT: [segment][Tp] path weights
+    __shared__ float es[kMaxTree][32];
+    __shared__ uint64_t anc[kMaxTree];
+    __shared__ int seg[kMaxTree];
+    __shared__ float share[kPartsAtOnce][kMaxTree], into[kMaxTree], first[kMaxTree], tops[kMaxTree], invs[kMaxTree];
     const size_t at = (size_t)bh * a.T;
-    for (int i = tid; i < m * a.Tp; i += 256) {
-        Ps[i] = a.P[at * a.Tp + i];
-        if (a.delta) As[i] = a.A[at * a.Tp + i];
-    }
-    const float *into = a.gates + ((size_t)bh * (c.nmax + 2) + cached_segments(c, a.p.pos[b]) + 1) * a.Tp;
-    float e[8];
+    after_previous();
+    const Line line = line_in(a.line, a.B);
+    const int where = line.row[b], pos = line.pos[b], m = line.nodes[b];
+    // rows of V, Z and the begun memory's read: not all of them count, but all are there
+    float e[8], z[8], y[8];
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
-        const int n = warp + 8 * x;
-        e[x] = n < m ? to_f(static_cast<const E *>(a.v)[(at + n) * D + rb * RB + r]) : 0.f;
-        if (a.delta && in0 && n < m && into[n] != 0.f) e[x] -= a.Z[((size_t)bh * a.Tp + n) * D + rb * RB + r];
+        const bool in = n0 + x < a.T;
+        const size_t there = ((size_t)bh * a.Tp + n0 + x) * D + row;
+        e[x] = in ? to_f(static_cast<const E *>(a.v)[(at + n0 + x) * D + row]) : 0.f;
+        z[x] = in && a.delta ? a.Z[there] : 0.f;
+        y[x] = in && SPLIT ? a.Y0[there] : 0.f;
+    }
+    for (int i = tid; i < a.T * a.Tp / 4; i += blockDim.x) {
+        const float4 p = reinterpret_cast<const float4 *>(a.P + at * a.Tp)[i];
+        const float4 q = a.delta ? reinterpret_cast<const float4 *>(a.A + at * a.Tp)[i] : p;
+        reinterpret_cast<float4 *>(Ps)[i] = p;
+        if (a.delta) reinterpret_cast<float4 *>(As)[i] = q;
+    }
+    if (where < 0 || m == 0) return;
+    const int nb = cached_segments(c, pos), in0 = pos % c.C;
+    const Parts parts(a, line, b, h, SPLIT ? nb : nb + (in0 ? 1 : 0));
+    for (int n = tid; n < kMaxTree; n += blockDim.x) {
+        const bool in = n < m;
+        anc[n] = in ? a.anc[(size_t)b * kMaxTree + n] : 0;
+        const int last = in && SPLIT ? a.seg[(size_t)b * kMaxTree + n] : 0;
+        seg[n] = last;
+        if (!SPLIT) {
+            into[n] = in ? a.gates[((size_t)bh * (c.nmax + 2) + nb + 1) * a.Tp + n] : 0.f;
+        } else if (in) {
+            const float *score = a.score + at * a.Tp + n;
+            const float2 *weight = a.weight + (size_t)bh * a.Tp + n;
+            const float d = in0 ? a.into[(size_t)bh * a.Tp + n] : 0.f;
+            const float s0 = score[0];
+            float top = -FLT_MAX, sum = 0.f;
+#pragma unroll 4
+            for (int j = parts.j0; j <= parts.j1; ++j) top = fmaxf(top, weight[(size_t)j * a.Tp].x);
+            for (int j = 0; j <= last; ++j) top = fmaxf(top, j ? score[(size_t)j * a.Tp] : s0);
+#pragma unroll 4
+            for (int j = parts.j0; j <= parts.j1; ++j) {
+                const float2 w = weight[(size_t)j * a.Tp];
+                sum += w.y * expf(w.x - top);
+            }
+            for (int j = 0; j <= last; ++j) sum += ws[j * a.Tp + n] = expf((j ? score[(size_t)j * a.Tp] : s0) - top);
+            const float inv = a.mode == MC_RESIDUAL ? 1.f : 1.f / sum;
+            for (int j = 0; j <= last; ++j) ws[j * a.Tp + n] *= inv;
+            tops[n] = top;
+            invs[n] = inv;
+            first[n] = ws[n] * d;           // of the begun memory's read
+            into[n] = last == 0 ? d : 0.f;  // of what it answers to the key
+        }
     }
     __syncthreads();
-    if (a.delta) {
-#pragma unroll 1
-        for (int j = 0; j < m; ++j) {
-            if (warp == j % 8 && lane < RB) {
+    if (SPLIT) {
+        for (int i = tid; i < m * a.Tp; i += blockDim.x) {
+            const int j = i / a.Tp, n = i % a.Tp;
+            if ((anc[n] >> j) & 1) Ps[i] *= ws[seg[j] * a.Tp + n];
+        }
+    }
+    const bool mine = n0 < m;
 #pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    if (x == j / 8) es[j][r] = e[x];
-            }
+    for (int x = 0; x < 8; ++x) {
+        const int n = n0 + x;
+        if (n >= m) e[x] = y[x] = 0.f;
+        else {
+            if (a.delta && into[n] != 0.f) e[x] -= SPLIT ? into[n] * z[x] : z[x];
+            y[x] = SPLIT && in0 ? first[n] * y[x] : 0.f;
+        }
+    }
+    for (int j0 = parts.j0; j0 <= parts.j1; j0 += kPartsAtOnce) {
+        const int cnt = min(kPartsAtOnce, parts.j1 - j0 + 1);
+        if (SPLIT) {
             __syncthreads();
+            for (int i = tid; i < cnt * m; i += blockDim.x) {
+                const int j = i / m, n = i % m;
+                share[j][n] = expf(a.weight[((size_t)j0 + j + bh) * a.Tp + n].x - tops[n]) * invs[n];
+            }
+        }
+        float p[kPartsAtOnce][8];
+#pragma unroll
+        for (int j = 0; j < kPartsAtOnce; ++j) {
+            const float *src = a.part + (((size_t)j0 + j + bh) * a.Tp + n0) * D + row;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) p[j][x] = j < cnt && n0 + x < m ? src[(size_t)x * D] : 0.f;
+        }
+        if (SPLIT) __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kPartsAtOnce; ++j)
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+                if (j < cnt && n0 + x < m) y[x] = SPLIT ? fmaf(share[j][n0 + x], p[j][x], y[x]) : y[x] + p[j][x];
+    }
+    // what the eight nodes of warp k wrote, for this warp's: P and A of one that is no ancestor are 0, but what it wrote may not
+    // be finite, and then it is not multiplied
+    auto take = [&](int k, int j, float ej, bool solve) {
+        const float *pr = Ps + (8 * k + j) * a.Tp + n0, *ar = As + (8 * k + j) * a.Tp + n0;
+        const float4 p0 = load4(pr), p1 = load4(pr + 4);
+        const float p[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+        float q[8];
+        if (solve) {
+            const float4 q0 = load4(ar), q1 = load4(ar + 4);
+            q[0] = q0.x; q[1] = q0.y; q[2] = q0.z; q[3] = q0.w; q[4] = q1.x; q[5] = q1.y; q[6] = q1.z; q[7] = q1.w;
+        }
+        if (isfinite(ej)) {
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
-                const int n = warp + 8 * x;
-                if (n > j && n < m) {
-                    const float w = As[n * a.Tp + j];
-                    if (w != 0.f) e[x] = fmaf(-w, es[j][r], e[x]);
+                y[x] = fmaf(p[x], ej, y[x]);
+                if (solve) e[x] = fmaf(-q[x], ej, e[x]);
+            }
+        } else {
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+                if ((anc[n0 + x] >> (8 * k + j)) & 1) {
+                    y[x] = fmaf(p[x], ej, y[x]);
+                    if (solve && q[x] != 0.f) e[x] = fmaf(-q[x], ej, e[x]);
                 }
+        }
+    };
+    uint64_t above = 0;
+    if (mine) {
+#pragma unroll
+        for (int x = 0; x < 8; ++x) above |= anc[n0 + x];
+    }
+    __syncthreads();
+    if (!a.delta) {
+#pragma unroll
+        for (int x = 0; x < 8; ++x) es[n0 + x][lane] = e[x];
+        __syncthreads();
+        if (mine) {
+            for (int k = 0; k <= warp; ++k) {
+                if (!((above >> (8 * k)) & 255)) continue;
+#pragma unroll 4
+                for (int j = 0; j < 8; ++j)
+                    if (8 * k + j < m) take(k, j, es[8 * k + j][lane], false);
             }
         }
     } else {
+        for (int k = 0; 8 * k < m; ++k) {
+            if (warp == k) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (n0 + j < m) {
+                        const float ej = e[j];
+                        es[n0 + j][lane] = ej;
+                        take(k, j, ej, true);
+                    }
+            }
+            __syncthreads();
+            if (warp > k && mine && ((above >> (8 * k)) & 255)) {
+#pragma unroll 4
+                for (int j = 0; j < 8; ++j) take(k, j, es[8 * k + j][lane], true);
+            }
+        }
+    }
+    if (lane < RB) {
 #pragma unroll
         for (int x = 0; x < 8; ++x)
-            if (warp + 8 * x < m && lane < RB) es[warp + 8 * x][r] = e[x];
-        __syncthreads();
-    }
-#pragma unroll
-    for (int x = 0; x < 8; ++x) {
-        const int n = warp + 8 * x;
-        if (n >= m) continue;
-        float y = sum_parts(a, bh, b, h, D, n, rb * RB + r);
-        for (int j = 0; j <= n; ++j) {
-            const float w = Ps[n * a.Tp + j];
-            if (w != 0.f) y = fmaf(w, es[j][r], y);  // a node that is no ancestor is not multiplied, whatever it holds
-        }
-        if (lane < RB) static_cast<E *>(a.y)[(at + n) * D + rb * RB + r] = from_f<E>(y);
+            if (n0 + x < m) static_cast<E *>(a.y)[(at + n0 + x) * D + row] = from_f<E>(y[x]);
     }
 }
 
@@ -422,10 +480,12 @@ __global__ void __launch_bounds__(256) step_finish(TreeArgs a)
     constexpr int RB = D < 32 ? D : 32, LPR = D / 4, RPW = 32 / LPR, PASS = RB / (8 * RPW) < 1 ? 1 : RB / (8 * RPW);
     const Paged &c = a.c;
     const int bh = (int)blockIdx.x / (D / RB), rb = (int)blockIdx.x % (D / RB), b = bh / c.H, h = bh % c.H;
-    const int row = a.p.act[b];
+    after_previous();
+    const Line line = line_in(a.line, a.B);
+    const int row = line.row[b], pos = line.pos[b], in0 = pos % c.C;
     if (row < 0) return;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int pos = a.p.pos[b], in0 = pos % c.C;
+    const Parts parts(a, line, b, h, cached_segments(c, pos));
     const int32_t *fresh = a.p.fresh + b;
     const bool ends = in0 == c.C - 1;
     const int page = ends && fresh[1] > fresh[0] ? a.p.list[fresh[0]] : -1;
@@ -438,8 +498,15 @@ __global__ void __launch_bounds__(256) step_finish(TreeArgs a)
         const float g_on = a.f0[(size_t)bh * a.Tp];
         float4 *mem = reinterpret_cast<float4 *>(c.online + (((size_t)row * c.H + h) * D + r0) * D) + lane % LPR;
         float4 m[PASS];
+        float sum[PASS];
 #pragma unroll
-        for (int x = 0; x < PASS; ++x) m[x] = in0 ? mem[x * RPW * (D / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int x = 0; x < PASS; ++x) {
+            m[x] = in0 ? mem[x * RPW * (D / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+            sum[x] = 0.f;
+        }
+        for (int j = parts.j0; j <= parts.j1; ++j)
+#pragma unroll
+            for (int x = 0; x < PASS; ++x) sum[x] += a.part[((size_t)j + bh) * a.Tp * D + r0 + x * RPW];
 #pragma unroll
         for (int x = 0; x < PASS; ++x) {
             const int r = r0 + x * RPW;
@@ -457,7 +524,7 @@ __global__ void __launch_bounds__(256) step_finish(TreeArgs a)
             float y = dot4(m[x], qv);
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-            if (lane % LPR == 0) static_cast<E *>(a.y)[at + r] = from_f<E>(sum_parts(a, bh, b, h, D, 0, r) + g_on * y);
+            if (lane % LPR == 0) static_cast<E *>(a.y)[at + r] = from_f<E>(fmaf(g_on, y, sum[x]));
         }
     }
     if (rb == 0 && tid < D) {
@@ -474,38 +541,32 @@ __global__ void __launch_bounds__(256) step_finish(TreeArgs a)
 template <typename E, int D>
 cudaError_t gates_impl(const TreeArgs &a, cudaStream_t s)
 {
-    const size_t smem = gates_smem(a.c);
-    cudaError_t e = cudaFuncSetAttribute(tree_gates<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    tree_gates<E, D><<<(unsigned)(a.B * a.c.H * ((a.T + kGroup - 1) / kGroup)), kGateThreads, smem, s>>>(a);
-    return cudaGetLastError();
+    return launch_early(tree_gates<E, D>, (size_t)a.B * a.c.H * a.groups + 1, kGateThreads, gates_smem(a), s, a);
 }
 
 template <typename E, int D>
 cudaError_t read_impl(const TreeArgs &a, cudaStream_t s)
 {
-    const unsigned grid = (unsigned)(a.ranges * a.groups);
-    if (a.T == 1) tree_read<E, D, 1><<<grid, 256, 0, s>>>(a);
-    else if (a.T == 2) tree_read<E, D, 2><<<grid, 256, 0, s>>>(a);
-    else if (a.T <= 4) tree_read<E, D, 4><<<grid, 256, 0, s>>>(a);
-    else tree_read<E, D, 8><<<grid, 256, 0, s>>>(a);
-    return cudaGetLastError();
+    const size_t grid = (size_t)a.ranges * a.groups, smem = sizeof(int) * Line::ints(a.B);
+    return a.T == 1   ? launch_early(tree_read<E, D, 1>, grid, 256, smem, s, a)
+           : a.T == 2 ? launch_early(tree_read<E, D, 2>, grid, 256, smem, s, a)
+           : a.T <= 4 ? launch_early(tree_read<E, D, 4>, grid, 256, smem, s, a)
+                      : launch_early(tree_read<E, D, 8>, grid, 256, smem, s, a);
 }
 
 template <typename E, int D>
 cudaError_t finish_impl(const TreeArgs &a, cudaStream_t s)
 {
     constexpr int RB = D < 32 ? D : 32;
-    const unsigned grid = (unsigned)(a.B * a.c.H * (D / RB));
-    if (a.step) {
-        step_finish<E, D><<<grid, 256, 0, s>>>(a);
-        return cudaGetLastError();
+    const size_t grid = (size_t)a.B * a.c.H * (D / RB);
+    if (a.step) return launch_early(step_finish<E, D>, grid, 256, 0, s, a);
+    const bool split = tree_tc_supported(a);
+    const size_t smem = sizeof(float) * ((a.delta ? 2 : 1) + (split ? 1 : 0)) * (size_t)a.T * a.Tp;
+    const int block = 32 * a.groups;  // a warp to eight nodes
+    if constexpr (sizeof(E) == 2 && D >= 64) {
+        if (split) return launch_early(tree_finish<E, D, true>, grid, block, smem, s, a);
     }
-    const size_t smem = sizeof(float) * 2 * kMaxTree * kMaxTree;
-    cudaError_t e = cudaFuncSetAttribute(tree_finish<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    tree_finish<E, D><<<grid, 256, smem, s>>>(a);
-    return cudaGetLastError();
+    return launch_early(tree_finish<E, D, false>, grid, block, smem, s, a);
 }
 
 template <typename E>
@@ -526,7 +587,10 @@ cudaError_t run(const TreeArgs &a, cudaStream_t s, int what)
 
 }  // namespace
 
-cudaError_t launch_tree_gates(const TreeArgs &a, cudaStream_t s) { return run(a, s, 0); }
+cudaError_t launch_tree_gates(const TreeArgs &a, cudaStream_t s)
+{
+    return tree_tc_supported(a) ? launch_tree_path_tc(a, s) : run(a, s, 0);
+}
 cudaError_t launch_tree_read(const TreeArgs &a, cudaStream_t s)
 {
     return tree_tc_supported(a) ? launch_tree_read_tc(a, s) : run(a, s, 1);

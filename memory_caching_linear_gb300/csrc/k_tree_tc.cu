@@ -1,22 +1,29 @@
-// k_tree_tc.cu -- the cached memories' reads of a drafted tree on the tensor cores (bf16 tokens, d = 64 or 128, more than 8
-// nodes, every cached memory read by every node: no SSC).
+// k_tree_tc.cu -- what a drafted tree reads of the cached memories, on the tensor cores (bf16 tokens, d = 64 or 128, more than
+// 8 nodes, every cached memory read by every node: no SSC).
 //
-// For the head at hand, D[r][t] = sum over memories i of M^(i)[r][:] . (g_{t,i} q_t): the fp32 memory is the A operand as it
-// comes by TMA (kind::tf32 takes 11 significant bits of it: 2^-11 of every product against the 2^-9 of y's own rounding), the
-// gate-scaled queries are B, rounded to tf32, and the sum over a head's memories stays in tensor memory.  A memory of 64 KB
-// is read from HBM once for all nodes, 1.5 us of an SM's share of the bandwidth, against 0.3 us of products at 64 nodes: HBM
-// is the bound, so the memories stream through a ring of 32-column panels (144 KB in flight on an SM) and everything else is
-// made to keep up.
+// The reads (tree_read_tc).  For the head at hand, D[r][t] = sum over memories i of M^(i)[r][:] . (g_{t,i} q_t): the fp32 memory is
+// the A operand as it comes by TMA (kind::tf32 takes 11 significant bits of it: 2^-11 of every product against the 2^-9 of
+// y's own rounding), the weighted queries are B, rounded to tf32, and the sum over a head's memories stays in tensor memory.
+// A memory of 64 KB is read from HBM once for all nodes, 1.5 us of an SM's share of the bandwidth, against 0.3 us of products
+// at 64 nodes: HBM is the bound, so the memories stream through a ring of 32-column panels (128 KB in flight on an SM) and
+// everything else is made to keep up.
 //
-// The memories of all heads and sequences form one line, cut into one range per CTA whatever the sequences' lengths; a head
-// that crosses a cut leaves partial sums, which tree_finish adds in their order.
+// The memories of all heads and sequences form one line, cut into one range per CTA whatever the sequences' lengths.  A range
+// works out the scores of its own memories when it comes to a head (while the ring fills), weighs them against its own largest
+// and leaves the sum of its weights with its partial read: tree_finish joins them, as a softmax over parts.  So nothing has to
+// be known of the other ranges before the memories can be read; and the begun segment's memory, whose weight hangs on the
+// path, is read without one.
 //
-// Warps 0-7 make B and drain D, warp 8 brings the panels, warp 9 issues the products.
+// The path's own products (tree_path_tc) are a small kernel that runs beside the reads: they do not wait for it, but
+// end after it.
+#include <cfloat>
 #include <cstdint>
 
+#include "mma_sync.cuh"
 #include "paged.cuh"
 #include "sm100.cuh"
 #include "tensormap.cuh"
+#include "tree_nodes.cuh"
 
 namespace mc {
 
@@ -25,12 +32,6 @@ using namespace sm100;
 namespace {
 
 __device__ int g_tree_abort;
-
-constexpr int kWorkers = 8, kThreads = 32 * (kWorkers + 2);
-constexpr int kRingBytes = 147456;            // nine panels of 128 rows, eighteen of 64
-constexpr int kMaxPanels = 18;
-constexpr int kBSlot = kMaxTree * 128 * 4;    // gate-scaled queries of one memory
-constexpr int kSmem = 1024 + kRingBytes + 2 * kBSlot;
 
 // kind::tf32: as idesc_bf16 with both formats tf32.
 __host__ __device__ constexpr uint32_t idesc_tf32(int M, int N)
@@ -51,39 +52,169 @@ __device__ __forceinline__ float to_tf32(float x)
     return __uint_as_float(r);
 }
 
-// One head's memories (or its begun memory for the keys) within a CTA's range.
+// Warp-level products (m16n8k16) take the columns of their operands in an order that makes a lane's four of every 16 adjacent:
+// tokens and keys come straight from global memory, 8 bytes a lane, and mean keys, in fp32, 16.
+// Rows g and g + 8 (g = lane / 4) of an A operand at columns 16 ks + 4 (lane % 4) .. + 3; null rows are zeros.
+__device__ __forceinline__ void rows_of(const __nv_bfloat16 *lo, const __nv_bfloat16 *hi, int col, uint32_t (&f)[4])
+{
+    const uint2 x = lo ? __ldg(reinterpret_cast<const uint2 *>(lo + col)) : make_uint2(0, 0);
+    const uint2 y = hi ? __ldg(reinterpret_cast<const uint2 *>(hi + col)) : make_uint2(0, 0);
+    f[0] = x.x;
+    f[1] = y.x;
+    f[2] = x.y;
+    f[3] = y.y;
+}
+
+// ------------------------------------------------------------------------------------------------ the path
+
+constexpr int kSpan = 32, kPathThreads = 256, kCol = kSpan + 1;
+// The two kernels run side by side: bounds above their blocks keep path and read to 96 and 128 registers a thread (24 K and
+// 40 K of an SM's 64 K).
+constexpr int kPathRegs = 640, kReadRegs = 512;
+
+// Scores of the path's segments, P without the gates, and A, for 32 nodes of a head at a time.  One CTA on an SM goes over its
+// share of the heads: little enough in registers and shared memory to run beside a CTA of tree_read_tc.
+template <int D>
+__global__ void __launch_bounds__(kPathRegs) tree_path_tc(TreeArgs a, int spans)
+{
+    constexpr int KS = D / 16;
+    __shared__ Nodes nodes;
+    __shared__ float uk[kMaxTree * kCol], us[kSpan];  // u . k [node][token], u . key sum
+    extern __shared__ int space[];
+    const Paged &c = a.c;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, c4 = lane % 4;
+    const bool routed = a.mode == MC_GRM;
+    after_previous();
+    let_next_start();
+    if (blockIdx.x == gridDim.x - 1) {  // one CTA more, for tree_finish
+        leave_line(a, space);
+        return;
+    }
+    const Line line = make_line(a, space, false);
+    for (long long item = blockIdx.x; item < (long long)a.B * c.H * spans; item += gridDim.x - 1) {
+        const int bh = (int)(item / spans), n0 = (int)(item % spans) * kSpan, b = bh / c.H, h = bh % c.H;
+        const int row = line.row[b], m = line.nodes[b], in0 = line.pos[b] % c.C;
+        if (row < 0 || n0 >= m) continue;
+        __syncthreads();  // the item before has read nodes and products
+        make_nodes<__nv_bfloat16>(a, nodes, b, bh, m, in0);
+        const __nv_bfloat16 *U = static_cast<const __nv_bfloat16 *>(a.u) + (size_t)bh * a.T * D;
+        const __nv_bfloat16 *Q = static_cast<const __nv_bfloat16 *>(a.q) + (size_t)bh * a.T * D;
+        const __nv_bfloat16 *K = static_cast<const __nv_bfloat16 *>(a.k) + (size_t)bh * a.T * D;
+        if (routed && in0) {  // the begun segment's keys
+            const float *sum = c.ksum + ((size_t)row * c.H + h) * D;
+            for (int t = warp; t < kSpan && n0 + t < m; t += 8) {
+                float x = 0.f;
+                if (lane < D / 4) x = dot4(load4(U + (size_t)(n0 + t) * D + 4 * lane), load4(sum + 4 * lane));
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+                if (lane == 0) us[t] = x;
+            }
+        }
+        // sixteen tokens and sixteen nodes a warp
+        const int x0 = warp / 2 * 16, lo = n0 + warp % 2 * 16 + g, hi = lo + 8;
+        if (x0 < m) {
+            float uf[2][4] = {}, qf[2][4] = {}, kf[2][4] = {};
+            auto row_of = [&](const __nv_bfloat16 *x, int n) { return n < m ? x + (size_t)n * D : nullptr; };
+#pragma unroll 4
+            for (int ks = 0; ks < KS; ++ks) {
+                const int col = 16 * ks + 4 * c4;
+                uint32_t key[4], f[4];
+                rows_of(row_of(K, x0 + g), row_of(K, x0 + 8 + g), col, key);  // B of two tiles: {0, 2} and {1, 3}
+                if (routed) {
+                    rows_of(row_of(U, lo), row_of(U, hi), col, f);
+                    mma::mma16816(uf[0], f, key[0], key[2]);
+                    mma::mma16816(uf[1], f, key[1], key[3]);
+                }
+                rows_of(row_of(Q, lo), row_of(Q, hi), col, f);
+                mma::mma16816(qf[0], f, key[0], key[2]);
+                mma::mma16816(qf[1], f, key[1], key[3]);
+                if (a.delta) {
+                    rows_of(row_of(K, lo), row_of(K, hi), col, f);
+                    mma::mma16816(kf[0], f, key[0], key[2]);
+                    mma::mma16816(kf[1], f, key[1], key[3]);
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const int x = x0 + 8 * nt + 2 * c4 + (y & 1), n = y & 2 ? hi : lo;
+                    uk[x * kCol + n - n0] = uf[nt][y];
+                    if (x >= m || n >= a.Tp) continue;
+                    const bool above = n < m && (nodes.anc[n] >> x) & 1;
+                    a.P[((size_t)bh * a.T + x) * a.Tp + n] = above ? path_read(a, nodes, n, x, 1.f, qf[nt][y]) : 0.f;
+                    if (a.delta) a.A[((size_t)bh * a.T + x) * a.Tp + n] = above ? path_meet(nodes, n, x, kf[nt][y]) : 0.f;
+                }
+        }
+        __syncthreads();
+        for (int t = warp; t < kSpan && n0 + t < m; t += 8) {
+            const int n = n0 + t, last = nodes.seg[n];
+            const uint64_t mine = nodes.anc[n];
+            float *score = a.score + (size_t)bh * a.T * a.Tp + n;
+            if (routed) {
+                for (int j = 0; j <= last; ++j) {
+                    const uint64_t w = mine & nodes.seg_set[j];
+                    float x = ((w >> lane) & 1 ? uk[lane * kCol + t] : 0.f) + ((w >> (lane + 32)) & 1 ? uk[(lane + 32) * kCol + t] : 0.f);
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+                    if (j == 0 && in0) x += us[t];
+                    if (lane == 0) score[(size_t)j * a.Tp] = x / (float)(j < last ? c.C : (in0 + __popcll(mine) - 1) % c.C + 1);
+                }
+            } else {
+                for (int j = lane; j <= last; j += 32) score[(size_t)j * a.Tp] = 0.f;
+            }
+            if (lane == 0) {
+                a.into[(size_t)bh * a.Tp + n] = a.delta ? decay_from_cache(nodes, n) : 1.f;
+                if (h == 0) {
+                    a.anc[(size_t)b * kMaxTree + n] = mine;
+                    a.seg[(size_t)b * kMaxTree + n] = last;
+                }
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------------------ the reads
+
+constexpr int kWorkers = 8, kThreads = 32 * (kWorkers + 2);
+constexpr int kRingBytes = 131072;            // eight panels of 128 rows, sixteen of 64
+constexpr int kMaxPanels = 16;
+constexpr int kBSlot = kMaxTree * 128 * 4;    // weighted queries of one memory
+constexpr int kULine = 288;                   // bytes between a run's router inputs: rows eight banks apart
+constexpr int kReadSmem = 1024 + kRingBytes + 2 * kBSlot + kMaxTree * kULine;
+
+enum { kCached, kBegunQ, kBegunK };
+// Memories of one head that follow each other in a CTA's range: cached ones, or the begun one for the queries or the keys.
 struct Run {
-    int b, h, bh, row, nb, m, i0, i1;
-    bool keys;
+    int h, bh, row, nb, m, i0, i1, kind;
 };
 // The runs of a range, in order; every role walks the same ones.
 struct Runs {
     long long x, end;
     int b;
-    __device__ Runs(const TreeArgs &a)
+    __device__ Runs(const TreeArgs &a, const Line &l)
     {
-        const long long U = (long long)a.p.units[a.B] * a.c.H, R = ranges_of(U, a.ranges);
+        const long long U = (long long)l.units[a.B] * a.c.H, R = ranges_of(U, a.ranges);
         const bool in = blockIdx.x < R;
         x = in ? range_begin(blockIdx.x, U, R) : 0;
         end = in ? range_begin(blockIdx.x + 1, U, R) : 0;
         b = 0;
     }
-    __device__ bool next(const TreeArgs &a, Run &r)
+    __device__ bool next(const TreeArgs &a, const Line &l, Run &r)
     {
         if (x >= end) return false;
-        while (x >= (long long)a.p.units[b + 1] * a.c.H) ++b;
-        const int u0 = a.p.units[b], nu = a.p.units[b + 1] - u0;
+        while (x >= (long long)l.units[b + 1] * a.c.H) ++b;
+        const int u0 = l.units[b], nu = l.units[b + 1] - u0;
         const long long in_b = x - (long long)u0 * a.c.H;
-        r.b = b;
         r.h = (int)(in_b / nu);
         r.bh = b * a.c.H + r.h;
-        r.row = a.p.act[b];
-        r.nb = cached_segments(a.c, a.p.pos[b]);
-        r.m = nodes_of(a, b);
+        r.row = l.row[b];
+        r.nb = cached_segments(a.c, l.pos[b]);
+        r.m = l.nodes[b];
         r.i0 = (int)(in_b % nu);
-        r.keys = r.i0 > r.nb;
+        r.kind = r.i0 < r.nb ? kCached : r.i0 == r.nb ? kBegunQ : kBegunK;
+        const int stop = r.kind == kCached ? r.nb : r.i0 + 1;
         const long long left = end - x;
-        const int stop = r.keys || nu <= r.nb + 1 ? nu : r.nb + 1;  // the keys' read is a run of its own
         r.i1 = left < stop - r.i0 ? r.i0 + (int)left : stop;
         x += r.i1 - r.i0;
         return true;
@@ -91,19 +222,22 @@ struct Runs {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kReadRegs)
 tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ CUtensorMap online, TreeArgs a)
 {
-    constexpr int PANELS = D / 32, kPanelBytes = D * 128, RING = kRingBytes / kPanelBytes;
+    constexpr int PANELS = D / 32, kPanelBytes = D * 128, RING = kRingBytes / kPanelBytes, KS = D / 16;
     extern __shared__ uint8_t raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint8_t *bs = ring + kRingBytes;  // (a 64-row panel's second half, which nobody reads, may be of the next one or of B)
-    __shared__ uint64_t full[kMaxPanels], empty[kMaxPanels], b_full[2], b_empty[2], d_full[2], d_empty[2], drain;
+    uint8_t *us = bs + 2 * kBSlot;
+    int *space = reinterpret_cast<int *>(raw + kReadSmem);
+    __shared__ uint64_t full[kMaxPanels], empty[kMaxPanels], b_full[2], b_empty[2], d_full[2], d_empty[2], staged, scored, drain;
+    __shared__ float top[kWorkers][kMaxTree];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
     const Paged &c = a.c;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int NT = (a.T + 15) / 16 * 16;                       // columns of D
+    const int NT = (a.T + 15) / 16 * 16;                           // columns of D
     const int groups = (NT + 31) / 32, writers = PANELS * groups;  // warps that make B: 32 tokens of one panel each
     if (tid == 0) {
         abort_flag = 0;
@@ -117,6 +251,8 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
             mbar_init(&d_full[i], 1);
             mbar_init(&d_empty[i], kWorkers);
         }
+        mbar_init(&staged, kWorkers);
+        mbar_init(&scored, kWorkers);
         mbar_init(&drain, 1);
         fence_mbar_init();
     }
@@ -124,11 +260,12 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
         tmem_alloc(&tmem_base, 128);
         tmem_relinquish();
     }
+    const Line line = make_line(a, space, false);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tb = tmem_base;
-    Runs runs(a);
+    Runs runs(a, line);
     Run r;
 
     if (warp == kWorkers) {
@@ -137,14 +274,14 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
             prefetch_tensormap(&online);
             uint32_t g = 0;
             bool ok = true;
-            while (ok && runs.next(a, r)) {
+            while (ok && runs.next(a, line, r)) {
                 const int32_t *table = c.table + (size_t)r.row * c.nmax;
-                int page = r.i0 < r.nb ? table[r.i0] : 0;
+                const bool cached = r.kind == kCached;
+                int page = cached ? table[r.i0] : 0;
                 for (int i = r.i0; ok && i < r.i1; ++i) {
                     const int p = page;
-                    if (i + 1 < r.nb && i + 1 < r.i1) page = table[i + 1];
+                    if (cached && i + 1 < r.i1) page = table[i + 1];
                     // a segment without a page is one past the pool: zeros
-                    const bool cached = i < r.nb;
                     const int at = cached ? (valid_page(c, p) < 0 ? c.P * c.H : p * c.H + r.h) : r.row * c.H + r.h;
                     for (int x = 0; x < PANELS; ++x, ++g) {
                         const uint32_t s = g % RING;
@@ -167,7 +304,7 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
             const uint32_t idesc = idesc_tf32(128, NT);
             uint32_t g = 0, u = 0, n = 0;
             bool ok = true;
-            while (ok && runs.next(a, r)) {
+            while (ok && runs.next(a, line, r)) {
                 const uint32_t d = tb + 64 * (n & 1);
                 ok = mbar_wait(&d_empty[n & 1], ((n >> 1) & 1) ^ 1, &abort_flag);
                 for (int i = r.i0; ok && i < r.i1; ++i, ++u) {
@@ -198,29 +335,113 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
         __syncwarp();
     } else {
         const int panel = warp % PANELS, t = warp / PANELS * 32 + lane;  // this thread's token and 32 columns of B
-        const bool writes = warp < writers;
-        uint32_t u = 0, n = 0;
+        const bool writes = warp < writers, routed = a.mode == MC_GRM;
+        uint32_t u = 0, n = 0, scorings = 0;
         bool ok = true;
-        while (ok && runs.next(a, r)) {
-            if (writes) {
-                uint32_t q[16];
-                const bool in = t < r.m;
-                if (in) {
-                    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(r.keys ? a.k : a.q) +
-                                                                       ((size_t)r.bh * a.T + t) * D + 32 * panel);
+        while (ok && runs.next(a, line, r)) {
+            float *scores = a.gates + (size_t)r.bh * (c.nmax + 2) * a.Tp;
+            const bool in = writes && t < r.m, cached = r.kind == kCached;
+            float best = 0.f;
+            if (cached && routed) {
+                // scores of the run's memories, eight segments a warp at a time; a mean key takes part in two bf16 terms (2^-17 of
+                // it, for weights that are not ranked).  The ring holds 3 us of memories: the loads here, which nothing hides,
+                // come in two rounds, pages' numbers and router inputs, then mean keys.
+                const int32_t *table = c.table + (size_t)r.row * c.nmax;
+                const int g = lane / 4, c4 = lane % 4;
+                const float low = __int_as_float(0xff800000);
+                int page = r.i0 + 8 * warp + g < r.i1 ? table[r.i0 + 8 * warp + g] : -1;
+                const uint4 *U = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.u) + (size_t)r.bh * a.T * D);
+                for (int x = tid; x < r.m * (D / 8); x += 32 * kWorkers)
+                    *reinterpret_cast<uint4 *>(us + x / (D / 8) * kULine + x % (D / 8) * 16) = __ldg(U + x);
+                float most[2 * (kMaxTree / 16)];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const uint4 w = __ldg(src + x);
-                        q[4 * x] = w.x;
-                        q[4 * x + 1] = w.y;
-                        q[4 * x + 2] = w.z;
-                        q[4 * x + 3] = w.w;
+                for (int x = 0; x < 2 * (kMaxTree / 16); ++x) most[x] = low;
+                bool waited = false;
+                for (int i0 = r.i0 + 8 * warp; i0 < r.i1 || !waited; i0 += 8 * kWorkers) {
+                    page = valid_page(c, page);
+                    const float *src = c.kbar + ((size_t)max(page, 0) * c.H + r.h) * D;
+                    float4 v[KS];
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) v[ks] = page >= 0 ? load4(src + 16 * ks + 4 * c4) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    const bool there0 = __shfl_sync(0xffffffffu, page, 8 * c4) >= 0, there1 = __shfl_sync(0xffffffffu, page, 8 * c4 + 4) >= 0;
+                    const int ahead = i0 + 8 * kWorkers + g;
+                    page = ahead < r.i1 ? table[ahead] : -1;
+                    if (!waited) {  // every warp has its share of the router inputs in place
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&staged);
+                        if (!(ok = mbar_wait(&staged, scorings & 1, &abort_flag))) break;
+                        waited = true;
+                        if (i0 >= r.i1) break;
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < kMaxTree / 16; ++mt) {
+                        if (16 * mt >= r.m) continue;
+                        const int lo = 16 * mt + g, hi = lo + 8;
+                        const uint8_t *ulo = us + lo * kULine + 8 * c4, *uhi = us + hi * kULine + 8 * c4;
+                        float s[4] = {};
+#pragma unroll
+                        for (int ks = 0; ks < KS; ++ks) {
+                            uint32_t h0, h1, l0, l1;
+                            const uint2 x = *reinterpret_cast<const uint2 *>(ulo + 32 * ks), y = *reinterpret_cast<const uint2 *>(uhi + 32 * ks);
+                            const uint32_t f[4] = {x.x, y.x, x.y, y.y};
+                            mma::split2(v[ks].x, v[ks].y, h0, l0);
+                            mma::split2(v[ks].z, v[ks].w, h1, l1);
+                            mma::mma16816(s, f, h0, h1);
+                            mma::mma16816(s, f, l0, l1);
+                        }
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {  // segment i0 + 2 c4 (+ 1), token lo or hi
+                            const int seg = i0 + 2 * c4 + (y & 1), token = y & 2 ? hi : lo;
+                            const float x = (y & 1 ? there1 : there0) ? s[y] : low;
+                            most[2 * mt + (y >> 1)] = fmaxf(most[2 * mt + (y >> 1)], x);
+                            if (seg < r.i1 && token < r.m) scores[(size_t)seg * a.Tp + token] = x;
+                        }
                     }
                 }
-                const float *gates = a.gates + (size_t)r.bh * (c.nmax + 2) * a.Tp + t;
-                float g = in ? gates[(size_t)r.i0 * a.Tp] : 0.f;
+                if (!ok) break;
+#pragma unroll
+                for (int x = 0; x < 2 * (kMaxTree / 16); ++x) {
+                    most[x] = fmaxf(most[x], __shfl_xor_sync(0xffffffffu, most[x], 1));
+                    most[x] = fmaxf(most[x], __shfl_xor_sync(0xffffffffu, most[x], 2));
+                    if (c4 == 0) top[warp][16 * (x / 2) + 8 * (x & 1) + g] = most[x];
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&scored);
+                if (!(ok = mbar_wait(&scored, scorings & 1, &abort_flag))) break;
+                if (in) {
+                    best = -FLT_MAX;  // (no segment of the run may have a page)
+#pragma unroll
+                    for (int x = 0; x < kWorkers; ++x) best = fmaxf(best, top[x][t]);
+                }
+                ++scorings;
+            }
+            uint32_t q[16];
+            if (in) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(r.kind == kBegunK ? a.k : a.q) +
+                                                                   ((size_t)r.bh * a.T + t) * D + 32 * panel);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const uint4 w = __ldg(src + x);
+                    q[4 * x] = w.x;
+                    q[4 * x + 1] = w.y;
+                    q[4 * x + 2] = w.z;
+                    q[4 * x + 3] = w.w;
+                }
+            }
+            float z = 0.f;
+            if (writes) {
+                const int32_t *table = c.table + (size_t)r.row * c.nmax;
+                // the weight's logarithm: a score; 0 for a page where nothing is scored
+                auto load = [&](int i) {
+                    if (!in || i >= r.i1) return 0.f;
+                    if (!cached) return 0.f;
+                    return routed ? scores[(size_t)i * a.Tp + t] : valid_page(c, table[i]) >= 0 ? 0.f : __int_as_float(0xff800000);
+                };
+                float next = load(r.i0);
                 for (int i = r.i0; i < r.i1; ++i, ++u) {
-                    const float next = in && i + 1 < r.i1 ? gates[(size_t)(i + 1) * a.Tp] : 0.f;
+                    const float g = expf(next - best);
+                    next = load(i + 1);
+                    z += g;
                     if (!(ok = mbar_wait(&b_empty[u & 1], ((u >> 1) & 1) ^ 1, &abort_flag))) break;
                     uint8_t *row = bs + (u & 1) * kBSlot + panel * NT * 128 + t * 128;
                     if (t < NT) {
@@ -239,14 +460,16 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&b_full[u & 1]);
-                    g = next;
                 }
             }
-            if (!ok || !(ok = mbar_wait(&d_full[n & 1], (n >> 1) & 1, &abort_flag))) break;
+            if (!ok) break;
+            const size_t part = (size_t)blockIdx.x + r.bh;
+            if (cached && in && panel == 0) a.weight[part * a.Tp + t] = make_float2(best, z);
+            if (!(ok = mbar_wait(&d_full[n & 1], (n >> 1) & 1, &abort_flag))) break;
             tc_fence_after();
             // rows 32 (warp % 4) + lane of D; the two warps of a quarter take every other 16 columns
             const int quarter = warp % 4, row = 32 * quarter + lane;
-            float *out = r.keys ? a.Z + (size_t)r.bh * a.Tp * D : a.part + ((size_t)blockIdx.x + r.bh) * a.Tp * D;
+            float *out = cached ? a.part + part * a.Tp * D : (r.kind == kBegunQ ? a.Y0 : a.Z) + (size_t)r.bh * a.Tp * D;
             for (int t0 = 16 * (warp / 4); t0 < NT; t0 += 32) {
                 float x[16];
                 tmem_ld16f(tmem_addr(tb + 64 * (n & 1), 32 * quarter, t0), x);
@@ -270,6 +493,16 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
         tmem_dealloc(tb, 128);
     }
     if (tid == 0 && abort_flag) atomicExch(&g_tree_abort, 1);
+    let_next_start();
+    after_previous();  // what comes after this kernel needs the path's products too
+}
+
+template <int D>
+cudaError_t path_impl(const TreeArgs &a, cudaStream_t s)
+{
+    const int spans = (a.T + kSpan - 1) / kSpan;
+    const long long items = (long long)a.B * a.c.H * spans;
+    return launch_early(tree_path_tc<D>, (size_t)(items < a.ranges ? items : a.ranges) + 1, kPathThreads, sizeof(int) * Line::ints(a.B), s, a, spans);
 }
 
 // A [matrices][D][D] fp32 tensor in boxes of 32 columns of one matrix, 128-byte swizzled.
@@ -294,17 +527,19 @@ bool tree_tc_supported(const TreeArgs &a)
     return a.bf16 && (a.c.d == 64 || a.c.d == 128) && a.T > 8 && a.mode != MC_SSC && (long long)a.c.P * a.c.H < (1ll << 31) - 1;
 }
 
+cudaError_t launch_tree_path_tc(const TreeArgs &a, cudaStream_t s)
+{
+    return a.c.d == 128 ? path_impl<128>(a, s) : path_impl<64>(a, s);
+}
+
 cudaError_t launch_tree_read_tc(const TreeArgs &a, cudaStream_t s)
 {
     CUtensorMap pages, online;
     if (!make_map(&pages, a.c.pages, (unsigned long long)a.c.P * a.c.H, a.c.d) ||
         !make_map(&online, a.c.online, (unsigned long long)a.c.S * a.c.H, a.c.d))
         return cudaErrorInvalidValue;
-    auto kern = a.c.d == 128 ? tree_read_tc<128> : tree_read_tc<64>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    kern<<<(unsigned)a.ranges, kThreads, kSmem, s>>>(pages, online, a);
-    return cudaGetLastError();
+    return launch_early(a.c.d == 128 ? tree_read_tc<128> : tree_read_tc<64>, (size_t)a.ranges, kThreads,
+                        kReadSmem + sizeof(int) * Line::ints(a.B), s, pages, online, a);
 }
 
 cudaError_t take_tree_abort(int *was_set)

@@ -98,21 +98,32 @@ int run_batch(const mc_paged_cache *cache, TreeArgs a, int agg_mode, cudaStream_
     const size_t BH = (size_t)a.B * c.H, T = a.T, B = a.B;
     a.Tp = (a.T + 7) / 8 * 8;
     a.groups = a.Tp / 8;
-    a.ranges = tree_tc_supported(a) ? kSms : std::max(1, 4 * kSms / a.groups);
+    const bool split = tree_tc_supported(a), writes = a.step || accept;
+    a.ranges = split ? kSms : std::max(1, 4 * kSms / a.groups);
     void *scratch = nullptr;
     for (int pass = 0; pass < 2; ++pass) {
         Carver cv{static_cast<char *>(scratch), 0};
-        a.p.path = cv.take<uint64_t>(B);
-        a.p.act = cv.take<int32_t>(B);
-        a.p.pos = cv.take<int32_t>(B);
-        a.p.len = cv.take<int32_t>(B);
-        a.p.fresh = cv.take<int32_t>(B + 1);
-        a.p.units = cv.take<int32_t>(B + 1);
-        a.p.list = cv.take<int32_t>(B * T);
+        if (writes) {
+            a.p.path = cv.take<uint64_t>(B);
+            a.p.act = cv.take<int32_t>(B);
+            a.p.pos = cv.take<int32_t>(B);
+            a.p.len = cv.take<int32_t>(B);
+            a.p.fresh = cv.take<int32_t>(B + 1);
+            a.p.list = cv.take<int32_t>(B * T);
+        }
         if (!accept) {
+            a.line = cv.take<int32_t>(Line::ints(a.B));
             a.gates = cv.take<float>(BH * (c.nmax + 2) * a.Tp);
             a.Z = cv.take<float>(a.delta && !a.step ? BH * a.Tp * c.d : 0);
+            if (split) {
+                a.Y0 = cv.take<float>(BH * a.Tp * c.d);
+                a.score = cv.take<float>(BH * T * a.Tp);
+                a.into = cv.take<float>(BH * a.Tp);
+                a.seg = cv.take<int32_t>(B * kMaxTree);
+                a.weight = cv.take<float2>((a.ranges + BH) * a.Tp);
+            }
             a.f0 = cv.take<float>(BH * a.Tp);
+            a.anc = cv.take<uint64_t>(B * kMaxTree);
             a.P = cv.take<float>(BH * T * a.Tp);
             a.A = cv.take<float>(a.delta ? BH * T * a.Tp : 0);
             a.part = cv.take<float>((a.ranges + BH) * a.Tp * c.d);
@@ -123,16 +134,16 @@ int run_batch(const mc_paged_cache *cache, TreeArgs a, int agg_mode, cudaStream_
         }
     }
     profile_call_start(s);
-    cudaError_t e = launch_plan(a, s);
-    profile_after_kernel(s, "plan_rows");
+    cudaError_t e = writes ? launch_plan(a, s) : cudaSuccess;
+    if (writes) profile_after_kernel(s, "plan_rows");
     if (e == cudaSuccess && accept) {
         e = launch_accept(a, s);
         profile_after_kernel(s, "accept_rows");
     } else if (e == cudaSuccess) {
         e = launch_tree_gates(a, s);
-        profile_after_kernel(s, "tree_gates");
+        profile_after_kernel(s, split ? "tree_path_tc" : "tree_gates");
         if (e == cudaSuccess) e = launch_tree_read(a, s);
-        profile_after_kernel(s, tree_tc_supported(a) ? "tree_read_tc" : "tree_read");
+        profile_after_kernel(s, split ? "tree_read_tc" : "tree_read");
         if (e == cudaSuccess) e = launch_tree_finish(a, s);
         profile_after_kernel(s, a.step ? "step_finish" : "tree_finish");
     }

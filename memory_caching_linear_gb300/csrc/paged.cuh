@@ -1,9 +1,9 @@
 // paged.cuh -- argument blocks and device helpers of decoding over a paged cache (mc_pages.cu, k_pages.cu, k_tree.cu,
 // k_tree_tc.cu).
 //
-// Every call over a batch begins with a plan (one CTA): which row of the cache each batch row works on, its position, and
+// Calls that write the cache begin with a plan (one CTA): which row of the cache each batch row works on, its position, and
 // what it needs of the pool.  The kernels after it read positions from the plan alone, so that the last of them may write
-// the cache's.
+// the cache's.  A tree's reads need no plan.
 #pragma once
 
 #include "mc_internal.cuh"
@@ -27,15 +27,14 @@ struct Paged {
     int P, S, H, d, C, nmax;
 };
 
-// What a call does with the batch rows' sequences.
+// What a call that writes does with the batch rows' sequences.
 struct Plan {
-    int32_t *act;      // [B] the cache's row, -1: nothing to do
+    int32_t *act;      // [B] the cache's row, -1: nothing to do; null: no plan
     int32_t *pos;      // [B] position before the call
     int32_t *len;      // [B] tokens added (accept: the path's length)
     uint64_t *path;    // [B] accept: the nodes of the path
     int32_t *fresh;    // [B + 1] where a batch row's new pages begin in list
     int32_t *list;     // new pages in order of batch row and time, -1 where none was free
-    int32_t *units;    // [B + 1] memories to read before those of batch row b, per head
 };
 
 struct TreeArgs {
@@ -47,12 +46,23 @@ struct TreeArgs {
     const int32_t *slots;                 // [B], or null (batch row b is slot b)
     const int32_t *last;                  // [B] accept: the last node of the path
     void *y;                              // [B][H][T][d]
+    // Scratch.  In what follows a split read is one whose cached memories are weighed as they are read, each range of them
+    // against its own largest score (k_tree_tc.cu); otherwise the gates are worked out first (k_tree.cu).
+    int32_t *line;                        // the batch's seats (Line)
     float *gates;                         // [BH][nmax + 2][Tp] gates of the cached memories, then what nodes read of the begun
-                                          // segment's with their queries (gate and decay) and with their keys (decay)
-    float *P, *A;                         // [BH][T][Tp] what a node reads of what its ancestors wrote; what they meet in its key
+                                          // segment's with their queries (gate and decay) and with their keys (decay); a split
+                                          // read's scores
+    float *P, *A;                         // [BH][T][Tp] per ancestor: what nodes read of what it wrote (a split read's without
+                                          // the gates); what it meets in their keys
+    float *score;                         // [BH][T][Tp] split: nodes' scores of their paths' segments
+    float *into;                          // [BH][Tp] split: decay from the cache to a node's deepest ancestor in the begun segment
+    uint64_t *anc;                        // [B][64] a node's ancestors and itself
+    int32_t *seg;                         // [B][64] its segment, counted from the one begun
     float *f0;                            // [BH][Tp] a step: the online memory's gate
-    float *Z;                             // [BH][Tp][d] the begun segment's memory read with the nodes' keys, decayed
+    float *Y0, *Z;                        // [BH][Tp][d] the begun segment's memory read with the nodes' queries (split, without gate
+                                          // and decay) and with their keys (decayed; split: without)
     float *part;                          // [ranges + BH][Tp][d] partial reads
+    float2 *weight;                       // [ranges + BH][Tp] split: their largest score and sum of exp(score - largest)
     int B, T, Tp, mode, topk;
     int ranges, groups;                   // shares of the memories; of the tokens
     bool bf16, delta, step, accept;
@@ -73,9 +83,101 @@ __device__ __forceinline__ int units_of(const TreeArgs &a, int pos)
 {
     return cached_segments(a.c, pos) + (!a.step && pos % a.c.C ? (a.delta ? 2 : 1) : 0);
 }
-__device__ __forceinline__ int nodes_of(const TreeArgs &a, int b)
+// A batch row's place: the cache's row (-1: nobody's), its position, and its nodes.  tell: what is out of range is reported.
+struct Seat {
+    int row, pos, m;
+};
+__device__ __forceinline__ Seat seat_of(const TreeArgs &a, int b, bool tell)
 {
-    return a.count ? max(0, min(a.count[b], a.T)) : a.T;
+    Seat s{-1, 0, a.T};
+    if (a.p.act) {
+        s.row = a.p.act[b];
+        s.pos = a.p.pos[b];
+        return s;
+    }
+    const Paged &c = a.c;
+    const int slot = a.slots ? a.slots[b] : b;
+    bool bad = slot < -1 || slot >= c.S;
+    if (!bad && slot >= 0) {
+        s.row = c.row[slot];
+        if ((unsigned)s.row >= (unsigned)c.S || (unsigned)(s.pos = c.pos[s.row]) > (unsigned)kMaxPos) {
+            bad = true;
+            s.row = -1;
+        } else if (a.count) {
+            const int n = a.count[b];
+            s.m = max(0, min(n, a.T));
+            bad = s.m != n;
+        }
+    }
+    if (bad && tell) atomicOr(c.status, MC_PAGES_INDEX);
+    return s;
+}
+__device__ __forceinline__ int units_of(const TreeArgs &a, const Seat &s) { return s.row < 0 || s.m == 0 ? 0 : units_of(a, s.pos); }
+
+// The whole batch's seats and where their memories begin in the line of all (per head): 4 B + 1 ints.  Finding them takes four
+// loads that wait for one another, so a kernel does it once, and a kernel at a call's end is left them in memory.
+struct Line {
+    int *row, *pos, *nodes, *units;
+    __host__ __device__ static size_t ints(int B) { return 4 * (size_t)B + 1; }
+};
+__host__ __device__ inline Line line_in(int *space, int B) { return Line{space, space + B, space + 2 * B, space + 3 * B}; }
+// In shared memory; the whole block calls it.  tell as for seat_of.
+__device__ inline Line make_line(const TreeArgs &a, int *space, bool tell)
+{
+    const Line l = line_in(space, a.B);
+    for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
+        const Seat s = seat_of(a, b, tell);
+        l.row[b] = s.row;
+        l.pos[b] = s.pos;
+        l.nodes[b] = s.m;
+        l.units[b + 1] = units_of(a, s);
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        int sum = 0;
+        for (int b0 = 0; b0 < a.B; b0 += 32) {
+            const int b = b0 + (int)threadIdx.x;
+            int x = b < a.B ? l.units[b + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if ((int)threadIdx.x >= o) x += y;
+            }
+            if (b < a.B) l.units[b + 1] = sum + x;
+            sum += __shfl_sync(0xffffffffu, x, 31);
+        }
+        if (threadIdx.x == 0) l.units[0] = 0;
+    }
+    __syncthreads();
+    return l;
+}
+// To memory, for tree_finish and step_finish.
+__device__ inline void leave_line(const TreeArgs &a, int *space)
+{
+    make_line(a, space, true);
+    for (size_t i = threadIdx.x; i < Line::ints(a.B); i += blockDim.x) a.line[i] = space[i];
+}
+
+// Kernels of a call come up while the one before still runs its last CTAs.  after_previous() waits for all that came
+// before; what a kernel does ahead of it must not depend on that.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename K, typename... A>
+cudaError_t launch_early(K *kern, size_t grid, int block, size_t smem, cudaStream_t s, const A &...args)
+{
+    cudaError_t e = smem > 16 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) : cudaSuccess;
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 __device__ __forceinline__ float dot4(const float4 &a, const float4 &b)
@@ -140,7 +242,8 @@ __device__ __forceinline__ void sum_groups(float (&p)[N], int lane)
 cudaError_t launch_plan(const TreeArgs &a, cudaStream_t s);
 cudaError_t launch_tree_gates(const TreeArgs &a, cudaStream_t s);
 cudaError_t launch_tree_read(const TreeArgs &a, cudaStream_t s);
-bool tree_tc_supported(const TreeArgs &a);
+bool tree_tc_supported(const TreeArgs &a);  // the split read on the tensor cores
+cudaError_t launch_tree_path_tc(const TreeArgs &a, cudaStream_t s);
 cudaError_t launch_tree_read_tc(const TreeArgs &a, cudaStream_t s);
 cudaError_t take_tree_abort(int *was_set);
 cudaError_t launch_tree_finish(const TreeArgs &a, cudaStream_t s);  // a step's end too
