@@ -502,6 +502,9 @@ cudaError_t path_impl(const TreeArgs &a, cudaStream_t s)
 {
     const int spans = (a.T + kSpan - 1) / kSpan;
     const long long items = (long long)a.B * a.c.H * spans;
+    // the SM's shared memory is divided for the CTA of reads that comes beside this one
+    cudaError_t e = cudaFuncSetAttribute(tree_path_tc<D>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
     return launch_early(tree_path_tc<D>, (size_t)(items < a.ranges ? items : a.ranges) + 1, kPathThreads, sizeof(int) * Line::ints(a.B), s, a, spans);
 }
 

@@ -52,22 +52,44 @@ __device__ void make_nodes(const TreeArgs &a, Nodes &s, int b, int bh, int m, in
         }
         __syncthreads();
     }
-    if (tid < m) {
-        const int j = (in0 + __popcll(set) - 1) / a.c.C;
+    if (tid < kMaxTree) {  // (two whole warps, each with its half of the sets)
+        const int j = tid < m ? (in0 + __popcll(set) - 1) / a.c.C : -1;
         s.seg[tid] = j;
-        atomicOr(reinterpret_cast<unsigned long long *>(&s.seg_set[j]), 1ull << tid);
+        const unsigned same = __match_any_sync(0xffffffffu, j);
+        if (j >= 0 && (same & ((1u << (tid % 32)) - 1)) == 0) reinterpret_cast<unsigned *>(&s.seg_set[j])[tid / 32] = same;
     }
-    __syncthreads();
-    if (a.delta && tid < m) {
-        float2 sum = make_float2(0.f, 0.f);
-        for (uint64_t w = set & s.seg_set[s.seg[tid]]; w; w &= w - 1) {
-            const float2 x = delta_parts(s.la[__ffsll(w) - 1]);
-            sum.x += x.x;
-            sum.y += x.y;
-        }
+    if (!a.delta) {
+        __syncthreads();
+        return;
+    }
+    // sums along the path, by doubling again: up to the segment's first node
+    float2 sum = make_float2(0.f, 0.f);
+    if (tid < m) {
+        sum = delta_parts(s.la[tid]);
+        f = a.parent ? a.parent[(size_t)b * a.T + tid] : -1;
+        if (f < -1 || f >= tid) f = -1;
         s.cum[tid] = sum;
     }
     __syncthreads();
+    if (tid < m) {
+        if (f >= 0 && s.seg[f] != s.seg[tid]) f = -1;
+        s.up[tid] = f;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int x = 1; x < m; x *= 2) {
+        if (tid < m && f >= 0) {
+            sum.x += s.cum[f].x;
+            sum.y += s.cum[f].y;
+            f = s.up[f];
+        }
+        __syncthreads();
+        if (tid < m) {
+            s.cum[tid] = sum;
+            s.up[tid] = f;
+        }
+        __syncthreads();
+    }
 }
 
 __device__ __forceinline__ float decay(const Nodes &s, int to, int from)
