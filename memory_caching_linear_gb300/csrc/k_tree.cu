@@ -295,10 +295,10 @@ struct Parts {
 //   Z = sum_p z_p exp(L_p - top) + sum_j exp(s_j - top), a part counts exp(L_p - top) / Z and path segment j, whose P and (j = 0)
 //   read of the begun memory wait for it, exp(s_j - top) / Z (Residual: 1 and 1; Mean: all scores 0).
 // Latency bounds it: loads that do not hang on one another are all under way before the first is used.
-constexpr int kPartsAtOnce = 4;
+constexpr int kPartsAtOnce = 2;
 
 template <typename E, int D, bool SPLIT>
-__global__ void __launch_bounds__(256) tree_finish(TreeArgs a)
+__global__ void __launch_bounds__(256, 4) tree_finish(TreeArgs a, int segments)
 {
     constexpr int RB = D < 32 ? D : 32;
     const Paged &c = a.c;
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(256) tree_finish(TreeArgs a)
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, row = rb * RB + lane % RB, n0 = 8 * warp;
     extern __shared__ __align__(16) float dyn[];
     float *Ps = dyn, *As = Ps + a.T * a.Tp;          // [m][Tp]
-    float *ws = As + (a.delta ? a.T * a.Tp : 0);     // SPLIT: [segment][Tp] path weights
+    float *ws = As + (a.delta ? a.T * a.Tp : 0);     // SPLIT: [segment][Tp] path weights; a path has path_segments() of them
     __shared__ float es[kMaxTree][32];
     __shared__ uint64_t anc[kMaxTree];
     __shared__ int seg[kMaxTree];
@@ -334,6 +334,16 @@ __global__ void __launch_bounds__(256) tree_finish(TreeArgs a)
     if (where < 0 || m == 0) return;
     const int nb = cached_segments(c, pos), in0 = pos % c.C;
     const Parts parts(a, line, b, h, SPLIT ? nb : nb + (in0 ? 1 : 0));
+    float p[kPartsAtOnce][8];  // partial reads: the next ones, under way
+    auto fetch = [&](int j0) {
+#pragma unroll
+        for (int j = 0; j < kPartsAtOnce; ++j) {
+            const float *src = a.part + (((size_t)j0 + j + bh) * a.Tp + n0) * D + row;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) p[j][x] = j0 + j <= parts.j1 && n0 + x < m ? src[(size_t)x * D] : 0.f;
+        }
+    };
+    fetch(parts.j0);
     for (int n = tid; n < kMaxTree; n += blockDim.x) {
         const bool in = n < m;
         anc[n] = in ? a.anc[(size_t)b * kMaxTree + n] : 0;
@@ -342,7 +352,7 @@ __global__ void __launch_bounds__(256) tree_finish(TreeArgs a)
         if (!SPLIT) {
             into[n] = in ? a.gates[((size_t)bh * (c.nmax + 2) + nb + 1) * a.Tp + n] : 0.f;
         } else if (in) {
-            const float *score = a.score + at * a.Tp + n;
+            const float *score = a.score + (size_t)bh * segments * a.Tp + n;
             const float2 *weight = a.weight + (size_t)bh * a.Tp + n;
             const float d = in0 ? a.into[(size_t)bh * a.Tp + n] : 0.f;
             const float s0 = score[0];
@@ -390,19 +400,13 @@ __global__ void __launch_bounds__(256) tree_finish(TreeArgs a)
                 share[j][n] = expf(a.weight[((size_t)j0 + j + bh) * a.Tp + n].x - tops[n]) * invs[n];
             }
         }
-        float p[kPartsAtOnce][8];
-#pragma unroll
-        for (int j = 0; j < kPartsAtOnce; ++j) {
-            const float *src = a.part + (((size_t)j0 + j + bh) * a.Tp + n0) * D + row;
-#pragma unroll
-            for (int x = 0; x < 8; ++x) p[j][x] = j < cnt && n0 + x < m ? src[(size_t)x * D] : 0.f;
-        }
         if (SPLIT) __syncthreads();
 #pragma unroll
         for (int j = 0; j < kPartsAtOnce; ++j)
 #pragma unroll
             for (int x = 0; x < 8; ++x)
                 if (j < cnt && n0 + x < m) y[x] = SPLIT ? fmaf(share[j][n0 + x], p[j][x], y[x]) : y[x] + p[j][x];
+        if (j0 + kPartsAtOnce <= parts.j1) fetch(j0 + kPartsAtOnce);
     }
     // what the eight nodes of warp k wrote, for this warp's: P and A of one that is no ancestor are 0, but what it wrote may not
     // be finite, and then it is not multiplied
@@ -561,12 +565,12 @@ cudaError_t finish_impl(const TreeArgs &a, cudaStream_t s)
     const size_t grid = (size_t)a.B * a.c.H * (D / RB);
     if (a.step) return launch_early(step_finish<E, D>, grid, 256, 0, s, a);
     const bool split = tree_tc_supported(a);
-    const size_t smem = sizeof(float) * ((a.delta ? 2 : 1) + (split ? 1 : 0)) * (size_t)a.T * a.Tp;
+    const size_t smem = sizeof(float) * ((size_t)(a.delta ? 2 : 1) * a.T + (split ? path_segments(a) : 0)) * a.Tp;
     const int block = 32 * a.groups;  // a warp to eight nodes
     if constexpr (sizeof(E) == 2 && D >= 64) {
-        if (split) return launch_early(tree_finish<E, D, true>, grid, block, smem, s, a);
+        if (split) return launch_early(tree_finish<E, D, true>, grid, block, smem, s, a, path_segments(a));
     }
-    return launch_early(tree_finish<E, D, false>, grid, block, smem, s, a);
+    return launch_early(tree_finish<E, D, false>, grid, block, smem, s, a, path_segments(a));
 }
 
 template <typename E>
@@ -587,14 +591,8 @@ cudaError_t run(const TreeArgs &a, cudaStream_t s, int what)
 
 }  // namespace
 
-cudaError_t launch_tree_gates(const TreeArgs &a, cudaStream_t s)
-{
-    return tree_tc_supported(a) ? launch_tree_path_tc(a, s) : run(a, s, 0);
-}
-cudaError_t launch_tree_read(const TreeArgs &a, cudaStream_t s)
-{
-    return tree_tc_supported(a) ? launch_tree_read_tc(a, s) : run(a, s, 1);
-}
+cudaError_t launch_tree_gates(const TreeArgs &a, cudaStream_t s) { return run(a, s, 0); }
+cudaError_t launch_tree_read(const TreeArgs &a, cudaStream_t s) { return run(a, s, 1); }
 cudaError_t launch_tree_finish(const TreeArgs &a, cudaStream_t s) { return run(a, s, 2); }
 
 }  // namespace mc

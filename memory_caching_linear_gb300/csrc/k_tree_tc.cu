@@ -5,7 +5,7 @@
 // the A operand as it comes by TMA (kind::tf32 takes 11 significant bits of it: 2^-11 of every product against the 2^-9 of
 // y's own rounding), the weighted queries are B, rounded to tf32, and the sum over a head's memories stays in tensor memory.
 // A memory of 64 KB is read from HBM once for all nodes, 1.5 us of an SM's share of the bandwidth, against 0.3 us of products
-// at 64 nodes: HBM is the bound, so the memories stream through a ring of 32-column panels (128 KB in flight on an SM) and
+// at 64 nodes: HBM is the bound, so the memories stream through a ring of 32-column panels (144 KB in flight on an SM) and
 // everything else is made to keep up.
 //
 // The memories of all heads and sequences form one line, cut into one range per CTA whatever the sequences' lengths.  A range
@@ -14,8 +14,8 @@
 // be known of the other ranges before the memories can be read; and the begun segment's memory, whose weight hangs on the
 // path, is read without one.
 //
-// The path's own products (tree_path_tc) are a small kernel that runs beside the reads: they do not wait for it, but
-// end after it.
+// The path's own products (tree_path_tc) are a small kernel that comes up beside the reads once these have their first scores.
+// It needs nothing of them, but ends after them, so that what follows has both.
 #include <cfloat>
 #include <cstdint>
 
@@ -68,14 +68,14 @@ __device__ __forceinline__ void rows_of(const __nv_bfloat16 *lo, const __nv_bflo
 // ------------------------------------------------------------------------------------------------ the path
 
 constexpr int kSpan = 32, kPathThreads = 256, kCol = kSpan + 1;
-// The two kernels run side by side: bounds above their blocks keep path and read to 96 and 128 registers a thread (24 K and
-// 40 K of an SM's 64 K).
-constexpr int kPathRegs = 640, kReadRegs = 512;
+// Registers a thread, so that a CTA of each runs on an SM: a quarter of it, with 512 registers a lane, has up to three of the
+// reads' ten warps and two of the path's eight.
+constexpr int kPathRegs = 88, kReadRegs = 112;
 
 // Scores of the path's segments, P without the gates, and A, for 32 nodes of a head at a time.  One CTA on an SM goes over its
 // share of the heads: little enough in registers and shared memory to run beside a CTA of tree_read_tc.
 template <int D>
-__global__ void __launch_bounds__(kPathRegs) tree_path_tc(TreeArgs a, int spans)
+__global__ void __maxnreg__(kPathRegs) tree_path_tc(TreeArgs a, int spans, int segments)
 {
     constexpr int KS = D / 16;
     __shared__ Nodes nodes;
@@ -84,10 +84,10 @@ __global__ void __launch_bounds__(kPathRegs) tree_path_tc(TreeArgs a, int spans)
     const Paged &c = a.c;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, c4 = lane % 4;
     const bool routed = a.mode == MC_GRM;
-    after_previous();
     let_next_start();
     if (blockIdx.x == gridDim.x - 1) {  // one CTA more, for tree_finish
         leave_line(a, space);
+        after_previous();
         return;
     }
     const Line line = make_line(a, space, false);
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kPathRegs) tree_path_tc(TreeArgs a, int spans)
         for (int t = warp; t < kSpan && n0 + t < m; t += 8) {
             const int n = n0 + t, last = nodes.seg[n];
             const uint64_t mine = nodes.anc[n];
-            float *score = a.score + (size_t)bh * a.T * a.Tp + n;
+            float *score = a.score + (size_t)bh * segments * a.Tp + n;
             if (routed) {
                 for (int j = 0; j <= last; ++j) {
                     const uint64_t w = mine & nodes.seg_set[j];
@@ -172,16 +172,17 @@ __global__ void __launch_bounds__(kPathRegs) tree_path_tc(TreeArgs a, int spans)
             }
         }
     }
+    after_previous();
 }
 
 // ------------------------------------------------------------------------------------------------ the reads
 
 constexpr int kWorkers = 8, kThreads = 32 * (kWorkers + 2);
-constexpr int kRingBytes = 131072;            // eight panels of 128 rows, sixteen of 64
-constexpr int kMaxPanels = 16;
+constexpr int kRingBytes = 147456;            // nine panels of 128 rows, eighteen of 64
+constexpr int kMaxPanels = 18;
 constexpr int kBSlot = kMaxTree * 128 * 4;    // weighted queries of one memory
-constexpr int kULine = 288;                   // bytes between a run's router inputs: rows eight banks apart
-constexpr int kReadSmem = 1024 + kRingBytes + 2 * kBSlot + kMaxTree * kULine;
+constexpr int kULine = 288;                   // bytes between a run's router inputs, where B's first goes later: rows eight banks apart
+constexpr int kReadSmem = 1024 + kRingBytes + 2 * kBSlot;
 
 enum { kCached, kBegunQ, kBegunK };
 // Memories of one head that follow each other in a CTA's range: cached ones, or the begun one for the queries or the keys.
@@ -222,20 +223,21 @@ struct Runs {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kReadRegs)
+__global__ void __maxnreg__(kReadRegs)
 tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ CUtensorMap online, TreeArgs a)
 {
     constexpr int PANELS = D / 32, kPanelBytes = D * 128, RING = kRingBytes / kPanelBytes, KS = D / 16;
     extern __shared__ uint8_t raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint8_t *bs = ring + kRingBytes;  // (a 64-row panel's second half, which nobody reads, may be of the next one or of B)
-    uint8_t *us = bs + 2 * kBSlot;
+    uint8_t *us = bs;  // (D of the run before is complete by then: nothing reads B)
     int *space = reinterpret_cast<int *>(raw + kReadSmem);
     __shared__ uint64_t full[kMaxPanels], empty[kMaxPanels], b_full[2], b_empty[2], d_full[2], d_empty[2], staged, scored, drain;
     __shared__ float top[kWorkers][kMaxTree];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
     const Paged &c = a.c;
+    after_previous();
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int NT = (a.T + 15) / 16 * 16;                           // columns of D
     const int groups = (NT + 31) / 32, writers = PANELS * groups;  // warps that make B: 32 tokens of one panel each
@@ -363,6 +365,12 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
                     float4 v[KS];
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks) v[ks] = page >= 0 ? load4(src + 16 * ks + 4 * c4) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    uint32_t kb_hi[KS][2], kb_lo[KS][2];
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+                        mma::split2(v[ks].x, v[ks].y, kb_hi[ks][0], kb_lo[ks][0]);
+                        mma::split2(v[ks].z, v[ks].w, kb_hi[ks][1], kb_lo[ks][1]);
+                    }
                     const bool there0 = __shfl_sync(0xffffffffu, page, 8 * c4) >= 0, there1 = __shfl_sync(0xffffffffu, page, 8 * c4 + 4) >= 0;
                     const int ahead = i0 + 8 * kWorkers + g;
                     page = ahead < r.i1 ? table[ahead] : -1;
@@ -381,13 +389,10 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
                         float s[4] = {};
 #pragma unroll
                         for (int ks = 0; ks < KS; ++ks) {
-                            uint32_t h0, h1, l0, l1;
                             const uint2 x = *reinterpret_cast<const uint2 *>(ulo + 32 * ks), y = *reinterpret_cast<const uint2 *>(uhi + 32 * ks);
                             const uint32_t f[4] = {x.x, y.x, x.y, y.y};
-                            mma::split2(v[ks].x, v[ks].y, h0, l0);
-                            mma::split2(v[ks].z, v[ks].w, h1, l1);
-                            mma::mma16816(s, f, h0, h1);
-                            mma::mma16816(s, f, l0, l1);
+                            mma::mma16816(s, f, kb_hi[ks][0], kb_hi[ks][1]);
+                            mma::mma16816(s, f, kb_lo[ks][0], kb_lo[ks][1]);
                         }
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {  // segment i0 + 2 c4 (+ 1), token lo or hi
@@ -414,6 +419,21 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
                     for (int x = 0; x < kWorkers; ++x) best = fmaxf(best, top[x][t]);
                 }
                 ++scorings;
+                // the next head's mean keys and router inputs, as far as L2
+                Runs then = runs;
+                Run x;
+                while (then.next(a, line, x))
+                    if (x.kind == kCached) {
+                        const int32_t *pages_of = c.table + (size_t)x.row * c.nmax;
+                        const char *inputs = reinterpret_cast<const char *>(static_cast<const __nv_bfloat16 *>(a.u) + (size_t)x.bh * a.T * D);
+                        for (int y = tid; y < x.m * D / 64; y += 32 * kWorkers)
+                            asm volatile("prefetch.global.L2 [%0];" ::"l"(inputs + 128 * y));
+                        for (int y = tid; y < (x.i1 - x.i0) * (D / 32); y += 32 * kWorkers) {
+                            const int p = valid_page(c, pages_of[x.i0 + y / (D / 32)]);
+                            if (p >= 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(c.kbar + ((size_t)p * c.H + x.h) * D + y % (D / 32) * 32));
+                        }
+                        break;
+                    }
             }
             uint32_t q[16];
             if (in) {
@@ -428,6 +448,7 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
                     q[4 * x + 3] = w.w;
                 }
             }
+            if (n == 0) let_next_start();
             float z = 0.f;
             if (writes) {
                 const int32_t *table = c.table + (size_t)r.row * c.nmax;
@@ -493,8 +514,6 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
         tmem_dealloc(tb, 128);
     }
     if (tid == 0 && abort_flag) atomicExch(&g_tree_abort, 1);
-    let_next_start();
-    after_previous();  // what comes after this kernel needs the path's products too
 }
 
 template <int D>
@@ -505,7 +524,8 @@ cudaError_t path_impl(const TreeArgs &a, cudaStream_t s)
     // the SM's shared memory is divided for the CTA of reads that comes beside this one
     cudaError_t e = cudaFuncSetAttribute(tree_path_tc<D>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
-    return launch_early(tree_path_tc<D>, (size_t)(items < a.ranges ? items : a.ranges) + 1, kPathThreads, sizeof(int) * Line::ints(a.B), s, a, spans);
+    return launch_early(tree_path_tc<D>, (size_t)(items < a.ranges ? items : a.ranges) + 1, kPathThreads, sizeof(int) * Line::ints(a.B), s, a, spans,
+                        path_segments(a));
 }
 
 // A [matrices][D][D] fp32 tensor in boxes of 32 columns of one matrix, 128-byte swizzled.

@@ -117,7 +117,7 @@ int run_batch(const mc_paged_cache *cache, TreeArgs a, int agg_mode, cudaStream_
             a.Z = cv.take<float>(a.delta && !a.step ? BH * a.Tp * c.d : 0);
             if (split) {
                 a.Y0 = cv.take<float>(BH * a.Tp * c.d);
-                a.score = cv.take<float>(BH * T * a.Tp);
+                a.score = cv.take<float>(BH * path_segments(a) * a.Tp);
                 a.into = cv.take<float>(BH * a.Tp);
                 a.seg = cv.take<int32_t>(B * kMaxTree);
                 a.weight = cv.take<float2>((a.ranges + BH) * a.Tp);
@@ -140,10 +140,10 @@ int run_batch(const mc_paged_cache *cache, TreeArgs a, int agg_mode, cudaStream_
         e = launch_accept(a, s);
         profile_after_kernel(s, "accept_rows");
     } else if (e == cudaSuccess) {
-        e = launch_tree_gates(a, s);
-        profile_after_kernel(s, split ? "tree_path_tc" : "tree_gates");
-        if (e == cudaSuccess) e = launch_tree_read(a, s);
-        profile_after_kernel(s, split ? "tree_read_tc" : "tree_read");
+        e = split ? launch_tree_read_tc(a, s) : launch_tree_gates(a, s);
+        profile_after_kernel(s, split ? "tree_read_tc" : "tree_gates");
+        if (e == cudaSuccess) e = split ? launch_tree_path_tc(a, s) : launch_tree_read(a, s);
+        profile_after_kernel(s, split ? "tree_path_tc" : "tree_read");
         if (e == cudaSuccess) e = launch_tree_finish(a, s);
         profile_after_kernel(s, a.step ? "step_finish" : "tree_finish");
     }

@@ -54,7 +54,7 @@ struct TreeArgs {
                                           // read's scores
     float *P, *A;                         // [BH][T][Tp] per ancestor: what nodes read of what it wrote (a split read's without
                                           // the gates); what it meets in their keys
-    float *score;                         // [BH][T][Tp] split: nodes' scores of their paths' segments
+    float *score;                         // [BH][path_segments()][Tp] split: nodes' scores of their paths' segments
     float *into;                          // [BH][Tp] split: decay from the cache to a node's deepest ancestor in the begun segment
     uint64_t *anc;                        // [B][64] a node's ancestors and itself
     int32_t *seg;                         // [B][64] its segment, counted from the one begun
@@ -157,6 +157,9 @@ __device__ inline void leave_line(const TreeArgs &a, int *space)
     make_line(a, space, true);
     for (size_t i = threadIdx.x; i < Line::ints(a.B); i += blockDim.x) a.line[i] = space[i];
 }
+
+// Segments that a path of T nodes can touch.
+inline int path_segments(const TreeArgs &a) { return (int)(((long long)a.c.C - 1 + a.T - 1) / a.c.C) + 1; }
 
 // Kernels of a call come up while the one before still runs its last CTAs.  after_previous() waits for all that came
 // before; what a kernel does ahead of it must not depend on that.
