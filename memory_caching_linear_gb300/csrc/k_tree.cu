@@ -287,27 +287,30 @@ struct Parts {
     }
 };
 
-// Solves for e and adds everything up: up to 32 rows of a head, a lane to a row and a warp to eight nodes, whose e and y it
-// keeps in registers.  A row needs its own e alone, so lanes share nothing but P and A.  The warps' nodes come in turns:
-// the warp at hand works out its eight e (a triangle) and leaves them in shared memory, the later ones take them up: eight
-// products with A and with P for every e.  The linear memory's e are the values: no turns.
+// Solves for e and adds everything up: 64 rows of a head (32 for d = 32, 16 for 16), two to a lane, and eight nodes to a warp,
+// whose e and y it keeps in registers.  A row needs its own e alone, so lanes share nothing but P and A.  The e come in turns of
+// eight: the warp at hand works its own out (a triangle) and leaves them in shared memory, the later ones take them up.
+// The linear memory's e are the values: no turns.  What is read of them, P e, follows for all warps at once.
 //   SPLIT: a split read.  With s the scores, a part's largest L_p and sum z_p, top = max(L_p, path scores) and
 //   Z = sum_p z_p exp(L_p - top) + sum_j exp(s_j - top), a part counts exp(L_p - top) / Z and path segment j, whose P and (j = 0)
 //   read of the begun memory wait for it, exp(s_j - top) / Z (Residual: 1 and 1; Mean: all scores 0).
-// Latency bounds it: loads that do not hang on one another are all under way before the first is used.
-constexpr int kPartsAtOnce = 2;
+// Instructions and latency bound it: what a warp loads of P and A serves both rows, an e that is nobody's ancestor costs a
+// branch, and loads that do not hang on one another are all under way before the first is used.
+constexpr int kPartsAtOnce = 1;
+
+template <int D> struct FinishRows { static constexpr int BLOCK = D < 64 ? D : 64, LANE = D < 64 ? 1 : 2; };
 
 template <typename E, int D, bool SPLIT>
-__global__ void __launch_bounds__(256, 4) tree_finish(TreeArgs a, int segments)
+__global__ void __launch_bounds__(256, 3) tree_finish(TreeArgs a, int segments)
 {
-    constexpr int RB = D < 32 ? D : 32;
+    constexpr int RB = FinishRows<D>::BLOCK, R = FinishRows<D>::LANE;
     const Paged &c = a.c;
     const int bh = (int)blockIdx.x / (D / RB), rb = (int)blockIdx.x % (D / RB), b = bh / c.H, h = bh % c.H;
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, row = rb * RB + lane % RB, n0 = 8 * warp;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, row = rb * RB + lane % RB, n0 = 8 * warp;  // (and row + 32)
     extern __shared__ __align__(16) float dyn[];
     float *Ps = dyn, *As = Ps + a.T * a.Tp;          // [m][Tp]
     float *ws = As + (a.delta ? a.T * a.Tp : 0);     // SPLIT: [segment][Tp] path weights; a path has path_segments() of them
-    __shared__ float es[kMaxTree][32];
+    __shared__ float es[kMaxTree][32 * R];
     __shared__ uint64_t anc[kMaxTree];
     __shared__ int seg[kMaxTree];
     __shared__ float share[kPartsAtOnce][kMaxTree], into[kMaxTree], first[kMaxTree], tops[kMaxTree], invs[kMaxTree];
@@ -316,15 +319,17 @@ __global__ void __launch_bounds__(256, 4) tree_finish(TreeArgs a, int segments)
     const Line line = line_in(a.line, a.B);
     const int where = line.row[b], pos = line.pos[b], m = line.nodes[b];
     // rows of V, Z and the begun memory's read: not all of them count, but all are there
-    float e[8], z[8], y[8];
+    float e[8][R], z[8][R], y[8][R];
 #pragma unroll
-    for (int x = 0; x < 8; ++x) {
-        const bool in = n0 + x < a.T;
-        const size_t there = ((size_t)bh * a.Tp + n0 + x) * D + row;
-        e[x] = in ? to_f(static_cast<const E *>(a.v)[(at + n0 + x) * D + row]) : 0.f;
-        z[x] = in && a.delta ? a.Z[there] : 0.f;
-        y[x] = in && SPLIT ? a.Y0[there] : 0.f;
-    }
+    for (int x = 0; x < 8; ++x)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const bool in = n0 + x < a.T;
+            const size_t there = ((size_t)bh * a.Tp + n0 + x) * D + row + 32 * r;
+            e[x][r] = in ? to_f(static_cast<const E *>(a.v)[(at + n0 + x) * D + row + 32 * r]) : 0.f;
+            z[x][r] = in && a.delta ? a.Z[there] : 0.f;
+            y[x][r] = in && SPLIT ? a.Y0[there] : 0.f;
+        }
     for (int i = tid; i < a.T * a.Tp / 4; i += blockDim.x) {
         const float4 p = reinterpret_cast<const float4 *>(a.P + at * a.Tp)[i];
         const float4 q = a.delta ? reinterpret_cast<const float4 *>(a.A + at * a.Tp)[i] : p;
@@ -334,61 +339,74 @@ __global__ void __launch_bounds__(256, 4) tree_finish(TreeArgs a, int segments)
     if (where < 0 || m == 0) return;
     const int nb = cached_segments(c, pos), in0 = pos % c.C;
     const Parts parts(a, line, b, h, SPLIT ? nb : nb + (in0 ? 1 : 0));
-    float p[kPartsAtOnce][8];  // partial reads: the next ones, under way
+    float p[kPartsAtOnce][8][R];  // partial reads: the next ones, under way
     auto fetch = [&](int j0) {
 #pragma unroll
         for (int j = 0; j < kPartsAtOnce; ++j) {
             const float *src = a.part + (((size_t)j0 + j + bh) * a.Tp + n0) * D + row;
 #pragma unroll
-            for (int x = 0; x < 8; ++x) p[j][x] = j0 + j <= parts.j1 && n0 + x < m ? src[(size_t)x * D] : 0.f;
+            for (int x = 0; x < 8; ++x)
+#pragma unroll
+                for (int r = 0; r < R; ++r) p[j][x][r] = j0 + j <= parts.j1 && n0 + x < m ? src[(size_t)x * D + 32 * r] : 0.f;
         }
     };
     fetch(parts.j0);
     for (int n = tid; n < kMaxTree; n += blockDim.x) {
         const bool in = n < m;
-        anc[n] = in ? a.anc[(size_t)b * kMaxTree + n] : 0;
-        const int last = in && SPLIT ? a.seg[(size_t)b * kMaxTree + n] : 0;
-        seg[n] = last;
+        const uint64_t set = in ? a.anc[(size_t)b * kMaxTree + n] : 0;
         if (!SPLIT) {
+            anc[n] = set;
             into[n] = in ? a.gates[((size_t)bh * (c.nmax + 2) + nb + 1) * a.Tp + n] : 0.f;
         } else if (in) {
+            // two path segments and four parts are the rule: their loads do not wait for one another
             const float *score = a.score + (size_t)bh * segments * a.Tp + n;
             const float2 *weight = a.weight + (size_t)bh * a.Tp + n;
-            const float d = in0 ? a.into[(size_t)bh * a.Tp + n] : 0.f;
-            const float s0 = score[0];
-            float top = -FLT_MAX, sum = 0.f;
-#pragma unroll 4
-            for (int j = parts.j0; j <= parts.j1; ++j) top = fmaxf(top, weight[(size_t)j * a.Tp].x);
-            for (int j = 0; j <= last; ++j) top = fmaxf(top, j ? score[(size_t)j * a.Tp] : s0);
-#pragma unroll 4
-            for (int j = parts.j0; j <= parts.j1; ++j) {
-                const float2 w = weight[(size_t)j * a.Tp];
-                sum += w.y * expf(w.x - top);
-            }
-            for (int j = 0; j <= last; ++j) sum += ws[j * a.Tp + n] = expf((j ? score[(size_t)j * a.Tp] : s0) - top);
+            const int last = a.seg[(size_t)b * kMaxTree + n];
+            float d = a.into[(size_t)bh * a.Tp + n];
+            const float s0 = score[0], s1 = score[segments > 1 ? a.Tp : 0];
+            float2 w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = parts.j0 + j <= parts.j1 ? weight[(size_t)(parts.j0 + j) * a.Tp] : make_float2(-FLT_MAX, 0.f);
+            auto path = [&](int j) { return j == 0 ? s0 : j == 1 ? s1 : score[(size_t)j * a.Tp]; };
+            if (!in0) d = 0.f;
+            float top = fmaxf(fmaxf(w[0].x, w[1].x), fmaxf(w[2].x, w[3].x));
+            for (int j = parts.j0 + 4; j <= parts.j1; ++j) top = fmaxf(top, weight[(size_t)j * a.Tp].x);
+            for (int j = 0; j <= last; ++j) top = fmaxf(top, path(j));
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum += w[j].y * expf(w[j].x - top);
+            for (int j = parts.j0 + 4; j <= parts.j1; ++j) sum += weight[(size_t)j * a.Tp].y * expf(weight[(size_t)j * a.Tp].x - top);
+            for (int j = 0; j <= last; ++j) sum += ws[j * a.Tp + n] = expf(path(j) - top);
             const float inv = a.mode == MC_RESIDUAL ? 1.f : 1.f / sum;
             for (int j = 0; j <= last; ++j) ws[j * a.Tp + n] *= inv;
+            anc[n] = set;
+            seg[n] = last;
             tops[n] = top;
             invs[n] = inv;
             first[n] = ws[n] * d;           // of the begun memory's read
             into[n] = last == 0 ? d : 0.f;  // of what it answers to the key
+        } else {
+            anc[n] = 0;
         }
     }
     __syncthreads();
     if (SPLIT) {
-        for (int i = tid; i < m * a.Tp; i += blockDim.x) {
-            const int j = i / a.Tp, n = i % a.Tp;
-            if ((anc[n] >> j) & 1) Ps[i] *= ws[seg[j] * a.Tp + n];
-        }
+        for (int j = warp; j < m; j += (int)blockDim.x / 32)
+            for (int n = lane; n < a.Tp; n += 32)
+                if ((anc[n] >> j) & 1) Ps[j * a.Tp + n] *= ws[seg[j] * a.Tp + n];
     }
-    const bool mine = n0 < m;
+    uint64_t above = 0;  // ancestors of any of the warp's nodes
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
         const int n = n0 + x;
-        if (n >= m) e[x] = y[x] = 0.f;
-        else {
-            if (a.delta && into[n] != 0.f) e[x] -= SPLIT ? into[n] * z[x] : z[x];
-            y[x] = SPLIT && in0 ? first[n] * y[x] : 0.f;
+        if (n < m) above |= anc[n];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (n >= m) e[x][r] = y[x][r] = 0.f;
+            else {
+                if (a.delta && into[n] != 0.f) e[x][r] -= SPLIT ? into[n] * z[x][r] : z[x][r];
+                y[x][r] = SPLIT && in0 ? first[n] * y[x][r] : 0.f;
+            }
         }
     }
     for (int j0 = parts.j0; j0 <= parts.j1; j0 += kPartsAtOnce) {
@@ -399,81 +417,89 @@ __global__ void __launch_bounds__(256, 4) tree_finish(TreeArgs a, int segments)
                 const int j = i / m, n = i % m;
                 share[j][n] = expf(a.weight[((size_t)j0 + j + bh) * a.Tp + n].x - tops[n]) * invs[n];
             }
+            __syncthreads();
         }
-        if (SPLIT) __syncthreads();
 #pragma unroll
         for (int j = 0; j < kPartsAtOnce; ++j)
 #pragma unroll
             for (int x = 0; x < 8; ++x)
-                if (j < cnt && n0 + x < m) y[x] = SPLIT ? fmaf(share[j][n0 + x], p[j][x], y[x]) : y[x] + p[j][x];
+                if (j < cnt && n0 + x < m) {
+                    const float w = SPLIT ? share[j][n0 + x] : 1.f;
+#pragma unroll
+                    for (int r = 0; r < R; ++r) y[x][r] = fmaf(w, p[j][x][r], y[x][r]);
+                }
         if (j0 + kPartsAtOnce <= parts.j1) fetch(j0 + kPartsAtOnce);
     }
-    // what the eight nodes of warp k wrote, for this warp's: P and A of one that is no ancestor are 0, but what it wrote may not
-    // be finite, and then it is not multiplied
-    auto take = [&](int k, int j, float ej, bool solve) {
-        const float *pr = Ps + (8 * k + j) * a.Tp + n0, *ar = As + (8 * k + j) * a.Tp + n0;
-        const float4 p0 = load4(pr), p1 = load4(pr + 4);
-        const float p[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
-        float q[8];
-        if (solve) {
-            const float4 q0 = load4(ar), q1 = load4(ar + 4);
-            q[0] = q0.x; q[1] = q0.y; q[2] = q0.z; q[3] = q0.w; q[4] = q1.x; q[5] = q1.y; q[6] = q1.z; q[7] = q1.w;
-        }
-        if (isfinite(ej)) {
+    // to[x] += sign W_{j,x} ej for this warp's nodes x: W of one that j is no ancestor of is 0, but ej may not be finite, and
+    // then it is not multiplied
+    auto take = [&](const float *W, float sign, int j, const float (&ej)[R], float (&to)[8][R]) {
+        const float4 w0 = load4(W + j * a.Tp + n0), w1 = load4(W + j * a.Tp + n0 + 4);
+        const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+        bool finite = true;
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                y[x] = fmaf(p[x], ej, y[x]);
-                if (solve) e[x] = fmaf(-q[x], ej, e[x]);
-            }
+        for (int r = 0; r < R; ++r) finite &= isfinite(ej[r]);
+        if (finite) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+#pragma unroll
+                for (int r = 0; r < R; ++r) to[x][r] = fmaf(sign * w[x], ej[r], to[x][r]);
         } else {
 #pragma unroll
             for (int x = 0; x < 8; ++x)
-                if ((anc[n0 + x] >> (8 * k + j)) & 1) {
-                    y[x] = fmaf(p[x], ej, y[x]);
-                    if (solve && q[x] != 0.f) e[x] = fmaf(-q[x], ej, e[x]);
-                }
+                if (w[x] != 0.f)
+#pragma unroll
+                    for (int r = 0; r < R; ++r) to[x][r] = fmaf(sign * w[x], ej[r], to[x][r]);
         }
     };
-    uint64_t above = 0;
-    if (mine) {
-#pragma unroll
-        for (int x = 0; x < 8; ++x) above |= anc[n0 + x];
-    }
     __syncthreads();
-    if (!a.delta) {
-#pragma unroll
-        for (int x = 0; x < 8; ++x) es[n0 + x][lane] = e[x];
-        __syncthreads();
-        if (mine) {
-            for (int k = 0; k <= warp; ++k) {
-                if (!((above >> (8 * k)) & 255)) continue;
-#pragma unroll 4
-                for (int j = 0; j < 8; ++j)
-                    if (8 * k + j < m) take(k, j, es[8 * k + j][lane], false);
-            }
-        }
-    } else {
+    const bool mine = n0 < m;
+    if (a.delta) {
         for (int k = 0; 8 * k < m; ++k) {
             if (warp == k) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     if (n0 + j < m) {
-                        const float ej = e[j];
-                        es[n0 + j][lane] = ej;
-                        take(k, j, ej, true);
+                        float ej[R];
+#pragma unroll
+                        for (int r = 0; r < R; ++r) es[n0 + j][lane + 32 * r] = ej[r] = e[j][r];
+                        take(As, -1.f, n0 + j, ej, e);
                     }
             }
             __syncthreads();
             if (warp > k && mine && ((above >> (8 * k)) & 255)) {
 #pragma unroll 4
-                for (int j = 0; j < 8; ++j) take(k, j, es[8 * k + j][lane], true);
+                for (int j = 8 * k; j < 8 * k + 8; ++j) {
+                    if (!((above >> j) & 1)) continue;
+                    float ej[R];
+#pragma unroll
+                    for (int r = 0; r < R; ++r) ej[r] = es[j][lane + 32 * r];
+                    take(As, -1.f, j, ej, e);
+                }
             }
+        }
+    } else {
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+#pragma unroll
+            for (int r = 0; r < R; ++r) es[n0 + x][lane + 32 * r] = e[x][r];
+        __syncthreads();
+    }
+    if (mine) {
+#pragma unroll 4
+        for (int j = 0; j < min(n0 + 8, m); ++j) {
+            if (!((above >> j) & 1)) continue;
+            float ej[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) ej[r] = es[j][lane + 32 * r];
+            take(Ps, 1.f, j, ej, y);
         }
     }
     if (lane < RB) {
 #pragma unroll
         for (int x = 0; x < 8; ++x)
-            if (n0 + x < m) static_cast<E *>(a.y)[(at + n0 + x) * D + row] = from_f<E>(y[x]);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (n0 + x < m) static_cast<E *>(a.y)[(at + n0 + x) * D + row + 32 * r] = from_f<E>(y[x][r]);
     }
 }
 
@@ -562,8 +588,9 @@ template <typename E, int D>
 cudaError_t finish_impl(const TreeArgs &a, cudaStream_t s)
 {
     constexpr int RB = D < 32 ? D : 32;
-    const size_t grid = (size_t)a.B * a.c.H * (D / RB);
-    if (a.step) return launch_early(step_finish<E, D>, grid, 256, 0, s, a);
+    const size_t heads = (size_t)a.B * a.c.H;
+    if (a.step) return launch_early(step_finish<E, D>, heads * (D / RB), 256, 0, s, a);
+    const size_t grid = heads * (D / FinishRows<D>::BLOCK);
     const bool split = tree_tc_supported(a);
     const size_t smem = sizeof(float) * ((size_t)(a.delta ? 2 : 1) * a.T + (split ? path_segments(a) : 0)) * a.Tp;
     const int block = 32 * a.groups;  // a warp to eight nodes
