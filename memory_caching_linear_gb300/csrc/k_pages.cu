@@ -45,13 +45,14 @@ __device__ int block_scan(int x, int *total)
     return before + incl - x;
 }
 
-// The lowest `want` free pages of the pool to list, in order, each with one reference; -1 where there are no more.
-__device__ void take_pages(const Paged &c, int want, int32_t *list)
+// The lowest `want` free pages of the pool to list, in order, each with one reference; -1 where there are no more.  head: the
+// references of page threadIdx.x.
+__device__ void take_pages(const Paged &c, int want, int32_t *list, int head)
 {
     int found = 0;
     for (int p0 = 0; p0 < c.P && found < want; p0 += kPlanThreads) {
         const int p = p0 + (int)threadIdx.x;
-        const bool free = p < c.P && __ldcg(c.refs + p) == 0;
+        const bool free = p < c.P && (p0 ? __ldcg(c.refs + p) : head) == 0;
         int here;
         const int at = found + block_scan(free, &here);
         if (free && at < want) {
@@ -73,6 +74,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_rows(TreeArgs a)
     __shared__ int taker[kMaxRows], lens[kMaxRows];
     taker[tid] = 0x7fffffff;
     lens[tid] = 0;
+    after_previous();
+    let_next_start();
+    const int head = tid < c.P ? __ldcg(c.refs + tid) : 1;  // the first references, wanted last
     __syncthreads();
     // which row: the slot's; a slot that several batch rows name is the first one's where it is written
     const bool in = tid < a.B;
@@ -134,99 +138,205 @@ __global__ void __launch_bounds__(kPlanThreads) plan_rows(TreeArgs a)
     if (in) a.p.fresh[tid] = fb;
     if (tid == 0) a.p.fresh[a.B] = want;
     if (want == 0) return;
-    take_pages(c, want, a.p.list);
+    take_pages(c, want, a.p.list, head);
     for (int i = 0; i < more; ++i) c.table[(size_t)row * c.nmax + s0 + i] = __ldcg(a.p.list + fb + i);
 }
 
-// The accepted tokens, one after the other, into the memory of the begun segment; what completes goes to its page.  A row of
-// a memory sees its own value's entry alone, so a CTA takes up to 32 rows of a head, a group of d / 4 lanes each, in
-// registers: the memory is read and written once.  The chain of a token is its key's dot product (five exchanges at d = 128)
-// and the update.
-template <typename E, int D>
-__global__ void __launch_bounds__(256) accept_rows(TreeArgs a)
+// Pairs of fp32 in one instruction.
+__device__ __forceinline__ uint64_t pair_of(float x, float y)
 {
-    constexpr int RB = D < 32 ? D : 32, LPR = D / 4, RPW = 32 / LPR, PASS = RB / (8 * RPW) < 1 ? 1 : RB / (8 * RPW);
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 of_pair(uint64_t p)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// The accepted tokens, one after the other, into the memory of the begun segment; what completes goes to its page.  A row of
+// a memory sees its own value's entry alone, so the memory stays in registers: it is read and written once, and a
+// CTA takes up to 64 rows of a head.  Instructions bound it, 4 d^2 products a token and what goes with them, so a lane holds
+// 16 columns of its rows (d / 16 lanes to a row, three exchanges for a key's dot product at d = 128) as pairs, several rows share
+// what is loaded of a token, and the memory is kept as M = s M': a token costs M' a dot product and an update, and only s,
+// the decays' product, its decay (M' takes s over when it falls below 2^-30).  What a token does to s, and where a segment
+// ends, is worked out once, ahead of the chain.
+// What the plan does not say -- tokens, where the memory lies -- is fetched while it is made.
+template <int D> struct AcceptShape {
+    static constexpr int ROWS = D < 64 ? D : 64, LANES = D / 16, GROUPS = 32 / LANES, R = D == 16 ? 1 : D == 32 ? 2 : 4;
+    static constexpr int PER_WARP = GROUPS * R, WARPS = ROWS < PER_WARP ? 1 : ROWS / PER_WARP;
+    static size_t smem(int T) { return sizeof(float) * T * (D + ROWS + 2); }
+};
+
+template <typename E, int D>
+__global__ void __launch_bounds__(32 * AcceptShape<D>::WARPS) accept_rows(TreeArgs a)
+{
+    using S = AcceptShape<D>;
+    constexpr int R = S::R, THREADS = 32 * S::WARPS;
     const Paged &c = a.c;
-    const int bh = (int)blockIdx.x / (D / RB), rb = (int)blockIdx.x % (D / RB), b = bh / c.H, h = bh % c.H;
-    const int row = a.p.act[b], n = a.p.len[b];
-    if (row < 0 || n == 0) return;
-    __shared__ __align__(16) float ks[kMaxTree][D];
-    __shared__ float vs[kMaxTree][RB], dec[kMaxTree], bet[kMaxTree];
+    const int bh = (int)blockIdx.x / (D / S::ROWS), rb = (int)blockIdx.x % (D / S::ROWS), b = bh / c.H, h = bh % c.H;
+    extern __shared__ __align__(16) float dyn[];
+    float *ks = dyn, *vs = ks + a.T * D, *dec = vs + a.T * S::ROWS, *bet = dec + a.T;  // [node][column], [node][row], [node]
+    __shared__ float4 turn[kMaxTree];  // of the path's tokens: M' is multiplied by (0: emptied), s, beta / s, page to write (as bits)
     __shared__ int node[kMaxTree];
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const uint64_t path = a.p.path[b];
-    if (tid < kMaxTree && (path >> tid) & 1) node[__popcll(path & ((1ull << tid) - 1))] = tid;
-    __syncthreads();
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, l = lane % S::LANES;
+    const int r0 = warp * S::PER_WARP + lane / S::LANES;  // and, a group's rows apart, r0 + GROUPS, ...
+    const bool rows = r0 < S::ROWS;
+    const int slot = a.slots ? a.slots[b] : b;
+    int guess = (unsigned)slot < (unsigned)c.S ? c.row[slot] : -1;  // (its position another CTA may have moved on)
+    if ((unsigned)guess >= (unsigned)c.S) guess = -1;
+    uint64_t m[R][8];
+    float4 *const mem = reinterpret_cast<float4 *>(c.online + (((size_t)max(guess, 0) * c.H + h) * D + rb * S::ROWS + r0) * D) + l;
+    constexpr int APART = S::GROUPS * (D / 4);
+    if (guess >= 0 && rows) {
+#pragma unroll
+        for (int x = 0; x < R; ++x)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 w = mem[x * APART + i * S::LANES];
+                m[x][2 * i] = pair_of(w.x, w.y);
+                m[x][2 * i + 1] = pair_of(w.z, w.w);
+            }
+    }
     const size_t at = (size_t)bh * a.T;
-    for (int i = tid; i < n * (D / 4); i += 256) {
-        const int j = i / (D / 4), x = i % (D / 4) * 4;
-        *reinterpret_cast<float4 *>(&ks[j][x]) = load4(static_cast<const E *>(a.k) + (at + node[j]) * D + x);
-    }
-    for (int i = tid; i < n * RB; i += 256)
-        vs[i / RB][i % RB] = to_f(static_cast<const E *>(a.v)[(at + node[i / RB]) * D + rb * RB + i % RB]);
-    if (a.delta && tid < n) {
-        dec[tid] = delta_decay(to_f(static_cast<const E *>(a.la)[at + node[tid]]));
-        bet[tid] = to_f(static_cast<const E *>(a.be)[at + node[tid]]);
+#pragma unroll 4
+    for (int i = tid; i < a.T * (D / 4); i += THREADS)
+        *reinterpret_cast<float4 *>(ks + 4 * i) = load4(static_cast<const E *>(a.k) + at * D + 4 * i);
+#pragma unroll 4
+    for (int i = tid; i < a.T * (S::ROWS / 4); i += THREADS)
+        *reinterpret_cast<float4 *>(vs + 4 * i) =
+            load4(static_cast<const E *>(a.v) + (at + i / (S::ROWS / 4)) * D + rb * S::ROWS + i % (S::ROWS / 4) * 4);
+    if (a.delta)
+        for (int i = tid; i < a.T; i += THREADS) {
+            dec[i] = delta_decay(to_f(static_cast<const E *>(a.la)[at + i]));
+            bet[i] = to_f(static_cast<const E *>(a.be)[at + i]);
+        }
+    after_previous();
+    const int row = a.p.act[b];
+    const uint64_t path = a.p.path[b];
+    if (row < 0 || path == 0) return;  // (else it is the row guessed)
+    const int pos = a.p.pos[b], in0 = pos % c.C, s0 = pos / c.C, n = __popcll(path);
+    const int32_t *list = a.p.list + a.p.fresh[b];
+    for (int x = tid; x < kMaxTree; x += THREADS)
+        if ((path >> x) & 1) node[__popcll(path & ((1ull << x) - 1))] = x;
+    __syncthreads();
+    for (int j = tid; j < n; j += THREADS) {
+        const int in = in0 + j, seg = in / c.C;  // counted from s0
+        int page = -1;
+        if ((in + 1) % c.C == 0 && s0 + seg < c.nmax) page = list[seg];
+        turn[j] = make_float4(in % c.C ? 1.f : 0.f, a.delta ? dec[node[j]] : 1.f, a.delta ? bet[node[j]] : 1.f, __int_as_float(page));
     }
     __syncthreads();
-    const int pos = a.p.pos[b], in0 = pos % c.C, s0 = pos / c.C;
-    const int32_t *list = a.p.list + a.p.fresh[b];
-    const int r0 = warp * RPW * PASS + lane / LPR;
-    if (warp * RPW * PASS < RB) {
-        float4 m[PASS];
-        float4 *mem = reinterpret_cast<float4 *>(c.online + (((size_t)row * c.H + h) * D + rb * RB + r0) * D) + lane % LPR;
-#pragma unroll
-        for (int x = 0; x < PASS; ++x) m[x] = in0 ? mem[x * RPW * (D / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
-        int in = in0, s = s0;
-        for (int j = 0; j < n; ++j) {
-            const float4 kv = *reinterpret_cast<const float4 *>(&ks[j][lane % LPR * 4]);
-            float e[PASS];
-#pragma unroll
-            for (int x = 0; x < PASS; ++x) e[x] = vs[j][r0 + x * RPW];
-            if (a.delta) {
-                const float d = in ? dec[j] : 0.f, be = bet[j];  // an empty memory has nothing to decay
-#pragma unroll
-                for (int x = 0; x < PASS; ++x) {
-                    m[x] = in ? scale4(d, m[x]) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    float p = dot4(m[x], kv);
-#pragma unroll
-                    for (int o = LPR / 2; o > 0; o >>= 1) p += __shfl_xor_sync(0xffffffffu, p, o);
-                    e[x] = be * (e[x] - p);
+    if (a.delta) {
+        if (tid == 0) {
+            float s = 1.f;
+            for (int j = 0; j < n; ++j) {
+                const float2 w = *reinterpret_cast<const float2 *>(&turn[j]);
+                s = w.x == 0.f ? 1.f : s * w.y;
+                if (s < 0x1p-30f) {
+                    turn[j].x = s;
+                    s = 1.f;
                 }
-            } else if (!in) {
-#pragma unroll
-                for (int x = 0; x < PASS; ++x) m[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-#pragma unroll
-            for (int x = 0; x < PASS; ++x) m[x] = fma4(e[x], kv, m[x]);
-            if (++in == c.C) {
-                const int page = s < c.nmax ? list[s - s0] : -1;
-                if (page >= 0) {
-                    float4 *to = reinterpret_cast<float4 *>(c.pages + (((size_t)page * c.H + h) * D + rb * RB + r0) * D) + lane % LPR;
-#pragma unroll
-                    for (int x = 0; x < PASS; ++x) to[x * RPW * (D / 4)] = m[x];
-                }
-                in = 0;
-                ++s;
+                turn[j].y = s;
             }
         }
-#pragma unroll
-        for (int x = 0; x < PASS; ++x) mem[x * RPW * (D / 4)] = m[x];
+        __syncthreads();
+        for (int j = tid; j < n; j += THREADS) turn[j].z /= turn[j].y;
+        __syncthreads();
     }
-    if (rb == 0 && tid < D) {
-        float *sum = c.ksum + ((size_t)row * c.H + h) * D + tid;
-        float x = in0 ? *sum : 0.f;
-        int in = in0, s = s0;
-        for (int j = 0; j < n; ++j) {
-            x = (in ? x : 0.f) + ks[j][tid];
-            if (++in == c.C) {
-                const int page = s < c.nmax ? list[s - s0] : -1;
-                if (page >= 0) c.kbar[((size_t)page * c.H + h) * D + tid] = x / (float)c.C;
-                in = 0;
-                ++s;
-            }
+    if (rows) {
+        if (!in0) {
+#pragma unroll
+            for (int x = 0; x < R; ++x)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m[x][i] = 0;
         }
-        *sum = x;
+        auto store = [&](float4 *to, float s) {
+#pragma unroll
+            for (int x = 0; x < R; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 lo = of_pair(m[x][2 * i]), hi = of_pair(m[x][2 * i + 1]);
+                    to[x * APART + i * S::LANES] = make_float4(s * lo.x, s * lo.y, s * hi.x, s * hi.y);
+                }
+        };
+        for (int j = 0; j < n; ++j) {
+            const float4 t = turn[j];
+            const float *kj = ks + node[j] * D + 4 * l, *vj = vs + node[j] * S::ROWS + r0;
+            if (t.x != 1.f) {
+                const uint64_t ss = pair_of(t.x, t.x);
+#pragma unroll
+                for (int x = 0; x < R; ++x)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) m[x][i] = t.x == 0.f ? 0 : mul_pair(m[x][i], ss);
+            }
+            uint64_t k[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const ulonglong2 kv = *reinterpret_cast<const ulonglong2 *>(kj + 4 * i * S::LANES);
+                k[2 * i] = kv.x;
+                k[2 * i + 1] = kv.y;
+            }
+            float e[R];
+#pragma unroll
+            for (int x = 0; x < R; ++x) e[x] = vj[x * S::GROUPS];
+            if (a.delta) {
+                float p[R];
+#pragma unroll
+                for (int x = 0; x < R; ++x) {
+                    uint64_t p0 = mul_pair(m[x][0], k[0]);
+#pragma unroll
+                    for (int i = 1; i < 8; ++i) p0 = fma_pair(m[x][i], k[i], p0);
+                    const float2 q = of_pair(p0);
+                    p[x] = q.x + q.y;
+                }
+#pragma unroll
+                for (int o = S::LANES / 2; o > 0; o >>= 1)
+#pragma unroll
+                    for (int x = 0; x < R; ++x) p[x] += __shfl_xor_sync(0xffffffffu, p[x], o);
+#pragma unroll
+                for (int x = 0; x < R; ++x) e[x] = t.z * fmaf(-t.y, p[x], e[x]);
+            }
+#pragma unroll
+            for (int x = 0; x < R; ++x) {
+                const uint64_t ee = pair_of(e[x], e[x]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m[x][i] = fma_pair(ee, k[i], m[x][i]);
+            }
+            const int page = __float_as_int(t.w);
+            if (page >= 0) store(reinterpret_cast<float4 *>(c.pages + (((size_t)page * c.H + h) * D + rb * S::ROWS + r0) * D) + l, t.y);
+        }
+        store(mem, turn[n - 1].y);
+    }
+    if (rb == 0) {
+        for (int x = tid; x < D; x += THREADS) {
+            float *sum = c.ksum + ((size_t)row * c.H + h) * D + x;
+            float t = in0 ? *sum : 0.f;
+            int in = in0;
+            for (int j = 0; j < n; ++j) {
+                t = (in ? t : 0.f) + ks[node[j] * D + x];
+                if (++in == c.C) {
+                    const int page = __float_as_int(turn[j].w);
+                    if (page >= 0) c.kbar[((size_t)page * c.H + h) * D + x] = t / (float)c.C;
+                    in = 0;
+                }
+            }
+            *sum = t;
+        }
         if (h == 0 && tid == 0) c.pos[row] = pos + n;
     }
 }
@@ -258,6 +368,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_fork(Paged c, const int32_t
     keeper[x] = 0x7fffffff;
     kept[x] = 0;
     spare[x] = -1;
+    after_previous();
+    let_next_start();
     rows[x] = in ? c.row[x] : -1;
     int f = -1;
     if (in) {
@@ -288,13 +400,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_fork(Paged c, const int32_t
     if (r >= 0) c.row[x] = r;
 }
 
-__global__ void __launch_bounds__(256) fork_rows(Paged c, const int32_t *from, const int32_t *to)
+__global__ void __launch_bounds__(256) fork_rows(Paged c, const int32_t *from, const int32_t *to, int pieces)
 {
-    const int x = blockIdx.y, f = from[x], t = to[x];
+    after_previous();
+    const int x = (int)(blockIdx.x / pieces), piece = (int)(blockIdx.x % pieces), f = from[x], t = to[x];
     if (f == -2) return;
     const size_t mem = (size_t)c.H * c.d * c.d, key = (size_t)c.H * c.d;
-    if (f >= 0) copy_piece(c.online + t * mem, c.online + f * mem, mem, blockIdx.x);
-    if (blockIdx.x) return;
+    if (f >= 0) copy_piece(c.online + t * mem, c.online + f * mem, mem, piece);
+    if (piece) return;
     for (int i = threadIdx.x; i < c.nmax; i += 256) {
         const int gone = valid_page(c, c.table[(size_t)t * c.nmax + i]);
         const int now = f >= 0 ? valid_page(c, c.table[(size_t)f * c.nmax + i]) : -1;
@@ -313,6 +426,8 @@ __global__ void __launch_bounds__(256) fork_rows(Paged c, const int32_t *from, c
 __global__ void __launch_bounds__(kPlanThreads) plan_compact(Paged dst, Paged src, int32_t *from, int32_t *map, int32_t *live)
 {
     int n = 0;
+    after_previous();
+    let_next_start();
     for (int p0 = 0; p0 < src.P; p0 += kPlanThreads) {
         const int p = p0 + (int)threadIdx.x, refs = p < src.P ? src.refs[p] : 0;
         int here;
@@ -334,6 +449,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_compact(Paged dst, Paged sr
 __global__ void __launch_bounds__(256) compact_move(Paged dst, Paged src, const int32_t *from, const int32_t *map,
                                                     const int32_t *live, int places, int pieces)
 {
+    after_previous();
     const size_t mem = (size_t)dst.H * dst.d * dst.d, key = (size_t)dst.H * dst.d;
     const int y = (int)(blockIdx.x / pieces), piece = (int)(blockIdx.x % pieces);
     if (y < places) {
@@ -380,7 +496,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_load(Paged c, int slot, int
         if (p >= 0) atomicSub(c.refs + p, 1);
     }
     __syncthreads();
-    take_pages(c, done, list);
+    take_pages(c, done, list, (int)threadIdx.x < c.P ? __ldcg(c.refs + threadIdx.x) : 1);
     for (int i = threadIdx.x; i < c.nmax; i += kPlanThreads) table[i] = i < done ? __ldcg(list + i) : -1;
     if (threadIdx.x == 0) {
         c.pos[row] = L;
@@ -419,17 +535,21 @@ __global__ void __launch_bounds__(256) load_segment(Paged c, const E *k, const f
     }
 }
 
-template <typename E>
+template <typename E, int D>
 cudaError_t accept_impl(const TreeArgs &a, cudaStream_t s)
 {
-    const unsigned heads = (unsigned)(a.B * a.c.H);
+    using S = AcceptShape<D>;
+    return launch_early(accept_rows<E, D>, (size_t)a.B * a.c.H * (D / S::ROWS), 32 * S::WARPS, S::smem(a.T), s, a);
+}
+template <typename E>
+cudaError_t accept_by_d(const TreeArgs &a, cudaStream_t s)
+{
     switch (a.c.d) {
-    case 16: accept_rows<E, 16><<<heads, 256, 0, s>>>(a); break;
-    case 32: accept_rows<E, 32><<<heads, 256, 0, s>>>(a); break;
-    case 64: accept_rows<E, 64><<<heads * 2, 256, 0, s>>>(a); break;
-    default: accept_rows<E, 128><<<heads * 4, 256, 0, s>>>(a); break;
+    case 16: return accept_impl<E, 16>(a, s);
+    case 32: return accept_impl<E, 32>(a, s);
+    case 64: return accept_impl<E, 64>(a, s);
+    default: return accept_impl<E, 128>(a, s);
     }
-    return cudaGetLastError();
 }
 
 template <typename E>
@@ -453,34 +573,31 @@ unsigned copy_pieces(const Paged &c) { return (unsigned)(((size_t)c.H * c.d * c.
 
 cudaError_t launch_plan(const TreeArgs &a, cudaStream_t s)
 {
-    plan_rows<<<1, kPlanThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_early(plan_rows, 1, kPlanThreads, 0, s, a);
 }
 
 cudaError_t launch_accept(const TreeArgs &a, cudaStream_t s)
 {
-    return a.bf16 ? accept_impl<__nv_bfloat16>(a, s) : accept_impl<float>(a, s);
+    return a.bf16 ? accept_by_d<__nv_bfloat16>(a, s) : accept_by_d<float>(a, s);
 }
 
 cudaError_t launch_fork(const Paged &c, const int32_t *src, int32_t *plan, cudaStream_t s)
 {
-    plan_fork<<<1, kPlanThreads, 0, s>>>(c, src, plan, plan + c.S);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    fork_rows<<<dim3(copy_pieces(c), (unsigned)c.S), 256, 0, s>>>(c, plan, plan + c.S);
-    return cudaGetLastError();
+    const int32_t *from = plan, *to = plan + c.S;
+    const unsigned pieces = copy_pieces(c);
+    cudaError_t e = launch_early(plan_fork, 1, kPlanThreads, 0, s, c, src, plan, plan + c.S);
+    return e == cudaSuccess ? launch_early(fork_rows, (size_t)pieces * c.S, 256, 0, s, c, from, to, (int)pieces) : e;
 }
 
 cudaError_t launch_pages_compact(const Paged &dst, const Paged &src, int32_t *plan, cudaStream_t s)
 {
     int32_t *live = plan, *from = plan + 1, *map = from + dst.P;
-    plan_compact<<<1, kPlanThreads, 0, s>>>(dst, src, from, map, live);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_early(plan_compact, 1, kPlanThreads, 0, s, dst, src, from, map, live);
     if (e != cudaSuccess) return e;
     const int places = dst.P < src.P ? dst.P : src.P;
     const unsigned pieces = copy_pieces(dst);
-    compact_move<<<pieces * (unsigned)(places + dst.S), 256, 0, s>>>(dst, src, from, map, live, places, (int)pieces);
-    return cudaGetLastError();
+    return launch_early(compact_move, (size_t)pieces * (places + dst.S), 256, 0, s, dst, src, (const int32_t *)from, (const int32_t *)map,
+                        (const int32_t *)live, places, (int)pieces);
 }
 
 cudaError_t launch_pages_load(const Paged &c, int slot, const void *k, const float *states, int L, bool bf16, int32_t *plan,

@@ -89,12 +89,8 @@ struct Seat {
 };
 __device__ __forceinline__ Seat seat_of(const TreeArgs &a, int b, bool tell)
 {
+    if (a.p.act) return Seat{a.p.act[b], a.p.pos[b], a.T};
     Seat s{-1, 0, a.T};
-    if (a.p.act) {
-        s.row = a.p.act[b];
-        s.pos = a.p.pos[b];
-        return s;
-    }
     const Paged &c = a.c;
     const int slot = a.slots ? a.slots[b] : b;
     bool bad = slot < -1 || slot >= c.S;
