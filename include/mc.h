@@ -60,6 +60,7 @@
 #ifndef MC_H_
 #define MC_H_
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -344,6 +345,8 @@ int mc_cache_compact(const void *k, const void *u, const float *prefill_states, 
  *                                        rows of one writing call name: taken as said below, never followed
  *                    MC_PAGES_NONE_FREE  a segment found no free page and is lost
  *                    MC_PAGES_TABLE_FULL a sequence has more than n_max segments; those after are lost
+ *   work         : mc_paged_work_bytes() bytes, zeroed once before the first call and then the library's (and again after
+ *                  MC_ERR_DEVICE_TIMEOUT, which leaves the cache undefined).
  *   n_seqs, n_max: 1 .. 1024; n_pages: 1 .. 2^20; seg_len >= 1; d as for every call.
  * An empty cache has refs, pos and status zero, table -1 and row the identity.  New pages are the lowest free ones, given out
  * in the order of the batch's rows and of time.  The batch of a call is B <= n_seqs rows of tokens; slots (int32 [B],
@@ -358,8 +361,12 @@ typedef struct {
     int32_t *refs;
     float *online, *ksum;
     int32_t *table, *pos, *row, *status;
+    void *work;
     int32_t n_pages, n_seqs, H, d, seg_len, n_max;
 } mc_paged_cache;
+
+/* Bytes of a cache's work (0 for sizes that no cache has).  Host only. */
+size_t mc_paged_work_bytes(int n_seqs, int H, int d);
 
 enum { MC_PAGES_INDEX = 1, MC_PAGES_NONE_FREE = 2, MC_PAGES_TABLE_FULL = 4 };
 

@@ -26,7 +26,7 @@ MC_ERR_ALLOC, MC_ERR_CUDA, MC_ERR_DEVICE_TIMEOUT, MC_ERR_ALIGN, MC_ERR_DEVICE = 
 MC_ERR_SCRATCH = -10
 
 EXPORTED = ("mc_forward", "mc_forward_f32", "mc_forward_swla", "mc_forward_segments", "mc_log_segments", "mc_backward", "mc_backward_f32", "mc_decode_step", "mc_forward_delta", "mc_backward_delta",
-            "mc_decode_step_delta", "mc_decode_step_evict", "mc_cache_compact", "mc_decode_step_paged",
+            "mc_decode_step_delta", "mc_decode_step_evict", "mc_cache_compact", "mc_paged_work_bytes", "mc_decode_step_paged",
             "mc_decode_tree", "mc_tree_accept", "mc_pages_fork", "mc_pages_compact", "mc_pages_load", "mc_ssc_select", "mc_forward_host", "mc_forward_noalloc",
             "mc_check_device", "mc_trim_scratch", "mc_set_readout_form", "mc_profile_begin", "mc_profile_end",
             "mc_profile_stage", "mc_status_string")
@@ -78,6 +78,8 @@ def load_library():
     lib.mc_decode_step_evict.restype = i
     lib.mc_cache_compact.argtypes = [vp] * 3 + [i] * 8 + [vp] * 6 + [i, vp, i, vp]
     lib.mc_cache_compact.restype = i
+    lib.mc_paged_work_bytes.argtypes = [i] * 3
+    lib.mc_paged_work_bytes.restype = ctypes.c_size_t
     lib.mc_decode_step_paged.argtypes = [vp] * 8 + [i] * 3 + [vp, i, vp]
     lib.mc_decode_step_paged.restype = i
     lib.mc_decode_tree.argtypes = [vp] * 10 + [i] * 4 + [vp, i, vp]
@@ -590,7 +592,7 @@ MC_PAGES_INDEX, MC_PAGES_NONE_FREE, MC_PAGES_TABLE_FULL = 1, 2, 4
 
 
 class _CPagedCache(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_void_p) for n in ("pages", "kbar", "refs", "online", "ksum", "table", "pos", "row", "status")] + \
+    _fields_ = [(n, ctypes.c_void_p) for n in ("pages", "kbar", "refs", "online", "ksum", "table", "pos", "row", "status", "work")] + \
                [(n, ctypes.c_int32) for n in ("n_pages", "n_seqs", "H", "d", "seg_len", "n_max")]
 
 
@@ -611,7 +613,8 @@ class PagedCache:
         self._t = {"pages": torch.zeros((n_pages, H, d, d), **f32), "kbar": torch.zeros((n_pages, H, d), **f32),
                    "refs": torch.zeros((n_pages,), **i32), "online": torch.zeros((n_seqs, H, d, d), **f32),
                    "ksum": torch.zeros((n_seqs, H, d), **f32), "table": torch.full((n_seqs, n_max), -1, **i32),
-                   "pos": torch.zeros((n_seqs,), **i32), "row": torch.arange(n_seqs, **i32), "status": torch.zeros((1,), **i32)}
+                   "pos": torch.zeros((n_seqs,), **i32), "row": torch.arange(n_seqs, **i32), "status": torch.zeros((1,), **i32),
+                   "work": torch.zeros((load_library().mc_paged_work_bytes(self.n_seqs, self.H, self.d),), dtype=torch.uint8, device=device)}
         self.device = self._t["pages"].device
         self._c = _CPagedCache(*[t.data_ptr() for t in self._t.values()], self.n_pages, self.n_seqs, self.H, self.d,
                                self.seg_len, self.n_max)

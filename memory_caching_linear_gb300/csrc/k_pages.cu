@@ -70,7 +70,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_rows(TreeArgs a)
 {
     const Paged &c = a.c;
     const int tid = threadIdx.x, lane = tid % 32;
-    const bool accept = a.accept;
     __shared__ int taker[kMaxRows], lens[kMaxRows];
     taker[tid] = 0x7fffffff;
     lens[tid] = 0;
@@ -101,37 +100,35 @@ __global__ void __launch_bounds__(kPlanThreads) plan_rows(TreeArgs a)
         report(c, MC_PAGES_INDEX);
         row = -1;
     }
-    if (accept) {  // the path to the last node, a warp to a batch row with two nodes' parents on each lane
-        for (int b = tid / 32; b < a.B; b += kPlanThreads / 32) {
-            const int32_t *par = a.parent + (size_t)b * a.T;
-            const int lo = lane < a.T ? par[lane] : -1, hi = lane + 32 < a.T ? par[lane + 32] : -1;
-            int x = a.last[b];
-            bool bad = x < -1 || x >= a.T;
-            if (bad) x = -1;
-            uint64_t path = 0;
-            while (x >= 0) {  // parents come before their nodes: at most 64 turns
-                path |= 1ull << x;
-                const int f0 = __shfl_sync(0xffffffffu, lo, x & 31), f1 = __shfl_sync(0xffffffffu, hi, x & 31);
-                const int f = x < 32 ? f0 : f1;
-                if (f < -1 || f >= x) bad = true;
-                x = f >= -1 && f < x ? f : -1;
-            }
-            if (lane == 0) {
-                if (bad) report(c, MC_PAGES_INDEX);
-                lens[b] = __popcll(path);
-                a.p.path[b] = path;
-            }
+    // the path to the last node, a warp to a batch row with two nodes' parents on each lane
+    for (int b = tid / 32; b < a.B; b += kPlanThreads / 32) {
+        const int32_t *par = a.parent + (size_t)b * a.T;
+        const int lo = lane < a.T ? par[lane] : -1, hi = lane + 32 < a.T ? par[lane + 32] : -1;
+        int x = a.last[b];
+        bool bad = x < -1 || x >= a.T;
+        if (bad) x = -1;
+        uint64_t path = 0;
+        while (x >= 0) {  // parents come before their nodes: at most 64 turns
+            path |= 1ull << x;
+            const int f0 = __shfl_sync(0xffffffffu, lo, x & 31), f1 = __shfl_sync(0xffffffffu, hi, x & 31);
+            const int f = x < 32 ? f0 : f1;
+            if (f < -1 || f >= x) bad = true;
+            x = f >= -1 && f < x ? f : -1;
         }
-        __syncthreads();
+        if (lane == 0) {
+            if (bad) report(c, MC_PAGES_INDEX);
+            lens[b] = __popcll(path);
+            a.p.path[b] = path;
+        }
     }
-    const int len = row < 0 ? 0 : a.step ? 1 : accept ? lens[tid] : 0;
+    __syncthreads();
+    const int len = row < 0 ? 0 : lens[tid];
     const int s0 = pos / c.C, s1 = (pos + len) / c.C;
     const int more = row < 0 ? 0 : min(s1, c.nmax) - min(s0, c.nmax);
     if (row >= 0 && s1 > s0 && s1 > c.nmax) report(c, MC_PAGES_TABLE_FULL);
     if (in) {
         a.p.act[tid] = row;
         a.p.pos[tid] = pos;
-        a.p.len[tid] = len;
     }
     int want;
     const int fb = block_scan(more, &want);

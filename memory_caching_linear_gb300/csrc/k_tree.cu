@@ -1,5 +1,4 @@
-// k_tree.cu -- what the tokens of a draft read: a tree of up to 64 nodes that goes on from a sequence of a paged cache (a
-// single token is a tree of one node).
+// k_tree.cu -- what the tokens of a draft read: a tree of up to 64 nodes that goes on from a sequence of a paged cache.
 //
 // Node n at depth e is the token at position pos + e; its ancestors and itself are the tokens that the memories it reads have
 // seen beyond the cache.  With seg(a) the segment of node a, counted from the one that the cache has begun (0), and, per
@@ -186,7 +185,6 @@ __global__ void __launch_bounds__(kGateThreads) tree_gates(TreeArgs a)
             const float into = a.delta ? decay_from_cache(nodes, n) : 1.f;  // of the begun segment's memory
             s[nb + 1] = in0 && last == 0 ? into : 0.f;
             s[nb] = in0 ? gp[warp][0] * into : 0.f;
-            if (a.step) a.f0[(size_t)bh * a.Tp] = gp[warp][0];  // a step's end reads the memory after the token
         }
     }
     __syncthreads();
@@ -195,8 +193,7 @@ __global__ void __launch_bounds__(kGateThreads) tree_gates(TreeArgs a)
         const int t = i % kGroup;
         out[(size_t)(i / kGroup) * a.Tp + t] = n0 + t < m ? sc[t * stride + i / kGroup] : 0.f;
     }
-    if (!a.step)
-        write_path<kGroup>(a, nodes, bh, n0, m, [&](int t, int j) { return gp[t][j]; }, [&](int t, int x) { return kq[t][x]; },
+    write_path<kGroup>(a, nodes, bh, n0, m, [&](int t, int j) { return gp[t][j]; }, [&](int t, int x) { return kq[t][x]; },
                            [&](int t, int x) { return kk[t][x]; });
 }
 
@@ -503,69 +500,6 @@ __global__ void __launch_bounds__(256, 3) tree_finish(TreeArgs a, int segments)
     }
 }
 
-// The end of a step: the token's update of the online memory, its read, and what it completes.  32 rows of a head.
-template <typename E, int D>
-__global__ void __launch_bounds__(256) step_finish(TreeArgs a)
-{
-    constexpr int RB = D < 32 ? D : 32, LPR = D / 4, RPW = 32 / LPR, PASS = RB / (8 * RPW) < 1 ? 1 : RB / (8 * RPW);
-    const Paged &c = a.c;
-    const int bh = (int)blockIdx.x / (D / RB), rb = (int)blockIdx.x % (D / RB), b = bh / c.H, h = bh % c.H;
-    after_previous();
-    const Line line = line_in(a.line, a.B);
-    const int row = line.row[b], pos = line.pos[b], in0 = pos % c.C;
-    if (row < 0) return;
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const Parts parts(a, line, b, h, cached_segments(c, pos));
-    const int32_t *fresh = a.p.fresh + b;
-    const bool ends = in0 == c.C - 1;
-    const int page = ends && fresh[1] > fresh[0] ? a.p.list[fresh[0]] : -1;
-    const size_t at = (size_t)bh * D;
-    if (warp * RPW * PASS < RB) {
-        const int r0 = rb * RB + warp * RPW * PASS + lane / LPR, c0 = lane % LPR * 4;
-        const float4 kv = load4(static_cast<const E *>(a.k) + at + c0), qv = load4(static_cast<const E *>(a.q) + at + c0);
-        const float dec = a.delta ? delta_decay(to_f(static_cast<const E *>(a.la)[bh])) : 1.f;
-        const float bet = a.delta ? to_f(static_cast<const E *>(a.be)[bh]) : 1.f;
-        const float g_on = a.f0[(size_t)bh * a.Tp];
-        float4 *mem = reinterpret_cast<float4 *>(c.online + (((size_t)row * c.H + h) * D + r0) * D) + lane % LPR;
-        float4 m[PASS];
-        float sum[PASS];
-#pragma unroll
-        for (int x = 0; x < PASS; ++x) {
-            m[x] = in0 ? mem[x * RPW * (D / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
-            sum[x] = 0.f;
-        }
-        for (int j = parts.j0; j <= parts.j1; ++j)
-#pragma unroll
-            for (int x = 0; x < PASS; ++x) sum[x] += a.part[((size_t)j + bh) * a.Tp * D + r0 + x * RPW];
-#pragma unroll
-        for (int x = 0; x < PASS; ++x) {
-            const int r = r0 + x * RPW;
-            float e = to_f(static_cast<const E *>(a.v)[at + r]);
-            if (a.delta) {
-                if (in0) m[x] = scale4(dec, m[x]);
-                float p = dot4(m[x], kv);
-#pragma unroll
-                for (int o = LPR / 2; o > 0; o >>= 1) p += __shfl_xor_sync(0xffffffffu, p, o);
-                e = bet * (e - p);
-            }
-            m[x] = fma4(e, kv, m[x]);
-            mem[x * RPW * (D / 4)] = m[x];
-            if (page >= 0) reinterpret_cast<float4 *>(c.pages + (((size_t)page * c.H + h) * D + r) * D)[lane % LPR] = m[x];
-            float y = dot4(m[x], qv);
-#pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-            if (lane % LPR == 0) static_cast<E *>(a.y)[at + r] = from_f<E>(fmaf(g_on, y, sum[x]));
-        }
-    }
-    if (rb == 0 && tid < D) {
-        float *sum = c.ksum + ((size_t)row * c.H + h) * D + tid;
-        const float x = (in0 ? *sum : 0.f) + to_f(static_cast<const E *>(a.k)[at + tid]);
-        *sum = x;
-        if (page >= 0) c.kbar[((size_t)page * c.H + h) * D + tid] = x / (float)c.C;
-        if (h == 0 && tid == 0) c.pos[row] = pos + 1;
-    }
-}
-
 // ------------------------------------------------------------------------------------------------ launchers
 
 template <typename E, int D>
@@ -587,10 +521,7 @@ cudaError_t read_impl(const TreeArgs &a, cudaStream_t s)
 template <typename E, int D>
 cudaError_t finish_impl(const TreeArgs &a, cudaStream_t s)
 {
-    constexpr int RB = D < 32 ? D : 32;
-    const size_t heads = (size_t)a.B * a.c.H;
-    if (a.step) return launch_early(step_finish<E, D>, heads * (D / RB), 256, 0, s, a);
-    const size_t grid = heads * (D / FinishRows<D>::BLOCK);
+    const size_t grid = (size_t)a.B * a.c.H * (D / FinishRows<D>::BLOCK);
     const bool split = tree_tc_supported(a);
     const size_t smem = sizeof(float) * ((size_t)(a.delta ? 2 : 1) * a.T + (split ? path_segments(a) : 0)) * a.Tp;
     const int block = 32 * a.groups;  // a warp to eight nodes

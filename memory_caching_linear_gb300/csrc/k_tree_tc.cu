@@ -293,11 +293,9 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
                     }
                 }
             }
-            if (!ok) {  // the copies under way land before the CTA leaves
-                for (uint32_t x = g > (uint32_t)RING ? g - RING : 0; x < g; ++x) {
-                    int gave_up = 0;
-                    mbar_wait_limit(&full[x % RING], (x / RING) & 1, &gave_up, kWaitLimitNs);
-                }
+            for (uint32_t x = g > (uint32_t)RING ? g - RING : 0; x < g; ++x) {  // no copy lands after the CTA has left
+                int gave_up = 0;
+                mbar_wait_limit(&full[x % RING], (x / RING) & 1, &gave_up, kWaitLimitNs);
             }
         }
         __syncwarp();

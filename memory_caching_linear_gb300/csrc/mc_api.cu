@@ -829,14 +829,15 @@ int mc_check_device(mc_stream_t stream)
         cudaGetLastError();
         return MC_ERR_CUDA;
     }
-    int was = 0, was_bwd = 0, was_gen = 0, was64 = 0, was_delta = 0, was_tree = 0;
+    int was = 0, was_bwd = 0, was_gen = 0, was64 = 0, was_delta = 0, was_tree = 0, was_step = 0;
     if (mc::take_device_abort(&was) != cudaSuccess || mc::take_bwd_abort(&was_bwd) != cudaSuccess ||
         mc::take_gen_abort(&was_gen) != cudaSuccess || mc::take_tc64_abort(&was64) != cudaSuccess ||
-        mc::take_delta_abort(&was_delta) != cudaSuccess || mc::take_tree_abort(&was_tree) != cudaSuccess) {
+        mc::take_delta_abort(&was_delta) != cudaSuccess || mc::take_tree_abort(&was_tree) != cudaSuccess ||
+        mc::take_step_abort(&was_step) != cudaSuccess) {
         cudaGetLastError();
         return MC_ERR_CUDA;
     }
-    return was || was_bwd || was_gen || was64 || was_delta || was_tree ? MC_ERR_DEVICE_TIMEOUT : MC_OK;
+    return was || was_bwd || was_gen || was64 || was_delta || was_tree || was_step ? MC_ERR_DEVICE_TIMEOUT : MC_OK;
 }
 
 int mc_profile_begin(void *const *events, int capacity)

@@ -1,9 +1,9 @@
-// paged.cuh -- argument blocks and device helpers of decoding over a paged cache (mc_pages.cu, k_pages.cu, k_tree.cu,
+// paged.cuh -- argument blocks and device helpers of decoding over a paged cache (mc_pages.cu, k_pages.cu, k_step.cu, k_tree.cu,
 // k_tree_tc.cu).
 //
-// Calls that write the cache begin with a plan (one CTA): which row of the cache each batch row works on, its position, and
-// what it needs of the pool.  The kernels after it read positions from the plan alone, so that the last of them may write
-// the cache's.  A tree's reads need no plan.
+// The acceptance of a path, a fork, a compaction and a prompt's loading begin with a plan (one CTA): which rows of the cache
+// are worked on, and what is needed of the pool.  The kernel after it takes positions from the plan alone, so that it may write
+// the cache's.  A step and a tree's reads need no plan.
 #pragma once
 
 #include "mc_internal.cuh"
@@ -27,12 +27,11 @@ struct Paged {
     int P, S, H, d, C, nmax;
 };
 
-// What a call that writes does with the batch rows' sequences.
+// What the acceptance of paths does with the batch rows' sequences.
 struct Plan {
     int32_t *act;      // [B] the cache's row, -1: nothing to do; null: no plan
     int32_t *pos;      // [B] position before the call
-    int32_t *len;      // [B] tokens added (accept: the path's length)
-    uint64_t *path;    // [B] accept: the nodes of the path
+    uint64_t *path;    // [B] the nodes of the path
     int32_t *fresh;    // [B + 1] where a batch row's new pages begin in list
     int32_t *list;     // new pages in order of batch row and time, -1 where none was free
 };
@@ -58,14 +57,13 @@ struct TreeArgs {
     float *into;                          // [BH][Tp] split: decay from the cache to a node's deepest ancestor in the begun segment
     uint64_t *anc;                        // [B][64] a node's ancestors and itself
     int32_t *seg;                         // [B][64] its segment, counted from the one begun
-    float *f0;                            // [BH][Tp] a step: the online memory's gate
     float *Y0, *Z;                        // [BH][Tp][d] the begun segment's memory read with the nodes' queries (split, without gate
                                           // and decay) and with their keys (decayed; split: without)
     float *part;                          // [ranges + BH][Tp][d] partial reads
     float2 *weight;                       // [ranges + BH][Tp] split: their largest score and sum of exp(score - largest)
     int B, T, Tp, mode, topk;
     int ranges, groups;                   // shares of the memories; of the tokens
-    bool bf16, delta, step, accept;
+    bool bf16, delta;
 };
 
 // The U memories that a call reads are cut into R = ranges_of(U) ranges, none of them empty: memory x is in range
@@ -81,7 +79,7 @@ __device__ __forceinline__ int valid_page(const Paged &c, int p) { return (unsig
 __device__ __forceinline__ int cached_segments(const Paged &c, int pos) { return min(pos / c.C, c.nmax); }
 __device__ __forceinline__ int units_of(const TreeArgs &a, int pos)
 {
-    return cached_segments(a.c, pos) + (!a.step && pos % a.c.C ? (a.delta ? 2 : 1) : 0);
+    return cached_segments(a.c, pos) + (pos % a.c.C ? (a.delta ? 2 : 1) : 0);
 }
 // A batch row's place: the cache's row (-1: nobody's), its position, and its nodes.  tell: what is out of range is reported.
 struct Seat {
@@ -89,7 +87,6 @@ struct Seat {
 };
 __device__ __forceinline__ Seat seat_of(const TreeArgs &a, int b, bool tell)
 {
-    if (a.p.act) return Seat{a.p.act[b], a.p.pos[b], a.T};
     Seat s{-1, 0, a.T};
     const Paged &c = a.c;
     const int slot = a.slots ? a.slots[b] : b;
@@ -117,17 +114,9 @@ struct Line {
     __host__ __device__ static size_t ints(int B) { return 4 * (size_t)B + 1; }
 };
 __host__ __device__ inline Line line_in(int *space, int B) { return Line{space, space + B, space + 2 * B, space + 3 * B}; }
-// In shared memory; the whole block calls it.  tell as for seat_of.
-__device__ inline Line make_line(const TreeArgs &a, int *space, bool tell)
+// units[b + 1] are row b's own memories: makes them sums.  The whole block calls it.
+__device__ inline void sum_line(const TreeArgs &a, const Line &l)
 {
-    const Line l = line_in(space, a.B);
-    for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
-        const Seat s = seat_of(a, b, tell);
-        l.row[b] = s.row;
-        l.pos[b] = s.pos;
-        l.nodes[b] = s.m;
-        l.units[b + 1] = units_of(a, s);
-    }
     __syncthreads();
     if (threadIdx.x < 32) {
         int sum = 0;
@@ -145,9 +134,22 @@ __device__ inline Line make_line(const TreeArgs &a, int *space, bool tell)
         if (threadIdx.x == 0) l.units[0] = 0;
     }
     __syncthreads();
+}
+// The batch's line in shared memory; the whole block calls it.  tell as for seat_of.
+__device__ inline Line make_line(const TreeArgs &a, int *space, bool tell)
+{
+    const Line l = line_in(space, a.B);
+    for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
+        const Seat s = seat_of(a, b, tell);
+        l.row[b] = s.row;
+        l.pos[b] = s.pos;
+        l.nodes[b] = s.m;
+        l.units[b + 1] = units_of(a, s);
+    }
+    sum_line(a, l);
     return l;
 }
-// To memory, for tree_finish and step_finish.
+// To memory, for tree_finish.
 __device__ inline void leave_line(const TreeArgs &a, int *space)
 {
     make_line(a, space, true);
@@ -245,7 +247,15 @@ bool tree_tc_supported(const TreeArgs &a);  // the split read on the tensor core
 cudaError_t launch_tree_path_tc(const TreeArgs &a, cudaStream_t s);
 cudaError_t launch_tree_read_tc(const TreeArgs &a, cudaStream_t s);
 cudaError_t take_tree_abort(int *was_set);
-cudaError_t launch_tree_finish(const TreeArgs &a, cudaStream_t s);  // a step's end too
+cudaError_t launch_tree_finish(const TreeArgs &a, cudaStream_t s);
+// A step's memory in the cache (mc_paged_cache's work): tickets, zero between calls, and partial reads.
+struct StepWork {
+    int32_t *turns;  // [S H + 1]
+    float *part;     // [ranges + S H][d + 2] a range's read, its largest score and sum of weights
+    float *online;   // [S H][d + 1] the online memory's read and score
+};
+cudaError_t launch_step(const TreeArgs &a, const StepWork &work, cudaStream_t s);
+cudaError_t take_step_abort(int *was_set);
 cudaError_t launch_accept(const TreeArgs &a, cudaStream_t s);
 cudaError_t launch_fork(const Paged &c, const int32_t *src, int32_t *plan, cudaStream_t s);
 cudaError_t launch_pages_compact(const Paged &dst, const Paged &src, int32_t *plan, cudaStream_t s);

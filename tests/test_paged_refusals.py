@@ -8,7 +8,7 @@ import memory_caching_linear_gb300 as mcl
 from memory_caching_linear_gb300 import build as mcbuild
 
 FAKE = 1 << 20  # an aligned address that is never read
-PTRS = ("pages", "kbar", "refs", "online", "ksum", "table", "pos", "row", "status")
+PTRS = ("pages", "kbar", "refs", "online", "ksum", "table", "pos", "row", "status", "work")
 
 
 @pytest.fixture(scope="module")
@@ -57,7 +57,7 @@ def test_caches(lib, call):
         assert call(lib, cache(**bad)) == mcl.MC_ERR_SHAPE, bad
     for n in PTRS:
         assert call(lib, cache(**{n: None})) == mcl.MC_ERR_NULL, n
-        off = 8 if n in ("pages", "kbar", "online", "ksum") else 2
+        off = 8 if n in ("pages", "kbar", "online", "ksum", "work") else 2
         assert call(lib, cache(**{n: FAKE + off})) == mcl.MC_ERR_ALIGN, n
 
 
@@ -105,7 +105,15 @@ def test_pools(lib):
     assert load(lib, k=None) == mcl.MC_ERR_NULL and load(lib, states=FAKE + 4) == mcl.MC_ERR_ALIGN
 
 
-def test_the_binding():
+def test_work_bytes(lib):
+    """Tickets of every head and one more, then 152 ranges' and every head's partial reads, then the online memories'."""
+    up = lambda x: -(-x // 256) * 256  # noqa: E731
+    for S, H, d in ((1, 1, 16), (24, 16, 128), (1024, 7, 64)):
+        assert lib.mc_paged_work_bytes(S, H, d) == up(4 * (S * H + 1)) + up(4 * (152 + S * H) * (d + 2)) + up(4 * S * H * (d + 1))
+    assert lib.mc_paged_work_bytes(0, 1, 16) == 0 and lib.mc_paged_work_bytes(1025, 1, 16) == 0 and lib.mc_paged_work_bytes(1, 0, 16) == 0
+
+
+def test_the_binding(lib):
     c = mcl.PagedCache(3, 2, 16, 4, 5, 7, device="cpu")
     assert c.table.tolist() == [[-1] * 5] * 3 and c.row.tolist() == [0, 1, 2] and c.refs.tolist() == [0] * 7
     with pytest.raises(AttributeError):
