@@ -31,20 +31,25 @@ size_t gates_smem(const TreeArgs &a)
     return 4 * (ints > floats ? ints : floats);
 }
 
-template <typename E, int D>
+// WHOLE: the rest too, for drafts of up to 8 nodes over few heads: a CTA has 8 (d = 128), 16 (64) or all rows of a head, a lane
+// group to each, and goes over all memories with the gates that it has worked out for itself.  One launch and no scratch.
+template <int D> struct WholeRows { static constexpr int PER_CTA = 8 * (32 / (D / 4)), CTAS = D / PER_CTA < 1 ? 1 : D / PER_CTA; };
+
+template <typename E, int D, bool WHOLE>
 __global__ void __launch_bounds__(kGateThreads) tree_gates(TreeArgs a)
 {
     constexpr int LPR = D / 4, RPW = 32 / LPR, WARPS = kGateThreads / 32;
     const Paged &c = a.c;
     extern __shared__ __align__(16) float dyn[];
     after_previous();
-    if (blockIdx.x == gridDim.x - 1) {  // one CTA more, for those that come after
+    if (!WHOLE && blockIdx.x == gridDim.x - 1) {  // one CTA more, for those that come after
         leave_line(a, reinterpret_cast<int *>(dyn));
         return;
     }
-    const int bh = (int)blockIdx.x / a.groups, n0 = (int)blockIdx.x % a.groups * kGroup, b = bh / c.H, h = bh % c.H;
+    const int per_head = WHOLE ? WholeRows<D>::CTAS : a.groups, bh = (int)blockIdx.x / per_head, part = (int)blockIdx.x % per_head;
+    const int n0 = WHOLE ? 0 : part * kGroup, b = bh / c.H, h = bh % c.H;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const Seat seat = seat_of(a, b, false);
+    const Seat seat = seat_of(a, b, WHOLE && h == 0 && part == 0 && tid == 0);
     const int row = seat.row, m = seat.m;
     if (row < 0 || n0 >= m) return;
     const int nb = cached_segments(c, seat.pos), in0 = seat.pos % c.C;
@@ -66,6 +71,21 @@ __global__ void __launch_bounds__(kGateThreads) tree_gates(TreeArgs a)
         if (a.delta) tok[2][t][x] = in ? to_f(static_cast<const E *>(a.k)[at]) : 0.f;
     }
     make_nodes<E>(a, nodes, b, bh, m, in0);
+
+    // WHOLE: this lane's row, and the first memories' entries under way
+    const int r = part * WholeRows<D>::PER_CTA + warp * RPW + lane / LPR, c0 = lane % LPR * 4;
+    const bool reads = WHOLE && warp * RPW + part * WholeRows<D>::PER_CTA < D;
+    const int count = nb + (in0 ? 1 : 0);  // memories to read
+    auto entry = [&](int i) {
+        if (i > nb || (i < nb && page[i] < 0) || (i == nb && !in0)) return make_float4(0.f, 0.f, 0.f, 0.f);
+        const float *M = i < nb ? c.pages + ((size_t)page[i] * c.H + h) * D * D : c.online + ((size_t)row * c.H + h) * D * D;
+        return __ldcs(reinterpret_cast<const float4 *>(M + (size_t)r * D + c0));
+    };
+    float4 ahead[4];
+    if (reads && a.mode != MC_SSC) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) ahead[x] = entry(x);
+    }
 
     // dot products of the group's tokens (tok[which]) with rows: LPR lanes to a row
     auto dots = [&](int which, int rows, auto load, auto store) {
@@ -188,6 +208,88 @@ __global__ void __launch_bounds__(kGateThreads) tree_gates(TreeArgs a)
         }
     }
     __syncthreads();
+    if constexpr (WHOLE) {
+        __shared__ float P[kGroup][kGroup], A[kGroup][kGroup];  // [node][ancestor]
+        __shared__ float base[WholeRows<D>::PER_CTA][2 * kGroup];
+        if (tid < kGroup * kGroup) {
+            const int n = tid / kGroup, x = tid % kGroup;
+            const bool above = n < m && (nodes.anc[n] >> x) & 1;
+            P[n][x] = above ? path_read(a, nodes, n, x, gp[n][nodes.seg[x]], kq[n][x]) : 0.f;
+            A[n][x] = above && a.delta ? path_meet(nodes, n, x, kk[n][x]) : 0.f;
+        }
+        __syncthreads();
+        if (!reads) return;
+        float y[kGroup] = {}, z[kGroup] = {};
+        float4 q[kGroup];
+#pragma unroll
+        for (int t = 0; t < kGroup; ++t) q[t] = *reinterpret_cast<const float4 *>(&tok[1][t][c0]);
+        for (int i0 = 0; i0 < count; i0 += 4) {
+            float4 w[4];
+            if (i0 == 0 && a.mode != MC_SSC) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) w[x] = ahead[x];
+            } else {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    bool any = false;
+                    if (a.mode == MC_SSC && i0 + x < count)
+#pragma unroll
+                        for (int t = 0; t < kGroup; ++t) any |= t < m && sc[t * stride + i0 + x] != 0.f;
+                    w[x] = a.mode != MC_SSC || any || i0 + x == nb ? entry(i0 + x) : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                if (i0 + x >= count) break;
+#pragma unroll
+                for (int t = 0; t < kGroup; ++t) {
+                    const float g = t < m ? sc[t * stride + i0 + x] : 0.f;
+                    if (g != 0.f) y[t] = fmaf(g, dot4(w[x], q[t]), y[t]);
+                }
+                if (a.delta && i0 + x == nb) {  // what the begun memory answers to the keys
+#pragma unroll
+                    for (int t = 0; t < kGroup; ++t) {
+                        const float f = t < m ? sc[t * stride + nb + 1] : 0.f;
+                        if (f != 0.f) z[t] = f * dot4(w[x], *reinterpret_cast<const float4 *>(&tok[2][t][c0]));
+                    }
+                }
+            }
+        }
+        const int rl = warp * RPW + lane / LPR;
+        sum_groups<kGroup, LPR>(y, lane);
+        sum_groups<kGroup, LPR>(z, lane);
+        if (stores<kGroup, LPR>(lane)) {
+#pragma unroll
+            for (int x = 0; x < kept<kGroup, LPR>(); ++x) {
+                base[rl][first<kGroup, LPR>(lane) + x] = y[x];
+                base[rl][kGroup + first<kGroup, LPR>(lane) + x] = z[x];
+            }
+        }
+        __syncwarp();
+        const int mine = warp * RPW + lane, mr = part * WholeRows<D>::PER_CTA + mine;  // a lane to a row: e in the nodes' order
+        if (lane >= RPW || mr >= D) return;
+        const size_t at = (size_t)bh * a.T;
+        float e[kGroup], out[kGroup];
+#pragma unroll
+        for (int t = 0; t < kGroup; ++t) {
+            e[t] = t < m ? to_f(static_cast<const E *>(a.v)[(at + t) * D + mr]) - base[mine][kGroup + t] : 0.f;
+            out[t] = base[mine][t];
+        }
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j) {
+            if (j >= m) break;
+#pragma unroll
+            for (int t = j; t < kGroup; ++t)
+                if (t < m && (nodes.anc[t] >> j) & 1) {
+                    out[t] = fmaf(P[t][j], e[j], out[t]);
+                    if (A[t][j] != 0.f) e[t] = fmaf(-A[t][j], e[j], e[t]);
+                }
+        }
+#pragma unroll
+        for (int t = 0; t < kGroup; ++t)
+            if (t < m) static_cast<E *>(a.y)[(at + t) * D + mr] = from_f<E>(out[t]);
+        return;
+    }
     float *out = a.gates + (size_t)bh * (c.nmax + 2) * a.Tp + n0;
     for (int i = tid; i < (nb + 2) * kGroup; i += kGateThreads) {
         const int t = i % kGroup;
@@ -505,7 +607,9 @@ __global__ void __launch_bounds__(256, 3) tree_finish(TreeArgs a, int segments)
 template <typename E, int D>
 cudaError_t gates_impl(const TreeArgs &a, cudaStream_t s)
 {
-    return launch_early(tree_gates<E, D>, (size_t)a.B * a.c.H * a.groups + 1, kGateThreads, gates_smem(a), s, a);
+    const size_t heads = (size_t)a.B * a.c.H;
+    return a.whole ? launch_early(tree_gates<E, D, true>, heads * WholeRows<D>::CTAS, kGateThreads, gates_smem(a), s, a)
+                   : launch_early(tree_gates<E, D, false>, heads * a.groups + 1, kGateThreads, gates_smem(a), s, a);
 }
 
 template <typename E, int D>
@@ -549,6 +653,12 @@ cudaError_t run(const TreeArgs &a, cudaStream_t s, int what)
 
 }  // namespace
 
+// While the memories that there is room for come to no more than 40 MB: 4 heads of d = 64 over 5 segments, 8 nodes, 11 us in one
+// launch and 17 in three; 16 heads of d = 128 over 20, 18 and 28; over 63 (66 MB) 48 and 39.
+bool tree_whole(const TreeArgs &a)
+{
+    return a.T <= kGroup && (long long)a.B * a.c.H * (a.c.nmax + 1) * a.c.d * a.c.d * 4 <= 40 << 20;
+}
 cudaError_t launch_tree_gates(const TreeArgs &a, cudaStream_t s) { return run(a, s, 0); }
 cudaError_t launch_tree_read(const TreeArgs &a, cudaStream_t s) { return run(a, s, 1); }
 cudaError_t launch_tree_finish(const TreeArgs &a, cudaStream_t s) { return run(a, s, 2); }

@@ -1,20 +1,19 @@
-// k_tree_tc.cu -- what a drafted tree reads of the cached memories, on the tensor cores (bf16 tokens, d = 64 or 128, more than
-// 8 nodes, every cached memory read by every node: no SSC).
+// k_tree_tc.cu -- what a drafted tree reads of the cached memories, on the tensor cores (bf16 tokens, d = 64 or 128, every cached
+// memory read by every node: no SSC).
 //
 // The reads (tree_read_tc).  For the head at hand, D[r][t] = sum over memories i of M^(i)[r][:] . (g_{t,i} q_t): the fp32 memory is
 // the A operand as it comes by TMA (kind::tf32 takes 11 significant bits of it: 2^-11 of every product against the 2^-9 of
 // y's own rounding), the weighted queries are B, rounded to tf32, and the sum over a head's memories stays in tensor memory.
 // A memory of 64 KB is read from HBM once for all nodes, 1.5 us of an SM's share of the bandwidth, against 0.3 us of products
-// at 64 nodes: HBM is the bound, so the memories stream through a ring of 32-column panels (144 KB in flight on an SM) and
-// everything else is made to keep up.
+// at 64 nodes: HBM is the bound, so the memories stream through a ring of 32-column panels (144 KB on an SM) and
+// everything else is made to keep up: a head's sums are brought out while the next one's panels and B are on their way.
 //
 // The memories of all heads and sequences form one line, cut into one range per CTA whatever the sequences' lengths.  A range
-// works out the scores of its own memories when it comes to a head (while the ring fills), weighs them against its own largest
-// and leaves the sum of its weights with its partial read: tree_finish joins them, as a softmax over parts.  So nothing has to
-// be known of the other ranges before the memories can be read; and the begun segment's memory, whose weight hangs on the
-// path, is read without one.
+// leaves the sum of its weights with its partial read, and tree_finish joins them, as a softmax over parts; the begun segment's
+// memory, whose weight hangs on the path, is read without one.
 //
-// The path's own products (tree_path_tc) are a small kernel that comes up beside the reads once these have their first scores.
+// The scores of the cached segments (tree_scores_tc) come first: the reads' CTAs come up beside them and fill their rings.
+// The path's own products (tree_path_tc) are a small kernel that comes up beside the reads once these are under way.
 // It needs nothing of them, but ends after them, so that what follows has both.
 #include <cfloat>
 #include <cstdint>
@@ -65,12 +64,93 @@ __device__ __forceinline__ void rows_of(const __nv_bfloat16 *lo, const __nv_bflo
     f[3] = y.y;
 }
 
-// ------------------------------------------------------------------------------------------------ the path
+// ------------------------------------------------------------------------------------------------ the scores
 
 constexpr int kSpan = 32, kPathThreads = 256, kCol = kSpan + 1;
+
+// Scores of a head's cached segments for 32 nodes, and every node's largest.  Eight segments a warp at a time; a mean key takes
+// part in two bf16 terms (2^-17 of it, for weights that are not ranked).  A chain of loads bounds it (slot, row, position,
+// page, mean key).
+template <int D>
+__global__ void __launch_bounds__(256) tree_scores_tc(TreeArgs a, int spans)
+{
+    constexpr int KS = D / 16, LINE = 2 * D + 32;  // router inputs in rows eight banks apart
+    __shared__ __align__(16) uint8_t us[kSpan * LINE];
+    __shared__ float top[8][kSpan];
+    const Paged &c = a.c;
+    const int bh = (int)blockIdx.x / spans, n0 = (int)blockIdx.x % spans * kSpan, b = bh / c.H, h = bh % c.H;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, c4 = lane % 4;
+    after_previous();
+    let_next_start();
+    const uint4 *U = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.u) + ((size_t)bh * a.T + n0) * D);
+    const int here = min(kSpan, a.T - n0);
+    uint4 inputs[kSpan * (D / 8) / 256];
+#pragma unroll
+    for (int x = 0; x < kSpan * (D / 8) / 256; ++x) inputs[x] = tid + 256 * x < here * (D / 8) ? __ldg(U + tid + 256 * x) : make_uint4(0, 0, 0, 0);
+    const Seat seat = seat_of(a, b, false);
+    if (seat.row < 0 || n0 >= seat.m) return;
+    const int nb = cached_segments(c, seat.pos);
+    const int32_t *table = c.table + (size_t)seat.row * c.nmax;
+    int page = 8 * warp + g < nb ? table[8 * warp + g] : -1;
+#pragma unroll
+    for (int x = 0; x < kSpan * (D / 8) / 256; ++x) {
+        const int y = tid + 256 * x;
+        *reinterpret_cast<uint4 *>(us + y / (D / 8) * LINE + y % (D / 8) * 16) = inputs[x];
+    }
+    __syncthreads();
+    const float low = __int_as_float(0xff800000);
+    float *scores = a.gates + (size_t)bh * a.c.nmax * a.Tp + n0, most[4] = {low, low, low, low};  // of rows g, g + 8, g + 16, g + 24
+    for (int i0 = 8 * warp; i0 < nb; i0 += 64) {
+        page = valid_page(c, page);
+        const float *src = c.kbar + ((size_t)max(page, 0) * c.H + h) * D;
+        uint32_t hi[KS][2], lo[KS][2];
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            const float4 v = page >= 0 ? load4(src + 16 * ks + 4 * c4) : make_float4(0.f, 0.f, 0.f, 0.f);
+            mma::split2(v.x, v.y, hi[ks][0], lo[ks][0]);
+            mma::split2(v.z, v.w, hi[ks][1], lo[ks][1]);
+        }
+        const bool there[2] = {__shfl_sync(0xffffffffu, page, 8 * c4) >= 0, __shfl_sync(0xffffffffu, page, 8 * c4 + 4) >= 0};
+        page = i0 + 64 + g < nb ? table[i0 + 64 + g] : -1;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+            const uint8_t *first = us + (16 * mt + g) * LINE + 8 * c4, *second = first + 8 * LINE;
+            float s[4] = {};
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                const uint2 x = *reinterpret_cast<const uint2 *>(first + 32 * ks), y = *reinterpret_cast<const uint2 *>(second + 32 * ks);
+                const uint32_t f[4] = {x.x, y.x, x.y, y.y};
+                mma::mma16816(s, f, hi[ks][0], hi[ks][1]);
+                mma::mma16816(s, f, lo[ks][0], lo[ks][1]);
+            }
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {  // segment i0 + 2 c4 (+ 1), node n0 + t
+                const int seg = i0 + 2 * c4 + (y & 1), t = 16 * mt + g + (y & 2 ? 8 : 0);
+                const float x = there[y & 1] ? s[y] : low;
+                most[2 * mt + (y >> 1)] = fmaxf(most[2 * mt + (y >> 1)], x);
+                if (seg < nb && n0 + t < seat.m) scores[(size_t)seg * a.Tp + t] = x;
+            }
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        most[x] = fmaxf(most[x], __shfl_xor_sync(0xffffffffu, most[x], 1));
+        most[x] = fmaxf(most[x], __shfl_xor_sync(0xffffffffu, most[x], 2));
+        if (c4 == 0) top[warp][8 * x + g] = most[x];
+    }
+    __syncthreads();
+    if (tid < kSpan && n0 + tid < seat.m) {
+        float best = -FLT_MAX;  // (no segment may have a page)
+#pragma unroll
+        for (int x = 0; x < 8; ++x) best = fmaxf(best, top[x][tid]);
+        a.top[(size_t)bh * a.Tp + n0 + tid] = best;
+    }
+}
+
+// ------------------------------------------------------------------------------------------------ the path
 // Registers a thread, so that a CTA of each runs on an SM: a quarter of it, with 512 registers a lane, has up to three of the
 // reads' ten warps and two of the path's eight.
-constexpr int kPathRegs = 88, kReadRegs = 112;
+constexpr int kPathRegs = 96, kReadRegs = 104;
 
 // Scores of the path's segments, P without the gates, and A, for 32 nodes of a head at a time.  One CTA on an SM goes over its
 // share of the heads: little enough in registers and shared memory to run beside a CTA of tree_read_tc.
@@ -181,7 +261,6 @@ constexpr int kWorkers = 8, kThreads = 32 * (kWorkers + 2);
 constexpr int kRingBytes = 147456;            // nine panels of 128 rows, eighteen of 64
 constexpr int kMaxPanels = 18;
 constexpr int kBSlot = kMaxTree * 128 * 4;    // weighted queries of one memory
-constexpr int kULine = 288;                   // bytes between a run's router inputs, where B's first goes later: rows eight banks apart
 constexpr int kReadSmem = 1024 + kRingBytes + 2 * kBSlot;
 
 enum { kCached, kBegunQ, kBegunK };
@@ -226,21 +305,20 @@ template <int D>
 __global__ void __maxnreg__(kReadRegs)
 tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ CUtensorMap online, TreeArgs a)
 {
-    constexpr int PANELS = D / 32, kPanelBytes = D * 128, RING = kRingBytes / kPanelBytes, KS = D / 16;
+    constexpr int PANELS = D / 32, kPanelBytes = D * 128, RING = kRingBytes / kPanelBytes;
+    constexpr int BATCH = 4 / PANELS;  // memories whose B share a slot and its handshake
     extern __shared__ uint8_t raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint8_t *bs = ring + kRingBytes;  // (a 64-row panel's second half, which nobody reads, may be of the next one or of B)
-    uint8_t *us = bs;  // (D of the run before is complete by then: nothing reads B)
     int *space = reinterpret_cast<int *>(raw + kReadSmem);
-    __shared__ uint64_t full[kMaxPanels], empty[kMaxPanels], b_full[2], b_empty[2], d_full[2], d_empty[2], staged, scored, drain;
-    __shared__ float top[kWorkers][kMaxTree];
+    __shared__ uint64_t full[kMaxPanels], empty[kMaxPanels], b_full[2], b_empty[2], d_full[2], d_empty[2], drain;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
     const Paged &c = a.c;
-    after_previous();
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    if (!a.scored) after_previous();  // (else the scores' kernel has waited for what came before)
     const int NT = (a.T + 15) / 16 * 16;                           // columns of D
-    const int groups = (NT + 31) / 32, writers = PANELS * groups;  // warps that make B: 32 tokens of one panel each
+    const int groups = (NT + 31) / 32, writers = PANELS * BATCH * groups;  // warps that make B: 32 tokens of one panel each
     if (tid == 0) {
         abort_flag = 0;
         for (int i = 0; i < RING; ++i) {
@@ -253,8 +331,6 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
             mbar_init(&d_full[i], 1);
             mbar_init(&d_empty[i], kWorkers);
         }
-        mbar_init(&staged, kWorkers);
-        mbar_init(&scored, kWorkers);
         mbar_init(&drain, 1);
         fence_mbar_init();
     }
@@ -307,19 +383,23 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
             while (ok && runs.next(a, line, r)) {
                 const uint32_t d = tb + 64 * (n & 1);
                 ok = mbar_wait(&d_empty[n & 1], ((n >> 1) & 1) ^ 1, &abort_flag);
-                for (int i = r.i0; ok && i < r.i1; ++i, ++u) {
+                for (int i = r.i0; ok && i < r.i1; i += BATCH, ++u) {
                     if (!(ok = mbar_wait(&b_full[u & 1], (u >> 1) & 1, &abort_flag))) break;
                     const uint32_t b0 = smem_u32(bs + (u & 1) * kBSlot);
-                    for (int x = 0; x < PANELS; ++x, ++g) {
-                        const uint32_t s = g % RING;
-                        if (!(ok = mbar_wait(&full[s], (g / RING) & 1, &abort_flag))) break;
-                        tc_fence_after();
-                        const uint32_t a0 = smem_u32(ring + s * kPanelBytes);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_tf32(d, make_desc_sw128(a0 + 32 * k, 0, 1024), make_desc_sw128(b0 + x * NT * 128 + 32 * k, 0, 1024),
-                                     idesc, i > r.i0 || x > 0 || k > 0);
-                        mma_commit(&empty[s]);
+                    for (int y = 0; y < BATCH; ++y) {
+                        if (!ok || i + y >= r.i1) break;
+                        for (int x = 0; x < PANELS; ++x, ++g) {
+                            const uint32_t s = g % RING;
+                            if (!(ok = mbar_wait(&full[s], (g / RING) & 1, &abort_flag))) break;
+                            tc_fence_after();
+                            const uint32_t a0 = smem_u32(ring + s * kPanelBytes), bx = b0 + (y * PANELS + x) * NT * 128;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_tf32(d, make_desc_sw128(a0 + 32 * k, 0, 1024), make_desc_sw128(bx + 32 * k, 0, 1024), idesc,
+                                         i + y > r.i0 || x > 0 || k > 0);
+                            mma_commit(&empty[s]);
+                        }
                     }
                     if (ok) mma_commit(&b_empty[u & 1]);
                 }
@@ -334,105 +414,38 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
         }
         __syncwarp();
     } else {
-        const int panel = warp % PANELS, t = warp / PANELS * 32 + lane;  // this thread's token and 32 columns of B
+        // this thread's memory of a slot's, 32 columns of B, and token
+        const int sub = warp / PANELS % BATCH, panel = warp % PANELS, t = warp / (PANELS * BATCH) * 32 + lane;
         const bool writes = warp < writers, routed = a.mode == MC_GRM;
-        uint32_t u = 0, n = 0, scorings = 0;
+        uint32_t u = 0, n = 0;
         bool ok = true;
-        while (ok && runs.next(a, line, r)) {
-            float *scores = a.gates + (size_t)r.bh * (c.nmax + 2) * a.Tp;
-            const bool in = writes && t < r.m, cached = r.kind == kCached;
-            float best = 0.f;
-            if (cached && routed) {
-                // scores of the run's memories, eight segments a warp at a time; a mean key takes part in two bf16 terms (2^-17 of
-                // it, for weights that are not ranked).  The ring holds 3 us of memories: the loads here, which nothing hides,
-                // come in two rounds, pages' numbers and router inputs, then mean keys.
-                const int32_t *table = c.table + (size_t)r.row * c.nmax;
-                const int g = lane / 4, c4 = lane % 4;
-                const float low = __int_as_float(0xff800000);
-                int page = r.i0 + 8 * warp + g < r.i1 ? table[r.i0 + 8 * warp + g] : -1;
-                const uint4 *U = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.u) + (size_t)r.bh * a.T * D);
-                for (int x = tid; x < r.m * (D / 8); x += 32 * kWorkers)
-                    *reinterpret_cast<uint4 *>(us + x / (D / 8) * kULine + x % (D / 8) * 16) = __ldg(U + x);
-                float most[2 * (kMaxTree / 16)];
+        after_previous();  // the scores
+        // the sums of run `i` to out: rows 32 (warp % 4) + lane of D; the two warps of a quarter take every other 16 columns
+        float *out = nullptr;
+        int nodes = 0;
+        auto bring_out = [&](uint32_t i) {
+            if (!mbar_wait(&d_full[i & 1], (i >> 1) & 1, &abort_flag)) return false;
+            tc_fence_after();
+            const int quarter = warp % 4, row = 32 * quarter + lane;
+            for (int t0 = 16 * (warp / 4); t0 < NT; t0 += 32) {
+                float x[16];
+                tmem_ld16f(tmem_addr(tb + 64 * (i & 1), 32 * quarter, t0), x);
+                tmem_wait_ld();
+                if (row < D) {
 #pragma unroll
-                for (int x = 0; x < 2 * (kMaxTree / 16); ++x) most[x] = low;
-                bool waited = false;
-                for (int i0 = r.i0 + 8 * warp; i0 < r.i1 || !waited; i0 += 8 * kWorkers) {
-                    page = valid_page(c, page);
-                    const float *src = c.kbar + ((size_t)max(page, 0) * c.H + r.h) * D;
-                    float4 v[KS];
-#pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) v[ks] = page >= 0 ? load4(src + 16 * ks + 4 * c4) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    uint32_t kb_hi[KS][2], kb_lo[KS][2];
-#pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) {
-                        mma::split2(v[ks].x, v[ks].y, kb_hi[ks][0], kb_lo[ks][0]);
-                        mma::split2(v[ks].z, v[ks].w, kb_hi[ks][1], kb_lo[ks][1]);
-                    }
-                    const bool there0 = __shfl_sync(0xffffffffu, page, 8 * c4) >= 0, there1 = __shfl_sync(0xffffffffu, page, 8 * c4 + 4) >= 0;
-                    const int ahead = i0 + 8 * kWorkers + g;
-                    page = ahead < r.i1 ? table[ahead] : -1;
-                    if (!waited) {  // every warp has its share of the router inputs in place
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&staged);
-                        if (!(ok = mbar_wait(&staged, scorings & 1, &abort_flag))) break;
-                        waited = true;
-                        if (i0 >= r.i1) break;
-                    }
-#pragma unroll
-                    for (int mt = 0; mt < kMaxTree / 16; ++mt) {
-                        if (16 * mt >= r.m) continue;
-                        const int lo = 16 * mt + g, hi = lo + 8;
-                        const uint8_t *ulo = us + lo * kULine + 8 * c4, *uhi = us + hi * kULine + 8 * c4;
-                        float s[4] = {};
-#pragma unroll
-                        for (int ks = 0; ks < KS; ++ks) {
-                            const uint2 x = *reinterpret_cast<const uint2 *>(ulo + 32 * ks), y = *reinterpret_cast<const uint2 *>(uhi + 32 * ks);
-                            const uint32_t f[4] = {x.x, y.x, x.y, y.y};
-                            mma::mma16816(s, f, kb_hi[ks][0], kb_hi[ks][1]);
-                            mma::mma16816(s, f, kb_lo[ks][0], kb_lo[ks][1]);
-                        }
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {  // segment i0 + 2 c4 (+ 1), token lo or hi
-                            const int seg = i0 + 2 * c4 + (y & 1), token = y & 2 ? hi : lo;
-                            const float x = (y & 1 ? there1 : there0) ? s[y] : low;
-                            most[2 * mt + (y >> 1)] = fmaxf(most[2 * mt + (y >> 1)], x);
-                            if (seg < r.i1 && token < r.m) scores[(size_t)seg * a.Tp + token] = x;
-                        }
-                    }
+                    for (int y = 0; y < 16; ++y)
+                        if (t0 + y < nodes) out[(size_t)(t0 + y) * D + row] = x[y];
                 }
-                if (!ok) break;
-#pragma unroll
-                for (int x = 0; x < 2 * (kMaxTree / 16); ++x) {
-                    most[x] = fmaxf(most[x], __shfl_xor_sync(0xffffffffu, most[x], 1));
-                    most[x] = fmaxf(most[x], __shfl_xor_sync(0xffffffffu, most[x], 2));
-                    if (c4 == 0) top[warp][16 * (x / 2) + 8 * (x & 1) + g] = most[x];
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&scored);
-                if (!(ok = mbar_wait(&scored, scorings & 1, &abort_flag))) break;
-                if (in) {
-                    best = -FLT_MAX;  // (no segment of the run may have a page)
-#pragma unroll
-                    for (int x = 0; x < kWorkers; ++x) best = fmaxf(best, top[x][t]);
-                }
-                ++scorings;
-                // the next head's mean keys and router inputs, as far as L2
-                Runs then = runs;
-                Run x;
-                while (then.next(a, line, x))
-                    if (x.kind == kCached) {
-                        const int32_t *pages_of = c.table + (size_t)x.row * c.nmax;
-                        const char *inputs = reinterpret_cast<const char *>(static_cast<const __nv_bfloat16 *>(a.u) + (size_t)x.bh * a.T * D);
-                        for (int y = tid; y < x.m * D / 64; y += 32 * kWorkers)
-                            asm volatile("prefetch.global.L2 [%0];" ::"l"(inputs + 128 * y));
-                        for (int y = tid; y < (x.i1 - x.i0) * (D / 32); y += 32 * kWorkers) {
-                            const int p = valid_page(c, pages_of[x.i0 + y / (D / 32)]);
-                            if (p >= 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(c.kbar + ((size_t)p * c.H + x.h) * D + y % (D / 32) * 32));
-                        }
-                        break;
-                    }
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&d_empty[i & 1]);
+            return true;
+        };
+        while (ok && runs.next(a, line, r)) {
+            const float *scores = a.gates + (size_t)r.bh * c.nmax * a.Tp;
+            const bool in = writes && t < r.m, cached = r.kind == kCached;
+            const float best = cached && in && routed ? a.top[(size_t)r.bh * a.Tp + t] : 0.f;
             uint32_t q[16];
             if (in) {
                 const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(r.kind == kBegunK ? a.k : a.q) +
@@ -448,6 +461,7 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
             }
             if (n == 0) let_next_start();
             float z = 0.f;
+            bool brought = false;
             if (writes) {
                 const int32_t *table = c.table + (size_t)r.row * c.nmax;
                 // the weight's logarithm: a score; 0 for a page where nothing is scored
@@ -456,14 +470,22 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
                     if (!cached) return 0.f;
                     return routed ? scores[(size_t)i * a.Tp + t] : valid_page(c, table[i]) >= 0 ? 0.f : __int_as_float(0xff800000);
                 };
-                float next = load(r.i0);
-                for (int i = r.i0; i < r.i1; ++i, ++u) {
-                    const float g = expf(next - best);
-                    next = load(i + 1);
-                    z += g;
+                float ahead[2 * BATCH];  // scores come from L2, whose latency is some memories' time
+#pragma unroll
+                for (int x = 0; x < 2 * BATCH; ++x) ahead[x] = load(r.i0 + x);
+                for (int i = r.i0; i < r.i1; i += BATCH, ++u) {
+                    float g = 0.f;
+#pragma unroll
+                    for (int y = 0; y < BATCH; ++y) {
+                        const float w = i + y < r.i1 ? expf(ahead[y] - best) : 0.f;
+                        z += w;
+                        if (y == sub) g = w;
+                        ahead[y] = ahead[y + BATCH];
+                        ahead[y + BATCH] = load(i + y + 2 * BATCH);
+                    }
                     if (!(ok = mbar_wait(&b_empty[u & 1], ((u >> 1) & 1) ^ 1, &abort_flag))) break;
-                    uint8_t *row = bs + (u & 1) * kBSlot + panel * NT * 128 + t * 128;
-                    if (t < NT) {
+                    uint8_t *row = bs + (u & 1) * kBSlot + (sub * PANELS + panel) * NT * 128 + t * 128;
+                    if (t < NT && i + sub < r.i1) {
 #pragma unroll
                         for (int x = 0; x < 8; ++x) {
                             float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -479,31 +501,21 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&b_full[u & 1]);
+                    if (i == r.i0 + BATCH && n > 0) {  // two slots ahead of the products
+                        if (!(ok = bring_out(n - 1))) break;
+                        brought = true;
+                    }
                 }
             }
+            if (ok && n > 0 && !brought) ok = bring_out(n - 1);
             if (!ok) break;
             const size_t part = (size_t)blockIdx.x + r.bh;
-            if (cached && in && panel == 0) a.weight[part * a.Tp + t] = make_float2(best, z);
-            if (!(ok = mbar_wait(&d_full[n & 1], (n >> 1) & 1, &abort_flag))) break;
-            tc_fence_after();
-            // rows 32 (warp % 4) + lane of D; the two warps of a quarter take every other 16 columns
-            const int quarter = warp % 4, row = 32 * quarter + lane;
-            float *out = cached ? a.part + part * a.Tp * D : (r.kind == kBegunQ ? a.Y0 : a.Z) + (size_t)r.bh * a.Tp * D;
-            for (int t0 = 16 * (warp / 4); t0 < NT; t0 += 32) {
-                float x[16];
-                tmem_ld16f(tmem_addr(tb + 64 * (n & 1), 32 * quarter, t0), x);
-                tmem_wait_ld();
-                if (row < D) {
-#pragma unroll
-                    for (int y = 0; y < 16; ++y)
-                        if (t0 + y < r.m) out[(size_t)(t0 + y) * D + row] = x[y];
-                }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&d_empty[n & 1]);
+            if (cached && in && panel == 0 && sub == 0) a.weight[part * a.Tp + t] = make_float2(best, z);
+            out = cached ? a.part + part * a.Tp * D : (r.kind == kBegunQ ? a.Y0 : a.Z) + (size_t)r.bh * a.Tp * D;
+            nodes = r.m;
             ++n;
         }
+        if (ok && n > 0) bring_out(n - 1);
     }
     tc_fence_before();
     __syncthreads();
@@ -512,6 +524,14 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
         tmem_dealloc(tb, 128);
     }
     if (tid == 0 && abort_flag) atomicExch(&g_tree_abort, 1);
+}
+
+template <int D>
+cudaError_t scores_impl(const TreeArgs &a, cudaStream_t s)
+{
+    const int spans = (a.T + kSpan - 1) / kSpan;
+    cudaError_t e = cudaFuncSetAttribute(tree_scores_tc<D>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    return e == cudaSuccess ? launch_early(tree_scores_tc<D>, (size_t)a.B * a.c.H * spans, 256, 0, s, a, spans) : e;
 }
 
 template <int D>
@@ -545,7 +565,12 @@ bool make_map(CUtensorMap *map, const float *base, unsigned long long matrices, 
 bool tree_tc_supported(const TreeArgs &a)
 {
     // every page and row of a head as a coordinate, and one past them
-    return a.bf16 && (a.c.d == 64 || a.c.d == 128) && a.T > 8 && a.mode != MC_SSC && (long long)a.c.P * a.c.H < (1ll << 31) - 1;
+    return a.bf16 && (a.c.d == 64 || a.c.d == 128) && a.mode != MC_SSC && (long long)a.c.P * a.c.H < (1ll << 31) - 1;
+}
+
+cudaError_t launch_tree_scores_tc(const TreeArgs &a, cudaStream_t s)
+{
+    return a.c.d == 128 ? scores_impl<128>(a, s) : scores_impl<64>(a, s);
 }
 
 cudaError_t launch_tree_path_tc(const TreeArgs &a, cudaStream_t s)

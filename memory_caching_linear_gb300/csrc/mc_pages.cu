@@ -122,10 +122,18 @@ int run_batch(const mc_paged_cache *cache, TreeArgs a, Call call, int agg_mode, 
         profile_after_kernel(s, "step_paged");
         return e == cudaSuccess ? MC_OK : fail(e);
     }
+    if (call == kTree && tree_whole(a)) {
+        a.whole = true;
+        profile_call_start(s);
+        const cudaError_t e = launch_tree_gates(a, s);
+        profile_after_kernel(s, "tree_whole");
+        return e == cudaSuccess ? MC_OK : fail(e);
+    }
     const size_t BH = (size_t)a.B * c.H, T = a.T, B = a.B;
     a.Tp = (a.T + 7) / 8 * 8;
     a.groups = a.Tp / 8;
     const bool split = tree_tc_supported(a);
+    a.scored = split && routed;
     a.ranges = split ? kSms : std::max(1, 4 * kSms / a.groups);
     void *scratch = nullptr;
     for (int pass = 0; pass < 2; ++pass) {
@@ -142,6 +150,7 @@ int run_batch(const mc_paged_cache *cache, TreeArgs a, Call call, int agg_mode, 
             a.gates = cv.take<float>(BH * (c.nmax + 2) * a.Tp);
             a.Z = cv.take<float>(a.delta ? BH * a.Tp * c.d : 0);
             if (split) {
+                a.top = cv.take<float>(BH * a.Tp);
                 a.Y0 = cv.take<float>(BH * a.Tp * c.d);
                 a.score = cv.take<float>(BH * path_segments(a) * a.Tp);
                 a.into = cv.take<float>(BH * a.Tp);
@@ -166,7 +175,9 @@ int run_batch(const mc_paged_cache *cache, TreeArgs a, Call call, int agg_mode, 
         if (e == cudaSuccess) e = launch_accept(a, s);
         profile_after_kernel(s, "accept_rows");
     } else {
-        e = split ? launch_tree_read_tc(a, s) : launch_tree_gates(a, s);
+        e = a.scored ? launch_tree_scores_tc(a, s) : cudaSuccess;
+        if (a.scored) profile_after_kernel(s, "tree_scores_tc");
+        if (e == cudaSuccess) e = split ? launch_tree_read_tc(a, s) : launch_tree_gates(a, s);
         profile_after_kernel(s, split ? "tree_read_tc" : "tree_gates");
         if (e == cudaSuccess) e = split ? launch_tree_path_tc(a, s) : launch_tree_read(a, s);
         profile_after_kernel(s, split ? "tree_path_tc" : "tree_read");

@@ -45,12 +45,13 @@ struct TreeArgs {
     const int32_t *slots;                 // [B], or null (batch row b is slot b)
     const int32_t *last;                  // [B] accept: the last node of the path
     void *y;                              // [B][H][T][d]
-    // Scratch.  In what follows a split read is one whose cached memories are weighed as they are read, each range of them
-    // against its own largest score (k_tree_tc.cu); otherwise the gates are worked out first (k_tree.cu).
+    // Scratch.  In what follows a split read is one whose cached memories are weighed as they are read, without what the path
+    // adds to the softmax (k_tree_tc.cu); otherwise the gates are worked out first (k_tree.cu).
     int32_t *line;                        // the batch's seats (Line)
     float *gates;                         // [BH][nmax + 2][Tp] gates of the cached memories, then what nodes read of the begun
-                                          // segment's with their queries (gate and decay) and with their keys (decay); a split
-                                          // read's scores
+                                          // segment's with their queries (gate and decay) and with their keys (decay); split:
+                                          // [BH][nmax][Tp] scores
+    float *top;                           // [BH][Tp] split: the largest of a node's
     float *P, *A;                         // [BH][T][Tp] per ancestor: what nodes read of what it wrote (a split read's without
                                           // the gates); what it meets in their keys
     float *score;                         // [BH][path_segments()][Tp] split: nodes' scores of their paths' segments
@@ -60,10 +61,11 @@ struct TreeArgs {
     float *Y0, *Z;                        // [BH][Tp][d] the begun segment's memory read with the nodes' queries (split, without gate
                                           // and decay) and with their keys (decayed; split: without)
     float *part;                          // [ranges + BH][Tp][d] partial reads
-    float2 *weight;                       // [ranges + BH][Tp] split: their largest score and sum of exp(score - largest)
+    float2 *weight;                       // [ranges + BH][Tp] split: top, or 0 without a router, and the sum of exp(score - top)
     int B, T, Tp, mode, topk;
     int ranges, groups;                   // shares of the memories; of the tokens
-    bool bf16, delta;
+    bool scored;                          // split: tree_scores_tc comes first
+    bool bf16, delta, whole;              // whole: tree_gates does all (a tree of up to 8 nodes over few heads)
 };
 
 // The U memories that a call reads are cut into R = ranges_of(U) ranges, none of them empty: memory x is in range
@@ -241,9 +243,11 @@ __device__ __forceinline__ void sum_groups(float (&p)[N], int lane)
 }
 
 cudaError_t launch_plan(const TreeArgs &a, cudaStream_t s);
+bool tree_whole(const TreeArgs &a);
 cudaError_t launch_tree_gates(const TreeArgs &a, cudaStream_t s);
 cudaError_t launch_tree_read(const TreeArgs &a, cudaStream_t s);
 bool tree_tc_supported(const TreeArgs &a);  // the split read on the tensor cores
+cudaError_t launch_tree_scores_tc(const TreeArgs &a, cudaStream_t s);
 cudaError_t launch_tree_path_tc(const TreeArgs &a, cudaStream_t s);
 cudaError_t launch_tree_read_tc(const TreeArgs &a, cudaStream_t s);
 cudaError_t take_tree_abort(int *was_set);
