@@ -13,6 +13,7 @@
 #include <cfloat>
 #include <cstdint>
 
+#include "mma_sync.cuh"
 #include "paged.cuh"
 #include "tree_nodes.cuh"
 
@@ -411,6 +412,7 @@ __global__ void __launch_bounds__(256, 3) tree_finish(TreeArgs a, int segments)
     float *ws = As + (a.delta ? a.T * a.Tp : 0);     // SPLIT: [segment][Tp] path weights; a path has path_segments() of them
     __shared__ float es[kMaxTree][32 * R];
     __shared__ uint64_t anc[kMaxTree];
+    __shared__ uint64_t seg_set[kMaxTree];
     __shared__ int seg[kMaxTree];
     __shared__ float share[kPartsAtOnce][kMaxTree], into[kMaxTree], first[kMaxTree], tops[kMaxTree], invs[kMaxTree];
     const size_t at = (size_t)bh * a.T;
@@ -430,12 +432,14 @@ __global__ void __launch_bounds__(256, 3) tree_finish(TreeArgs a, int segments)
             y[x][r] = in && SPLIT ? a.Y0[there] : 0.f;
         }
     for (int i = tid; i < a.T * a.Tp / 4; i += blockDim.x) {
-        const float4 p = reinterpret_cast<const float4 *>(a.P + at * a.Tp)[i];
-        const float4 q = a.delta ? reinterpret_cast<const float4 *>(a.A + at * a.Tp)[i] : p;
-        reinterpret_cast<float4 *>(Ps)[i] = p;
-        if (a.delta) reinterpret_cast<float4 *>(As)[i] = q;
+        mma::cp16(mma::smem_addr(Ps + 4 * i), a.P + at * a.Tp + 4 * i, true);
+        if (a.delta) mma::cp16(mma::smem_addr(As + 4 * i), a.A + at * a.Tp + 4 * i, true);
     }
-    if (where < 0 || m == 0) return;
+    mma::cp_commit();
+    if (where < 0 || m == 0) {
+        mma::cp_wait<0>();
+        return;
+    }
     const int nb = cached_segments(c, pos), in0 = pos % c.C;
     const Parts parts(a, line, b, h, SPLIT ? nb : nb + (in0 ? 1 : 0));
     float p[kPartsAtOnce][8][R];  // partial reads: the next ones, under way
@@ -488,11 +492,12 @@ __global__ void __launch_bounds__(256, 3) tree_finish(TreeArgs a, int segments)
             anc[n] = 0;
         }
     }
+    mma::cp_wait<0>();
     __syncthreads();
-    if (SPLIT) {
-        for (int j = warp; j < m; j += (int)blockDim.x / 32)
-            for (int n = lane; n < a.Tp; n += 32)
-                if ((anc[n] >> j) & 1) Ps[j * a.Tp + n] *= ws[seg[j] * a.Tp + n];
+    if (SPLIT) {  // the path segments' nodes
+        if (tid < segments) seg_set[tid] = 0;
+        __syncthreads();
+        if (tid < m) atomicOr(reinterpret_cast<unsigned *>(&seg_set[seg[tid]]) + tid / 32, 1u << (tid % 32));
     }
     uint64_t above = 0;  // ancestors of any of the warp's nodes
 #pragma unroll
@@ -584,13 +589,30 @@ __global__ void __launch_bounds__(256, 3) tree_finish(TreeArgs a, int segments)
         __syncthreads();
     }
     if (mine) {
+        auto read = [&](uint64_t of, float (&to)[8][R]) {
 #pragma unroll 4
-        for (int j = 0; j < min(n0 + 8, m); ++j) {
-            if (!((above >> j) & 1)) continue;
-            float ej[R];
+            for (int j = 0; j < min(n0 + 8, m); ++j) {
+                if (!((of >> j) & 1)) continue;
+                float ej[R];
 #pragma unroll
-            for (int r = 0; r < R; ++r) ej[r] = es[j][lane + 32 * r];
-            take(Ps, 1.f, j, ej, y);
+                for (int r = 0; r < R; ++r) ej[r] = es[j][lane + 32 * r];
+                take(Ps, 1.f, j, ej, to);
+            }
+        };
+        if (!SPLIT) {
+            read(above, y);
+        } else {
+            for (int k = 0; k < segments; ++k) {
+                const uint64_t of = above & seg_set[k];
+                if (!of) continue;
+                float part[8][R] = {};
+                read(of, part);
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        if (n0 + x < m && seg[n0 + x] >= k) y[x][r] = fmaf(ws[k * a.Tp + n0 + x], part[x][r], y[x][r]);
+            }
         }
     }
     if (lane < RB) {
