@@ -133,6 +133,17 @@ __global__ void __launch_bounds__(kThreads, 1) step_paged(TreeArgs a, StepWork w
     const bool routed = a.mode == MC_GRM || a.mode == MC_SSC, sparse = a.mode == MC_SSC;
 
     if (warp == kWorkers) {
+        if (lane > 0 && routed) {  // the range's mean keys, as far as L2: scores are wanted at once where a head begins
+            int b = 0;
+            for (long long x = begin + lane - 1; x < end; x += 31) {
+                while (x >= (long long)line.units[b + 1] * c.H) ++b;
+                const int nu = line.units[b + 1] - line.units[b];
+                const int in_b = (int)(x - (long long)line.units[b] * c.H), h = in_b / nu, i = in_b % nu;
+                const int p = i < nu - 1 ? valid_page(c, c.table[(size_t)line.row[b] * c.nmax + i]) : -1;
+                if (p >= 0)
+                    for (int y = 0; y < D * 4; y += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(c.kbar + ((size_t)p * c.H + h) * D + y / 4));
+            }
+        }
         if (lane == 0) {
             uint32_t g = 0, picks = 0;
             bool ok = true;
@@ -140,8 +151,8 @@ __global__ void __launch_bounds__(kThreads, 1) step_paged(TreeArgs a, StepWork w
             for (long long x = begin; ok && x < end;) {
                 while (x >= (long long)line.units[b + 1] * c.H) ++b;
                 const int nu = line.units[b + 1] - line.units[b], nb = nu - 1, row = line.row[b], in0 = line.pos[b] % c.C;
-                const long long in_b = x - (long long)line.units[b] * c.H;
-                const int h = (int)(in_b / nu), i0 = (int)(in_b % nu), i1 = (int)(end - x < nu - i0 ? i0 + (end - x) : nu);
+                const int in_b = (int)(x - (long long)line.units[b] * c.H);
+                const int h = in_b / nu, i0 = in_b % nu, i1 = (int)(end - x < nu - i0 ? i0 + (end - x) : nu);
                 x += i1 - i0;
                 if (sparse && i0 < nb) {  // which of them the router keeps
                     if (!(ok = mbar_wait(&chosen, picks & 1, &abort_flag))) break;
@@ -193,8 +204,8 @@ __global__ void __launch_bounds__(kThreads, 1) step_paged(TreeArgs a, StepWork w
     for (long long x = begin; ok && x < end;) {
         while (x >= (long long)line.units[b + 1] * c.H) ++b;
         const int nu = line.units[b + 1] - line.units[b], nb = nu - 1, row = line.row[b], pos = line.pos[b], in0 = pos % c.C;
-        const long long u0 = (long long)line.units[b] * c.H, in_b = x - u0;
-        const int h = (int)(in_b / nu), i0 = (int)(in_b % nu), i1 = (int)(end - x < nu - i0 ? i0 + (end - x) : nu);
+        const long long u0 = (long long)line.units[b] * c.H;
+        const int in_b = (int)(x - u0), h = in_b / nu, i0 = in_b % nu, i1 = (int)(end - x < nu - i0 ? i0 + (end - x) : nu);
         x += i1 - i0;
         const int bh = b * c.H + h, stop = min(i1, nb);
         const size_t at = (size_t)bh * D;
