@@ -128,8 +128,9 @@ __global__ void __launch_bounds__(kThreads, 1) step_paged(TreeArgs a, StepWork w
     after_previous();
     const Line line = make_line_once(a, space, taker, blockIdx.x == 0);
     const long long U = (long long)line.units[a.B] * c.H, R = ranges_of(U, a.ranges);
-    if (blockIdx.x >= R) return;
-    const long long begin = range_begin(blockIdx.x, U, R), end = range_begin(blockIdx.x + 1, U, R);
+    // a CTA without a range counts at the end too: it has read positions, from which all must work out the same line
+    const bool in = blockIdx.x < R;
+    const long long begin = in ? range_begin(blockIdx.x, U, R) : 0, end = in ? range_begin(blockIdx.x + 1, U, R) : 0;
     const bool routed = a.mode == MC_GRM || a.mode == MC_SSC, sparse = a.mode == MC_SSC;
 
     if (warp == kWorkers) {
@@ -423,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) step_paged(TreeArgs a, StepWork w
         __threadfence();
         ok = gather();
     }
-    if (ok && tid == 0) last = atomicAdd(work.turns + (size_t)c.S * c.H, 1) == (int)R - 1;
+    if (ok && tid == 0) last = atomicAdd(work.turns + (size_t)c.S * c.H, 1) == (int)gridDim.x - 1;
     if (ok) ok = gather();
     if (ok && last) {
         __threadfence();

@@ -510,3 +510,122 @@ def test_many_sequences():
     mcl.mc_pages_fork(cache, i32(src))
     ref.fork(src)
     same(cache, ref)
+
+
+# n_max so large that a draft of few nodes takes more than one launch (the capacity says so, not what is cached): every kernel
+# for 1, 2, 4 and 8 nodes
+@pytest.mark.parametrize("mode,topk", [(GRM, 0), (SSC, 2), (SOUP, 0), (MEAN, 0), (RESIDUAL, 0)])
+@pytest.mark.parametrize("T", [1, 2, 3, 8])
+@pytest.mark.parametrize("d,H,n_max,dtype", [(16, 44, 1000, torch.float32), (32, 22, 512, torch.bfloat16), (64, 12, 250, torch.bfloat16),
+                                             (128, 8, 90, torch.float32), (128, 7, 100, torch.bfloat16)])
+def test_few_nodes_over_much_room(d, H, n_max, dtype, T, mode, topk):
+    gen, rng = seeded(d + T)
+    ref = Ref(2, H, d, 3, n_max, 16).fill([9, 4], [1, 0], gen, rng)
+    x = tokens(gen, 2, H, T, d, dtype)
+    if (T + mode) % 2:
+        x[4] = x[5] = None
+    cache = on_gpu(ref)
+    run_tree(cache, ref, x, draft(rng, 2, T, "tree"), [T, max(T - 1, 1)], [1, 0], mode, topk, dtype)
+
+
+@pytest.mark.parametrize("mode,topk", [(GRM, 0), (SSC, 2)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_steps_read_nothing_else(dtype, mode, topk):
+    """A step with NaN in free pages, in rows to pad with, in begun segments that nothing has entered; a segment without a page and
+    one whose page does not exist; inputs that are parts of larger tensors."""
+    gen, rng = seeded(31)
+    H, d, C, nan = 2, 64, 4, float("nan")
+    ref = Ref(4, H, d, C, 8, 24).fill([5, 3, 2, 4], [0, 3, 1, 3], gen, rng)
+    ref.table[1][0] = ref.table[3][2] = -1
+    x = [z[:, :, 0].contiguous() for z in tokens(gen, 4, H, 1, d, dtype)]
+    cache = on_gpu(ref)
+    cache.table[1, 0] = 24  # past the pool: not followed
+    free = [p for p in range(24) if ref.refs[p] == 0]
+    cache.pages[free], cache.kbar[free] = nan, nan
+    cache.online[0], cache.ksum[0] = nan, nan
+    wide = [torch.full((6, *z.shape[1:]), nan, dtype=dtype, device="cuda") for z in x]
+    for w, z in zip(wide, x):
+        w[1:4] = z[:3].cuda()
+    part = [w[1:5] for w in wide]  # the fourth row is NaN and nobody's
+    y = torch.full((4, H, d), 7.0, dtype=dtype, device="cuda")
+    slots = torch.tensor([9, 3, 0, 1, -1], dtype=torch.int32, device="cuda")[1:]
+    mcl.mc_decode_step_paged(cache, *part[:4], mode, topk, log_alpha=part[4], beta=part[5], slots=slots, y=y)
+    want = ref.step(*x, [3, 0, 1, -1], mode, topk)
+    for b in range(3):
+        near(y[b], want[b], TOL[dtype])
+    assert (y[3] == 7).all() and cache.pos.tolist() == ref.pos and cache.refs.tolist() == ref.refs
+    for b, i in ((3, 4), (1, 3)):  # the segments that the call completed
+        p = cache.table[b, i].item()
+        assert p == ref.table[b][i]
+        near(cache.pages[p].double().cpu(), ref.pages[p], 1e-4)
+        near(cache.kbar[p].double().cpu(), ref.kbar[p], 1e-4)
+
+
+def test_steps_beside_other_work():
+    """Small steps while another stream keeps the GPU busy, so that CTAs of one call come up at unlike times; every token completes
+    a segment, which changes how many of them have work."""
+    gen, rng = seeded(13)
+    H, d, C = 2, 32, 1
+    ref = Ref(3, H, d, C, 40, 130).fill([0, 2, 1], [0, 0, 0], gen, rng)
+    cache = on_gpu(ref)
+    xs = [[z[:, :, 0].contiguous() for z in tokens(gen, 3, H, 1, d, torch.float32)] for _ in range(30)]
+    on = [[gpu(z) for z in x] for x in xs]
+    side = torch.cuda.Stream()
+    m = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(30):
+            m = torch.relu(m + 1.0) * 0.5
+            m = (m @ m) * 1e-5
+    ys = [mcl.mc_decode_step_paged(cache, *x[:4], GRM, log_alpha=x[4], beta=x[5]) for x in on]
+    torch.cuda.synchronize()
+    for x, y in zip(xs, ys):
+        want = ref.step(*x, None, GRM, 0)
+        near(y, torch.stack([want[b] for b in range(3)]), 1e-4)
+    same(cache, ref)
+
+
+def test_a_given_stream_and_two_graphs():
+    """Calls on a stream given by name, and graphs of two caches replayed at once: neither touches the other's work."""
+    ref, x, parent = pair(5)
+    tok = [t[:, :, 0].contiguous() for t in x]
+    a, b, c = on_gpu(ref), on_gpu(ref), on_gpu(ref)
+    last = i32([4, 3, 2])
+    everything = lambda k, **s: (  # noqa: E731
+        mcl.mc_decode_tree(k, *x[:4], parent, GRM, log_alpha=x[4], beta=x[5], **s),
+        mcl.mc_tree_accept(k, x[1], x[2], parent, last, log_alpha=x[4], beta=x[5], **s),
+        mcl.mc_decode_step_paged(k, *tok[:4], GRM, log_alpha=tok[4], beta=tok[5], **s),
+        mcl.mc_pages_fork(k, src, **s))
+    src = i32([1, 2, 0])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    want = [everything(a) for _ in range(3)]
+    torch.cuda.synchronize()
+    got = [everything(c, stream=side) for _ in range(3)]
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert torch.equal(w[0], g[0]) and torch.equal(w[2], g[2])
+    same_bits = lambda p, q: all(torch.equal(getattr(p, n), getattr(q, n)) for n in FLOATS + INTS)  # noqa: E731
+    assert same_bits(a, c) and a.status.item() == 0
+    d = on_gpu(ref)
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for k in (b, d):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            t = mcl.mc_decode_tree(k, *x[:4], parent, GRM, log_alpha=x[4], beta=x[5])
+            mcl.mc_tree_accept(k, x[1], x[2], parent, last, log_alpha=x[4], beta=x[5])
+            z = mcl.mc_decode_step_paged(k, *tok[:4], GRM, log_alpha=tok[4], beta=tok[5])
+            mcl.mc_pages_fork(k, src)
+        graphs.append(g)
+        outs.append((t, z))
+    streams = [torch.cuda.Stream() for _ in graphs]
+    torch.cuda.synchronize()
+    for w in want:
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for t, z in outs:
+            assert torch.equal(t, w[0]) and torch.equal(z, w[2])
+    assert same_bits(a, b) and same_bits(a, d)
