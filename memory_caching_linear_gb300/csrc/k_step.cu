@@ -3,7 +3,9 @@
 //
 // As in a tree's split read (k_tree_tc.cu) the memories of all heads and sequences form one line that is cut evenly over the
 // SMs, each range weighing its cached memories against its own largest score, so sequences of unlike lengths keep every SM as
-// busy as any.  The online memory is the last of its head's: whoever has it updates it (e = v - a M k, M <- a M + beta e k^T),
+// busy as any.  The end of a head -- its online memory, and the scores of the next one -- takes as long as 1024 / d memories
+// (512 KB at d = 128), and has that much room in the line, or the ranges with most ends would run on alone: 16 heads of
+// d = 128, 16 sequences of 2 to 63 segments 120 -> 88 us, 32 of up to 10 93 -> 55.  The online memory is the last of its head's: whoever has it updates it (e = v - a M k, M <- a M + beta e k^T),
 // writes it, and reads it.  Nothing waits for another CTA: the last one to come to a head's end joins the partial reads, in
 // their order, and the last one of all moves positions on and gives out pages (a CTA that needs to know its page before
 // looks it up as the last one will).
@@ -30,6 +32,7 @@ constexpr int kWorkers = 8, kThreads = 32 * (kWorkers + 1), kMaxStages = 24;
 template <int D>
 struct StepShape {
     static constexpr int BYTES = D * D * 4, STAGES = D == 128 ? 3 : D == 64 ? 12 : 24;
+    static constexpr int REST = 1024 / D;  // what a head's end costs, in memories
     static constexpr int LPR = D / 4, RPW = 32 / LPR, PASS = D / (kWorkers * RPW) < 1 ? 1 : D / (kWorkers * RPW);
 };
 // After the ring: seats (Line), slots' takers, and a head's scores and pages.
@@ -39,8 +42,9 @@ size_t step_smem(const TreeArgs &a)
     return 128 + (size_t)StepShape<D>::STAGES * StepShape<D>::BYTES + sizeof(int) * (Line::ints(a.B) + a.c.S + 2 * (size_t)a.c.nmax);
 }
 
-// The seats of a call that writes: a slot that several batch rows name is the first one's.
-__device__ Line make_line_once(const TreeArgs &a, int *space, int *taker, bool tell)
+// The seats of a call that writes: a slot that several batch rows name is the first one's.  Where there is a memory for every
+// range, `rest` more, which nobody reads, come after those of a head.
+__device__ Line make_line_once(const TreeArgs &a, int *space, int *taker, int rest, bool tell)
 {
     const Paged &c = a.c;
     const Line l = line_in(space, a.B);
@@ -59,9 +63,17 @@ __device__ Line make_line_once(const TreeArgs &a, int *space, int *taker, bool t
             l.row[b] = -1;
             if (tell) atomicOr(c.status, MC_PAGES_INDEX);
         }
-        l.units[b + 1] = l.row[b] >= 0 ? cached_segments(c, l.pos[b]) + 1 : 0;
+        l.units[b + 1] = l.row[b] >= 0 ? cached_segments(c, l.pos[b]) + 1 + (1 << 21) : 0;  // (their number above the sum)
     }
     sum_line(a, l);
+    const unsigned mask = (1u << 21) - 1, total = (unsigned)l.units[a.B] & mask;
+    const unsigned more = (long long)total * c.H >= a.ranges ? rest : 0;
+    __syncthreads();
+    for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
+        const unsigned x = (unsigned)l.units[b + 1];
+        l.units[b + 1] = (int)((x & mask) + more * (x >> 21));
+    }
+    __syncthreads();
     return l;
 }
 
@@ -126,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1) step_paged(TreeArgs a, StepWork w
         fence_mbar_init();
     }
     after_previous();
-    const Line line = make_line_once(a, space, taker, blockIdx.x == 0);
+    const Line line = make_line_once(a, space, taker, S::REST, blockIdx.x == 0);
     const long long U = (long long)line.units[a.B] * c.H, R = ranges_of(U, a.ranges);
     // a CTA without a range counts at the end too: it has read positions, from which all must work out the same line
     const bool in = blockIdx.x < R;
@@ -140,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1) step_paged(TreeArgs a, StepWork w
                 while (x >= (long long)line.units[b + 1] * c.H) ++b;
                 const int nu = line.units[b + 1] - line.units[b];
                 const int in_b = (int)(x - (long long)line.units[b] * c.H), h = in_b / nu, i = in_b % nu;
-                const int p = i < nu - 1 ? valid_page(c, c.table[(size_t)line.row[b] * c.nmax + i]) : -1;
+                const int p = i < cached_segments(c, line.pos[b]) ? valid_page(c, c.table[(size_t)line.row[b] * c.nmax + i]) : -1;
                 if (p >= 0)
                     for (int y = 0; y < D * 4; y += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(c.kbar + ((size_t)p * c.H + h) * D + y / 4));
             }
@@ -151,10 +163,11 @@ __global__ void __launch_bounds__(kThreads, 1) step_paged(TreeArgs a, StepWork w
             int b = 0;
             for (long long x = begin; ok && x < end;) {
                 while (x >= (long long)line.units[b + 1] * c.H) ++b;
-                const int nu = line.units[b + 1] - line.units[b], nb = nu - 1, row = line.row[b], in0 = line.pos[b] % c.C;
+                const int nu = line.units[b + 1] - line.units[b], nb = cached_segments(c, line.pos[b]), row = line.row[b], in0 = line.pos[b] % c.C;
                 const int in_b = (int)(x - (long long)line.units[b] * c.H);
-                const int h = in_b / nu, i0 = in_b % nu, i1 = (int)(end - x < nu - i0 ? i0 + (end - x) : nu);
-                x += i1 - i0;
+                const int h = in_b / nu, i0 = in_b % nu, i1 = min((int)(end - x < nu - i0 ? i0 + (end - x) : nu), nb + 1);
+                x += (end - x < nu - i0 ? end - x : nu - i0);
+                if (i0 > nb) continue;
                 if (sparse && i0 < nb) {  // which of them the router keeps
                     if (!(ok = mbar_wait(&chosen, picks & 1, &abort_flag))) break;
                     ++picks;
@@ -204,10 +217,11 @@ __global__ void __launch_bounds__(kThreads, 1) step_paged(TreeArgs a, StepWork w
     int b = 0;
     for (long long x = begin; ok && x < end;) {
         while (x >= (long long)line.units[b + 1] * c.H) ++b;
-        const int nu = line.units[b + 1] - line.units[b], nb = nu - 1, row = line.row[b], pos = line.pos[b], in0 = pos % c.C;
+        const int nu = line.units[b + 1] - line.units[b], row = line.row[b], pos = line.pos[b], nb = cached_segments(c, pos), in0 = pos % c.C;
         const long long u0 = (long long)line.units[b] * c.H;
-        const int in_b = (int)(x - u0), h = in_b / nu, i0 = in_b % nu, i1 = (int)(end - x < nu - i0 ? i0 + (end - x) : nu);
-        x += i1 - i0;
+        const int in_b = (int)(x - u0), h = in_b / nu, i0 = in_b % nu, i1 = min((int)(end - x < nu - i0 ? i0 + (end - x) : nu), nb + 1);
+        x += (end - x < nu - i0 ? end - x : nu - i0);
+        if (i0 > nb) continue;
         const int bh = b * c.H + h, stop = min(i1, nb);
         const size_t at = (size_t)bh * D;
         const float4 q = load4(static_cast<const E *>(a.q) + at + c0);
@@ -318,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) step_paged(TreeArgs a, StepWork w
                 part[D + 1] = z;
             }
         }
-        if (i1 == nu) {  // the online memory
+        if (i1 > nb) {  // the online memory
             const bool ends = in0 == c.C - 1;
             const float4 k = load4(static_cast<const E *>(a.k) + at + c0);
             if (ends && warp == 0) {  // the page that the last CTA will give this row
@@ -386,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) step_paged(TreeArgs a, StepWork w
         }
         // the head's last CTA joins what all of them left
         const long long head0 = u0 + (long long)h * nu;
-        const int j0 = range_of(head0, U, R), j1 = range_of(head0 + nu - 1, U, R);
+        const int j0 = range_of(head0, U, R), j1 = range_of(head0 + nb, U, R);
         bool joins = j0 == j1;
         if (!joins) {
             __threadfence();
