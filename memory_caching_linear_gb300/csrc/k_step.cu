@@ -32,7 +32,6 @@ constexpr int kWorkers = 8, kThreads = 32 * (kWorkers + 1), kMaxStages = 24;
 template <int D>
 struct StepShape {
     static constexpr int BYTES = D * D * 4, STAGES = D == 128 ? 3 : D == 64 ? 12 : 24;
-    static constexpr int REST = 1024 / D;  // what a head's end costs, in memories
     static constexpr int LPR = D / 4, RPW = 32 / LPR, PASS = D / (kWorkers * RPW) < 1 ? 1 : D / (kWorkers * RPW);
 };
 // After the ring: seats (Line), slots' takers, and a head's scores and pages.
@@ -42,9 +41,8 @@ size_t step_smem(const TreeArgs &a)
     return 128 + (size_t)StepShape<D>::STAGES * StepShape<D>::BYTES + sizeof(int) * (Line::ints(a.B) + a.c.S + 2 * (size_t)a.c.nmax);
 }
 
-// The seats of a call that writes: a slot that several batch rows name is the first one's.  Where there is a memory for every
-// range, `rest` more, which nobody reads, come after those of a head.
-__device__ Line make_line_once(const TreeArgs &a, int *space, int *taker, int rest, bool tell)
+// The seats of a call that writes: a slot that several batch rows name is the first one's.
+__device__ Line make_line_once(const TreeArgs &a, int *space, int *taker, bool tell)
 {
     const Paged &c = a.c;
     const Line l = line_in(space, a.B);
@@ -63,17 +61,9 @@ __device__ Line make_line_once(const TreeArgs &a, int *space, int *taker, int re
             l.row[b] = -1;
             if (tell) atomicOr(c.status, MC_PAGES_INDEX);
         }
-        l.units[b + 1] = l.row[b] >= 0 ? cached_segments(c, l.pos[b]) + 1 + (1 << 21) : 0;  // (their number above the sum)
+        l.units[b + 1] = l.row[b] >= 0 ? cached_segments(c, l.pos[b]) + 1 : 0;
     }
     sum_line(a, l);
-    const unsigned mask = (1u << 21) - 1, total = (unsigned)l.units[a.B] & mask;
-    const unsigned more = (long long)total * c.H >= a.ranges ? rest : 0;
-    __syncthreads();
-    for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
-        const unsigned x = (unsigned)l.units[b + 1];
-        l.units[b + 1] = (int)((x & mask) + more * (x >> 21));
-    }
-    __syncthreads();
     return l;
 }
 
@@ -138,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1) step_paged(TreeArgs a, StepWork w
         fence_mbar_init();
     }
     after_previous();
-    const Line line = make_line_once(a, space, taker, S::REST, blockIdx.x == 0);
+    const Line line = make_line_once(a, space, taker, blockIdx.x == 0);
     const long long U = (long long)line.units[a.B] * c.H, R = ranges_of(U, a.ranges);
     // a CTA without a range counts at the end too: it has read positions, from which all must work out the same line
     const bool in = blockIdx.x < R;
@@ -474,8 +464,9 @@ __global__ void __launch_bounds__(kThreads, 1) step_paged(TreeArgs a, StepWork w
 }
 
 template <typename E, int D>
-cudaError_t step_impl(const TreeArgs &a, const StepWork &work, cudaStream_t s)
+cudaError_t step_impl(TreeArgs a, const StepWork &work, cudaStream_t s)
 {
+    a.rest = 1024 / D;
     return launch_early(step_paged<E, D>, (size_t)a.ranges, kThreads, step_smem<D>(a), s, a, work);
 }
 template <typename E>

@@ -326,9 +326,13 @@ __global__ void __launch_bounds__(256) tree_read(TreeArgs a)
         const int nu = line.units[b + 1] - line.units[b];
         const long long in_b = x - (long long)line.units[b] * c.H;
         const int bh = b * c.H + (int)(in_b / nu), h = (int)(in_b / nu), row = line.row[b], nb = cached_segments(c, line.pos[b]);
-        const int i0 = (int)(in_b % nu);
+        const int i0 = (int)(in_b % nu), all = units_of(a, line.pos[b]);
+        if (i0 >= all) {  // past what comes after a head's memories
+            x += nu - i0;
+            continue;
+        }
         const bool for_keys = i0 > nb;
-        const int stop = for_keys || nu <= nb + 1 ? nu : nb + 1;  // the keys' read is apart
+        const int stop = for_keys || all <= nb + 1 ? all : nb + 1;  // the keys' read is apart
         const int i1 = (int)(end - x < stop - i0 ? i0 + (end - x) : stop);
         x += i1 - i0;
         const int m = line.nodes[b];

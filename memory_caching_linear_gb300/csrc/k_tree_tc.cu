@@ -282,16 +282,23 @@ struct Runs {
     }
     __device__ bool next(const TreeArgs &a, const Line &l, Run &r)
     {
-        if (x >= end) return false;
-        while (x >= (long long)l.units[b + 1] * a.c.H) ++b;
-        const int u0 = l.units[b], nu = l.units[b + 1] - u0;
-        const long long in_b = x - (long long)u0 * a.c.H;
+        int nu, read;
+        long long in_b;
+        while (true) {
+            if (x >= end) return false;
+            while (x >= (long long)l.units[b + 1] * a.c.H) ++b;
+            nu = l.units[b + 1] - l.units[b];
+            in_b = x - (long long)l.units[b] * a.c.H;
+            r.i0 = (int)(in_b % nu);
+            read = units_of(a, l.pos[b]);
+            if (r.i0 < read) break;
+            x += nu - r.i0;  // past what comes after a head's memories
+        }
         r.h = (int)(in_b / nu);
         r.bh = b * a.c.H + r.h;
         r.row = l.row[b];
         r.nb = cached_segments(a.c, l.pos[b]);
         r.m = l.nodes[b];
-        r.i0 = (int)(in_b % nu);
         r.kind = r.i0 < r.nb ? kCached : r.i0 == r.nb ? kBegunQ : kBegunK;
         const int stop = r.kind == kCached ? r.nb : r.i0 + 1;
         const long long left = end - x;

@@ -64,6 +64,7 @@ struct TreeArgs {
     float2 *weight;                       // [ranges + BH][Tp] split: top, or 0 without a router, and the sum of exp(score - top)
     int B, T, Tp, mode, topk;
     int ranges, groups;                   // shares of the memories; of the tokens
+    int rest;                             // what a head's end costs, in memories (sum_line)
     bool scored;                          // split: tree_scores_tc comes first
     bool bf16, delta, whole;              // whole: tree_gates does all (a tree of up to 8 nodes over few heads)
 };
@@ -116,22 +117,31 @@ struct Line {
     __host__ __device__ static size_t ints(int B) { return 4 * (size_t)B + 1; }
 };
 __host__ __device__ inline Line line_in(int *space, int B) { return Line{space, space + B, space + 2 * B, space + 3 * B}; }
-// units[b + 1] are row b's own memories: makes them sums.  The whole block calls it.
+// units[b + 1] are row b's own memories: makes them sums.  Where there is a memory for every range, a.rest more, which nobody
+// reads, come after those of a head.  The whole block calls it.
 __device__ inline void sum_line(const TreeArgs &a, const Line &l)
 {
+    constexpr unsigned kSum = (1u << 21) - 1;  // rows with memories are counted above it
     __syncthreads();
     if (threadIdx.x < 32) {
-        int sum = 0;
+        unsigned sum = 0;
         for (int b0 = 0; b0 < a.B; b0 += 32) {
             const int b = b0 + (int)threadIdx.x;
-            int x = b < a.B ? l.units[b + 1] : 0;
+            unsigned x = b < a.B ? (unsigned)l.units[b + 1] : 0;
+            if (x) x += kSum + 1;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
                 if ((int)threadIdx.x >= o) x += y;
             }
-            if (b < a.B) l.units[b + 1] = sum + x;
+            if (b < a.B) l.units[b + 1] = (int)(sum + x);
             sum += __shfl_sync(0xffffffffu, x, 31);
+        }
+        const unsigned rest = (long long)(sum & kSum) * a.c.H >= a.ranges ? a.rest : 0;
+        __syncwarp();
+        for (int b = threadIdx.x; b < a.B; b += 32) {
+            const unsigned x = (unsigned)l.units[b + 1];
+            l.units[b + 1] = (int)((x & kSum) + rest * (x >> 21));
         }
         if (threadIdx.x == 0) l.units[0] = 0;
     }
