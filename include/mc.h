@@ -393,9 +393,9 @@ int mc_decode_step_paged(const mc_paged_cache *cache, const void *q, const void 
  *                     and their y stays as it is.  NULL: T.  Numbers outside 0 .. T are taken as the nearest in it.
  *   slots           : as above; a slot may come any number of times.
  *   T               : 1 .. 64.  Other arguments and errors as mc_decode_step_paged.
- * Accuracy as mc_decode_step: fp32 inputs 1e-4, bf16 ones 1e-2 of the largest value.  With bf16 inputs, d >= 64, T > 8 and no
- * SSC the cached memories are rounded to the tensor cores' 11 significant bits on the way (2^-11 of their values, against
- * the 2^-9 of y's own rounding).
+ * Accuracy as mc_decode_step: fp32 inputs 1e-4, bf16 ones 1e-2 of the largest value.  With bf16 inputs, d >= 64 and no SSC the
+ * memories in the cache are rounded to the tensor cores' 11 significant bits on the way (2^-11 of their values, against the
+ * 2^-9 of y's own rounding), unless T <= 8 and B H (n_max + 1) d^2 <= 10 * 2^20.
  */
 int mc_decode_tree(const mc_paged_cache *cache, const void *q, const void *k, const void *v, const void *u,
                    const void *log_alpha, const void *beta, const int32_t *parent, const int32_t *count,

@@ -173,6 +173,8 @@ __device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b)
 // the decays' product, its decay (M' takes s over when it falls below 2^-30).  What a token does to s, and where a segment
 // ends, is worked out once, ahead of the chain.
 // What the plan does not say -- tokens, where the memory lies -- is fetched while it is made.
+// 16 heads of d = 128, 16 sequences, 32 tokens, bf16: 33 us with the plan (gated delta; linear 24), of which a CTA's chain is 12,
+// 0.4 us a token; one user 16.  Four CTAs an SM at 128 registers instead of three at 161: 33, and 94 -> 100 at twice both.
 template <int D> struct AcceptShape {
     static constexpr int ROWS = D < 64 ? D : 64, LANES = D / 16, GROUPS = 32 / LANES, R = D == 16 ? 1 : D == 32 ? 2 : 4;
     static constexpr int PER_WARP = GROUPS * R, WARPS = ROWS < PER_WARP ? 1 : ROWS / PER_WARP;
@@ -356,6 +358,7 @@ __device__ __forceinline__ void copy_piece(float *to, const float *from, size_t 
 // else the lowest's); the other slots take the rows that nobody goes on from, in order.  So what is read is never written,
 // and only true copies move: a permutation of the slots moves nothing.  from [S]: the row to copy to to[S]; -1 none (the
 // slot is freed), -2 nothing to do.
+// Two launches and their chains of loads bound it: 8.5 us for four samples of one user, 11.4 for 28 copies of 1 MB.
 __global__ void __launch_bounds__(kPlanThreads) plan_fork(Paged c, const int32_t *src, int32_t *from, int32_t *to)
 {
     __shared__ int keeper[kMaxRows], rows[kMaxRows], spare[kMaxRows];
@@ -419,7 +422,8 @@ __global__ void __launch_bounds__(256) fork_rows(Paged c, const int32_t *from, c
 }
 
 // Compaction: the live pages of src, in order, to the first pages of dst.  from [dst.P]: the page of src that comes here;
-// map [src.P]: where a page goes, -1 if it is free or there is no room; live [1]: pages to move.
+// map [src.P]: where a page goes, -1 if it is free or there is no room; live [1]: pages to move.  HBM bounds it: 0.96 GB
+// read and written in 139 us, 6.9 TB/s; a small pool is two launches, 8 us.
 __global__ void __launch_bounds__(kPlanThreads) plan_compact(Paged dst, Paged src, int32_t *from, int32_t *map, int32_t *live)
 {
     int n = 0;

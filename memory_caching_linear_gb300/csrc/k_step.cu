@@ -12,7 +12,8 @@
 //
 // The memories, 4 d^2 bytes each, come by bulk copies through a ring of 192 KB (d >= 64) and are read from there, a lane
 // holding four columns of every row that it adds up.  HBM bounds a batch, a chain of loads (slot, row, position, page, mean
-// key, memory) and two rounds of counting a single user.
+// key, memory) and two rounds of counting a single user.  16 heads of d = 128, bf16, gated delta: 8 sequences of up to 63
+// segments 83 us a token (5.2 TB/s), one of 5 segments 12.5 and of 40 15.7.
 #include <cfloat>
 #include <cstdint>
 

@@ -15,6 +15,9 @@
 // The scores of the cached segments (tree_scores_tc) come first: the reads' CTAs come up beside them and fill their rings.
 // The path's own products (tree_path_tc) are a small kernel that comes up beside the reads once these are under way.
 // It needs nothing of them, but ends after them, so that what follows has both.
+//
+// 16 heads of d = 128, bf16: 12 sequences of up to 96 segments, 64 nodes, gated delta 189 us (scores 12, reads 155 at 6.2 TB/s,
+// path 51 beside them, finish 30); 8 of up to 63, 32 nodes, linear 98 (8, 78, 18, 14; cold, each alone).
 #include <cfloat>
 #include <cstdint>
 
