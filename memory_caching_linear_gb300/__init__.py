@@ -370,7 +370,8 @@ def _sequence_args(q, named, dims):
 
 
 def _new(t, name, dtype, shape, dev):
-    t = torch.empty(shape, dtype=dtype, device=dev) if t is None else t
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
     _check(t, name, dtype, shape, dev)
     return t
 
@@ -645,7 +646,7 @@ def _paged(cache, dev=None):
 
 
 def _paged_batch(cache, first, name, dims):
-    """The batch size of a call whose first token tensor is [B, H, (T,) d]; its checks."""
+    """Checks of a call's cache and of its first token tensor, [B, H, (T,) d]."""
     if not isinstance(first, torch.Tensor) or first.dim() != dims:
         raise ValueError(f"{name} must be [B, H, d]" if dims == 3 else f"{name} must be [B, H, T, d]")
     if first.device.type != "cuda":
@@ -662,15 +663,19 @@ def _paged_batch(cache, first, name, dims):
         raise ValueError("a draft has 1 .. 64 nodes")
 
 
-def _tokens_match(first, others, gates, indexes):
+def _tokens_match(tokens, u, log_alpha, beta, indexes):
+    """Checks of a call's tokens (name, tensor; the first gives shape and type), gates and index arrays (name, tensor, shape)."""
+    first = tokens[0][1]
     shape, dev, dtype = first.shape, first.device, first.dtype
-    for t, n in others:
-        if t is not None:
-            _check(t, n, dtype, shape, dev)
-    for t, n in gates:
-        if t is not None:
-            _check(t, n, dtype, shape[:-1], dev)
-    for t, n, want in indexes:
+    for n, t in tokens:
+        _check(t, n, dtype, shape, dev)
+    if u is not None:
+        _check(u, "u", dtype, shape, dev)
+    if log_alpha is not None:
+        _check(log_alpha, "log_alpha", dtype, shape[:-1], dev)
+    if beta is not None:
+        _check(beta, "beta", dtype, shape[:-1], dev)
+    for n, t, want in indexes:
         if t is not None:
             _check(t, n, torch.int32, want, dev)
 
@@ -682,8 +687,7 @@ def mc_decode_step_paged(cache: PagedCache, q, k, v, u, agg_mode: int, topk: int
     b).  Positions advance on the device, so the call may be captured and replayed.  Returns y [B, H, d]; rows of nobody stay
     as they are in a y that is given, and are anything in a new one."""
     _paged_batch(cache, q, "q", 3)
-    _tokens_match(q, ((q, "q"), (k, "k"), (v, "v"), (u, "u")), ((log_alpha, "log_alpha"), (beta, "beta")),
-                  ((slots, "slots", q.shape[:1]),))
+    _tokens_match((("q", q), ("k", k), ("v", v)), u, log_alpha, beta, (("slots", slots, q.shape[:1]),))
     y = _new(y, "y", q.dtype, q.shape, q.device)
     with _on(q.device):
         st = load_library().mc_decode_step_paged(
@@ -703,8 +707,8 @@ def mc_decode_tree(cache: PagedCache, q, k, v, u, parent, agg_mode: int, topk: i
     d]; what is beyond count, and rows of nobody, stay as they are in a y that is given, and are anything in a new one."""
     _paged_batch(cache, q, "q", 4)
     B, _, T, _ = q.shape
-    _tokens_match(q, ((q, "q"), (k, "k"), (v, "v"), (u, "u")), ((log_alpha, "log_alpha"), (beta, "beta")),
-                  ((parent, "parent", (B, T)), (count, "count", (B,)), (slots, "slots", (B,))))
+    _tokens_match((("q", q), ("k", k), ("v", v)), u, log_alpha, beta,
+                  (("parent", parent, (B, T)), ("count", count, (B,)), ("slots", slots, (B,))))
     y = _new(y, "y", q.dtype, q.shape, q.device)
     with _on(q.device):
         st = load_library().mc_decode_tree(
@@ -721,8 +725,8 @@ def mc_tree_accept(cache: PagedCache, k, v, parent, last, *, log_alpha=None, bet
     the other arguments as :func:`mc_decode_tree` was given them."""
     _paged_batch(cache, k, "k", 4)
     B, _, T, _ = k.shape
-    _tokens_match(k, ((k, "k"), (v, "v")), ((log_alpha, "log_alpha"), (beta, "beta")),
-                  ((parent, "parent", (B, T)), (last, "last", (B,)), (slots, "slots", (B,))))
+    _tokens_match((("k", k), ("v", v)), None, log_alpha, beta,
+                  (("parent", parent, (B, T)), ("last", last, (B,)), ("slots", slots, (B,))))
     with _on(k.device):
         st = load_library().mc_tree_accept(
             cache._ref, k.data_ptr(), v.data_ptr(), _ptr(log_alpha), _ptr(beta), _ptr(parent), _ptr(last), _ptr(slots), B, T,

@@ -483,6 +483,8 @@ __global__ void __launch_bounds__(256) compact_move(Paged dst, Paged src, const 
 // A prompt into a slot: its old pages go back, its complete segments get the lowest free ones.
 __global__ void __launch_bounds__(kPlanThreads) plan_load(Paged c, int slot, int L, int done, int32_t *list)
 {
+    after_previous();
+    let_next_start();
     const int row = c.row[slot];
     if ((unsigned)row >= (unsigned)c.S) {
         if (threadIdx.x == 0) {
@@ -513,18 +515,21 @@ __global__ void __launch_bounds__(256) load_segment(Paged c, const E *k, const f
 {
     constexpr int PARTS = 256 / (D / 4);
     const int n = (int)blockIdx.x / c.H, h = (int)blockIdx.x % c.H, N = (L + c.C - 1) / c.C;
+    after_previous();
     const bool tail = n == done;
     const int at = list[done] < 0 ? -1 : list[tail ? done : n];
     if (at < 0) return;
     const int len = min(c.C, L - n * c.C);  // 0: no segment is begun
     float *to = (tail ? c.online : c.pages) + ((size_t)at * c.H + h) * D * D;
     const float *from = states + ((size_t)h * N + n) * D * D;
+#pragma unroll 8
     for (int i = threadIdx.x; i < D * D / 4; i += 256)
         reinterpret_cast<float4 *>(to)[i] = len > 0 ? reinterpret_cast<const float4 *>(from)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
     __shared__ float4 sums[256];
     const int part = threadIdx.x / (D / 4), x = threadIdx.x % (D / 4);
     const E *kp = k + ((size_t)h * L + (size_t)n * c.C) * D + x * 4;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
     for (int t = part; t < len; t += PARTS) s = fma4(1.f, load4(kp + (size_t)t * D), s);
     sums[threadIdx.x] = s;
     __syncthreads();
@@ -560,12 +565,11 @@ cudaError_t load_impl(const Paged &c, const void *k, const float *states, int L,
     const unsigned ctas = (unsigned)((done + 1) * c.H);
     const E *kk = static_cast<const E *>(k);
     switch (c.d) {
-    case 16: load_segment<E, 16><<<ctas, 256, 0, s>>>(c, kk, states, L, done, list); break;
-    case 32: load_segment<E, 32><<<ctas, 256, 0, s>>>(c, kk, states, L, done, list); break;
-    case 64: load_segment<E, 64><<<ctas, 256, 0, s>>>(c, kk, states, L, done, list); break;
-    default: load_segment<E, 128><<<ctas, 256, 0, s>>>(c, kk, states, L, done, list); break;
+    case 16: return launch_early(load_segment<E, 16>, ctas, 256, 0, s, c, kk, states, L, done, list);
+    case 32: return launch_early(load_segment<E, 32>, ctas, 256, 0, s, c, kk, states, L, done, list);
+    case 64: return launch_early(load_segment<E, 64>, ctas, 256, 0, s, c, kk, states, L, done, list);
+    default: return launch_early(load_segment<E, 128>, ctas, 256, 0, s, c, kk, states, L, done, list);
     }
-    return cudaGetLastError();
 }
 
 unsigned copy_pieces(const Paged &c) { return (unsigned)(((size_t)c.H * c.d * c.d + kCopyFloats - 1) / kCopyFloats); }
@@ -604,8 +608,7 @@ cudaError_t launch_pages_compact(const Paged &dst, const Paged &src, int32_t *pl
 cudaError_t launch_pages_load(const Paged &c, int slot, const void *k, const float *states, int L, bool bf16, int32_t *plan,
                               cudaStream_t s)
 {
-    plan_load<<<1, kPlanThreads, 0, s>>>(c, slot, L, L / c.C, plan);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_early(plan_load, 1, kPlanThreads, 0, s, c, slot, L, L / c.C, plan);
     if (e != cudaSuccess) return e;
     return bf16 ? load_impl<__nv_bfloat16>(c, k, states, L, plan, s) : load_impl<float>(c, k, states, L, plan, s);
 }

@@ -629,3 +629,21 @@ def test_a_given_stream_and_two_graphs():
         for t, z in outs:
             assert torch.equal(t, w[0]) and torch.equal(z, w[2])
     assert same_bits(a, b) and same_bits(a, d)
+
+
+def test_tokens_that_are_missing_are_refused():
+    ref, x, parent = pair(4)
+    cache = on_gpu(ref)
+    tok = [t[:, :, 0].contiguous() for t in x]
+    for i in range(1, 3):
+        with pytest.raises(TypeError):
+            mcl.mc_decode_tree(cache, *(None if i == j else t for j, t in enumerate(x[:4])), parent, GRM)
+        with pytest.raises(TypeError):
+            mcl.mc_decode_step_paged(cache, *(None if i == j else t for j, t in enumerate(tok[:4])), GRM)
+    with pytest.raises(TypeError):
+        mcl.mc_tree_accept(cache, x[1], None, parent, i32([0, 0, 0]))
+    for call in (lambda: mcl.mc_tree_accept(cache, x[1], x[2], parent, None), lambda: mcl.mc_tree_accept(cache, x[1], x[2], None, i32([0, 0, 0])),
+                 lambda: mcl.mc_decode_tree(cache, *x[:4], None, GRM)):
+        with pytest.raises(mcl.MCError):
+            call()
+    same(cache, ref, 1e-7)
