@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(256) tree_scores_tc(TreeArgs a, int spans)
 // reads' ten warps and two of the path's eight.
 constexpr int kPathRegs = 96, kReadRegs = 104;
 
-// Scores of the path's segments, P without the gates, and A, for 32 nodes of a head at a time.  One CTA on an SM goes over its
+// Scores of the path's segments, P without the gates, and A, for 32 nodes of a head at a time.  A CTA goes over its
 // share of the heads: little enough in registers and shared memory to run beside a CTA of tree_read_tc.
 template <int D>
 __global__ void __maxnreg__(kPathRegs) tree_path_tc(TreeArgs a, int spans, int segments)
@@ -552,7 +552,11 @@ cudaError_t path_impl(const TreeArgs &a, cudaStream_t s)
     // the SM's shared memory is divided for the CTA of reads that comes beside this one
     cudaError_t e = cudaFuncSetAttribute(tree_path_tc<D>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
-    return launch_early(tree_path_tc<D>, (size_t)(items < a.ranges ? items : a.ranges) + 1, kPathThreads, sizeof(int) * Line::ints(a.B), s, a, spans,
+    // one CTA an SM beside the reads of many segments; where there is room for few, most of the path comes after them, and three
+    // fit: 16 heads of d = 128, gated delta, 64 nodes, 32 sequences of 5 to 10 segments 227 -> 198 us, 12 of up to 96 189 -> 206;
+    // of up to 16 nodes there is too little for that: d = 64, 32 sequences of up to 10 segments 48 -> 52
+    const long long most = (long long)a.ranges * (a.c.nmax <= 16 && a.T > 16 ? 3 : 1);
+    return launch_early(tree_path_tc<D>, (size_t)(items < most ? items : most) + 1, kPathThreads, sizeof(int) * Line::ints(a.B), s, a, spans,
                         path_segments(a));
 }
 
