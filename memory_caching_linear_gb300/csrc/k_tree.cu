@@ -13,7 +13,7 @@
 // them, and tree_finish last; a draft of up to 8 nodes over little room is tree_gates' alone (tree_whole).  The cached
 // memories' bytes, read once for all nodes, bound a batch, launches and chains of loads everything small.
 // On the CUDA cores (fp32, d < 64, SSC): 3 sequences, 6 heads of d = 64, 29 segments of 7, 13 nodes, SSC, fp32 31 us in three
-// launches; 8 sequences of 2 to 63 segments, 16 heads of d = 128, 8 nodes, fp32 97 us (29 of bytes), bound by products.
+// launches; 8 sequences of 2 to 63 segments, 16 heads of d = 128, 32 nodes, delta, fp32 234 us (30 of bytes), bound by products.
 #include <cfloat>
 #include <cstdint>
 
@@ -307,13 +307,16 @@ __global__ void __launch_bounds__(kGateThreads) tree_gates(TreeArgs a)
 // ------------------------------------------------------------------------------------------------ read
 
 // One memory after the other for up to 8 tokens on the CUDA cores.  A lane holds four columns of its rows and adds
-// M[r][c..] . (g q)[c..] over the memories of a head; the lanes are joined once per head.
+// M[r][c..] . (g q)[c..] over the memories of a head; the lanes are joined once per head.  Several CTAs share a range, each with
+// a part of a memory's rows (read_blocks).
 template <typename E, int D, int TG>
-__global__ void __launch_bounds__(256) tree_read(TreeArgs a)
+__global__ void __launch_bounds__(256, 2) tree_read(TreeArgs a)
 {
-    constexpr int LPR = D / 4, RPW = 32 / LPR, PASS = D / (8 * RPW) < 1 ? 1 : D / (8 * RPW);
+    constexpr int BLOCKS = read_blocks(D);
+    constexpr int LPR = D / 4, RPW = 32 / LPR, PASS = D / (8 * RPW * BLOCKS) < 1 ? 1 : D / (8 * RPW * BLOCKS);
     const Paged &c = a.c;
-    const int range = (int)blockIdx.x / a.groups, n0 = (int)blockIdx.x % a.groups * kGroup;
+    const int range = (int)blockIdx.x / (a.groups * BLOCKS), n0 = (int)blockIdx.x / BLOCKS % a.groups * kGroup;
+    const int from = (int)blockIdx.x % BLOCKS * (8 * RPW * PASS);  // the CTA's first row
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     extern __shared__ int space[];
     after_previous();
@@ -323,7 +326,7 @@ __global__ void __launch_bounds__(256) tree_read(TreeArgs a)
     if (range >= R || warp * RPW * PASS >= D) return;
     long long x = range_begin(range, U, R);
     const long long end = range_begin(range + 1, U, R);
-    const int r0 = warp * RPW * PASS + lane / LPR, c0 = lane % LPR * 4;
+    const int r0 = from + warp * RPW * PASS + lane / LPR, c0 = lane % LPR * 4;
     int b = 0;
     while (x < end) {
         while (x >= (long long)line.units[b + 1] * c.H) ++b;
@@ -646,7 +649,7 @@ cudaError_t gates_impl(const TreeArgs &a, cudaStream_t s)
 template <typename E, int D>
 cudaError_t read_impl(const TreeArgs &a, cudaStream_t s)
 {
-    const size_t grid = (size_t)a.ranges * a.groups, smem = sizeof(int) * Line::ints(a.B);
+    const size_t grid = (size_t)a.ranges * a.groups * read_blocks(D), smem = sizeof(int) * Line::ints(a.B);
     return a.T == 1   ? launch_early(tree_read<E, D, 1>, grid, 256, smem, s, a)
            : a.T == 2 ? launch_early(tree_read<E, D, 2>, grid, 256, smem, s, a)
            : a.T <= 4 ? launch_early(tree_read<E, D, 4>, grid, 256, smem, s, a)

@@ -134,7 +134,7 @@ int run_batch(const mc_paged_cache *cache, TreeArgs a, Call call, int agg_mode, 
     a.groups = a.Tp / 8;
     const bool split = tree_tc_supported(a);
     a.scored = split && routed;
-    a.ranges = split ? kSms : std::max(1, 4 * kSms / a.groups);
+    a.ranges = split ? kSms : std::max(1, 4 * kSms / (a.groups * read_blocks(c.d)));
     // a head's end, on the tensor cores: 16 heads of d = 128, 16 sequences of 2 to 63 segments, 16 nodes 101 -> 97 us, of d = 64,
     // 32 of up to 10 58 -> 48; twice as much gives nothing more.  None on the CUDA cores, whose ranges are a quarter as long and
     // bound by products: 16 sequences of 2 to 63 segments, d = 64, 16 nodes in fp32, 84 without and 86 with it

@@ -168,6 +168,11 @@ __device__ inline void leave_line(const TreeArgs &a, int *space)
     for (size_t i = threadIdx.x; i < Line::ints(a.B); i += blockDim.x) a.line[i] = space[i];
 }
 
+// CTAs of tree_read that share a range, each with a part of the rows: four rows to a lane at d = 128 (and 64), two CTAs an SM.
+// With 16 rows there is one (fp32, 16 heads: 4 sequences of 30 to 63 segments, 24 nodes 226 -> 157 us; 2 of up to 63, 4 heads, 16
+// nodes 57 -> 36), with two what goes with a memory outweighs its products (157 -> 232; d = 64, 84 -> 113).
+__host__ __device__ constexpr int read_blocks(int d) { return d == 128 ? 4 : 1; }
+
 // Segments that a path of T nodes can touch.
 inline int path_segments(const TreeArgs &a) { return (int)(((long long)a.c.C - 1 + a.T - 1) / a.c.C) + 1; }
 
