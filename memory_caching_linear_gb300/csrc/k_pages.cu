@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(256) load_segment(Paged c, const E *k, const f
                                                     const int32_t *list)
 {
     constexpr int PARTS = 256 / (D / 4);
-    const int n = (int)blockIdx.x / c.H, h = (int)blockIdx.x % c.H, N = (L + c.C - 1) / c.C;
+    const int n = (int)blockIdx.x / c.H, h = (int)blockIdx.x % c.H, N = (L - 1) / c.C + 1;  // (L + C need not fit)
     after_previous();
     const bool tail = n == done;
     const int at = list[done] < 0 ? -1 : list[tail ? done : n];
