@@ -72,7 +72,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_rows(TreeArgs a)
     const int tid = threadIdx.x, lane = tid % 32;
     __shared__ int taker[kMaxRows], lens[kMaxRows];
     taker[tid] = 0x7fffffff;
-    lens[tid] = 0;
     after_previous();
     let_next_start();
     const int head = tid < c.P ? __ldcg(c.refs + tid) : 1;  // the first references, wanted last
@@ -100,8 +99,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_rows(TreeArgs a)
         report(c, MC_PAGES_INDEX);
         row = -1;
     }
-    // the path to the last node, a warp to a batch row with two nodes' parents on each lane
+    lens[tid] = row < 0 ? -1 : 0;
+    __syncthreads();
+    // the path to the last node, a warp to a batch row with two nodes' parents on each lane; a row of nobody has none
     for (int b = tid / 32; b < a.B; b += kPlanThreads / 32) {
+        if (lens[b] < 0) continue;
         const int32_t *par = a.parent + (size_t)b * a.T;
         const int lo = lane < a.T ? par[lane] : -1, hi = lane + 32 < a.T ? par[lane + 32] : -1;
         int x = a.last[b];

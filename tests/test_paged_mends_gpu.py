@@ -30,3 +30,28 @@ def test_a_prompt_in_a_segment_that_never_ends(d, L, dtype, C):
     y = mcl.mc_decode_step_paged(cache, *(gpu(t) for t in one[:4]), GRM, log_alpha=gpu(one[4]), beta=gpu(one[5]), slots=i32([1]))
     near(y, ref.step(*one, [1], GRM, 0)[0], 1e-4 if dtype == torch.float32 else 1e-2)
     same(cache, ref)
+
+
+@pytest.mark.parametrize("delta", [False, True])
+def test_rows_to_pad_with_are_not_read_by_an_acceptance(delta):
+    """Nodes and parents that do not exist, in rows of nobody: nothing is reported, nothing changes but the other rows'."""
+    gen, rng = seeded(40)
+    H, d, C, T = 2, 64, 5, 12
+    ref = Ref(4, H, d, C, 8, 30).fill([2, 1, 0, 3], [4, 0, 3, 2], gen, rng)
+    cache = on_gpu(ref)
+    x = tokens(gen, 4, H, T, d, torch.bfloat16)
+    if not delta:
+        x[4] = x[5] = None
+    parent, last, slots = draft(rng, 4, T, "tree"), [T - 1, 5, 7, 3], [3, -1, 0, -1]
+    garbage = [1 << 30, -(1 << 31), 77, -2] * (T // 4)
+    on = [gpu(t) for t in x]
+    for t in on[1:3] + on[4:]:
+        if t is not None:
+            t[1], t[3] = float("nan"), float("nan")
+    for junk in ([T, 1 << 30], [-9, T - 1]):
+        mcl.mc_tree_accept(cache, on[1], on[2], i32([parent[0], garbage, parent[2], garbage]), i32([last[0], junk[0], last[2], junk[1]]),
+                           log_alpha=on[4], beta=on[5], slots=i32(slots))
+        ref.accept(x[1], x[2], x[4], x[5], parent, last, slots)
+        assert ref.status == [0] and cache.status.tolist() == [0]
+        same(cache, ref)
+    cache.check()
