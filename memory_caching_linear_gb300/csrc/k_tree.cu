@@ -407,13 +407,16 @@ struct Parts {
 //   read of the begun memory wait for it, exp(s_j - top) / Z (Residual: 1 and 1; Mean: all scores 0).
 // Instructions and latency bound it: what a warp loads of P and A serves both rows, an e that is nobody's ancestor costs a
 // branch, and loads that do not hang on one another are all under way before the first is used.  64 nodes, 12 sequences,
-// 16 heads of d = 128, gated delta 30 us; 32 nodes, 8 sequences, linear 14.
+// 16 heads of d = 128, gated delta 30 us; 32 nodes, 8 sequences, linear 12.
+// A split read's finish wants 128 registers (at 80 it spills, and what is spilled goes to L2): so it runs where all CTAs are on
+// the SMs at once with them (8 sequences, 16 heads, 32 nodes: the call 105 -> 101 us, d = 64 70 -> 66), and at 80 where they
+// are not (12 sequences, 64 nodes: 199 against 204).
 constexpr int kPartsAtOnce = 1;
 
 template <int D> struct FinishRows { static constexpr int BLOCK = D < 64 ? D : 64, LANE = D < 64 ? 1 : 2; };
 
-template <typename E, int D, bool SPLIT>
-__global__ void __launch_bounds__(256, 3) tree_finish(TreeArgs a, int segments)
+template <typename E, int D, bool SPLIT, int PER_SM>
+__global__ void __launch_bounds__(256, PER_SM) tree_finish(TreeArgs a, int segments)
 {
     constexpr int RB = FinishRows<D>::BLOCK, R = FinishRows<D>::LANE;
     const Paged &c = a.c;
@@ -454,6 +457,9 @@ __global__ void __launch_bounds__(256, 3) tree_finish(TreeArgs a, int segments)
     }
     const int nb = cached_segments(c, pos), in0 = pos % c.C;
     const Parts parts(a, line, b, h, SPLIT ? nb : nb + (in0 ? 1 : 0));
+    constexpr bool HALVES = SPLIT && D == 64;  // two memories of 64 rows go through the tensor cores at once: a read is two sums
+    const size_t second = (a.ranges + (size_t)a.B * c.H) * a.Tp * D;
+    float p2[8][R] = {};  // (of the second halves)
     float p[kPartsAtOnce][8][R];  // partial reads: the next ones, under way
     auto fetch = [&](int j0) {
 #pragma unroll
@@ -462,7 +468,11 @@ __global__ void __launch_bounds__(256, 3) tree_finish(TreeArgs a, int segments)
 #pragma unroll
             for (int x = 0; x < 8; ++x)
 #pragma unroll
-                for (int r = 0; r < R; ++r) p[j][x][r] = j0 + j <= parts.j1 && n0 + x < m ? src[(size_t)x * D + 32 * r] : 0.f;
+                for (int r = 0; r < R; ++r) {
+                    const bool there = j0 + j <= parts.j1 && n0 + x < m;
+                    p[j][x][r] = there ? src[(size_t)x * D + 32 * r] : 0.f;
+                    if (HALVES) p2[x][r] = there ? src[second + (size_t)x * D + 32 * r] : 0.f;
+                }
         }
     };
     fetch(parts.j0);
@@ -542,7 +552,7 @@ __global__ void __launch_bounds__(256, 3) tree_finish(TreeArgs a, int segments)
                 if (j < cnt && n0 + x < m) {
                     const float w = SPLIT ? share[j][n0 + x] : 1.f;
 #pragma unroll
-                    for (int r = 0; r < R; ++r) y[x][r] = fmaf(w, p[j][x][r], y[x][r]);
+                    for (int r = 0; r < R; ++r) y[x][r] = fmaf(w, HALVES ? p[j][x][r] + p2[x][r] : p[j][x][r], y[x][r]);
                 }
         if (j0 + kPartsAtOnce <= parts.j1) fetch(j0 + kPartsAtOnce);
     }
@@ -664,9 +674,13 @@ cudaError_t finish_impl(const TreeArgs &a, cudaStream_t s)
     const size_t smem = sizeof(float) * ((size_t)(a.delta ? 2 : 1) * a.T + (split ? path_segments(a) : 0)) * a.Tp;
     const int block = 32 * a.groups;  // a warp to eight nodes
     if constexpr (sizeof(E) == 2 && D >= 64) {
-        if (split) return launch_early(tree_finish<E, D, true>, grid, block, smem, s, a, path_segments(a));
+        if (split) {
+            const bool room = grid * block <= 152 * 512;
+            return room ? launch_early(tree_finish<E, D, true, 2>, grid, block, smem, s, a, path_segments(a))
+                        : launch_early(tree_finish<E, D, true, 3>, grid, block, smem, s, a, path_segments(a));
+        }
     }
-    return launch_early(tree_finish<E, D, false>, grid, block, smem, s, a, path_segments(a));
+    return launch_early(tree_finish<E, D, false, 3>, grid, block, smem, s, a, path_segments(a));
 }
 
 template <typename E>

@@ -1,12 +1,19 @@
 // k_tree_tc.cu -- what a drafted tree reads of the cached memories, on the tensor cores (bf16 tokens, d = 64 or 128, every cached
 // memory read by every node: no SSC).
 //
-// The reads (tree_read_tc).  For the head at hand, D[r][t] = sum over memories i of M^(i)[r][:] . (g_{t,i} q_t): the fp32 memory is
-// the A operand as it comes by TMA (kind::tf32 takes 11 significant bits of it: 2^-11 of every product against the 2^-9 of
-// y's own rounding), the weighted queries are B, rounded to tf32, and the sum over a head's memories stays in tensor memory.
-// A memory of 64 KB is read from HBM once for all nodes, 1.5 us of an SM's share of the bandwidth, against 0.3 us of products
-// at 64 nodes: HBM is the bound, so the memories stream through a ring of 32-column panels (144 KB on an SM) and
-// everything else is made to keep up: a head's sums are brought out while the next one's panels and B are on their way.
+// The reads (tree_read_tc).  A memory's products with a head's queries, D[r][t] = M[r][:] . q_t, are made by tcgen05.mma in bf16: the
+// queries are bf16 as they come, and the fp32 memory, which comes by TMA, is split into two bf16 terms, each rounded to
+// nearest, that go through tensor memory (together within 2^-18 of every value, to either side; the sums are fp32).  The
+// softmax weights are applied to D in fp32, so a read is as accurate as an fp32 one.  A third term would make the split exact; it
+// cost 297 us against 279 where both were tried (64 nodes, 12 sequences, gated delta; neither without spills), and no output
+// shows it.  kind::tf32 takes the memory as it comes, but cuts it off after 11 bits: up to 2^-10 of a value, and always
+// towards zero.  With what is cut off as a second operand it is as accurate too, in twice the products (8 columns each, not
+// 16), which one thread issues, 60 to 80 clocks each: 264 us, bound by that, against 217 as it is.
+// A memory of 64 KB is read from HBM once for all nodes, 1.5 us of an SM's share of the bandwidth; eight warps need about that for
+// the split, the weights and the sums, one thread 0.6 us for the products of 64 nodes.  So the memories stream through a ring
+// of 32-column panels (176 KB on an SM), and the split of one tile (a memory of 128 rows, two of 64) runs beside the products
+// of the one before and the sums of the one before that.  With all of an SM's memory shared, what a thread spills goes to L2: the
+// kernel keeps within its registers.
 //
 // The memories of all heads and sequences form one line, cut into one range per CTA whatever the sequences' lengths.  A range
 // leaves the sum of its weights with its partial read, and tree_finish joins them, as a softmax over parts; the begun segment's
@@ -34,25 +41,6 @@ using namespace sm100;
 namespace {
 
 __device__ int g_tree_abort;
-
-// kind::tf32: as idesc_bf16 with both formats tf32.
-__host__ __device__ constexpr uint32_t idesc_tf32(int M, int N)
-{
-    return (1u << 4) | (2u << 7) | (2u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-__device__ __forceinline__ void mma_tf32(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::tf32 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-__device__ __forceinline__ float to_tf32(float x)
-{
-    uint32_t r;
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
-    return __uint_as_float(r);
-}
 
 // Warp-level products (m16n8k16) take the columns of their operands in an order that makes a lane's four of every 16 adjacent:
 // tokens and keys come straight from global memory, 8 bytes a lane, and mean keys, in fp32, 16.
@@ -152,8 +140,9 @@ __global__ void __launch_bounds__(256) tree_scores_tc(TreeArgs a, int spans)
 
 // ------------------------------------------------------------------------------------------------ the path
 // Registers a thread, so that a CTA of each runs on an SM: a quarter of it, with 512 registers a lane, has up to three of the
-// reads' ten warps and two of the path's eight.
-constexpr int kPathRegs = 96, kReadRegs = 104;
+// reads' ten warps and two of the path's eight.  Neither spills (64 nodes, 12 sequences, gated delta: 217 us; at 112 and 80 the
+// reads do, 234, at 104 and 96 267).
+constexpr int kPathRegs = 64, kReadRegs = 128;
 
 // Scores of the path's segments, P without the gates, and A, for 32 nodes of a head at a time.  A CTA goes over its
 // share of the heads: little enough in registers and shared memory to run beside a CTA of tree_read_tc.
@@ -198,7 +187,7 @@ __global__ void __maxnreg__(kPathRegs) tree_path_tc(TreeArgs a, int spans, int s
         if (x0 < m) {
             float uf[2][4] = {}, qf[2][4] = {}, kf[2][4] = {};
             auto row_of = [&](const __nv_bfloat16 *x, int n) { return n < m ? x + (size_t)n * D : nullptr; };
-#pragma unroll 4
+#pragma unroll 2
             for (int ks = 0; ks < KS; ++ks) {
                 const int col = 16 * ks + 4 * c4;
                 uint32_t key[4], f[4];
@@ -261,10 +250,45 @@ __global__ void __maxnreg__(kPathRegs) tree_path_tc(TreeArgs a, int spans, int s
 // ------------------------------------------------------------------------------------------------ the reads
 
 constexpr int kWorkers = 8, kThreads = 32 * (kWorkers + 2);
-constexpr int kRingBytes = 147456;            // nine panels of 128 rows, eighteen of 64
-constexpr int kMaxPanels = 18;
-constexpr int kBSlot = kMaxTree * 128 * 4;    // weighted queries of one memory
-constexpr int kReadSmem = 1024 + kRingBytes + 2 * kBSlot;
+constexpr int kPanels = 11;                   // of the ring: 128 rows (a memory's, or two memories' of 64) by 32 columns
+constexpr int kPanelBytes = 128 * 128;
+// Columns of tensor memory: of a tile's sums (two tiles), then of every 64 columns' two terms (two tiles again).
+constexpr int kSums = 64, kTerm = 32, kTerms = 2 * kTerm;
+// The ring and two heads' queries.
+template <int D> struct ReadSmem {
+    static constexpr int B = kMaxTree * D * 2, BYTES = 1024 + kPanels * kPanelBytes + 2 * B;
+};
+
+// A panel of the ring and how often it has been used, modulo 2.
+struct Place {
+    uint32_t s = 0, phase = 0;
+    __device__ __forceinline__ void advance(uint32_t by)
+    {
+        s += by;
+        if (s >= kPanels) {
+            s -= kPanels;
+            phase ^= 1;
+        }
+    }
+};
+
+// Pairs of fp32 in one instruction: x - y.
+__device__ __forceinline__ float2 minus(float2 x, float2 y)
+{
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, m;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 m, {%6, %6};\n\t"
+        "fma.rn.f32x2 x, y, m, x;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(-1.f));
+    return r;
+}
+// The largest magnitude; NaN if any is.
+__device__ __forceinline__ float most(float x, float y, float z)
+{
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
 
 enum { kCached, kBegunQ, kBegunK };
 // Memories of one head that follow each other in a CTA's range: cached ones, or the begun one for the queries or the keys.
@@ -315,29 +339,29 @@ template <int D>
 __global__ void __maxnreg__(kReadRegs)
 tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ CUtensorMap online, TreeArgs a)
 {
-    constexpr int PANELS = D / 32, kPanelBytes = D * 128, RING = kRingBytes / kPanelBytes;
-    constexpr int BATCH = 4 / PANELS;  // memories whose B share a slot and its handshake
+    constexpr int PANELS = D / 32, BLOCKS = D / 64, BATCH = 128 / D;  // of a tile: panels, pairs of them, and memories
     extern __shared__ uint8_t raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *bs = ring + kRingBytes;  // (a 64-row panel's second half, which nobody reads, may be of the next one or of B)
-    int *space = reinterpret_cast<int *>(raw + kReadSmem);
-    __shared__ uint64_t full[kMaxPanels], empty[kMaxPanels], b_full[2], b_empty[2], d_full[2], d_empty[2], drain;
+    uint8_t *bs = ring + kPanels * kPanelBytes;
+    int *space = reinterpret_cast<int *>(raw + ReadSmem<D>::BYTES);
+    __shared__ uint64_t full[kPanels], empty[kPanels], terms[2], b_full[2], d_full[2], d_empty[2], drain;
+    __shared__ __align__(16) float weights[kWorkers][2][32];
+    __shared__ struct { float *out; int nodes; } done[kWorkers];  // the run before
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
     const Paged &c = a.c;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     if (!a.scored) after_previous();  // (else the scores' kernel has waited for what came before)
-    const int NT = (a.T + 15) / 16 * 16;                           // columns of D
-    const int groups = (NT + 31) / 32, writers = PANELS * BATCH * groups;  // warps that make B: 32 tokens of one panel each
+    const int NT = (a.T + 15) / 16 * 16;  // columns of D
     if (tid == 0) {
         abort_flag = 0;
-        for (int i = 0; i < RING; ++i) {
+        for (int i = 0; i < kPanels; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&empty[i], kWorkers / 2);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&b_full[i], writers);
-            mbar_init(&b_empty[i], 1);
+            mbar_init(&terms[i], kWorkers);
+            mbar_init(&b_full[i], kWorkers);
             mbar_init(&d_full[i], 1);
             mbar_init(&d_empty[i], kWorkers);
         }
@@ -345,7 +369,7 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
         fence_mbar_init();
     }
     if (warp == 0) {
-        tmem_alloc(&tmem_base, 128);
+        tmem_alloc(&tmem_base, 512);
         tmem_relinquish();
     }
     const Line line = make_line(a, space, false);
@@ -360,61 +384,67 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
         if (lane == 0) {
             prefetch_tensormap(&pages);
             prefetch_tensormap(&online);
-            uint32_t g = 0;
+            Place p;
+            uint32_t used = 0;  // panels, as far as the ring's number of them
             bool ok = true;
             while (ok && runs.next(a, line, r)) {
+                prefetch_l2(static_cast<const __nv_bfloat16 *>(r.kind == kBegunK ? a.k : a.q) + (size_t)r.bh * a.T * D, a.T * D * 2);
                 const int32_t *table = c.table + (size_t)r.row * c.nmax;
                 const bool cached = r.kind == kCached;
-                int page = cached ? table[r.i0] : 0;
-                for (int i = r.i0; ok && i < r.i1; ++i) {
-                    const int p = page;
-                    if (cached && i + 1 < r.i1) page = table[i + 1];
-                    // a segment without a page is one past the pool: zeros
-                    const int at = cached ? (valid_page(c, p) < 0 ? c.P * c.H : p * c.H + r.h) : r.row * c.H + r.h;
-                    for (int x = 0; x < PANELS; ++x, ++g) {
-                        const uint32_t s = g % RING;
-                        if (!(ok = mbar_wait(&empty[s], ((g / RING) & 1) ^ 1, &abort_flag))) break;
-                        mbar_arrive_expect_tx(&full[s], kPanelBytes);
-                        tma_load_3d(ring + s * kPanelBytes, cached ? &pages : &online, 32 * x, 0, at, &full[s]);
+                int page[BATCH];
+#pragma unroll
+                for (int y = 0; y < BATCH; ++y) page[y] = cached && r.i0 + y < r.i1 ? table[r.i0 + y] : 0;
+                for (int i = r.i0; ok && i < r.i1; i += BATCH) {
+                    int at[BATCH];
+#pragma unroll
+                    for (int y = 0; y < BATCH; ++y) {
+                        const int was = page[y];
+                        if (cached && i + BATCH + y < r.i1) page[y] = table[i + BATCH + y];
+                        // a segment without a page is one past the pool: zeros
+                        at[y] = cached ? (valid_page(c, was) < 0 ? c.P * c.H : was * c.H + r.h) : r.row * c.H + r.h;
+                    }
+                    const int here = min(BATCH, r.i1 - i);
+                    for (int x = 0; x < PANELS; ++x) {
+                        if (!(ok = mbar_wait(&empty[p.s], p.phase ^ 1, &abort_flag))) break;
+                        mbar_arrive_expect_tx(&full[p.s], here * (kPanelBytes / BATCH));
+#pragma unroll
+                        for (int y = 0; y < BATCH; ++y)
+                            if (y < here)
+                                tma_load_3d(ring + p.s * kPanelBytes + y * (kPanelBytes / BATCH), cached ? &pages : &online, 32 * x, 0, at[y], &full[p.s]);
+                        p.advance(1);
+                        used = min(used + 1, (uint32_t)kPanels);
                     }
                 }
             }
-            for (uint32_t x = g > (uint32_t)RING ? g - RING : 0; x < g; ++x) {  // no copy lands after the CTA has left
+            for (; used > 0; --used) {  // no copy lands after the CTA has left
                 int gave_up = 0;
-                mbar_wait_limit(&full[x % RING], (x / RING) & 1, &gave_up, kWaitLimitNs);
+                const uint32_t s = p.s >= used ? p.s - used : p.s + kPanels - used;
+                mbar_wait_limit(&full[s], p.s >= used ? p.phase : p.phase ^ 1, &gave_up, kWaitLimitNs);
             }
         }
         __syncwarp();
     } else if (warp == kWorkers + 1) {
         if (lane == 0) {
-            const uint32_t idesc = idesc_tf32(128, NT);
-            uint32_t g = 0, u = 0, n = 0;
+            const uint32_t idesc = idesc_bf16(128, NT, false, false);
+            uint32_t u = 0, n = 0;
             bool ok = true;
             while (ok && runs.next(a, line, r)) {
-                const uint32_t d = tb + 64 * (n & 1);
-                ok = mbar_wait(&d_empty[n & 1], ((n >> 1) & 1) ^ 1, &abort_flag);
-                for (int i = r.i0; ok && i < r.i1; i += BATCH, ++u) {
-                    if (!(ok = mbar_wait(&b_full[u & 1], (u >> 1) & 1, &abort_flag))) break;
-                    const uint32_t b0 = smem_u32(bs + (u & 1) * kBSlot);
+                ok = mbar_wait(&b_full[u & 1], (u >> 1) & 1, &abort_flag);
+                const uint32_t b0 = smem_u32(bs + (u & 1) * ReadSmem<D>::B);
+                for (int i = r.i0; ok && i < r.i1; i += BATCH, ++n) {
+                    if (!(ok = mbar_wait(&d_empty[n & 1], ((n >> 1) & 1) ^ 1, &abort_flag) &&
+                               mbar_wait(&terms[n & 1], (n >> 1) & 1, &abort_flag)))
+                        break;
+                    tc_fence_after();
+                    const uint32_t d = tb + kSums * (n & 1), a0 = tb + 2 * kSums + BLOCKS * kTerms * (n & 1);
+                    const uint64_t bx = make_desc_sw128(b0, 0, 1024);
 #pragma unroll
-                    for (int y = 0; y < BATCH; ++y) {
-                        if (!ok || i + y >= r.i1) break;
-                        for (int x = 0; x < PANELS; ++x, ++g) {
-                            const uint32_t s = g % RING;
-                            if (!(ok = mbar_wait(&full[s], (g / RING) & 1, &abort_flag))) break;
-                            tc_fence_after();
-                            const uint32_t a0 = smem_u32(ring + s * kPanelBytes), bx = b0 + (y * PANELS + x) * NT * 128;
+                    for (int x = 0; x < BLOCKS; ++x)
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_tf32(d, make_desc_sw128(a0 + 32 * k, 0, 1024), make_desc_sw128(bx + 32 * k, 0, 1024), idesc,
-                                         i + y > r.i0 || x > 0 || k > 0);
-                            mma_commit(&empty[s]);
-                        }
-                    }
-                    if (ok) mma_commit(&b_empty[u & 1]);
+                        for (int y = 0; y < 8; ++y) mma_ts(d, a0 + kTerms * x + 8 * y, bx + (uint64_t)(x * NT * 8 + 2 * (y % 4)), idesc, x > 0 || y > 0);
+                    mma_commit(&d_full[n & 1]);
                 }
-                if (ok) mma_commit(&d_full[n & 1]);
-                ++n;
+                ++u;
             }
             if (!ok) {  // the products under way end before tensor memory is freed
                 int gave_up = 0;
@@ -424,27 +454,35 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
         }
         __syncwarp();
     } else {
-        // this thread's memory of a slot's, 32 columns of B, and token
-        const int sub = warp / PANELS % BATCH, panel = warp % PANELS, t = warp / (PANELS * BATCH) * 32 + lane;
-        const bool writes = warp < writers, routed = a.mode == MC_GRM;
+        // this thread's row of a tile, the warp's panels (every other) and columns of D (16 of every 32); the node whose weights the lane forms
+        const int quarter = warp % 4, side = warp / 4, row = 32 * quarter + lane, half = row / D, t = 16 * side + lane % 16 + (lane & 16) * 2;
         uint32_t u = 0, n = 0;
-        bool ok = true;
-        after_previous();  // the scores
-        // the sums of run `i` to out: rows 32 (warp % 4) + lane of D; the two warps of a quarter take every other 16 columns
-        float *out = nullptr;
-        int nodes = 0;
-        auto bring_out = [&](uint32_t i) {
+        Place at;
+        at.advance(side);
+        bool ok = true, counts = false;  // counts: the half's memory is there in the tile before
+        float acc[2][16];
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int x = 0; x < 16; ++x) acc[y][x] = 0.f;
+        // tile i's sums, weighted
+        auto add_up = [&](uint32_t i) {
             if (!mbar_wait(&d_full[i & 1], (i >> 1) & 1, &abort_flag)) return false;
             tc_fence_after();
-            const int quarter = warp % 4, row = 32 * quarter + lane;
-            for (int t0 = 16 * (warp / 4); t0 < NT; t0 += 32) {
-                float x[16];
-                tmem_ld16f(tmem_addr(tb + 64 * (i & 1), 32 * quarter, t0), x);
-                tmem_wait_ld();
-                if (row < D) {
 #pragma unroll
-                    for (int y = 0; y < 16; ++y)
-                        if (t0 + y < nodes) out[(size_t)(t0 + y) * D + row] = x[y];
+            for (int y = 0; y < 2; ++y) {
+                if (16 * side + 32 * y >= NT) break;
+                float x[16];
+                tmem_ld16f(tmem_addr(tb + kSums * (i & 1), 32 * quarter, 16 * side + 32 * y), x);
+                tmem_wait_ld();
+                if (!counts) continue;
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const float4 w = load4(&weights[warp][i & 1][16 * y + 4 * z]);
+                    acc[y][4 * z] = fmaf(w.x, x[4 * z], acc[y][4 * z]);
+                    acc[y][4 * z + 1] = fmaf(w.y, x[4 * z + 1], acc[y][4 * z + 1]);
+                    acc[y][4 * z + 2] = fmaf(w.z, x[4 * z + 2], acc[y][4 * z + 2]);
+                    acc[y][4 * z + 3] = fmaf(w.w, x[4 * z + 3], acc[y][4 * z + 3]);
                 }
             }
             tc_fence_before();
@@ -452,86 +490,148 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
             if (lane == 0) mbar_arrive(&d_empty[i & 1]);
             return true;
         };
-        while (ok && runs.next(a, line, r)) {
-            const float *scores = a.gates + (size_t)r.bh * c.nmax * a.Tp;
-            const bool in = writes && t < r.m, cached = r.kind == kCached;
-            const float best = cached && in && routed ? a.top[(size_t)r.bh * a.Tp + t] : 0.f;
-            uint32_t q[16];
-            if (in) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(r.kind == kBegunK ? a.k : a.q) +
-                                                                   ((size_t)r.bh * a.T + t) * D + 32 * panel);
+        // a run's sums to where they belong, in eights of nodes, for which there is room
+        auto bring_out = [&]() {
+            const int nodes = done[warp].nodes;
+            float *out = done[warp].out + row % D;
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const uint4 w = __ldg(src + x);
-                    q[4 * x] = w.x;
-                    q[4 * x + 1] = w.y;
-                    q[4 * x + 2] = w.z;
-                    q[4 * x + 3] = w.w;
+            for (int y = 0; y < 4; ++y) {
+                const int node = 16 * side + 32 * (y / 2) + 8 * (y % 2);
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    if (node < nodes) out[(size_t)(node + x) * D] = acc[y / 2][8 * (y % 2) + x];
+                    acc[y / 2][8 * (y % 2) + x] = 0.f;
                 }
             }
-            if (n == 0) let_next_start();
-            float z = 0.f;
-            bool brought = false;
-            if (writes) {
-                const int32_t *table = c.table + (size_t)r.row * c.nmax;
-                // the weight's logarithm: a score; 0 for a page where nothing is scored
-                auto load = [&](int i) {
-                    if (!in || i >= r.i1) return 0.f;
-                    if (!cached) return 0.f;
-                    return routed ? scores[(size_t)i * a.Tp + t] : valid_page(c, table[i]) >= 0 ? 0.f : __int_as_float(0xff800000);
-                };
-                float ahead[2 * BATCH];  // scores come from L2, whose latency is some memories' time
+        };
+        for (bool more = true; ok && more;) {
+            more = runs.next(a, line, r);
+            if (!more) {  // one turn more, for the last tile's sums
+                r.i0 = r.m = 0;
+                r.i1 = 1;
+                r.kind = kBegunQ;
+            }
+            if (more) {
+                // B: the head's queries (or keys).  Its slot is free: every warp has seen the end of the run before the last one.
+                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(r.kind == kBegunK ? a.k : a.q) + (size_t)r.bh * a.T * D);
+                uint8_t *b = bs + (u & 1) * ReadSmem<D>::B;
+#pragma unroll 4
+                for (int x = tid; x < NT * (D / 8); x += 32 * kWorkers) {
+                    const int node = x / (D / 8), piece = x % (D / 8);
+                    const uint4 w = node < r.m ? __ldg(src + x) : make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(b + piece / 8 * NT * 128 + node * 128 + (((piece % 8) ^ (node & 7)) << 4)) = w;
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b_full[u & 1]);
+            }
+            if (u == 0) {
+                after_previous();  // the scores
+                let_next_start();
+            }
+            const bool in = t < r.m, scored = r.kind == kCached && a.scored && in;
+            const float best = scored ? a.top[(size_t)r.bh * a.Tp + t] : 0.f;
+            const float *next = a.gates + ((size_t)r.bh * c.nmax + r.i0) * a.Tp + t;
+            // the weight's logarithm: a score, or 0 (what has no page is read as zeros)
+            auto load = [&](int i) {
+                const float x = scored && i < r.i1 ? *next : 0.f;
+                next += a.Tp;
+                return x;
+            };
+            float ahead[2 * BATCH];  // scores come from L2, whose latency is some memories' time
 #pragma unroll
-                for (int x = 0; x < 2 * BATCH; ++x) ahead[x] = load(r.i0 + x);
-                for (int i = r.i0; i < r.i1; i += BATCH, ++u) {
-                    float g = 0.f;
+            for (int x = 0; x < 2 * BATCH; ++x) ahead[x] = load(r.i0 + x);
+            float z = 0.f;
+            for (int i = r.i0; i < r.i1; i += BATCH, ++n) {
+                const bool there = i + half < r.i1;
+                if (more) {
+                    const uint32_t to = tmem_addr(tb + 2 * kSums + BLOCKS * kTerms * (n & 1) + 16 * side, 32 * quarter, 0);
+#pragma unroll 1
+                    for (int x = 0; x < BLOCKS; ++x) {
+                        if (!(ok = mbar_wait(&full[at.s], at.phase, &abort_flag))) break;
+                        if (there) {  // (what lies in the rows of a memory that is not there goes into sums that nobody takes)
+                            const uint8_t *from = ring + at.s * kPanelBytes + row * 128;
+                            float4 all[8];
+#pragma unroll
+                            for (int y = 0; y < 8; ++y) all[y] = *reinterpret_cast<const float4 *>(from + ((y ^ (row & 7)) << 4));
+#pragma unroll
+                            for (int z = 0; z < 2; ++z) {
+                                uint32_t hi[8], lo[8];
+                                float big = 0.f;
+#pragma unroll
+                                for (int y = 0; y < 4; ++y) {
+                                    const float4 w = all[4 * z + y];
+                                    hi[2 * y] = mma::pack2(w.x, w.y);
+                                    hi[2 * y + 1] = mma::pack2(w.z, w.w);
+                                    const float2 p = minus(make_float2(w.x, w.y), make_float2(mma::low_f(hi[2 * y]), mma::high_f(hi[2 * y])));
+                                    const float2 q = minus(make_float2(w.z, w.w), make_float2(mma::low_f(hi[2 * y + 1]), mma::high_f(hi[2 * y + 1])));
+                                    lo[2 * y] = mma::pack2(p.x, p.y);
+                                    lo[2 * y + 1] = mma::pack2(q.x, q.y);
+                                    big = most(most(big, p.x, p.y), q.x, q.y);
+                                }
+                                if (!(big < FLT_MAX)) {  // not finite, or rounded to what is not: the first term cut off; of what is not finite it is all
+#pragma unroll
+                                    for (int y = 0; y < 8; ++y) {
+                                        const uint2 w = *reinterpret_cast<const uint2 *>(from + (((4 * z + y / 2) ^ (row & 7)) << 4) + y % 2 * 8);
+                                        const float p = __uint_as_float(w.x), q = __uint_as_float(w.y);
+                                        const uint32_t p0 = w.x & 0xffff0000u, q0 = w.y & 0xffff0000u;
+                                        hi[y] = p0 >> 16 | q0 | (isnan(p) ? 0x40u : 0u) | (isnan(q) ? 0x400000u : 0u);
+                                        lo[y] = mma::pack2(isfinite(p) ? p - __uint_as_float(p0) : 0.f, isfinite(q) ? q - __uint_as_float(q0) : 0.f);
+                                    }
+                                }
+                                __syncwarp();
+                                tmem_st8(to + kTerms * x + 8 * z, hi);
+                                tmem_st8(to + kTerms * x + kTerm + 8 * z, lo);
+                            }
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&empty[at.s]);
+                        at.advance(2);
+                    }
+                    if (!ok) break;
+                    float mine = 0.f;
 #pragma unroll
                     for (int y = 0; y < BATCH; ++y) {
-                        const float w = i + y < r.i1 ? expf(ahead[y] - best) : 0.f;
+                        const float w = in && i + y < r.i1 ? expf(ahead[y] - best) : 0.f;
                         z += w;
-                        if (y == sub) g = w;
+                        if (y == half) mine = w;
                         ahead[y] = ahead[y + BATCH];
                         ahead[y + BATCH] = load(i + y + 2 * BATCH);
                     }
-                    if (!(ok = mbar_wait(&b_empty[u & 1], ((u >> 1) & 1) ^ 1, &abort_flag))) break;
-                    uint8_t *row = bs + (u & 1) * kBSlot + (sub * PANELS + panel) * NT * 128 + t * 128;
-                    if (t < NT && i + sub < r.i1) {
-#pragma unroll
-                        for (int x = 0; x < 8; ++x) {
-                            float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (in) {
-                                w.x = to_tf32(g * __uint_as_float(q[2 * x] << 16));
-                                w.y = to_tf32(g * __uint_as_float(q[2 * x] & 0xffff0000u));
-                                w.z = to_tf32(g * __uint_as_float(q[2 * x + 1] << 16));
-                                w.w = to_tf32(g * __uint_as_float(q[2 * x + 1] & 0xffff0000u));
-                            }
-                            *reinterpret_cast<float4 *>(row + ((x ^ (t & 7)) << 4)) = w;
-                        }
-                        fence_async_smem();
-                    }
+                    weights[warp][n & 1][lane] = mine;
+                    tmem_wait_st();
+                    tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&b_full[u & 1]);
-                    if (i == r.i0 + BATCH && n > 0) {  // two slots ahead of the products
-                        if (!(ok = bring_out(n - 1))) break;
-                        brought = true;
-                    }
+                    if (lane == 0) mbar_arrive(&terms[n & 1]);
                 }
+                if (n > 0) {  // a tile behind the products
+                    if (!(ok = add_up(n - 1))) break;
+                    if (i == r.i0) bring_out();
+                }
+                counts = there;
             }
-            if (ok && n > 0 && !brought) ok = bring_out(n - 1);
-            if (!ok) break;
+            if (!ok || !more) break;
             const size_t part = (size_t)blockIdx.x + r.bh;
-            if (cached && in && panel == 0 && sub == 0) a.weight[part * a.Tp + t] = make_float2(best, z);
-            out = cached ? a.part + part * a.Tp * D : (r.kind == kBegunQ ? a.Y0 : a.Z) + (size_t)r.bh * a.Tp * D;
-            nodes = r.m;
-            ++n;
+            if (r.kind == kCached && !a.scored) {  // nothing is scored: the pages that there are
+                z = 0.f;
+                for (int i = r.i0; i < r.i1; ++i) z += valid_page(c, c.table[(size_t)r.row * c.nmax + i]) >= 0 ? 1.f : 0.f;
+            }
+            if (r.kind == kCached && in && quarter == 0) a.weight[part * a.Tp + t] = make_float2(best, z);
+            if (lane == 0) {  // of the cached memories both halves' sums, which tree_finish adds
+                const bool cached = r.kind == kCached;
+                done[warp].out = cached ? a.part + (part + (half ? a.ranges + (size_t)a.B * c.H : 0)) * a.Tp * D
+                                        : (r.kind == kBegunQ ? a.Y0 : a.Z) + (size_t)r.bh * a.Tp * D;
+                done[warp].nodes = half && !cached ? 0 : r.m;
+            }
+            __syncwarp();
+            ++u;
         }
-        if (ok && n > 0) bring_out(n - 1);
     }
     tc_fence_before();
     __syncthreads();
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc(tb, 128);
+        tmem_dealloc(tb, 512);
     }
     if (tid == 0 && abort_flag) atomicExch(&g_tree_abort, 1);
 }
@@ -599,7 +699,7 @@ cudaError_t launch_tree_read_tc(const TreeArgs &a, cudaStream_t s)
         !make_map(&online, a.c.online, (unsigned long long)a.c.S * a.c.H, a.c.d))
         return cudaErrorInvalidValue;
     return launch_early(a.c.d == 128 ? tree_read_tc<128> : tree_read_tc<64>, (size_t)a.ranges, kThreads,
-                        kReadSmem + sizeof(int) * Line::ints(a.B), s, pages, online, a);
+                        (a.c.d == 128 ? ReadSmem<128>::BYTES : ReadSmem<64>::BYTES) + sizeof(int) * Line::ints(a.B), s, pages, online, a);
 }
 
 cudaError_t take_tree_abort(int *was_set)

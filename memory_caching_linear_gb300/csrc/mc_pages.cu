@@ -164,7 +164,7 @@ int run_batch(const mc_paged_cache *cache, TreeArgs a, Call call, int agg_mode, 
             a.anc = cv.take<uint64_t>(B * kMaxTree);
             a.P = cv.take<float>(BH * T * a.Tp);
             a.A = cv.take<float>(a.delta ? BH * T * a.Tp : 0);
-            a.part = cv.take<float>((a.ranges + BH) * a.Tp * c.d);
+            a.part = cv.take<float>((a.ranges + BH) * a.Tp * c.d * (split && c.d == 64 ? 2 : 1));
         }
         if (pass == 0 && scratch_alloc(&scratch, cv.used, s) != cudaSuccess) {
             cudaGetLastError();
