@@ -60,7 +60,7 @@ __device__ __forceinline__ void rows_of(const __nv_bfloat16 *lo, const __nv_bflo
 constexpr int kSpan = 32, kPathThreads = 256, kCol = kSpan + 1;
 
 // Scores of a head's cached segments for 32 nodes, and every node's largest.  Eight segments a warp at a time; a mean key takes
-// part in two bf16 terms (2^-17 of it, for weights that are not ranked).  A chain of loads bounds it (slot, row, position,
+// part in three bf16 terms (2^-25 of it).  A chain of loads bounds it (slot, row, position,
 // page, mean key).
 template <int D>
 __global__ void __launch_bounds__(256) tree_scores_tc(TreeArgs a, int spans)
@@ -94,12 +94,12 @@ __global__ void __launch_bounds__(256) tree_scores_tc(TreeArgs a, int spans)
     for (int i0 = 8 * warp; i0 < nb; i0 += 64) {
         page = valid_page(c, page);
         const float *src = c.kbar + ((size_t)max(page, 0) * c.H + h) * D;
-        uint32_t hi[KS][2], lo[KS][2];
+        uint32_t hi[KS][2], mid[KS][2], lo[KS][2];
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             const float4 v = page >= 0 ? load4(src + 16 * ks + 4 * c4) : make_float4(0.f, 0.f, 0.f, 0.f);
-            mma::split2(v.x, v.y, hi[ks][0], lo[ks][0]);
-            mma::split2(v.z, v.w, hi[ks][1], lo[ks][1]);
+            mma::split3(v.x, v.y, hi[ks][0], mid[ks][0], lo[ks][0]);
+            mma::split3(v.z, v.w, hi[ks][1], mid[ks][1], lo[ks][1]);
         }
         const bool there[2] = {__shfl_sync(0xffffffffu, page, 8 * c4) >= 0, __shfl_sync(0xffffffffu, page, 8 * c4 + 4) >= 0};
         page = i0 + 64 + g < nb ? table[i0 + 64 + g] : -1;
@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(256) tree_scores_tc(TreeArgs a, int spans)
                 const uint2 x = *reinterpret_cast<const uint2 *>(first + 32 * ks), y = *reinterpret_cast<const uint2 *>(second + 32 * ks);
                 const uint32_t f[4] = {x.x, y.x, x.y, y.y};
                 mma::mma16816(s, f, hi[ks][0], hi[ks][1]);
+                mma::mma16816(s, f, mid[ks][0], mid[ks][1]);
                 mma::mma16816(s, f, lo[ks][0], lo[ks][1]);
             }
 #pragma unroll

@@ -118,3 +118,71 @@ def test_drafts(d, dtype, delta, mode, topk, T, tree, C, shape):
         if rows:
             near(got[b][:, rows], torch.stack([want[b, j] for j in rows], 1), TOL[dtype])
     same_sampled(cache, ref)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("mode", [GRM, MEAN])
+def test_drafts_lose_no_bits_but_the_output_s(d, mode):
+    """Memories and queries of one sign, where errors of one sign add up.  An output is fp32's within 1e-5 of its size -- its
+    products are within 2^-18 = 4e-6, its weights and sums much closer -- and rounded to bf16 once: off by at most
+    2^-8 of itself.  On average the rounding is off by nothing: of n outputs with errors evenly spread up to 2^-8 either
+    way the mean is within 2^-8 / sqrt(3 n), and with five times that and 1e-5 the bound is 6e-5 for n = 1e5."""
+    cache, ref, gen, rng = sampled(d, 48, LONG, 3 * d, False)
+    for n in ("pages", "online", "kbar", "ksum"):
+        getattr(cache, n).abs_()
+        getattr(ref, n).abs_()
+    B, T = len(LONG), 33
+    x, few = inputs(gen, B, T, d, torch.bfloat16, False, mode)
+    for i in (0, 1, 2):
+        x[i].abs_()
+        few[i] = x[i][:, HEADS]
+    q, k, v, u, la, be = (gpu(t) for t in x)
+    parent = draft(rng, B, T, "tree")
+    y = mcl.mc_decode_tree(cache, q, k, v, u, i32(parent), mode)
+    want = ref.tree(*few, parent, None, None, mode, 0)
+    want = torch.stack([torch.stack([want[b, j] for j in range(T)], 1) for b in range(B)])
+    got = y[:, HEADS].double().cpu()
+    assert (want > 0).all()
+    off = (got - want) / want
+    assert float(off.abs().max()) <= 2 ** -8 + 1e-5
+    assert off.numel() > 1e5 / 2 and abs(float(off.mean())) <= 5 * 2 ** -8 / (3 * off.numel()) ** 0.5 + 1e-5
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_drafts_of_what_is_not_finite(d):
+    """An infinity, a NaN (one that differs from an infinity in its last bit) and numbers at the type's ends in cached memories:
+    outputs are what the products and sums in 64 bits are, where those fit; the other sequences' are untouched."""
+    cache, ref, gen, rng = sampled(d, 48, [6, 5, 7, 4], d, False)
+    B, T = 4, 20
+    cache.pages.mul_(0.125)
+    ref.pages.mul_(0.125)
+    x, few = inputs(gen, B, T, d, torch.bfloat16, False, MEAN)
+    for i in (0,):
+        x[i].abs_().clamp_min_(2.0 ** -8)
+        few[i] = x[i][:, HEADS]
+    last_nan = torch.tensor([0x7f800001], dtype=torch.int32).view(torch.float32)
+    odd = [(0, float("inf")), (1, float("nan")), (2, last_nan.item())]
+    for b, value in odd:
+        p = ref.table[ref.row[b]][2]
+        if b == 2:
+            cache.pages.view(torch.int32)[p, :, 3, 5] = 0x7f800001
+        else:
+            cache.pages[p, :, 3, 5] = value
+        ref.pages[p, :, 3, 5] = float("nan") if b else value
+    p = ref.table[ref.row[3]][1]
+    cache.pages[p, :, 7, 4], ref.pages[p, :, 7, 4] = 3.4e38, float(torch.tensor(3.4e38))
+    q, k, v, u, la, be = (gpu(t) for t in x)
+    parent = draft(rng, B, T, "star")
+    y = mcl.mc_decode_tree(cache, q, k, v, None, i32(parent), MEAN)
+    want = ref.tree(*few, parent, None, None, MEAN, 0)
+    got = y[:, HEADS].double().cpu()
+    for (b, j), w in want.items():
+        rest = torch.ones(d, dtype=torch.bool)
+        rest[7 if b == 3 else 3] = False
+        near(got[b, :, j][:, rest], w[:, rest], 1e-2)
+        if b == 0:
+            assert (got[b, :, j, 3] == float("inf")).all()
+        elif b < 3:
+            assert torch.isnan(got[b, :, j, 3]).all()
+        else:
+            assert float((got[b, :, j, 7] / w[:, 7] - 1).abs().max()) <= 2 ** -8 + 1e-4
