@@ -386,7 +386,8 @@ int mc_decode_step_paged(const mc_paged_cache *cache, const void *q, const void 
 /*
  * mc_decode_tree -- what T drafted tokens of every sequence would read, the cache left as it is.  Node n goes on from node
  * parent[n] < n, or from the cache (-1): it reads what mc_decode_step_paged would read after the tokens on its path, segments
- * that the path itself completes among it.
+ * that the path itself completes among it, if each of these found a page.  A draft needs none for them: where the table ends
+ * (n_max) or the pool runs out it reads them all the same, whereas an acceptance or a step loses them and says so in status.
  *   q, k, v, u, y   : [B][H][T][d]; log_alpha, beta [B][H][T] or both NULL.
  *   parent          : int32 [B][T], device (NULL only for T = 1).  A parent out of range is taken as -1.
  *   count           : int32 [B], device: sequence b's nodes are 0 .. count[b] - 1; the others are not read (nor their parents)

@@ -703,8 +703,8 @@ def mc_decode_tree(cache: PagedCache, q, k, v, u, parent, agg_mode: int, topk: i
                    count=None, slots=None, y=None, stream=None):
     """What a tree of T drafted tokens of every sequence would read (``mc_decode_tree`` in mc.h); the cache stays as it is.  q, k,
     v, u [B, H, T, d], for the gated delta memory log_alpha and beta [B, H, T]; ``parent`` int32 [B, T] (-1: the cache),
-    ``count`` int32 [B] nodes of each sequence (None: T), ``slots`` as in :func:`mc_decode_step_paged`.  Returns y [B, H, T,
-    d]; what is beyond count, and rows of nobody, stay as they are in a y that is given, and are anything in a new one."""
+    ``count`` int32 [B] nodes of each sequence (None: T), ``slots`` as in :func:`mc_decode_step_paged`.  Segments that a path
+    completes are read whether or not a page would be found for them.  Returns y [B, H, T, d]; what is beyond count, and rows of nobody, stay as they are in a y that is given, and are anything in a new one."""
     _paged_batch(cache, q, "q", 4)
     B, _, T, _ = q.shape
     _tokens_match((("q", q), ("k", k), ("v", v)), u, log_alpha, beta,

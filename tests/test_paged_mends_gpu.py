@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import memory_caching_linear_gb300 as mcl
-from paged_ref import GRM, Ref, draft, seeded, tokens
+from paged_ref import GRM, MEAN, SSC, TABLE_FULL, Ref, draft, seeded, tokens
 from test_paged_gpu import gpu, i32, near, on_gpu, run_tree, same
 
 pytestmark = pytest.mark.gpu
@@ -55,3 +55,31 @@ def test_rows_to_pad_with_are_not_read_by_an_acceptance(delta):
         assert ref.status == [0] and cache.status.tolist() == [0]
         same(cache, ref)
     cache.check()
+
+
+@pytest.mark.parametrize("T,d,dtype", [(7, 64, torch.bfloat16), (20, 64, torch.bfloat16), (20, 32, torch.float32), (12, 128, torch.float32)])
+@pytest.mark.parametrize("mode,topk", [(GRM, 0), (SSC, 2), (MEAN, 0)])
+def test_drafts_where_the_table_ends(T, d, dtype, mode, topk):
+    """Whether a path's segments would find a place does not matter to what is read: the same as with a table of room; the
+    acceptance loses them and says so."""
+    gen, rng = seeded(T + d)
+    H, C, S = 2, 2, 2
+    ref = Ref(S, H, d, C, 4, 12).fill([3, 4], [1, 0], gen, rng)
+    wide = mcl.PagedCache(S, H, d, C, 40, 12)
+    cache = on_gpu(ref)
+    for n in ("pages", "kbar", "online", "ksum", "refs", "pos", "row"):
+        getattr(wide, n).copy_(getattr(cache, n))
+    wide.table[:, :4] = cache.table
+    x = tokens(gen, S, H, T, d, dtype)
+    if mode == MEAN:
+        x[3] = None
+    parent = draft(rng, S, T, "chain")
+    y = run_tree(cache, ref, x, parent, None, None, mode, topk, dtype)
+    on = [gpu(t) for t in x]
+    z = mcl.mc_decode_tree(wide, *on[:4], i32(parent), mode, topk, log_alpha=on[4], beta=on[5])
+    near(z, y.double().cpu(), 1e-4 if dtype == torch.float32 else 1e-2)
+    assert cache.status.item() == 0 and wide.status.item() == 0
+    mcl.mc_tree_accept(cache, on[1], on[2], i32(parent), i32([T - 1, 0]), log_alpha=on[4], beta=on[5])
+    ref.accept(x[1], x[2], x[4], x[5], parent, [T - 1, 0], None)
+    assert ref.status == [TABLE_FULL]
+    same(cache, ref)
