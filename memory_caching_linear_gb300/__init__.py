@@ -616,10 +616,21 @@ class PagedCache:
                    "ksum": torch.zeros((n_seqs, H, d), **f32), "table": torch.full((n_seqs, n_max), -1, **i32),
                    "pos": torch.zeros((n_seqs,), **i32), "row": torch.arange(n_seqs, **i32), "status": torch.zeros((1,), **i32),
                    "work": torch.zeros((load_library().mc_paged_work_bytes(self.n_seqs, self.H, self.d),), dtype=torch.uint8, device=device)}
+        self._point()
+
+    def _point(self):
+        """The library's view of the tensors."""
         self.device = self._t["pages"].device
         self._c = _CPagedCache(*[t.data_ptr() for t in self._t.values()], self.n_pages, self.n_seqs, self.H, self.d,
                                self.seg_len, self.n_max)
         self._ref = ctypes.addressof(self._c)
+
+    def __getstate__(self):  # copies and pickles have tensors, and so addresses, of their own
+        return {n: x for n, x in self.__dict__.items() if n not in ("_c", "_ref")}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
+        self._point()
 
     pages, kbar, refs, online, ksum, table, pos, row, status = (
         property(lambda self, n=n: self._t[n]) for n in

@@ -1,5 +1,7 @@
 """Calls of the paged cache that the other tests' sizes do not reach.  Tolerances as in test_paged_gpu.py: of an output's largest
 value 1e-4 with fp32 inputs, 1e-2 with bf16 ones; what is copied or counted is equal."""
+import copy
+
 import pytest
 import torch
 
@@ -83,3 +85,21 @@ def test_drafts_where_the_table_ends(T, d, dtype, mode, topk):
     ref.accept(x[1], x[2], x[4], x[5], parent, [T - 1, 0], None)
     assert ref.status == [TABLE_FULL]
     same(cache, ref)
+
+
+def test_a_copied_cache_goes_its_own_way():
+    gen, rng = seeded(12)
+    H, d, C, T = 2, 64, 4, 6
+    ref = Ref(2, H, d, C, 8, 20).fill([3, 2], [3, 1], gen, rng)
+    cache = on_gpu(ref)
+    x = [z[:, :, 0].contiguous() for z in tokens(gen, 2, H, 1, d, torch.float32)]
+    on = [gpu(z) for z in x]
+    step = lambda c: mcl.mc_decode_step_paged(c, *on[:4], GRM, log_alpha=on[4], beta=on[5])  # noqa: E731
+    step(cache)
+    ref.step(*x, None, GRM, 0)
+    twin, ref2 = copy.deepcopy(cache), copy.deepcopy(ref)
+    for _ in range(2):
+        y, want = step(twin), ref2.step(*x, None, GRM, 0)
+        near(y, torch.stack([want[0], want[1]]), 1e-4)
+    same(twin, ref2)
+    same(cache, ref)  # as it was when it was copied
