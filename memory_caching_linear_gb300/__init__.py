@@ -639,6 +639,8 @@ class PagedCache:
     def check(self):
         """Wait for the device and raise if a call met a bad index, an empty pool or a full table since the last check
         (``status``, which is cleared)."""
+        if self.device.type == "cuda":
+            torch.cuda.synchronize(self.device)  # calls may be under way on any stream
         bits = int(self.status.item())
         if bits:
             self.status.zero_()

@@ -103,3 +103,22 @@ def test_a_copied_cache_goes_its_own_way():
         near(y, torch.stack([want[0], want[1]]), 1e-4)
     same(twin, ref2)
     same(cache, ref)  # as it was when it was copied
+
+
+def test_check_waits_for_every_stream():
+    """A bad index in a call on a stream that is busy when check() is called on another."""
+    gen, rng = seeded(14)
+    ref = Ref(2, 1, 16, 4, 4, 8).fill([1, 1], [0, 0], gen, rng)
+    cache = on_gpu(ref)
+    on = [gpu(z[:, :, 0].contiguous()) for z in tokens(gen, 2, 1, 1, 16, torch.float32)]
+    side, m = torch.cuda.Stream(), torch.randn(4096, 4096, device="cuda")
+    slots = i32([0, 5])
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(30):
+            m = (m @ m) * 1e-5
+        mcl.mc_decode_step_paged(cache, *on[:4], GRM, slots=slots)
+    with pytest.raises(RuntimeError, match="index"):
+        cache.check()
+    cache.check()
+    assert cache.status.item() == 0
