@@ -32,10 +32,12 @@ int fail(cudaError_t e)
 
 bool aligned(const void *p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
 
+bool has_width(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
+
 int check_cache(const mc_paged_cache *c, Paged &p)
 {
     if (!c) return MC_ERR_NULL;
-    if (c->d != 16 && c->d != 32 && c->d != 64 && c->d != 128) return MC_ERR_SHAPE;
+    if (!has_width(c->d)) return MC_ERR_SHAPE;
     if (c->H < 1 || c->seg_len < 1 || c->n_seqs < 1 || c->n_seqs > kMaxRows || c->n_max < 1 || c->n_max > kMaxPaged ||
         c->n_pages < 1 || c->n_pages > (1 << 20))
         return MC_ERR_SHAPE;
@@ -211,7 +213,7 @@ extern "C" {
 
 size_t mc_paged_work_bytes(int n_seqs, int H, int d)
 {
-    if (n_seqs < 1 || n_seqs > mc::kMaxRows || H < 1 || H > (1 << 20) || d < 1 || d > 128) return 0;
+    if (n_seqs < 1 || n_seqs > mc::kMaxRows || H < 1 || H > (1 << 20) || !mc::has_width(d)) return 0;
     return mc::step_plan(n_seqs, H, d).total;
 }
 
