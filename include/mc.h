@@ -338,7 +338,8 @@ int mc_cache_compact(const void *k, const void *u, const float *prefill_states, 
  *                  multiple of seg_len.
  *   table        : int32 [n_seqs][n_max], page of segment i; -1 from segment pos / seg_len on, and for one that found no
  *                  page (it is not there: no gate, no read).
- *   pos          : int32 [n_seqs], tokens seen, 0 .. 2^30.  An empty slot is a sequence at 0.
+ *   pos          : int32 [n_seqs], tokens seen, 0 .. 2^30.  An empty slot is a sequence at 0.  A call that takes a sequence past
+ *                  2^30 is carried out; to those after it that position is out of range.
  *   row          : int32 [n_seqs], a permutation: slot x's online, ksum, table and pos lie in row row[x].
  *   status       : int32 [1], an OR of MC_PAGES_* that calls set and nobody clears but the caller:
  *                    MC_PAGES_INDEX      a slot, parent, node, count, row or position out of range, or a slot that two
@@ -423,7 +424,7 @@ int mc_pages_fork(const mc_paged_cache *cache, const int32_t *src, mc_stream_t s
 
 /*
  * mc_pages_compact -- everything in src to dst, another cache: the live pages come first, in their order, and row becomes the
- * identity.  What dst held is gone; slots and pages past those of src are empty.  dst has H, d and seg_len of src and at least
+ * identity.  dst shares no array with src but status and work (MC_ERR_SHAPE).  What dst held is gone; slots and pages past those of src are empty.  dst has H, d and seg_len of src and at least
  * its n_seqs and n_max; its pages may be fewer (a live page that has no place is lost: MC_PAGES_NONE_FREE in dst's status).
  */
 int mc_pages_compact(const mc_paged_cache *dst, const mc_paged_cache *src, mc_stream_t stream);

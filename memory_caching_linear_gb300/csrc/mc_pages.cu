@@ -269,7 +269,9 @@ int mc_pages_compact(const mc_paged_cache *dst, const mc_paged_cache *src, mc_st
     if (st != MC_OK) return st;
     if (to.H != from.H || to.d != from.d || to.C != from.C || to.S < from.S || to.nmax < from.nmax) return MC_ERR_SHAPE;
     if ((st = mc::check_cache_pointers(to, dst->work)) != MC_OK || (st = mc::check_cache_pointers(from, src->work)) != MC_OK) return st;
-    if (to.pages == from.pages || to.online == from.online || to.table == from.table || to.refs == from.refs) return MC_ERR_SHAPE;
+    if (to.pages == from.pages || to.kbar == from.kbar || to.refs == from.refs || to.online == from.online || to.ksum == from.ksum ||
+        to.table == from.table || to.pos == from.pos || to.row == from.row)
+        return MC_ERR_SHAPE;
     if ((st = mc::check_device()) != MC_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return mc::with_plan(1 + (size_t)to.P + from.P, s, [&](int32_t *plan) { return mc::launch_pages_compact(to, from, plan, s); });
