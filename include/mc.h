@@ -354,8 +354,9 @@ int mc_cache_compact(const void *k, const void *u, const float *prefill_states, 
  * device, NULL: row b is slot b) says whose they are, -1 (a row to pad with) nobody's: such a row is not read and its outputs
  * stay as they are.  Every call returns without synchronising, takes positions from the device, and may be captured
  * into a graph and replayed.  Two calls on one cache are ordered by the caller unless both only read it (mc_decode_tree, and
- * mc_pages_compact of its source).  Integer arrays are aligned to 4 bytes, log_alpha and beta to their element, all others
- * to 16.  No input shares memory with an output.
+ * mc_pages_compact of its source).  The same call on the same cache gives the same bits; which sums of a sequence are formed
+ * apart, and so its last bits, depends on the whole batch.  Integer arrays are aligned to 4 bytes, log_alpha and beta to their
+ * element, all others to 16.  No input shares memory with an output.
  */
 typedef struct {
     float *pages, *kbar;
@@ -396,8 +397,10 @@ int mc_decode_step_paged(const mc_paged_cache *cache, const void *q, const void 
  *   slots           : as above; a slot may come any number of times.
  *   T               : 1 .. 64.  Other arguments and errors as mc_decode_step_paged.
  * Accuracy as mc_decode_step: fp32 inputs 1e-4, bf16 ones 1e-2 of the largest value.  With bf16 inputs, d >= 64 and no SSC the
- * memories in the cache are rounded to the tensor cores' 11 significant bits on the way (2^-11 of their values, against the
- * 2^-9 of y's own rounding), unless T <= 8 and B H (n_max + 1) d^2 <= 10 * 2^20.
+ * memories are read in two bf16 terms, rounded to nearest (within 2^-18 of every value, against the 2^-8 of y's own rounding),
+ * unless T <= 8 and B H (n_max + 1) d^2 <= 10 * 2^20; all else is fp32.
+ * Scratch: up to 4 B H T (n_max + 3 T + 4 d + 10) bytes, T rounded up to a multiple of 8, and 6 MB; n_max counts, not what is
+ * cached.
  */
 int mc_decode_tree(const mc_paged_cache *cache, const void *q, const void *k, const void *v, const void *u,
                    const void *log_alpha, const void *beta, const int32_t *parent, const int32_t *count,
@@ -424,8 +427,9 @@ int mc_pages_fork(const mc_paged_cache *cache, const int32_t *src, mc_stream_t s
 
 /*
  * mc_pages_compact -- everything in src to dst, another cache: the live pages come first, in their order, and row becomes the
- * identity.  dst shares no array with src but status and work (MC_ERR_SHAPE).  What dst held is gone; slots and pages past those of src are empty.  dst has H, d and seg_len of src and at least
- * its n_seqs and n_max; its pages may be fewer (a live page that has no place is lost: MC_PAGES_NONE_FREE in dst's status).
+ * identity.  What dst held is gone; slots and pages past those of src are empty.  dst has H, d and seg_len of src, at least
+ * its n_seqs and n_max, and arrays of its own but for status and work, else MC_ERR_SHAPE; its pages may be fewer (a live page
+ * that has no place is lost: MC_PAGES_NONE_FREE in dst's status).
  */
 int mc_pages_compact(const mc_paged_cache *dst, const mc_paged_cache *src, mc_stream_t stream);
 

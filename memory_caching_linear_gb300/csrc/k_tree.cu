@@ -411,8 +411,6 @@ struct Parts {
 // A split read's finish wants 128 registers (at 80 it spills, and what is spilled goes to L2): so it runs where all CTAs are on
 // the SMs at once with them (8 sequences, 16 heads, 32 nodes: the call 105 -> 101 us, d = 64 70 -> 66), and at 80 where they
 // are not (12 sequences, 64 nodes: 199 against 204).
-constexpr int kPartsAtOnce = 1;
-
 template <int D> struct FinishRows { static constexpr int BLOCK = D < 64 ? D : 64, LANE = D < 64 ? 1 : 2; };
 
 template <typename E, int D, bool SPLIT, int PER_SM>
@@ -429,7 +427,7 @@ __global__ void __launch_bounds__(256, PER_SM) tree_finish(TreeArgs a, int segme
     __shared__ uint64_t anc[kMaxTree];
     __shared__ uint64_t seg_set[kMaxTree];
     __shared__ int seg[kMaxTree];
-    __shared__ float share[kPartsAtOnce][kMaxTree], into[kMaxTree], first[kMaxTree], tops[kMaxTree], invs[kMaxTree];
+    __shared__ float share[kMaxTree], into[kMaxTree], first[kMaxTree], tops[kMaxTree], invs[kMaxTree];
     const size_t at = (size_t)bh * a.T;
     after_previous();
     const Line line = line_in(a.line, a.B);
@@ -460,20 +458,17 @@ __global__ void __launch_bounds__(256, PER_SM) tree_finish(TreeArgs a, int segme
     constexpr bool HALVES = SPLIT && D == 64;  // two memories of 64 rows go through the tensor cores at once: a read is two sums
     const size_t second = (a.ranges + (size_t)a.B * c.H) * a.Tp * D;
     float p2[8][R] = {};  // (of the second halves)
-    float p[kPartsAtOnce][8][R];  // partial reads: the next ones, under way
-    auto fetch = [&](int j0) {
+    float p[8][R];  // partial reads: the next ones, under way
+    auto fetch = [&](int j) {
+        const float *src = a.part + (((size_t)j + bh) * a.Tp + n0) * D + row;
 #pragma unroll
-        for (int j = 0; j < kPartsAtOnce; ++j) {
-            const float *src = a.part + (((size_t)j0 + j + bh) * a.Tp + n0) * D + row;
+        for (int x = 0; x < 8; ++x)
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const bool there = j0 + j <= parts.j1 && n0 + x < m;
-                    p[j][x][r] = there ? src[(size_t)x * D + 32 * r] : 0.f;
-                    if (HALVES) p2[x][r] = there ? src[second + (size_t)x * D + 32 * r] : 0.f;
-                }
-        }
+            for (int r = 0; r < R; ++r) {
+                const bool there = j <= parts.j1 && n0 + x < m;
+                p[x][r] = there ? src[(size_t)x * D + 32 * r] : 0.f;
+                if (HALVES) p2[x][r] = there ? src[second + (size_t)x * D + 32 * r] : 0.f;
+            }
     };
     fetch(parts.j0);
     for (int n = tid; n < kMaxTree; n += blockDim.x) {
@@ -535,26 +530,20 @@ __global__ void __launch_bounds__(256, PER_SM) tree_finish(TreeArgs a, int segme
             }
         }
     }
-    for (int j0 = parts.j0; j0 <= parts.j1; j0 += kPartsAtOnce) {
-        const int cnt = min(kPartsAtOnce, parts.j1 - j0 + 1);
+    for (int j = parts.j0; j <= parts.j1; ++j) {
         if (SPLIT) {
             __syncthreads();
-            for (int i = tid; i < cnt * m; i += blockDim.x) {
-                const int j = i / m, n = i % m;
-                share[j][n] = expf(a.weight[((size_t)j0 + j + bh) * a.Tp + n].x - tops[n]) * invs[n];
-            }
+            for (int n = tid; n < m; n += blockDim.x) share[n] = expf(a.weight[((size_t)j + bh) * a.Tp + n].x - tops[n]) * invs[n];
             __syncthreads();
         }
 #pragma unroll
-        for (int j = 0; j < kPartsAtOnce; ++j)
+        for (int x = 0; x < 8; ++x)
+            if (n0 + x < m) {
+                const float w = SPLIT ? share[n0 + x] : 1.f;
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-                if (j < cnt && n0 + x < m) {
-                    const float w = SPLIT ? share[j][n0 + x] : 1.f;
-#pragma unroll
-                    for (int r = 0; r < R; ++r) y[x][r] = fmaf(w, HALVES ? p[j][x][r] + p2[x][r] : p[j][x][r], y[x][r]);
-                }
-        if (j0 + kPartsAtOnce <= parts.j1) fetch(j0 + kPartsAtOnce);
+                for (int r = 0; r < R; ++r) y[x][r] = fmaf(w, HALVES ? p[x][r] + p2[x][r] : p[x][r], y[x][r]);
+            }
+        if (j < parts.j1) fetch(j + 1);
     }
     // to[x] += sign W_{j,x} ej for this warp's nodes x: W of one that j is no ancestor of is 0, but ej may not be finite, and
     // then it is not multiplied
@@ -702,7 +691,8 @@ cudaError_t run(const TreeArgs &a, cudaStream_t s, int what)
 }  // namespace
 
 // While the memories that there is room for come to no more than 40 MB: 4 heads of d = 64 over 5 segments, 8 nodes, 11 us in one
-// launch and 17 in three; 16 heads of d = 128 over 20, 18 and 28; over 63 (66 MB) 48 and 39.
+// launch and 17 in three; 16 heads of d = 128 over 20, 18 and 28; over 63 (66 MB) 48 and 39.  The host knows the room, not
+// what is cached: in a table of 1024 the first of these takes the three launches (34 us cold against 16).
 bool tree_whole(const TreeArgs &a)
 {
     return a.T <= kGroup && (long long)a.B * a.c.H * (a.c.nmax + 1) * a.c.d * a.c.d * 4 <= 40 << 20;

@@ -29,7 +29,7 @@ struct Paged {
 
 // What the acceptance of paths does with the batch rows' sequences.
 struct Plan {
-    int32_t *act;      // [B] the cache's row, -1: nothing to do; null: no plan
+    int32_t *act;      // [B] the cache's row, -1: nothing to do
     int32_t *pos;      // [B] position before the call
     uint64_t *path;    // [B] the nodes of the path
     int32_t *fresh;    // [B + 1] where a batch row's new pages begin in list
@@ -60,7 +60,7 @@ struct TreeArgs {
     int32_t *seg;                         // [B][64] its segment, counted from the one begun
     float *Y0, *Z;                        // [BH][Tp][d] the begun segment's memory read with the nodes' queries (split, without gate
                                           // and decay) and with their keys (decayed; split: without)
-    float *part;                          // [ranges + BH][Tp][d] partial reads
+    float *part;                          // [ranges + BH][Tp][d] partial reads (split at d = 64: twice, the sums of every other memory)
     float2 *weight;                       // [ranges + BH][Tp] split: top, or 0 without a router, and the sum of exp(score - top)
     int B, T, Tp, mode, topk;
     int ranges, groups;                   // shares of the memories; of the tokens
