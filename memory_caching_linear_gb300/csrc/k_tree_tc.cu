@@ -23,8 +23,8 @@
 // The path's own products (tree_path_tc) are a small kernel that comes up beside the reads once these are under way.
 // It needs nothing of them, but ends after them, so that what follows has both.
 //
-// 16 heads of d = 128, bf16: 12 sequences of up to 96 segments, 64 nodes, gated delta 189 us (scores 12, reads 155 at 6.2 TB/s,
-// path 51 beside them, finish 30); 8 of up to 63, 32 nodes, linear 98 (8, 78, 18, 14; cold, each alone).
+// 16 heads of d = 128, bf16: 12 sequences of up to 96 segments, 64 nodes, gated delta 200 us (scores 13, reads 165 at 5.9 TB/s,
+// path 53 beside them, finish 29); 8 of up to 63, 32 nodes, linear 102 (8, 79, 18, 12; cold, each alone).
 #include <cfloat>
 #include <cstdint>
 
@@ -63,7 +63,7 @@ constexpr int kSpan = 32, kPathThreads = 256, kCol = kSpan + 1;
 // part in three bf16 terms (2^-25 of it).  A chain of loads bounds it (slot, row, position,
 // page, mean key).
 template <int D>
-__global__ void __launch_bounds__(256) tree_scores_tc(TreeArgs a, int spans)
+__global__ void __launch_bounds__(256, 3) tree_scores_tc(TreeArgs a, int spans)
 {
     constexpr int KS = D / 16, LINE = 2 * D + 32;  // router inputs in rows eight banks apart
     __shared__ __align__(16) uint8_t us[kSpan * LINE];
@@ -94,31 +94,33 @@ __global__ void __launch_bounds__(256) tree_scores_tc(TreeArgs a, int spans)
     for (int i0 = 8 * warp; i0 < nb; i0 += 64) {
         page = valid_page(c, page);
         const float *src = c.kbar + ((size_t)max(page, 0) * c.H + h) * D;
-        uint32_t hi[KS][2], mid[KS][2], lo[KS][2];
+        float4 v[KS];
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            const float4 v = page >= 0 ? load4(src + 16 * ks + 4 * c4) : make_float4(0.f, 0.f, 0.f, 0.f);
-            mma::split3(v.x, v.y, hi[ks][0], mid[ks][0], lo[ks][0]);
-            mma::split3(v.z, v.w, hi[ks][1], mid[ks][1], lo[ks][1]);
-        }
+        for (int ks = 0; ks < KS; ++ks) v[ks] = page >= 0 ? load4(src + 16 * ks + 4 * c4) : make_float4(0.f, 0.f, 0.f, 0.f);
         const bool there[2] = {__shfl_sync(0xffffffffu, page, 8 * c4) >= 0, __shfl_sync(0xffffffffu, page, 8 * c4 + 4) >= 0};
         page = i0 + 64 + g < nb ? table[i0 + 64 + g] : -1;
+        float s[2][4] = {};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            uint32_t hi[2], mid[2], lo[2];
+            mma::split3(v[ks].x, v[ks].y, hi[0], mid[0], lo[0]);
+            mma::split3(v[ks].z, v[ks].w, hi[1], mid[1], lo[1]);
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+                const uint8_t *first = us + (16 * mt + g) * LINE + 8 * c4 + 32 * ks, *second = first + 8 * LINE;
+                const uint2 x = *reinterpret_cast<const uint2 *>(first), y = *reinterpret_cast<const uint2 *>(second);
+                const uint32_t f[4] = {x.x, y.x, x.y, y.y};
+                mma::mma16816(s[mt], f, hi[0], hi[1]);
+                mma::mma16816(s[mt], f, mid[0], mid[1]);
+                mma::mma16816(s[mt], f, lo[0], lo[1]);
+            }
+        }
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
-            const uint8_t *first = us + (16 * mt + g) * LINE + 8 * c4, *second = first + 8 * LINE;
-            float s[4] = {};
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                const uint2 x = *reinterpret_cast<const uint2 *>(first + 32 * ks), y = *reinterpret_cast<const uint2 *>(second + 32 * ks);
-                const uint32_t f[4] = {x.x, y.x, x.y, y.y};
-                mma::mma16816(s, f, hi[ks][0], hi[ks][1]);
-                mma::mma16816(s, f, mid[ks][0], mid[ks][1]);
-                mma::mma16816(s, f, lo[ks][0], lo[ks][1]);
-            }
 #pragma unroll
             for (int y = 0; y < 4; ++y) {  // segment i0 + 2 c4 (+ 1), node n0 + t
                 const int seg = i0 + 2 * c4 + (y & 1), t = 16 * mt + g + (y & 2 ? 8 : 0);
-                const float x = there[y & 1] ? s[y] : low;
+                const float x = there[y & 1] ? s[mt][y] : low;
                 most[2 * mt + (y >> 1)] = fmaxf(most[2 * mt + (y >> 1)], x);
                 if (seg < nb && n0 + t < seat.m) scores[(size_t)seg * a.Tp + t] = x;
             }
@@ -654,8 +656,9 @@ cudaError_t path_impl(const TreeArgs &a, cudaStream_t s)
     cudaError_t e = cudaFuncSetAttribute(tree_path_tc<D>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
     // one CTA an SM beside the reads of many segments; where there is room for few, most of the path comes after them, and three
-    // fit: 16 heads of d = 128, gated delta, 64 nodes, 32 sequences of 5 to 10 segments 227 -> 198 us, 12 of up to 96 189 -> 206;
-    // of up to 16 nodes there is too little for that: d = 64, 32 sequences of up to 10 segments 48 -> 52
+    // fit: 16 heads of d = 128, gated delta, 64 nodes, 32 sequences of 5 to 10 segments 230 -> 198 us, 12 of up to 96 189 -> 206;
+    // of up to 16 nodes there is too little for that: d = 64, 32 sequences of up to 10 segments 48 -> 52.  The host knows the
+    // room, not what is cached: the same short sequences in a table of 17 or 1024 take the 230
     const long long most = (long long)a.ranges * (a.c.nmax <= 16 && a.T > 16 ? 3 : 1);
     return launch_early(tree_path_tc<D>, (size_t)(items < most ? items : most) + 1, kPathThreads, sizeof(int) * Line::ints(a.B), s, a, spans,
                         path_segments(a));
