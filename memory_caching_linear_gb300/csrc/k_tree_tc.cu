@@ -449,7 +449,7 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
                 }
                 ++u;
             }
-            if (!ok) {  // the products under way end before tensor memory is freed
+            if (n > 0) {  // the products under way end before tensor memory is freed, whoever has given up
                 int gave_up = 0;
                 mma_commit(&drain);
                 mbar_wait_limit(&drain, 0, &gave_up, kWaitLimitNs);
@@ -630,6 +630,8 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
             ++u;
         }
     }
+    __syncwarp();
+    tmem_wait_st();  // (of a conversion that was given up)
     tc_fence_before();
     __syncthreads();
     if (warp == 0) {

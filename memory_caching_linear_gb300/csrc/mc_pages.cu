@@ -137,9 +137,10 @@ int run_batch(const mc_paged_cache *cache, TreeArgs a, Call call, int agg_mode, 
     const bool split = tree_tc_supported(a);
     a.scored = split && routed;
     a.ranges = split ? kSms : std::max(1, 4 * kSms / (a.groups * read_blocks(c.d)));
-    // a head's end, on the tensor cores: 16 heads of d = 128, 16 sequences of 2 to 63 segments, 16 nodes 101 -> 97 us, of d = 64,
-    // 32 of up to 10 58 -> 48; twice as much gives nothing more.  None on the CUDA cores, whose ranges are a quarter as long and
-    // bound by products: 16 sequences of 2 to 63 segments, d = 64, 16 nodes in fp32, 84 without and 86 with it
+    // a head's end, on the tensor cores: 16 heads of d = 128, 16 sequences of 2 to 62 segments, 16 nodes 145 -> 125 us (caches
+    // flushed), d = 64, 8 of up to 63, 32 nodes 82 -> 65; twice as much 125 and 59, four times 131 and 61.  None on the CUDA
+    // cores, whose ranges are a quarter as long and bound by products: 16 sequences of 2 to 63 segments, d = 64, 16 nodes in
+    // fp32, 84 without and 86 with it
     a.rest = split ? 256 / c.d : 0;
     void *scratch = nullptr;
     for (int pass = 0; pass < 2; ++pass) {

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import memory_caching_linear_gb300 as mcl
-from paged_ref import GRM, MEAN, SSC, TABLE_FULL, Ref, draft, seeded, tokens
+from paged_ref import GRM, MEAN, RESIDUAL, SSC, TABLE_FULL, Ref, draft, seeded, tokens
 from test_paged_gpu import gpu, i32, near, on_gpu, run_tree, same
 
 pytestmark = pytest.mark.gpu
@@ -122,3 +122,30 @@ def test_check_waits_for_every_stream():
         cache.check()
     cache.check()
     assert cache.status.item() == 0
+
+
+@pytest.mark.parametrize("d,dtype", [(64, torch.bfloat16), (128, torch.bfloat16), (32, torch.bfloat16), (64, torch.float32)])
+@pytest.mark.parametrize("mode,topk", [(GRM, 0), (MEAN, 0), (RESIDUAL, 0), (SSC, 3)])
+@pytest.mark.parametrize("T", [5, 21])
+def test_segments_without_a_page(T, mode, topk, d, dtype):
+    """Segments that found none -- first, last, every other, all of a sequence -- under every aggregation; NaN in free pages."""
+    gen, rng = seeded(d + T)
+    H, C, S = 3, 4, 4
+    ref = Ref(S, H, d, C, 12, 40).fill([7, 5, 9, 4], [1, 0, 3, 2], gen, rng)
+    gone = {0: [0], 1: [4], 2: [0, 2, 4, 6, 8], 3: [0, 1, 2, 3]}
+    for b, which in gone.items():
+        for i in which:
+            ref.refs[ref.table[b][i]] = 0
+            ref.table[b][i] = -1
+    cache = on_gpu(ref)
+    free = [p for p in range(40) if ref.refs[p] == 0]
+    cache.pages[free], cache.kbar[free] = float("nan"), float("nan")
+    x = tokens(gen, S, H, T, d, dtype)
+    if mode in (MEAN, RESIDUAL):
+        x[3] = None
+    run_tree(cache, ref, x, draft(rng, S, T, "tree"), [T, T - 1, T, T], [2, 0, 3, 1], mode, topk, dtype)
+    one = [None if t is None else t[:, :, 0].contiguous() for t in x]
+    on = [gpu(t) for t in one]
+    y = mcl.mc_decode_step_paged(cache, *on[:4], mode, topk, log_alpha=on[4], beta=on[5])
+    want = ref.step(*one, None, mode, topk)
+    near(y, torch.stack([want[b] for b in range(S)]), 1e-4 if dtype == torch.float32 else 1e-2)
