@@ -374,7 +374,8 @@ enum { MC_PAGES_INDEX = 1, MC_PAGES_NONE_FREE = 2, MC_PAGES_TABLE_FULL = 4 };
 
 /*
  * mc_decode_step_paged -- one decoding step of every sequence in the batch, as mc_decode_step treats its token; a segment that it
- * completes gets a page.
+ * completes gets a page.  (The lowest free one is looked for from the pool's first: the more pages in use lie before it, the longer
+ * such a step takes.)
  *   q, k, v, u      : the tokens, [B][H][d] (u may be NULL for Residual and Mean); y: the same, written.
  *   log_alpha, beta : [B][H] for the gated delta memory, both NULL for the linear one.
  *   slots           : as above; a slot that comes twice is the first row's alone.

@@ -11,9 +11,9 @@
 // 16), which one thread issues, 60 to 80 clocks each: 264 us, bound by that, against 217 as it is.
 // A memory of 64 KB is read from HBM once for all nodes, 1.5 us of an SM's share of the bandwidth; eight warps need about that for
 // the split, the weights and the sums, one thread 0.6 us for the products of 64 nodes.  So the memories stream through a ring
-// of 32-column panels (176 KB on an SM), and the split of one tile (a memory of 128 rows, two of 64) runs beside the products
-// of the one before and the sums of the one before that.  With all of an SM's memory shared, what a thread spills goes to L2: the
-// kernel keeps within its registers.
+// of 32-column panels (144 KB on an SM; 160 and 176 give nothing), and the split of one tile (a memory of 128 rows, two of 64)
+// runs beside the products of the one before and the sums of the one before that.  With most of an SM's memory shared, what a
+// thread spills goes to L2: the kernel keeps within its registers.
 //
 // The memories of all heads and sequences form one line, cut into one range per CTA whatever the sequences' lengths.  A range
 // leaves the sum of its weights with its partial read, and tree_finish joins them, as a softmax over parts; the begun segment's
@@ -253,7 +253,7 @@ __global__ void __maxnreg__(kPathRegs) tree_path_tc(TreeArgs a, int spans, int s
 // ------------------------------------------------------------------------------------------------ the reads
 
 constexpr int kWorkers = 8, kThreads = 32 * (kWorkers + 2);
-constexpr int kPanels = 11;                   // of the ring: 128 rows (a memory's, or two memories' of 64) by 32 columns
+constexpr int kPanels = 9;                   // of the ring: 128 rows (a memory's, or two memories' of 64) by 32 columns
 constexpr int kPanelBytes = 128 * 128;
 // Columns of tensor memory: of a tile's sums (two tiles), then of every 64 columns' two terms (two tiles again).
 constexpr int kSums = 64, kTerm = 32, kTerms = 2 * kTerm;
@@ -261,6 +261,8 @@ constexpr int kSums = 64, kTerm = 32, kTerms = 2 * kTerm;
 template <int D> struct ReadSmem {
     static constexpr int B = kMaxTree * D * 2, BYTES = 1024 + kPanels * kPanelBytes + 2 * B;
 };
+// With the line of a full batch and up to 4 KB of static memory an SM has room for it.
+static_assert(ReadSmem<128>::BYTES + 4 * (4 * kMaxRows + 1) + 4096 <= 227 * 1024);
 
 // A panel of the ring and how often it has been used, modulo 2.
 struct Place {

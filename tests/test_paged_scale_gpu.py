@@ -186,3 +186,22 @@ def test_drafts_of_what_is_not_finite(d):
             assert torch.isnan(got[b, :, j, 3]).all()
         else:
             assert float((got[b, :, j, 7] / w[:, 7] - 1).abs().max()) <= 2 ** -8 + 1e-4
+
+
+@pytest.mark.parametrize("d,T,dtype", [(128, 9, torch.bfloat16), (64, 9, torch.bfloat16), (128, 2, torch.bfloat16), (128, 3, torch.float32)])
+def test_a_full_batch_of_drafts(d, T, dtype):
+    """1024 sequences: the most rows that a call takes, all of whose places a CTA holds in shared memory."""
+    S, C = 1024, 4
+    gen, rng = seeded(d + T)
+    segs = [rng.randrange(3) for _ in range(S)]
+    n_max = 700 if T < 9 else 4  # (room for so much that a few nodes take every kernel)
+    ref = Ref(S, 1, d, C, n_max, sum(segs) + 8).fill(segs, [rng.randrange(C) for _ in range(S)], gen, rng)
+    cache = ref.to(mcl.PagedCache(S, 1, d, C, n_max, ref.P))
+    x = tokens(gen, S, 1, T, d, dtype)
+    parent = draft(rng, S, T, "tree")
+    y = torch.full((S, 1, T, d), 7.0, dtype=dtype, device="cuda")
+    q, k, v, u, la, be = (gpu(t) for t in x)
+    mcl.mc_decode_tree(cache, q, k, v, u, i32(parent), GRM, log_alpha=la, beta=be, y=y)
+    want = ref.tree(*x, parent, None, None, GRM, 0)
+    near(y, torch.stack([torch.stack([want[b, j] for j in range(T)], 1) for b in range(S)]), TOL[dtype])
+    assert cache.status.item() == 0
