@@ -253,7 +253,7 @@ __global__ void __maxnreg__(kPathRegs) tree_path_tc(TreeArgs a, int spans, int s
 // ------------------------------------------------------------------------------------------------ the reads
 
 constexpr int kWorkers = 8, kThreads = 32 * (kWorkers + 2);
-constexpr int kPanels = 9;                   // of the ring: 128 rows (a memory's, or two memories' of 64) by 32 columns
+constexpr int kPanels = 9;                    // of the ring: 128 rows (a memory's, or two memories' of 64) by 32 columns
 constexpr int kPanelBytes = 128 * 128;
 // Columns of tensor memory: of a tile's sums (two tiles), then of every 64 columns' two terms (two tiles again).
 constexpr int kSums = 64, kTerm = 32, kTerms = 2 * kTerm;
@@ -383,7 +383,7 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
     tc_fence_after();
     const uint32_t tb = tmem_base;
     Runs runs(a, line);
-    Run r;
+    Run r{};
 
     if (warp == kWorkers) {
         if (lane == 0) {
@@ -459,7 +459,8 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
         }
         __syncwarp();
     } else {
-        // this thread's row of a tile, the warp's panels (every other) and columns of D (16 of every 32); the node whose weights the lane forms
+        // this thread's row of a tile, the warp's panels (every other) and columns of D (16 of every 32); the node whose weights
+        // the lane forms
         const int quarter = warp % 4, side = warp / 4, row = 32 * quarter + lane, half = row / D, t = 16 * side + lane % 16 + (lane & 16) * 2;
         uint32_t u = 0, n = 0;
         Place at;
@@ -574,7 +575,8 @@ tree_read_tc(const __grid_constant__ CUtensorMap pages, const __grid_constant__ 
                                     lo[2 * y + 1] = mma::pack2(q.x, q.y);
                                     big = most(most(big, p.x, p.y), q.x, q.y);
                                 }
-                                if (!(big < FLT_MAX)) {  // not finite, or rounded to what is not: the first term cut off; of what is not finite it is all
+                                // not finite, or rounded to what is not: the first term cut off; of what is not finite it is all
+                                if (!(big < FLT_MAX)) {
 #pragma unroll
                                     for (int y = 0; y < 8; ++y) {
                                         const uint2 w = *reinterpret_cast<const uint2 *>(from + (((4 * z + y / 2) ^ (row & 7)) << 4) + y % 2 * 8);
